@@ -1,0 +1,235 @@
+// vt_tables.cu -- block tables and slot maps from request lengths.
+//
+// For request r with len_r tokens in blocks of 2^shift:
+//   blocks_r = ceil(len_r / 2^shift), shared_r = min(blocks_r, prefix blocks),
+//   have_r = max(held_r, shared_r), need_r = max(0, blocks_r - have_r),
+//   off_r = need_0 + ... + need_(r-1);
+//   table[r][held_r..shared_r) = prefix blocks,
+//   table[r][have_r + i] = free[cursor + off_r + i], i < need_r;
+// and the token at position p of r lives in slot table[r][p >> shift] <<
+// shift | (p mod 2^shift).  A request whose blocks do not fit the free list, or
+// whose lengths are not valid, gets none.
+//
+// One launch, in which no CTA waits for another: every CTA scans all B
+// requests itself (12 bytes a request, from L2), keeps the two prefix sums in
+// shared memory and then writes its own part of the table and of the slot map.
+// A token's block is worked out from its source (old table entry, prefix or
+// free list), never read from an entry that this launch writes.  What bounds it:
+// launch latency for a decode step's sizes, the 12 bytes written a token for
+// prompts.
+#include "vt_device.cuh"
+#include "vt_paged.h"
+
+namespace vt {
+namespace {
+
+constexpr int kTabThreads = 512;
+constexpr int kTabWarps = kTabThreads / 32;
+constexpr int kTokensPerThread = 4;
+constexpr int kColsPerItem = 256;
+
+struct RowNeed {
+  int64_t need, query;
+  int held, have, blocks;
+  bool bad;
+};
+
+__device__ __forceinline__ RowNeed row_need(const TablesArgs& a, int r) {
+  RowNeed n;
+  const int64_t len = a.seq_lens[r], q = a.query_lens[r];
+  const int64_t blocks = (len + (1ll << a.shift) - 1) >> a.shift;
+  n.bad = len < 0 || q < 0 || q > len || blocks > a.cols;
+  n.blocks = n.bad ? 0 : (int)blocks;
+  const int h = a.held ? a.held[r] : 0;
+  n.held = min(max(h, 0), a.cols);
+  n.have = max(n.held, min(n.blocks, a.n_prefix));
+  n.need = n.bad ? 0 : max(0, n.blocks - n.have);
+  n.query = n.bad ? 0 : q;
+  return n;
+}
+
+// Inclusive block scan of two values; *tot_* get the totals.
+__device__ __forceinline__ void block_scan2(int64_t& x, int64_t& y, int64_t* sx, int64_t* sy) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t px = __shfl_up_sync(0xffffffffu, x, o), py = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += px;
+      y += py;
+    }
+  }
+  if (lane == 31) {
+    sx[w] = x;
+    sy[w] = y;
+  }
+  __syncthreads();
+  int64_t ax = 0, ay = 0;
+  for (int i = 0; i < w; ++i) {
+    ax += sx[i];
+    ay += sy[i];
+  }
+  x += ax;
+  y += ay;
+}
+
+__device__ __forceinline__ int clamp31(int64_t v) {
+  return (int)(v > 0x7fffffffll ? 0x7fffffffll : v);
+}
+
+__global__ void __launch_bounds__(kTabThreads) tables_kernel(TablesArgs a) {
+  extern __shared__ int32_t dyn[];
+  int32_t* s_start = dyn;             // [B + 1] first token of each request
+  int32_t* s_off = dyn + a.B + 1;     // [B] first free-list entry, or -1: the request got none
+  __shared__ int64_t sx[kTabWarps], sy[kTabWarps];
+  __shared__ int64_t carry[2];
+  __shared__ int s_cursor;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool first = blockIdx.x == 0;
+  const int c_in = a.cursor[0];
+  const int64_t c0 = c_in < 0 ? a.n_free : min(c_in, a.n_free);  // outside: nothing is free
+  if (tid == 0) {
+    carry[0] = carry[1] = 0;
+    s_cursor = 0;
+  }
+  __syncthreads();
+  for (int base = 0; base < a.B; base += kTabThreads) {
+    const int r = base + tid;
+    RowNeed n{};
+    if (r < a.B) n = row_need(a, r);
+    int64_t x = n.need, y = n.query;
+    block_scan2(x, y, sx, sy);
+    x += carry[0];
+    y += carry[1];
+    if (r < a.B) {
+      const bool full = n.need > 0 && c0 + x > a.n_free;
+      const bool ok = !n.bad && !full;
+      s_off[r] = ok ? clamp31(c0 + x - n.need) : -1;
+      s_start[r + 1] = clamp31(y);
+      if (ok && n.need > 0) atomicMax(&s_cursor, (int)x);
+      if (first) {
+        a.out_held[r] = ok ? max(n.held, n.blocks) : n.held;
+        a.starts[r + 1] = clamp31(y);
+        a.status[r] = n.bad ? 2 : full ? 1 : 0;
+      }
+    }
+    __syncthreads();
+    if (tid == kTabThreads - 1) {
+      carry[0] = x;
+      carry[1] = y;
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    s_start[0] = 0;
+    if (first) {
+      a.starts[0] = 0;
+      a.out_cursor[0] = s_cursor > 0 ? (int)c0 + s_cursor : c_in;
+    }
+  }
+  __syncthreads();
+
+  // the table: (request, 256 columns) items over the warps of the grid
+  const int per_row = (a.cols + kColsPerItem - 1) / kColsPerItem;
+  const int64_t items = (int64_t)a.B * per_row;
+  for (int64_t it = (int64_t)blockIdx.x * kTabWarps + warp; it < items;
+       it += (int64_t)gridDim.x * kTabWarps) {
+    const int r = (int)(it / per_row);
+    const int c_lo = (int)(it % per_row) * kColsPerItem;
+    const int c_hi = min(a.cols, c_lo + kColsPerItem);
+    const RowNeed n = row_need(a, r);
+    const int off = s_off[r];
+    const int live = off >= 0 ? n.blocks : 0;
+    const int from = max(c_lo, n.held), to = a.held ? min(c_hi, live) : c_hi;
+    int32_t* row = a.table + (int64_t)r * a.ld;
+    for (int c = from + lane; c < to; c += 32) {
+      int id = -1;
+      if (c < live) id = c < n.have ? a.prefix[c] : a.free_blocks[off + (c - n.have)];
+      row[c] = id;
+    }
+  }
+
+  // the slot map: four tokens in a row to a thread
+  const int64_t per_cta = (int64_t)kTabThreads * kTokensPerThread;
+  for (int64_t base = (int64_t)blockIdx.x * per_cta; base < a.capacity;
+       base += (int64_t)gridDim.x * per_cta) {
+    const int64_t t0 = base + (int64_t)tid * kTokensPerThread;
+    if (t0 >= a.capacity) continue;
+    int64_t slot[kTokensPerThread];
+    int32_t pos[kTokensPerThread];
+#pragma unroll
+    for (int i = 0; i < kTokensPerThread; ++i) {
+      slot[i] = -1;
+      pos[i] = -1;
+    }
+    if (t0 < s_start[a.B]) {
+      int lo = 0, hi = a.B;  // the request of t0: the last start at or below it that has tokens
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_start[mid] <= t0) lo = mid;
+        else hi = mid;
+      }
+      int r = lo;
+      RowNeed n = row_need(a, r);
+      int off = s_off[r];
+      int64_t len = a.seq_lens[r];
+#pragma unroll
+      for (int i = 0; i < kTokensPerThread; ++i) {
+        const int64_t t = t0 + i;
+        if (t < s_start[a.B]) {
+          if (t >= s_start[r + 1]) {
+            do ++r;
+            while (t >= s_start[r + 1]);
+            n = row_need(a, r);
+            off = s_off[r];
+            len = a.seq_lens[r];
+          }
+          if (off >= 0) {
+            const int p = (int)(len - n.query + (t - s_start[r]));
+            const int c = p >> a.shift;
+            const int id = c < n.held   ? a.table[(int64_t)r * a.ld + c]
+                           : c < n.have ? a.prefix[c]
+                                        : a.free_blocks[off + (c - n.have)];
+            pos[i] = p;
+            slot[i] = ((int64_t)id << a.shift) + (p & ((1 << a.shift) - 1));
+          }
+        }
+      }
+    }
+    if (a.vec && t0 + kTokensPerThread <= a.capacity) {
+      *reinterpret_cast<longlong2*>(a.slots + t0) = make_longlong2(slot[0], slot[1]);
+      *reinterpret_cast<longlong2*>(a.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTokensPerThread; ++i)
+        if (t0 + i < a.capacity) {
+          a.slots[t0 + i] = slot[i];
+          a.positions[t0 + i] = pos[i];
+        }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tables(const TablesArgs& a, int num_sms, cudaStream_t stream) {
+  const size_t smem = sizeof(int32_t) * (2 * (size_t)a.B + 1);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t tiles = (a.capacity + kTabThreads * kTokensPerThread - 1) /
+                        (kTabThreads * kTokensPerThread);
+  const int64_t items =
+      ((int64_t)a.B * ((a.cols + kColsPerItem - 1) / kColsPerItem) + 4 * kTabWarps - 1) /
+      (4 * kTabWarps);
+  int64_t grid = tiles > items ? tiles : items;
+  if (grid > 2 * num_sms) grid = 2 * num_sms;
+  if (grid < 1) grid = 1;
+  tables_kernel<<<(unsigned)grid, kTabThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace vt

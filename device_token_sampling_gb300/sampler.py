@@ -17,6 +17,7 @@ from . import _build
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+DTYPE_F16 = 2  # PagedBatch.attention only
 
 VT_OK = 0
 VT_ERR_INVALID_ARG = -1
@@ -47,6 +48,12 @@ class Config(C.Structure):
     _fields_ = [("max_batch", C.c_int32), ("max_vocab", C.c_int32),
                 ("max_logprobs", C.c_int32), ("max_history", C.c_int32),
                 ("device", C.c_int32), ("host_io", C.c_int32)]
+
+
+class PagedConfig(C.Structure):
+    _fields_ = [("max_batch", C.c_int32), ("block_size", C.c_int32), ("max_blocks", C.c_int32),
+                ("q_heads", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("device", C.c_int32)]
 
 
 P = C.c_void_p
@@ -85,6 +92,14 @@ SIGNATURES = {
     "vt_shard_merge": (C.c_int, [P, P, I32, I32, I32, I32, I32, P, P, P, P, P]),
     "vt_sample_noalloc": (C.c_int, [I32, P, I32, I32, I32, I64, P, P, P, P, P, I32, P, P, P, P,
                                     P, I32, P, C.c_char_p, I32]),
+    "vt_paged_create": (C.c_int, [C.POINTER(PagedConfig), C.POINTER(P)]),
+    "vt_paged_destroy": (None, [P]),
+    "vt_paged_last_error": (C.c_char_p, [P]),
+    "vt_paged_check_errors": (C.c_int, [P]),
+    "vt_paged_tables": (C.c_int, [P, I32, P, P, P, P, I32, P, I32, P, P, I64, P, P, P, P, P, I64,
+                                  P, P]),
+    "vt_paged_attention": (C.c_int, [P, I32, I32, P, I64, I64, P, P, I32, I64, I64, I64, P, I64,
+                                     P, P, I32, I32, C.c_float, P, P, P]),
     "vt_last_error": (C.c_char_p, [P]),
     "vt_status_string": (C.c_char_p, [C.c_int]),
 }

@@ -65,6 +65,7 @@ extern "C" {
 /* ---- logits element types ----------------------------------------------- */
 #define VT_DTYPE_F32 0  /* IEEE binary32                                        */
 #define VT_DTYPE_BF16 1 /* bfloat16 (the top 16 bits of a binary32), widened exactly */
+#define VT_DTYPE_F16 2  /* IEEE binary16 (vt_paged_attention only)              */
 
 /* ---- per-row status written by vt_sample (see vt_get_row_status) ------- */
 #define VT_ROW_OK 0           /* token drawn                                    */
@@ -454,6 +455,117 @@ int vt_shard_partials(vt_sampler* handle, const void* logits, int32_t dtype, int
 int vt_shard_merge(vt_sampler* handle, const void* parts, int32_t S, int32_t B, int32_t V,
                    int32_t K, int32_t num_logprobs, int32_t* out_tokens, float* out_logprobs,
                    int32_t* out_topk_ids, float* out_topk_logprobs, void* stream);
+
+/* ---- the batch's cache: block tables and attention behind a shared prefix ---
+ * Continuations of one prompt share its part of a paged key/value cache.  A
+ * vt_paged handle lays the cache out on the device from the requests' lengths
+ * (vt_paged_tables) and attends over it with the shared part computed once for
+ * all requests (vt_paged_attention).  The conventions are the sampler's: codes,
+ * streams, ownership, and no allocation after create.  The calls of one handle
+ * share its workspace: calls that may overlap on the GPU (other streams) need
+ * handles of their own or an order between them. */
+typedef struct vt_paged vt_paged; /* opaque handle */
+
+#define VT_PAGED_MAX_BATCH 16384
+
+typedef struct vt_paged_config {
+  int32_t max_batch;  /* largest B of any call, 1..VT_PAGED_MAX_BATCH            */
+  int32_t block_size; /* tokens in a cache block: a power of two, 1..1024       */
+  int32_t max_blocks; /* columns of a table row; max_blocks * block_size <= 2^30 */
+  int32_t q_heads;    /* attention: query heads, a multiple of kv_heads, <= 1024;
+                         0 (with kv_heads and head_dim 0): tables alone         */
+  int32_t kv_heads;
+  int32_t head_dim;   /* 64 or 128                                              */
+  int32_t device;     /* CUDA device ordinal                                    */
+} vt_paged_config;
+
+/* Create a handle and allocate its workspace.  Errors: VT_ERR_INVALID_ARG (null
+ * pointer, value out of range), VT_ERR_CUDA (no such device, out of memory, not
+ * an sm_103 GPU). */
+int vt_paged_create(const vt_paged_config* config, vt_paged** out);
+
+/* Free the handle after its pending work.  NULL is ignored. */
+void vt_paged_destroy(vt_paged* handle);
+
+/* Message for the last failing call on `handle` ("" if none). */
+const char* vt_paged_last_error(const vt_paged* handle);
+
+/* Synchronise the handle's last stream and report what its kernels met since
+ * the previous check: VT_ERR_TIMEOUT (a bounded wait ran out; the outputs are
+ * not valid), VT_ERR_INVALID_ARG (vt_paged_attention met a block id outside
+ * the cache and left its tokens out), VT_OK otherwise.  Clears what it reports. */
+int vt_paged_check_errors(vt_paged* handle);
+
+/* Block tables and slot maps from request lengths.  All arrays are device
+ * memory.  Request r has seq_lens[r] tokens in the cache after this step, the
+ * last query_lens[r] of them new.  It needs ceil(seq_lens[r] / block_size)
+ * blocks: the first num_prefix_blocks of them are prefix_blocks (shared by all
+ * requests; fewer when the request is shorter), the others its own, taken from
+ * the free list in request order.
+ *   held              [B] columns of each table row already filled, or NULL for
+ *                     a new table.  Columns below held are left as they are.
+ *   free_blocks       [num_free] block ids; the entries from *cursor on are free.
+ *   table             [B][ld_table] (ld_table >= max_blocks).  New table: every
+ *                     column is written, -1 past the request's blocks.  With held:
+ *                     only the columns of new blocks are written.
+ *   out_held, out_cursor   held and *cursor after the call (not the arrays held
+ *                     and cursor themselves).
+ *   out_starts        [B + 1] sums of the query lengths: request r's new tokens
+ *                     are out_starts[r] .. out_starts[r + 1] - 1 (held at 2^31 - 1).
+ *   out_slots         [capacity] per new token, block * block_size + its place in
+ *   out_positions     the block, and its position in the request; -1 past the
+ *                     last token.  Tokens past capacity are not written.
+ *   out_status        [B]: 0; 1 when the request's new blocks do not fit what is
+ *                     left of the free list after the requests before it; 2 when
+ *                     its lengths are not 0 <= query <= seq or need more than
+ *                     max_blocks.  A request with status 1 or 2 gets no block, its
+ *                     table row no new entry (-1 throughout in a new table), its
+ *                     tokens slot -1; with status 2 it also has no tokens.
+ * A *cursor outside [0, num_free] counts as an empty free list.  One launch;
+ * enqueues only; may be captured.  Errors: VT_ERR_INVALID_ARG (null array, bad
+ * size, held or cursor given as its own output), VT_ERR_CAPACITY (B >
+ * max_batch), VT_ERR_CUDA. */
+int vt_paged_tables(vt_paged* handle, int32_t B, const int32_t* seq_lens,
+                    const int32_t* query_lens, const int32_t* held, const int32_t* prefix_blocks,
+                    int32_t num_prefix_blocks, const int32_t* free_blocks, int32_t num_free,
+                    const int32_t* cursor, int32_t* table, int64_t ld_table, int32_t* out_held,
+                    int32_t* out_cursor, int32_t* out_starts, int64_t* out_slots,
+                    int32_t* out_positions, int64_t capacity, int32_t* out_status, void* stream);
+
+/* Attention of one query token a request over the paged cache:
+ * out[b][h] = sum_j p_j v_j / sum_j p_j over the positions j < seq_lens[b], with
+ * p_j = exp(scale * q[b][h] . k_j).  Positions below prefix_len are read through
+ * prefix_blocks, for all requests at once; the others through the request's
+ * table row.  All arrays are device memory.
+ *   dtype           VT_DTYPE_BF16 or VT_DTYPE_F16: q, the cache and out.
+ *   q               request b's head h starts at q + b * q_row + h * q_head.
+ *   k_cache, v_cache  num_blocks blocks; token t of block i, kv head g starts at
+ *                   i * block_stride + t * token_stride + g * head_stride
+ *                   (elements).  Query head h uses kv head h / (q_heads / kv_heads).
+ *   table           [B][ld_table] block ids; columns from prefix_len / block_size on
+ *                   are read.
+ *   seq_lens        [B], values up to max_blocks * block_size (larger ones are cut
+ *                   there).  0: out is 0 and the log-sum -inf.  A request shorter
+ *                   than the prefix attends to its own length of it.
+ *   prefix_blocks   the ids of the blocks that hold positions 0 .. prefix_len - 1.
+ *   prefix_len      0 (nothing shared) .. max_blocks * block_size.
+ *   max_seq_len     an upper bound of seq_lens that shapes the launch; 0: the
+ *                   tables' capacity.  Longer requests come out right, more slowly.
+ *   out             [B][q_heads][head_dim], contiguous.
+ *   out_lse         float [B][q_heads]: ln sum_j p_j; may be NULL.
+ * q, the caches and out start on 16 bytes and the strides are multiples of 8
+ * elements.  A block id outside [0, num_blocks) leaves its tokens out
+ * (vt_paged_check_errors reports it).  Scores, maxima and sums are fp32; the
+ * weights are rounded to dtype for the product with V.  Enqueues only; may be
+ * captured.  Errors: VT_ERR_INVALID_ARG, VT_ERR_CAPACITY (B > max_batch),
+ * VT_ERR_STATE (a handle without heads), VT_ERR_CUDA. */
+int vt_paged_attention(vt_paged* handle, int32_t dtype, int32_t B, const void* q, int64_t q_row,
+                       int64_t q_head, const void* k_cache, const void* v_cache,
+                       int32_t num_blocks, int64_t block_stride, int64_t token_stride,
+                       int64_t head_stride, const int32_t* table, int64_t ld_table,
+                       const int32_t* seq_lens, const int32_t* prefix_blocks, int32_t prefix_len,
+                       int32_t max_seq_len, float scale, void* out, float* out_lse,
+                       void* stream);
 
 /* Message for the last failing call on `handle` ("" if none); static storage
  * owned by the handle, valid until the next call on it. */
