@@ -242,4 +242,21 @@ void plan_probs(int B, int V, int num_sms, int* splits, int* range);
 // The two launches (partials, then the probabilities) on `stream`.
 cudaError_t launch_probs(const ProbsArgs& args, int dtype, cudaStream_t stream);
 
+// ---- draws from given uniform numbers (vt_given.cu) --------------------------
+struct GivenArgs {
+  const void* logits;        // [B][ld]
+  int64_t ld;
+  int32_t B, V;
+  int32_t aligned;           // rows 16-byte aligned
+  const RowParams* params;   // [B]
+  const float* uniforms;     // [B][draws]
+  int32_t draws;
+  int32_t* out_tokens;       // [B][draws]
+  float* out_logprobs;       // [B][draws] or null
+  int32_t* row_status;       // [B]
+  int32_t* err_word;
+  int32_t slice, mass_bits;  // filled by launch_given
+};
+cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t stream);
+
 }  // namespace vt

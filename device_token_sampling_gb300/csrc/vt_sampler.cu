@@ -1063,6 +1063,55 @@ int vt_shard_merge(vt_sampler* h, const void* parts, int32_t S, int32_t B, int32
   return VT_OK;
 }
 
+int vt_sample_given(vt_sampler* h, const void* logits, int32_t dtype, int32_t B, int32_t V,
+                    int64_t ld, const float* uniforms, int32_t draws, int32_t* out_tokens,
+                    float* out_logprobs, void* stream) {
+  if (!h) return VT_ERR_INVALID_ARG;
+  if (h->params_B == 0) return set_err(h, VT_ERR_STATE, "vt_sample_given before vt_reset_params");
+  if (B < 1) return set_err(h, VT_ERR_INVALID_ARG, "B=%d: need B >= 1", B);
+  if (B > h->params_B)
+    return set_err(h, VT_ERR_STATE, "B=%d but parameters were reset for %d rows", B, h->params_B);
+  if (dtype != VT_DTYPE_F32 && dtype != VT_DTYPE_BF16)
+    return set_err(h, VT_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (V < 1 || ld < V)
+    return set_err(h, VT_ERR_INVALID_ARG, "V=%d, ld=%lld: need 1 <= V <= ld", V, (long long)ld);
+  if (V > h->cfg.max_vocab)
+    return set_err(h, VT_ERR_CAPACITY, "V=%d above max_vocab=%d", V, h->cfg.max_vocab);
+  if (draws < 1 || draws > VT_GIVEN_MAX_DRAWS)
+    return set_err(h, VT_ERR_INVALID_ARG, "draws=%d outside [1, %d]", draws, VT_GIVEN_MAX_DRAWS);
+  if (!logits || !uniforms || !out_tokens)
+    return set_err(h, VT_ERR_INVALID_ARG, "null logits, uniforms or tokens");
+  const size_t es = dtype == VT_DTYPE_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % es)
+    return set_err(h, VT_ERR_INVALID_ARG, "logits not aligned to their elements");
+  for (int r = 0; r < B; ++r)
+    if (h->row_flags[r] & (vt::kRowPenalty | vt::kRowDecay))
+      return set_err(h, VT_ERR_INVALID_ARG,
+                     "row %d: vt_sample_given takes no penalties and no top-p decay", r);
+  DeviceGuard guard(h->cfg.device);
+  if (!guard.ok) return set_err(h, VT_ERR_CUDA, "cannot select device %d", h->cfg.device);
+  vt::GivenArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.logits = logits;
+  a.ld = ld;
+  a.B = B;
+  a.V = V;
+  a.aligned = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && (ld * es) % 16 == 0;
+  a.params = h->d_params;
+  a.uniforms = uniforms;
+  a.draws = draws;
+  a.out_tokens = out_tokens;
+  a.out_logprobs = out_logprobs;
+  a.row_status = h->d_status;
+  a.err_word = h->d_err;
+  cudaStream_t st = (cudaStream_t)stream;
+  VT_CK(h, vt::launch_given(a, dtype, h->num_sms, st));
+  h->last_B = B;
+  h->last_stream = st;
+  h->err.clear();
+  return VT_OK;
+}
+
 int vt_debug_wait_probe(vt_sampler* h, int64_t limit_ns, void* stream) {
   if (!h || limit_ns < 1 || limit_ns > 1000000000LL) return VT_ERR_INVALID_ARG;
   DeviceGuard guard(h->cfg.device);

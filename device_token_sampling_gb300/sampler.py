@@ -72,6 +72,7 @@ SIGNATURES = {
     "vt_reset_token_counts_ex": (C.c_int, [P, I32, P, P, P, P, P, P]),
     "vt_sample": (C.c_int, [P, P, I32, I32, I32, I64, I32, I32, P, P, P, P, P]),
     "vt_sample_ex": (C.c_int, [P, P, I32, I32, I32, I64, I32, I32, P, P, P, P, P, I64, P]),
+    "vt_sample_given": (C.c_int, [P, P, I32, I32, I32, I64, P, I32, P, P, P]),
     "vt_sample_host": (C.c_int, [P, P, I32, I32, I32, I64, I32, I32, P, P, P, P, P]),
     "vt_check_device_errors": (C.c_int, [P]),
     "vt_get_row_status": (C.c_int, [P, P, P]),
@@ -290,6 +291,48 @@ class Sampler:
         rc = self._lib.vt_sample_ex(*args, P(probs.data_ptr()), probs.stride(0),
                                     _stream_ptr(stream))
         self._check(rc, "vt_sample_ex")
+        return out
+
+    def sample_given(self, logits, uniforms, V: int | None = None, out=None, stream=None,
+                     dtype: int | None = None):
+        """vt_sample_given: draw from given uniform numbers.  ``logits`` as in ``sample``;
+        ``uniforms`` a float32 CUDA tensor [B] (one draw a row) or [B, draws].  Returns
+        ``(tokens, logprobs)``, int32 and float32 in the shape of ``uniforms``.  Rows take no
+        penalties and no top-p decay.  Stream-ordered; nothing waits."""
+        import torch
+        if logits.dim() != 2 or not logits.is_cuda or logits.stride(1) != 1:
+            raise ValueError("logits must be a 2-D CUDA tensor with contiguous rows")
+        if dtype is None:
+            dtype = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
+                     torch.uint16: DTYPE_BF16, torch.int16: DTYPE_BF16}.get(logits.dtype)
+            if dtype is None:
+                raise ValueError(f"unsupported logits dtype {logits.dtype}")
+        B = logits.shape[0]
+        V = logits.shape[1] if V is None else V
+        ld = logits.stride(0) if B > 1 else max(logits.stride(0), logits.shape[1])
+        if V > logits.shape[1]:
+            raise ValueError(f"V={V} is past the rows' {logits.shape[1]} columns")
+        if (uniforms.dtype != torch.float32 or uniforms.device != logits.device
+                or uniforms.dim() not in (1, 2) or uniforms.shape[0] != B
+                or not uniforms.is_contiguous()):
+            raise ValueError("uniforms must be a contiguous float32 tensor [B] or [B, draws] "
+                             "beside the logits")
+        draws = 1 if uniforms.dim() == 1 else uniforms.shape[1]
+        if out is None:
+            out = (torch.empty_like(uniforms, dtype=torch.int32), torch.empty_like(uniforms))
+            if stream is not None:
+                for t in out:
+                    t.record_stream(stream)
+        tok, lp = out
+        for t, name, dt in ((tok, "tokens", torch.int32), (lp, "logprobs", torch.float32)):
+            if t is not None and (t.dtype != dt or t.shape != uniforms.shape
+                                  or t.device != logits.device or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {dt} tensor like uniforms")
+        rc = self._lib.vt_sample_given(self._h, P(logits.data_ptr()), dtype, B, V, ld,
+                                       P(uniforms.data_ptr()), draws, P(tok.data_ptr()),
+                                       None if lp is None else P(lp.data_ptr()),
+                                       _stream_ptr(stream))
+        self._check(rc, "vt_sample_given")
         return out
 
     def sample_ptr(self, logits_ptr: int, dtype: int, B: int, V: int, ld: int, num_logprobs: int,

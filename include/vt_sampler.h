@@ -224,6 +224,37 @@ int vt_sample_ex(vt_sampler* handle, const void* logits, int32_t dtype, int32_t 
                  float* out_logprobs, int32_t* out_topk_ids, float* out_topk_logprobs,
                  float* out_probs, int64_t ld_probs, void* stream);
 
+/* Draw tokens from given uniform numbers: `draws` tokens for each of rows
+ * 0..B-1, all from the row's one filtered distribution (the first step of
+ * several continuations of one prompt, random numbers made elsewhere, common
+ * random numbers between runs).  The rows' temperature, min-p, top-k and top-p
+ * are those of vt_reset_params, and the kept set is vt_sample's: z_t = z *
+ * (1.0f / T) in fp32, min-p, then top-k, then top-p on the order (z_t
+ * descending, index ascending).  With w_j = exp(z_t,j - max z_t):
+ *   token(u) = the first kept j, in index order, with
+ *              sum of w over the kept i <= j  >  u * sum of w over the kept set;
+ * a greedy row gives its lowest-index argmax for every u.
+ *   logits, dtype, V, ld   as vt_sample (other alignments: slower, same result).
+ *   uniforms       device float[B][draws], values in [0, 1); below 0 and NaN count
+ *                  as 0, and 1 and more draw the last kept token.
+ *   draws          1..VT_GIVEN_MAX_DRAWS.
+ *   out_tokens     device int32[B][draws]; -1 for a row with status NONFINITE or
+ *                  EMPTY.
+ *   out_logprobs   device float[B][draws]: log-softmax of z_t over the whole row
+ *                  at the token (NaN for a row without a token); may be NULL.
+ * The sums that decide a token are integers of 2^-42 (V = 2^20) to 2^-45 of the
+ * largest mass, each mass within 2.5e-10 of its value: a token differs from the
+ * exactly computed one with a probability below 1e-4 a draw.  Same inputs give the same outputs.
+ * Row status (vt_get_row_status) is written; seeds, counts and the debug views
+ * are not touched.  One launch; enqueues only; may be captured.  Errors:
+ * VT_ERR_STATE (no vt_reset_params, or B larger than its rows),
+ * VT_ERR_INVALID_ARG (also: a row with penalties or top-p decay),
+ * VT_ERR_CAPACITY (V > max_vocab), VT_ERR_CUDA. */
+#define VT_GIVEN_MAX_DRAWS 65536
+int vt_sample_given(vt_sampler* handle, const void* logits, int32_t dtype, int32_t B, int32_t V,
+                    int64_t ld, const float* uniforms, int32_t draws, int32_t* out_tokens,
+                    float* out_logprobs, void* stream);
+
 /* vt_sample from host memory: vt_sample_host_async, then vt_sample_host_wait
  * (the outputs are in the host arrays when it returns).  Errors as vt_sample,
  * plus VT_ERR_STATE when the handle has no host staging (host_io = 0). */
