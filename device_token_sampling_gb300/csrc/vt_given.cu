@@ -7,11 +7,11 @@
 // kept mass.
 //
 // Tokens are whole numbers decided by comparing sums of up to 2^20 masses, so
-// masses are fixed-point integers: their sums are exact and the same in any
-// order, and a mass is within 2.5e-10 of exp() in relative terms plus half a
-// unit of the fixed point (mass_of).  A prefix of N random such errors moves a
-// boundary by about 2.5e-10 / sqrt(N) of W, which puts the chance of a row's
-// token differing from the exact one below 1e-5 even for a flat row.
+// masses are integers (struct Mass): their sums are exact and the same in any
+// order, and a mass is within 6e-10 (rms 2e-10) of exp() in relative terms.  A
+// prefix of N such errors moves a boundary by about 2e-10 / sqrt(N) of W (N the
+// distinct values among bf16 logits), which puts the chance of a draw differing
+// from the exact one below 1e-5 even for a flat row.
 //
 // One thread-block cluster to a row.  Each CTA keeps its slice of the row in
 // shared memory (one read of the logits); everything after that runs on chip,
@@ -32,51 +32,77 @@ constexpr int kGivenThreads = 512;
 constexpr int kGivenWarps = kGivenThreads / 32;
 constexpr int kSeg = 512;           // elements a warp takes at a time, in vocabulary order
 constexpr int kMaxSegs = 128;       // segments of a slice
-constexpr int kSelBins = 2048;
+constexpr int kBins = 2048;
+constexpr float kBinsPerNat = 64.f;  // linear bins: 32 nats below the maximum, then one for all
+constexpr int kList = 2048;         // candidates a row's leader CTA holds
+constexpr int kListTopK = 1024;     // largest top-k taken from the threads' maxima
 constexpr int kLoadChunks = 8;
 constexpr int kMaxIdx = 0x7fffffff;
-constexpr uint32_t kLowestKey = 0x00800000u;  // ord_key(-FLT_MAX): every finite element
 
-// 2^(-i/128) in units of 2^-31, from powers of 2^(-1/128).
+// 2^(i/128) in units of 2^-30, from powers of 2^(1/128).
 struct MassTable {
   uint32_t v[128];
   constexpr MassTable() : v() {
-    double x = 2147483648.0;
+    double x = 1073741824.0;
     for (int i = 0; i < 128; ++i) {
       v[i] = (uint32_t)(x + 0.5);
-      x *= 0.99459942348363317565247768622217;
+      x *= 1.0054299011128028;
     }
   }
 };
 __constant__ MassTable c_mass_table = MassTable();
 
-// exp(z - m) for z <= m in units of 2^-S, rounded to nearest.
-//   z - m = dh + dl exactly (Knuth's TwoSum); t = -(dh + dl) log2(e) as th + tl
-//   with an error below 2^-45; k = the multiple of 1/128 next to t, r = k - t in
-//   [-1/256, 1/256], so that w = 2^-floor(k) * table[128 frac(k)] * 2^r and
-//   2^r - 1 is a cubic within 2^-38, whose fp32 evaluation is off by 2^-33.
-__device__ __forceinline__ uint64_t mass_of(float z, float m, int S, const uint32_t* table) {
-  const float dh = __fsub_rn(z, m);
-  const float bb = __fsub_rn(dh, z);
-  const float aa = __fsub_rn(dh, bb);
-  const float dl = __fadd_rn(__fsub_rn(z, aa), __fsub_rn(-m, bb));
-  const float th = __fmul_rn(-dh, kLog2e);
-  float tl = __fmaf_rn(-dh, kLog2e, -th);
-  tl = __fmaf_rn(-dh, 1.92596299e-8f, tl);  // log2(e) - fl(log2(e))
-  tl = __fmaf_rn(-dl, kLog2e, tl);
-  if (!(th < 62.f)) return 0;  // -inf, or below half a unit
-  const float magic = 12582912.f;  // 1.5 * 2^23: the integer next to 128 th in the low bits
-  const float kb = __fmaf_rn(th, 128.f, magic);
-  const int k = __float_as_int(kb) - __float_as_int(magic);
-  const float r = __fsub_rn(__fmaf_rn(__fsub_rn(kb, magic), 0.0078125f, -th), tl);
-  const float q = __fmul_rn(
-      r, __fmaf_rn(r, __fmaf_rn(r, 0.0555041087f, 0.240226507f), 0.693147181f));
-  const int qi = __float2int_rn(__fmul_rn(q, 0x1p38f));
-  const uint32_t t = table[k & 127];
-  const int64_t mant = ((int64_t)t << 31) + (((int64_t)(uint64_t)t * qi) >> 7);
-  const int sh = 62 - S + (k >> 7);
-  return sh > 62 ? 0ull : (uint64_t)((mant + (1ll << (sh - 1))) >> sh);
-}
+constexpr int kElemBits = 53;  // masses of single elements: units of 2^-53 of 2^E
+
+// Masses as integers: exp(z) = 2^(z log2(e)) relative to 2^E, the power of two
+// next above the maximum, so that no subtraction of the maximum rounds.
+//   p + e = z log2(e) with an error below 2^-40; k = the multiple of 1/128 next
+//   to p, r = p - k + e in [-1/256, 1/256]: the mass is 2^floor(k) *
+//   table[128 frac(k)] * 2^r, and 2^r - 1 is a cubic within 2^-38 whose fp32
+//   evaluation is off by 2^-33.
+// About 25 instructions, no division, one conversion and one shared load.  For a
+// maximum beyond 2^13 the reduction would run out of bits; there z - m is
+// exact wherever the mass is not 0 (z within a factor 2 of m), so the row's
+// values are shifted by c = m (else c = 0).
+struct Mass {
+  float inv_t, c, floor_p;
+  int e128;  // 128 * E
+  const uint32_t* table;
+
+  __device__ __forceinline__ Mass(float inv_t_, float m, const uint32_t* table_) {
+    inv_t = inv_t_;
+    table = table_;
+    c = fabsf(m) < 8192.f ? 0.f : m;
+    const int E = (int)floorf(__fmul_rn(m - c, kLog2e)) + 1;
+    e128 = E * 128;
+    floor_p = (float)(E - 62);
+  }
+  __device__ __forceinline__ float z(float x) const { return __fmul_rn(x, inv_t); }
+  // mass of the tempered value z in units of 2^(E - kElemBits), truncated
+  __device__ __forceinline__ uint64_t of(float z) const {
+    z = __fsub_rn(z, c);
+    const float p = fmaxf(__fmul_rn(z, kLog2e), floor_p);  // -inf and far below: mass 0
+    const float e = __fmaf_rn(z, 1.92596303e-8f, __fmaf_rn(z, kLog2e, -p));
+    const float magic = 12582912.f;  // 1.5 * 2^23: the integer next to 128 p in the low bits
+    const float kb = __fmaf_rn(p, 128.f, magic);
+    const int k = __float_as_int(kb) - __float_as_int(magic);
+    const float r = __fadd_rn(__fmaf_rn(__fsub_rn(kb, magic), -0.0078125f, p), e);
+    const float q = __fmul_rn(r, __fmaf_rn(r, __fmaf_rn(r, 238388332.f, 1031764991.f),
+                                           2977044472.f));  // (2^r - 1) 2^32
+    const int sh = 62 - kElemBits + ((e128 - k + 127) >> 7);
+    const int64_t t = (int64_t)table[k & 127];
+    const int64_t mant = (t << 32) + t * (int64_t)__float2int_rn(q);
+    return p == floor_p ? 0ull : (uint64_t)mant >> sh;
+  }
+  // ln of a sum of masses in units of 2^(E - bits), relative to the maximum m
+  __device__ __forceinline__ float ln_sum(uint64_t w, int bits, float m) const {
+    const float E = (float)(e128 >> 7);
+    const float lw = logf(__ull2float_rn(w) * exp2f((float)-bits));
+    // E ln 2 - (m - c) in one rounding, ln 2 in two parts
+    return lw + (__fmaf_rn(E, 0.693147182464599609375f, -__fsub_rn(m, c)) +
+                 E * -1.904654299957e-9f);
+  }
+};
 
 // floor(f * W) for 0 <= f < 1, exactly; f >= 1 gives W - 1, f <= 0 and NaN give 0.
 __device__ __forceinline__ uint64_t part_of(uint64_t W, float f) {
@@ -90,12 +116,12 @@ __device__ __forceinline__ uint64_t part_of(uint64_t W, float f) {
   return sh < 64 ? (hi << (64 - sh)) | (lo >> sh) : hi >> (sh - 64);
 }
 
-// The kept set: keys above `key`, and elements at it up to index `idx`.
+// The kept set: tempered values above z, and those at z up to index idx.
 struct Cut {
-  uint32_t key;
+  float z;
   int idx;
-  __device__ __forceinline__ bool keeps(uint32_t k, int j) const {
-    return k > key || (k == key && j <= idx);
+  __device__ __forceinline__ bool keeps(float v, int j) const {
+    return v >= z && (idx == kMaxIdx || v > z || j <= idx);
   }
 };
 
@@ -104,15 +130,11 @@ struct Cut {
 struct Shown {
   float max;
   float expsum;
-  uint64_t mass;
+  uint64_t mass, all;
   int count;
   int index;
-};
-
-struct Found {
-  int bin;
-  uint32_t count;      // elements in the bin
-  uint64_t above_n, above_w;
+  Cut cut;
+  int ok;
 };
 
 template <typename T>
@@ -152,6 +174,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// Inclusive sums over a warp.
+template <typename U>
+__device__ __forceinline__ U warp_scan(U v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const U p = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += p;
+  }
+  return v;
+}
+
 template <typename T, bool STAGED>
 struct Slice {
   static constexpr int N = Vec<T>::N;
@@ -173,161 +207,209 @@ struct Slice {
     }
   }
   __device__ __forceinline__ int segs() const { return n > 0 ? (n + kSeg - 1) / kSeg : 0; }
+  // position of the first of a lane's N elements in iteration i of segment s
+  static __device__ __forceinline__ int at(int s, int i) {
+    return s * kSeg + (i * 32 + (threadIdx.x & 31)) * N;
+  }
+};
+
+// The candidates of a row in vocabulary order, on its leader CTA.
+struct List {
+  uint32_t key[kList];  // ord_key of the tempered value
+  int idx[kList];
+  uint64_t mass[kList];
+};
+
+struct Hist {
+  uint32_t n[kBins];
+  uint64_t w[kBins];
 };
 
 struct Shared {
   Shown shown;
-  Found found;
-  int best;
-  uint32_t table[128];
   float red_f[kGivenWarps];
-  uint64_t red_w[kGivenWarps];
+  uint64_t red_w[kGivenWarps], red_w2[kGivenWarps];
   uint32_t red_n[kGivenWarps];
   int red_i[kGivenWarps];
   uint64_t bars[kLoadChunks];
+  uint32_t table[128];
   uint64_t seg_w[kMaxSegs];   // masses of the segments, then their inclusive sums
-  int seg_n[kMaxSegs];
-  uint32_t hist_n[kSelBins];
-  uint64_t hist_w[kSelBins];
+  int seg_n[kMaxSegs];        // candidates of the segments, then those before each
+  int lo, hi;
+  int bin;
+  uint32_t bin_n;
+  uint64_t above_n, above_w;
+  union {
+    Hist hist;
+    List list;
+  };
 };
 
-// The row's boundary by radix selection on the order key, 11 + 11 + 10 bits.
+// The row of this cluster.
+template <typename T, bool STAGED>
+struct Row {
+  Slice<T, STAGED> sl;
+  Shared& sh;
+  Mass mass;
+  float m;        // tempered maximum
+  int slice;      // elements per CTA
+  int drop;       // row sums are in units of 2^(E - kElemBits + drop)
+  __device__ __forceinline__ Row(const Slice<T, STAGED>& sl_, Shared& sh_, const Mass& mass_,
+                                 float m_, int slice_, int drop_)
+      : sl(sl_), sh(sh_), mass(mass_), m(m_), slice(slice_),
+        drop(drop_) {}
+  __device__ __forceinline__ Shared* at(int rank) {
+    return cg::this_cluster().map_shared_rank(&sh, rank);
+  }
+  __device__ __forceinline__ uint64_t coarse(uint64_t w) const {
+    return (w + (1ull << (drop - 1))) >> drop;
+  }
+  __device__ __forceinline__ float bins_below(float z) const {
+    return __fmul_rn(__fsub_rn(m, z), kBinsPerNat);
+  }
+};
+
+__device__ __forceinline__ int bin_of(float t) {
+  return t < (float)(kBins - 1) ? (int)t : kBins - 1;
+}
+
+// Block-wide exclusive sums of (n, w) in thread order; ends with the warps' sums
+// in red_n / red_w (not yet safe to overwrite).
+__device__ __forceinline__ void block_scan(Shared& sh, uint64_t n, uint64_t w, uint64_t* en,
+                                           uint64_t* ew) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t in = warp_scan(n), iw = warp_scan(w);
+  if (lane == 31) {
+    sh.red_w2[warp] = in;
+    sh.red_w[warp] = iw;
+  }
+  __syncthreads();
+  uint64_t bn = in - n, bw = iw - w;
+  for (int i = 0; i < warp; ++i) {
+    bn += sh.red_w2[i];
+    bw += sh.red_w[i];
+  }
+  *en = bn;
+  *ew = bw;
+}
+
+// The row's boundary by radix selection on the order key, 11 + 11 + 10 bits, for
+// any number of equal elements.  The way of last resort: it counts every element
+// by shared atomics, thousands to an address.
 //   MASS: elements are kept while the mass before them is <= target.
 //   else: the first `target` of them are kept (1 <= target <= their number).
 // Every CTA of the cluster returns the same cut.
 template <typename T, bool STAGED, bool MASS>
-__device__ Cut select(const Slice<T, STAGED>& sl, Shared& sh, cg::cluster_group& cluster, Cut cut,
-                      float inv_t, float m, int S, uint64_t target) {
+__device__ __noinline__ Cut radix_select(const Row<T, STAGED>& row_in, Cut cut, uint64_t target) {
+  Row<T, STAGED> rw = row_in;  // in registers
   using SL = Slice<T, STAGED>;
+  const SL& sl = rw.sl;
+  Shared& sh = rw.sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = cluster.num_blocks();
+  const int C = cg::this_cluster().num_blocks();
   uint32_t prefix = 0;
   uint64_t above_n = 0, above_w = 0;
   uint32_t ties = 0;
-  constexpr int kShift[3] = {21, 10, 0}, kBits[3] = {11, 11, 10};
 #pragma unroll 1
   for (int level = 0; level < 3; ++level) {
-    const int shift = kShift[level], bits = kBits[level], top = shift + bits;
-    for (int i = tid; i < kSelBins; i += kGivenThreads) {
-      sh.hist_n[i] = 0;
-      sh.hist_w[i] = 0;
+    const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
+    __syncthreads();
+    for (int i = tid; i < kBins; i += kGivenThreads) {
+      sh.hist.n[i] = 0;
+      sh.hist.w[i] = 0;
     }
-    if (tid == 0) sh.best = -1;
+    if (tid == 0) sh.hi = -1;
     __syncthreads();
     for (int s = warp; s < sl.segs(); s += kGivenWarps) {
 #pragma unroll 1
       for (int i = 0; i < SL::kIters; ++i) {
-        const int at = s * kSeg + (i * 32 + lane) * SL::N;
+        const int at = SL::at(s, i);
         float x[SL::N];
         sl.load(at, x);
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < SL::N; ++e) {
-          const float z = __fmul_rn(x[e], inv_t);
+          const float z = rw.mass.z(x[e]);
+          if (!cut.keeps(z, sl.base + at + e)) continue;
           const uint32_t k = ord_key(z);
-          if (!cut.keeps(k, sl.base + at + e)) continue;
-          if (level > 0 && (k >> top) != prefix) continue;
+          if (level > 0 && (k >> (shift + bits)) != prefix) continue;
           const uint32_t bin = (k >> shift) & ((1u << bits) - 1);
-          atomicAdd(&sh.hist_n[bin], 1u);
+          atomicAdd(&sh.hist.n[bin], 1u);
           if (MASS) {
-            const uint64_t w = mass_of(z, m, S, sh.table);
-            if (w) atomicAdd((unsigned long long*)&sh.hist_w[bin], (unsigned long long)w);
+            const uint64_t w = rw.coarse(rw.mass.of(z));
+            if (w) atomicAdd((unsigned long long*)&sh.hist.w[bin], (unsigned long long)w);
           }
         }
       }
     }
-    cluster.sync();
+    cg::this_cluster().sync();
     // four bins to a thread, in descending order; sums over the cluster, then a scan
-    uint32_t cn[4];
+    uint32_t cn[4], tn = 0;
     uint64_t cw[4], tw = 0;
-    uint32_t tn = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int bin = kSelBins - 1 - (tid * 4 + q);
+      const int bin = kBins - 1 - (tid * 4 + q);
       cn[q] = 0;
       cw[q] = 0;
       for (int r = 0; r < C; ++r) {
-        const Shared* o = cluster.map_shared_rank(&sh, r);
-        cn[q] += o->hist_n[bin];
-        if (MASS) cw[q] += o->hist_w[bin];
+        cn[q] += rw.at(r)->hist.n[bin];
+        if (MASS) cw[q] += rw.at(r)->hist.w[bin];
       }
       tn += cn[q];
       tw += cw[q];
     }
-    uint32_t in = tn;
-    uint64_t iw = tw;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t pn = __shfl_up_sync(0xffffffffu, in, o);
-      const uint64_t pw = __shfl_up_sync(0xffffffffu, iw, o);
-      if (lane >= o) {
-        in += pn;
-        iw += pw;
-      }
-    }
-    if (lane == 31) {
-      sh.red_n[warp] = in;
-      sh.red_w[warp] = iw;
-    }
-    __syncthreads();
-    uint64_t bn = above_n + in - tn, bw = above_w + iw - tw;
-    for (int i = 0; i < warp; ++i) {
-      bn += sh.red_n[i];
-      bw += sh.red_w[i];
-    }
-    uint64_t an = bn, aw = bw;
+    uint64_t bn, bw;
+    block_scan(sh, tn, tw, &bn, &bw);
+    uint64_t an = above_n + bn, aw = above_w + bw;
     int mine = -1;
+    uint64_t mine_n = 0, mine_w = 0;
+    uint32_t mine_c = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const bool here = cn[q] > 0 && (MASS ? aw <= target : an < target);
-      if (here) mine = tid * 4 + q;  // the last such bin holds the boundary
+      if (cn[q] > 0 && (MASS ? aw <= target : an < target)) {
+        mine = tid * 4 + q;  // the last such bin holds the boundary
+        mine_n = an;
+        mine_w = aw;
+        mine_c = cn[q];
+      }
       an += cn[q];
       aw += cw[q];
     }
-    if (mine >= 0) atomicMax(&sh.best, mine);
+    if (mine >= 0) atomicMax(&sh.hi, mine);
     __syncthreads();
-    if (mine >= 0 && mine == sh.best) {
-      an = bn;
-      aw = bw;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (tid * 4 + q == mine) {
-          sh.found.bin = kSelBins - 1 - mine;
-          sh.found.count = cn[q];
-          sh.found.above_n = an;
-          sh.found.above_w = aw;
-        }
-        an += cn[q];
-        aw += cw[q];
-      }
+    if (mine >= 0 && mine == sh.hi) {
+      sh.bin = kBins - 1 - mine;
+      sh.bin_n = mine_c;
+      sh.above_n = mine_n;
+      sh.above_w = mine_w;
     }
-    cluster.sync();  // also: no CTA clears its bins while another reads them
-    prefix = (prefix << bits) | (uint32_t)sh.found.bin;
-    above_n = sh.found.above_n;
-    above_w = sh.found.above_w;
-    ties = sh.found.count;
+    cg::this_cluster().sync();  // also: no CTA clears its bins while another reads them
+    prefix = (prefix << bits) | (uint32_t)sh.bin;
+    above_n = sh.above_n;
+    above_w = sh.above_w;
+    ties = sh.bin_n;
   }
-  const uint32_t key = prefix;
+  const float zk = key_value(prefix);
   uint64_t take;
   if (MASS) {
-    const uint64_t w = mass_of(key_value(key), m, S, sh.table);
+    const uint64_t w = rw.coarse(rw.mass.of(zk));
     take = w ? (target - above_w) / w + 1 : ties;
   } else {
     take = target - above_n;
   }
-  const int old_idx = key == cut.key ? cut.idx : kMaxIdx;
-  if (take >= ties) return Cut{key, old_idx};
+  const int old_idx = zk == cut.z ? cut.idx : kMaxIdx;
+  if (take >= ties) return Cut{zk, old_idx};
 
   // the index of the take-th of the equal elements
   for (int s = warp; s < sl.segs(); s += kGivenWarps) {
     int c = 0;
 #pragma unroll 1
     for (int i = 0; i < SL::kIters; ++i) {
-      const int at = s * kSeg + (i * 32 + lane) * SL::N;
+      const int at = SL::at(s, i);
       float x[SL::N];
       sl.load(at, x);
 #pragma unroll
       for (int e = 0; e < SL::N; ++e)
-        c += ord_key(__fmul_rn(x[e], inv_t)) == key && sl.base + at + e <= old_idx;
+        c += rw.mass.z(x[e]) == zk && sl.base + at + e <= old_idx;
     }
     c = warp_sum_i(c);
     if (lane == 0) sh.seg_n[s] = c;
@@ -339,150 +421,675 @@ __device__ Cut select(const Slice<T, STAGED>& sl, Shared& sh, cg::cluster_group&
     sh.shown.count = c;
     sh.shown.index = -1;
   }
-  cluster.sync();
+  cg::this_cluster().sync();
   uint64_t before = 0;
-  for (int r = 0; r < (int)cluster.block_rank(); ++r)
-    before += cluster.map_shared_rank(&sh, r)->shown.count;
+  for (int r = 0; r < (int)cg::this_cluster().block_rank(); ++r) before += rw.at(r)->shown.count;
   if (take > before && take <= before + sh.shown.count && warp == 0) {
     int left = (int)(take - before), s = 0;
     while (left > sh.seg_n[s]) left -= sh.seg_n[s++];
-    for (int i = 0; i < SL::kIters; ++i) {
-      const int at = s * kSeg + (i * 32 + lane) * SL::N;
+    for (int i = 0; i < SL::kIters && left > 0; ++i) {
+      const int at = SL::at(s, i);
       float x[SL::N];
       sl.load(at, x);
       int c = 0;
 #pragma unroll
-      for (int e = 0; e < SL::N; ++e)
-        c += ord_key(__fmul_rn(x[e], inv_t)) == key && sl.base + at + e <= old_idx;
-      int inc = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += t;
-      }
+      for (int e = 0; e < SL::N; ++e) c += rw.mass.z(x[e]) == zk && sl.base + at + e <= old_idx;
+      const int inc = warp_scan(c);
       if (left > inc - c && left <= inc) {
-        int at_tie = left - (inc - c);
+        int nth = left - (inc - c);
 #pragma unroll
         for (int e = 0; e < SL::N; ++e)
-          if (ord_key(__fmul_rn(x[e], inv_t)) == key && --at_tie == 0)
-            sh.shown.index = sl.base + at + e;
+          if (rw.mass.z(x[e]) == zk && --nth == 0) sh.shown.index = sl.base + at + e;
       }
       left -= __shfl_sync(0xffffffffu, inc, 31);
-      if (left <= 0) break;
     }
   }
-  cluster.sync();
+  cg::this_cluster().sync();
   int idx = -1;
-  for (int r = 0; r < C; ++r) idx = max(idx, cluster.map_shared_rank(&sh, r)->shown.index);
-  cluster.sync();
-  return Cut{key, idx};
+  for (int r = 0; r < C; ++r) idx = max(idx, rw.at(r)->shown.index);
+  cg::this_cluster().sync();
+  return Cut{zk, idx};
 }
 
-// Mass (and number) of the kept elements, by segment into sh.seg_w as inclusive
-// sums; returns the cluster's total and, in *before, that of the CTAs ahead.
-template <typename T, bool STAGED>
-__device__ uint64_t kept_mass(const Slice<T, STAGED>& sl, Shared& sh, cg::cluster_group& cluster,
-                              const Cut& cut, float inv_t, float m, int S, uint64_t* before) {
-  using SL = Slice<T, STAGED>;
+// The boundary within the leader's list of n candidates (in vocabulary order), by
+// radix selection on the order key, 8 bits at a time; `target` as above, masses
+// in list units.  Called by all threads of the leader.
+template <bool MASS>
+__device__ __noinline__ Cut list_select(Shared& sh, uint32_t* hn, unsigned long long* hw, int n,
+                                        uint64_t target) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t prefix = 0;
+  uint64_t before = 0;  // elements (or mass) ahead of the prefix
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (tid < 256) {
+      hn[tid] = 0;
+      if (MASS) hw[tid] = 0;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kGivenThreads) {
+      const uint32_t k = sh.list.key[i];
+      if (shift < 24 && (k >> (shift + 8)) != prefix) continue;
+      const int bin = (k >> shift) & 255;
+      if (MASS) {
+        const uint64_t w = sh.list.mass[i];
+        if (!w) continue;  // no part in the selection by mass
+        atomicAdd(&hw[bin], (unsigned long long)w);
+      }
+      atomicAdd(&hn[bin], 1u);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // lane l owns bins 255 - 8l .. 248 - 8l
+      uint64_t v[8], sum = 0;
+      uint32_t c[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        c[q] = hn[255 - 8 * lane - q];
+        v[q] = MASS ? (uint64_t)hw[255 - 8 * lane - q] : c[q];
+        sum += v[q];
+      }
+      uint64_t a = before + warp_scan(sum) - sum;
+      int mine = -1;
+      uint64_t mine_a = 0;
+      uint32_t mine_c = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (c[q] > 0 && (MASS ? a <= target : a < target)) {
+          mine = 8 * lane + q;
+          mine_a = a;
+          mine_c = c[q];
+        }
+        a += v[q];
+      }
+      const unsigned has = __ballot_sync(0xffffffffu, mine >= 0);
+      if (has && lane == 31 - __clz(has)) {
+        sh.bin = 255 - mine;
+        sh.bin_n = mine_c;
+        sh.above_w = mine_a;
+      }
+    }
+    __syncthreads();
+    prefix = (prefix << 8) | (uint32_t)sh.bin;
+    before = sh.above_w;
+  }
+  // the take-th of the elements at the key, in vocabulary order
+  if (warp == 0) {
+    const uint32_t ties = sh.bin_n;
+    int found = kMaxIdx;
+    uint32_t seen = 0;
+    uint64_t take = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      const bool tie = i < n && sh.list.key[i] == prefix && (!MASS || sh.list.mass[i] > 0);
+      const unsigned mask = __ballot_sync(0xffffffffu, tie);
+      if (!mask) continue;
+      if (take == 0) {
+        const uint64_t w = MASS ? sh.list.mass[i0 + __ffs(mask) - 1] : 1;
+        take = MASS ? (target - before) / w + 1 : target - before;
+        if (take >= ties) break;
+      }
+      const uint32_t rank = seen + __popc(mask & ((1u << lane) - 1)) + 1;
+      if (tie && rank == take) found = sh.list.idx[i];
+      seen += __popc(mask);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) found = min(found, __shfl_xor_sync(0xffffffffu, found, o));
+    if (lane == 0) sh.shown.cut = Cut{key_value(prefix), found};
+  }
+  __syncthreads();
+  return sh.shown.cut;
+}
+
+// The threads' sums of seg_n to the elements before each segment; the CTA's
+// total is returned to every thread of warp 0.
+__device__ __forceinline__ int scan_segments(Shared& sh, int segs) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int s0 = 0; s0 < segs; s0 += 32) {
+    const int c = s0 + lane < segs ? sh.seg_n[s0 + lane] : 0;
+    const int inc = warp_scan(c) + carry;
+    if (s0 + lane < segs) sh.seg_n[s0 + lane] = inc - c;
+    carry = __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return carry;
+}
+
+// The elements that `wanted` takes, of every CTA, into the leader's list in
+// vocabulary order.  seg_n holds how many each segment has (every warp its own
+// segments, before a block barrier); returns their number in the cluster, or
+// -1 when the list does not hold them.  The caller's next cluster barrier
+// publishes the list.
+template <typename T, bool STAGED, typename F>
+__device__ __forceinline__ int gather(Row<T, STAGED>& rw, F wanted) {
+  using SL = Slice<T, STAGED>;
+  const SL& sl = rw.sl;
+  Shared& sh = rw.sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp == 0) {
+    const int c = scan_segments(sh, sl.segs());
+    if (lane == 0) sh.shown.count = c;
+  }
+  cg::this_cluster().sync();
+  int total = 0, base = 0;
+  for (int r = 0; r < (int)cg::this_cluster().num_blocks(); ++r) {
+    if (r == (int)cg::this_cluster().block_rank()) base = total;
+    total += rw.at(r)->shown.count;
+  }
+  if (total > kList) return -1;
+  List& list = rw.at(0)->list;
+  const int mine = sh.shown.count;
   for (int s = warp; s < sl.segs(); s += kGivenWarps) {
-    uint64_t w = 0;
+    int off = base + sh.seg_n[s];
+    if (off == base + (s + 1 < sl.segs() ? sh.seg_n[s + 1] : mine)) continue;
+    for (int i = 0; i < SL::kIters; ++i) {
+      const int at = SL::at(s, i);
+      float x[SL::N];
+      sl.load(at, x);
+      int c = 0;
+#pragma unroll
+      for (int e = 0; e < SL::N; ++e) c += wanted(x[e], sl.base + at + e);
+      const int inc = warp_scan(c);
+      int p = off + inc - c;
+#pragma unroll
+      for (int e = 0; e < SL::N; ++e)
+        if (wanted(x[e], sl.base + at + e)) {
+          list.key[p] = ord_key(rw.mass.z(x[e]));
+          list.idx[p] = sl.base + at + e;
+          ++p;
+        }
+      off += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  return total;
+}
+
+// Elements kept by a cut in the linear bins lo .. hi.
+template <typename T, bool STAGED>
+struct InBins {
+  const Row<T, STAGED>& rw;
+  Cut cut;
+  int lo, hi;
+  __device__ __forceinline__ bool operator()(float x, int j) const {
+    const float z = rw.mass.z(x);
+    const int bin = bin_of(rw.bins_below(z));
+    return cut.keeps(z, j) && bin >= lo && bin <= hi;
+  }
+};
+
+constexpr int kListDrop = 2;  // list masses: units of 2^(E - kElemBits + 2), 2048 below 2^62
+
+// The boundary of the elements kept by `cut` by one linear histogram below the
+// maximum, which brackets it, and a list of the elements in the bracket.
+//   MASS: target is the top-p share `p`; on success the CTAs' seg_w hold the
+//   masses of the kept elements (element units) and *row_mass the mass of all
+//   elements kept by `cut`.
+//   else: the first `top_k` are kept.
+// Returns false (the same in every CTA) when the bracket holds too many.
+template <typename T, bool STAGED, bool MASS>
+__device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_io, float p, int top_k,
+                                         uint64_t* row_mass) {
+  Row<T, STAGED> rw = row_in;  // in registers
+  using SL = Slice<T, STAGED>;
+  const SL& sl = rw.sl;
+  Shared& sh = rw.sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = cg::this_cluster().num_blocks();
+  const Cut cut = *cut_io;
+  for (int i = tid; i < kBins; i += kGivenThreads) sh.hist.n[i] = 0;
+  if (tid == 0) {
+    sh.lo = kBins;
+    sh.hi = -1;
+  }
+  __syncthreads();
+  // by mass: each element adds its mass relative to its bin's upper edge in
+  // units of 2^-12, so a bin's mass is known to within 1.3e-4 of itself
+  for (int s = warp; s < sl.segs(); s += kGivenWarps) {
 #pragma unroll 1
     for (int i = 0; i < SL::kIters; ++i) {
-      const int at = s * kSeg + (i * 32 + lane) * SL::N;
+      const int at = SL::at(s, i);
       float x[SL::N];
       sl.load(at, x);
 #pragma unroll
       for (int e = 0; e < SL::N; ++e) {
-        const float z = __fmul_rn(x[e], inv_t);
-        if (cut.keeps(ord_key(z), sl.base + at + e)) w += mass_of(z, m, S, sh.table);
+        const float z = rw.mass.z(x[e]);
+        if (!cut.keeps(z, sl.base + at + e)) continue;
+        const float t = rw.bins_below(z);
+        const int bin = bin_of(t);
+        uint32_t add = 1;
+        if (MASS) {
+          const float f = t - (float)bin;
+          add = bin == kBins - 1 ? 0 : (uint32_t)__fmaf_rn(f, __fmaf_rn(f, 0.5f, -64.f), 4096.5f);
+        }
+        if (add) atomicAdd(&sh.hist.n[bin], add);
+      }
+    }
+  }
+  cg::this_cluster().sync();
+  uint32_t cn[4];
+  uint64_t tn = 0;
+  float cf[4], tf = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int bin = tid * 4 + q;
+    uint64_t c = 0;
+    for (int r = 0; r < C; ++r) c += rw.at(r)->hist.n[bin];
+    cn[q] = (uint32_t)min(c, (uint64_t)0xffffffffu);
+    cf[q] = MASS ? (float)c * ex2_approx((float)bin * (-kLog2e / kBinsPerNat)) : 0.f;
+    tn += c;
+    tf += cf[q];
+  }
+  uint64_t above_n = 0;  // elements above the bracket (by count)
+  if (MASS) {
+    const float inc = warp_scan(tf);
+    if (lane == 31) sh.red_f[warp] = inc;
+    __syncthreads();
+    float a = inc - tf, all = 0.f;
+    for (int i = 0; i < kGivenWarps; ++i) {
+      if (i < warp) a += sh.red_f[i];
+      all += sh.red_f[i];
+    }
+    constexpr float kSlack = 1.f / 1024;  // bins and sums, both sides
+    const float want = p * all;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (cn[q] > 0) {
+        // bins that end before the target are kept whole, those that begin
+        // after it not at all
+        if (a + cf[q] >= want * (1.f - kSlack)) atomicMin(&sh.lo, tid * 4 + q);
+        if (a <= want * (1.f + kSlack)) atomicMax(&sh.hi, tid * 4 + q);
+      }
+      a += cf[q];
+    }
+  } else {
+    uint64_t a, unused;
+    block_scan(sh, tn, 0, &a, &unused);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (a < (uint64_t)top_k && a + cn[q] >= (uint64_t)top_k) {
+        sh.lo = sh.hi = tid * 4 + q;
+        sh.above_n = a;
+      }
+      a += cn[q];
+    }
+  }
+  __syncthreads();
+  const int lo = sh.lo, hi = sh.hi;
+  above_n = MASS ? 0 : sh.above_n;
+  if (lo > hi) return false;  // (a histogram without mass)
+
+  uint64_t w_above = 0, w_all = 0;
+  for (int s = warp; s < sl.segs(); s += kGivenWarps) {
+    uint64_t above = 0, rest = 0;
+    int c = 0;
+#pragma unroll 1
+    for (int i = 0; i < SL::kIters; ++i) {
+      const int at = SL::at(s, i);
+      float x[SL::N];
+      sl.load(at, x);
+#pragma unroll
+      for (int e = 0; e < SL::N; ++e) {
+        const float z = rw.mass.z(x[e]);
+        const bool in = cut.keeps(z, sl.base + at + e);
+        const int bin = bin_of(rw.bins_below(z));
+        c += in && bin >= lo && bin <= hi;
+        if (MASS) {
+          const uint64_t w = in ? rw.mass.of(z) : 0;
+          if (bin < lo) above += w;
+          else rest += w;
+        }
+      }
+    }
+    c = warp_sum_i(c);
+    if (MASS) {
+      above = warp_sum_u64(above);
+      rest = warp_sum_u64(rest);
+    }
+    if (lane == 0) {
+      sh.seg_n[s] = c;
+      if (MASS) {
+        sh.seg_w[s] = above;
+        w_above += rw.coarse(above);
+        w_all += rw.coarse(above + rest);
+      }
+    }
+  }
+  if (MASS && lane == 0) {
+    sh.red_w[warp] = w_above;
+    sh.red_w2[warp] = w_all;
+  }
+  __syncthreads();
+  if (MASS && tid == 0) {
+    w_above = w_all = 0;
+    for (int i = 0; i < kGivenWarps; ++i) {
+      w_above += sh.red_w[i];
+      w_all += sh.red_w2[i];
+    }
+    sh.shown.mass = w_above;
+    sh.shown.all = w_all;
+  }
+  const int n = gather(rw, InBins<T, STAGED>{rw, cut, lo, hi});
+  if (MASS) {
+    w_above = w_all = 0;
+    for (int r = 0; r < C; ++r) {
+      w_above += rw.at(r)->shown.mass;
+      w_all += rw.at(r)->shown.all;
+    }
+    *row_mass = w_all;
+  }
+  cg::this_cluster().sync();
+  if (n <= 0) return false;
+  if (cg::this_cluster().block_rank() == 0) {
+    // scratch for the list's histograms: the segment counts are done with
+    uint32_t* hn = reinterpret_cast<uint32_t*>(&sh.list.mass[0]);
+    unsigned long long* hw = nullptr;
+    bool ok = true;
+    Cut found{0.f, kMaxIdx};
+    if (MASS) {
+      __shared__ uint32_t s_hn[256];
+      __shared__ unsigned long long s_hw[256];
+      hn = s_hn;
+      hw = s_hw;
+      uint64_t mine = 0;
+      for (int i = tid; i < n; i += kGivenThreads) {
+        const uint64_t w = (rw.mass.of(key_value(sh.list.key[i])) + 2) >> kListDrop;
+        sh.list.mass[i] = w;
+        mine += w;
+      }
+      uint64_t e, ew;
+      block_scan(sh, 0, mine, &e, &ew);
+      uint64_t band = 0;
+      for (int i = 0; i < kGivenWarps; ++i) band += sh.red_w[i];
+      const uint64_t target = part_of(w_all, p);
+      // the boundary lies in the bracket: the mass above it is within the
+      // target, that at its end is not
+      ok = w_above <= target;
+      const uint64_t left = ok ? (target - w_above) << (rw.drop - kListDrop) : 0;
+      ok = ok && left < band && (target - w_above) < (1ull << (62 - rw.drop));
+      if (ok) found = list_select<true>(sh, hn, hw, n, left);
+      if (ok)
+        for (int i = tid; i < n; i += kGivenThreads) {
+          const int j = sh.list.idx[i];
+          const float z = key_value(sh.list.key[i]);
+          if (found.keeps(z, j)) {
+            const int r = j / rw.slice;
+            atomicAdd((unsigned long long*)&rw.at(r)->seg_w[(j - r * rw.slice) / kSeg],
+                      (unsigned long long)rw.mass.of(z));
+          }
+        }
+    } else {
+      found = list_select<false>(sh, hn, hw, n, (uint64_t)top_k - above_n);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      sh.shown.cut = found;
+      sh.shown.ok = ok;
+    }
+  }
+  cg::this_cluster().sync();
+  const Cut found = rw.at(0)->shown.cut;
+  const bool ok = rw.at(0)->shown.ok;
+  if (ok) *cut_io = found;
+  return ok;
+}
+
+// Masses of the kept elements by segment, into seg_w (element units).
+template <typename T, bool STAGED>
+__device__ __noinline__ void kept_mass(const Row<T, STAGED>& row_in, const Cut cut) {
+  Row<T, STAGED> rw = row_in;  // in registers
+  using SL = Slice<T, STAGED>;
+  const SL& sl = rw.sl;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int s = warp; s < sl.segs(); s += kGivenWarps) {
+    uint64_t w = 0;
+#pragma unroll 1
+    for (int i = 0; i < SL::kIters; ++i) {
+      const int at = SL::at(s, i);
+      float x[SL::N];
+      sl.load(at, x);
+#pragma unroll
+      for (int e = 0; e < SL::N; ++e) {
+        const float z = rw.mass.z(x[e]);
+        const uint64_t v = rw.mass.of(z);
+        w += cut.keeps(z, sl.base + at + e) ? v : 0;
       }
     }
     w = warp_sum_u64(w);
-    if (lane == 0) sh.seg_w[s] = w;
+    if (lane == 0) rw.sh.seg_w[s] = w;
   }
+}
+
+// seg_w to inclusive sums in row units; the cluster's total, and the mass of the
+// CTAs before this one.
+template <typename T, bool STAGED>
+__device__ uint64_t sum_segments(Row<T, STAGED>& rw, uint64_t* before) {
+  Shared& sh = rw.sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, segs = rw.sl.segs();
   __syncthreads();
   if (warp == 0) {
     uint64_t carry = 0;
-    for (int s0 = 0; s0 < sl.segs(); s0 += 32) {
-      uint64_t w = s0 + lane < sl.segs() ? sh.seg_w[s0 + lane] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t p = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += p;
-      }
-      w += carry;
-      if (s0 + lane < sl.segs()) sh.seg_w[s0 + lane] = w;
+    for (int s0 = 0; s0 < segs; s0 += 32) {
+      const uint64_t w =
+          warp_scan(s0 + lane < segs ? rw.coarse(sh.seg_w[s0 + lane]) : (uint64_t)0) + carry;
+      if (s0 + lane < segs) sh.seg_w[s0 + lane] = w;
       carry = __shfl_sync(0xffffffffu, w, 31);
     }
     if (lane == 0) sh.shown.mass = carry;
   }
-  cluster.sync();
+  cg::this_cluster().sync();
   uint64_t total = 0, b = 0;
-  for (int r = 0; r < (int)cluster.num_blocks(); ++r) {
-    if (r == (int)cluster.block_rank()) b = total;
-    total += cluster.map_shared_rank(&sh, r)->shown.mass;
+  for (int r = 0; r < (int)cg::this_cluster().num_blocks(); ++r) {
+    if (r == (int)cg::this_cluster().block_rank()) b = total;
+    total += rw.at(r)->shown.mass;
   }
-  cluster.sync();
+  cg::this_cluster().sync();
   *before = b;
   return total;
 }
 
 // The first kept element of this CTA whose inclusive mass (from the CTA's start)
-// exceeds t; one warp, t below the CTA's mass.
+// exceeds t (row units, below the CTA's mass); one warp.
 template <typename T, bool STAGED>
-__device__ int find_draw(const Slice<T, STAGED>& sl, const Shared& sh, const Cut& cut, float inv_t,
-                         float m, int S, uint64_t t, float* z_out) {
+__device__ int find_draw(const Row<T, STAGED>& rw, const Cut& cut, uint64_t t, float* z_out) {
   using SL = Slice<T, STAGED>;
+  const SL& sl = rw.sl;
   const int lane = threadIdx.x & 31;
   int s = 0;
   for (int s0 = 0; s0 < sl.segs(); s0 += 32) {
-    const bool past = s0 + lane < sl.segs() && sh.seg_w[s0 + lane] <= t;
+    const bool past = s0 + lane < sl.segs() && rw.sh.seg_w[s0 + lane] <= t;
     s += __popc(__ballot_sync(0xffffffffu, past));
   }
-  if (s > 0) t -= sh.seg_w[s - 1];
+  if (s > 0) t -= rw.sh.seg_w[s - 1];
+  t <<= rw.drop;  // element units
   int idx = -1;
   float zz = 0.f;
   for (int i = 0; i < SL::kIters; ++i) {
-    const int at = s * kSeg + (i * 32 + lane) * SL::N;
+    const int at = SL::at(s, i);
     float x[SL::N];
     sl.load(at, x);
     uint64_t w[SL::N], sum = 0;
 #pragma unroll
     for (int e = 0; e < SL::N; ++e) {
-      const float z = __fmul_rn(x[e], inv_t);
-      w[e] = cut.keeps(ord_key(z), sl.base + at + e) ? mass_of(z, m, S, sh.table) : 0;
+      const float z = rw.mass.z(x[e]);
+      w[e] = cut.keeps(z, sl.base + at + e) ? rw.mass.of(z) : 0;
       sum += w[e];
     }
-    uint64_t inc = sum;
+    const uint64_t inc = warp_scan(sum);
+    uint64_t run = inc - sum;
+    // the segment's sum was rounded to row units: a t within that of its end
+    // takes the last element that has mass
+    int here = -1, last = -1;
+    float z_here = 0.f, z_last = 0.f;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t p = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += p;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, inc > t);
-    if (hit) {
-      const int owner = __ffs(hit) - 1;
-      uint64_t run = inc - sum;
-#pragma unroll
-      for (int e = 0; e < SL::N; ++e) {
-        run += w[e];
-        if (idx < 0 && run > t) {
-          idx = sl.base + at + e;
-          zz = __fmul_rn(x[e], inv_t);
+    for (int e = 0; e < SL::N; ++e) {
+      run += w[e];
+      if (w[e] > 0) {
+        last = sl.base + at + e;
+        z_last = rw.mass.z(x[e]);
+        if (here < 0 && run > t) {
+          here = last;
+          z_here = z_last;
         }
       }
-      *z_out = __shfl_sync(0xffffffffu, zz, owner);
-      return __shfl_sync(0xffffffffu, idx, owner);
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, here >= 0);
+    if (hit) {
+      const int owner = __ffs(hit) - 1;
+      *z_out = __shfl_sync(0xffffffffu, z_here, owner);
+      return __shfl_sync(0xffffffffu, here, owner);
+    }
+    const unsigned any = __ballot_sync(0xffffffffu, last >= 0);
+    if (any) {
+      const int owner = 31 - __clz(any);
+      zz = __shfl_sync(0xffffffffu, z_last, owner);
+      idx = __shfl_sync(0xffffffffu, last, owner);
     }
     t -= __shfl_sync(0xffffffffu, inc, 31);
   }
-  *z_out = 0.f;
-  return -1;
+  *z_out = zz;
+  return idx;
+}
+
+// A row with 1 < top_k <= kListTopK: the threads' maxima give a value that at
+// least top_k elements reach; those elements go to the leader's list, where
+// min-p, top-k and top-p are settled and the draws made.  Adds ln sum exp on the
+// way.  Returns false (in every CTA) when the list does not hold them.
+template <typename T, bool STAGED>
+__device__ __noinline__ bool draw_from_list(const Row<T, STAGED>& row_in, const GivenArgs& a,
+                                            const RowParams& P, const Cut minp, float thread_max,
+                                            int row, float* ln_s_out) {
+  Row<T, STAGED> rw = row_in;  // in registers
+  using SL = Slice<T, STAGED>;
+  const SL& sl = rw.sl;
+  Shared& sh = rw.sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = cg::this_cluster().num_blocks();
+  for (int i = tid; i < kBins; i += kGivenThreads) sh.hist.n[i] = 0;
+  if (tid == 0) sh.hi = kBins - 1;
+  __syncthreads();
+  if (thread_max > -INFINITY)
+    atomicAdd(&sh.hist.n[bin_of(rw.bins_below(rw.mass.z(thread_max)))], 1u);
+  cg::this_cluster().sync();
+  {
+    uint32_t cn[4];
+    uint64_t tn = 0, b, unused;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      cn[q] = 0;
+      for (int r = 0; r < C; ++r) cn[q] += rw.at(r)->hist.n[tid * 4 + q];
+      tn += cn[q];
+    }
+    block_scan(sh, tn, 0, &b, &unused);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (b < (uint64_t)P.top_k && b + cn[q] >= (uint64_t)P.top_k) sh.hi = tid * 4 + q;
+      b += cn[q];
+    }
+  }
+  __syncthreads();
+  // (fewer than top_k threads with a finite element: every finite element)
+  const float edge = sh.hi == kBins - 1 ? INFINITY : (float)(sh.hi + 1);
+  auto wanted = [&](float x, int) { return rw.bins_below(rw.mass.z(x)) < edge; };
+  float expsum = 0.f;
+  for (int s = warp; s < sl.segs(); s += kGivenWarps) {
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < SL::kIters; ++i) {
+      float x[SL::N];
+      sl.load(SL::at(s, i), x);
+#pragma unroll
+      for (int e = 0; e < SL::N; ++e) {
+        const float t = rw.bins_below(rw.mass.z(x[e]));
+        c += t < edge;
+        expsum += ex2_approx(__fmul_rn(t, -kLog2e / kBinsPerNat));
+      }
+    }
+    c = warp_sum_i(c);
+    if (lane == 0) sh.seg_n[s] = c;
+  }
+  expsum = warp_sum_f(expsum);
+  if (lane == 0) sh.red_f[warp] = expsum;
+  __syncthreads();
+  if (tid == 0) {
+    expsum = 0.f;
+    for (int i = 0; i < kGivenWarps; ++i) expsum += sh.red_f[i];
+    sh.shown.expsum = expsum;
+  }
+  const int n = gather(rw, wanted);
+  expsum = 0.f;
+  for (int r = 0; r < C; ++r) expsum += rw.at(r)->shown.expsum;
+  const float ln_s = logf(expsum);
+  *ln_s_out = ln_s;
+  cg::this_cluster().sync();
+  if (n < 0) return false;
+  if (cg::this_cluster().block_rank() != 0) return true;
+
+  __shared__ uint32_t s_hn[256];
+  __shared__ unsigned long long s_hw[256];
+  List& list = sh.list;
+  Cut cut = minp;
+  int c = 0;
+  for (int i = tid; i < n; i += kGivenThreads) c += key_value(list.key[i]) >= cut.z;
+  c = warp_sum_i(c);
+  if (lane == 0) sh.red_i[warp] = c;
+  __syncthreads();
+  int kept = 0;
+  for (int i = 0; i < kGivenWarps; ++i) kept += sh.red_i[i];
+  if (kept > P.top_k) {
+    // elements that min-p leaves out come after the others in the order
+    cut = list_select<false>(sh, s_hn, s_hw, n, (uint64_t)P.top_k);
+  }
+  // each thread holds four neighbours of the list
+  uint64_t w[4], sum = 0, total = 0, unused, ahead;
+  auto weigh = [&]() {
+    sum = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = tid * 4 + q;
+      w[q] = 0;
+      if (i < n) {
+        const float z = key_value(list.key[i]);
+        if (cut.keeps(z, list.idx[i])) w[q] = (rw.mass.of(z) + 2) >> kListDrop;
+      }
+      sum += w[q];
+    }
+    __syncthreads();
+    block_scan(sh, 0, sum, &unused, &ahead);
+    total = 0;
+    for (int i = 0; i < kGivenWarps; ++i) total += sh.red_w[i];
+  };
+  weigh();
+  if (P.flags & kRowTopP) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (tid * 4 + q < n) list.mass[tid * 4 + q] = w[q];
+    __syncthreads();
+    cut = list_select<true>(sh, s_hn, s_hw, n, part_of(total, P.top_p));
+    weigh();
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    ahead += w[q];
+    if (tid * 4 + q < n) list.mass[tid * 4 + q] = ahead;  // inclusive
+  }
+  __syncthreads();
+  for (int d = tid; d < a.draws; d += kGivenThreads) {
+    const int64_t o = (int64_t)row * a.draws + d;
+    const uint64_t t = part_of(total, a.uniforms[o]);
+    int lo = 0, hi = n - 1;  // the first entry whose inclusive mass exceeds t
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (list.mass[mid] > t) hi = mid;
+      else lo = mid + 1;
+    }
+    a.out_tokens[o] = list.idx[lo];
+    if (a.out_logprobs)
+      a.out_logprobs[o] = __fsub_rn(__fsub_rn(key_value(list.key[lo]), rw.m), ln_s);
+  }
+  return true;
 }
 
 template <typename T, bool STAGED>
-__global__ void __launch_bounds__(kGivenThreads) given_kernel(GivenArgs a) {
+__global__ void __launch_bounds__(kGivenThreads, 2) given_kernel(GivenArgs a) {
   using SL = Slice<T, STAGED>;
   extern __shared__ __align__(128) unsigned char dyn[];
   Shared& sh = *reinterpret_cast<Shared*>(dyn);
@@ -520,7 +1127,8 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(GivenArgs a) {
     for (int i = n_bulk + tid; i < n_pad; i += kGivenThreads) stage[i] = i < sl.n ? src[i] : none;
     __syncthreads();
     for (int c = 0; c * chunk < n_pad; ++c) {
-      if (c * chunk < n_bulk && !mbar_wait_bounded(&sh.bars[c], 0)) atomicOr(a.err_word, kErrTimeout);
+      if (c * chunk < n_bulk && !mbar_wait_bounded(&sh.bars[c], 0))
+        atomicOr(a.err_word, kErrTimeout);
       const int end = min(n_pad, (c + 1) * chunk);
       for (int at = c * chunk + tid * SL::N; at < end; at += kGivenThreads * SL::N) {
         float x[SL::N];
@@ -537,6 +1145,7 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(GivenArgs a) {
       for (int e = 0; e < SL::N; ++e) mx = max_nan(mx, x[e]);
     }
   }
+  const float thread_max = mx;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (lane == 0) sh.red_f[warp] = mx;
@@ -548,8 +1157,7 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(GivenArgs a) {
   cluster.sync();
   mx = -INFINITY;
   for (int r = 0; r < C; ++r) mx = max_nan(mx, cluster.map_shared_rank(&sh, r)->shown.max);
-  const float inv_t = P.inv_t;
-  const float m = __fmul_rn(mx, inv_t);
+  const float m = __fmul_rn(mx, P.inv_t);
   const int status = isnan(mx) || m == INFINITY ? kRowNonfinite : m == -INFINITY ? kRowEmpty : kRowOk;
   if (rank == 0 && tid == 0) a.row_status[row] = status;
   int32_t* out_tok = a.out_tokens + (int64_t)row * a.draws;
@@ -562,21 +1170,45 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(GivenArgs a) {
     cluster.sync();  // the others have read this CTA's maximum
     return;
   }
+  const Mass mass(P.inv_t, m, sh.table);
+  Row<T, STAGED> rw(sl, sh, mass, m, a.slice, a.drop);
 
-  // ln sum exp(z - m) for the log-probs; a greedy row's lowest index at the maximum
-  float expsum = 0.f;
-  int first = kMaxIdx;
+  Cut cut{-3.402823466e38f, kMaxIdx};
+  if ((P.flags & kRowMinP) && !(P.flags & kRowGreedy)) {
+    // the smallest z with z - m >= ln(min_p), both sides in double
+    float zt = __double2float_rn((double)m + P.log_min_p);
+    if ((double)zt - (double)m < P.log_min_p) {
+      zt = nextafterf(zt, INFINITY);
+    } else {
+      const float below = nextafterf(zt, -INFINITY);
+      if ((double)below - (double)m >= P.log_min_p) zt = below;
+    }
+    cut.z = fmaxf(cut.z, zt);
+  }
   const bool greedy = P.flags & kRowGreedy;
-  if (out_lp || greedy) {
+  const bool topk = !greedy && P.top_k > 1 && P.top_k < a.V;
+  float ln_s = 0.f;
+  bool have_ln_s = false;
+  if (topk && P.top_k <= kListTopK && 2 * P.top_k <= C * kGivenThreads) {
+    if (draw_from_list(rw, a, P, cut, thread_max, row, &ln_s)) return;
+    have_ln_s = true;
+  }
+
+  // ln sum exp(z - m) where the masses will not give it; a greedy row's lowest
+  // index at the maximum
+  const bool all_mass = !greedy && !topk && !(P.flags & kRowMinP);
+  if (greedy || (out_lp && !have_ln_s && !all_mass)) {
+    float expsum = 0.f;
+    int first = kMaxIdx;
     for (int s = warp; s < sl.segs(); s += kGivenWarps) {
-#pragma unroll 1
+#pragma unroll
       for (int i = 0; i < SL::kIters; ++i) {
-        const int at = s * kSeg + (i * 32 + lane) * SL::N;
+        const int at = SL::at(s, i);
         float x[SL::N];
         sl.load(at, x);
 #pragma unroll
         for (int e = 0; e < SL::N; ++e) {
-          expsum += ex2_approx(__fmul_rn(__fsub_rn(__fmul_rn(x[e], inv_t), m), kLog2e));
+          expsum += ex2_approx(__fmul_rn(__fsub_rn(rw.mass.z(x[e]), m), kLog2e));
           if (greedy && x[e] == mx) first = min(first, sl.base + at + e);
         }
       }
@@ -602,48 +1234,35 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(GivenArgs a) {
     cluster.sync();
     expsum = 0.f;
     for (int r = 0; r < C; ++r) {
-      const Shared* o = cluster.map_shared_rank(&sh, r);
-      expsum += o->shown.expsum;
-      first = min(first, o->shown.index);
+      expsum += rw.at(r)->shown.expsum;
+      first = min(first, rw.at(r)->shown.index);
     }
     cluster.sync();
-  }
-  const float ln_s = logf(expsum);
-  if (greedy) {
-    for (int d = rank * kGivenThreads + tid; d < a.draws; d += C * kGivenThreads) {
-      out_tok[d] = first;
-      if (out_lp) out_lp[d] = -ln_s;
+    ln_s = logf(expsum);
+    if (greedy) {
+      for (int d = rank * kGivenThreads + tid; d < a.draws; d += C * kGivenThreads) {
+        out_tok[d] = first;
+        if (out_lp) out_lp[d] = -ln_s;
+      }
+      return;
     }
-    return;
   }
 
   // the kept set
-  const int S = a.mass_bits;
-  Cut cut{kLowestKey, kMaxIdx};
-  if (P.flags & kRowMinP) {
-    // the smallest z with z - m >= ln(min_p), both sides in double
-    float zt = __double2float_rn((double)m + P.log_min_p);
-    if ((double)zt - (double)m < P.log_min_p) {
-      zt = nextafterf(zt, INFINITY);
-    } else {
-      const float below = nextafterf(zt, -INFINITY);
-      if ((double)below - (double)m >= P.log_min_p) zt = below;
-    }
-    cut.key = max(cut.key, ord_key(zt));
-  }
-  if (P.top_k > 1 && P.top_k < a.V) {
+  if (topk) {
+    // (an element count decides whether top-k cuts anything)
     int c = 0;
     for (int s = warp; s < sl.segs(); s += kGivenWarps) {
 #pragma unroll 1
       for (int i = 0; i < SL::kIters; ++i) {
-        const int at = s * kSeg + (i * 32 + lane) * SL::N;
         float x[SL::N];
-        sl.load(at, x);
+        sl.load(SL::at(s, i), x);
 #pragma unroll
-        for (int e = 0; e < SL::N; ++e) c += ord_key(__fmul_rn(x[e], inv_t)) >= cut.key;
+        for (int e = 0; e < SL::N; ++e) c += rw.mass.z(x[e]) >= cut.z;
       }
     }
     c = warp_sum_i(c);
+    __syncthreads();
     if (lane == 0) sh.red_i[warp] = c;
     __syncthreads();
     if (tid == 0) {
@@ -653,17 +1272,26 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(GivenArgs a) {
     }
     cluster.sync();
     int n = 0;
-    for (int r = 0; r < C; ++r) n += cluster.map_shared_rank(&sh, r)->shown.count;
+    for (int r = 0; r < C; ++r) n += rw.at(r)->shown.count;
     cluster.sync();
-    if (n > P.top_k)
-      cut = select<T, STAGED, false>(sl, sh, cluster, cut, inv_t, m, S, (uint64_t)P.top_k);
+    if (n > P.top_k && !band_select<T, STAGED, false>(rw, &cut, 0.f, P.top_k, nullptr))
+      cut = radix_select<T, STAGED, false>(rw, cut, (uint64_t)P.top_k);
   }
-  uint64_t before;
-  uint64_t W = kept_mass(sl, sh, cluster, cut, inv_t, m, S, &before);
+  uint64_t before, W, all;
   if (P.flags & kRowTopP) {
-    cut = select<T, STAGED, true>(sl, sh, cluster, cut, inv_t, m, S, part_of(W, P.top_p));
-    W = kept_mass(sl, sh, cluster, cut, inv_t, m, S, &before);
+    const Cut from = cut;
+    if (!band_select<T, STAGED, true>(rw, &cut, P.top_p, 0, &all)) {
+      kept_mass(rw, from);
+      all = sum_segments(rw, &before);
+      cut = radix_select<T, STAGED, true>(rw, from, part_of(all, P.top_p));
+      kept_mass(rw, cut);
+    }
+    W = sum_segments(rw, &before);
+  } else {
+    kept_mass(rw, cut);
+    W = all = sum_segments(rw, &before);
   }
+  if (all_mass) ln_s = rw.mass.ln_sum(all, kElemBits - a.drop, m);
 
   // the draws: each by a warp of the CTA that holds its mass
   const uint64_t mine = sh.shown.mass;
@@ -671,7 +1299,7 @@ __global__ void __launch_bounds__(kGivenThreads) given_kernel(GivenArgs a) {
     const uint64_t t = part_of(W, a.uniforms[(int64_t)row * a.draws + d]);
     if (t < before || t - before >= mine) continue;
     float z;
-    const int j = find_draw(sl, sh, cut, inv_t, m, S, t - before, &z);
+    const int j = find_draw(rw, cut, t - before, &z);
     if (lane == 0) {
       out_tok[d] = j;
       if (out_lp) out_lp[d] = __fsub_rn(__fsub_rn(z, m), ln_s);
@@ -714,10 +1342,10 @@ cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t strea
                           ((int64_t)a.B * cluster < 2 * num_sms && slice_of(cluster) > 4096)))
     cluster *= 2;
   a.slice = slice_of(cluster);
-  // the largest scale whose sums of V masses stay below 2^63
+  // sums of V masses stay below 2^62
   int bits = 0;
   while ((1ll << bits) < a.V) ++bits;
-  a.mass_bits = min(45, 62 - bits);
+  a.drop = max(kListDrop, bits + kElemBits - 62);
   const size_t head = (sizeof(Shared) + 127) / 128 * 128;
   const size_t staged = head + (size_t)a.slice * es;
   const bool fits = staged <= 227 * 1024 - 1024;

@@ -255,7 +255,7 @@ struct GivenArgs {
   float* out_logprobs;       // [B][draws] or null
   int32_t* row_status;       // [B]
   int32_t* err_word;
-  int32_t slice, mass_bits;  // filled by launch_given
+  int32_t slice, drop;       // filled by launch_given
 };
 cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t stream);
 
