@@ -32,10 +32,12 @@ constexpr int kGivenThreads = 512;
 constexpr int kGivenWarps = kGivenThreads / 32;
 constexpr int kSeg = 512;           // elements a warp takes at a time, in vocabulary order
 constexpr int kMaxSegs = 128;       // segments of a slice
+constexpr int kMaxCtas = 16;        // CTAs of a row at most
 constexpr int kBins = 2048;
 constexpr float kBinsPerNat = 64.f;  // linear bins: 32 nats below the maximum, then one for all
 constexpr int kList = 2048;         // candidates a row's leader CTA holds
-constexpr int kListTopK = 1024;     // largest top-k taken from the threads' maxima
+constexpr int kListTopK = 1024;     // largest top-k taken from group maxima
+constexpr int kListPerThread = kList / kGivenThreads;
 constexpr int kLoadChunks = 8;
 constexpr int kMaxIdx = 0x7fffffff;
 
@@ -125,15 +127,17 @@ struct Cut {
   }
 };
 
-// What a CTA shows the others of its cluster (each field written once between
-// two cluster barriers).
-struct Shown {
-  float max;
-  float expsum;
-  uint64_t mass, all;
-  int count;
-  int index;
-  Cut cut;
+// A CTA's mailboxes: slot r is written by CTA r of its cluster before a cluster
+// barrier and read here after it, so that no reader waits on remote loads.  Each
+// field serves one exchange, or exchanges with another barrier between the
+// reading of one and the writing of the next.
+struct Mail {
+  float max[kMaxCtas];
+  float expsum[kMaxCtas];
+  uint64_t mass[kMaxCtas], all[kMaxCtas], kept[kMaxCtas];
+  int count[kMaxCtas], total[kMaxCtas];
+  int index[kMaxCtas], tie[kMaxCtas];
+  Cut cut;  // from the leader
   int ok;
 };
 
@@ -186,6 +190,8 @@ __device__ __forceinline__ U warp_scan(U v) {
   return v;
 }
 
+static_assert(2 * kListTopK <= kBins, "the groups' maxima fit their array");
+
 template <typename T, bool STAGED>
 struct Slice {
   static constexpr int N = Vec<T>::N;
@@ -217,19 +223,20 @@ struct Slice {
 struct List {
   uint32_t key[kList];  // ord_key of the tempered value
   int idx[kList];
-  uint64_t mass[kList];
 };
 
 struct Hist {
-  uint32_t n[kBins];
-  uint64_t w[kBins];
+  uint32_t own[kBins];
+  union {
+    uint32_t sum[kBins];     // over the cluster
+    float group_max[kBins];  // maxima of groups of elements, of all CTAs
+  };
 };
 
 struct Shared {
-  Shown shown;
+  Mail mail;
   float red_f[kGivenWarps];
-  uint64_t red_w[kGivenWarps], red_w2[kGivenWarps];
-  uint32_t red_n[kGivenWarps];
+  uint64_t red_w[kGivenWarps], red_n[kGivenWarps];
   int red_i[kGivenWarps];
   uint64_t bars[kLoadChunks];
   uint32_t table[128];
@@ -238,7 +245,10 @@ struct Shared {
   int lo, hi;
   int bin;
   uint32_t bin_n;
-  uint64_t above_n, above_w;
+  uint64_t above;
+  uint32_t digit_n[256];      // radix selection, 8 bits at a time
+  unsigned long long digit_w[256];
+  uint64_t run[kGivenThreads];  // inclusive masses of the threads' list entries
   union {
     Hist hist;
     List list;
@@ -261,6 +271,13 @@ struct Row {
   __device__ __forceinline__ Shared* at(int rank) {
     return cg::this_cluster().map_shared_rank(&sh, rank);
   }
+  // thread r of the block stores v in this CTA's slot of CTA r's mailbox
+  template <typename V>
+  __device__ __forceinline__ void send(V (Mail::*field)[kMaxCtas], V v) {
+    const int C = cg::this_cluster().num_blocks();
+    if ((int)threadIdx.x < C)
+      (at((int)threadIdx.x)->mail.*field)[cg::this_cluster().block_rank()] = v;
+  }
   __device__ __forceinline__ uint64_t coarse(uint64_t w) const {
     return (w + (1ull << (drop - 1))) >> drop;
   }
@@ -273,27 +290,80 @@ __device__ __forceinline__ int bin_of(float t) {
   return t < (float)(kBins - 1) ? (int)t : kBins - 1;
 }
 
-// Block-wide exclusive sums of (n, w) in thread order; ends with the warps' sums
-// in red_n / red_w (not yet safe to overwrite).
-__device__ __forceinline__ void block_scan(Shared& sh, uint64_t n, uint64_t w, uint64_t* en,
-                                           uint64_t* ew) {
+// Block-wide exclusive sum in thread order, and the total.
+__device__ __forceinline__ uint64_t block_scan(Shared& sh, uint64_t w, uint64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint64_t in = warp_scan(n), iw = warp_scan(w);
-  if (lane == 31) {
-    sh.red_w2[warp] = in;
-    sh.red_w[warp] = iw;
-  }
+  const uint64_t inc = warp_scan(w);
   __syncthreads();
-  uint64_t bn = in - n, bw = iw - w;
-  for (int i = 0; i < warp; ++i) {
-    bn += sh.red_w2[i];
-    bw += sh.red_w[i];
+  if (lane == 31) sh.red_w[warp] = inc;
+  __syncthreads();
+  uint64_t before = inc - w, all = 0;
+#pragma unroll
+  for (int i = 0; i < kGivenWarps; ++i) {
+    if (i < warp) before += sh.red_w[i];
+    all += sh.red_w[i];
   }
-  *en = bn;
-  *ew = bw;
+  *total = all;
+  return before;
 }
 
-// The row's boundary by radix selection on the order key, 11 + 11 + 10 bits, for
+// Sum over the block, in warp 0's order; every thread gets it.
+__device__ __forceinline__ float block_sum(Shared& sh, float v) {
+  v = warp_sum_f(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh.red_f[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kGivenWarps; ++i) v += sh.red_f[i];
+  return v;
+}
+__device__ __forceinline__ int block_sum(Shared& sh, int v) {
+  v = warp_sum_i(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh.red_i[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int i = 0; i < kGivenWarps; ++i) v += sh.red_i[i];
+  return v;
+}
+
+// Of 256 digits' (elements, weight), counted from 255 down after `before`: the
+// digit that holds the boundary, into sh.bin / bin_n / above.  Warp 0.
+template <bool MASS>
+__device__ __forceinline__ void find_digit(Shared& sh, uint64_t before, uint64_t target) {
+  const int lane = threadIdx.x & 31;
+  uint64_t v[8], sum = 0;
+  uint32_t c[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    c[q] = sh.digit_n[255 - 8 * lane - q];
+    v[q] = MASS ? (uint64_t)sh.digit_w[255 - 8 * lane - q] : c[q];
+    sum += v[q];
+  }
+  uint64_t a = before + warp_scan(sum) - sum;
+  int mine = -1;
+  uint64_t mine_a = 0;
+  uint32_t mine_c = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    if (c[q] > 0 && (MASS ? a <= target : a < target)) {
+      mine = 8 * lane + q;
+      mine_a = a;
+      mine_c = c[q];
+    }
+    a += v[q];
+  }
+  const unsigned has = __ballot_sync(0xffffffffu, mine >= 0);
+  if (has && lane == 31 - __clz(has)) {  // the last such digit
+    sh.bin = 255 - mine;
+    sh.bin_n = mine_c;
+    sh.above = mine_a;
+  }
+}
+
+// The row's boundary by radix selection on the order key, 8 bits at a time, for
 // any number of equal elements.  The way of last resort: it counts every element
 // by shared atomics, thousands to an address.
 //   MASS: elements are kept while the mass before them is <= target.
@@ -305,101 +375,67 @@ __device__ __noinline__ Cut radix_select(const Row<T, STAGED>& row_in, Cut cut, 
   using SL = Slice<T, STAGED>;
   const SL& sl = rw.sl;
   Shared& sh = rw.sh;
+  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = cg::this_cluster().num_blocks();
+  const int rank = cluster.block_rank();
   uint32_t prefix = 0;
-  uint64_t above_n = 0, above_w = 0;
-  uint32_t ties = 0;
+  uint64_t before = 0;
 #pragma unroll 1
-  for (int level = 0; level < 3; ++level) {
-    const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
-    __syncthreads();
-    for (int i = tid; i < kBins; i += kGivenThreads) {
-      sh.hist.n[i] = 0;
-      sh.hist.w[i] = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    if (tid < 256) {
+      sh.digit_n[tid] = 0;
+      sh.digit_w[tid] = 0;
     }
-    if (tid == 0) sh.hi = -1;
-    __syncthreads();
+    cluster.sync();
     for (int s = warp; s < sl.segs(); s += kGivenWarps) {
 #pragma unroll 1
       for (int i = 0; i < SL::kIters; ++i) {
         const int at = SL::at(s, i);
         float x[SL::N];
         sl.load(at, x);
-#pragma unroll 1
+#pragma unroll
         for (int e = 0; e < SL::N; ++e) {
           const float z = rw.mass.z(x[e]);
-          if (!cut.keeps(z, sl.base + at + e)) continue;
           const uint32_t k = ord_key(z);
-          if (level > 0 && (k >> (shift + bits)) != prefix) continue;
-          const uint32_t bin = (k >> shift) & ((1u << bits) - 1);
-          atomicAdd(&sh.hist.n[bin], 1u);
+          if (!cut.keeps(z, sl.base + at + e)) continue;
+          if (shift < 24 && (k >> (shift + 8)) != prefix) continue;
+          const int bin = (k >> shift) & 255;
+          atomicAdd(&sh.digit_n[bin], 1u);
           if (MASS) {
             const uint64_t w = rw.coarse(rw.mass.of(z));
-            if (w) atomicAdd((unsigned long long*)&sh.hist.w[bin], (unsigned long long)w);
+            if (w) atomicAdd(&sh.digit_w[bin], (unsigned long long)w);
           }
         }
       }
     }
-    cg::this_cluster().sync();
-    // four bins to a thread, in descending order; sums over the cluster, then a scan
-    uint32_t cn[4], tn = 0;
-    uint64_t cw[4], tw = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int bin = kBins - 1 - (tid * 4 + q);
-      cn[q] = 0;
-      cw[q] = 0;
-      for (int r = 0; r < C; ++r) {
-        cn[q] += rw.at(r)->hist.n[bin];
-        if (MASS) cw[q] += rw.at(r)->hist.w[bin];
-      }
-      tn += cn[q];
-      tw += cw[q];
-    }
-    uint64_t bn, bw;
-    block_scan(sh, tn, tw, &bn, &bw);
-    uint64_t an = above_n + bn, aw = above_w + bw;
-    int mine = -1;
-    uint64_t mine_n = 0, mine_w = 0;
-    uint32_t mine_c = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (cn[q] > 0 && (MASS ? aw <= target : an < target)) {
-        mine = tid * 4 + q;  // the last such bin holds the boundary
-        mine_n = an;
-        mine_w = aw;
-        mine_c = cn[q];
-      }
-      an += cn[q];
-      aw += cw[q];
-    }
-    if (mine >= 0) atomicMax(&sh.hi, mine);
     __syncthreads();
-    if (mine >= 0 && mine == sh.hi) {
-      sh.bin = kBins - 1 - mine;
-      sh.bin_n = mine_c;
-      sh.above_n = mine_n;
-      sh.above_w = mine_w;
+    // the others' digits are added to the leader's, which finds the boundary
+    if (rank != 0 && tid < 256 && sh.digit_n[tid]) {
+      atomicAdd(&rw.at(0)->digit_n[tid], sh.digit_n[tid]);
+      if (MASS) atomicAdd(&rw.at(0)->digit_w[tid], sh.digit_w[tid]);
     }
-    cg::this_cluster().sync();  // also: no CTA clears its bins while another reads them
-    prefix = (prefix << bits) | (uint32_t)sh.bin;
-    above_n = sh.above_n;
-    above_w = sh.above_w;
-    ties = sh.bin_n;
+    cluster.sync();
+    if (rank == 0 && warp == 0) find_digit<MASS>(sh, before, target);
+    cluster.sync();
+    const Shared* lead = rw.at(0);
+    prefix = (prefix << 8) | (uint32_t)lead->bin;
+    before = lead->above;
   }
+  const uint32_t ties = rw.at(0)->bin_n;
+  cluster.sync();
   const float zk = key_value(prefix);
   uint64_t take;
   if (MASS) {
     const uint64_t w = rw.coarse(rw.mass.of(zk));
-    take = w ? (target - above_w) / w + 1 : ties;
+    take = w ? (target - before) / w + 1 : ties;
   } else {
-    take = target - above_n;
+    take = target - before;
   }
   const int old_idx = zk == cut.z ? cut.idx : kMaxIdx;
   if (take >= ties) return Cut{zk, old_idx};
 
   // the index of the take-th of the equal elements
+  int mine = 0;
   for (int s = warp; s < sl.segs(); s += kGivenWarps) {
     int c = 0;
 #pragma unroll 1
@@ -412,20 +448,20 @@ __device__ __noinline__ Cut radix_select(const Row<T, STAGED>& row_in, Cut cut, 
         c += rw.mass.z(x[e]) == zk && sl.base + at + e <= old_idx;
     }
     c = warp_sum_i(c);
-    if (lane == 0) sh.seg_n[s] = c;
+    if (lane == 0) {
+      sh.seg_n[s] = c;
+      mine += c;
+    }
   }
+  mine = block_sum(sh, mine);
+  rw.send(&Mail::total, mine);
+  cluster.sync();
+  uint64_t ahead = 0;
+  for (int r = 0; r < rank; ++r) ahead += sh.mail.total[r];
+  if (tid == 0) sh.lo = -1;
   __syncthreads();
-  if (tid == 0) {
-    int c = 0;
-    for (int s = 0; s < sl.segs(); ++s) c += sh.seg_n[s];
-    sh.shown.count = c;
-    sh.shown.index = -1;
-  }
-  cg::this_cluster().sync();
-  uint64_t before = 0;
-  for (int r = 0; r < (int)cg::this_cluster().block_rank(); ++r) before += rw.at(r)->shown.count;
-  if (take > before && take <= before + sh.shown.count && warp == 0) {
-    int left = (int)(take - before), s = 0;
+  if (take > ahead && take <= ahead + mine && warp == 0) {
+    int left = (int)(take - ahead), s = 0;
     while (left > sh.seg_n[s]) left -= sh.seg_n[s++];
     for (int i = 0; i < SL::kIters && left > 0; ++i) {
       const int at = SL::at(s, i);
@@ -439,78 +475,52 @@ __device__ __noinline__ Cut radix_select(const Row<T, STAGED>& row_in, Cut cut, 
         int nth = left - (inc - c);
 #pragma unroll
         for (int e = 0; e < SL::N; ++e)
-          if (rw.mass.z(x[e]) == zk && --nth == 0) sh.shown.index = sl.base + at + e;
+          if (rw.mass.z(x[e]) == zk && --nth == 0) sh.lo = sl.base + at + e;
       }
       left -= __shfl_sync(0xffffffffu, inc, 31);
     }
   }
-  cg::this_cluster().sync();
+  __syncthreads();
+  rw.send(&Mail::tie, sh.lo);
+  cluster.sync();
   int idx = -1;
-  for (int r = 0; r < C; ++r) idx = max(idx, rw.at(r)->shown.index);
-  cg::this_cluster().sync();
+  for (int r = 0; r < (int)cluster.num_blocks(); ++r) idx = max(idx, sh.mail.tie[r]);
   return Cut{zk, idx};
 }
 
 // The boundary within the leader's list of n candidates (in vocabulary order), by
-// radix selection on the order key, 8 bits at a time; `target` as above, masses
-// in list units.  Called by all threads of the leader.
-template <bool MASS>
-__device__ __noinline__ Cut list_select(Shared& sh, uint32_t* hn, unsigned long long* hw, int n,
-                                        uint64_t target) {
+// radix selection on the order key; `target` as above.  weight(i): entry i's
+// mass in list units, 0 when it has no part in the selection.  Called by all
+// threads of the leader.
+template <bool MASS, typename W>
+__device__ __forceinline__ Cut list_select(Shared& sh, int n, uint64_t target, W weight) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t prefix = 0;
   uint64_t before = 0;  // elements (or mass) ahead of the prefix
+#pragma unroll 1
   for (int shift = 24; shift >= 0; shift -= 8) {
     if (tid < 256) {
-      hn[tid] = 0;
-      if (MASS) hw[tid] = 0;
+      sh.digit_n[tid] = 0;
+      if (MASS) sh.digit_w[tid] = 0;
     }
     __syncthreads();
+#pragma unroll 1
     for (int i = tid; i < n; i += kGivenThreads) {
       const uint32_t k = sh.list.key[i];
       if (shift < 24 && (k >> (shift + 8)) != prefix) continue;
       const int bin = (k >> shift) & 255;
       if (MASS) {
-        const uint64_t w = sh.list.mass[i];
-        if (!w) continue;  // no part in the selection by mass
-        atomicAdd(&hw[bin], (unsigned long long)w);
+        const uint64_t w = weight(i);
+        if (!w) continue;
+        atomicAdd(&sh.digit_w[bin], (unsigned long long)w);
       }
-      atomicAdd(&hn[bin], 1u);
+      atomicAdd(&sh.digit_n[bin], 1u);
     }
     __syncthreads();
-    if (warp == 0) {
-      // lane l owns bins 255 - 8l .. 248 - 8l
-      uint64_t v[8], sum = 0;
-      uint32_t c[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        c[q] = hn[255 - 8 * lane - q];
-        v[q] = MASS ? (uint64_t)hw[255 - 8 * lane - q] : c[q];
-        sum += v[q];
-      }
-      uint64_t a = before + warp_scan(sum) - sum;
-      int mine = -1;
-      uint64_t mine_a = 0;
-      uint32_t mine_c = 0;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if (c[q] > 0 && (MASS ? a <= target : a < target)) {
-          mine = 8 * lane + q;
-          mine_a = a;
-          mine_c = c[q];
-        }
-        a += v[q];
-      }
-      const unsigned has = __ballot_sync(0xffffffffu, mine >= 0);
-      if (has && lane == 31 - __clz(has)) {
-        sh.bin = 255 - mine;
-        sh.bin_n = mine_c;
-        sh.above_w = mine_a;
-      }
-    }
+    if (warp == 0) find_digit<MASS>(sh, before, target);
     __syncthreads();
     prefix = (prefix << 8) | (uint32_t)sh.bin;
-    before = sh.above_w;
+    before = sh.above;
   }
   // the take-th of the elements at the key, in vocabulary order
   if (warp == 0) {
@@ -518,26 +528,27 @@ __device__ __noinline__ Cut list_select(Shared& sh, uint32_t* hn, unsigned long 
     int found = kMaxIdx;
     uint32_t seen = 0;
     uint64_t take = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane;
-      const bool tie = i < n && sh.list.key[i] == prefix && (!MASS || sh.list.mass[i] > 0);
-      const unsigned mask = __ballot_sync(0xffffffffu, tie);
-      if (!mask) continue;
-      if (take == 0) {
-        const uint64_t w = MASS ? sh.list.mass[i0 + __ffs(mask) - 1] : 1;
-        take = MASS ? (target - before) / w + 1 : target - before;
-        if (take >= ties) break;
+    if (ties > 1) {
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        const bool tie = i < n && sh.list.key[i] == prefix && (!MASS || weight(i) > 0);
+        const unsigned mask = __ballot_sync(0xffffffffu, tie);
+        if (!mask) continue;
+        if (take == 0) {
+          take = MASS ? (target - before) / weight(i0 + __ffs(mask) - 1) + 1 : target - before;
+          if (take >= ties) break;
+        }
+        const uint32_t nth = seen + __popc(mask & ((1u << lane) - 1)) + 1;
+        if (tie && nth == take) found = sh.list.idx[i];
+        seen += __popc(mask);
       }
-      const uint32_t rank = seen + __popc(mask & ((1u << lane) - 1)) + 1;
-      if (tie && rank == take) found = sh.list.idx[i];
-      seen += __popc(mask);
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) found = min(found, __shfl_xor_sync(0xffffffffu, found, o));
-    if (lane == 0) sh.shown.cut = Cut{key_value(prefix), found};
+      for (int o = 16; o > 0; o >>= 1) found = min(found, __shfl_xor_sync(0xffffffffu, found, o));
+    }
+    if (lane == 0) sh.mail.cut = Cut{key_value(prefix), found};
   }
   __syncthreads();
-  return sh.shown.cut;
+  return sh.mail.cut;
 }
 
 // The threads' sums of seg_n to the elements before each segment; the CTA's
@@ -556,43 +567,51 @@ __device__ __forceinline__ int scan_segments(Shared& sh, int segs) {
 
 // The elements that `wanted` takes, of every CTA, into the leader's list in
 // vocabulary order.  seg_n holds how many each segment has (every warp its own
-// segments, before a block barrier); returns their number in the cluster, or
-// -1 when the list does not hold them.  The caller's next cluster barrier
-// publishes the list.
-template <typename T, bool STAGED, typename F>
-__device__ __forceinline__ int gather(Row<T, STAGED>& rw, F wanted) {
+// segments); `post` sends what else the others need with the same barrier.
+// Returns their number in the cluster, or -1 when the list does not hold them.
+// The caller's next cluster barrier publishes the list.
+template <typename T, bool STAGED, typename F, typename G>
+__device__ __forceinline__ int gather(Row<T, STAGED>& rw, F wanted, G post) {
   using SL = Slice<T, STAGED>;
   const SL& sl = rw.sl;
   Shared& sh = rw.sh;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int warp = threadIdx.x >> 5;
+  __syncthreads();
   if (warp == 0) {
     const int c = scan_segments(sh, sl.segs());
-    if (lane == 0) sh.shown.count = c;
+    rw.send(&Mail::count, c);
   }
-  cg::this_cluster().sync();
+  post();
+  cluster.sync();
   int total = 0, base = 0;
-  for (int r = 0; r < (int)cg::this_cluster().num_blocks(); ++r) {
-    if (r == (int)cg::this_cluster().block_rank()) base = total;
-    total += rw.at(r)->shown.count;
+  const int rank = cluster.block_rank();
+  for (int r = 0; r < (int)cluster.num_blocks(); ++r) {
+    if (r == rank) base = total;
+    total += sh.mail.count[r];
   }
   if (total > kList) return -1;
   List& list = rw.at(0)->list;
-  const int mine = sh.shown.count;
+  const int mine = sh.mail.count[rank];
   for (int s = warp; s < sl.segs(); s += kGivenWarps) {
-    int off = base + sh.seg_n[s];
-    if (off == base + (s + 1 < sl.segs() ? sh.seg_n[s + 1] : mine)) continue;
+    const int from = sh.seg_n[s], to = s + 1 < sl.segs() ? sh.seg_n[s + 1] : mine;
+    if (from == to) continue;
+    int off = base + from;
+#pragma unroll 1
     for (int i = 0; i < SL::kIters; ++i) {
       const int at = SL::at(s, i);
       float x[SL::N];
       sl.load(at, x);
-      int c = 0;
+      unsigned take = 0;
 #pragma unroll
-      for (int e = 0; e < SL::N; ++e) c += wanted(x[e], sl.base + at + e);
+      for (int e = 0; e < SL::N; ++e) take |= wanted(x[e], sl.base + at + e) ? 1u << e : 0u;
+      if (!__any_sync(0xffffffffu, take)) continue;
+      const int c = __popc(take);
       const int inc = warp_scan(c);
       int p = off + inc - c;
 #pragma unroll
       for (int e = 0; e < SL::N; ++e)
-        if (wanted(x[e], sl.base + at + e)) {
+        if ((take >> e) & 1) {
           list.key[p] = ord_key(rw.mass.z(x[e]));
           list.idx[p] = sl.base + at + e;
           ++p;
@@ -624,25 +643,29 @@ constexpr int kListDrop = 2;  // list masses: units of 2^(E - kElemBits + 2), 20
 //   masses of the kept elements (element units) and *row_mass the mass of all
 //   elements kept by `cut`.
 //   else: the first `top_k` are kept.
-// Returns false (the same in every CTA) when the bracket holds too many.
+// Returns false (the same in every CTA) when the bracket holds too many, or, by
+// mass, turns out not to hold the boundary.
 template <typename T, bool STAGED, bool MASS>
-__device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_io, float p, int top_k,
-                                         uint64_t* row_mass) {
+__device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_io, float p,
+                                         int top_k, uint64_t* row_mass) {
   Row<T, STAGED> rw = row_in;  // in registers
   using SL = Slice<T, STAGED>;
   const SL& sl = rw.sl;
   Shared& sh = rw.sh;
+  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = cg::this_cluster().num_blocks();
+  const int C = cluster.num_blocks(), rank = cluster.block_rank();
   const Cut cut = *cut_io;
-  for (int i = tid; i < kBins; i += kGivenThreads) sh.hist.n[i] = 0;
+  constexpr int kPer = kBins / kGivenThreads;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kGivenThreads] = 0;
   if (tid == 0) {
     sh.lo = kBins;
     sh.hi = -1;
   }
   __syncthreads();
   // by mass: each element adds its mass relative to its bin's upper edge in
-  // units of 2^-12, so a bin's mass is known to within 1.3e-4 of itself
+  // units of 1/4095, so a bin's mass is known to within 1.3e-4 of itself
   for (int s = warp; s < sl.segs(); s += kGivenWarps) {
 #pragma unroll 1
     for (int i = 0; i < SL::kIters; ++i) {
@@ -652,35 +675,40 @@ __device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_
 #pragma unroll
       for (int e = 0; e < SL::N; ++e) {
         const float z = rw.mass.z(x[e]);
-        if (!cut.keeps(z, sl.base + at + e)) continue;
         const float t = rw.bins_below(z);
         const int bin = bin_of(t);
         uint32_t add = 1;
         if (MASS) {
           const float f = t - (float)bin;
-          add = bin == kBins - 1 ? 0 : (uint32_t)__fmaf_rn(f, __fmaf_rn(f, 0.5f, -64.f), 4096.5f);
+          add = (uint32_t)__fmaf_rn(f, __fmaf_rn(f, 0.4999f, -63.984f), 4095.5f);
         }
-        if (add) atomicAdd(&sh.hist.n[bin], add);
+        if (cut.keeps(z, sl.base + at + e) && !(MASS && bin == kBins - 1))
+          atomicAdd(&sh.hist.own[bin], add);
       }
     }
   }
-  cg::this_cluster().sync();
-  uint32_t cn[4];
-  uint64_t tn = 0;
-  float cf[4], tf = 0.f;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int bin = tid * 4 + q;
-    uint64_t c = 0;
-    for (int r = 0; r < C; ++r) c += rw.at(r)->hist.n[bin];
-    cn[q] = (uint32_t)min(c, (uint64_t)0xffffffffu);
-    cf[q] = MASS ? (float)c * ex2_approx((float)bin * (-kLog2e / kBinsPerNat)) : 0.f;
-    tn += c;
-    tf += cf[q];
+  // the cluster's histogram: CTA r sums a share of the bins and sends it to all
+  cluster.sync();
+  const int share = kBins / C;
+  for (int q = tid; q < share; q += kGivenThreads) {
+    const int bin = rank * share + q;
+    uint32_t c = 0;
+    for (int r = 0; r < C; ++r) c += rw.at(r)->hist.own[bin];
+    for (int r = 0; r < C; ++r) rw.at(r)->hist.sum[bin] = c;
   }
+  cluster.sync();
+  uint32_t cn[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) cn[q] = sh.hist.sum[tid * kPer + q];
   uint64_t above_n = 0;  // elements above the bracket (by count)
   if (MASS) {
-    const float inc = warp_scan(tf);
+    float cf[kPer], tf = 0.f;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      cf[q] = (float)cn[q] * ex2_approx((float)(tid * kPer + q) * (-kLog2e / kBinsPerNat));
+      tf += cf[q];
+    }
+    float inc = warp_scan(tf);
     if (lane == 31) sh.red_f[warp] = inc;
     __syncthreads();
     float a = inc - tf, all = 0.f;
@@ -688,33 +716,35 @@ __device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_
       if (i < warp) a += sh.red_f[i];
       all += sh.red_f[i];
     }
-    constexpr float kSlack = 1.f / 1024;  // bins and sums, both sides
+    constexpr float kSlack = 1.f / 6144;  // of the bins' masses and their fp32 sums
     const float want = p * all;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kPer; ++q) {
       if (cn[q] > 0) {
         // bins that end before the target are kept whole, those that begin
         // after it not at all
-        if (a + cf[q] >= want * (1.f - kSlack)) atomicMin(&sh.lo, tid * 4 + q);
-        if (a <= want * (1.f + kSlack)) atomicMax(&sh.hi, tid * 4 + q);
+        if (a + cf[q] >= want * (1.f - kSlack)) atomicMin(&sh.lo, tid * kPer + q);
+        if (a <= want * (1.f + kSlack)) atomicMax(&sh.hi, tid * kPer + q);
       }
       a += cf[q];
     }
   } else {
-    uint64_t a, unused;
-    block_scan(sh, tn, 0, &a, &unused);
+    uint64_t tn = 0, unused;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kPer; ++q) tn += cn[q];
+    uint64_t a = block_scan(sh, tn, &unused);
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
       if (a < (uint64_t)top_k && a + cn[q] >= (uint64_t)top_k) {
-        sh.lo = sh.hi = tid * 4 + q;
-        sh.above_n = a;
+        sh.lo = sh.hi = tid * kPer + q;
+        sh.above = a;
       }
       a += cn[q];
     }
   }
   __syncthreads();
   const int lo = sh.lo, hi = sh.hi;
-  above_n = MASS ? 0 : sh.above_n;
+  if (!MASS) above_n = sh.above;
   if (lo > hi) return false;  // (a histogram without mass)
 
   uint64_t w_above = 0, w_all = 0;
@@ -734,8 +764,8 @@ __device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_
         c += in && bin >= lo && bin <= hi;
         if (MASS) {
           const uint64_t w = in ? rw.mass.of(z) : 0;
-          if (bin < lo) above += w;
-          else rest += w;
+          above += bin < lo ? w : 0;
+          rest += w;
         }
       }
     }
@@ -749,63 +779,47 @@ __device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_
       if (MASS) {
         sh.seg_w[s] = above;
         w_above += rw.coarse(above);
-        w_all += rw.coarse(above + rest);
+        w_all += rw.coarse(rest);
       }
     }
   }
   if (MASS && lane == 0) {
     sh.red_w[warp] = w_above;
-    sh.red_w2[warp] = w_all;
+    sh.red_n[warp] = w_all;
   }
-  __syncthreads();
-  if (MASS && tid == 0) {
-    w_above = w_all = 0;
-    for (int i = 0; i < kGivenWarps; ++i) {
-      w_above += sh.red_w[i];
-      w_all += sh.red_w2[i];
+  const int n = gather(rw, InBins<T, STAGED>{rw, cut, lo, hi}, [&]() {
+    if (MASS && warp == 0) {
+      w_above = warp_sum_u64(lane < kGivenWarps ? sh.red_w[lane] : 0);
+      w_all = warp_sum_u64(lane < kGivenWarps ? sh.red_n[lane] : 0);
+      rw.send(&Mail::mass, w_above);
+      rw.send(&Mail::all, w_all);
     }
-    sh.shown.mass = w_above;
-    sh.shown.all = w_all;
-  }
-  const int n = gather(rw, InBins<T, STAGED>{rw, cut, lo, hi});
+  });
   if (MASS) {
     w_above = w_all = 0;
     for (int r = 0; r < C; ++r) {
-      w_above += rw.at(r)->shown.mass;
-      w_all += rw.at(r)->shown.all;
+      w_above += sh.mail.mass[r];
+      w_all += sh.mail.all[r];
     }
     *row_mass = w_all;
   }
-  cg::this_cluster().sync();
+  cluster.sync();
   if (n <= 0) return false;
-  if (cg::this_cluster().block_rank() == 0) {
-    // scratch for the list's histograms: the segment counts are done with
-    uint32_t* hn = reinterpret_cast<uint32_t*>(&sh.list.mass[0]);
-    unsigned long long* hw = nullptr;
+  if (rank == 0) {
     bool ok = true;
     Cut found{0.f, kMaxIdx};
     if (MASS) {
-      __shared__ uint32_t s_hn[256];
-      __shared__ unsigned long long s_hw[256];
-      hn = s_hn;
-      hw = s_hw;
-      uint64_t mine = 0;
-      for (int i = tid; i < n; i += kGivenThreads) {
-        const uint64_t w = (rw.mass.of(key_value(sh.list.key[i])) + 2) >> kListDrop;
-        sh.list.mass[i] = w;
-        mine += w;
-      }
-      uint64_t e, ew;
-      block_scan(sh, 0, mine, &e, &ew);
-      uint64_t band = 0;
-      for (int i = 0; i < kGivenWarps; ++i) band += sh.red_w[i];
+      auto weight = [&](int i) { return (rw.mass.of(key_value(sh.list.key[i])) + 2) >> kListDrop; };
+      uint64_t mine = 0, band;
+      for (int i = tid; i < n; i += kGivenThreads) mine += weight(i);
+      block_scan(sh, mine, &band);
       const uint64_t target = part_of(w_all, p);
       // the boundary lies in the bracket: the mass above it is within the
       // target, that at its end is not
-      ok = w_above <= target;
+      ok = w_above <= target && (target - w_above) < (1ull << (62 - rw.drop));
       const uint64_t left = ok ? (target - w_above) << (rw.drop - kListDrop) : 0;
-      ok = ok && left < band && (target - w_above) < (1ull << (62 - rw.drop));
-      if (ok) found = list_select<true>(sh, hn, hw, n, left);
+      ok = ok && left < band;
+      if (ok) found = list_select<true>(sh, n, left, weight);
       if (ok)
         for (int i = tid; i < n; i += kGivenThreads) {
           const int j = sh.list.idx[i];
@@ -817,19 +831,16 @@ __device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_
           }
         }
     } else {
-      found = list_select<false>(sh, hn, hw, n, (uint64_t)top_k - above_n);
+      found = list_select<false>(sh, n, (uint64_t)top_k - above_n, [](int) { return 1ull; });
     }
-    __syncthreads();
-    if (tid == 0) {
-      sh.shown.cut = found;
-      sh.shown.ok = ok;
+    if (tid < C) {
+      rw.at(tid)->mail.cut = found;
+      rw.at(tid)->mail.ok = ok;
     }
   }
-  cg::this_cluster().sync();
-  const Cut found = rw.at(0)->shown.cut;
-  const bool ok = rw.at(0)->shown.ok;
-  if (ok) *cut_io = found;
-  return ok;
+  cluster.sync();
+  if (sh.mail.ok) *cut_io = sh.mail.cut;
+  return sh.mail.ok;
 }
 
 // Masses of the kept elements by segment, into seg_w (element units).
@@ -858,11 +869,12 @@ __device__ __noinline__ void kept_mass(const Row<T, STAGED>& row_in, const Cut c
   }
 }
 
-// seg_w to inclusive sums in row units; the cluster's total, and the mass of the
-// CTAs before this one.
+// seg_w to inclusive sums in row units; returns the cluster's total, the mass of
+// the CTAs before this one and this CTA's.
 template <typename T, bool STAGED>
-__device__ uint64_t sum_segments(Row<T, STAGED>& rw, uint64_t* before) {
+__device__ uint64_t sum_segments(Row<T, STAGED>& rw, uint64_t* before, uint64_t* own) {
   Shared& sh = rw.sh;
+  cg::cluster_group cluster = cg::this_cluster();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, segs = rw.sl.segs();
   __syncthreads();
   if (warp == 0) {
@@ -873,16 +885,16 @@ __device__ uint64_t sum_segments(Row<T, STAGED>& rw, uint64_t* before) {
       if (s0 + lane < segs) sh.seg_w[s0 + lane] = w;
       carry = __shfl_sync(0xffffffffu, w, 31);
     }
-    if (lane == 0) sh.shown.mass = carry;
+    rw.send(&Mail::kept, carry);
   }
-  cg::this_cluster().sync();
-  uint64_t total = 0, b = 0;
-  for (int r = 0; r < (int)cg::this_cluster().num_blocks(); ++r) {
-    if (r == (int)cg::this_cluster().block_rank()) b = total;
-    total += rw.at(r)->shown.mass;
+  cluster.sync();
+  uint64_t total = 0;
+  const int rank = cluster.block_rank();
+  for (int r = 0; r < (int)cluster.num_blocks(); ++r) {
+    if (r == rank) *before = total;
+    total += sh.mail.kept[r];
   }
-  cg::this_cluster().sync();
-  *before = b;
+  *own = sh.mail.kept[rank];
   return total;
 }
 
@@ -949,46 +961,58 @@ __device__ int find_draw(const Row<T, STAGED>& rw, const Cut& cut, uint64_t t, f
   return idx;
 }
 
-// A row with 1 < top_k <= kListTopK: the threads' maxima give a value that at
-// least top_k elements reach; those elements go to the leader's list, where
-// min-p, top-k and top-p are settled and the draws made.  Adds ln sum exp on the
-// way.  Returns false (in every CTA) when the list does not hold them.
+// Threads whose maximum counts as one group, for a row of C CTAs: so many groups
+// that at least twice top_k remain.  0: the row has too few threads.
+__device__ __forceinline__ int group_threads(int C, int top_k) {
+  if (top_k < 2 || top_k > kListTopK || 2 * top_k > C * kGivenThreads) return 0;
+  int g = 1;
+  while (g < 32 && C * kGivenThreads / (2 * g) >= 2 * top_k) g *= 2;
+  return g;  // at most 2 * kListTopK groups, both powers of two
+}
+
+// A row with 1 < top_k <= kListTopK: the maxima of groups of elements (in
+// hist.group_max) give a value that at least top_k elements reach; those elements
+// go to the leader's list, where min-p, top-k and top-p are settled and the draws
+// made.  Adds ln sum exp on the way.  Returns false (in every CTA) when the list
+// does not hold them.
 template <typename T, bool STAGED>
 __device__ __noinline__ bool draw_from_list(const Row<T, STAGED>& row_in, const GivenArgs& a,
-                                            const RowParams& P, const Cut minp, float thread_max,
+                                            const RowParams& P, const Cut minp, int groups,
                                             int row, float* ln_s_out) {
   Row<T, STAGED> rw = row_in;  // in registers
   using SL = Slice<T, STAGED>;
   const SL& sl = rw.sl;
   Shared& sh = rw.sh;
+  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = cg::this_cluster().num_blocks();
-  for (int i = tid; i < kBins; i += kGivenThreads) sh.hist.n[i] = 0;
+  constexpr int kPer = kBins / kGivenThreads;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kGivenThreads] = 0;
   if (tid == 0) sh.hi = kBins - 1;
   __syncthreads();
-  if (thread_max > -INFINITY)
-    atomicAdd(&sh.hist.n[bin_of(rw.bins_below(rw.mass.z(thread_max)))], 1u);
-  cg::this_cluster().sync();
+  for (int i = tid; i < groups; i += kGivenThreads) {
+    const float x = sh.hist.group_max[i];
+    if (x > -INFINITY) atomicAdd(&sh.hist.own[bin_of(rw.bins_below(rw.mass.z(x)))], 1u);
+  }
+  __syncthreads();
   {
-    uint32_t cn[4];
-    uint64_t tn = 0, b, unused;
+    uint32_t cn[kPer];
+    uint64_t tn = 0, unused;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      cn[q] = 0;
-      for (int r = 0; r < C; ++r) cn[q] += rw.at(r)->hist.n[tid * 4 + q];
+    for (int q = 0; q < kPer; ++q) {
+      cn[q] = sh.hist.own[tid * kPer + q];
       tn += cn[q];
     }
-    block_scan(sh, tn, 0, &b, &unused);
+    uint64_t b = block_scan(sh, tn, &unused);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (b < (uint64_t)P.top_k && b + cn[q] >= (uint64_t)P.top_k) sh.hi = tid * 4 + q;
+    for (int q = 0; q < kPer; ++q) {
+      if (b < (uint64_t)P.top_k && b + cn[q] >= (uint64_t)P.top_k) sh.hi = tid * kPer + q;
       b += cn[q];
     }
   }
   __syncthreads();
-  // (fewer than top_k threads with a finite element: every finite element)
+  // (fewer than top_k groups with a finite element: every finite element)
   const float edge = sh.hi == kBins - 1 ? INFINITY : (float)(sh.hi + 1);
-  auto wanted = [&](float x, int) { return rw.bins_below(rw.mass.z(x)) < edge; };
   float expsum = 0.f;
   for (int s = warp; s < sl.segs(); s += kGivenWarps) {
     int c = 0;
@@ -1006,84 +1030,62 @@ __device__ __noinline__ bool draw_from_list(const Row<T, STAGED>& row_in, const 
     c = warp_sum_i(c);
     if (lane == 0) sh.seg_n[s] = c;
   }
-  expsum = warp_sum_f(expsum);
-  if (lane == 0) sh.red_f[warp] = expsum;
-  __syncthreads();
-  if (tid == 0) {
-    expsum = 0.f;
-    for (int i = 0; i < kGivenWarps; ++i) expsum += sh.red_f[i];
-    sh.shown.expsum = expsum;
-  }
-  const int n = gather(rw, wanted);
+  expsum = block_sum(sh, expsum);
+  const int n = gather(rw, [&](float x, int) { return rw.bins_below(rw.mass.z(x)) < edge; },
+                       [&]() { rw.send(&Mail::expsum, expsum); });
   expsum = 0.f;
-  for (int r = 0; r < C; ++r) expsum += rw.at(r)->shown.expsum;
+  for (int r = 0; r < (int)cluster.num_blocks(); ++r) expsum += sh.mail.expsum[r];
   const float ln_s = logf(expsum);
   *ln_s_out = ln_s;
-  cg::this_cluster().sync();
+  cluster.sync();
   if (n < 0) return false;
-  if (cg::this_cluster().block_rank() != 0) return true;
+  if (cluster.block_rank() != 0) return true;
 
-  __shared__ uint32_t s_hn[256];
-  __shared__ unsigned long long s_hw[256];
-  List& list = sh.list;
+  const List& list = sh.list;
   Cut cut = minp;
-  int c = 0;
-  for (int i = tid; i < n; i += kGivenThreads) c += key_value(list.key[i]) >= cut.z;
-  c = warp_sum_i(c);
-  if (lane == 0) sh.red_i[warp] = c;
-  __syncthreads();
   int kept = 0;
-  for (int i = 0; i < kGivenWarps; ++i) kept += sh.red_i[i];
-  if (kept > P.top_k) {
-    // elements that min-p leaves out come after the others in the order
-    cut = list_select<false>(sh, s_hn, s_hw, n, (uint64_t)P.top_k);
-  }
-  // each thread holds four neighbours of the list
-  uint64_t w[4], sum = 0, total = 0, unused, ahead;
-  auto weigh = [&]() {
-    sum = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int i = tid * 4 + q;
-      w[q] = 0;
-      if (i < n) {
-        const float z = key_value(list.key[i]);
-        if (cut.keeps(z, list.idx[i])) w[q] = (rw.mass.of(z) + 2) >> kListDrop;
-      }
-      sum += w[q];
-    }
-    __syncthreads();
-    block_scan(sh, 0, sum, &unused, &ahead);
-    total = 0;
-    for (int i = 0; i < kGivenWarps; ++i) total += sh.red_w[i];
+  for (int i = tid; i < n; i += kGivenThreads) kept += key_value(list.key[i]) >= cut.z;
+  kept = block_sum(sh, kept);
+  // (elements that min-p leaves out come after the others in the order)
+  if (kept > P.top_k)
+    cut = list_select<false>(sh, n, (uint64_t)P.top_k, [](int) { return 1ull; });
+  auto weight = [&](int i) -> uint64_t {
+    if (i >= n) return 0;
+    const float z = key_value(list.key[i]);
+    return cut.keeps(z, list.idx[i]) ? (rw.mass.of(z) + 2) >> kListDrop : 0;
   };
-  weigh();
+  // each thread holds a few neighbours of the list
+  auto own = [&]() {
+    uint64_t sum = 0;
+#pragma unroll
+    for (int q = 0; q < kListPerThread; ++q) sum += weight(tid * kListPerThread + q);
+    return sum;
+  };
+  uint64_t total, mine = own();
+  uint64_t ahead = block_scan(sh, mine, &total);
   if (P.flags & kRowTopP) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (tid * 4 + q < n) list.mass[tid * 4 + q] = w[q];
-    __syncthreads();
-    cut = list_select<true>(sh, s_hn, s_hw, n, part_of(total, P.top_p));
-    weigh();
+    const Cut next = list_select<true>(sh, n, part_of(total, P.top_p), weight);
+    cut = next;
+    mine = own();
+    ahead = block_scan(sh, mine, &total);
   }
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    ahead += w[q];
-    if (tid * 4 + q < n) list.mass[tid * 4 + q] = ahead;  // inclusive
-  }
+  sh.run[tid] = ahead + mine;
   __syncthreads();
   for (int d = tid; d < a.draws; d += kGivenThreads) {
     const int64_t o = (int64_t)row * a.draws + d;
     const uint64_t t = part_of(total, a.uniforms[o]);
-    int lo = 0, hi = n - 1;  // the first entry whose inclusive mass exceeds t
+    int lo = 0, hi = kGivenThreads - 1;  // the first thread whose inclusive mass exceeds t
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (list.mass[mid] > t) hi = mid;
+      if (sh.run[mid] > t) hi = mid;
       else lo = mid + 1;
     }
-    a.out_tokens[o] = list.idx[lo];
+    uint64_t run = lo > 0 ? sh.run[lo - 1] : 0;
+    int i = lo * kListPerThread;
+    for (run += weight(i); run <= t; run += weight(i)) ++i;
+    a.out_tokens[o] = list.idx[i];
     if (a.out_logprobs)
-      a.out_logprobs[o] = __fsub_rn(__fsub_rn(key_value(list.key[lo]), rw.m), ln_s);
+      a.out_logprobs[o] = __fsub_rn(__fsub_rn(key_value(list.key[i]), rw.m), ln_s);
   }
   return true;
 }
@@ -1145,18 +1147,31 @@ __global__ void __launch_bounds__(kGivenThreads, 2) given_kernel(GivenArgs a) {
       for (int e = 0; e < SL::N; ++e) mx = max_nan(mx, x[e]);
     }
   }
-  const float thread_max = mx;
+  // the maximum to every CTA, and for a top-k row the maxima of groups of threads
+  const bool greedy = P.flags & kRowGreedy;
+  const bool topk = !greedy && P.top_k > 1 && P.top_k < a.V;
+  const int group = topk ? group_threads(C, P.top_k) : 0;
+  float gmax = mx;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int o = 1; o < 32; o <<= 1) {
+    if (o < group) gmax = max_nan(gmax, __shfl_xor_sync(0xffffffffu, gmax, o));
+    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
   if (lane == 0) sh.red_f[warp] = mx;
-  __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < kGivenWarps; ++i) mx = max_nan(mx, sh.red_f[i]);
-    sh.shown.max = mx;
+  cluster.sync();  // every CTA of the cluster runs before its memory is written
+  if (group && (tid & (group - 1)) == 0)
+    for (int r = 0; r < C; ++r)
+      cluster.map_shared_rank(&sh, r)->hist.group_max[rank * (kGivenThreads / group) + tid / group] =
+          gmax;
+  if (tid < C) {
+    mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kGivenWarps; ++i) mx = max_nan(mx, sh.red_f[i]);
+    cluster.map_shared_rank(&sh, tid)->mail.max[rank] = mx;
   }
   cluster.sync();
   mx = -INFINITY;
-  for (int r = 0; r < C; ++r) mx = max_nan(mx, cluster.map_shared_rank(&sh, r)->shown.max);
+  for (int r = 0; r < C; ++r) mx = max_nan(mx, sh.mail.max[r]);
   const float m = __fmul_rn(mx, P.inv_t);
   const int status = isnan(mx) || m == INFINITY ? kRowNonfinite : m == -INFINITY ? kRowEmpty : kRowOk;
   if (rank == 0 && tid == 0) a.row_status[row] = status;
@@ -1167,7 +1182,6 @@ __global__ void __launch_bounds__(kGivenThreads, 2) given_kernel(GivenArgs a) {
       out_tok[d] = -1;
       if (out_lp) out_lp[d] = NAN;
     }
-    cluster.sync();  // the others have read this CTA's maximum
     return;
   }
   const Mass mass(P.inv_t, m, sh.table);
@@ -1185,12 +1199,10 @@ __global__ void __launch_bounds__(kGivenThreads, 2) given_kernel(GivenArgs a) {
     }
     cut.z = fmaxf(cut.z, zt);
   }
-  const bool greedy = P.flags & kRowGreedy;
-  const bool topk = !greedy && P.top_k > 1 && P.top_k < a.V;
   float ln_s = 0.f;
   bool have_ln_s = false;
-  if (topk && P.top_k <= kListTopK && 2 * P.top_k <= C * kGivenThreads) {
-    if (draw_from_list(rw, a, P, cut, thread_max, row, &ln_s)) return;
+  if (group) {
+    if (draw_from_list(rw, a, P, cut, C * kGivenThreads / group, row, &ln_s)) return;
     have_ln_s = true;
   }
 
@@ -1213,31 +1225,24 @@ __global__ void __launch_bounds__(kGivenThreads, 2) given_kernel(GivenArgs a) {
         }
       }
     }
-    expsum = warp_sum_f(expsum);
+    expsum = block_sum(sh, expsum);
+    rw.send(&Mail::expsum, expsum);
+    if (greedy) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
-    __syncthreads();
-    if (lane == 0) {
-      sh.red_f[warp] = expsum;
-      sh.red_i[warp] = first;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      expsum = 0.f;
-      for (int i = 0; i < kGivenWarps; ++i) {
-        expsum += sh.red_f[i];
-        first = min(first, sh.red_i[i]);
-      }
-      sh.shown.expsum = expsum;
-      sh.shown.index = first;
+      for (int o = 16; o > 0; o >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+      if (lane == 0) sh.red_i[warp] = first;
+      __syncthreads();
+      if (tid < C)
+        for (int i = 0; i < kGivenWarps; ++i) first = min(first, sh.red_i[i]);
+      rw.send(&Mail::index, first);
     }
     cluster.sync();
     expsum = 0.f;
+    first = kMaxIdx;
     for (int r = 0; r < C; ++r) {
-      expsum += rw.at(r)->shown.expsum;
-      first = min(first, rw.at(r)->shown.index);
+      expsum += sh.mail.expsum[r];
+      if (greedy) first = min(first, sh.mail.index[r]);
     }
-    cluster.sync();
     ln_s = logf(expsum);
     if (greedy) {
       for (int d = rank * kGivenThreads + tid; d < a.draws; d += C * kGivenThreads) {
@@ -1261,40 +1266,30 @@ __global__ void __launch_bounds__(kGivenThreads, 2) given_kernel(GivenArgs a) {
         for (int e = 0; e < SL::N; ++e) c += rw.mass.z(x[e]) >= cut.z;
       }
     }
-    c = warp_sum_i(c);
-    __syncthreads();
-    if (lane == 0) sh.red_i[warp] = c;
-    __syncthreads();
-    if (tid == 0) {
-      c = 0;
-      for (int i = 0; i < kGivenWarps; ++i) c += sh.red_i[i];
-      sh.shown.count = c;
-    }
+    rw.send(&Mail::total, block_sum(sh, c));
     cluster.sync();
     int n = 0;
-    for (int r = 0; r < C; ++r) n += rw.at(r)->shown.count;
-    cluster.sync();
+    for (int r = 0; r < C; ++r) n += sh.mail.total[r];
     if (n > P.top_k && !band_select<T, STAGED, false>(rw, &cut, 0.f, P.top_k, nullptr))
       cut = radix_select<T, STAGED, false>(rw, cut, (uint64_t)P.top_k);
   }
-  uint64_t before, W, all;
+  uint64_t before, mine, W, all;
   if (P.flags & kRowTopP) {
     const Cut from = cut;
     if (!band_select<T, STAGED, true>(rw, &cut, P.top_p, 0, &all)) {
       kept_mass(rw, from);
-      all = sum_segments(rw, &before);
+      all = sum_segments(rw, &before, &mine);
       cut = radix_select<T, STAGED, true>(rw, from, part_of(all, P.top_p));
       kept_mass(rw, cut);
     }
-    W = sum_segments(rw, &before);
+    W = sum_segments(rw, &before, &mine);
   } else {
     kept_mass(rw, cut);
-    W = all = sum_segments(rw, &before);
+    W = all = sum_segments(rw, &before, &mine);
   }
   if (all_mass) ln_s = rw.mass.ln_sum(all, kElemBits - a.drop, m);
 
   // the draws: each by a warp of the CTA that holds its mass
-  const uint64_t mine = sh.shown.mass;
   for (int d = warp; d < a.draws; d += kGivenWarps) {
     const uint64_t t = part_of(W, a.uniforms[(int64_t)row * a.draws + d]);
     if (t < before || t - before >= mine) continue;
@@ -1337,9 +1332,10 @@ cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t strea
   // fill the GPU
   int cluster = 1;
   auto slice_of = [&](int c) { return ((a.V + c - 1) / c + kSeg - 1) / kSeg * kSeg; };
-  while (cluster < 16 && ((int64_t)slice_of(cluster) * es > 80 * 1024 ||
-                          slice_of(cluster) > kSeg * kMaxSegs ||
-                          ((int64_t)a.B * cluster < 2 * num_sms && slice_of(cluster) > 4096)))
+  while (cluster < kMaxCtas && ((int64_t)slice_of(cluster) * es > 80 * 1024 ||
+                                slice_of(cluster) > kSeg * kMaxSegs ||
+                                ((int64_t)a.B * cluster * 2 <= 2 * num_sms &&
+                                 slice_of(cluster) > 4096)))
     cluster *= 2;
   a.slice = slice_of(cluster);
   // sums of V masses stay below 2^62
