@@ -13,9 +13,13 @@
 // distinct values among bf16 logits), which puts the chance of a draw differing
 // from the exact one below 1e-5 even for a flat row.
 //
-// One thread-block cluster to a row.  Each CTA keeps its slice of the row in
-// shared memory (one read of the logits); everything after that runs on chip,
-// with the cluster's sums exchanged through distributed shared memory.
+// Two launches.  stream_kernel reads the logits once: a warp takes 1024 of them
+// into registers and leaves their maximum, the maxima of their 64-element groups
+// and their sum of masses (or of exponentials), relative to their own maximum,
+// so that nothing waits for the row's.  finish_kernel settles each row from these
+// and reads again only the segments and groups that can matter: one segment for
+// an unfiltered or greedy row's token, the groups that reach the top_k-th group
+// maximum, the whole row (from L2) only for top-p over everything.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -28,18 +32,21 @@ namespace cg = cooperative_groups;
 namespace vt {
 namespace {
 
-constexpr int kGivenThreads = 512;
-constexpr int kGivenWarps = kGivenThreads / 32;
-constexpr int kSeg = 512;           // elements a warp takes at a time, in vocabulary order
-constexpr int kMaxSegs = 128;       // segments of a slice
-constexpr int kMaxCtas = 16;        // CTAs of a row at most
+constexpr int kStreamThreads = 256;
+constexpr int kThreadsF = 512;      // of finish_kernel
+constexpr int kWarpsF = kThreadsF / 32;
+constexpr int kSeg = kGivenSeg;     // elements a warp takes at a time, in vocabulary order
+constexpr int kGroup = kGivenGroup; // elements that share a group maximum
+constexpr int kGroupsPerSeg = kSeg / kGroup;
+constexpr int kMaxSegs = 1024;      // of a row: V <= 2^20
+constexpr int kMaxCtas = 8;         // CTAs that finish a row
 constexpr int kBins = 2048;
 constexpr float kBinsPerNat = 64.f;  // linear bins: 32 nats below the maximum, then one for all
 constexpr int kList = 2048;         // candidates a row's leader CTA holds
 constexpr int kListTopK = 1024;     // largest top-k taken from group maxima
-constexpr int kListPerThread = kList / kGivenThreads;
-constexpr int kLoadChunks = 8;
+constexpr int kListPerThread = kList / kThreadsF;
 constexpr int kMaxIdx = 0x7fffffff;
+constexpr float kWide = 8000.f;     // maxima beyond: segment sums are not used
 
 // 2^(i/128) in units of 2^-30, from powers of 2^(1/128).
 struct MassTable {
@@ -127,20 +134,6 @@ struct Cut {
   }
 };
 
-// A CTA's mailboxes: slot r is written by CTA r of its cluster before a cluster
-// barrier and read here after it, so that no reader waits on remote loads.  Each
-// field serves one exchange, or exchanges with another barrier between the
-// reading of one and the writing of the next.
-struct Mail {
-  float max[kMaxCtas];
-  float expsum[kMaxCtas];
-  uint64_t mass[kMaxCtas], all[kMaxCtas], kept[kMaxCtas];
-  int count[kMaxCtas], total[kMaxCtas];
-  int index[kMaxCtas], tie[kMaxCtas];
-  Cut cut;  // from the leader
-  int ok;
-};
-
 template <typename T>
 struct Vec;
 template <>
@@ -190,33 +183,117 @@ __device__ __forceinline__ U warp_scan(U v) {
   return v;
 }
 
-static_assert(2 * kListTopK <= kBins, "the groups' maxima fit their array");
-
-template <typename T, bool STAGED>
-struct Slice {
-  static constexpr int N = Vec<T>::N;
+// One row's logits in global memory.
+template <typename T>
+struct RowData {
+  static constexpr int N = Vec<T>::N;           // elements of a 16-byte load
   static constexpr int kIters = kSeg / (32 * N);
-  const T* data;   // shared memory (padded with -inf to whole segments) or the row itself
-  int n;           // elements of this CTA (may be <= 0)
-  int base;        // vocabulary index of the first
-  bool vec;        // 16-byte loads from global memory
-
-  // elements at + 0 .. N - 1 of the slice; -inf past its end
-  __device__ __forceinline__ void load(int at, float (&x)[N]) const {
-    if (STAGED) {
-      Vec<T>::unpack(*reinterpret_cast<const uint4*>(data + at), x);
-    } else if (vec && at + N <= n) {
-      Vec<T>::unpack(__ldg(reinterpret_cast<const uint4*>(data + at)), x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = at + i < n ? elem(data[at + i]) : -INFINITY;
-    }
-  }
-  __device__ __forceinline__ int segs() const { return n > 0 ? (n + kSeg - 1) / kSeg : 0; }
+  const T* data;
+  int V;
+  bool vec;  // 16-byte loads
   // position of the first of a lane's N elements in iteration i of segment s
   static __device__ __forceinline__ int at(int s, int i) {
-    return s * kSeg + (i * 32 + (threadIdx.x & 31)) * N;
+    return s * kSeg + (i * 32 + (int)(threadIdx.x & 31)) * N;
   }
+  __device__ __forceinline__ uint4 raw(int p) const {
+    if (vec && p + N <= V) return __ldg(reinterpret_cast<const uint4*>(data + p));
+    alignas(16) T x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = p + i < V ? data[p + i] : static_cast<T>(-INFINITY);
+    return *reinterpret_cast<const uint4*>(x);
+  }
+  // elements p .. p + N - 1; -inf past the row's end
+  __device__ __forceinline__ void load(int p, float (&x)[N]) const { Vec<T>::unpack(raw(p), x); }
+};
+
+// Whether a row's segments are summed as masses (else as exponentials for the
+// log-probs): rows whose kept mass, or top-p total, is that of every element.
+__device__ __forceinline__ bool sums_masses(const RowParams& P, int V) {
+  return !(P.flags & (kRowGreedy | kRowMinP)) && !(P.top_k > 1 && P.top_k < V);
+}
+
+// One warp to a segment of 1024 logits, in registers (bf16: four 16-byte loads a
+// lane, fp32 eight).  What bounds it: HBM.  It keeps the loads of one segment a
+// warp in flight and needs no barrier.
+template <typename T>
+__global__ void __launch_bounds__(kStreamThreads, sizeof(T) == 2 ? 5 : 4)
+    stream_kernel(GivenArgs a) {
+  using RD = RowData<T>;
+  __shared__ uint32_t table[128];
+  if (threadIdx.x < 128) table[threadIdx.x] = c_mass_table.v[threadIdx.x];
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int lane = threadIdx.x & 31;
+  const uint32_t items = (uint32_t)a.B * a.segs, step = gridDim.x * (kStreamThreads / 32);
+  for (uint32_t it = blockIdx.x * (kStreamThreads / 32) + (threadIdx.x >> 5); it < items;
+       it += step) {
+    const int row = (int)(it / a.segs), seg = (int)(it % a.segs);
+    const RowData<T> rd{static_cast<const T*>(a.logits) + row * a.ld, a.V, a.aligned != 0};
+    uint4 v[RD::kIters];
+#pragma unroll
+    for (int i = 0; i < RD::kIters; ++i) v[i] = rd.raw(RD::at(seg, i));
+    const RowParams P = a.params[row];
+    float mx = -INFINITY;
+    constexpr int kLanes = kGroup / RD::N;  // lanes of a group
+    float* gmax = a.group_max + ((int64_t)row * a.segs + seg) * kGroupsPerSeg;
+#pragma unroll
+    for (int i = 0; i < RD::kIters; ++i) {
+      float x[RD::N];
+      Vec<T>::unpack(v[i], x);
+      float g = x[0];
+#pragma unroll
+      for (int e = 1; e < RD::N; ++e) g = max_nan(g, x[e]);
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, o));
+      if (lane % kLanes == 0) gmax[i * (32 / kLanes) + lane / kLanes] = g;
+      mx = max_nan(mx, g);
+    }
+#pragma unroll
+    for (int o = kLanes; o < 32; o <<= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float zm = __fmul_rn(mx, P.inv_t);
+    uint64_t sum = 0;
+    if (zm > -INFINITY && zm < INFINITY) {  // else the row has no token, or this part no mass
+      if (sums_masses(P, a.V)) {
+        const Mass mass(P.inv_t, zm, table);
+#pragma unroll
+        for (int i = 0; i < RD::kIters; ++i) {
+          float x[RD::N];
+          Vec<T>::unpack(v[i], x);
+#pragma unroll
+          for (int e = 0; e < RD::N; ++e) sum += mass.of(mass.z(x[e]));
+        }
+        sum = warp_sum_u64(sum);
+      } else if (a.out_logprobs) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < RD::kIters; ++i) {
+          float x[RD::N];
+          Vec<T>::unpack(v[i], x);
+#pragma unroll
+          for (int e = 0; e < RD::N; ++e)
+            s += ex2_approx(__fmul_rn(__fsub_rn(__fmul_rn(x[e], P.inv_t), zm), kLog2e));
+        }
+        sum = __float_as_uint(warp_sum_f(s));
+      }
+    }
+    if (lane == 0) {
+      a.seg_max[(int64_t)row * a.segs + seg] = mx;
+      a.seg_sum[(int64_t)row * a.segs + seg] = sum;
+    }
+  }
+}
+
+// ---- finishing a row ---------------------------------------------------------
+
+// A CTA's mailboxes: slot r is written by CTA r of its team before a team barrier
+// and read here after it, so that no reader waits on remote loads.  Each field
+// serves one exchange, or exchanges with another barrier between the reading of
+// one and the writing of the next.
+struct Mail {
+  uint64_t mass[kMaxCtas], all[kMaxCtas], kept[kMaxCtas];
+  int count[kMaxCtas], total[kMaxCtas], tie[kMaxCtas];
+  Cut cut;  // from the leader
+  int ok;
 };
 
 // The candidates of a row in vocabulary order, on its leader CTA.
@@ -227,56 +304,66 @@ struct List {
 
 struct Hist {
   uint32_t own[kBins];
-  union {
-    uint32_t sum[kBins];     // over the cluster
-    float group_max[kBins];  // maxima of groups of elements, of all CTAs
-  };
+  uint32_t sum[kBins];  // over the team
 };
 
 struct Shared {
   Mail mail;
-  float red_f[kGivenWarps];
-  uint64_t red_w[kGivenWarps], red_n[kGivenWarps];
-  int red_i[kGivenWarps];
-  uint64_t bars[kLoadChunks];
+  float red_f[kWarpsF];
+  uint64_t red_w[kWarpsF], red_n[kWarpsF];
+  int red_i[kWarpsF];
   uint32_t table[128];
-  uint64_t seg_w[kMaxSegs];   // masses of the segments, then their inclusive sums
+  float seg_max[kMaxSegs];    // raw maxima of the row's segments
+  uint64_t seg_w[kMaxSegs];   // their masses (element units), then inclusive sums
   int seg_n[kMaxSegs];        // candidates of the segments, then those before each
   int lo, hi;
   int bin;
   uint32_t bin_n;
   uint64_t above;
+  Cut cut;
   uint32_t digit_n[256];      // radix selection, 8 bits at a time
   unsigned long long digit_w[256];
-  uint64_t run[kGivenThreads];  // inclusive masses of the threads' list entries
+  union {
+    uint64_t run[kThreadsF];    // inclusive masses of the threads' list entries
+    uint64_t sorted[kList];     // (key, ~position in the list), descending
+    uint16_t groups[kMaxSegs * kGroupsPerSeg / 2];  // groups to read, in order
+  };
   union {
     Hist hist;
     List list;
   };
 };
 
-// The row of this cluster.
-template <typename T, bool STAGED>
+// A row and the CTAs that finish it (a team: the cluster, or rank 0 alone).
+template <typename T>
 struct Row {
-  Slice<T, STAGED> sl;
+  RowData<T> rd;
   Shared& sh;
   Mass mass;
-  float m;        // tempered maximum
-  int slice;      // elements per CTA
-  int drop;       // row sums are in units of 2^(E - kElemBits + drop)
-  __device__ __forceinline__ Row(const Slice<T, STAGED>& sl_, Shared& sh_, const Mass& mass_,
-                                 float m_, int slice_, int drop_)
-      : sl(sl_), sh(sh_), mass(mass_), m(m_), slice(slice_),
-        drop(drop_) {}
-  __device__ __forceinline__ Shared* at(int rank) {
-    return cg::this_cluster().map_shared_rank(&sh, rank);
+  float m;      // tempered maximum
+  int segs;     // of the row
+  int drop;     // row sums are in units of 2^(E - kElemBits + drop)
+  int C, rank;  // the team
+  int s0, s1;   // this CTA's segments
+  int per;      // segments to a CTA
+  __device__ __forceinline__ Row(const RowData<T>& rd_, Shared& sh_, const Mass& mass_, float m_,
+                                 int segs_, int drop_, int C_, int rank_)
+      : rd(rd_), sh(sh_), mass(mass_), m(m_), segs(segs_), drop(drop_), C(C_), rank(rank_) {
+    per = (segs + C - 1) / C;
+    s0 = min(segs, rank * per);
+    s1 = min(segs, s0 + per);
+  }
+  __device__ __forceinline__ Shared* at(int r) {
+    return C > 1 ? cg::this_cluster().map_shared_rank(&sh, r) : &sh;
+  }
+  __device__ __forceinline__ void sync() {
+    if (C > 1) cg::this_cluster().sync();
+    else __syncthreads();
   }
   // thread r of the block stores v in this CTA's slot of CTA r's mailbox
   template <typename V>
   __device__ __forceinline__ void send(V (Mail::*field)[kMaxCtas], V v) {
-    const int C = cg::this_cluster().num_blocks();
-    if ((int)threadIdx.x < C)
-      (at((int)threadIdx.x)->mail.*field)[cg::this_cluster().block_rank()] = v;
+    if ((int)threadIdx.x < C) (at((int)threadIdx.x)->mail.*field)[rank] = v;
   }
   __device__ __forceinline__ uint64_t coarse(uint64_t w) const {
     return (w + (1ull << (drop - 1))) >> drop;
@@ -284,6 +371,7 @@ struct Row {
   __device__ __forceinline__ float bins_below(float z) const {
     return __fmul_rn(__fsub_rn(m, z), kBinsPerNat);
   }
+  __device__ __forceinline__ float seg_top(int s) const { return mass.z(sh.seg_max[s]); }
 };
 
 __device__ __forceinline__ int bin_of(float t) {
@@ -299,7 +387,7 @@ __device__ __forceinline__ uint64_t block_scan(Shared& sh, uint64_t w, uint64_t*
   __syncthreads();
   uint64_t before = inc - w, all = 0;
 #pragma unroll
-  for (int i = 0; i < kGivenWarps; ++i) {
+  for (int i = 0; i < kWarpsF; ++i) {
     if (i < warp) before += sh.red_w[i];
     all += sh.red_w[i];
   }
@@ -315,7 +403,7 @@ __device__ __forceinline__ float block_sum(Shared& sh, float v) {
   __syncthreads();
   v = 0.f;
 #pragma unroll
-  for (int i = 0; i < kGivenWarps; ++i) v += sh.red_f[i];
+  for (int i = 0; i < kWarpsF; ++i) v += sh.red_f[i];
   return v;
 }
 __device__ __forceinline__ int block_sum(Shared& sh, int v) {
@@ -325,7 +413,7 @@ __device__ __forceinline__ int block_sum(Shared& sh, int v) {
   __syncthreads();
   v = 0;
 #pragma unroll
-  for (int i = 0; i < kGivenWarps; ++i) v += sh.red_i[i];
+  for (int i = 0; i < kWarpsF; ++i) v += sh.red_i[i];
   return v;
 }
 
@@ -364,20 +452,17 @@ __device__ __forceinline__ void find_digit(Shared& sh, uint64_t before, uint64_t
 }
 
 // The row's boundary by radix selection on the order key, 8 bits at a time, for
-// any number of equal elements.  The way of last resort: it counts every element
-// by shared atomics, thousands to an address.
+// any number of equal elements: the way of last resort.  A warp whose elements
+// fall on one digit adds them up first (equal values would all go to one address).
 //   MASS: elements are kept while the mass before them is <= target.
 //   else: the first `target` of them are kept (1 <= target <= their number).
-// Every CTA of the cluster returns the same cut.
-template <typename T, bool STAGED, bool MASS>
-__device__ __noinline__ Cut radix_select(const Row<T, STAGED>& row_in, Cut cut, uint64_t target) {
-  Row<T, STAGED> rw = row_in;  // in registers
-  using SL = Slice<T, STAGED>;
-  const SL& sl = rw.sl;
+// Every CTA of the team returns the same cut.
+template <typename T, bool MASS>
+__device__ __noinline__ Cut radix_select(const Row<T>& row_in, Cut cut, uint64_t target) {
+  Row<T> rw = row_in;  // in registers
+  using RD = RowData<T>;
   Shared& sh = rw.sh;
-  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = cluster.block_rank();
   uint32_t prefix = 0;
   uint64_t before = 0;
 #pragma unroll 1
@@ -386,43 +471,52 @@ __device__ __noinline__ Cut radix_select(const Row<T, STAGED>& row_in, Cut cut, 
       sh.digit_n[tid] = 0;
       sh.digit_w[tid] = 0;
     }
-    cluster.sync();
-    for (int s = warp; s < sl.segs(); s += kGivenWarps) {
+    rw.sync();
+    for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
+      if (rw.seg_top(s) < cut.z) continue;
 #pragma unroll 1
-      for (int i = 0; i < SL::kIters; ++i) {
-        const int at = SL::at(s, i);
-        float x[SL::N];
-        sl.load(at, x);
-#pragma unroll
-        for (int e = 0; e < SL::N; ++e) {
+      for (int i = 0; i < RD::kIters; ++i) {
+        const int at = RD::at(s, i);
+        float x[RD::N];
+        rw.rd.load(at, x);
+#pragma unroll 1
+        for (int e = 0; e < RD::N; ++e) {
           const float z = rw.mass.z(x[e]);
           const uint32_t k = ord_key(z);
-          if (!cut.keeps(z, sl.base + at + e)) continue;
-          if (shift < 24 && (k >> (shift + 8)) != prefix) continue;
+          const bool in = cut.keeps(z, at + e) && (shift == 24 || (k >> (shift + 8)) == prefix);
           const int bin = (k >> shift) & 255;
-          atomicAdd(&sh.digit_n[bin], 1u);
-          if (MASS) {
-            const uint64_t w = rw.coarse(rw.mass.of(z));
-            if (w) atomicAdd(&sh.digit_w[bin], (unsigned long long)w);
+          const unsigned ins = __ballot_sync(0xffffffffu, in);
+          if (!ins) continue;
+          const uint64_t w = MASS && in ? rw.coarse(rw.mass.of(z)) : 0;
+          const int first = __shfl_sync(0xffffffffu, bin, __ffs(ins) - 1);
+          if (__all_sync(0xffffffffu, !in || bin == first)) {
+            const uint64_t sum = MASS ? warp_sum_u64(w) : 0;
+            if (lane == 0) {
+              atomicAdd(&sh.digit_n[first], (unsigned)__popc(ins));
+              if (MASS && sum) atomicAdd(&sh.digit_w[first], (unsigned long long)sum);
+            }
+          } else if (in) {
+            atomicAdd(&sh.digit_n[bin], 1u);
+            if (MASS && w) atomicAdd(&sh.digit_w[bin], (unsigned long long)w);
           }
         }
       }
     }
     __syncthreads();
     // the others' digits are added to the leader's, which finds the boundary
-    if (rank != 0 && tid < 256 && sh.digit_n[tid]) {
+    if (rw.rank != 0 && tid < 256 && sh.digit_n[tid]) {
       atomicAdd(&rw.at(0)->digit_n[tid], sh.digit_n[tid]);
       if (MASS) atomicAdd(&rw.at(0)->digit_w[tid], sh.digit_w[tid]);
     }
-    cluster.sync();
-    if (rank == 0 && warp == 0) find_digit<MASS>(sh, before, target);
-    cluster.sync();
+    rw.sync();
+    if (rw.rank == 0 && warp == 0) find_digit<MASS>(sh, before, target);
+    rw.sync();
     const Shared* lead = rw.at(0);
     prefix = (prefix << 8) | (uint32_t)lead->bin;
     before = lead->above;
   }
   const uint32_t ties = rw.at(0)->bin_n;
-  cluster.sync();
+  rw.sync();
   const float zk = key_value(prefix);
   uint64_t take;
   if (MASS) {
@@ -436,18 +530,19 @@ __device__ __noinline__ Cut radix_select(const Row<T, STAGED>& row_in, Cut cut, 
 
   // the index of the take-th of the equal elements
   int mine = 0;
-  for (int s = warp; s < sl.segs(); s += kGivenWarps) {
+  for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
     int c = 0;
+    if (rw.seg_top(s) >= zk) {
 #pragma unroll 1
-    for (int i = 0; i < SL::kIters; ++i) {
-      const int at = SL::at(s, i);
-      float x[SL::N];
-      sl.load(at, x);
+      for (int i = 0; i < RD::kIters; ++i) {
+        const int at = RD::at(s, i);
+        float x[RD::N];
+        rw.rd.load(at, x);
 #pragma unroll
-      for (int e = 0; e < SL::N; ++e)
-        c += rw.mass.z(x[e]) == zk && sl.base + at + e <= old_idx;
+        for (int e = 0; e < RD::N; ++e) c += rw.mass.z(x[e]) == zk && at + e <= old_idx;
+      }
+      c = warp_sum_i(c);
     }
-    c = warp_sum_i(c);
     if (lane == 0) {
       sh.seg_n[s] = c;
       mine += c;
@@ -455,210 +550,180 @@ __device__ __noinline__ Cut radix_select(const Row<T, STAGED>& row_in, Cut cut, 
   }
   mine = block_sum(sh, mine);
   rw.send(&Mail::total, mine);
-  cluster.sync();
+  rw.sync();
   uint64_t ahead = 0;
-  for (int r = 0; r < rank; ++r) ahead += sh.mail.total[r];
+  for (int r = 0; r < rw.rank; ++r) ahead += sh.mail.total[r];
   if (tid == 0) sh.lo = -1;
   __syncthreads();
   if (take > ahead && take <= ahead + mine && warp == 0) {
-    int left = (int)(take - ahead), s = 0;
+    int left = (int)(take - ahead), s = rw.s0;
     while (left > sh.seg_n[s]) left -= sh.seg_n[s++];
-    for (int i = 0; i < SL::kIters && left > 0; ++i) {
-      const int at = SL::at(s, i);
-      float x[SL::N];
-      sl.load(at, x);
+    for (int i = 0; i < RD::kIters && left > 0; ++i) {
+      const int at = RD::at(s, i);
+      float x[RD::N];
+      rw.rd.load(at, x);
       int c = 0;
 #pragma unroll
-      for (int e = 0; e < SL::N; ++e) c += rw.mass.z(x[e]) == zk && sl.base + at + e <= old_idx;
+      for (int e = 0; e < RD::N; ++e) c += rw.mass.z(x[e]) == zk && at + e <= old_idx;
       const int inc = warp_scan(c);
       if (left > inc - c && left <= inc) {
         int nth = left - (inc - c);
 #pragma unroll
-        for (int e = 0; e < SL::N; ++e)
-          if (rw.mass.z(x[e]) == zk && --nth == 0) sh.lo = sl.base + at + e;
+        for (int e = 0; e < RD::N; ++e)
+          if (rw.mass.z(x[e]) == zk && --nth == 0) sh.lo = at + e;
       }
       left -= __shfl_sync(0xffffffffu, inc, 31);
     }
   }
   __syncthreads();
   rw.send(&Mail::tie, sh.lo);
-  cluster.sync();
+  rw.sync();
   int idx = -1;
-  for (int r = 0; r < (int)cluster.num_blocks(); ++r) idx = max(idx, sh.mail.tie[r]);
+  for (int r = 0; r < rw.C; ++r) idx = max(idx, sh.mail.tie[r]);
   return Cut{zk, idx};
 }
 
-// The boundary within the leader's list of n candidates (in vocabulary order), by
-// radix selection on the order key; `target` as above.  weight(i): entry i's
-// mass in list units, 0 when it has no part in the selection.  Called by all
-// threads of the leader.
-template <bool MASS, typename W>
-__device__ __forceinline__ Cut list_select(Shared& sh, int n, uint64_t target, W weight) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t prefix = 0;
-  uint64_t before = 0;  // elements (or mass) ahead of the prefix
-#pragma unroll 1
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) {
-      sh.digit_n[tid] = 0;
-      if (MASS) sh.digit_w[tid] = 0;
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int i = tid; i < n; i += kGivenThreads) {
-      const uint32_t k = sh.list.key[i];
-      if (shift < 24 && (k >> (shift + 8)) != prefix) continue;
-      const int bin = (k >> shift) & 255;
-      if (MASS) {
-        const uint64_t w = weight(i);
-        if (!w) continue;
-        atomicAdd(&sh.digit_w[bin], (unsigned long long)w);
-      }
-      atomicAdd(&sh.digit_n[bin], 1u);
-    }
-    __syncthreads();
-    if (warp == 0) find_digit<MASS>(sh, before, target);
-    __syncthreads();
-    prefix = (prefix << 8) | (uint32_t)sh.bin;
-    before = sh.above;
+constexpr int kListDrop = 2;  // list masses: units of 2^(E - kElemBits + 2), 2048 below 2^62
+
+// The leader's list in the order (z descending, index ascending), into sh.sorted:
+// a bitonic sort with four neighbouring entries in each thread's registers, so
+// that of the 66 steps over 2048 entries 21 stay in a thread, 35 are shuffles and
+// only 10 go through shared memory.  Threads past the entries take part in the
+// barriers alone.
+constexpr int kSortPer = 4;
+static_assert(kSortPer * kThreadsF == kList, "a thread holds four entries of a full list");
+__device__ __noinline__ void sort_list(Shared& sh, int n) {
+  const int tid = threadIdx.x;
+  int N = 128;
+  while (N < n) N *= 2;
+  const bool on = tid * kSortPer < N;  // whole warps
+  uint64_t v[kSortPer];
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kSortPer; ++q) {
+    const int i = tid * kSortPer + q;
+    v[q] = i < n ? ((uint64_t)sh.list.key[i] << 32) | (uint32_t)~i : 0ull;
   }
-  // the take-th of the elements at the key, in vocabulary order
-  if (warp == 0) {
-    const uint32_t ties = sh.bin_n;
-    int found = kMaxIdx;
-    uint32_t seen = 0;
-    uint64_t take = 0;
-    if (ties > 1) {
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const int i = i0 + lane;
-        const bool tie = i < n && sh.list.key[i] == prefix && (!MASS || weight(i) > 0);
-        const unsigned mask = __ballot_sync(0xffffffffu, tie);
-        if (!mask) continue;
-        if (take == 0) {
-          take = MASS ? (target - before) / weight(i0 + __ffs(mask) - 1) + 1 : target - before;
-          if (take >= ties) break;
+  for (int k = 2; k <= N; k <<= 1) {
+    int j = k >> 1;
+    if (j >= 32 * kSortPer) {
+      // through shared memory, all large steps of this merge
+      for (; j >= 32 * kSortPer; j >>= 1) {
+        __syncthreads();
+        if (on) {
+#pragma unroll
+          for (int q = 0; q < kSortPer; ++q) sh.sorted[q * kThreadsF + tid] = v[q];
         }
-        const uint32_t nth = seen + __popc(mask & ((1u << lane) - 1)) + 1;
-        if (tie && nth == take) found = sh.list.idx[i];
-        seen += __popc(mask);
+        __syncthreads();
+        if (on) {
+          const int other = tid ^ (j / kSortPer);
+          const bool lower = (tid & (j / kSortPer)) == 0;
+          const bool desc = ((tid * kSortPer) & k) == 0;
+#pragma unroll
+          for (int q = 0; q < kSortPer; ++q) {
+            const uint64_t o = sh.sorted[q * kThreadsF + other];
+            v[q] = (lower == desc) == (v[q] > o) ? v[q] : o;
+          }
+        }
+      }
+    }
+    if (on) {
+      for (; j >= kSortPer; j >>= 1) {
+        const int d = j / kSortPer;
+        const bool lower = (tid & d) == 0;
+        const bool desc = ((tid * kSortPer) & k) == 0;
+#pragma unroll
+        for (int q = 0; q < kSortPer; ++q) {
+          const uint64_t o = __shfl_xor_sync(0xffffffffu, v[q], d);
+          v[q] = (lower == desc) == (v[q] > o) ? v[q] : o;
+        }
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) found = min(found, __shfl_xor_sync(0xffffffffu, found, o));
+      for (int jj = kSortPer / 2; jj > 0; jj >>= 1) {
+        if (jj > j) continue;
+#pragma unroll
+        for (int q = 0; q < kSortPer; ++q) {
+          if (q & jj) continue;
+          const bool desc = ((tid * kSortPer + q) & k) == 0;
+          const uint64_t x = v[q], y = v[q | jj];
+          const bool swap = desc ? x < y : x > y;
+          v[q] = swap ? y : x;
+          v[q | jj] = swap ? x : y;
+        }
+      }
     }
-    if (lane == 0) sh.mail.cut = Cut{key_value(prefix), found};
   }
   __syncthreads();
-  return sh.mail.cut;
+  if (on) {
+#pragma unroll
+    for (int q = 0; q < kSortPer; ++q) sh.sorted[tid * kSortPer + q] = v[q];
+  }
+  __syncthreads();
+}
+// The cut whose last element is entry i of the sorted list.
+__device__ __forceinline__ Cut sorted_cut(const Shared& sh, int i) {
+  const uint64_t e = sh.sorted[i];
+  return Cut{key_value((uint32_t)(e >> 32)), sh.list.idx[~(uint32_t)e]};
+}
+// Of the first n entries of the sorted list, those with a mass (list units) of at
+// most target before them: the cut, and their total mass in *all.  `share` >= 0:
+// the target is that part of the total instead.
+__device__ __forceinline__ Cut cut_by_mass(Shared& sh, const Mass& mass, int n, uint64_t target,
+                                           float share, uint64_t* all) {
+  const int tid = threadIdx.x;
+  uint64_t w[kListPerThread], sum = 0;
+#pragma unroll
+  for (int q = 0; q < kListPerThread; ++q) {
+    const int i = tid * kListPerThread + q;
+    w[q] = i < n ? (mass.of(key_value((uint32_t)(sh.sorted[i] >> 32))) + 2) >> kListDrop : 0;
+    sum += w[q];
+  }
+  uint64_t a = block_scan(sh, sum, all);
+  if (share >= 0.f) target = part_of(*all, share);
+  int kept = 0;
+#pragma unroll
+  for (int q = 0; q < kListPerThread; ++q) {
+    kept += tid * kListPerThread + q < n && a <= target;
+    a += w[q];
+  }
+  kept = block_sum(sh, kept);
+  return sorted_cut(sh, kept - 1);
 }
 
-// The threads' sums of seg_n to the elements before each segment; the CTA's
-// total is returned to every thread of warp 0.
-__device__ __forceinline__ int scan_segments(Shared& sh, int segs) {
+// seg_n of this CTA's segments to the elements before each; their total (warp 0).
+template <typename T>
+__device__ __forceinline__ int scan_segments(const Row<T>& rw) {
   const int lane = threadIdx.x & 31;
   int carry = 0;
-  for (int s0 = 0; s0 < segs; s0 += 32) {
-    const int c = s0 + lane < segs ? sh.seg_n[s0 + lane] : 0;
+  for (int b = rw.s0; b < rw.s1; b += 32) {
+    const int c = b + lane < rw.s1 ? rw.sh.seg_n[b + lane] : 0;
     const int inc = warp_scan(c) + carry;
-    if (s0 + lane < segs) sh.seg_n[s0 + lane] = inc - c;
+    if (b + lane < rw.s1) rw.sh.seg_n[b + lane] = inc - c;
     carry = __shfl_sync(0xffffffffu, inc, 31);
   }
   return carry;
 }
 
-// The elements that `wanted` takes, of every CTA, into the leader's list in
-// vocabulary order.  seg_n holds how many each segment has (every warp its own
-// segments); `post` sends what else the others need with the same barrier.
-// Returns their number in the cluster, or -1 when the list does not hold them.
-// The caller's next cluster barrier publishes the list.
-template <typename T, bool STAGED, typename F, typename G>
-__device__ __forceinline__ int gather(Row<T, STAGED>& rw, F wanted, G post) {
-  using SL = Slice<T, STAGED>;
-  const SL& sl = rw.sl;
-  Shared& sh = rw.sh;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int warp = threadIdx.x >> 5;
-  __syncthreads();
-  if (warp == 0) {
-    const int c = scan_segments(sh, sl.segs());
-    rw.send(&Mail::count, c);
-  }
-  post();
-  cluster.sync();
-  int total = 0, base = 0;
-  const int rank = cluster.block_rank();
-  for (int r = 0; r < (int)cluster.num_blocks(); ++r) {
-    if (r == rank) base = total;
-    total += sh.mail.count[r];
-  }
-  if (total > kList) return -1;
-  List& list = rw.at(0)->list;
-  const int mine = sh.mail.count[rank];
-  for (int s = warp; s < sl.segs(); s += kGivenWarps) {
-    const int from = sh.seg_n[s], to = s + 1 < sl.segs() ? sh.seg_n[s + 1] : mine;
-    if (from == to) continue;
-    int off = base + from;
-#pragma unroll 1
-    for (int i = 0; i < SL::kIters; ++i) {
-      const int at = SL::at(s, i);
-      float x[SL::N];
-      sl.load(at, x);
-      unsigned take = 0;
-#pragma unroll
-      for (int e = 0; e < SL::N; ++e) take |= wanted(x[e], sl.base + at + e) ? 1u << e : 0u;
-      if (!__any_sync(0xffffffffu, take)) continue;
-      const int c = __popc(take);
-      const int inc = warp_scan(c);
-      int p = off + inc - c;
-#pragma unroll
-      for (int e = 0; e < SL::N; ++e)
-        if ((take >> e) & 1) {
-          list.key[p] = ord_key(rw.mass.z(x[e]));
-          list.idx[p] = sl.base + at + e;
-          ++p;
-        }
-      off += __shfl_sync(0xffffffffu, inc, 31);
-    }
-  }
-  return total;
-}
-
-// Elements kept by a cut in the linear bins lo .. hi.
-template <typename T, bool STAGED>
-struct InBins {
-  const Row<T, STAGED>& rw;
-  Cut cut;
-  int lo, hi;
-  __device__ __forceinline__ bool operator()(float x, int j) const {
-    const float z = rw.mass.z(x);
-    const int bin = bin_of(rw.bins_below(z));
-    return cut.keeps(z, j) && bin >= lo && bin <= hi;
-  }
-};
-
-constexpr int kListDrop = 2;  // list masses: units of 2^(E - kElemBits + 2), 2048 below 2^62
-
 // The boundary of the elements kept by `cut` by one linear histogram below the
 // maximum, which brackets it, and a list of the elements in the bracket.
-//   MASS: target is the top-p share `p`; on success the CTAs' seg_w hold the
-//   masses of the kept elements (element units) and *row_mass the mass of all
-//   elements kept by `cut`.
+//   MASS: the boundary of the top-p share `p` of *row_mass, the mass of all
+//   elements kept by `cut` (row units; 0: not known yet, and set here).  On
+//   success the CTAs' seg_w hold the masses of the kept elements (element units).
 //   else: the first `top_k` are kept.
 // Returns false (the same in every CTA) when the bracket holds too many, or, by
 // mass, turns out not to hold the boundary.
-template <typename T, bool STAGED, bool MASS>
-__device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_io, float p,
-                                         int top_k, uint64_t* row_mass) {
-  Row<T, STAGED> rw = row_in;  // in registers
-  using SL = Slice<T, STAGED>;
-  const SL& sl = rw.sl;
+template <typename T, bool MASS>
+__device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, float p, int top_k,
+                                         uint64_t* row_mass) {
+  Row<T> rw = row_in;  // in registers
+  using RD = RowData<T>;
   Shared& sh = rw.sh;
-  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = cluster.num_blocks(), rank = cluster.block_rank();
   const Cut cut = *cut_io;
-  constexpr int kPer = kBins / kGivenThreads;
+  constexpr int kPer = kBins / kThreadsF;
+  __syncthreads();
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kGivenThreads] = 0;
+  for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kThreadsF] = 0;
   if (tid == 0) {
     sh.lo = kBins;
     sh.hi = -1;
@@ -666,14 +731,15 @@ __device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_
   __syncthreads();
   // by mass: each element adds its mass relative to its bin's upper edge in
   // units of 1/4095, so a bin's mass is known to within 1.3e-4 of itself
-  for (int s = warp; s < sl.segs(); s += kGivenWarps) {
-#pragma unroll 1
-    for (int i = 0; i < SL::kIters; ++i) {
-      const int at = SL::at(s, i);
-      float x[SL::N];
-      sl.load(at, x);
+  for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
+    if (rw.seg_top(s) < cut.z) continue;
+#pragma unroll 2
+    for (int i = 0; i < RD::kIters; ++i) {
+      const int at = RD::at(s, i);
+      float x[RD::N];
+      rw.rd.load(at, x);
 #pragma unroll
-      for (int e = 0; e < SL::N; ++e) {
+      for (int e = 0; e < RD::N; ++e) {
         const float z = rw.mass.z(x[e]);
         const float t = rw.bins_below(z);
         const int bin = bin_of(t);
@@ -682,24 +748,30 @@ __device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_
           const float f = t - (float)bin;
           add = (uint32_t)__fmaf_rn(f, __fmaf_rn(f, 0.4999f, -63.984f), 4095.5f);
         }
-        if (cut.keeps(z, sl.base + at + e) && !(MASS && bin == kBins - 1))
+        if (cut.keeps(z, at + e) && !(MASS && bin == kBins - 1))
           atomicAdd(&sh.hist.own[bin], add);
       }
     }
   }
-  // the cluster's histogram: CTA r sums a share of the bins and sends it to all
-  cluster.sync();
-  const int share = kBins / C;
-  for (int q = tid; q < share; q += kGivenThreads) {
-    const int bin = rank * share + q;
-    uint32_t c = 0;
-    for (int r = 0; r < C; ++r) c += rw.at(r)->hist.own[bin];
-    for (int r = 0; r < C; ++r) rw.at(r)->hist.sum[bin] = c;
+  // the team's histogram: CTA r sums a share of the bins and sends it to all
+  rw.sync();
+  const uint32_t* bins = sh.hist.own;
+  if (rw.C > 1) {
+    const int share = kBins / rw.C;
+    for (int q = tid; q < share; q += kThreadsF) {
+      const int bin = rw.rank * share + q;
+      uint32_t c = 0;
+#pragma unroll 4
+      for (int r = 0; r < rw.C; ++r) c += rw.at(r)->hist.own[bin];
+#pragma unroll 4
+      for (int r = 0; r < rw.C; ++r) rw.at(r)->hist.sum[bin] = c;
+    }
+    rw.sync();
+    bins = sh.hist.sum;
   }
-  cluster.sync();
   uint32_t cn[kPer];
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) cn[q] = sh.hist.sum[tid * kPer + q];
+  for (int q = 0; q < kPer; ++q) cn[q] = bins[tid * kPer + q];
   uint64_t above_n = 0;  // elements above the bracket (by count)
   if (MASS) {
     float cf[kPer], tf = 0.f;
@@ -708,11 +780,11 @@ __device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_
       cf[q] = (float)cn[q] * ex2_approx((float)(tid * kPer + q) * (-kLog2e / kBinsPerNat));
       tf += cf[q];
     }
-    float inc = warp_scan(tf);
+    const float inc = warp_scan(tf);
     if (lane == 31) sh.red_f[warp] = inc;
     __syncthreads();
     float a = inc - tf, all = 0.f;
-    for (int i = 0; i < kGivenWarps; ++i) {
+    for (int i = 0; i < kWarpsF; ++i) {
       if (i < warp) a += sh.red_f[i];
       all += sh.red_f[i];
     }
@@ -747,32 +819,35 @@ __device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_
   if (!MASS) above_n = sh.above;
   if (lo > hi) return false;  // (a histogram without mass)
 
+  // the masses above the bracket, and how many elements are in it; segments that
+  // end below it are not read, unless the mass of all is wanted
+  const bool want_all = MASS && *row_mass == 0;
   uint64_t w_above = 0, w_all = 0;
-  for (int s = warp; s < sl.segs(); s += kGivenWarps) {
+  for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
     uint64_t above = 0, rest = 0;
     int c = 0;
+    if (want_all || bin_of(rw.bins_below(rw.seg_top(s))) <= hi) {
 #pragma unroll 1
-    for (int i = 0; i < SL::kIters; ++i) {
-      const int at = SL::at(s, i);
-      float x[SL::N];
-      sl.load(at, x);
+      for (int i = 0; i < RD::kIters; ++i) {
+        const int at = RD::at(s, i);
+        float x[RD::N];
+        rw.rd.load(at, x);
 #pragma unroll
-      for (int e = 0; e < SL::N; ++e) {
-        const float z = rw.mass.z(x[e]);
-        const bool in = cut.keeps(z, sl.base + at + e);
-        const int bin = bin_of(rw.bins_below(z));
-        c += in && bin >= lo && bin <= hi;
-        if (MASS) {
-          const uint64_t w = in ? rw.mass.of(z) : 0;
-          above += bin < lo ? w : 0;
-          rest += w;
+        for (int e = 0; e < RD::N; ++e) {
+          const float z = rw.mass.z(x[e]);
+          const bool in = cut.keeps(z, at + e);
+          const int bin = bin_of(rw.bins_below(z));
+          c += in && bin >= lo && bin <= hi;
+          if (MASS && in && (bin < lo || want_all)) {
+            const uint64_t w = rw.mass.of(z);
+            above += bin < lo ? w : 0;
+            rest += w;
+          }
         }
       }
-    }
-    c = warp_sum_i(c);
-    if (MASS) {
-      above = warp_sum_u64(above);
-      rest = warp_sum_u64(rest);
+      c = warp_sum_i(c);
+      if (MASS) above = warp_sum_u64(above);
+      if (want_all) rest = warp_sum_u64(rest);
     }
     if (lane == 0) {
       sh.seg_n[s] = c;
@@ -787,142 +862,184 @@ __device__ __noinline__ bool band_select(const Row<T, STAGED>& row_in, Cut* cut_
     sh.red_w[warp] = w_above;
     sh.red_n[warp] = w_all;
   }
-  const int n = gather(rw, InBins<T, STAGED>{rw, cut, lo, hi}, [&]() {
-    if (MASS && warp == 0) {
-      w_above = warp_sum_u64(lane < kGivenWarps ? sh.red_w[lane] : 0);
-      w_all = warp_sum_u64(lane < kGivenWarps ? sh.red_n[lane] : 0);
+  __syncthreads();
+  if (warp == 0) {
+    const int c = scan_segments(rw);
+    rw.send(&Mail::count, c);
+    if (MASS) {
+      w_above = warp_sum_u64(lane < kWarpsF ? sh.red_w[lane] : 0);
+      w_all = warp_sum_u64(lane < kWarpsF ? sh.red_n[lane] : 0);
       rw.send(&Mail::mass, w_above);
       rw.send(&Mail::all, w_all);
     }
-  });
+  }
+  rw.sync();
+  int n = 0, base = 0;
+  for (int r = 0; r < rw.C; ++r) {
+    if (r == rw.rank) base = n;
+    n += sh.mail.count[r];
+  }
   if (MASS) {
     w_above = w_all = 0;
-    for (int r = 0; r < C; ++r) {
+    for (int r = 0; r < rw.C; ++r) {
       w_above += sh.mail.mass[r];
       w_all += sh.mail.all[r];
     }
-    *row_mass = w_all;
+    if (want_all) *row_mass = w_all;
+    else w_all = *row_mass;
   }
-  cluster.sync();
-  if (n <= 0) return false;
-  if (rank == 0) {
+  if (n <= kList) {
+    // the bracket's elements into the leader's list, in vocabulary order
+    List& list = rw.at(0)->list;
+    const int mine = sh.mail.count[rw.rank];
+    for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
+      const int from = sh.seg_n[s], to = s + 1 < rw.s1 ? sh.seg_n[s + 1] : mine;
+      if (from == to) continue;
+      int off = base + from;
+#pragma unroll 1
+      for (int i = 0; i < RD::kIters; ++i) {
+        const int at = RD::at(s, i);
+        float x[RD::N];
+        rw.rd.load(at, x);
+        unsigned take = 0;
+#pragma unroll
+        for (int e = 0; e < RD::N; ++e) {
+          const float z = rw.mass.z(x[e]);
+          const int bin = bin_of(rw.bins_below(z));
+          take |= cut.keeps(z, at + e) && bin >= lo && bin <= hi ? 1u << e : 0u;
+        }
+        if (!__any_sync(0xffffffffu, take)) continue;
+        const int c = __popc(take);
+        const int inc = warp_scan(c);
+        int q = off + inc - c;
+#pragma unroll
+        for (int e = 0; e < RD::N; ++e)
+          if ((take >> e) & 1) {
+            list.key[q] = ord_key(rw.mass.z(x[e]));
+            list.idx[q] = at + e;
+            ++q;
+          }
+        off += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+  }
+  rw.sync();
+  if (n <= 0 || n > kList) return false;
+  if (rw.rank == 0) {
     bool ok = true;
     Cut found{0.f, kMaxIdx};
+    sort_list(sh, n);
     if (MASS) {
-      auto weight = [&](int i) { return (rw.mass.of(key_value(sh.list.key[i])) + 2) >> kListDrop; };
-      uint64_t mine = 0, band;
-      for (int i = tid; i < n; i += kGivenThreads) mine += weight(i);
-      block_scan(sh, mine, &band);
       const uint64_t target = part_of(w_all, p);
       // the boundary lies in the bracket: the mass above it is within the
       // target, that at its end is not
       ok = w_above <= target && (target - w_above) < (1ull << (62 - rw.drop));
       const uint64_t left = ok ? (target - w_above) << (rw.drop - kListDrop) : 0;
+      uint64_t band;
+      found = cut_by_mass(sh, rw.mass, n, left, -1.f, &band);
       ok = ok && left < band;
-      if (ok) found = list_select<true>(sh, n, left, weight);
       if (ok)
-        for (int i = tid; i < n; i += kGivenThreads) {
+        for (int i = tid; i < n; i += kThreadsF) {
           const int j = sh.list.idx[i];
           const float z = key_value(sh.list.key[i]);
-          if (found.keeps(z, j)) {
-            const int r = j / rw.slice;
-            atomicAdd((unsigned long long*)&rw.at(r)->seg_w[(j - r * rw.slice) / kSeg],
+          if (found.keeps(z, j))
+            atomicAdd((unsigned long long*)&rw.at(j / kSeg / rw.per)->seg_w[j / kSeg],
                       (unsigned long long)rw.mass.of(z));
-          }
         }
     } else {
-      found = list_select<false>(sh, n, (uint64_t)top_k - above_n, [](int) { return 1ull; });
+      found = sorted_cut(sh, (int)(top_k - above_n) - 1);
     }
-    if (tid < C) {
+    if (tid < rw.C) {
       rw.at(tid)->mail.cut = found;
       rw.at(tid)->mail.ok = ok;
     }
   }
-  cluster.sync();
-  if (sh.mail.ok) *cut_io = sh.mail.cut;
-  return sh.mail.ok;
+  rw.sync();
+  const bool ok = sh.mail.ok;
+  if (ok) *cut_io = sh.mail.cut;
+  return ok;
 }
 
 // Masses of the kept elements by segment, into seg_w (element units).
-template <typename T, bool STAGED>
-__device__ __noinline__ void kept_mass(const Row<T, STAGED>& row_in, const Cut cut) {
-  Row<T, STAGED> rw = row_in;  // in registers
-  using SL = Slice<T, STAGED>;
-  const SL& sl = rw.sl;
+template <typename T>
+__device__ __noinline__ void kept_mass(const Row<T>& row_in, const Cut cut) {
+  Row<T> rw = row_in;  // in registers
+  using RD = RowData<T>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int s = warp; s < sl.segs(); s += kGivenWarps) {
+  const float least = fmaxf(cut.z, rw.m - 64.f);  // no mass below
+  for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
     uint64_t w = 0;
-#pragma unroll 1
-    for (int i = 0; i < SL::kIters; ++i) {
-      const int at = SL::at(s, i);
-      float x[SL::N];
-      sl.load(at, x);
+    if (rw.seg_top(s) >= least) {
+#pragma unroll 2
+      for (int i = 0; i < RD::kIters; ++i) {
+        const int at = RD::at(s, i);
+        float x[RD::N];
+        rw.rd.load(at, x);
 #pragma unroll
-      for (int e = 0; e < SL::N; ++e) {
-        const float z = rw.mass.z(x[e]);
-        const uint64_t v = rw.mass.of(z);
-        w += cut.keeps(z, sl.base + at + e) ? v : 0;
+        for (int e = 0; e < RD::N; ++e) {
+          const float z = rw.mass.z(x[e]);
+          if (cut.keeps(z, at + e)) w += rw.mass.of(z);
+        }
       }
+      w = warp_sum_u64(w);
     }
-    w = warp_sum_u64(w);
     if (lane == 0) rw.sh.seg_w[s] = w;
   }
 }
 
-// seg_w to inclusive sums in row units; returns the cluster's total, the mass of
-// the CTAs before this one and this CTA's.
-template <typename T, bool STAGED>
-__device__ uint64_t sum_segments(Row<T, STAGED>& rw, uint64_t* before, uint64_t* own) {
+// seg_w of this CTA's segments to inclusive sums in row units; returns the team's
+// total, the mass of the CTAs before this one and this CTA's.
+template <typename T>
+__device__ uint64_t sum_segments(Row<T>& rw, uint64_t* before, uint64_t* own) {
   Shared& sh = rw.sh;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, segs = rw.sl.segs();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
   if (warp == 0) {
     uint64_t carry = 0;
-    for (int s0 = 0; s0 < segs; s0 += 32) {
+    for (int b = rw.s0; b < rw.s1; b += 32) {
       const uint64_t w =
-          warp_scan(s0 + lane < segs ? rw.coarse(sh.seg_w[s0 + lane]) : (uint64_t)0) + carry;
-      if (s0 + lane < segs) sh.seg_w[s0 + lane] = w;
+          warp_scan(b + lane < rw.s1 ? rw.coarse(sh.seg_w[b + lane]) : (uint64_t)0) + carry;
+      if (b + lane < rw.s1) sh.seg_w[b + lane] = w;
       carry = __shfl_sync(0xffffffffu, w, 31);
     }
     rw.send(&Mail::kept, carry);
   }
-  cluster.sync();
+  rw.sync();
   uint64_t total = 0;
-  const int rank = cluster.block_rank();
-  for (int r = 0; r < (int)cluster.num_blocks(); ++r) {
-    if (r == rank) *before = total;
+  for (int r = 0; r < rw.C; ++r) {
+    if (r == rw.rank) *before = total;
     total += sh.mail.kept[r];
   }
-  *own = sh.mail.kept[rank];
+  *own = sh.mail.kept[rw.rank];
   return total;
 }
 
 // The first kept element of this CTA whose inclusive mass (from the CTA's start)
 // exceeds t (row units, below the CTA's mass); one warp.
-template <typename T, bool STAGED>
-__device__ int find_draw(const Row<T, STAGED>& rw, const Cut& cut, uint64_t t, float* z_out) {
-  using SL = Slice<T, STAGED>;
-  const SL& sl = rw.sl;
+template <typename T>
+__device__ int find_draw(const Row<T>& rw, const Cut& cut, uint64_t t, float* z_out) {
+  using RD = RowData<T>;
   const int lane = threadIdx.x & 31;
-  int s = 0;
-  for (int s0 = 0; s0 < sl.segs(); s0 += 32) {
-    const bool past = s0 + lane < sl.segs() && rw.sh.seg_w[s0 + lane] <= t;
-    s += __popc(__ballot_sync(0xffffffffu, past));
+  int lo = rw.s0, hi = rw.s1 - 1;  // the first segment whose inclusive mass exceeds t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (rw.sh.seg_w[mid] > t) hi = mid;
+    else lo = mid + 1;
   }
-  if (s > 0) t -= rw.sh.seg_w[s - 1];
+  if (lo > rw.s0) t -= rw.sh.seg_w[lo - 1];
   t <<= rw.drop;  // element units
   int idx = -1;
   float zz = 0.f;
-  for (int i = 0; i < SL::kIters; ++i) {
-    const int at = SL::at(s, i);
-    float x[SL::N];
-    sl.load(at, x);
-    uint64_t w[SL::N], sum = 0;
+#pragma unroll 1
+  for (int i = 0; i < RD::kIters; ++i) {
+    const int at = RD::at(lo, i);
+    float x[RD::N];
+    rw.rd.load(at, x);
+    uint64_t w[RD::N], sum = 0;
 #pragma unroll
-    for (int e = 0; e < SL::N; ++e) {
+    for (int e = 0; e < RD::N; ++e) {
       const float z = rw.mass.z(x[e]);
-      w[e] = cut.keeps(z, sl.base + at + e) ? rw.mass.of(z) : 0;
+      w[e] = cut.keeps(z, at + e) ? rw.mass.of(z) : 0;
       sum += w[e];
     }
     const uint64_t inc = warp_scan(sum);
@@ -932,10 +1049,10 @@ __device__ int find_draw(const Row<T, STAGED>& rw, const Cut& cut, uint64_t t, f
     int here = -1, last = -1;
     float z_here = 0.f, z_last = 0.f;
 #pragma unroll
-    for (int e = 0; e < SL::N; ++e) {
+    for (int e = 0; e < RD::N; ++e) {
       run += w[e];
       if (w[e] > 0) {
-        last = sl.base + at + e;
+        last = at + e;
         z_last = rw.mass.z(x[e]);
         if (here < 0 && run > t) {
           here = last;
@@ -961,37 +1078,32 @@ __device__ int find_draw(const Row<T, STAGED>& rw, const Cut& cut, uint64_t t, f
   return idx;
 }
 
-// Threads whose maximum counts as one group, for a row of C CTAs: so many groups
-// that at least twice top_k remain.  0: the row has too few threads.
-__device__ __forceinline__ int group_threads(int C, int top_k) {
-  if (top_k < 2 || top_k > kListTopK || 2 * top_k > C * kGivenThreads) return 0;
-  int g = 1;
-  while (g < 32 && C * kGivenThreads / (2 * g) >= 2 * top_k) g *= 2;
-  return g;  // at most 2 * kListTopK groups, both powers of two
+// Whether the group maxima give a top-k row's candidates: at least twice top_k
+// groups, so that the elements that reach the top_k-th maximum are not many more.
+__device__ __forceinline__ bool listable(int top_k, int V) {
+  return top_k <= kListTopK && 2 * top_k <= V / kGroup;
 }
 
-// A row with 1 < top_k <= kListTopK: the maxima of groups of elements (in
-// hist.group_max) give a value that at least top_k elements reach; those elements
-// go to the leader's list, where min-p, top-k and top-p are settled and the draws
-// made.  Adds ln sum exp on the way.  Returns false (in every CTA) when the list
-// does not hold them.
-template <typename T, bool STAGED>
-__device__ __noinline__ bool draw_from_list(const Row<T, STAGED>& row_in, const GivenArgs& a,
-                                            const RowParams& P, const Cut minp, int groups,
-                                            int row, float* ln_s_out) {
-  Row<T, STAGED> rw = row_in;  // in registers
-  using SL = Slice<T, STAGED>;
-  const SL& sl = rw.sl;
+// A listable top-k row, by one CTA: the groups that reach the top_k-th group
+// maximum hold its candidates, which go to the list; min-p, top-k and top-p are
+// settled there and the draws made.  Returns false when the list does not hold
+// them.
+template <typename T>
+__device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArgs& a,
+                                            const RowParams& P, const Cut minp, int row,
+                                            float ln_s) {
+  Row<T> rw = row_in;  // in registers
   Shared& sh = rw.sh;
-  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kPer = kBins / kGivenThreads;
+  const float* gmax = a.group_max + (int64_t)row * rw.segs * kGroupsPerSeg;
+  const int groups = rw.segs * kGroupsPerSeg;
+  constexpr int kPer = kBins / kThreadsF;
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kGivenThreads] = 0;
+  for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kThreadsF] = 0;
   if (tid == 0) sh.hi = kBins - 1;
   __syncthreads();
-  for (int i = tid; i < groups; i += kGivenThreads) {
-    const float x = sh.hist.group_max[i];
+  for (int i = tid; i < groups; i += kThreadsF) {
+    const float x = gmax[i];
     if (x > -INFINITY) atomicAdd(&sh.hist.own[bin_of(rw.bins_below(rw.mass.z(x)))], 1u);
   }
   __syncthreads();
@@ -1013,68 +1125,111 @@ __device__ __noinline__ bool draw_from_list(const Row<T, STAGED>& row_in, const 
   __syncthreads();
   // (fewer than top_k groups with a finite element: every finite element)
   const float edge = sh.hi == kBins - 1 ? INFINITY : (float)(sh.hi + 1);
-  float expsum = 0.f;
-  for (int s = warp; s < sl.segs(); s += kGivenWarps) {
+  // the groups that reach it, in order
+  int n_groups = 0;
+  constexpr int kCap = (int)(sizeof(sh.groups) / sizeof(sh.groups[0]));
+  for (int b = 0; b < groups; b += kThreadsF) {
+    const int i = b + tid;
+    const bool in = i < groups && rw.bins_below(rw.mass.z(gmax[i])) < edge;
+    const unsigned mask = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) sh.red_i[warp] = __popc(mask);
+    __syncthreads();
+    int at = n_groups, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarpsF; ++w) {
+      if (w < warp) at += sh.red_i[w];
+      all += sh.red_i[w];
+    }
+    at += __popc(mask & ((1u << lane) - 1));
+    if (in && at < kCap) sh.groups[at] = (uint16_t)i;
+    n_groups += all;
+    __syncthreads();
+  }
+  if (n_groups > kCap || n_groups > kList) return false;
+  // a warp to a group: two elements a lane, in order
+  auto pair = [&](int g, float (&x)[2]) {
+    const int p = (int)sh.groups[g] * kGroup + lane * 2;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) x[e] = p + e < rw.rd.V ? elem(rw.rd.data[p + e]) : -INFINITY;
+    return p;
+  };
+  uint16_t* before = reinterpret_cast<uint16_t*>(sh.seg_w);  // candidates of each group
+  static_assert(sizeof(sh.seg_w) >= kList * sizeof(uint16_t), "a count for every listed group");
+  for (int g = warp; g < n_groups; g += kWarpsF) {
+    float x[2];
+    pair(g, x);
     int c = 0;
 #pragma unroll
-    for (int i = 0; i < SL::kIters; ++i) {
-      float x[SL::N];
-      sl.load(SL::at(s, i), x);
-#pragma unroll
-      for (int e = 0; e < SL::N; ++e) {
-        const float t = rw.bins_below(rw.mass.z(x[e]));
-        c += t < edge;
-        expsum += ex2_approx(__fmul_rn(t, -kLog2e / kBinsPerNat));
-      }
-    }
-    c = warp_sum_i(c);
-    if (lane == 0) sh.seg_n[s] = c;
+    for (int e = 0; e < 2; ++e)
+      c += __popc(__ballot_sync(0xffffffffu, rw.bins_below(rw.mass.z(x[e])) < edge));
+    if (lane == 0) before[g] = (uint16_t)c;
   }
-  expsum = block_sum(sh, expsum);
-  const int n = gather(rw, [&](float x, int) { return rw.bins_below(rw.mass.z(x)) < edge; },
-                       [&]() { rw.send(&Mail::expsum, expsum); });
-  expsum = 0.f;
-  for (int r = 0; r < (int)cluster.num_blocks(); ++r) expsum += sh.mail.expsum[r];
-  const float ln_s = logf(expsum);
-  *ln_s_out = ln_s;
-  cluster.sync();
-  if (n < 0) return false;
-  if (cluster.block_rank() != 0) return true;
-
-  const List& list = sh.list;
-  Cut cut = minp;
+  __syncthreads();
+  uint64_t n64;
+  {
+    int c[kListPerThread];
+    uint64_t sum = 0;
+#pragma unroll
+    for (int q = 0; q < kListPerThread; ++q) {
+      const int g = tid * kListPerThread + q;
+      c[q] = g < n_groups ? before[g] : 0;
+      sum += c[q];
+    }
+    uint64_t b = block_scan(sh, sum, &n64);
+    if (n64 > (uint64_t)kList) return false;
+#pragma unroll
+    for (int q = 0; q < kListPerThread; ++q) {
+      const int g = tid * kListPerThread + q;
+      if (g < n_groups) before[g] = (uint16_t)b;
+      b += c[q];
+    }
+  }
+  const int n = (int)n64;
+  __syncthreads();
+  List& list = sh.list;
+  for (int g = warp; g < n_groups; g += kWarpsF) {
+    float x[2];
+    const int p = pair(g, x);
+    bool in[2];
+    unsigned mask[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      in[e] = rw.bins_below(rw.mass.z(x[e])) < edge;
+      mask[e] = __ballot_sync(0xffffffffu, in[e]);
+    }
+    const unsigned below = (1u << lane) - 1;
+    int at = before[g] + __popc(mask[0] & below) + __popc(mask[1] & below);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (in[e]) {
+        list.key[at] = ord_key(rw.mass.z(x[e]));
+        list.idx[at] = p + e;
+        ++at;
+      }
+  }
+  sort_list(sh, n);  // (over the groups' memory, after a barrier)
   int kept = 0;
-  for (int i = tid; i < n; i += kGivenThreads) kept += key_value(list.key[i]) >= cut.z;
-  kept = block_sum(sh, kept);
-  // (elements that min-p leaves out come after the others in the order)
-  if (kept > P.top_k)
-    cut = list_select<false>(sh, n, (uint64_t)P.top_k, [](int) { return 1ull; });
+  for (int i = tid; i < n; i += kThreadsF) kept += key_value(list.key[i]) >= minp.z;
+  kept = min(block_sum(sh, kept), P.top_k);
+  uint64_t total;
+  const Cut cut = P.flags & kRowTopP ? cut_by_mass(sh, rw.mass, kept, 0, P.top_p, &total)
+                                     : sorted_cut(sh, kept - 1);
+  // each thread holds a few neighbours of the list
   auto weight = [&](int i) -> uint64_t {
     if (i >= n) return 0;
     const float z = key_value(list.key[i]);
     return cut.keeps(z, list.idx[i]) ? (rw.mass.of(z) + 2) >> kListDrop : 0;
   };
-  // each thread holds a few neighbours of the list
-  auto own = [&]() {
-    uint64_t sum = 0;
+  uint64_t mine = 0;
 #pragma unroll
-    for (int q = 0; q < kListPerThread; ++q) sum += weight(tid * kListPerThread + q);
-    return sum;
-  };
-  uint64_t total, mine = own();
-  uint64_t ahead = block_scan(sh, mine, &total);
-  if (P.flags & kRowTopP) {
-    const Cut next = list_select<true>(sh, n, part_of(total, P.top_p), weight);
-    cut = next;
-    mine = own();
-    ahead = block_scan(sh, mine, &total);
-  }
+  for (int q = 0; q < kListPerThread; ++q) mine += weight(tid * kListPerThread + q);
+  const uint64_t ahead = block_scan(sh, mine, &total);
   sh.run[tid] = ahead + mine;
   __syncthreads();
-  for (int d = tid; d < a.draws; d += kGivenThreads) {
+  for (int d = tid; d < a.draws; d += kThreadsF) {
     const int64_t o = (int64_t)row * a.draws + d;
     const uint64_t t = part_of(total, a.uniforms[o]);
-    int lo = 0, hi = kGivenThreads - 1;  // the first thread whose inclusive mass exceeds t
+    int lo = 0, hi = kThreadsF - 1;  // the first thread whose inclusive mass exceeds t
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (sh.run[mid] > t) hi = mid;
@@ -1090,105 +1245,118 @@ __device__ __noinline__ bool draw_from_list(const Row<T, STAGED>& row_in, const 
   return true;
 }
 
-template <typename T, bool STAGED>
-__global__ void __launch_bounds__(kGivenThreads, 2) given_kernel(GivenArgs a) {
-  using SL = Slice<T, STAGED>;
+template <typename T>
+__global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
+  using RD = RowData<T>;
   extern __shared__ __align__(128) unsigned char dyn[];
   Shared& sh = *reinterpret_cast<Shared*>(dyn);
-  T* stage = reinterpret_cast<T*>(dyn + ((sizeof(Shared) + 127) / 128) * 128);
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int C = cluster.num_blocks(), rank = cluster.block_rank();
-  const int row = blockIdx.x / C;
+  const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
+  const int row = blockIdx.x / ctas;
   const RowParams P = a.params[row];
-  const T* src = static_cast<const T*>(a.logits) + (int64_t)row * a.ld + (int64_t)rank * a.slice;
-  SL sl;
-  sl.base = rank * a.slice;
-  sl.n = min(a.slice, a.V - sl.base);
-  sl.vec = a.aligned;
-  sl.data = STAGED ? stage : src;
-  if (tid < 128) sh.table[tid] = c_mass_table.v[tid];
-
-  // the row's maximum; with STAGED, taken as the slice arrives
-  float mx = -INFINITY;
-  const int n_pad = sl.segs() * kSeg;
-  if (STAGED) {
-    const int chunk = (((n_pad / kLoadChunks) + kSeg - 1) / kSeg) * kSeg;
-    const int n_bulk = a.aligned && sl.n > 0 ? sl.n / SL::N * SL::N : 0;
-    if (tid < kLoadChunks) mbar_init(&sh.bars[tid], 1);
-    fence_mbar_init();
-    __syncthreads();
-    if (tid == 0 && n_bulk > 0) {
-      for (int c = 0; c * chunk < n_bulk; ++c) {
-        const uint32_t bytes = (uint32_t)min(chunk, n_bulk - c * chunk) * sizeof(T);
-        mbar_arrive_expect_tx(&sh.bars[c], bytes);
-        bulk_copy_g2s(stage + c * chunk, src + c * chunk, bytes, &sh.bars[c]);
-      }
-    }
-    const T none = static_cast<T>(-INFINITY);
-    for (int i = n_bulk + tid; i < n_pad; i += kGivenThreads) stage[i] = i < sl.n ? src[i] : none;
-    __syncthreads();
-    for (int c = 0; c * chunk < n_pad; ++c) {
-      if (c * chunk < n_bulk && !mbar_wait_bounded(&sh.bars[c], 0))
-        atomicOr(a.err_word, kErrTimeout);
-      const int end = min(n_pad, (c + 1) * chunk);
-      for (int at = c * chunk + tid * SL::N; at < end; at += kGivenThreads * SL::N) {
-        float x[SL::N];
-        sl.load(at, x);
-#pragma unroll
-        for (int e = 0; e < SL::N; ++e) mx = max_nan(mx, x[e]);
-      }
-    }
-  } else {
-    for (int at = tid * SL::N; at < sl.n; at += kGivenThreads * SL::N) {
-      float x[SL::N];
-      sl.load(at, x);
-#pragma unroll
-      for (int e = 0; e < SL::N; ++e) mx = max_nan(mx, x[e]);
-    }
-  }
-  // the maximum to every CTA, and for a top-k row the maxima of groups of threads
   const bool greedy = P.flags & kRowGreedy;
   const bool topk = !greedy && P.top_k > 1 && P.top_k < a.V;
-  const int group = topk ? group_threads(C, P.top_k) : 0;
-  float gmax = mx;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    if (o < group) gmax = max_nan(gmax, __shfl_xor_sync(0xffffffffu, gmax, o));
-    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const bool from_list = topk && listable(P.top_k, a.V);
+  // rows that may read all their elements again are finished by the whole cluster
+  const bool team = ctas > 1 && !greedy && !from_list &&
+                    (topk || (P.flags & (kRowTopP | kRowMinP)));
+  if (rank > 0 && !team) return;
+  if (tid < 128) sh.table[tid] = c_mass_table.v[tid];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // the row's maximum
+  const float* seg_max = a.seg_max + (int64_t)row * a.segs;
+  const uint64_t* seg_sum = a.seg_sum + (int64_t)row * a.segs;
+  float mx = -INFINITY;
+  for (int s = tid; s < a.segs; s += kThreadsF) {
+    const float v = seg_max[s];
+    sh.seg_max[s] = v;
+    mx = max_nan(mx, v);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   if (lane == 0) sh.red_f[warp] = mx;
-  cluster.sync();  // every CTA of the cluster runs before its memory is written
-  if (group && (tid & (group - 1)) == 0)
-    for (int r = 0; r < C; ++r)
-      cluster.map_shared_rank(&sh, r)->hist.group_max[rank * (kGivenThreads / group) + tid / group] =
-          gmax;
-  if (tid < C) {
-    mx = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kGivenWarps; ++i) mx = max_nan(mx, sh.red_f[i]);
-    cluster.map_shared_rank(&sh, tid)->mail.max[rank] = mx;
-  }
-  cluster.sync();
+  if (team) cluster.sync();  // every CTA of the team runs before its memory is written
+  else __syncthreads();
   mx = -INFINITY;
-  for (int r = 0; r < C; ++r) mx = max_nan(mx, sh.mail.max[r]);
+#pragma unroll
+  for (int i = 0; i < kWarpsF; ++i) mx = max_nan(mx, sh.red_f[i]);
   const float m = __fmul_rn(mx, P.inv_t);
   const int status = isnan(mx) || m == INFINITY ? kRowNonfinite : m == -INFINITY ? kRowEmpty : kRowOk;
-  if (rank == 0 && tid == 0) a.row_status[row] = status;
   int32_t* out_tok = a.out_tokens + (int64_t)row * a.draws;
   float* out_lp = a.out_logprobs ? a.out_logprobs + (int64_t)row * a.draws : nullptr;
+  if (rank == 0 && tid == 0) a.row_status[row] = status;
   if (status != kRowOk) {
-    for (int d = rank * kGivenThreads + tid; d < a.draws; d += C * kGivenThreads) {
-      out_tok[d] = -1;
-      if (out_lp) out_lp[d] = NAN;
-    }
+    if (rank == 0)
+      for (int d = tid; d < a.draws; d += kThreadsF) {
+        out_tok[d] = -1;
+        if (out_lp) out_lp[d] = NAN;
+      }
     return;
   }
   const Mass mass(P.inv_t, m, sh.table);
-  Row<T, STAGED> rw(sl, sh, mass, m, a.slice, a.drop);
+  const RowData<T> rd{static_cast<const T*>(a.logits) + row * a.ld, a.V, a.aligned != 0};
+  Row<T> rw(rd, sh, mass, m, a.segs, a.drop, team ? ctas : 1, team ? rank : 0);
 
+  // ln sum exp(z - m) from the segments' sums; masses to element units of the row
+  float ln_s = 0.f;
+  const bool masses = sums_masses(P, a.V);
+  const bool usable = masses && fabsf(m) < kWide;
+  uint64_t all = 0;  // mass of every element, row units (0: not known)
+  if (usable) {
+    for (int s = tid; s < a.segs; s += kThreadsF) {
+      const float zm = mass.z(sh.seg_max[s]);
+      uint64_t w = 0;
+      if (zm > -INFINITY) {
+        const int sh_r = (mass.e128 - Mass(P.inv_t, zm, sh.table).e128) >> 7;
+        w = fabsf(zm) < 8192.f && sh_r < 64 ? seg_sum[s] >> sh_r : 0;
+      }
+      sh.seg_w[s] = w;
+      all += rw.coarse(w);
+    }
+    block_scan(sh, all, &all);
+    ln_s = mass.ln_sum(all, kElemBits - a.drop, m);
+  } else if (out_lp && !masses) {
+    float e = 0.f;
+    for (int s = tid; s < a.segs; s += kThreadsF) {
+      const float zm = mass.z(sh.seg_max[s]);
+      if (zm > -INFINITY)
+        e += __uint_as_float((uint32_t)seg_sum[s]) *
+             ex2_approx(__fmul_rn(__fsub_rn(zm, m), kLog2e));
+    }
+    ln_s = logf(block_sum(sh, e));
+  }
+
+  if (greedy) {
+    // the lowest index at the maximum: the first segment that has it
+    int first = kMaxIdx;
+    for (int s = tid; s < a.segs; s += kThreadsF)
+      if (sh.seg_max[s] == mx) first = min(first, s);
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) sh.red_i[warp] = first;
+    __syncthreads();
+    for (int i = 0; i < kWarpsF; ++i) first = min(first, sh.red_i[i]);
+    int j = kMaxIdx;
+#pragma unroll 1
+    for (int i = 0; i < RD::kIters; ++i) {
+      float x[RD::N];
+      rd.load(RD::at(first, i), x);
+#pragma unroll
+      for (int e = RD::N - 1; e >= 0; --e)
+        if (x[e] == mx) j = min(j, RD::at(first, i) + e);
+    }
+    j = __reduce_min_sync(0xffffffffu, j);
+    for (int d = tid; d < a.draws; d += kThreadsF) {
+      out_tok[d] = j;
+      if (out_lp) out_lp[d] = -ln_s;
+    }
+    return;
+  }
+
+  // the kept set
   Cut cut{-3.402823466e38f, kMaxIdx};
-  if ((P.flags & kRowMinP) && !(P.flags & kRowGreedy)) {
+  if (P.flags & kRowMinP) {
     // the smallest z with z - m >= ln(min_p), both sides in double
     float zt = __double2float_rn((double)m + P.log_min_p);
     if ((double)zt - (double)m < P.log_min_p) {
@@ -1199,98 +1367,47 @@ __global__ void __launch_bounds__(kGivenThreads, 2) given_kernel(GivenArgs a) {
     }
     cut.z = fmaxf(cut.z, zt);
   }
-  float ln_s = 0.f;
-  bool have_ln_s = false;
-  if (group) {
-    if (draw_from_list(rw, a, P, cut, C * kGivenThreads / group, row, &ln_s)) return;
-    have_ln_s = true;
-  }
-
-  // ln sum exp(z - m) where the masses will not give it; a greedy row's lowest
-  // index at the maximum
-  const bool all_mass = !greedy && !topk && !(P.flags & kRowMinP);
-  if (greedy || (out_lp && !have_ln_s && !all_mass)) {
-    float expsum = 0.f;
-    int first = kMaxIdx;
-    for (int s = warp; s < sl.segs(); s += kGivenWarps) {
-#pragma unroll
-      for (int i = 0; i < SL::kIters; ++i) {
-        const int at = SL::at(s, i);
-        float x[SL::N];
-        sl.load(at, x);
-#pragma unroll
-        for (int e = 0; e < SL::N; ++e) {
-          expsum += ex2_approx(__fmul_rn(__fsub_rn(rw.mass.z(x[e]), m), kLog2e));
-          if (greedy && x[e] == mx) first = min(first, sl.base + at + e);
-        }
-      }
-    }
-    expsum = block_sum(sh, expsum);
-    rw.send(&Mail::expsum, expsum);
-    if (greedy) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
-      if (lane == 0) sh.red_i[warp] = first;
-      __syncthreads();
-      if (tid < C)
-        for (int i = 0; i < kGivenWarps; ++i) first = min(first, sh.red_i[i]);
-      rw.send(&Mail::index, first);
-    }
-    cluster.sync();
-    expsum = 0.f;
-    first = kMaxIdx;
-    for (int r = 0; r < C; ++r) {
-      expsum += sh.mail.expsum[r];
-      if (greedy) first = min(first, sh.mail.index[r]);
-    }
-    ln_s = logf(expsum);
-    if (greedy) {
-      for (int d = rank * kGivenThreads + tid; d < a.draws; d += C * kGivenThreads) {
-        out_tok[d] = first;
-        if (out_lp) out_lp[d] = -ln_s;
-      }
-      return;
-    }
-  }
-
-  // the kept set
+  if (from_list && draw_from_list(rw, a, P, cut, row, ln_s)) return;
   if (topk) {
     // (an element count decides whether top-k cuts anything)
     int c = 0;
-    for (int s = warp; s < sl.segs(); s += kGivenWarps) {
+    for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
+      if (rw.seg_top(s) < cut.z) continue;
 #pragma unroll 1
-      for (int i = 0; i < SL::kIters; ++i) {
-        float x[SL::N];
-        sl.load(SL::at(s, i), x);
+      for (int i = 0; i < RD::kIters; ++i) {
+        float x[RD::N];
+        rd.load(RD::at(s, i), x);
 #pragma unroll
-        for (int e = 0; e < SL::N; ++e) c += rw.mass.z(x[e]) >= cut.z;
+        for (int e = 0; e < RD::N; ++e) c += rw.mass.z(x[e]) >= cut.z;
       }
     }
     rw.send(&Mail::total, block_sum(sh, c));
-    cluster.sync();
+    rw.sync();
     int n = 0;
-    for (int r = 0; r < C; ++r) n += sh.mail.total[r];
-    if (n > P.top_k && !band_select<T, STAGED, false>(rw, &cut, 0.f, P.top_k, nullptr))
-      cut = radix_select<T, STAGED, false>(rw, cut, (uint64_t)P.top_k);
+    for (int r = 0; r < rw.C; ++r) n += sh.mail.total[r];
+    if (n > P.top_k && !band_select<T, false>(rw, &cut, 0.f, P.top_k, nullptr))
+      cut = radix_select<T, false>(rw, cut, (uint64_t)P.top_k);
   }
-  uint64_t before, mine, W, all;
+  uint64_t before, mine, W;
   if (P.flags & kRowTopP) {
     const Cut from = cut;
-    if (!band_select<T, STAGED, true>(rw, &cut, P.top_p, 0, &all)) {
+    uint64_t row_mass = all;
+    if (!band_select<T, true>(rw, &cut, P.top_p, 0, &row_mass)) {
       kept_mass(rw, from);
-      all = sum_segments(rw, &before, &mine);
-      cut = radix_select<T, STAGED, true>(rw, from, part_of(all, P.top_p));
+      row_mass = sum_segments(rw, &before, &mine);
+      cut = radix_select<T, true>(rw, from, part_of(row_mass, P.top_p));
       kept_mass(rw, cut);
     }
+    if (masses && !usable) ln_s = mass.ln_sum(row_mass, kElemBits - a.drop, m);
     W = sum_segments(rw, &before, &mine);
   } else {
-    kept_mass(rw, cut);
-    W = all = sum_segments(rw, &before, &mine);
+    if (!usable) kept_mass(rw, cut);
+    W = sum_segments(rw, &before, &mine);
+    if (masses && !usable) ln_s = mass.ln_sum(W, kElemBits - a.drop, m);
   }
-  if (all_mass) ln_s = rw.mass.ln_sum(all, kElemBits - a.drop, m);
 
   // the draws: each by a warp of the CTA that holds its mass
-  for (int d = warp; d < a.draws; d += kGivenWarps) {
+  for (int d = warp; d < a.draws; d += kWarpsF) {
     const uint64_t t = part_of(W, a.uniforms[(int64_t)row * a.draws + d]);
     if (t < before || t - before >= mine) continue;
     float z;
@@ -1302,54 +1419,46 @@ __global__ void __launch_bounds__(kGivenThreads, 2) given_kernel(GivenArgs a) {
   }
 }
 
-template <typename T, bool STAGED>
-cudaError_t launch_given_typed(const GivenArgs& a, int cluster, size_t smem, cudaStream_t stream) {
-  auto* kernel = given_kernel<T, STAGED>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess && cluster > 8)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+template <typename T>
+cudaError_t launch_given_typed(const GivenArgs& a, int num_sms, int ctas, cudaStream_t stream) {
+  const int64_t warps = (int64_t)a.B * a.segs;
+  const int per_sm = sizeof(T) == 2 ? 5 : 4;  // as in its launch bounds
+  int64_t grid = (warps + kStreamThreads / 32 - 1) / (kStreamThreads / 32);
+  if (grid > (int64_t)per_sm * num_sms) grid = (int64_t)per_sm * num_sms;
+  stream_kernel<T><<<(unsigned)grid, kStreamThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(finish_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)sizeof(Shared));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.B * cluster));
-  cfg.blockDim = dim3(kGivenThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3((unsigned)(a.B * ctas));
+  cfg.blockDim = dim3(kThreadsF);
+  cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  // its prologue overlaps the end of stream_kernel (griddepcontrol.wait)
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, finish_kernel<T>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t stream) {
-  const int es = dtype == VT_DTYPE_F32 ? 4 : 2;
-  // slices small enough for two CTAs on an SM, and for few rows enough CTAs to
-  // fill the GPU
-  int cluster = 1;
-  auto slice_of = [&](int c) { return ((a.V + c - 1) / c + kSeg - 1) / kSeg * kSeg; };
-  while (cluster < kMaxCtas && ((int64_t)slice_of(cluster) * es > 80 * 1024 ||
-                                slice_of(cluster) > kSeg * kMaxSegs ||
-                                ((int64_t)a.B * cluster * 2 <= 2 * num_sms &&
-                                 slice_of(cluster) > 4096)))
-    cluster *= 2;
-  a.slice = slice_of(cluster);
+  a.segs = (a.V + kSeg - 1) / kSeg;
   // sums of V masses stay below 2^62
   int bits = 0;
   while ((1ll << bits) < a.V) ++bits;
   a.drop = max(kListDrop, bits + kElemBits - 62);
-  const size_t head = (sizeof(Shared) + 127) / 128 * 128;
-  const size_t staged = head + (size_t)a.slice * es;
-  const bool fits = staged <= 227 * 1024 - 1024;
-  if (dtype == VT_DTYPE_F32)
-    return fits ? launch_given_typed<float, true>(a, cluster, staged, stream)
-                : launch_given_typed<float, false>(a, cluster, head, stream);
-  return fits ? launch_given_typed<__nv_bfloat16, true>(a, cluster, staged, stream)
-              : launch_given_typed<__nv_bfloat16, false>(a, cluster, head, stream);
+  const int ctas = a.B <= 38 ? 8 : 4;
+  return dtype == VT_DTYPE_F32 ? launch_given_typed<float>(a, num_sms, ctas, stream)
+                               : launch_given_typed<__nv_bfloat16>(a, num_sms, ctas, stream);
 }
 
 }  // namespace vt

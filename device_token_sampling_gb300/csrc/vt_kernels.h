@@ -243,6 +243,9 @@ void plan_probs(int B, int V, int num_sms, int* splits, int* range);
 cudaError_t launch_probs(const ProbsArgs& args, int dtype, cudaStream_t stream);
 
 // ---- draws from given uniform numbers (vt_given.cu) --------------------------
+constexpr int kGivenSeg = 1024;   // logits of a segment
+constexpr int kGivenGroup = 64;   // logits of a group
+
 struct GivenArgs {
   const void* logits;        // [B][ld]
   int64_t ld;
@@ -254,8 +257,12 @@ struct GivenArgs {
   int32_t* out_tokens;       // [B][draws]
   float* out_logprobs;       // [B][draws] or null
   int32_t* row_status;       // [B]
-  int32_t* err_word;
-  int32_t slice, drop;       // filled by launch_given
+  // scratch, of the rows' segments: [B][segs] maxima and sums, [B][segs * 16]
+  // group maxima
+  float* seg_max;
+  uint64_t* seg_sum;
+  float* group_max;
+  int32_t segs, drop;        // filled by launch_given
 };
 cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t stream);
 

@@ -50,6 +50,11 @@ struct vt_sampler {
   size_t flat_bytes = 0;
   float2* d_probs_part = nullptr;  // (max, exp-sum) partials of the filtered distribution
   size_t probs_part_cap = 0;
+  // scratch of vt_sample_given: sums and maxima of the rows' segments, maxima of
+  // their groups
+  uint64_t* d_given_sum = nullptr;
+  float* d_given_max = nullptr;
+  float* d_given_gmax = nullptr;
   // the side stream: rows routed straight to the selection kernel run there,
   // beside the main stream's launches (fork and join through events)
   cudaStream_t side = nullptr;
@@ -177,6 +182,9 @@ void free_all(vt_sampler* h) {
   dfree(h->d_rows);
   dfree(h->d_flat);
   dfree(h->d_probs_part);
+  dfree(h->d_given_sum);
+  dfree(h->d_given_max);
+  dfree(h->d_given_gmax);
   if (h->h_rows) cudaFreeHost(h->h_rows);
   if (h->ev_fork) cudaEventDestroy(h->ev_fork);
   if (h->ev_join) cudaEventDestroy(h->ev_join);
@@ -291,6 +299,10 @@ int vt_sampler_create(const vt_sampler_config* cfg, vt_sampler** out) {
                                        vt::kProbsMaxRange + 1) +
                       (size_t)vt::kProbsCtasPerSm * h->num_sms;
   dal((void**)&h->d_probs_part, h->probs_part_cap * sizeof(float2));
+  const size_t segs = (size_t)(cfg->max_vocab + vt::kGivenSeg - 1) / vt::kGivenSeg;
+  dal((void**)&h->d_given_sum, B * segs * sizeof(uint64_t));
+  dal((void**)&h->d_given_max, B * segs * sizeof(float));
+  dal((void**)&h->d_given_gmax, B * segs * (vt::kGivenSeg / vt::kGivenGroup) * sizeof(float));
   hal((void**)&h->h_rows, B * sizeof(int32_t));
   hal((void**)&h->h_params, B * sizeof(vt::RowParams));
   hal((void**)&h->h_seeds, B * sizeof(uint64_t));
@@ -1103,7 +1115,9 @@ int vt_sample_given(vt_sampler* h, const void* logits, int32_t dtype, int32_t B,
   a.out_tokens = out_tokens;
   a.out_logprobs = out_logprobs;
   a.row_status = h->d_status;
-  a.err_word = h->d_err;
+  a.seg_sum = h->d_given_sum;
+  a.seg_max = h->d_given_max;
+  a.group_max = h->d_given_gmax;
   cudaStream_t st = (cudaStream_t)stream;
   VT_CK(h, vt::launch_given(a, dtype, h->num_sms, st));
   h->last_B = B;
