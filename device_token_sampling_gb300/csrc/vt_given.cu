@@ -8,8 +8,8 @@
 //
 // Tokens are whole numbers decided by comparing sums of up to 2^20 masses, so
 // masses are integers (struct Mass): their sums are exact and the same in any
-// order, and a mass is within 6e-10 (rms 2e-10) of exp() in relative terms.  A
-// prefix of N such errors moves a boundary by about 2e-10 / sqrt(N) of W (N the
+// order, and a mass is within 1.2e-9 (rms 4e-10) of exp() in relative terms.  A
+// prefix of N such errors moves a boundary by about 4e-10 / sqrt(N) of W (N the
 // distinct values among bf16 logits), which puts the chance of a draw differing
 // from the exact one below 1e-5 even for a flat row.
 //
@@ -39,77 +39,102 @@ constexpr int kSeg = kGivenSeg;     // elements a warp takes at a time, in vocab
 constexpr int kGroup = kGivenGroup; // elements that share a group maximum
 constexpr int kGroupsPerSeg = kSeg / kGroup;
 constexpr int kMaxSegs = 1024;      // of a row: V <= 2^20
-constexpr int kMaxCtas = 8;         // CTAs that finish a row
+constexpr int kMaxCtas = 16;        // CTAs that finish a row
 constexpr int kBins = 2048;
 constexpr float kBinsPerNat = 64.f;  // linear bins: 32 nats below the maximum, then one for all
 constexpr int kList = 2048;         // candidates a row's leader CTA holds
 constexpr int kListTopK = 1024;     // largest top-k taken from group maxima
 constexpr int kListPerThread = kList / kThreadsF;
 constexpr int kMaxIdx = 0x7fffffff;
-constexpr float kWide = 8000.f;     // maxima beyond: segment sums are not used
+constexpr float kNarrow = 5000.f;   // maxima beyond: masses relative to the maximum itself
+constexpr float kUsable = 4900.f;   // maxima beyond: the segments' sums are not used
 
-// 2^(i/128) in units of 2^-30, from powers of 2^(1/128).
+constexpr int kTable = 512, kTableLog = 9;
+constexpr int kElemBits = 53;   // masses of single elements: units of 2^-53 of 2^E
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: x + kMagic holds rint(x) in its low bits
+constexpr float kMagic512 = 24576.f;  // 1.5 * 2^14: x + kMagic512 holds rint(512 x)
+constexpr uint32_t kMagicBits = 0x4b400000u, kMagic512Bits = 0x46c00000u;
+
+// 2^(i/512) in units of 2^-30, from powers of 2^(1/512): as an integer less
+// kMagicBits, and as a float.
 struct MassTable {
-  uint32_t v[128];
+  uint2 v[kTable];
   constexpr MassTable() : v() {
     double x = 1073741824.0;
-    for (int i = 0; i < 128; ++i) {
-      v[i] = (uint32_t)(x + 0.5);
-      x *= 1.0054299011128028;
+    for (int i = 0; i < kTable; ++i) {
+      v[i].x = (uint32_t)(x + 0.5) - kMagicBits;
+      v[i].y = float_bits(x);
+      x *= 1.0013547198921082;
     }
+  }
+  // the bits of the float next to x, 2^30 <= x < 2^31
+  static constexpr uint32_t float_bits(double x) {
+    return ((127u + 30u) << 23) + (uint32_t)((x - 1073741824.0) / 128.0 + 0.5);
   }
 };
 __constant__ MassTable c_mass_table = MassTable();
 
-constexpr int kElemBits = 53;  // masses of single elements: units of 2^-53 of 2^E
+// x >> n, 0 from 32 on.
+__device__ __forceinline__ uint32_t shr(uint32_t x, int n) {
+  uint32_t r;
+  asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(n));
+  return r;
+}
 
 // Masses as integers: exp(z) = 2^(z log2(e)) relative to 2^E, the power of two
 // next above the maximum, so that no subtraction of the maximum rounds.
-//   p + e = z log2(e) with an error below 2^-40; k = the multiple of 1/128 next
-//   to p, r = p - k + e in [-1/256, 1/256]: the mass is 2^floor(k) *
-//   table[128 frac(k)] * 2^r, and 2^r - 1 is a cubic within 2^-38 whose fp32
-//   evaluation is off by 2^-33.
-// About 25 instructions, no division, one conversion and one shared load.  For a
-// maximum beyond 2^13 the reduction would run out of bits; there z - m is
-// exact wherever the mass is not 0 (z within a factor 2 of m), so the row's
-// values are shifted by c = m (else c = 0).
+//   k = the multiple of 1/512 next to z log2(e), r = z log2(e) - k in [-1/1024,
+//   1/1024] by two FMAs (exact to 2^-34): the mass is 2^floor(k) *
+//   table[512 frac(k)] * 2^r, with 2^r - 1 as a quadratic (within 2^-34), the
+//   mantissa an integer in units of 2^-30.
+// 24 instructions: roundings to integers go by the two magic numbers, not by
+// conversions (an eighth of the rate), the mantissa by an FMA, not by an integer
+// product.  For a maximum beyond 5000 the reduction would run out of bits;
+// there z - m is exact wherever the mass is not 0 (z within a factor 2 of m), so
+// the row's values are shifted by c = m (else c = 0).
 struct Mass {
-  float inv_t, c, floor_p;
-  int e128;  // 128 * E
-  const uint32_t* table;
+  float inv_t, c, floor_z;
+  uint32_t e_bits;  // kMagic512Bits + kTable * E + kTable - 1
+  const uint2* table;
 
-  __device__ __forceinline__ Mass(float inv_t_, float m, const uint32_t* table_) {
+  __device__ __forceinline__ Mass(float inv_t_, float m, const uint2* table_) {
     inv_t = inv_t_;
     table = table_;
-    c = fabsf(m) < 8192.f ? 0.f : m;
+    c = fabsf(m) < kNarrow ? 0.f : m;
     const int E = (int)floorf(__fmul_rn(m - c, kLog2e)) + 1;
-    e128 = E * 128;
-    floor_p = (float)(E - 62);
+    e_bits = kMagic512Bits + (uint32_t)(E * kTable + kTable - 1);
+    floor_z = (float)(E - 56) * kLn2;  // shifted out whole: -inf and far below have mass 0
+  }
+  __device__ __forceinline__ int E() const {
+    return ((int)(e_bits - kMagic512Bits) - (kTable - 1)) >> kTableLog;
   }
   __device__ __forceinline__ float z(float x) const { return __fmul_rn(x, inv_t); }
-  // mass of the tempered value z in units of 2^(E - kElemBits), truncated
-  __device__ __forceinline__ uint64_t of(float z) const {
-    z = __fsub_rn(z, c);
-    const float p = fmaxf(__fmul_rn(z, kLog2e), floor_p);  // -inf and far below: mass 0
-    const float e = __fmaf_rn(z, 1.92596303e-8f, __fmaf_rn(z, kLog2e, -p));
-    const float magic = 12582912.f;  // 1.5 * 2^23: the integer next to 128 p in the low bits
-    const float kb = __fmaf_rn(p, 128.f, magic);
-    const int k = __float_as_int(kb) - __float_as_int(magic);
-    const float r = __fadd_rn(__fmaf_rn(__fsub_rn(kb, magic), -0.0078125f, p), e);
-    const float q = __fmul_rn(r, __fmaf_rn(r, __fmaf_rn(r, 238388332.f, 1031764991.f),
-                                           2977044472.f));  // (2^r - 1) 2^32
-    const int sh = 62 - kElemBits + ((e128 - k + 127) >> 7);
-    const int64_t t = (int64_t)table[k & 127];
-    const int64_t mant = (t << 32) + t * (int64_t)__float2int_rn(q);
-    return p == floor_p ? 0ull : (uint64_t)mant >> sh;
+  // mass of the tempered value z, truncated to units of 2^(E - kElemBits), added to acc
+  __device__ __forceinline__ uint64_t add(uint64_t acc, float z) const {
+    z = fmaxf(__fsub_rn(z, c), floor_z);
+    const float kb = __fmaf_rn(z, kLog2e, kMagic512);
+    float r = __fmaf_rn(z, kLog2e, -__fsub_rn(kb, kMagic512));
+    r = __fmaf_rn(z, 1.92596303e-8f, r);  // log2(e) - fl(log2(e))
+    const float q = __fmul_rn(r, __fmaf_rn(r, 0.240226507f, 0.693147181f));
+    const uint32_t k = __float_as_uint(kb);
+    const uint2 t = *reinterpret_cast<const uint2*>(reinterpret_cast<const char*>(table) +
+                                                    ((k << 3) & ((kTable - 1) << 3)));
+    const uint32_t mant = t.x + __float_as_uint(__fmaf_rn(q, __uint_as_float(t.y), kMagic));
+    // mant 2^(kElemBits - 30 - n), n = E - floor(k) >= 0
+    const int n = (int)(e_bits - k) >> kTableLog;
+    constexpr int kUp = kElemBits - 30;
+    const uint32_t lo = shr(mant, max(n - kUp, 0));
+    const uint32_t up = max(shr(1u << kUp, n), 1u);
+    return acc + (uint64_t)lo * up;
   }
+  __device__ __forceinline__ uint64_t of(float z) const { return add(0, z); }
   // ln of a sum of masses in units of 2^(E - bits), relative to the maximum m
   __device__ __forceinline__ float ln_sum(uint64_t w, int bits, float m) const {
-    const float E = (float)(e128 >> 7);
+    const float e = (float)E();
     const float lw = logf(__ull2float_rn(w) * exp2f((float)-bits));
     // E ln 2 - (m - c) in one rounding, ln 2 in two parts
-    return lw + (__fmaf_rn(E, 0.693147182464599609375f, -__fsub_rn(m, c)) +
-                 E * -1.904654299957e-9f);
+    return lw + (__fmaf_rn(e, 0.693147182464599609375f, -__fsub_rn(m, c)) +
+                 e * -1.904654299957e-9f);
   }
 };
 
@@ -134,11 +159,26 @@ struct Cut {
   }
 };
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float max(const uint4& v) {
+    const uint32_t u = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return max_nan(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
   static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -151,6 +191,10 @@ struct Vec<__nv_bfloat16> {
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
+  static __device__ __forceinline__ float max(const uint4& v) {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                   max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
   static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x);
     x[1] = __uint_as_float(v.y);
@@ -165,11 +209,6 @@ __device__ __forceinline__ float elem(__nv_bfloat16 x) { return __bfloat162float
 template <>
 __device__ __forceinline__ float elem(float x) { return x; }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 // Inclusive sums over a warp.
 template <typename U>
@@ -206,6 +245,36 @@ struct RowData {
   __device__ __forceinline__ void load(int p, float (&x)[N]) const { Vec<T>::unpack(raw(p), x); }
 };
 
+// f(x, p) on the N elements from p on of every lane, over segment s in order.
+// Four loads are in flight; the body is there once, whatever the element type,
+// because the first pass of a row through long unrolled code is bound by
+// instruction fetches.
+template <typename T, typename F>
+__device__ __forceinline__ void each_vector(const RowData<T>& rd, int s, F f) {
+  using RD = RowData<T>;
+#pragma unroll 1
+  for (int h = 0; h < RD::kIters; h += 4) {
+    uint4 v0 = rd.raw(RD::at(s, h)), v1 = rd.raw(RD::at(s, h + 1)), v2 = rd.raw(RD::at(s, h + 2)),
+          v3 = rd.raw(RD::at(s, h + 3));
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      float x[RD::N];
+      Vec<T>::unpack(v0, x);
+      v0 = v1;
+      v1 = v2;
+      v2 = v3;
+      f(x, RD::at(s, h + i));
+    }
+  }
+}
+
+// Exponentials for the log-probs are 2^(z log2(e) - lse_base(max)): one FMA, with
+// the values of a far maximum shifted by it first, as in struct Mass.
+__device__ __forceinline__ float lse_shift(float zm) { return fabsf(zm) < kNarrow ? 0.f : zm; }
+__device__ __forceinline__ float lse_base(float zm) {
+  return __fmul_rn(zm - lse_shift(zm), kLog2e);
+}
+
 // Whether a row's segments are summed as masses (else as exponentials for the
 // log-probs): rows whose kept mass, or top-p total, is that of every element.
 __device__ __forceinline__ bool sums_masses(const RowParams& P, int V) {
@@ -219,8 +288,8 @@ template <typename T>
 __global__ void __launch_bounds__(kStreamThreads, sizeof(T) == 2 ? 5 : 4)
     stream_kernel(GivenArgs a) {
   using RD = RowData<T>;
-  __shared__ uint32_t table[128];
-  if (threadIdx.x < 128) table[threadIdx.x] = c_mass_table.v[threadIdx.x];
+  __shared__ uint2 table[kTable];
+  for (int i = threadIdx.x; i < kTable; i += kStreamThreads) table[i] = c_mass_table.v[i];
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31;
@@ -238,11 +307,7 @@ __global__ void __launch_bounds__(kStreamThreads, sizeof(T) == 2 ? 5 : 4)
     float* gmax = a.group_max + ((int64_t)row * a.segs + seg) * kGroupsPerSeg;
 #pragma unroll
     for (int i = 0; i < RD::kIters; ++i) {
-      float x[RD::N];
-      Vec<T>::unpack(v[i], x);
-      float g = x[0];
-#pragma unroll
-      for (int e = 1; e < RD::N; ++e) g = max_nan(g, x[e]);
+      float g = Vec<T>::max(v[i]);
 #pragma unroll
       for (int o = 1; o < kLanes; o <<= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, o));
       if (lane % kLanes == 0) gmax[i * (32 / kLanes) + lane / kLanes] = g;
@@ -260,18 +325,19 @@ __global__ void __launch_bounds__(kStreamThreads, sizeof(T) == 2 ? 5 : 4)
           float x[RD::N];
           Vec<T>::unpack(v[i], x);
 #pragma unroll
-          for (int e = 0; e < RD::N; ++e) sum += mass.of(mass.z(x[e]));
+          for (int e = 0; e < RD::N; ++e) sum = mass.add(sum, mass.z(x[e]));
         }
         sum = warp_sum_u64(sum);
       } else if (a.out_logprobs) {
         float s = 0.f;
+        const float shift = lse_shift(zm), base = lse_base(zm);
 #pragma unroll
         for (int i = 0; i < RD::kIters; ++i) {
           float x[RD::N];
           Vec<T>::unpack(v[i], x);
 #pragma unroll
           for (int e = 0; e < RD::N; ++e)
-            s += ex2_approx(__fmul_rn(__fsub_rn(__fmul_rn(x[e], P.inv_t), zm), kLog2e));
+            s += ex2_approx(__fmaf_rn(__fsub_rn(__fmul_rn(x[e], P.inv_t), shift), kLog2e, -base));
         }
         sum = __float_as_uint(warp_sum_f(s));
       }
@@ -312,15 +378,15 @@ struct Shared {
   float red_f[kWarpsF];
   uint64_t red_w[kWarpsF], red_n[kWarpsF];
   int red_i[kWarpsF];
-  uint32_t table[128];
+  uint2 table[kTable];
   float seg_max[kMaxSegs];    // raw maxima of the row's segments
   uint64_t seg_w[kMaxSegs];   // their masses (element units), then inclusive sums
   int seg_n[kMaxSegs];        // candidates of the segments, then those before each
   int lo, hi;
+  float least[3];             // thresholds on raw logits
   int bin;
   uint32_t bin_n;
   uint64_t above;
-  Cut cut;
   uint32_t digit_n[256];      // radix selection, 8 bits at a time
   unsigned long long digit_w[256];
   union {
@@ -334,11 +400,17 @@ struct Shared {
   };
 };
 
+// This CTA's shared memory, by its own name: a reference handed into a function
+// that is not inlined would make every access, and every atomic, a generic one.
+__device__ __forceinline__ Shared& smem() {
+  extern __shared__ __align__(128) unsigned char dyn[];
+  return *reinterpret_cast<Shared*>(dyn);
+}
+
 // A row and the CTAs that finish it (a team: the cluster, or rank 0 alone).
 template <typename T>
 struct Row {
   RowData<T> rd;
-  Shared& sh;
   Mass mass;
   float m;      // tempered maximum
   int segs;     // of the row
@@ -346,15 +418,15 @@ struct Row {
   int C, rank;  // the team
   int s0, s1;   // this CTA's segments
   int per;      // segments to a CTA
-  __device__ __forceinline__ Row(const RowData<T>& rd_, Shared& sh_, const Mass& mass_, float m_,
-                                 int segs_, int drop_, int C_, int rank_)
-      : rd(rd_), sh(sh_), mass(mass_), m(m_), segs(segs_), drop(drop_), C(C_), rank(rank_) {
+  __device__ __forceinline__ Row(const RowData<T>& rd_, const Mass& mass_, float m_, int segs_,
+                                 int drop_, int C_, int rank_)
+      : rd(rd_), mass(mass_), m(m_), segs(segs_), drop(drop_), C(C_), rank(rank_) {
     per = (segs + C - 1) / C;
     s0 = min(segs, rank * per);
     s1 = min(segs, s0 + per);
   }
   __device__ __forceinline__ Shared* at(int r) {
-    return C > 1 ? cg::this_cluster().map_shared_rank(&sh, r) : &sh;
+    return C > 1 ? cg::this_cluster().map_shared_rank(&smem(), r) : &smem();
   }
   __device__ __forceinline__ void sync() {
     if (C > 1) cg::this_cluster().sync();
@@ -368,14 +440,17 @@ struct Row {
   __device__ __forceinline__ uint64_t coarse(uint64_t w) const {
     return (w + (1ull << (drop - 1))) >> drop;
   }
-  __device__ __forceinline__ float bins_below(float z) const {
-    return __fmul_rn(__fsub_rn(m, z), kBinsPerNat);
+  // distance below the maximum in bins, with the bin's number rounded into it:
+  // kMagic + the bin, as a float; monotone in z
+  __device__ __forceinline__ float dist(float z) const {
+    return fminf(__fmaf_rn(z, -kBinsPerNat, m * kBinsPerNat), (float)(kBins - 1));
   }
-  __device__ __forceinline__ float seg_top(int s) const { return mass.z(sh.seg_max[s]); }
+  __device__ __forceinline__ float bin_f(float z) const { return __fadd_rn(dist(z), kMagic); }
+  __device__ __forceinline__ float seg_top(int s) const { return mass.z(smem().seg_max[s]); }
 };
 
-__device__ __forceinline__ int bin_of(float t) {
-  return t < (float)(kBins - 1) ? (int)t : kBins - 1;
+__device__ __forceinline__ int bin_no(float bin_f) {
+  return __float_as_int(bin_f) - __float_as_int(kMagic);
 }
 
 // Block-wide exclusive sum in thread order, and the total.
@@ -415,6 +490,26 @@ __device__ __forceinline__ int block_sum(Shared& sh, int v) {
 #pragma unroll
   for (int i = 0; i < kWarpsF; ++i) v += sh.red_i[i];
   return v;
+}
+
+// The smallest logit x whose tempered value z(x) satisfies `reaches`, a predicate
+// that holds from some z on: a search of the order keys, 32 at a time.  One warp.
+template <typename F>
+__device__ __forceinline__ float least_logit(const Mass& mass, F reaches) {
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t lo = 0;  // the answer is at or above
+#pragma unroll 1
+  for (int shift = 27; shift >= -3; shift -= 5) {
+    const uint32_t step = shift > 0 ? 1u << shift : 1u;
+    const uint32_t key = lo + lane * step + (step - 1);  // the last of the lane's share
+    const float x = key_value(key);
+    // (NaN keys lie below -inf and above +inf)
+    const bool yes = key >= lo && (key >= 0xff800000u || (key >= 0x007fffffu && reaches(mass.z(x))));
+    const unsigned no = __popc(__ballot_sync(0xffffffffu, !yes));
+    if (no == 32) return INFINITY;
+    lo += no * step;
+  }
+  return key_value(lo);
 }
 
 // Of 256 digits' (elements, weight), counted from 255 down after `before`: the
@@ -460,8 +555,9 @@ __device__ __forceinline__ void find_digit(Shared& sh, uint64_t before, uint64_t
 template <typename T, bool MASS>
 __device__ __noinline__ Cut radix_select(const Row<T>& row_in, Cut cut, uint64_t target) {
   Row<T> rw = row_in;  // in registers
+  rw.mass.table = smem().table;
   using RD = RowData<T>;
-  Shared& sh = rw.sh;
+  Shared& sh = smem();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t prefix = 0;
   uint64_t before = 0;
@@ -585,15 +681,31 @@ __device__ __noinline__ Cut radix_select(const Row<T>& row_in, Cut cut, uint64_t
 
 constexpr int kListDrop = 2;  // list masses: units of 2^(E - kElemBits + 2), 2048 below 2^62
 
-// The leader's list in the order (z descending, index ascending), into sh.sorted:
-// a bitonic sort with four neighbouring entries in each thread's registers, so
-// that of the 66 steps over 2048 entries 21 stay in a thread, 35 are shuffles and
-// only 10 go through shared memory.  Threads past the entries take part in the
-// barriers alone.
+// sh.sorted[0, n), entries of (key, ~index), into the order (z descending, index
+// ascending).  Up to 512: every entry counts those ahead of it, the comparisons
+// shared out over all threads.  Beyond: a bitonic sort with four neighbouring
+// entries in each thread's registers, so that of the 66 steps over 2048 entries
+// 21 stay in a thread, 35 are shuffles and only 10 go through shared memory.
 constexpr int kSortPer = 4;
 static_assert(kSortPer * kThreadsF == kList, "a thread holds four entries of a full list");
-__device__ __noinline__ void sort_list(Shared& sh, int n) {
+__device__ __noinline__ void sort_entries(int n) {
+  Shared& sh = smem();
   const int tid = threadIdx.x;
+  __syncthreads();
+  if (n <= kThreadsF) {
+    int parts = 1;  // threads that share an entry: neighbours, at most a warp
+    while (parts < 32 && 2 * parts * n <= kThreadsF) parts *= 2;
+    const int i = tid / parts, part = tid % parts;
+    const uint64_t mine = i < n ? sh.sorted[i] : 0ull;
+    int ahead = 0;
+    if (i < n)
+      for (int j = part; j < n; j += parts) ahead += sh.sorted[j] > mine;
+    for (int o = 1; o < parts; o *= 2) ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+    __syncthreads();
+    if (i < n && part == 0) sh.sorted[ahead] = mine;
+    __syncthreads();
+    return;
+  }
   int N = 128;
   while (N < n) N *= 2;
   const bool on = tid * kSortPer < N;  // whole warps
@@ -602,7 +714,7 @@ __device__ __noinline__ void sort_list(Shared& sh, int n) {
 #pragma unroll
   for (int q = 0; q < kSortPer; ++q) {
     const int i = tid * kSortPer + q;
-    v[q] = i < n ? ((uint64_t)sh.list.key[i] << 32) | (uint32_t)~i : 0ull;
+    v[q] = i < n ? sh.sorted[i] : 0ull;
   }
   for (int k = 2; k <= N; k <<= 1) {
     int j = k >> 1;
@@ -663,7 +775,7 @@ __device__ __noinline__ void sort_list(Shared& sh, int n) {
 // The cut whose last element is entry i of the sorted list.
 __device__ __forceinline__ Cut sorted_cut(const Shared& sh, int i) {
   const uint64_t e = sh.sorted[i];
-  return Cut{key_value((uint32_t)(e >> 32)), sh.list.idx[~(uint32_t)e]};
+  return Cut{key_value((uint32_t)(e >> 32)), (int)~(uint32_t)e};
 }
 // Of the first n entries of the sorted list, those with a mass (list units) of at
 // most target before them: the cut, and their total mass in *all.  `share` >= 0:
@@ -690,20 +802,6 @@ __device__ __forceinline__ Cut cut_by_mass(Shared& sh, const Mass& mass, int n, 
   return sorted_cut(sh, kept - 1);
 }
 
-// seg_n of this CTA's segments to the elements before each; their total (warp 0).
-template <typename T>
-__device__ __forceinline__ int scan_segments(const Row<T>& rw) {
-  const int lane = threadIdx.x & 31;
-  int carry = 0;
-  for (int b = rw.s0; b < rw.s1; b += 32) {
-    const int c = b + lane < rw.s1 ? rw.sh.seg_n[b + lane] : 0;
-    const int inc = warp_scan(c) + carry;
-    if (b + lane < rw.s1) rw.sh.seg_n[b + lane] = inc - c;
-    carry = __shfl_sync(0xffffffffu, inc, 31);
-  }
-  return carry;
-}
-
 // The boundary of the elements kept by `cut` by one linear histogram below the
 // maximum, which brackets it, and a list of the elements in the bracket.
 //   MASS: the boundary of the top-p share `p` of *row_mass, the mass of all
@@ -716,8 +814,9 @@ template <typename T, bool MASS>
 __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, float p, int top_k,
                                          uint64_t* row_mass) {
   Row<T> rw = row_in;  // in registers
+  rw.mass.table = smem().table;
   using RD = RowData<T>;
-  Shared& sh = rw.sh;
+  Shared& sh = smem();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Cut cut = *cut_io;
   constexpr int kPer = kBins / kThreadsF;
@@ -728,30 +827,34 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
     sh.lo = kBins;
     sh.hi = -1;
   }
+  if (warp == 0) {
+    const float x = least_logit(rw.mass, [&](float z) { return z >= cut.z; });
+    if (lane == 0) sh.least[0] = x;
+  }
   __syncthreads();
-  // by mass: each element adds its mass relative to its bin's upper edge in
-  // units of 1/4095, so a bin's mass is known to within 1.3e-4 of itself
+  const bool plain = cut.idx == kMaxIdx;  // a threshold on the logits says it all
+  const float x_cut = sh.least[0];
+  // by mass: each element adds its mass relative to its bin's middle in units of
+  // 1/4063, so a bin's mass is known to within 1.3e-4 of itself
   for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
-    if (rw.seg_top(s) < cut.z) continue;
-#pragma unroll 2
-    for (int i = 0; i < RD::kIters; ++i) {
-      const int at = RD::at(s, i);
-      float x[RD::N];
-      rw.rd.load(at, x);
+    if (sh.seg_max[s] < x_cut) continue;
+    each_vector(rw.rd, s, [&](const float(&x)[RD::N], int at) {
 #pragma unroll
       for (int e = 0; e < RD::N; ++e) {
         const float z = rw.mass.z(x[e]);
-        const float t = rw.bins_below(z);
-        const int bin = bin_of(t);
+        const float t = rw.dist(z);
+        const float b = __fadd_rn(t, kMagic);
         uint32_t add = 1;
-        if (MASS) {
-          const float f = t - (float)bin;
-          add = (uint32_t)__fmaf_rn(f, __fmaf_rn(f, 0.4999f, -63.984f), 4095.5f);
+        if (MASS) {  // 4063 e^(-f / 64), f in [-1/2, 1/2], through a rounding by 2^23
+          const float f = __fsub_rn(t, __fsub_rn(b, kMagic));
+          add = __float_as_uint(__fmaf_rn(f, __fmaf_rn(f, 0.49597f, -63.484f), 8388608.f + 4063.f)) &
+                0x1fffu;
         }
-        if (cut.keeps(z, at + e) && !(MASS && bin == kBins - 1))
-          atomicAdd(&sh.hist.own[bin], add);
+        if (x[e] >= x_cut && (plain || cut.keeps(z, at + e)) &&
+            !(MASS && t >= (float)(kBins - 1)))
+          atomicAdd(&sh.hist.own[bin_no(b)], add);
       }
-    }
+    });
   }
   // the team's histogram: CTA r sums a share of the bins and sends it to all
   rw.sync();
@@ -819,43 +922,57 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
   if (!MASS) above_n = sh.above;
   if (lo > hi) return false;  // (a histogram without mass)
 
-  // the masses above the bracket, and how many elements are in it; segments that
-  // end below it are not read, unless the mass of all is wanted
+  // the masses above the bracket, and the bracket's elements into this CTA's
+  // entries; segments that end below it are not read, unless the mass of all is
+  // wanted
   const bool want_all = MASS && *row_mass == 0;
+  if (warp == 1 || warp == 2) {
+    const float edge = kMagic + (float)(warp == 1 ? lo - 1 : hi);
+    const float x = least_logit(rw.mass, [&](float z) { return rw.bin_f(z) <= edge; });
+    if (lane == 0) sh.least[warp] = x;
+  }
   uint64_t w_above = 0, w_all = 0;
+  if (tid == 0) sh.bin = 0;  // entries so far
+  __syncthreads();
+  const float x_up = fmaxf(sh.least[1], x_cut), x_band = fmaxf(sh.least[2], x_cut);
   for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
     uint64_t above = 0, rest = 0;
-    int c = 0;
-    if (want_all || bin_of(rw.bins_below(rw.seg_top(s))) <= hi) {
-#pragma unroll 1
-      for (int i = 0; i < RD::kIters; ++i) {
-        const int at = RD::at(s, i);
-        float x[RD::N];
-        rw.rd.load(at, x);
+    if (sh.seg_max[s] >= (want_all ? x_cut : x_band)) {
+      each_vector(rw.rd, s, [&](const float(&x)[RD::N], int at) {
+        unsigned take = 0;
 #pragma unroll
         for (int e = 0; e < RD::N; ++e) {
           const float z = rw.mass.z(x[e]);
-          const bool in = cut.keeps(z, at + e);
-          const int bin = bin_of(rw.bins_below(z));
-          c += in && bin >= lo && bin <= hi;
-          if (MASS && in && (bin < lo || want_all)) {
-            const uint64_t w = rw.mass.of(z);
-            above += bin < lo ? w : 0;
-            rest += w;
+          const bool kept = plain || cut.keeps(z, at + e);
+          const bool up = x[e] >= x_up && kept;
+          take |= x[e] >= x_band && kept && !up ? 1u << e : 0u;
+          if (MASS) {  // (a select, not a branch: the eight masses overlap)
+            above = rw.mass.add(above, up ? z : -INFINITY);
+            if (want_all) rest = rw.mass.add(rest, x[e] >= x_cut && kept ? z : -INFINITY);
           }
         }
-      }
-      c = warp_sum_i(c);
+        if (!__any_sync(0xffffffffu, take)) return;
+        const int c = __popc(take);
+        const int inc = warp_scan(c);
+        int q = 0;
+        if (lane == 31) q = atomicAdd(&sh.bin, inc);
+        q = __shfl_sync(0xffffffffu, q, 31) + inc - c;
+#pragma unroll 1
+        for (; take; take &= take - 1, ++q) {
+          const int e = __ffs(take) - 1;
+          if (q < kList) {
+            const float z = rw.mass.z(elem(rw.rd.data[at + e]));
+            sh.sorted[q] = ((uint64_t)ord_key(z) << 32) | (uint32_t)~(at + e);
+          }
+        }
+      });
       if (MASS) above = warp_sum_u64(above);
       if (want_all) rest = warp_sum_u64(rest);
     }
-    if (lane == 0) {
-      sh.seg_n[s] = c;
-      if (MASS) {
-        sh.seg_w[s] = above;
-        w_above += rw.coarse(above);
-        w_all += rw.coarse(rest);
-      }
+    if (MASS && lane == 0) {
+      sh.seg_w[s] = above;
+      w_above += rw.coarse(above);
+      w_all += rw.coarse(rest);
     }
   }
   if (MASS && lane == 0) {
@@ -863,15 +980,12 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
     sh.red_n[warp] = w_all;
   }
   __syncthreads();
-  if (warp == 0) {
-    const int c = scan_segments(rw);
-    rw.send(&Mail::count, c);
-    if (MASS) {
-      w_above = warp_sum_u64(lane < kWarpsF ? sh.red_w[lane] : 0);
-      w_all = warp_sum_u64(lane < kWarpsF ? sh.red_n[lane] : 0);
-      rw.send(&Mail::mass, w_above);
-      rw.send(&Mail::all, w_all);
-    }
+  rw.send(&Mail::count, sh.bin);
+  if (MASS && warp == 0) {
+    w_above = warp_sum_u64(lane < kWarpsF ? sh.red_w[lane] : 0);
+    w_all = warp_sum_u64(lane < kWarpsF ? sh.red_n[lane] : 0);
+    rw.send(&Mail::mass, w_above);
+    rw.send(&Mail::all, w_all);
   }
   rw.sync();
   int n = 0, base = 0;
@@ -888,47 +1002,17 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
     if (want_all) *row_mass = w_all;
     else w_all = *row_mass;
   }
-  if (n <= kList) {
-    // the bracket's elements into the leader's list, in vocabulary order
-    List& list = rw.at(0)->list;
-    const int mine = sh.mail.count[rw.rank];
-    for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
-      const int from = sh.seg_n[s], to = s + 1 < rw.s1 ? sh.seg_n[s + 1] : mine;
-      if (from == to) continue;
-      int off = base + from;
-#pragma unroll 1
-      for (int i = 0; i < RD::kIters; ++i) {
-        const int at = RD::at(s, i);
-        float x[RD::N];
-        rw.rd.load(at, x);
-        unsigned take = 0;
-#pragma unroll
-        for (int e = 0; e < RD::N; ++e) {
-          const float z = rw.mass.z(x[e]);
-          const int bin = bin_of(rw.bins_below(z));
-          take |= cut.keeps(z, at + e) && bin >= lo && bin <= hi ? 1u << e : 0u;
-        }
-        if (!__any_sync(0xffffffffu, take)) continue;
-        const int c = __popc(take);
-        const int inc = warp_scan(c);
-        int q = off + inc - c;
-#pragma unroll
-        for (int e = 0; e < RD::N; ++e)
-          if ((take >> e) & 1) {
-            list.key[q] = ord_key(rw.mass.z(x[e]));
-            list.idx[q] = at + e;
-            ++q;
-          }
-        off += __shfl_sync(0xffffffffu, inc, 31);
-      }
-    }
+  if (n <= kList && rw.rank > 0) {  // behind the leader's own, in any order
+    const int own = sh.mail.count[rw.rank];
+    uint64_t* to = rw.at(0)->sorted + base;
+    for (int i = tid; i < own; i += kThreadsF) to[i] = sh.sorted[i];
   }
   rw.sync();
   if (n <= 0 || n > kList) return false;
   if (rw.rank == 0) {
     bool ok = true;
     Cut found{0.f, kMaxIdx};
-    sort_list(sh, n);
+    sort_entries(n);
     if (MASS) {
       const uint64_t target = part_of(w_all, p);
       // the boundary lies in the bracket: the mass above it is within the
@@ -940,8 +1024,8 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
       ok = ok && left < band;
       if (ok)
         for (int i = tid; i < n; i += kThreadsF) {
-          const int j = sh.list.idx[i];
-          const float z = key_value(sh.list.key[i]);
+          const int j = (int)~(uint32_t)sh.sorted[i];
+          const float z = key_value((uint32_t)(sh.sorted[i] >> 32));
           if (found.keeps(z, j))
             atomicAdd((unsigned long long*)&rw.at(j / kSeg / rw.per)->seg_w[j / kSeg],
                       (unsigned long long)rw.mass.of(z));
@@ -964,26 +1048,32 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
 template <typename T>
 __device__ __noinline__ void kept_mass(const Row<T>& row_in, const Cut cut) {
   Row<T> rw = row_in;  // in registers
+  rw.mass.table = smem().table;
   using RD = RowData<T>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float least = fmaxf(cut.z, rw.m - 64.f);  // no mass below
+  __syncthreads();
+  if (warp == 0) {
+    const float least = fmaxf(cut.z, rw.m - 64.f);  // no mass below
+    const float x = least_logit(rw.mass, [&](float z) { return z >= least; });
+    if (lane == 0) smem().least[0] = x;
+  }
+  __syncthreads();
+  const float x_cut = smem().least[0];
+  const bool plain = cut.idx == kMaxIdx;
   for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
     uint64_t w = 0;
-    if (rw.seg_top(s) >= least) {
-#pragma unroll 2
-      for (int i = 0; i < RD::kIters; ++i) {
-        const int at = RD::at(s, i);
-        float x[RD::N];
-        rw.rd.load(at, x);
+    if (smem().seg_max[s] >= x_cut) {
+      each_vector(rw.rd, s, [&](const float(&x)[RD::N], int at) {
 #pragma unroll
         for (int e = 0; e < RD::N; ++e) {
           const float z = rw.mass.z(x[e]);
-          if (cut.keeps(z, at + e)) w += rw.mass.of(z);
+          const bool in = x[e] >= x_cut && (plain || cut.keeps(z, at + e));
+          w = rw.mass.add(w, in ? z : -INFINITY);
         }
-      }
+      });
       w = warp_sum_u64(w);
     }
-    if (lane == 0) rw.sh.seg_w[s] = w;
+    if (lane == 0) smem().seg_w[s] = w;
   }
 }
 
@@ -991,7 +1081,7 @@ __device__ __noinline__ void kept_mass(const Row<T>& row_in, const Cut cut) {
 // total, the mass of the CTAs before this one and this CTA's.
 template <typename T>
 __device__ uint64_t sum_segments(Row<T>& rw, uint64_t* before, uint64_t* own) {
-  Shared& sh = rw.sh;
+  Shared& sh = smem();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
   if (warp == 0) {
@@ -1023,10 +1113,10 @@ __device__ int find_draw(const Row<T>& rw, const Cut& cut, uint64_t t, float* z_
   int lo = rw.s0, hi = rw.s1 - 1;  // the first segment whose inclusive mass exceeds t
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (rw.sh.seg_w[mid] > t) hi = mid;
+    if (smem().seg_w[mid] > t) hi = mid;
     else lo = mid + 1;
   }
-  if (lo > rw.s0) t -= rw.sh.seg_w[lo - 1];
+  if (lo > rw.s0) t -= smem().seg_w[lo - 1];
   t <<= rw.drop;  // element units
   int idx = -1;
   float zz = 0.f;
@@ -1093,7 +1183,8 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
                                             const RowParams& P, const Cut minp, int row,
                                             float ln_s) {
   Row<T> rw = row_in;  // in registers
-  Shared& sh = rw.sh;
+  rw.mass.table = smem().table;
+  Shared& sh = smem();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float* gmax = a.group_max + (int64_t)row * rw.segs * kGroupsPerSeg;
   const int groups = rw.segs * kGroupsPerSeg;
@@ -1104,7 +1195,7 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   __syncthreads();
   for (int i = tid; i < groups; i += kThreadsF) {
     const float x = gmax[i];
-    if (x > -INFINITY) atomicAdd(&sh.hist.own[bin_of(rw.bins_below(rw.mass.z(x)))], 1u);
+    if (x > -INFINITY) atomicAdd(&sh.hist.own[bin_no(rw.bin_f(rw.mass.z(x)))], 1u);
   }
   __syncthreads();
   {
@@ -1124,13 +1215,22 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   }
   __syncthreads();
   // (fewer than top_k groups with a finite element: every finite element)
-  const float edge = sh.hi == kBins - 1 ? INFINITY : (float)(sh.hi + 1);
+  const bool any = sh.hi == kBins - 1;
+  if (warp == 0) {
+    const float edge = kMagic + (float)sh.hi;
+    const float x = least_logit(
+        rw.mass, [&](float z) { return z > -INFINITY && (any || rw.bin_f(z) <= edge); });
+    if (lane == 0) sh.least[0] = x;
+  }
+  __syncthreads();
+  const float x_least = sh.least[0];
+  auto reaches = [&](float x) { return x >= x_least; };
   // the groups that reach it, in order
   int n_groups = 0;
   constexpr int kCap = (int)(sizeof(sh.groups) / sizeof(sh.groups[0]));
   for (int b = 0; b < groups; b += kThreadsF) {
     const int i = b + tid;
-    const bool in = i < groups && rw.bins_below(rw.mass.z(gmax[i])) < edge;
+    const bool in = i < groups && reaches(gmax[i]);
     const unsigned mask = __ballot_sync(0xffffffffu, in);
     if (lane == 0) sh.red_i[warp] = __popc(mask);
     __syncthreads();
@@ -1146,23 +1246,28 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
     __syncthreads();
   }
   if (n_groups > kCap || n_groups > kList) return false;
-  // a warp to a group: two elements a lane, in order
-  auto pair = [&](int g, float (&x)[2]) {
-    const int p = (int)sh.groups[g] * kGroup + lane * 2;
+  // a warp to a group, two elements a lane, in order; kAhead groups' loads at once
+  constexpr int kAhead = 8;
+  auto fetch = [&](int g0, float (&x)[kAhead][2]) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) x[e] = p + e < rw.rd.V ? elem(rw.rd.data[p + e]) : -INFINITY;
-    return p;
+    for (int q = 0; q < kAhead; ++q) {
+      const int g = g0 + q * kWarpsF;
+      const int p = g < n_groups ? (int)sh.groups[g] * kGroup + lane * 2 : rw.rd.V;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) x[q][e] = p + e < rw.rd.V ? elem(rw.rd.data[p + e]) : -INFINITY;
+    }
   };
   uint16_t* before = reinterpret_cast<uint16_t*>(sh.seg_w);  // candidates of each group
   static_assert(sizeof(sh.seg_w) >= kList * sizeof(uint16_t), "a count for every listed group");
-  for (int g = warp; g < n_groups; g += kWarpsF) {
-    float x[2];
-    pair(g, x);
-    int c = 0;
+  for (int g0 = warp; g0 < n_groups; g0 += kWarpsF * kAhead) {
+    float x[kAhead][2];
+    fetch(g0, x);
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      c += __popc(__ballot_sync(0xffffffffu, rw.bins_below(rw.mass.z(x[e])) < edge));
-    if (lane == 0) before[g] = (uint16_t)c;
+    for (int q = 0; q < kAhead; ++q) {
+      const int c = __popc(__ballot_sync(0xffffffffu, reaches(x[q][0]))) +
+                    __popc(__ballot_sync(0xffffffffu, reaches(x[q][1])));
+      if (lane == 0 && g0 + q * kWarpsF < n_groups) before[g0 + q * kWarpsF] = (uint16_t)c;
+    }
   }
   __syncthreads();
   uint64_t n64;
@@ -1187,27 +1292,30 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   const int n = (int)n64;
   __syncthreads();
   List& list = sh.list;
-  for (int g = warp; g < n_groups; g += kWarpsF) {
-    float x[2];
-    const int p = pair(g, x);
-    bool in[2];
-    unsigned mask[2];
+  for (int g0 = warp; g0 < n_groups; g0 += kWarpsF * kAhead) {
+    float x[kAhead][2];
+    fetch(g0, x);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      in[e] = rw.bins_below(rw.mass.z(x[e])) < edge;
-      mask[e] = __ballot_sync(0xffffffffu, in[e]);
+    for (int q = 0; q < kAhead; ++q) {
+      const int g = g0 + q * kWarpsF;
+      const bool in[2] = {reaches(x[q][0]), reaches(x[q][1])};
+      const unsigned m0 = __ballot_sync(0xffffffffu, in[0]), m1 = __ballot_sync(0xffffffffu, in[1]);
+      if (g >= n_groups) continue;
+      const unsigned below = (1u << lane) - 1;
+      int at = before[g] + __popc(m0 & below) + __popc(m1 & below);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (in[e]) {
+          list.key[at] = ord_key(rw.mass.z(x[q][e]));
+          list.idx[at] = (int)sh.groups[g] * kGroup + lane * 2 + e;
+          ++at;
+        }
     }
-    const unsigned below = (1u << lane) - 1;
-    int at = before[g] + __popc(mask[0] & below) + __popc(mask[1] & below);
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (in[e]) {
-        list.key[at] = ord_key(rw.mass.z(x[e]));
-        list.idx[at] = p + e;
-        ++at;
-      }
   }
-  sort_list(sh, n);  // (over the groups' memory, after a barrier)
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreadsF)  // (over the groups' memory)
+    sh.sorted[i] = ((uint64_t)list.key[i] << 32) | (uint32_t)~list.idx[i];
+  sort_entries(n);
   int kept = 0;
   for (int i = tid; i < n; i += kThreadsF) kept += key_value(list.key[i]) >= minp.z;
   kept = min(block_sum(sh, kept), P.top_k);
@@ -1248,8 +1356,7 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
 template <typename T>
 __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
   using RD = RowData<T>;
-  extern __shared__ __align__(128) unsigned char dyn[];
-  Shared& sh = *reinterpret_cast<Shared*>(dyn);
+  Shared& sh = smem();
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
@@ -1262,7 +1369,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
   const bool team = ctas > 1 && !greedy && !from_list &&
                     (topk || (P.flags & (kRowTopP | kRowMinP)));
   if (rank > 0 && !team) return;
-  if (tid < 128) sh.table[tid] = c_mass_table.v[tid];
+  for (int i = tid; i < kTable; i += kThreadsF) sh.table[i] = c_mass_table.v[i];
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // the row's maximum
@@ -1297,20 +1404,20 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
   }
   const Mass mass(P.inv_t, m, sh.table);
   const RowData<T> rd{static_cast<const T*>(a.logits) + row * a.ld, a.V, a.aligned != 0};
-  Row<T> rw(rd, sh, mass, m, a.segs, a.drop, team ? ctas : 1, team ? rank : 0);
+  Row<T> rw(rd, mass, m, a.segs, a.drop, team ? ctas : 1, team ? rank : 0);
 
   // ln sum exp(z - m) from the segments' sums; masses to element units of the row
   float ln_s = 0.f;
   const bool masses = sums_masses(P, a.V);
-  const bool usable = masses && fabsf(m) < kWide;
+  const bool usable = masses && fabsf(m) < kUsable;
   uint64_t all = 0;  // mass of every element, row units (0: not known)
   if (usable) {
     for (int s = tid; s < a.segs; s += kThreadsF) {
       const float zm = mass.z(sh.seg_max[s]);
       uint64_t w = 0;
       if (zm > -INFINITY) {
-        const int sh_r = (mass.e128 - Mass(P.inv_t, zm, sh.table).e128) >> 7;
-        w = fabsf(zm) < 8192.f && sh_r < 64 ? seg_sum[s] >> sh_r : 0;
+        const int sh_r = mass.E() - Mass(P.inv_t, zm, sh.table).E();
+        w = fabsf(zm) < kNarrow && sh_r < 64 ? seg_sum[s] >> sh_r : 0;
       }
       sh.seg_w[s] = w;
       all += rw.coarse(w);
@@ -1323,9 +1430,14 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
       const float zm = mass.z(sh.seg_max[s]);
       if (zm > -INFINITY)
         e += __uint_as_float((uint32_t)seg_sum[s]) *
-             ex2_approx(__fmul_rn(__fsub_rn(zm, m), kLog2e));
+             ex2_approx(fmaxf(fabsf(zm), fabsf(m)) < kNarrow
+                            ? lse_base(zm) - lse_base(m)
+                            : __fmul_rn(__fsub_rn(zm, m), kLog2e));
     }
-    ln_s = logf(block_sum(sh, e));
+    // lse_base(m) ln 2 - m in one rounding, ln 2 in two parts
+    ln_s = logf(block_sum(sh, e)) +
+           (__fmaf_rn(lse_base(m), 0.693147182464599609375f, lse_shift(m) - m) +
+            lse_base(m) * -1.904654299957e-9f);
   }
 
   if (greedy) {
@@ -1430,6 +1542,8 @@ cudaError_t launch_given_typed(const GivenArgs& a, int num_sms, int ctas, cudaSt
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(finish_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)sizeof(Shared));
+  if (e == cudaSuccess && ctas > 8)
+    e = cudaFuncSetAttribute(finish_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.B * ctas));
@@ -1456,7 +1570,7 @@ cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t strea
   int bits = 0;
   while ((1ll << bits) < a.V) ++bits;
   a.drop = max(kListDrop, bits + kElemBits - 62);
-  const int ctas = a.B <= 38 ? 8 : 4;
+  const int ctas = a.B <= 9 ? 16 : a.B <= 38 ? 8 : 4;
   return dtype == VT_DTYPE_F32 ? launch_given_typed<float>(a, num_sms, ctas, stream)
                                : launch_given_typed<__nv_bfloat16>(a, num_sms, ctas, stream);
 }
