@@ -40,8 +40,8 @@ constexpr int kGroup = kGivenGroup; // elements that share a group maximum
 constexpr int kGroupsPerSeg = kSeg / kGroup;
 constexpr int kMaxSegs = 1024;      // of a row: V <= 2^20
 constexpr int kMaxCtas = 16;        // CTAs that finish a row
-constexpr int kBins = 2048;
-constexpr float kBinsPerNat = 64.f;  // linear bins: 32 nats below the maximum, then one for all
+constexpr int kBins = 4096;
+constexpr float kBinsPerNat = 128.f;  // linear bins: 32 nats below the maximum, then one for all
 constexpr int kList = 2048;         // candidates a row's leader CTA holds
 constexpr int kListTopK = 1024;     // largest top-k taken from group maxima
 constexpr int kListPerThread = kList / kThreadsF;
@@ -440,15 +440,23 @@ struct Row {
   __device__ __forceinline__ uint64_t coarse(uint64_t w) const {
     return (w + (1ull << (drop - 1))) >> drop;
   }
-  // distance below the maximum in bins, with the bin's number rounded into it:
-  // kMagic + the bin, as a float; monotone in z
-  __device__ __forceinline__ float dist(float z) const {
-    return fminf(__fmaf_rn(z, -kBinsPerNat, m * kBinsPerNat), (float)(kBins - 1));
-  }
-  __device__ __forceinline__ float bin_f(float z) const { return __fadd_rn(dist(z), kMagic); }
   __device__ __forceinline__ float seg_top(int s) const { return mass.z(smem().seg_max[s]); }
 };
 
+// Linear bins, per_nat to a unit below `top`; values above it go to bin 0.
+struct Bins {
+  float per_nat, top_bins;
+  __device__ __forceinline__ Bins(float top, float per_nat_) {
+    per_nat = per_nat_;
+    top_bins = __fmul_rn(top, per_nat_);
+  }
+  // distance below the top in bins; monotone in z
+  __device__ __forceinline__ float dist(float z) const {
+    return fminf(fmaxf(__fmaf_rn(z, -per_nat, top_bins), 0.f), (float)(kBins - 1));
+  }
+  // kMagic + the number of the bin, as a float
+  __device__ __forceinline__ float bin_f(float z) const { return __fadd_rn(dist(z), kMagic); }
+};
 __device__ __forceinline__ int bin_no(float bin_f) {
   return __float_as_int(bin_f) - __float_as_int(kMagic);
 }
@@ -802,14 +810,16 @@ __device__ __forceinline__ Cut cut_by_mass(Shared& sh, const Mass& mass, int n, 
   return sorted_cut(sh, kept - 1);
 }
 
-// The boundary of the elements kept by `cut` by one linear histogram below the
-// maximum, which brackets it, and a list of the elements in the bracket.
+// The boundary of the elements kept by `cut` by linear histograms, which bracket
+// it closer and closer, and a list of the elements in the bracket, once it holds
+// them.  One histogram over the row nearly always does; the masses above a
+// bracket are summed exactly before the next is made of it.
 //   MASS: the boundary of the top-p share `p` of *row_mass, the mass of all
 //   elements kept by `cut` (row units; 0: not known yet, and set here).  On
 //   success the CTAs' seg_w hold the masses of the kept elements (element units).
 //   else: the first `top_k` are kept.
-// Returns false (the same in every CTA) when the bracket holds too many, or, by
-// mass, turns out not to hold the boundary.
+// Returns false (the same in every CTA) when too many elements are equal, or, by
+// mass, when a bracket turns out not to hold the boundary.
 template <typename T, bool MASS>
 __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, float p, int top_k,
                                          uint64_t* row_mass) {
@@ -821,12 +831,6 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
   const Cut cut = *cut_io;
   constexpr int kPer = kBins / kThreadsF;
   __syncthreads();
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kThreadsF] = 0;
-  if (tid == 0) {
-    sh.lo = kBins;
-    sh.hi = -1;
-  }
   if (warp == 0) {
     const float x = least_logit(rw.mass, [&](float z) { return z >= cut.z; });
     if (lane == 0) sh.least[0] = x;
@@ -834,190 +838,226 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
   __syncthreads();
   const bool plain = cut.idx == kMaxIdx;  // a threshold on the logits says it all
   const float x_cut = sh.least[0];
-  // by mass: each element adds its mass relative to its bin's middle in units of
-  // 1/4063, so a bin's mass is known to within 1.3e-4 of itself
-  for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
-    if (sh.seg_max[s] < x_cut) continue;
-    each_vector(rw.rd, s, [&](const float(&x)[RD::N], int at) {
+  float x_from = x_cut, x_to = INFINITY;  // the bracket: x_from <= x < x_to
+  float top = rw.m, per_nat = kBinsPerNat;
+  uint64_t target = MASS && *row_mass ? part_of(*row_mass, p) : 0;
+  uint64_t w_above = 0;  // mass above the bracket
+  uint64_t n_above = 0;  // (by count) elements above it
+  int n = 0;
+#pragma unroll 1
+  for (int level = 0;; ++level) {
+    const Bins bins(top, per_nat);
 #pragma unroll
-      for (int e = 0; e < RD::N; ++e) {
-        const float z = rw.mass.z(x[e]);
-        const float t = rw.dist(z);
-        const float b = __fadd_rn(t, kMagic);
-        uint32_t add = 1;
-        if (MASS) {  // 4063 e^(-f / 64), f in [-1/2, 1/2], through a rounding by 2^23
-          const float f = __fsub_rn(t, __fsub_rn(b, kMagic));
-          add = __float_as_uint(__fmaf_rn(f, __fmaf_rn(f, 0.49597f, -63.484f), 8388608.f + 4063.f)) &
-                0x1fffu;
-        }
-        if (x[e] >= x_cut && (plain || cut.keeps(z, at + e)) &&
-            !(MASS && t >= (float)(kBins - 1)))
-          atomicAdd(&sh.hist.own[bin_no(b)], add);
-      }
-    });
-  }
-  // the team's histogram: CTA r sums a share of the bins and sends it to all
-  rw.sync();
-  const uint32_t* bins = sh.hist.own;
-  if (rw.C > 1) {
-    const int share = kBins / rw.C;
-    for (int q = tid; q < share; q += kThreadsF) {
-      const int bin = rw.rank * share + q;
-      uint32_t c = 0;
-#pragma unroll 4
-      for (int r = 0; r < rw.C; ++r) c += rw.at(r)->hist.own[bin];
-#pragma unroll 4
-      for (int r = 0; r < rw.C; ++r) rw.at(r)->hist.sum[bin] = c;
+    for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kThreadsF] = 0;
+    if (tid == 0) {
+      sh.lo = kBins;
+      sh.hi = -1;
     }
-    rw.sync();
-    bins = sh.hist.sum;
-  }
-  uint32_t cn[kPer];
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) cn[q] = bins[tid * kPer + q];
-  uint64_t above_n = 0;  // elements above the bracket (by count)
-  if (MASS) {
-    float cf[kPer], tf = 0.f;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      cf[q] = (float)cn[q] * ex2_approx((float)(tid * kPer + q) * (-kLog2e / kBinsPerNat));
-      tf += cf[q];
-    }
-    const float inc = warp_scan(tf);
-    if (lane == 31) sh.red_f[warp] = inc;
     __syncthreads();
-    float a = inc - tf, all = 0.f;
-    for (int i = 0; i < kWarpsF; ++i) {
-      if (i < warp) a += sh.red_f[i];
-      all += sh.red_f[i];
-    }
-    constexpr float kSlack = 1.f / 6144;  // of the bins' masses and their fp32 sums
-    const float want = p * all;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      if (cn[q] > 0) {
-        // bins that end before the target are kept whole, those that begin
-        // after it not at all
-        if (a + cf[q] >= want * (1.f - kSlack)) atomicMin(&sh.lo, tid * kPer + q);
-        if (a <= want * (1.f + kSlack)) atomicMax(&sh.hi, tid * kPer + q);
-      }
-      a += cf[q];
-    }
-  } else {
-    uint64_t tn = 0, unused;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) tn += cn[q];
-    uint64_t a = block_scan(sh, tn, &unused);
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      if (a < (uint64_t)top_k && a + cn[q] >= (uint64_t)top_k) {
-        sh.lo = sh.hi = tid * kPer + q;
-        sh.above = a;
-      }
-      a += cn[q];
-    }
-  }
-  __syncthreads();
-  const int lo = sh.lo, hi = sh.hi;
-  if (!MASS) above_n = sh.above;
-  if (lo > hi) return false;  // (a histogram without mass)
-
-  // the masses above the bracket, and the bracket's elements into this CTA's
-  // entries; segments that end below it are not read, unless the mass of all is
-  // wanted
-  const bool want_all = MASS && *row_mass == 0;
-  if (warp == 1 || warp == 2) {
-    const float edge = kMagic + (float)(warp == 1 ? lo - 1 : hi);
-    const float x = least_logit(rw.mass, [&](float z) { return rw.bin_f(z) <= edge; });
-    if (lane == 0) sh.least[warp] = x;
-  }
-  uint64_t w_above = 0, w_all = 0;
-  if (tid == 0) sh.bin = 0;  // entries so far
-  __syncthreads();
-  const float x_up = fmaxf(sh.least[1], x_cut), x_band = fmaxf(sh.least[2], x_cut);
-  for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
-    uint64_t above = 0, rest = 0;
-    if (sh.seg_max[s] >= (want_all ? x_cut : x_band)) {
+    // by mass: each element adds its mass relative to its bin's middle in units of
+    // 1/4063, so a bin's mass is known to within 1.3e-4 of itself
+    const float c1 = -4063.f / per_nat, c2 = 4063.f * 0.5f / (per_nat * per_nat);
+    for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
+      if (sh.seg_max[s] < x_from) continue;
       each_vector(rw.rd, s, [&](const float(&x)[RD::N], int at) {
-        unsigned take = 0;
 #pragma unroll
         for (int e = 0; e < RD::N; ++e) {
           const float z = rw.mass.z(x[e]);
-          const bool kept = plain || cut.keeps(z, at + e);
-          const bool up = x[e] >= x_up && kept;
-          take |= x[e] >= x_band && kept && !up ? 1u << e : 0u;
-          if (MASS) {  // (a select, not a branch: the eight masses overlap)
-            above = rw.mass.add(above, up ? z : -INFINITY);
-            if (want_all) rest = rw.mass.add(rest, x[e] >= x_cut && kept ? z : -INFINITY);
+          const float t = bins.dist(z);
+          const float b = __fadd_rn(t, kMagic);
+          uint32_t add = 1;
+          if (MASS) {  // 4063 e^(-f / per_nat), f in [-1/2, 1/2], through a rounding by 2^23
+            const float f = __fsub_rn(t, __fsub_rn(b, kMagic));
+            add = __float_as_uint(__fmaf_rn(f, __fmaf_rn(f, c2, c1), 8388608.f + 4063.f)) & 0x1fffu;
           }
-        }
-        if (!__any_sync(0xffffffffu, take)) return;
-        const int c = __popc(take);
-        const int inc = warp_scan(c);
-        int q = 0;
-        if (lane == 31) q = atomicAdd(&sh.bin, inc);
-        q = __shfl_sync(0xffffffffu, q, 31) + inc - c;
-#pragma unroll 1
-        for (; take; take &= take - 1, ++q) {
-          const int e = __ffs(take) - 1;
-          if (q < kList) {
-            const float z = rw.mass.z(elem(rw.rd.data[at + e]));
-            sh.sorted[q] = ((uint64_t)ord_key(z) << 32) | (uint32_t)~(at + e);
-          }
+          if (x[e] >= x_from && x[e] < x_to && (plain || cut.keeps(z, at + e)) &&
+              !(MASS && t >= (float)(kBins - 1)))
+            atomicAdd(&sh.hist.own[bin_no(b)], add);
         }
       });
-      if (MASS) above = warp_sum_u64(above);
-      if (want_all) rest = warp_sum_u64(rest);
+    }
+    // the team's histogram: CTA r sums a share of the bins and sends it to all
+    rw.sync();
+    const uint32_t* from = sh.hist.own;
+    if (rw.C > 1) {
+      const int share = kBins / rw.C;
+      for (int q = tid; q < share; q += kThreadsF) {
+        const int bin = rw.rank * share + q;
+        uint32_t c = 0;
+#pragma unroll 4
+        for (int r = 0; r < rw.C; ++r) c += rw.at(r)->hist.own[bin];
+#pragma unroll 4
+        for (int r = 0; r < rw.C; ++r) rw.at(r)->hist.sum[bin] = c;
+      }
+      rw.sync();
+      from = sh.hist.sum;
+    }
+    uint32_t cn[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) cn[q] = from[tid * kPer + q];
+    uint64_t above_n = 0;
+    if (MASS) {
+      float cf[kPer], tf = 0.f;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        cf[q] = (float)cn[q] * ex2_approx((float)(tid * kPer + q) * (-kLog2e / per_nat));
+        tf += cf[q];
+      }
+      const float inc = warp_scan(tf);
+      if (lane == 31) sh.red_f[warp] = inc;
+      __syncthreads();
+      float a = inc - tf, all = 0.f;
+      for (int i = 0; i < kWarpsF; ++i) {
+        if (i < warp) a += sh.red_f[i];
+        all += sh.red_f[i];
+      }
+      constexpr float kSlack = 1.f / 6144;  // of the bins' masses and their fp32 sums
+      // the target in the histogram's units (4063 of the mass at `top`)
+      const float want =
+          target ? __ull2float_rn(target - w_above) * 4063.f /
+                       (__ull2float_rn(rw.mass.of(top)) * exp2f((float)-rw.drop))
+                 : p * all;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        if (cn[q] > 0) {
+          // bins that end before the target are kept whole, those that begin
+          // after it not at all
+          if (a + cf[q] >= want * (1.f - kSlack)) atomicMin(&sh.lo, tid * kPer + q);
+          if (a <= want * (1.f + kSlack)) atomicMax(&sh.hi, tid * kPer + q);
+        }
+        a += cf[q];
+      }
+    } else {
+      uint64_t tn = 0, unused;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) tn += cn[q];
+      uint64_t a = n_above + block_scan(sh, tn, &unused);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        if (a < (uint64_t)top_k && a + cn[q] >= (uint64_t)top_k) {
+          sh.lo = sh.hi = tid * kPer + q;
+          sh.above = a;
+        }
+        a += cn[q];
+      }
+    }
+    __syncthreads();
+    const int lo = sh.lo, hi = sh.hi;
+    if (!MASS) above_n = sh.above;
+    if (lo > hi) return false;  // (a histogram without mass)
+
+    // the masses above the new bracket, and its elements into this CTA's entries;
+    // segments that end below it are not read, unless the mass of all is wanted
+    const bool want_all = MASS && target == 0;
+    if (warp == 1 || warp == 2) {
+      const float edge = kMagic + (float)(warp == 1 ? lo - 1 : hi);
+      const float x = least_logit(rw.mass, [&](float z) { return bins.bin_f(z) <= edge; });
+      if (lane == 0) sh.least[warp] = x;
+    }
+    if (tid == 0) sh.bin = 0;  // entries so far
+    __syncthreads();
+    // (bin 0 has no element above it, the last bin none below)
+    const float x_up = lo == 0 ? x_to : fminf(fmaxf(sh.least[1], x_from), x_to);
+    const float x_band = hi == kBins - 1 ? x_from : fmaxf(sh.least[2], x_from);
+    uint64_t w_more = 0, w_all = 0;
+    for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
+      uint64_t above = 0, rest = 0;
+      if (sh.seg_max[s] >= (want_all ? x_cut : x_band)) {
+        each_vector(rw.rd, s, [&](const float(&x)[RD::N], int at) {
+          unsigned take = 0;
+#pragma unroll
+          for (int e = 0; e < RD::N; ++e) {
+            const float z = rw.mass.z(x[e]);
+            const bool in = x[e] < x_to && (plain || cut.keeps(z, at + e));
+            const bool up = x[e] >= x_up && in;
+            take |= x[e] >= x_band && in && !up ? 1u << e : 0u;
+            if (MASS) {  // (a select, not a branch: the eight masses overlap)
+              above = rw.mass.add(above, up ? z : -INFINITY);
+              if (want_all) rest = rw.mass.add(rest, x[e] >= x_cut && in ? z : -INFINITY);
+            }
+          }
+          if (!__any_sync(0xffffffffu, take)) return;
+          const int c = __popc(take);
+          const int inc = warp_scan(c);
+          int q = 0;
+          if (lane == 31) q = atomicAdd(&sh.bin, inc);
+          q = __shfl_sync(0xffffffffu, q, 31) + inc - c;
+#pragma unroll 1
+          for (; take; take &= take - 1, ++q) {
+            const int e = __ffs(take) - 1;
+            if (q < kList) {
+              const float z = rw.mass.z(elem(rw.rd.data[at + e]));
+              sh.sorted[q] = ((uint64_t)ord_key(z) << 32) | (uint32_t)~(at + e);
+            }
+          }
+        });
+        if (MASS) above = warp_sum_u64(above);
+        if (want_all) rest = warp_sum_u64(rest);
+      }
+      if (MASS && lane == 0) {
+        sh.seg_w[s] = level > 0 ? sh.seg_w[s] + above : above;
+        w_more += rw.coarse(above);
+        w_all += rw.coarse(rest);
+      }
     }
     if (MASS && lane == 0) {
-      sh.seg_w[s] = above;
-      w_above += rw.coarse(above);
-      w_all += rw.coarse(rest);
+      sh.red_w[warp] = w_more;
+      sh.red_n[warp] = w_all;
     }
-  }
-  if (MASS && lane == 0) {
-    sh.red_w[warp] = w_above;
-    sh.red_n[warp] = w_all;
-  }
-  __syncthreads();
-  rw.send(&Mail::count, sh.bin);
-  if (MASS && warp == 0) {
-    w_above = warp_sum_u64(lane < kWarpsF ? sh.red_w[lane] : 0);
-    w_all = warp_sum_u64(lane < kWarpsF ? sh.red_n[lane] : 0);
-    rw.send(&Mail::mass, w_above);
-    rw.send(&Mail::all, w_all);
-  }
-  rw.sync();
-  int n = 0, base = 0;
-  for (int r = 0; r < rw.C; ++r) {
-    if (r == rw.rank) base = n;
-    n += sh.mail.count[r];
-  }
-  if (MASS) {
-    w_above = w_all = 0;
+    __syncthreads();
+    rw.send(&Mail::count, sh.bin);
+    if (MASS && warp == 0) {
+      w_more = warp_sum_u64(lane < kWarpsF ? sh.red_w[lane] : 0);
+      w_all = warp_sum_u64(lane < kWarpsF ? sh.red_n[lane] : 0);
+      rw.send(&Mail::mass, w_more);
+      rw.send(&Mail::all, w_all);
+    }
+    rw.sync();
+    n = 0;
+    int base = 0;
     for (int r = 0; r < rw.C; ++r) {
-      w_above += sh.mail.mass[r];
-      w_all += sh.mail.all[r];
+      if (r == rw.rank) base = n;
+      n += sh.mail.count[r];
     }
-    if (want_all) *row_mass = w_all;
-    else w_all = *row_mass;
+    if (MASS) {
+      w_all = 0;
+      for (int r = 0; r < rw.C; ++r) {
+        w_above += sh.mail.mass[r];
+        w_all += sh.mail.all[r];
+      }
+      if (want_all) {
+        *row_mass = w_all;
+        target = part_of(w_all, p);
+      }
+      if (w_above > target) return false;  // the boundary is above the bracket
+    } else {
+      n_above = above_n;
+    }
+    if (n <= kList) {
+      if (rw.rank > 0) {  // behind the leader's own, in any order
+        const int own = sh.mail.count[rw.rank];
+        uint64_t* to = rw.at(0)->sorted + base;
+        for (int i = tid; i < own; i += kThreadsF) to[i] = sh.sorted[i];
+      }
+      rw.sync();
+      if (n == 0) return false;
+      break;
+    }
+    rw.sync();
+    if (level == 2) return false;
+    x_from = x_band;
+    x_to = x_up;
+    top -= ((float)lo - 0.5f) / per_nat;
+    per_nat *= (float)(kBins - 2) / (float)(hi - lo + 1);
   }
-  if (n <= kList && rw.rank > 0) {  // behind the leader's own, in any order
-    const int own = sh.mail.count[rw.rank];
-    uint64_t* to = rw.at(0)->sorted + base;
-    for (int i = tid; i < own; i += kThreadsF) to[i] = sh.sorted[i];
-  }
-  rw.sync();
-  if (n <= 0 || n > kList) return false;
   if (rw.rank == 0) {
     bool ok = true;
     Cut found{0.f, kMaxIdx};
     sort_entries(n);
     if (MASS) {
-      const uint64_t target = part_of(w_all, p);
       // the boundary lies in the bracket: the mass above it is within the
       // target, that at its end is not
-      ok = w_above <= target && (target - w_above) < (1ull << (62 - rw.drop));
+      ok = (target - w_above) < (1ull << (62 - rw.drop));
       const uint64_t left = ok ? (target - w_above) << (rw.drop - kListDrop) : 0;
       uint64_t band;
       found = cut_by_mass(sh, rw.mass, n, left, -1.f, &band);
@@ -1031,7 +1071,7 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
                       (unsigned long long)rw.mass.of(z));
         }
     } else {
-      found = sorted_cut(sh, (int)(top_k - above_n) - 1);
+      found = sorted_cut(sh, (int)(top_k - n_above) - 1);
     }
     if (tid < rw.C) {
       rw.at(tid)->mail.cut = found;
@@ -1188,14 +1228,31 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float* gmax = a.group_max + (int64_t)row * rw.segs * kGroupsPerSeg;
   const int groups = rw.segs * kGroupsPerSeg;
+  const Bins bins(rw.m, kBinsPerNat);
   constexpr int kPer = kBins / kThreadsF;
+  constexpr int kHold = 8;  // neighbouring group maxima a thread holds: 4096 a round
+  auto hold = [&](int b, float (&g)[kHold]) {
+    const int i = b + tid * kHold;
+    float4 lo = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), hi = lo;
+    if (i < groups) {  // (a segment has 16 groups)
+      lo = *reinterpret_cast<const float4*>(gmax + i);
+      hi = *reinterpret_cast<const float4*>(gmax + i + 4);
+    }
+    g[0] = lo.x, g[1] = lo.y, g[2] = lo.z, g[3] = lo.w;
+    g[4] = hi.x, g[5] = hi.y, g[6] = hi.z, g[7] = hi.w;
+  };
+  float g[kHold];
+  hold(0, g);
 #pragma unroll
   for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kThreadsF] = 0;
   if (tid == 0) sh.hi = kBins - 1;
   __syncthreads();
-  for (int i = tid; i < groups; i += kThreadsF) {
-    const float x = gmax[i];
-    if (x > -INFINITY) atomicAdd(&sh.hist.own[bin_no(rw.bin_f(rw.mass.z(x)))], 1u);
+#pragma unroll 1
+  for (int b = 0; b < groups; b += kHold * kThreadsF) {
+    if (b > 0) hold(b, g);
+#pragma unroll
+    for (int q = 0; q < kHold; ++q)
+      if (g[q] > -INFINITY) atomicAdd(&sh.hist.own[bin_no(bins.bin_f(rw.mass.z(g[q])))], 1u);
   }
   __syncthreads();
   {
@@ -1219,54 +1276,59 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   if (warp == 0) {
     const float edge = kMagic + (float)sh.hi;
     const float x = least_logit(
-        rw.mass, [&](float z) { return z > -INFINITY && (any || rw.bin_f(z) <= edge); });
+        rw.mass, [&](float z) { return z > -INFINITY && (any || bins.bin_f(z) <= edge); });
     if (lane == 0) sh.least[0] = x;
   }
   __syncthreads();
   const float x_least = sh.least[0];
-  auto reaches = [&](float x) { return x >= x_least; };
   // the groups that reach it, in order
   int n_groups = 0;
   constexpr int kCap = (int)(sizeof(sh.groups) / sizeof(sh.groups[0]));
-  for (int b = 0; b < groups; b += kThreadsF) {
-    const int i = b + tid;
-    const bool in = i < groups && reaches(gmax[i]);
-    const unsigned mask = __ballot_sync(0xffffffffu, in);
-    if (lane == 0) sh.red_i[warp] = __popc(mask);
-    __syncthreads();
-    int at = n_groups, all = 0;
+#pragma unroll 1
+  for (int b = 0; b < groups; b += kHold * kThreadsF) {
+    if (groups > kHold * kThreadsF) hold(b, g);
+    int c = 0;
 #pragma unroll
-    for (int w = 0; w < kWarpsF; ++w) {
-      if (w < warp) at += sh.red_i[w];
-      all += sh.red_i[w];
-    }
-    at += __popc(mask & ((1u << lane) - 1));
-    if (in && at < kCap) sh.groups[at] = (uint16_t)i;
-    n_groups += all;
-    __syncthreads();
+    for (int q = 0; q < kHold; ++q) c += g[q] >= x_least;
+    uint64_t all;
+    int at = n_groups + (int)block_scan(sh, (uint64_t)c, &all);
+#pragma unroll
+    for (int q = 0; q < kHold; ++q)
+      if (g[q] >= x_least) {
+        if (at < kCap) sh.groups[at] = (uint16_t)(b + tid * kHold + q);
+        ++at;
+      }
+    n_groups += (int)all;
   }
-  if (n_groups > kCap || n_groups > kList) return false;
-  // a warp to a group, two elements a lane, in order; kAhead groups' loads at once
-  constexpr int kAhead = 8;
-  auto fetch = [&](int g0, float (&x)[kAhead][2]) {
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      const int g = g0 + q * kWarpsF;
-      const int p = g < n_groups ? (int)sh.groups[g] * kGroup + lane * 2 : rw.rd.V;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) x[q][e] = p + e < rw.rd.V ? elem(rw.rd.data[p + e]) : -INFINITY;
-    }
+  if (n_groups > kList) return false;
+  __syncthreads();
+  // a warp takes kVecGroups groups with one 16-byte load a lane, in order
+  constexpr int kLanes = kGroup / RowData<T>::N, kVecGroups = 32 / kLanes;
+  const int rounds = (n_groups + kVecGroups - 1) / kVecGroups;
+  uint16_t* before = reinterpret_cast<uint16_t*>(sh.seg_w);  // candidates of each round
+  static_assert(sizeof(sh.seg_w) >= kList * sizeof(uint16_t), "a count for every round");
+  auto place = [&](int r) {
+    const int g = r * kVecGroups + lane / kLanes;
+    return g < n_groups ? (int)sh.groups[g] * kGroup + (lane % kLanes) * RowData<T>::N : rw.rd.V;
   };
-  uint16_t* before = reinterpret_cast<uint16_t*>(sh.seg_w);  // candidates of each group
-  static_assert(sizeof(sh.seg_w) >= kList * sizeof(uint16_t), "a count for every listed group");
-  for (int g0 = warp; g0 < n_groups; g0 += kWarpsF * kAhead) {
-    float x[kAhead][2];
-    fetch(g0, x);
+  auto taken = [&](const uint4& v) {
+    float x[RowData<T>::N];
+    Vec<T>::unpack(v, x);
+    unsigned take = 0;
+#pragma unroll
+    for (int e = 0; e < RowData<T>::N; ++e) take |= x[e] >= x_least ? 1u << e : 0u;
+    return take;
+  };
+  constexpr int kAhead = 4;
+#pragma unroll 1
+  for (int r0 = warp; r0 < rounds; r0 += kWarpsF * kAhead) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) v[q] = rw.rd.raw(place(r0 + q * kWarpsF));
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
-      const int c = __popc(__ballot_sync(0xffffffffu, reaches(x[q][0]))) +
-                    __popc(__ballot_sync(0xffffffffu, reaches(x[q][1])));
-      if (lane == 0 && g0 + q * kWarpsF < n_groups) before[g0 + q * kWarpsF] = (uint16_t)c;
+      const int c = warp_sum_i(__popc(taken(v[q])));
+      if (lane == 0 && r0 + q * kWarpsF < rounds) before[r0 + q * kWarpsF] = (uint16_t)c;
     }
   }
   __syncthreads();
@@ -1276,40 +1338,40 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
     uint64_t sum = 0;
 #pragma unroll
     for (int q = 0; q < kListPerThread; ++q) {
-      const int g = tid * kListPerThread + q;
-      c[q] = g < n_groups ? before[g] : 0;
+      const int r = tid * kListPerThread + q;
+      c[q] = r < rounds ? before[r] : 0;
       sum += c[q];
     }
     uint64_t b = block_scan(sh, sum, &n64);
     if (n64 > (uint64_t)kList) return false;
 #pragma unroll
     for (int q = 0; q < kListPerThread; ++q) {
-      const int g = tid * kListPerThread + q;
-      if (g < n_groups) before[g] = (uint16_t)b;
+      const int r = tid * kListPerThread + q;
+      if (r < rounds) before[r] = (uint16_t)b;
       b += c[q];
     }
   }
   const int n = (int)n64;
   __syncthreads();
   List& list = sh.list;
-  for (int g0 = warp; g0 < n_groups; g0 += kWarpsF * kAhead) {
-    float x[kAhead][2];
-    fetch(g0, x);
+#pragma unroll 1
+  for (int r0 = warp; r0 < rounds; r0 += kWarpsF * kAhead) {
+    unsigned take[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) take[q] = taken(rw.rd.raw(place(r0 + q * kWarpsF)));
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
-      const int g = g0 + q * kWarpsF;
-      const bool in[2] = {reaches(x[q][0]), reaches(x[q][1])};
-      const unsigned m0 = __ballot_sync(0xffffffffu, in[0]), m1 = __ballot_sync(0xffffffffu, in[1]);
-      if (g >= n_groups) continue;
-      const unsigned below = (1u << lane) - 1;
-      int at = before[g] + __popc(m0 & below) + __popc(m1 & below);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (in[e]) {
-          list.key[at] = ord_key(rw.mass.z(x[q][e]));
-          list.idx[at] = (int)sh.groups[g] * kGroup + lane * 2 + e;
-          ++at;
-        }
+      const int c = __popc(take[q]);
+      const int inc = warp_scan(c);
+      if (r0 + q * kWarpsF >= rounds) break;
+      int at = before[r0 + q * kWarpsF] + inc - c;
+      const int p = place(r0 + q * kWarpsF);
+#pragma unroll 1
+      for (unsigned t = take[q]; t; t &= t - 1, ++at) {
+        const int j = p + __ffs(t) - 1;
+        list.key[at] = ord_key(rw.mass.z(elem(rw.rd.data[j])));
+        list.idx[at] = j;
+      }
     }
   }
   __syncthreads();
