@@ -41,7 +41,7 @@ constexpr int kGroupsPerSeg = kSeg / kGroup;
 constexpr int kMaxSegs = 1024;      // of a row: V <= 2^20
 constexpr int kMaxCtas = 16;        // CTAs that finish a row
 constexpr int kBins = 4096;
-constexpr float kBinsPerNat = 128.f;  // linear bins: 32 nats below the maximum, then one for all
+constexpr float kBinsPerLogit = 128.f;  // linear bins: 32 logits below the maximum, then one for all
 constexpr int kList = 2048;         // candidates a row's leader CTA holds
 constexpr int kListTopK = 1024;     // largest top-k taken from group maxima
 constexpr int kListPerThread = kList / kThreadsF;
@@ -457,6 +457,10 @@ struct Bins {
   // kMagic + the number of the bin, as a float
   __device__ __forceinline__ float bin_f(float z) const { return __fadd_rn(dist(z), kMagic); }
 };
+// Bins of a fixed width in logits, whatever the temperature.
+__device__ __forceinline__ float per_nat_of(float inv_t) {
+  return fminf(fmaxf(kBinsPerLogit / inv_t, 1e-30f), 1e30f);
+}
 __device__ __forceinline__ int bin_no(float bin_f) {
   return __float_as_int(bin_f) - __float_as_int(kMagic);
 }
@@ -839,7 +843,9 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
   const bool plain = cut.idx == kMaxIdx;  // a threshold on the logits says it all
   const float x_cut = sh.least[0];
   float x_from = x_cut, x_to = INFINITY;  // the bracket: x_from <= x < x_to
-  float top = rw.m, per_nat = kBinsPerNat;
+  // (by mass: bins narrow enough for the quadratic below)
+  float top = rw.m, per_nat = per_nat_of(rw.mass.inv_t);
+  if (MASS) per_nat = fmaxf(per_nat, 16.f);
   uint64_t target = MASS && *row_mass ? part_of(*row_mass, p) : 0;
   uint64_t w_above = 0;  // mass above the bracket
   uint64_t n_above = 0;  // (by count) elements above it
@@ -1044,11 +1050,12 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
       break;
     }
     rw.sync();
-    if (level == 2) return false;
+    if (level == 3) return false;
     x_from = x_band;
     x_to = x_up;
     top -= ((float)lo - 0.5f) / per_nat;
-    per_nat *= (float)(kBins - 2) / (float)(hi - lo + 1);
+    // (the last bin has no end: the next bins begin where it does)
+    if (hi < kBins - 1) per_nat *= (float)(kBins - 2) / (float)(hi - lo + 1);
   }
   if (rw.rank == 0) {
     bool ok = true;
@@ -1228,7 +1235,7 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float* gmax = a.group_max + (int64_t)row * rw.segs * kGroupsPerSeg;
   const int groups = rw.segs * kGroupsPerSeg;
-  const Bins bins(rw.m, kBinsPerNat);
+  const Bins bins(rw.m, per_nat_of(rw.mass.inv_t));
   constexpr int kPer = kBins / kThreadsF;
   constexpr int kHold = 8;  // neighbouring group maxima a thread holds: 4096 a round
   auto hold = [&](int b, float (&g)[kHold]) {
