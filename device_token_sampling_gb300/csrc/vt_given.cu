@@ -412,15 +412,15 @@ template <typename T>
 struct Row {
   RowData<T> rd;
   Mass mass;
-  float m;      // tempered maximum
+  float mx, m;  // maximum, tempered maximum
   int segs;     // of the row
   int drop;     // row sums are in units of 2^(E - kElemBits + drop)
   int C, rank;  // the team
   int s0, s1;   // this CTA's segments
   int per;      // segments to a CTA
-  __device__ __forceinline__ Row(const RowData<T>& rd_, const Mass& mass_, float m_, int segs_,
-                                 int drop_, int C_, int rank_)
-      : rd(rd_), mass(mass_), m(m_), segs(segs_), drop(drop_), C(C_), rank(rank_) {
+  __device__ __forceinline__ Row(const RowData<T>& rd_, const Mass& mass_, float mx_, float m_,
+                                 int segs_, int drop_, int C_, int rank_)
+      : rd(rd_), mass(mass_), mx(mx_), m(m_), segs(segs_), drop(drop_), C(C_), rank(rank_) {
     per = (segs + C - 1) / C;
     s0 = min(segs, rank * per);
     s1 = min(segs, s0 + per);
@@ -443,24 +443,21 @@ struct Row {
   __device__ __forceinline__ float seg_top(int s) const { return mass.z(smem().seg_max[s]); }
 };
 
-// Linear bins, per_nat to a unit below `top`; values above it go to bin 0.
+// Linear bins of the logits below `top` (no logit above it is asked for): a fixed
+// number to a logit, whatever the temperature.
 struct Bins {
-  float per_nat, top_bins;
-  __device__ __forceinline__ Bins(float top, float per_nat_) {
-    per_nat = per_nat_;
-    top_bins = __fmul_rn(top, per_nat_);
+  float per, top_bins;
+  __device__ __forceinline__ Bins(float top, float per_) {
+    per = per_;
+    top_bins = __fmul_rn(top, per_);
   }
-  // distance below the top in bins; monotone in z
-  __device__ __forceinline__ float dist(float z) const {
-    return fminf(fmaxf(__fmaf_rn(z, -per_nat, top_bins), 0.f), (float)(kBins - 1));
+  // distance below the top in bins
+  __device__ __forceinline__ float dist(float x) const { return __fmaf_rn(x, -per, top_bins); }
+  // kMagic + the number of the bin, as a float; the last bin has no end
+  __device__ __forceinline__ float bin_f(float x) const {
+    return __fadd_rn(fminf(dist(x), (float)(kBins - 1)), kMagic);
   }
-  // kMagic + the number of the bin, as a float
-  __device__ __forceinline__ float bin_f(float z) const { return __fadd_rn(dist(z), kMagic); }
 };
-// Bins of a fixed width in logits, whatever the temperature.
-__device__ __forceinline__ float per_nat_of(float inv_t) {
-  return fminf(fmaxf(kBinsPerLogit / inv_t, 1e-30f), 1e30f);
-}
 __device__ __forceinline__ int bin_no(float bin_f) {
   return __float_as_int(bin_f) - __float_as_int(kMagic);
 }
@@ -818,15 +815,14 @@ __device__ __forceinline__ Cut cut_by_mass(Shared& sh, const Mass& mass, int n, 
 // it closer and closer, and a list of the elements in the bracket, once it holds
 // them.  One histogram over the row nearly always does; the masses above a
 // bracket are summed exactly before the next is made of it.
-//   MASS: the boundary of the top-p share `p` of *row_mass, the mass of all
-//   elements kept by `cut` (row units; 0: not known yet, and set here).  On
-//   success the CTAs' seg_w hold the masses of the kept elements (element units).
-//   else: the first `top_k` are kept.
+//   MASS: elements are kept while the mass before them is <= target (row units).
+//   On success the CTAs' seg_w hold the masses of the kept elements (element units).
+//   else: the first `target` of them are kept.
+// PLAIN: `cut` has no index, so that a threshold on the logits says it all.
 // Returns false (the same in every CTA) when too many elements are equal, or, by
 // mass, when a bracket turns out not to hold the boundary.
-template <typename T, bool MASS>
-__device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, float p, int top_k,
-                                         uint64_t* row_mass) {
+template <typename T, bool MASS, bool PLAIN>
+__device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint64_t target) {
   Row<T> rw = row_in;  // in registers
   rw.mass.table = smem().table;
   using RD = RowData<T>;
@@ -840,19 +836,17 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
     if (lane == 0) sh.least[0] = x;
   }
   __syncthreads();
-  const bool plain = cut.idx == kMaxIdx;  // a threshold on the logits says it all
-  const float x_cut = sh.least[0];
-  float x_from = x_cut, x_to = INFINITY;  // the bracket: x_from <= x < x_to
+  float x_from = sh.least[0], x_to = INFINITY;  // the bracket: x_from <= x < x_to
   // (by mass: bins narrow enough for the quadratic below)
-  float top = rw.m, per_nat = per_nat_of(rw.mass.inv_t);
-  if (MASS) per_nat = fmaxf(per_nat, 16.f);
-  uint64_t target = MASS && *row_mass ? part_of(*row_mass, p) : 0;
-  uint64_t w_above = 0;  // mass above the bracket
-  uint64_t n_above = 0;  // (by count) elements above it
+  float per = MASS ? fmaxf(kBinsPerLogit, 16.f * rw.mass.inv_t) : kBinsPerLogit;
+  // (edges off the grid that bf16 logits lie on: a value on an edge would fall
+  // to either side)
+  float top = rw.mx + 0.3f / per;
+  uint64_t above = 0;  // mass (or elements) above the bracket
   int n = 0;
 #pragma unroll 1
   for (int level = 0;; ++level) {
-    const Bins bins(top, per_nat);
+    const Bins bins(top, per);
 #pragma unroll
     for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kThreadsF] = 0;
     if (tid == 0) {
@@ -862,23 +856,25 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
     __syncthreads();
     // by mass: each element adds its mass relative to its bin's middle in units of
     // 1/4063, so a bin's mass is known to within 1.3e-4 of itself
-    const float c1 = -4063.f / per_nat, c2 = 4063.f * 0.5f / (per_nat * per_nat);
+    const float nats = rw.mass.inv_t / per;  // to a bin
+    const float c1 = -4063.f * nats, c2 = 4063.f * 0.5f * nats * nats;
     for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
       if (sh.seg_max[s] < x_from) continue;
       each_vector(rw.rd, s, [&](const float(&x)[RD::N], int at) {
 #pragma unroll
         for (int e = 0; e < RD::N; ++e) {
-          const float z = rw.mass.z(x[e]);
-          const float t = bins.dist(z);
-          const float b = __fadd_rn(t, kMagic);
-          uint32_t add = 1;
-          if (MASS) {  // 4063 e^(-f / per_nat), f in [-1/2, 1/2], through a rounding by 2^23
+          const float t = bins.dist(x[e]);
+          bool in = x[e] >= x_from && x[e] < x_to;
+          if (!PLAIN) in = in && cut.keeps(rw.mass.z(x[e]), at + e);
+          if (MASS) {  // 4063 e^(-f nats), f in [-1/2, 1/2], through a rounding by 2^23
+            const float b = __fadd_rn(t, kMagic);
             const float f = __fsub_rn(t, __fsub_rn(b, kMagic));
-            add = __float_as_uint(__fmaf_rn(f, __fmaf_rn(f, c2, c1), 8388608.f + 4063.f)) & 0x1fffu;
+            const uint32_t add =
+                __float_as_uint(__fmaf_rn(f, __fmaf_rn(f, c2, c1), 8388608.f + 4063.f)) & 0x1fffu;
+            if (in && t < (float)(kBins - 1)) atomicAdd(&sh.hist.own[max(bin_no(b), 0)], add);
+          } else {
+            if (in) atomicAdd(&sh.hist.own[max(bin_no(bins.bin_f(x[e])), 0)], 1u);
           }
-          if (x[e] >= x_from && x[e] < x_to && (plain || cut.keeps(z, at + e)) &&
-              !(MASS && t >= (float)(kBins - 1)))
-            atomicAdd(&sh.hist.own[bin_no(b)], add);
         }
       });
     }
@@ -901,28 +897,24 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
     uint32_t cn[kPer];
 #pragma unroll
     for (int q = 0; q < kPer; ++q) cn[q] = from[tid * kPer + q];
-    uint64_t above_n = 0;
     if (MASS) {
       float cf[kPer], tf = 0.f;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
-        cf[q] = (float)cn[q] * ex2_approx((float)(tid * kPer + q) * (-kLog2e / per_nat));
+        cf[q] = (float)cn[q] * ex2_approx((float)(tid * kPer + q) * (-kLog2e * nats));
         tf += cf[q];
       }
       const float inc = warp_scan(tf);
       if (lane == 31) sh.red_f[warp] = inc;
       __syncthreads();
-      float a = inc - tf, all = 0.f;
-      for (int i = 0; i < kWarpsF; ++i) {
+      float a = inc - tf;
+      for (int i = 0; i < kWarpsF; ++i)
         if (i < warp) a += sh.red_f[i];
-        all += sh.red_f[i];
-      }
       constexpr float kSlack = 1.f / 6144;  // of the bins' masses and their fp32 sums
       // the target in the histogram's units (4063 of the mass at `top`)
-      const float want =
-          target ? __ull2float_rn(target - w_above) * 4063.f /
-                       (__ull2float_rn(rw.mass.of(top)) * exp2f((float)-rw.drop))
-                 : p * all;
+      const float want = __ull2float_rn(target - above) * 4063.f /
+                         exp2f(__fmaf_rn(rw.mass.z(top) - rw.mass.c, kLog2e,
+                                         (float)(kElemBits - rw.drop - rw.mass.E())));
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
         if (cn[q] > 0) {
@@ -937,50 +929,47 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
       uint64_t tn = 0, unused;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) tn += cn[q];
-      uint64_t a = n_above + block_scan(sh, tn, &unused);
+      uint64_t a = above + block_scan(sh, tn, &unused);
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
-        if (a < (uint64_t)top_k && a + cn[q] >= (uint64_t)top_k) {
-          sh.lo = sh.hi = tid * kPer + q;
-          sh.above = a;
-        }
+        if (a < target && a + cn[q] >= target) sh.lo = sh.hi = tid * kPer + q;
         a += cn[q];
       }
     }
     __syncthreads();
     const int lo = sh.lo, hi = sh.hi;
-    if (!MASS) above_n = sh.above;
     if (lo > hi) return false;  // (a histogram without mass)
 
-    // the masses above the new bracket, and its elements into this CTA's entries;
-    // segments that end below it are not read, unless the mass of all is wanted
-    const bool want_all = MASS && target == 0;
+    // the new bracket, by tempered values: the elements from the far edge of bin
+    // hi up to the near edge of bin lo
+    const float near = top - ((float)lo - 0.5f) / per, far = top - ((float)hi + 0.5f) / per;
     if (warp == 1 || warp == 2) {
-      const float edge = kMagic + (float)(warp == 1 ? lo - 1 : hi);
-      const float x = least_logit(rw.mass, [&](float z) { return bins.bin_f(z) <= edge; });
+      const float edge = rw.mass.z(warp == 1 ? near : far);
+      const float x = least_logit(rw.mass, [&](float z) { return z > edge; });
       if (lane == 0) sh.least[warp] = x;
     }
     if (tid == 0) sh.bin = 0;  // entries so far
     __syncthreads();
-    // (bin 0 has no element above it, the last bin none below)
     const float x_up = lo == 0 ? x_to : fminf(fmaxf(sh.least[1], x_from), x_to);
     const float x_band = hi == kBins - 1 ? x_from : fmaxf(sh.least[2], x_from);
-    uint64_t w_more = 0, w_all = 0;
+    // the masses (or number) above it, and its elements into this CTA's entries;
+    // segments that end below it are not read
+    uint64_t more = 0;
     for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
-      uint64_t above = 0, rest = 0;
-      if (sh.seg_max[s] >= (want_all ? x_cut : x_band)) {
+      uint64_t up_w = 0;
+      if (sh.seg_max[s] >= x_band) {
         each_vector(rw.rd, s, [&](const float(&x)[RD::N], int at) {
           unsigned take = 0;
 #pragma unroll
           for (int e = 0; e < RD::N; ++e) {
             const float z = rw.mass.z(x[e]);
-            const bool in = x[e] < x_to && (plain || cut.keeps(z, at + e));
+            bool in = x[e] < x_to;
+            if (!PLAIN) in = in && cut.keeps(z, at + e);
             const bool up = x[e] >= x_up && in;
             take |= x[e] >= x_band && in && !up ? 1u << e : 0u;
-            if (MASS) {  // (a select, not a branch: the eight masses overlap)
-              above = rw.mass.add(above, up ? z : -INFINITY);
-              if (want_all) rest = rw.mass.add(rest, x[e] >= x_cut && in ? z : -INFINITY);
-            }
+            // (a select, not a branch: the masses of a vector overlap)
+            if (MASS) up_w = rw.mass.add(up_w, up ? z : -INFINITY);
+            else up_w += up;
           }
           if (!__any_sync(0xffffffffu, take)) return;
           const int c = __popc(take);
@@ -997,48 +986,26 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
             }
           }
         });
-        if (MASS) above = warp_sum_u64(above);
-        if (want_all) rest = warp_sum_u64(rest);
+        up_w = warp_sum_u64(up_w);
       }
-      if (MASS && lane == 0) {
-        sh.seg_w[s] = level > 0 ? sh.seg_w[s] + above : above;
-        w_more += rw.coarse(above);
-        w_all += rw.coarse(rest);
+      if (lane == 0) {
+        if (MASS) sh.seg_w[s] = level > 0 ? sh.seg_w[s] + up_w : up_w;
+        more += MASS ? rw.coarse(up_w) : up_w;
       }
     }
-    if (MASS && lane == 0) {
-      sh.red_w[warp] = w_more;
-      sh.red_n[warp] = w_all;
-    }
+    if (lane == 0) sh.red_w[warp] = more;
     __syncthreads();
     rw.send(&Mail::count, sh.bin);
-    if (MASS && warp == 0) {
-      w_more = warp_sum_u64(lane < kWarpsF ? sh.red_w[lane] : 0);
-      w_all = warp_sum_u64(lane < kWarpsF ? sh.red_n[lane] : 0);
-      rw.send(&Mail::mass, w_more);
-      rw.send(&Mail::all, w_all);
-    }
+    if (warp == 0) rw.send(&Mail::mass, (uint64_t)warp_sum_u64(lane < kWarpsF ? sh.red_w[lane] : 0));
     rw.sync();
     n = 0;
     int base = 0;
     for (int r = 0; r < rw.C; ++r) {
       if (r == rw.rank) base = n;
       n += sh.mail.count[r];
+      above += sh.mail.mass[r];
     }
-    if (MASS) {
-      w_all = 0;
-      for (int r = 0; r < rw.C; ++r) {
-        w_above += sh.mail.mass[r];
-        w_all += sh.mail.all[r];
-      }
-      if (want_all) {
-        *row_mass = w_all;
-        target = part_of(w_all, p);
-      }
-      if (w_above > target) return false;  // the boundary is above the bracket
-    } else {
-      n_above = above_n;
-    }
+    if (MASS ? above > target : above >= target) return false;  // the boundary is above it
     if (n <= kList) {
       if (rw.rank > 0) {  // behind the leader's own, in any order
         const int own = sh.mail.count[rw.rank];
@@ -1053,9 +1020,9 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
     if (level == 3) return false;
     x_from = x_band;
     x_to = x_up;
-    top -= ((float)lo - 0.5f) / per_nat;
+    top = fminf(near, top);
     // (the last bin has no end: the next bins begin where it does)
-    if (hi < kBins - 1) per_nat *= (float)(kBins - 2) / (float)(hi - lo + 1);
+    if (hi < kBins - 1) per *= (float)(kBins - 2) / (float)(hi - lo + 1);
   }
   if (rw.rank == 0) {
     bool ok = true;
@@ -1064,8 +1031,8 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
     if (MASS) {
       // the boundary lies in the bracket: the mass above it is within the
       // target, that at its end is not
-      ok = (target - w_above) < (1ull << (62 - rw.drop));
-      const uint64_t left = ok ? (target - w_above) << (rw.drop - kListDrop) : 0;
+      ok = (target - above) < (1ull << (62 - rw.drop));
+      const uint64_t left = ok ? (target - above) << (rw.drop - kListDrop) : 0;
       uint64_t band;
       found = cut_by_mass(sh, rw.mass, n, left, -1.f, &band);
       ok = ok && left < band;
@@ -1078,7 +1045,8 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, floa
                       (unsigned long long)rw.mass.of(z));
         }
     } else {
-      found = sorted_cut(sh, (int)(top_k - n_above) - 1);
+      ok = target - above <= (uint64_t)n;
+      found = sorted_cut(sh, ok ? (int)(target - above) - 1 : 0);
     }
     if (tid < rw.C) {
       rw.at(tid)->mail.cut = found;
@@ -1156,7 +1124,6 @@ __device__ uint64_t sum_segments(Row<T>& rw, uint64_t* before, uint64_t* own) {
 template <typename T>
 __device__ int find_draw(const Row<T>& rw, const Cut& cut, uint64_t t, float* z_out) {
   using RD = RowData<T>;
-  const int lane = threadIdx.x & 31;
   int lo = rw.s0, hi = rw.s1 - 1;  // the first segment whose inclusive mass exceeds t
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -1235,7 +1202,7 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float* gmax = a.group_max + (int64_t)row * rw.segs * kGroupsPerSeg;
   const int groups = rw.segs * kGroupsPerSeg;
-  const Bins bins(rw.m, per_nat_of(rw.mass.inv_t));
+  const Bins bins(rw.mx, kBinsPerLogit);
   constexpr int kPer = kBins / kThreadsF;
   constexpr int kHold = 8;  // neighbouring group maxima a thread holds: 4096 a round
   auto hold = [&](int b, float (&g)[kHold]) {
@@ -1259,7 +1226,7 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
     if (b > 0) hold(b, g);
 #pragma unroll
     for (int q = 0; q < kHold; ++q)
-      if (g[q] > -INFINITY) atomicAdd(&sh.hist.own[bin_no(bins.bin_f(rw.mass.z(g[q])))], 1u);
+      if (g[q] > -INFINITY) atomicAdd(&sh.hist.own[max(bin_no(bins.bin_f(g[q])), 0)], 1u);
   }
   __syncthreads();
   {
@@ -1281,9 +1248,10 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   // (fewer than top_k groups with a finite element: every finite element)
   const bool any = sh.hi == kBins - 1;
   if (warp == 0) {
-    const float edge = kMagic + (float)sh.hi;
-    const float x = least_logit(
-        rw.mass, [&](float z) { return z > -INFINITY && (any || bins.bin_f(z) <= edge); });
+    // (the far edge of that bin, a little further: a superset will do)
+    const float edge =
+        any ? -INFINITY : rw.mass.z(rw.mx - ((float)sh.hi + 0.51f) / kBinsPerLogit);
+    const float x = least_logit(rw.mass, [&](float z) { return z > edge; });
     if (lane == 0) sh.least[0] = x;
   }
   __syncthreads();
@@ -1473,7 +1441,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
   }
   const Mass mass(P.inv_t, m, sh.table);
   const RowData<T> rd{static_cast<const T*>(a.logits) + row * a.ld, a.V, a.aligned != 0};
-  Row<T> rw(rd, mass, m, a.segs, a.drop, team ? ctas : 1, team ? rank : 0);
+  Row<T> rw(rd, mass, mx, m, a.segs, a.drop, team ? ctas : 1, team ? rank : 0);
 
   // ln sum exp(z - m) from the segments' sums; masses to element units of the row
   float ln_s = 0.f;
@@ -1566,20 +1534,23 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
     rw.sync();
     int n = 0;
     for (int r = 0; r < rw.C; ++r) n += sh.mail.total[r];
-    if (n > P.top_k && !band_select<T, false>(rw, &cut, 0.f, P.top_k, nullptr))
+    if (n > P.top_k && !band_select<T, false, true>(rw, &cut, (uint64_t)P.top_k))
       cut = radix_select<T, false>(rw, cut, (uint64_t)P.top_k);
   }
   uint64_t before, mine, W;
   if (P.flags & kRowTopP) {
+    if (all == 0) {  // the mass of what top-p is a share of
+      kept_mass(rw, cut);
+      all = sum_segments(rw, &before, &mine);
+      if (masses) ln_s = mass.ln_sum(all, kElemBits - a.drop, m);
+    }
     const Cut from = cut;
-    uint64_t row_mass = all;
-    if (!band_select<T, true>(rw, &cut, P.top_p, 0, &row_mass)) {
-      kept_mass(rw, from);
-      row_mass = sum_segments(rw, &before, &mine);
-      cut = radix_select<T, true>(rw, from, part_of(row_mass, P.top_p));
+    const uint64_t target = part_of(all, P.top_p);
+    if (!(cut.idx == kMaxIdx ? band_select<T, true, true>(rw, &cut, target)
+                             : band_select<T, true, false>(rw, &cut, target))) {
+      cut = radix_select<T, true>(rw, from, target);
       kept_mass(rw, cut);
     }
-    if (masses && !usable) ln_s = mass.ln_sum(row_mass, kElemBits - a.drop, m);
     W = sum_segments(rw, &before, &mine);
   } else {
     if (!usable) kept_mass(rw, cut);
