@@ -79,11 +79,19 @@ bool config_ok(const vt_paged_config& c) {
 void plan_attention(const vt_paged* h, int B, int prefix_len, int max_len, vt::AttnArgs& a) {
   const int want = 4 * h->num_sms;
   const int64_t rows = (int64_t)B * a.hq;
-  a.prefix_tiles = (int)ceil_div((int64_t)B * a.G, 16);
+  // more than one 16-row tile of rows behind the prefix: the tensor-memory kernel,
+  // 256 rows to a CTA, one CTA to an SM (below, that kernel would pad 128-row tiles)
+  a.prefix_mma = prefix_len > 0 && (int64_t)B * a.G > 16 && vt::prefix_mma_takes(a);
+  a.prefix_tiles = (int)ceil_div((int64_t)B * a.G, a.prefix_mma ? 128 : 16);
   a.own_tiles = (int)ceil_div(a.G, 16);
   const int64_t own_len = std::max(1, max_len - (prefix_len & ~15));
   int64_t sp = 0, so;
-  if (prefix_len > 0)
+  const int step = a.prefix_mma ? 128 : 64;  // tokens a split is a multiple of
+  if (a.prefix_mma)
+    // splits so that the grid is one round of CTAs
+    sp = std::clamp<int64_t>(h->num_sms / std::max<int64_t>(1, ceil_div(a.prefix_tiles, 2) * a.hkv),
+                             1, std::min<int64_t>(64, ceil_div(prefix_len, step)));
+  else if (prefix_len > 0)
     sp = std::clamp<int64_t>(ceil_div(want, (int64_t)a.prefix_tiles * a.hkv), 1,
                              std::min<int64_t>(64, ceil_div(prefix_len, 64)));
   so = std::clamp<int64_t>(ceil_div(want, (int64_t)a.own_tiles * a.hkv * B), 1,
@@ -94,7 +102,7 @@ void plan_attention(const vt_paged* h, int B, int prefix_len, int max_len, vt::A
   }
   a.prefix_splits = a.prefix_chunk = 0;
   if (sp > 0) {
-    a.prefix_chunk = (int)ceil_div(ceil_div(prefix_len, sp), 64) * 64;
+    a.prefix_chunk = (int)ceil_div(ceil_div(prefix_len, sp), step) * step;
     a.prefix_splits = (int)ceil_div(prefix_len, a.prefix_chunk);
   }
   a.own_splits = (int)so;

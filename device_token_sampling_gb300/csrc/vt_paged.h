@@ -53,7 +53,8 @@ struct AttnArgs {
   int32_t B, hq, hkv, G;       // G = hq / hkv
   float scale_log2;            // scale * log2(e)
   // the work: prefix units first, then the requests' own units
-  int32_t prefix_tiles;        // row tiles of one kv head's B * G rows
+  int32_t prefix_mma;          // the prefix runs on prefix_kernel, 128 rows to a tile
+  int32_t prefix_tiles;        // row tiles (16 or 128 rows) of one kv head's B * G rows
   int32_t prefix_splits, prefix_chunk;  // splits of [0, prefix_len), tokens in each
   int32_t own_tiles;           // 16-row tiles of G heads
   int32_t own_splits, own_chunk;
@@ -66,5 +67,9 @@ struct AttnArgs {
 // dtype as VT_DTYPE_BF16 / VT_DTYPE_F16; head_dim 64 or 128.
 cudaError_t launch_prefix_attention(const AttnArgs& a, int dtype, int head_dim,
                                     cudaStream_t stream);
+// The prefix's part of it (vt_prefix_mma.cu): whether its layout can be taken, and
+// the launch.
+bool prefix_mma_takes(const AttnArgs& a);
+cudaError_t launch_prefix_mma(const AttnArgs& a, int dtype, int head_dim, cudaStream_t stream);
 
 }  // namespace vt

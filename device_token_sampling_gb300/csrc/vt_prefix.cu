@@ -9,6 +9,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "vt_device.cuh"
 #include "vt_paged.h"
 #include "vt_sampler.h"
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(AttnArgs a) {
 
   // which unit
   int u = blockIdx.x;
-  const int n_prefix_units = a.prefix_tiles * a.hkv * a.prefix_splits;
+  const int n_prefix_units = a.prefix_mma ? 0 : a.prefix_tiles * a.hkv * a.prefix_splits;
   const bool prefix = u < n_prefix_units;
   int kvh, tile, split, b0 = 0, t0, t1;
   const int32_t* table;
@@ -394,7 +396,11 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(split_kernel<T, D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
-  const int64_t units = (int64_t)a.prefix_tiles * a.hkv * a.prefix_splits +
+  if (a.prefix_mma &&
+      (e = launch_prefix_mma(a, std::is_same<T, __half>::value ? VT_DTYPE_F16 : VT_DTYPE_BF16, D,
+                             stream)) != cudaSuccess)
+    return e;
+  const int64_t units = (a.prefix_mma ? 0 : (int64_t)a.prefix_tiles * a.hkv * a.prefix_splits) +
                         (int64_t)a.own_tiles * a.hkv * a.B * a.own_splits;
   split_kernel<T, D><<<(unsigned)units, kSplitWarps * 32, S::kBytes, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

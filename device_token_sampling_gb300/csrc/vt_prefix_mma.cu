@@ -1,0 +1,574 @@
+// vt_prefix_mma.cu -- the shared prefix on the 5th-generation tensor cores.
+//
+// The rows of a kv head, B * G query heads against one prefix, are a matrix
+// product S = Q K^T, a softmax, and a product P V.  A CTA takes up to 256 rows
+// (two tiles of 128) and one split of the prefix, 128 tokens at a time:
+//   - the load warp brings K and V tiles by TMA, block by block of the cache,
+//     into two-stage rings of 128-byte-swizzled shared memory;
+//   - one thread issues the MMAs: S_t = Q_t K^T into tensor memory, O_t += P_t V
+//     with P_t read from tensor memory and V as it lies (token-major);
+//   - a warpgroup per tile, one thread to a row, turns S into weights: running
+//     maximum and sum in registers, P back to tensor memory in the cache's type.
+// The tiles are out of step by half a period (S_0, P_1 V, S_1, P_0 V), so that one
+// tile's exponentials run under the other's products.  The accumulators are
+// rescaled only when a row's maximum has grown by more than 2^8 since the last
+// time; sums and accumulators stay far inside fp32.
+// What bounds it: the exponentials and the products take the same time (128 x 128
+// each: 1024 cycles of the special function units, 1024 of the tensor cores).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "vt_device.cuh"
+#include "vt_paged.h"
+#include "vt_sampler.h"
+
+namespace vt {
+namespace {
+
+constexpr int kTileRows = 128;
+constexpr int kTileTokens = 128;
+constexpr int kKvStages = 2;
+constexpr int kMmaThreads = 320;  // two softmax warpgroups, the MMA warp, the load warp
+constexpr int kMaskRing = 8;      // tiles whose token masks are kept
+constexpr float kGrowth = 8.f;    // log2 units a maximum may grow before a rescaling
+
+template <int D>
+struct MmaSmem {
+  static constexpr int kHalf = kTileRows * 128;            // 128 rows of 64 elements
+  static constexpr int kTile = (D / 64) * kHalf;           // bytes of a Q, K or V tile
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + 2 * kTile;
+  static constexpr int kV = kK + kKvStages * kTile;
+  static constexpr int kBytes = kV + kKvStages * kTile + 1024;  // room to align to 1024
+};
+
+// tensor memory columns: S of both tiles, O of both; P in S's own columns where
+// there is no room beside them (head_dim 128)
+template <int D>
+struct Tmem {
+  static constexpr int kS = 0, kO = 2 * kTileTokens;
+  static constexpr bool kShared = D > 64;
+  static constexpr int kP = kShared ? 0 : kO + 2 * D;
+  static constexpr int kPStep = kShared ? kTileTokens : kTileTokens / 2;
+};
+
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  // start address, leading and stride byte offsets in 16-byte units; descriptor
+  // version 1; 128-byte swizzle
+  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lbo >> 4) << 16) |
+         ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+#define VT_R8(r, i)                                                                       \
+  "=r"((r)[i]), "=r"((r)[i + 1]), "=r"((r)[i + 2]), "=r"((r)[i + 3]), "=r"((r)[i + 4]),   \
+      "=r"((r)[i + 5]), "=r"((r)[i + 6]), "=r"((r)[i + 7])
+#define VT_I8(r, i)                                                                   \
+  "r"((r)[i]), "r"((r)[i + 1]), "r"((r)[i + 2]), "r"((r)[i + 3]), "r"((r)[i + 4]),    \
+      "r"((r)[i + 5]), "r"((r)[i + 6]), "r"((r)[i + 7])
+// 32 columns of this thread's lane
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+      "%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : VT_R8(r, 0), VT_R8(r, 8), VT_R8(r, 16), VT_R8(r, 24)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+      "%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      VT_I8(r, 0), VT_I8(r, 8), VT_I8(r, 16), VT_I8(r, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Registers that a load has filled are not used before this point.
+#define VT_P8(r, i)                                                                       \
+  "+r"((r)[i]), "+r"((r)[i + 1]), "+r"((r)[i + 2]), "+r"((r)[i + 3]), "+r"((r)[i + 4]),   \
+      "+r"((r)[i + 5]), "+r"((r)[i + 6]), "+r"((r)[i + 7])
+__device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
+  asm volatile("" : VT_P8(r, 0), VT_P8(r, 8), VT_P8(r, 16), VT_P8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                         int d, int token, int head, int block) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(smem_addr(bar)), "r"(d), "r"(token), "r"(head), "r"(block)
+      : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+struct Bars {
+  uint64_t k_full[kKvStages], k_empty[kKvStages], v_full[kKvStages], v_empty[kKvStages];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t v_tail;  // the last V tile's rows past the end are zeros
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+    prefix_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v) {
+  using S = MmaSmem<D>;
+  using TM = Tmem<D>;
+  extern __shared__ unsigned char dyn[];
+  __shared__ Bars bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ uint32_t s_mask[kMaskRing][4];
+  __shared__ int s_whole[kMaskRing];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_addr(dyn) + 1023) & ~1023u;
+  unsigned char* mem = dyn + (base - smem_addr(dyn));
+
+  int u = blockIdx.x;
+  const int kvh = u % a.hkv;
+  u /= a.hkv;
+  const int pairs = (a.prefix_tiles + 1) / 2;
+  const int pair = u % pairs, split = u / pairs;
+  const int n_rows = a.B * a.G;
+  const bool two = pair * 2 + 1 < a.prefix_tiles;
+  const int t0 = split * a.prefix_chunk, t1 = min(t0 + a.prefix_chunk, a.prefix_len);
+  const int n_tiles = (t1 - t0 + kTileTokens - 1) / kTileTokens;
+  // the split ends inside a block: what the copy brings from behind its end may be
+  // anything, and a weight of 0 times NaN is NaN
+  const int box = min(1 << a.shift, kTileTokens);  // tokens of a copy
+  const bool ragged = t1 % box != 0;
+
+  // Q into swizzled shared memory, negated where the scale is negative
+  const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+  for (int i = tid; i < (two ? 2 : 1) * kTileRows * (D / 8); i += kMmaThreads) {
+    const int row = i / (D / 8), c = i % (D / 8);
+    const int r = pair * 2 * kTileRows + row;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < n_rows) {
+      const int b = r / a.G;
+      v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + b * a.q_row +
+                                          (kvh * a.G + r % a.G) * a.q_head + c * 8);
+      v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+    }
+    const int in = row % kTileRows;
+    *reinterpret_cast<uint4*>(mem + S::kQ + (row / kTileRows) * S::kTile + (c / 8) * S::kHalf +
+                              in * 128 + (((c & 7) ^ (in & 7)) << 4)) = v;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kKvStages; ++i) {
+      mbar_init(&bars.k_full[i], 1);
+      mbar_init(&bars.v_full[i], 1);
+      mbar_init(&bars.k_empty[i], 1);
+      mbar_init(&bars.v_empty[i], 1);
+    }
+    mbar_init(&bars.v_tail, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars.s_full[t], 1);
+      mbar_init(&bars.p_full[t], kTileRows);
+      mbar_init(&bars.pv_done[t], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_addr(&s_tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s_tmem;
+  bool ok = true;
+
+  if (warp == 9) {
+    // ---- loads -----------------------------------------------------------------
+    const int boxes = kTileTokens / box;
+    int issued = 0;
+    for (int j = 0; j < n_tiles; ++j) {
+      const int st = j % kKvStages, tok0 = t0 + j * kTileTokens;
+      const uint32_t par = ((j / kKvStages) & 1) ^ 1;
+      // the blocks of this tile, up to 128 of them: four a lane
+      int blk[4];
+      unsigned good[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = q * 32 + lane, tok = tok0 + i * box;
+        blk[q] = i < boxes && tok < t1 ? a.prefix_blocks[tok >> a.shift] : -1;
+        const bool fine = blk[q] >= 0 && blk[q] < a.num_blocks;
+        if (i < boxes && tok < t1 && !fine) atomicOr(a.err_word, kErrBadBlock);
+        if (!fine) blk[q] = a.num_blocks;  // outside: the copy fills zeros
+        good[q] = __ballot_sync(0xffffffffu, fine);
+      }
+      if (lane < 4) {
+        uint32_t m = 0;
+        for (int i = 0; i < 32; ++i) {
+          const int t = lane * 32 + i, bx = t / box;
+          m |= ((good[bx >> 5] >> (bx & 31)) & 1u) && tok0 + t < t1 ? 1u << i : 0u;
+        }
+        s_mask[j % kMaskRing][lane] = m;
+        const unsigned all = __ballot_sync(0xfu, m == 0xffffffffu);
+        if (lane == 0) s_whole[j % kMaskRing] = all == 0xfu;
+      }
+      __syncwarp();
+      const int in_block = tok0 & ((1 << a.shift) - 1);  // (blocks longer than a tile)
+      ok = mbar_wait_bounded(&bars.k_empty[st], par);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bars.k_full[st], S::kTile);
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = q * 32 + lane;
+        if (i < boxes)
+          for (int h = 0; h < D / 64; ++h)
+            tma_tile(base + S::kK + st * S::kTile + h * S::kHalf + i * box * 128, &map_k,
+                     &bars.k_full[st], h * 64, in_block, kvh, blk[q]);
+      }
+      ok = mbar_wait_bounded(&bars.v_empty[st], par);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bars.v_full[st], S::kTile);
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = q * 32 + lane;
+        if (i < boxes)
+          for (int h = 0; h < D / 64; ++h)
+            tma_tile(base + S::kV + st * S::kTile + h * S::kHalf + i * box * 128, &map_v,
+                     &bars.v_full[st], h * 64, in_block, kvh, blk[q]);
+      }
+      issued = j + 1;
+    }
+    if (ragged && issued == n_tiles) {
+      const int j = n_tiles - 1, st = j % kKvStages;
+      ok = ok && mbar_wait_bounded(&bars.v_full[st], (j / kKvStages) & 1);
+      const int from = t1 - t0 - j * kTileTokens, to = (from + box - 1) / box * box;
+      for (int i = from * 8 + lane; i < to * 8; i += 32)
+        for (int h = 0; h < D / 64; ++h)
+          *reinterpret_cast<uint4*>(mem + S::kV + st * S::kTile + h * S::kHalf + i * 16) =
+              make_uint4(0, 0, 0, 0);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.v_tail);
+    }
+    // no copy is in flight when the CTA's memory goes to another
+    for (int j = max(0, issued - kKvStages); j < issued; ++j) {
+      mbar_wait_bounded(&bars.k_full[j % kKvStages], (j / kKvStages) & 1, 100000000ull);
+      mbar_wait_bounded(&bars.v_full[j % kKvStages], (j / kKvStages) & 1, 100000000ull);
+    }
+  } else if (warp == 8) {
+    // ---- MMAs ------------------------------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      // fp32 accumulators; K-major A and B; N = 128 tokens, M = 128
+      constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) |
+                                   ((kTileTokens / 8) << 17) | ((kTileRows / 16) << 24);
+      // B (V) is N-major: its rows are tokens; N = D
+      constexpr uint32_t kIdescO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) |
+                                   ((uint32_t)(D / 8) << 17) | ((kTileRows / 16) << 24);
+      auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
+        const uint32_t q = base + S::kQ + t * S::kTile,
+                       k = base + S::kK + (j % kKvStages) * S::kTile;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks / 4) * S::kHalf + (ks % 4) * 32;
+          mma_ss(tmem + TM::kS + t * kTileTokens, smem_desc(q + off, 16, 1024),
+                 smem_desc(k + off, 16, 1024), kIdescS, ks > 0);
+        }
+        mma_commit(&bars.s_full[t]);
+      };
+      auto values = [&](int t, int j) {  // O_t += P_t V_j
+        const uint32_t v = base + S::kV + (j % kKvStages) * S::kTile;
+#pragma unroll
+        for (int ks = 0; ks < kTileTokens / 16; ++ks)
+          mma_ts(tmem + TM::kO + t * D, tmem + TM::kP + t * TM::kPStep + ks * 8,
+                 smem_desc(v + ks * 16 * 128, S::kHalf, 1024), kIdescO, j > 0 || ks > 0);
+        mma_commit(&bars.pv_done[t]);
+      };
+      auto wait = [&](uint64_t* bar, int j) {
+        ok = ok && mbar_wait_bounded(bar, j & 1);
+        return ok;
+      };
+      auto wait_v = [&](int j) {
+        ok = ok && mbar_wait_bounded(&bars.v_full[j % kKvStages], (j / kKvStages) & 1);
+        if (ragged && j == n_tiles - 1) ok = ok && mbar_wait_bounded(&bars.v_tail, 0);
+        return ok;
+      };
+      auto wait_st = [&](uint64_t* bars_, int j) {
+        ok = ok && mbar_wait_bounded(&bars_[j % kKvStages], (j / kKvStages) & 1);
+        return ok;
+      };
+      for (int j = 0; j <= n_tiles; ++j) {
+        if (j < n_tiles) {
+          // S_0's columns: P_0 of the tile before has been used (head_dim 64: its
+          // scores have been read, which P_0 being there says)
+          if (!wait_st(bars.k_full, j)) break;
+          if (j > 0 && !wait(TM::kShared ? &bars.pv_done[0] : &bars.p_full[0], j - 1)) break;
+          fence_after();
+          scores(0, j);
+          if (!two) mma_commit(&bars.k_empty[j % kKvStages]);
+        }
+        if (two && j > 0) {
+          if (!wait(&bars.p_full[1], j - 1) || !wait_v(j - 1)) break;
+          fence_after();
+          values(1, j - 1);
+          mma_commit(&bars.v_empty[(j - 1) % kKvStages]);
+        }
+        if (j < n_tiles) {
+          if (two) {
+            if (TM::kShared && j > 0 && !wait(&bars.pv_done[1], j - 1)) break;
+            fence_after();
+            scores(1, j);
+            mma_commit(&bars.k_empty[j % kKvStages]);
+          }
+          if (!wait(&bars.p_full[0], j) || !wait_v(j)) break;
+          fence_after();
+          values(0, j);
+          if (!two) mma_commit(&bars.v_empty[j % kKvStages]);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: warpgroup t, one thread to a row --------------------------------
+    const int t = warp >> 2;
+    if (t == 0 || two) {
+      const int in = tid & (kTileRows - 1);
+      const int r = (pair * 2 + t) * kTileRows + in;
+      const bool live = r < n_rows;
+      const int b = live ? r / a.G : 0, head = kvh * a.G + (live ? r % a.G : 0);
+      const int lim = live ? min(max(a.seq_lens[b], 0), a.prefix_len) : 0x7fffffff;
+      const int lim_min = __reduce_min_sync(0xffffffffu, lim);
+      // (a scale of 0 as one that leaves masked scores at -inf)
+      const float sc = fmaxf(fabsf(a.scale_log2), 1e-30f);
+      const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane (warp % 4) * 32
+      const uint32_t ts = tmem + lanes + TM::kS + t * kTileTokens;
+      const uint32_t tp = tmem + lanes + TM::kP + t * TM::kPStep;
+      const uint32_t to = tmem + lanes + TM::kO + t * D;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n_tiles; ++j) {
+        ok = mbar_wait_bounded(&bars.s_full[t], j & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s[q], ts + q * 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) loaded(s[q]);
+        const int tok0 = t0 + j * kTileTokens;
+        if (!s_whole[j % kMaskRing] || tok0 + kTileTokens > lim_min) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t mask = s_mask[j % kMaskRing][q];
+            const int left = lim - tok0 - q * 32;
+            const uint32_t keep =
+                mask & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((keep >> i) & 1)) s[q][i] = 0xff800000u;
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][i]));
+        const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc);
+        // (the products with the tile before are done: S_t was made after them, or
+        // with columns of its own P_t's barrier below has been waited for)
+        const bool grow = m_new > m + kGrowth;
+        if (!TM::kShared && j > 0) {
+          ok = mbar_wait_bounded(&bars.pv_done[t], (j - 1) & 1);  // P_t's columns are free
+          if (!__all_sync(0xffffffffu, ok)) break;
+          fence_after();
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2_approx(m - m_new) : 1.f;
+          if (grow) m = m_new;
+          l *= f;
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o, to + c);
+              tmem_wait_ld();
+              loaded(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(to + c, o);
+            }
+          }
+        }
+        const float off = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int e = half * 64 + 2 * i;
+            const float p0 = ex2_approx(__fmaf_rn(__uint_as_float(s[e >> 5][e & 31]), sc, -off));
+            const float p1 =
+                ex2_approx(__fmaf_rn(__uint_as_float(s[e >> 5][(e & 31) + 1]), sc, -off));
+            sum[(2 * i) & 3] += p0;
+            sum[(2 * i + 1) & 3] += p1;
+            // the weights are rounded to the cache's type for the tensor cores (a
+            // relative 2^-9 in bf16, 2^-12 in fp16, each its own way); the sum is not
+            p[i] = pack2<T>(p0, p1);
+          }
+          tmem_st32(tp + half * 32, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        fence_before();
+        mbar_arrive(&bars.p_full[t]);
+      }
+      // the row's part
+      if (ok) ok = mbar_wait_bounded(&bars.pv_done[t], (n_tiles - 1) & 1);
+      if (__all_sync(0xffffffffu, ok)) {
+        fence_after();
+        const int64_t at = (int64_t)split * a.B * a.hq + (int64_t)b * a.hq + head;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o, to + c);
+          tmem_wait_ld();
+          loaded(o);
+          if (live && l != 0.f)
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(a.part_o + at * D + c + i) =
+                  make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
+        if (live) a.part_ml[at] = make_float2(m, l);
+      }
+    }
+  }
+  if (!ok) atomicOr(a.err_word, kErrTimeout);
+  fence_before();
+  __syncthreads();
+  if (warp == 8)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+bool make_map(CUtensorMap* map, const AttnArgs& a, const void* cache, int dtype, int head_dim) {
+  const cuuint64_t dims[4] = {(cuuint64_t)head_dim, 1ull << a.shift, (cuuint64_t)a.hkv,
+                              (cuuint64_t)a.num_blocks};
+  const cuuint64_t strides[3] = {(cuuint64_t)a.token_stride * 2, (cuuint64_t)a.head_stride * 2,
+                                 (cuuint64_t)a.block_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)(a.shift < 7 ? 1 << a.shift : kTileTokens), 1, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return encode_tiled()(map,
+                        dtype == VT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        4, const_cast<void*>(cache), dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+                         cudaStream_t stream) {
+  cudaError_t e =
+      cudaFuncSetAttribute(prefix_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           MmaSmem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  const int grid = (a.prefix_tiles + 1) / 2 * a.hkv * a.prefix_splits;
+  prefix_kernel<T, D><<<grid, kMmaThreads, MmaSmem<D>::kBytes, stream>>>(a, mk, mv);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool prefix_mma_takes(const AttnArgs& a) {
+  // whole swizzle atoms to a copy; strides a tensor map can hold
+  const int64_t most = 1ll << 38;
+  return a.shift >= 3 && a.block_stride > 0 && a.token_stride > 0 && a.head_stride > 0 &&
+         a.block_stride < most && a.token_stride < most && a.head_stride < most &&
+         encode_tiled() != nullptr;
+}
+
+cudaError_t launch_prefix_mma(const AttnArgs& a, int dtype, int head_dim, cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  if (!make_map(&mk, a, a.k, dtype, head_dim) || !make_map(&mv, a, a.v, dtype, head_dim))
+    return cudaErrorInvalidValue;
+  if (dtype == VT_DTYPE_BF16)
+    return head_dim == 128 ? launch_typed<__nv_bfloat16, 128>(a, mk, mv, stream)
+                           : launch_typed<__nv_bfloat16, 64>(a, mk, mv, stream);
+  return head_dim == 128 ? launch_typed<__half, 128>(a, mk, mv, stream)
+                         : launch_typed<__half, 64>(a, mk, mv, stream);
+}
+
+}  // namespace vt
