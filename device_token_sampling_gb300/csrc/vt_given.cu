@@ -1580,11 +1580,6 @@ cudaError_t launch_given_typed(const GivenArgs& a, int num_sms, int ctas, cudaSt
   stream_kernel<T><<<(unsigned)grid, kStreamThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(finish_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)sizeof(Shared));
-  if (e == cudaSuccess && ctas > 8)
-    e = cudaFuncSetAttribute(finish_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.B * ctas));
   cfg.blockDim = dim3(kThreadsF);
@@ -1603,6 +1598,19 @@ cudaError_t launch_given_typed(const GivenArgs& a, int num_sms, int ctas, cudaSt
 }
 
 }  // namespace
+
+template <typename T>
+cudaError_t prepare_given_typed() {
+  const cudaError_t e = cudaFuncSetAttribute(
+      finish_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(finish_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+
+cudaError_t prepare_given() {
+  const cudaError_t e = prepare_given_typed<float>();
+  return e != cudaSuccess ? e : prepare_given_typed<__nv_bfloat16>();
+}
 
 cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t stream) {
   a.segs = (a.V + kSeg - 1) / kSeg;

@@ -264,6 +264,8 @@ struct GivenArgs {
   float* group_max;
   int32_t segs, drop;        // filled by launch_given
 };
+// Kernel attributes, once for the current device.
+cudaError_t prepare_given();
 cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t stream);
 
 }  // namespace vt

@@ -131,7 +131,8 @@ int vt_paged_create(const vt_paged_config* config, vt_paged** out) {
             prop.major == 10 && prop.minor == 3;  // built for sm_103a only
   if (ok) {
     h->num_sms = prop.multiProcessorCount;
-    ok = cudaMalloc(&h->d_err, sizeof(int32_t)) == cudaSuccess &&
+    ok = vt::prepare_tables() == cudaSuccess && vt::prepare_prefix_attention() == cudaSuccess &&
+         cudaMalloc(&h->d_err, sizeof(int32_t)) == cudaSuccess &&
          cudaMemset(h->d_err, 0, sizeof(int32_t)) == cudaSuccess &&
          cudaMallocHost(&h->h_err, sizeof(int32_t)) == cudaSuccess;
   }

@@ -67,6 +67,10 @@ struct AttnArgs {
 // dtype as VT_DTYPE_BF16 / VT_DTYPE_F16; head_dim 64 or 128.
 cudaError_t launch_prefix_attention(const AttnArgs& a, int dtype, int head_dim,
                                     cudaStream_t stream);
+// Kernel attributes, once for the current device.
+cudaError_t prepare_tables();
+cudaError_t prepare_prefix_attention();
+cudaError_t prepare_prefix_mma();
 // The prefix's part of it (vt_prefix_mma.cu): whether its layout can be taken, and
 // the launch.
 bool prefix_mma_takes(const AttnArgs& a);

@@ -393,9 +393,7 @@ __global__ void __launch_bounds__(128) join_kernel(AttnArgs a) {
 template <typename T, int D>
 cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   using S = SplitSmem<D>;
-  cudaError_t e = cudaFuncSetAttribute(split_kernel<T, D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   if (a.prefix_mma &&
       (e = launch_prefix_mma(a, std::is_same<T, __half>::value ? VT_DTYPE_F16 : VT_DTYPE_BF16, D,
                              stream)) != cudaSuccess)
@@ -410,6 +408,17 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t prepare_prefix_attention() {
+  cudaError_t e;
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if ((e = cudaFuncSetAttribute(split_kernel<__nv_bfloat16, 64>, attr, SplitSmem<64>::kBytes)) ||
+      (e = cudaFuncSetAttribute(split_kernel<__nv_bfloat16, 128>, attr, SplitSmem<128>::kBytes)) ||
+      (e = cudaFuncSetAttribute(split_kernel<__half, 64>, attr, SplitSmem<64>::kBytes)) ||
+      (e = cudaFuncSetAttribute(split_kernel<__half, 128>, attr, SplitSmem<128>::kBytes)))
+    return e;
+  return prepare_prefix_mma();
+}
 
 cudaError_t launch_prefix_attention(const AttnArgs& a, int dtype, int head_dim,
                                     cudaStream_t stream) {

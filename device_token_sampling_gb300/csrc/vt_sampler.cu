@@ -254,6 +254,7 @@ int vt_sampler_create(const vt_sampler_config* cfg, vt_sampler** out) {
   // the largest row must fit the shared-memory plan (16 CTAs per row at most)
   const vt::LaunchPlan worst = vt::plan_layout(cfg->max_vocab, 4, 16, true, true);
   if (worst.smem > (size_t)prop.sharedMemPerBlockOptin) return bail(VT_ERR_CAPACITY);
+  if (vt::prepare_given() != cudaSuccess) return bail(VT_ERR_CUDA);
   h->num_sms = prop.multiProcessorCount;
 
   const size_t B = (size_t)cfg->max_batch;

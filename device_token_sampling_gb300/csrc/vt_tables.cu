@@ -19,6 +19,7 @@
 // prompts.
 #include "vt_device.cuh"
 #include "vt_paged.h"
+#include "vt_sampler.h"
 
 namespace vt {
 namespace {
@@ -213,13 +214,13 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(TablesArgs a) {
 
 }  // namespace
 
+cudaError_t prepare_tables() {
+  return cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)sizeof(int32_t) * (2 * VT_PAGED_MAX_BATCH + 1));
+}
+
 cudaError_t launch_tables(const TablesArgs& a, int num_sms, cudaStream_t stream) {
   const size_t smem = sizeof(int32_t) * (2 * (size_t)a.B + 1);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
   const int64_t tiles = (a.capacity + kTabThreads * kTokensPerThread - 1) /
                         (kTabThreads * kTokensPerThread);
   const int64_t items =

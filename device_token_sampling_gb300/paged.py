@@ -9,28 +9,30 @@ from __future__ import annotations
 
 import ctypes as C
 
-from .sampler import (DTYPE_BF16, DTYPE_F16, VT_OK, P, PagedConfig, VtError, _stream_ptr,
-                      load_library)
+import torch
+
+from .sampler import (DTYPE_BF16, DTYPE_F16, VT_OK, P, PagedConfig, VtError, load_library,
+                      raw_stream)
+
+# A decode step makes these calls once a layer or once a token, and at its sizes
+# the host's share is the larger one: checks read each attribute once, pointers go
+# to ctypes as plain integers.
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
-def _ids(t, name, shape, device, dtype=None):
-    """A contiguous int32 (or ``dtype``) tensor of ``shape`` (None: any size) on ``device``."""
-    import torch
-    dtype = dtype or torch.int32
-    if not torch.is_tensor(t) or t.dtype != dtype or t.dim() != len(shape):
-        raise ValueError(f"{name} must be a {len(shape)}-D {dtype} tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
-    if any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, need {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return P(t.data_ptr())
+def _ids(t, name, device, size=None, dtype=_I32):
+    """The address of a contiguous 1-D tensor of ``size`` elements (None: any) on ``device``."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device
+            and t.dim() == 1 and t.is_contiguous() and (size is None or t.shape[0] == size)):
+        what = (f"{tuple(t.shape)} {t.dtype} on {t.device}" if isinstance(t, torch.Tensor)
+                else type(t).__name__)
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor "
+                         f"[{'n' if size is None else size}] on cuda:{device}, not {what}")
+    return t.data_ptr()
 
 
 def _on_stream(stream, tensors):
     """Outputs made here for another stream than the current one live until it is done."""
-    import torch
     if stream is not None and stream != torch.cuda.current_stream(stream.device):
         for t in tensors:
             t.record_stream(stream)
@@ -41,7 +43,6 @@ class PagedBatch:
 
     def __init__(self, max_batch: int, block_size: int, max_blocks: int, q_heads: int = 0,
                  kv_heads: int = 0, head_dim: int = 0, device: int | None = None):
-        import torch
         self._h = None
         self._lib = load_library()
         if device is None:
@@ -55,6 +56,7 @@ class PagedBatch:
             raise VtError(rc, f"vt_paged_create({max_batch}, {block_size}, {max_blocks}, "
                               f"{q_heads}, {kv_heads}, {head_dim}, device={self.device})")
         self._h = h
+        self._shape = (block_size, q_heads, kv_heads, head_dim)
 
     # -- lifetime ------------------------------------------------------------
     def close(self):
@@ -83,10 +85,6 @@ class PagedBatch:
         """Wait for the last call and raise what its kernels met."""
         self._check(self._lib.vt_paged_check_errors(self._h), "vt_paged_check_errors")
 
-    def _device(self):
-        import torch
-        return torch.device("cuda", self.device)
-
     # -- block tables ----------------------------------------------------------
     def build_tables(self, table, seq_lens, query_lens, free_blocks, cursor, held=None,
                      prefix_blocks=None, capacity: int | None = None, out=None, stream=None):
@@ -97,43 +95,51 @@ class PagedBatch:
         starts, slots, positions, status)``: int32 [B], [1] and [B + 1], int64 and int32
         [capacity] (default: ``B``, one token a request), int32 [B].  ``out`` gives those six
         tensors; ``held`` and ``cursor`` among them must not be the inputs.  Nothing waits."""
-        import torch
-        dev = self._device()
-        if not torch.is_tensor(seq_lens) or seq_lens.dim() != 1:
-            raise ValueError("seq_lens must be a 1-D int32 tensor")
-        B = seq_lens.shape[0]
-        p_seq = _ids(seq_lens, "seq_lens", (B,), dev)
-        p_query = _ids(query_lens, "query_lens", (B,), dev)
-        p_free = _ids(free_blocks, "free_blocks", (None,), dev)
-        p_cursor = _ids(cursor, "cursor", (1,), dev)
-        p_held = None if held is None else _ids(held, "held", (B,), dev)
-        p_prefix = None if prefix_blocks is None else _ids(prefix_blocks, "prefix_blocks",
-                                                           (None,), dev)
-        if (not torch.is_tensor(table) or table.dtype != torch.int32 or table.dim() != 2
-                or table.device != dev or table.shape[0] != B
-                or table.shape[1] < self.cfg.max_blocks or table.stride(1) != 1):
-            raise ValueError(f"table must be an int32 tensor [{B}, >= {self.cfg.max_blocks}] on "
-                             f"{dev} with contiguous rows")
+        dev = self.device
+        B = seq_lens.shape[0] if isinstance(seq_lens, torch.Tensor) and seq_lens.dim() else 0
+        p_seq = _ids(seq_lens, "seq_lens", dev, B)
+        p_query = _ids(query_lens, "query_lens", dev, B)
+        p_free = _ids(free_blocks, "free_blocks", dev)
+        p_cursor = _ids(cursor, "cursor", dev, 1)
+        p_held = None if held is None else _ids(held, "held", dev, B)
+        if prefix_blocks is None:
+            p_prefix, n_prefix = None, 0
+        else:
+            p_prefix, n_prefix = _ids(prefix_blocks, "prefix_blocks", dev), prefix_blocks.shape[0]
+        p_table, ld = self._table(table, B, self.cfg.max_blocks)
         n = B if capacity is None else int(capacity)
         if n < 0:
             raise ValueError(f"capacity={n}")
         if out is None:
-            i32 = dict(dtype=torch.int32, device=dev)
-            out = (torch.empty(B, **i32), torch.empty(1, **i32), torch.empty(B + 1, **i32),
-                   torch.empty(n, dtype=torch.int64, device=dev), torch.empty(n, **i32),
-                   torch.empty(B, **i32))
-            _on_stream(stream, out)
-        names = ("held", "cursor", "starts", "slots", "positions", "status")
-        shapes = ((B,), (1,), (B + 1,), (n,), (n,), (B,))
-        po = [_ids(t, "out " + nm, sh, dev, torch.int64 if nm == "slots" else None)
-              for t, nm, sh in zip(out, names, shapes)]
+            o_held, o_cursor, o_starts, o_status = seq_lens.new_empty(3 * B + 2).split(
+                (B, 1, B + 1, B))
+            o_slots = torch.empty(n, dtype=_I64, device=seq_lens.device)
+            o_pos = seq_lens.new_empty(n)
+            out = (o_held, o_cursor, o_starts, o_slots, o_pos, o_status)
+            if stream is not None:
+                _on_stream(stream, (o_held, o_slots, o_pos))
+            po = [t.data_ptr() for t in out]
+        else:
+            names = ("held", "cursor", "starts", "slots", "positions", "status")
+            sizes = (B, 1, B + 1, n, n, B)
+            po = [_ids(t, "out " + nm, dev, k, _I64 if nm == "slots" else _I32)
+                  for t, nm, k in zip(out, names, sizes, strict=True)]
         rc = self._lib.vt_paged_tables(
-            self._h, B, p_seq, p_query, p_held, p_prefix,
-            0 if prefix_blocks is None else prefix_blocks.shape[0], p_free, free_blocks.shape[0],
-            p_cursor, P(table.data_ptr()), table.stride(0) if B > 1 else table.shape[1], po[0],
-            po[1], po[2], po[3], po[4], n, po[5], _stream_ptr(stream))
-        self._check(rc, "vt_paged_tables")
-        return tuple(out)
+            self._h, B, p_seq, p_query, p_held, p_prefix, n_prefix, p_free, free_blocks.shape[0],
+            p_cursor, p_table, ld, po[0], po[1], po[2], po[3], po[4], n, po[5],
+            raw_stream(stream, dev))
+        if rc != VT_OK:
+            self._check(rc, "vt_paged_tables")
+        return out
+
+    def _table(self, table, B, columns):
+        """Address and row stride of a block table."""
+        if not (isinstance(table, torch.Tensor) and table.dtype is _I32 and table.dim() == 2
+                and table.get_device() == self.device and table.shape[0] == B
+                and table.shape[1] >= columns and table.stride(1) == 1):
+            raise ValueError(f"table must be an int32 tensor [{B}, >= {columns}] on "
+                             f"cuda:{self.device} with contiguous rows")
+        return table.data_ptr(), table.stride(0) if B > 1 else table.shape[1]
 
     # -- attention ---------------------------------------------------------------
     def attention(self, q, k_cache, v_cache, table, seq_lens, prefix_blocks=None,
@@ -147,60 +153,55 @@ class PagedBatch:
         [blocks, kv_heads, block_size, head_dim] goes in transposed) are bf16 or fp16.
         Returns ``(out, lse)``: q's type [B, q_heads, head_dim] and float32 [B, q_heads].
         ``scale`` defaults to head_dim ** -0.5.  Nothing waits."""
-        import torch
-        dev, c = self._device(), self.cfg
-        if c.q_heads == 0:
+        dev = self.device
+        block_size, q_heads, kv_heads, d = self._shape
+        if q_heads == 0:
             raise ValueError("this PagedBatch was made without heads")
-        if not torch.is_tensor(q) or q.dim() != 3 or q.device != dev:
-            raise ValueError(f"q must be a 3-D tensor on {dev}")
-        B = q.shape[0]
-        dtype = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}.get(q.dtype)
+        qt = q.dtype if isinstance(q, torch.Tensor) else None
+        dtype = DTYPE_BF16 if qt is torch.bfloat16 else DTYPE_F16 if qt is torch.float16 else None
         if dtype is None:
-            raise ValueError(f"unsupported dtype {q.dtype}")
-        if tuple(q.shape) != (B, c.q_heads, c.head_dim) or q.stride(2) != 1:
-            raise ValueError(f"q must be [B, {c.q_heads}, {c.head_dim}] with contiguous heads")
-        want = (k_cache.shape[0], c.block_size, c.kv_heads, c.head_dim)
+            raise ValueError(f"unsupported q: {qt or type(q).__name__}")
+        B = q.shape[0]
+        if q.shape != (B, q_heads, d) or q.get_device() != dev or q.stride(2) != 1:
+            raise ValueError(f"q must be [B, {q_heads}, {d}] on cuda:{dev} with contiguous heads, "
+                             f"not {tuple(q.shape)} on {q.device}")
+        kv = k_cache.stride()
         for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-            if t.dtype != q.dtype or t.device != dev or tuple(t.shape) != want:
-                raise ValueError(f"{name} must be a {q.dtype} tensor [blocks, {c.block_size}, "
-                                 f"{c.kv_heads}, {c.head_dim}] on {dev}")
-            if t.stride(3) != 1 or t.stride() != k_cache.stride():
+            shape = t.shape
+            if (t.dtype is not qt or t.get_device() != dev or len(shape) != 4
+                    or shape != (k_cache.shape[0], block_size, kv_heads, d)):
+                raise ValueError(f"{name} must be a {qt} tensor [blocks, {block_size}, "
+                                 f"{kv_heads}, {d}] on cuda:{dev}, not {tuple(shape)}")
+            if t.stride() != kv or kv[3] != 1:
                 raise ValueError("the caches must have equal strides and contiguous heads")
-        if (not torch.is_tensor(table) or table.dtype != torch.int32 or table.dim() != 2
-                or table.device != dev or table.shape[0] != B or table.stride(1) != 1):
-            raise ValueError(f"table must be an int32 tensor [{B}, columns] on {dev} with "
-                             "contiguous rows")
-        if max_seq_len > table.shape[1] * c.block_size:
+        p_table, ld = self._table(table, B, 1)
+        if max_seq_len > table.shape[1] * block_size:
             raise ValueError(f"max_seq_len={max_seq_len} is past the table's columns")
-        p_seq = _ids(seq_lens, "seq_lens", (B,), dev)
+        p_seq = _ids(seq_lens, "seq_lens", dev, B)
         p_prefix = None
         if prefix_len > 0:
-            if prefix_blocks is None:
-                raise ValueError("prefix_len without prefix_blocks")
-            p_prefix = _ids(prefix_blocks, "prefix_blocks", (None,), dev)
-            if prefix_blocks.shape[0] * c.block_size < prefix_len:
+            p_prefix = _ids(prefix_blocks, "prefix_blocks", dev)
+            if prefix_blocks.shape[0] * block_size < prefix_len:
                 raise ValueError(f"{prefix_blocks.shape[0]} prefix blocks do not hold "
                                  f"{prefix_len} tokens")
-        made = []
+        made = out is None or lse is None
         if out is None:
-            out = torch.empty((B, c.q_heads, c.head_dim), dtype=q.dtype, device=dev)
-            made.append(out)
-        elif (out.dtype != q.dtype or out.device != dev or not out.is_contiguous()
-              or tuple(out.shape) != (B, c.q_heads, c.head_dim)):
-            raise ValueError(f"out must be a contiguous {q.dtype} tensor like q")
+            out = q.new_empty((B, q_heads, d))
+        elif (out.dtype is not qt or out.get_device() != dev or not out.is_contiguous()
+              or out.shape != q.shape):
+            raise ValueError(f"out must be a contiguous {qt} tensor like q")
         if lse is None:
-            lse = torch.empty((B, c.q_heads), dtype=torch.float32, device=dev)
-            made.append(lse)
-        elif (lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous()
-              or tuple(lse.shape) != (B, c.q_heads)):
-            raise ValueError(f"lse must be a contiguous float32 tensor [{B}, {c.q_heads}]")
-        _on_stream(stream, made)
+            lse = torch.empty((B, q_heads), dtype=_F32, device=q.device)
+        elif (lse.dtype is not _F32 or lse.get_device() != dev or not lse.is_contiguous()
+              or lse.shape != (B, q_heads)):
+            raise ValueError(f"lse must be a contiguous float32 tensor [{B}, {q_heads}]")
+        if made and stream is not None:
+            _on_stream(stream, (out, lse))
         rc = self._lib.vt_paged_attention(
-            self._h, dtype, B, P(q.data_ptr()), q.stride(0), q.stride(1), P(k_cache.data_ptr()),
-            P(v_cache.data_ptr()), k_cache.shape[0], k_cache.stride(0), k_cache.stride(1),
-            k_cache.stride(2), P(table.data_ptr()), table.stride(0) if B > 1 else table.shape[1],
-            p_seq, p_prefix, int(prefix_len), int(max_seq_len),
-            c.head_dim ** -0.5 if scale is None else float(scale), P(out.data_ptr()),
-            P(lse.data_ptr()), _stream_ptr(stream))
-        self._check(rc, "vt_paged_attention")
+            self._h, dtype, B, q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_cache.shape[0], kv[0], kv[1], kv[2], p_table, ld, p_seq,
+            p_prefix, int(prefix_len), int(max_seq_len), d ** -0.5 if scale is None else scale,
+            out.data_ptr(), lse.data_ptr(), raw_stream(stream, dev))
+        if rc != VT_OK:
+            self._check(rc, "vt_paged_attention")
         return out, lse

@@ -136,6 +136,14 @@ def _stream_ptr(stream):
     return P(stream.cuda_stream)
 
 
+def raw_stream(stream, device: int) -> int:
+    """The cudaStream_t of ``stream`` (None: the current stream of ``device``) as an integer."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 class Sampler:
     """One sampler handle (``vt_sampler_create``) on one CUDA device."""
 
@@ -303,36 +311,42 @@ class Sampler:
         if logits.dim() != 2 or not logits.is_cuda or logits.stride(1) != 1:
             raise ValueError("logits must be a 2-D CUDA tensor with contiguous rows")
         if dtype is None:
-            dtype = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16,
-                     torch.uint16: DTYPE_BF16, torch.int16: DTYPE_BF16}.get(logits.dtype)
-            if dtype is None:
-                raise ValueError(f"unsupported logits dtype {logits.dtype}")
-        B = logits.shape[0]
-        V = logits.shape[1] if V is None else V
-        ld = logits.stride(0) if B > 1 else max(logits.stride(0), logits.shape[1])
-        if V > logits.shape[1]:
-            raise ValueError(f"V={V} is past the rows' {logits.shape[1]} columns")
-        if (uniforms.dtype != torch.float32 or uniforms.device != logits.device
-                or uniforms.dim() not in (1, 2) or uniforms.shape[0] != B
-                or not uniforms.is_contiguous()):
+            t = logits.dtype
+            if t is torch.float32:
+                dtype = DTYPE_F32
+            elif t is torch.bfloat16 or t is torch.uint16 or t is torch.int16:
+                dtype = DTYPE_BF16
+            else:
+                raise ValueError(f"unsupported logits dtype {t}")
+        B, cols = logits.shape
+        if V is None:
+            V = cols
+        elif V > cols:
+            raise ValueError(f"V={V} is past the rows' {cols} columns")
+        shape, dev = uniforms.shape, logits.get_device()
+        if (uniforms.dtype is not torch.float32 or uniforms.get_device() != dev
+                or len(shape) not in (1, 2) or shape[0] != B or not uniforms.is_contiguous()):
             raise ValueError("uniforms must be a contiguous float32 tensor [B] or [B, draws] "
                              "beside the logits")
-        draws = 1 if uniforms.dim() == 1 else uniforms.shape[1]
         if out is None:
-            out = (torch.empty_like(uniforms, dtype=torch.int32), torch.empty_like(uniforms))
+            lp = torch.empty_like(uniforms)
+            tok = torch.empty_like(uniforms, dtype=torch.int32)
             if stream is not None:
-                for t in out:
-                    t.record_stream(stream)
-        tok, lp = out
-        for t, name, dt in ((tok, "tokens", torch.int32), (lp, "logprobs", torch.float32)):
-            if t is not None and (t.dtype != dt or t.shape != uniforms.shape
-                                  or t.device != logits.device or not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous {dt} tensor like uniforms")
-        rc = self._lib.vt_sample_given(self._h, P(logits.data_ptr()), dtype, B, V, ld,
-                                       P(uniforms.data_ptr()), draws, P(tok.data_ptr()),
-                                       None if lp is None else P(lp.data_ptr()),
-                                       _stream_ptr(stream))
-        self._check(rc, "vt_sample_given")
+                tok.record_stream(stream)
+                lp.record_stream(stream)
+            out = (tok, lp)
+        else:
+            tok, lp = out
+            for t, name, dt in ((tok, "tokens", torch.int32), (lp, "logprobs", torch.float32)):
+                if t is not None and (t.dtype is not dt or t.shape != shape
+                                      or t.get_device() != dev or not t.is_contiguous()):
+                    raise ValueError(f"{name} must be a contiguous {dt} tensor like uniforms")
+        rc = self._lib.vt_sample_given(
+            self._h, logits.data_ptr(), dtype, B, V, logits.stride(0) if B > 1 else cols,
+            uniforms.data_ptr(), 1 if len(shape) == 1 else shape[1], tok.data_ptr(),
+            None if lp is None else lp.data_ptr(), raw_stream(stream, self.device))
+        if rc != VT_OK:
+            self._check(rc, "vt_sample_given")
         return out
 
     def sample_ptr(self, logits_ptr: int, dtype: int, B: int, V: int, ld: int, num_logprobs: int,
