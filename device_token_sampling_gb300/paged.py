@@ -111,13 +111,11 @@ class PagedBatch:
         if n < 0:
             raise ValueError(f"capacity={n}")
         if out is None:
-            o_held, o_cursor, o_starts, o_status = seq_lens.new_empty(3 * B + 2).split(
-                (B, 1, B + 1, B))
-            o_slots = torch.empty(n, dtype=_I64, device=seq_lens.device)
-            o_pos = seq_lens.new_empty(n)
-            out = (o_held, o_cursor, o_starts, o_slots, o_pos, o_status)
+            new = seq_lens.new_empty
+            out = (new(B), new(1), new(B + 1), torch.empty(n, dtype=_I64, device=seq_lens.device),
+                   new(n), new(B))
             if stream is not None:
-                _on_stream(stream, (o_held, o_slots, o_pos))
+                _on_stream(stream, out)
             po = [t.data_ptr() for t in out]
         else:
             names = ("held", "cursor", "starts", "slots", "positions", "status")
