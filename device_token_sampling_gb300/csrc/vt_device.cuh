@@ -121,6 +121,19 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t phase,
   return true;
 }
 
+// The same where the wait is on a kernel's critical path: bounded by the SM's
+// clock (limit_cycles, about 2 s), which is read in a few cycles, and read only
+// every 64 polls.
+__device__ __forceinline__ bool mbar_wait_clocked(uint64_t* bar, uint32_t phase,
+                                                  long long limit_cycles = 4000000000ll) {
+  if (mbar_try_wait(bar, phase)) return true;
+  const long long t0 = clock64();
+  for (uint32_t polls = 1;; ++polls) {
+    if (mbar_try_wait(bar, phase)) return true;
+    if ((polls & 63u) == 0 && (clock64() - t0 > limit_cycles || polls >= (1u << 28))) return false;
+  }
+}
+
 // Bulk (non-tensor) async copy global -> this CTA's shared memory, completing
 // `bytes` of transaction count on `bar`.  dst, src 16-byte aligned; bytes a
 // multiple of 16.

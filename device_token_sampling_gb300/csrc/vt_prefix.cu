@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(AttnArgs a) {
       const int next = block_of(ahead + kSplitWarps);
       if (ahead < g_end) issue(ahead, blk, st == 0 ? kStages - 1 : st - 1);
       blk = next;
-      ok = mbar_wait_bounded(&bars[warp][st], phase);
+      ok = mbar_wait_clocked(&bars[warp][st], phase);
       if (!ok) break;
       const uint32_t mask = s_mask[warp][st];
       const T* sk = ring + st * 2 * S::kTile;
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(AttnArgs a) {
     }
     if (!ok) {
       // the copies in flight land before this CTA's shared memory goes to another
-      for (int i = 0; i < kStages; ++i) mbar_wait_bounded(&bars[warp][i], phase, 100000000ull);
+      for (int i = 0; i < kStages; ++i) mbar_wait_clocked(&bars[warp][i], phase, 200000000ll);
       atomicOr(a.err_word, kErrTimeout);
     }
 #pragma unroll

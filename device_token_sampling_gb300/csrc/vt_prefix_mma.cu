@@ -2,21 +2,26 @@
 //
 // The rows of a kv head, B * G query heads against one prefix, are a matrix
 // product S = Q K^T, a softmax, and a product P V.  A CTA takes up to 256 rows
-// (two tiles of 128) and one split of the prefix, 128 tokens at a time:
-//   - the load warp brings K and V tiles by TMA, block by block of the cache,
-//     into two-stage rings of 128-byte-swizzled shared memory;
-//   - one thread issues the MMAs: S_t = Q_t K^T into tensor memory, O_t += P_t V
+// (two tiles of 128) and one split of the prefix, 64 tokens at a step:
+//   - the load warp brings K and V tiles of 128 tokens by TMA, block by block of
+//     the cache, into two-stage rings of 128-byte-swizzled shared memory;
+//   - a thread per tile issues its MMAs (one for both was bound by its own
+//     instructions: 2900 cycles a step): S_t = Q_t K^T into tensor memory, O_t += P_t V
 //     with P_t read from tensor memory and V as it lies (token-major);
 //   - a warpgroup per tile, one thread to a row, turns S into weights: running
-//     maximum and sum in registers, P back to tensor memory in the cache's type.
-// The tiles are out of step by half a period (S_0, P_1 V, S_1, P_0 V), so that one
-// tile's exponentials run under the other's products.  A warp rescales its rows'
+//     maximum and sum in registers, P in the cache's type over the first columns
+//     of its own S.
+// Each tile has two S buffers, so that its next scores are made while it is at its
+// exponentials: with one, scores, exponentials and product of a tile are one
+// serial chain (a 128-token step then took 5000 cycles for two tiles; 85 us for
+// 1024 rows of 8 kv heads against 16384 tokens).  A warp rescales its rows'
 // accumulators only when one of their maxima has grown.  (To wait until it has
-// grown by 2^8 saves 4 of 85 us on 1024 rows of 8 kv heads against 16384 tokens,
-// but then the largest weight is no longer exactly 1, and the rounding of the
-// weights to bf16 costs 1.5e-3 of the result instead of 1.07e-3.)
-// What bounds it: the exponentials and the products take the same time (128 x 128
-// each: 1024 cycles of the special function units, 1024 of the tensor cores).
+// grown by 2^8 saves 4 us of those 85, but then the largest weight is no longer
+// exactly 1, and the rounding of the weights to bf16 costs 1.5e-3 of the result
+// instead of 1.07e-3.)
+// What bounds it: per 64 tokens and 256 rows 1024 cycles of the special function
+// units and 1280 of the tensor cores (the scores read 48 KB of shared memory a
+// tile, at 128 bytes a cycle).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -31,9 +36,11 @@ namespace vt {
 namespace {
 
 constexpr int kTileRows = 128;
-constexpr int kTileTokens = 128;
+constexpr int kTileTokens = 128;  // of a K or V tile
+constexpr int kStep = 64;         // tokens of a step
 constexpr int kKvStages = 2;
-constexpr int kMmaThreads = 320;  // two softmax warpgroups, the MMA warp, the load warp
+constexpr int kMmaThreads = 352;  // two softmax warpgroups, an MMA warp to each, the load warp
+constexpr int kMmaWarp = 8, kLoadWarp = 10;
 constexpr int kMaskRing = 8;      // tiles whose token masks are kept
 
 template <int D>
@@ -46,38 +53,51 @@ struct MmaSmem {
   static constexpr int kBytes = kV + kKvStages * kTile + 1024;  // room to align to 1024
 };
 
-// tensor memory columns: S of both tiles, O of both; P in S's own columns where
-// there is no room beside them (head_dim 128)
+// tensor memory columns: two S buffers of each tile, then O of each tile; P lies
+// over the first half of the S it was made from
 template <int D>
 struct Tmem {
-  static constexpr int kS = 0, kO = 2 * kTileTokens;
-  static constexpr bool kShared = D > 64;
-  static constexpr int kP = kShared ? 0 : kO + 2 * D;
-  static constexpr int kPStep = kShared ? kTileTokens : kTileTokens / 2;
+  static constexpr int kO = 4 * kStep;
+  static __device__ __forceinline__ uint32_t s(int t, int j) {
+    return (uint32_t)((t * 2 + (j & 1)) * kStep);
+  }
 };
 
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  // start address, leading and stride byte offsets in 16-byte units; descriptor
-  // version 1; 128-byte swizzle
-  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(lbo >> 4) << 16) |
-         ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared memory descriptors: start address, leading and stride byte offsets in
+// 16-byte units; descriptor version 1; 128-byte swizzle.  Only the low word moves
+// from one MMA to the next.
+__device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t sbo) {
+  return (sbo >> 4) | (1u << 14) | (2u << 29);
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3ffff) >> 4) | ((lbo >> 4) << 16);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                       uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi,
+                                       uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
+}
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -157,7 +177,9 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
 
 struct Bars {
   uint64_t k_full[kKvStages], k_empty[kKvStages], v_full[kKvStages], v_empty[kKvStages];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  // of each tile, by the parity of the step where a second step may begin before
+  // the first is noticed
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_done[2];
   uint64_t v_tail;  // the last V tile's rows past the end are zeros
 };
 
@@ -172,7 +194,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ uint32_t s_mask[kMaskRing][4];
   __shared__ int s_whole[kMaskRing];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // (through a shuffle, so that the roles' control flow and addresses are known to
+  // be the same in a warp: MMA operands live in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t base = (smem_addr(dyn) + 1023) & ~1023u;
   unsigned char* mem = dyn + (base - smem_addr(dyn));
 
@@ -185,6 +210,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const bool two = pair * 2 + 1 < a.prefix_tiles;
   const int t0 = split * a.prefix_chunk, t1 = min(t0 + a.prefix_chunk, a.prefix_len);
   const int n_tiles = (t1 - t0 + kTileTokens - 1) / kTileTokens;
+  const int n_steps = (t1 - t0 + kStep - 1) / kStep;
   // the split ends inside a block: what the copy brings from behind its end may be
   // anything, and a weight of 0 times NaN is NaN
   const int box = min(1 << a.shift, kTileTokens);  // tokens of a copy
@@ -210,18 +236,21 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     for (int i = 0; i < kKvStages; ++i) {
       mbar_init(&bars.k_full[i], 1);
       mbar_init(&bars.v_full[i], 1);
-      mbar_init(&bars.k_empty[i], 1);
-      mbar_init(&bars.v_empty[i], 1);
+      mbar_init(&bars.k_empty[i], two ? 2 : 1);  // (each tile's MMAs)
+      mbar_init(&bars.v_empty[i], two ? 2 : 1);
     }
     mbar_init(&bars.v_tail, 1);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars.s_full[t], 1);
-      mbar_init(&bars.p_full[t], kTileRows);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars.s_full[t][i], 1);
+        mbar_init(&bars.p_full[t][i], kTileRows);
+      }
       mbar_init(&bars.pv_done[t], 1);
+      mbar_init(&bars.o_done[t], 1);
     }
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_addr(&s_tmem))
                  : "memory");
@@ -231,10 +260,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   bool ok = true;
 
-  if (warp == 9) {
+  if (warp == kLoadWarp) {
     // ---- loads -----------------------------------------------------------------
     const int boxes = kTileTokens / box;
     int issued = 0;
@@ -265,7 +294,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       }
       __syncwarp();
       const int in_block = tok0 & ((1 << a.shift) - 1);  // (blocks longer than a tile)
-      ok = mbar_wait_bounded(&bars.k_empty[st], par);
+      ok = mbar_wait_clocked(&bars.k_empty[st], par);
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&bars.k_full[st], S::kTile);
       __syncwarp();
@@ -277,7 +306,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             tma_tile(base + S::kK + st * S::kTile + h * S::kHalf + i * box * 128, &map_k,
                      &bars.k_full[st], h * 64, in_block, kvh, blk[q]);
       }
-      ok = mbar_wait_bounded(&bars.v_empty[st], par);
+      ok = mbar_wait_clocked(&bars.v_empty[st], par);
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&bars.v_full[st], S::kTile);
       __syncwarp();
@@ -293,7 +322,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     if (ragged && issued == n_tiles) {
       const int j = n_tiles - 1, st = j % kKvStages;
-      ok = ok && mbar_wait_bounded(&bars.v_full[st], (j / kKvStages) & 1);
+      ok = ok && mbar_wait_clocked(&bars.v_full[st], (j / kKvStages) & 1);
       const int from = t1 - t0 - j * kTileTokens, to = (from + box - 1) / box * box;
       for (int i = from * 8 + lane; i < to * 8; i += 32)
         for (int h = 0; h < D / 64; ++h)
@@ -305,82 +334,72 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     // no copy is in flight when the CTA's memory goes to another
     for (int j = max(0, issued - kKvStages); j < issued; ++j) {
-      mbar_wait_bounded(&bars.k_full[j % kKvStages], (j / kKvStages) & 1, 100000000ull);
-      mbar_wait_bounded(&bars.v_full[j % kKvStages], (j / kKvStages) & 1, 100000000ull);
+      mbar_wait_clocked(&bars.k_full[j % kKvStages], (j / kKvStages) & 1, 200000000ll);
+      mbar_wait_clocked(&bars.v_full[j % kKvStages], (j / kKvStages) & 1, 200000000ll);
     }
-  } else if (warp == 8) {
+  } else if (warp >= kMmaWarp) {
     // ---- MMAs ------------------------------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-      // fp32 accumulators; K-major A and B; N = 128 tokens, M = 128
-      constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) |
-                                   ((kTileTokens / 8) << 17) | ((kTileRows / 16) << 24);
-      // B (V) is N-major: its rows are tokens; N = D
-      constexpr uint32_t kIdescO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) |
-                                   ((uint32_t)(D / 8) << 17) | ((kTileRows / 16) << 24);
-      auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
-        const uint32_t q = base + S::kQ + t * S::kTile,
-                       k = base + S::kK + (j % kKvStages) * S::kTile;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks / 4) * S::kHalf + (ks % 4) * 32;
-          mma_ss(tmem + TM::kS + t * kTileTokens, smem_desc(q + off, 16, 1024),
-                 smem_desc(k + off, 16, 1024), kIdescS, ks > 0);
-        }
-        mma_commit(&bars.s_full[t]);
-      };
-      auto values = [&](int t, int j) {  // O_t += P_t V_j
-        const uint32_t v = base + S::kV + (j % kKvStages) * S::kTile;
-#pragma unroll
-        for (int ks = 0; ks < kTileTokens / 16; ++ks)
-          mma_ts(tmem + TM::kO + t * D, tmem + TM::kP + t * TM::kPStep + ks * 8,
-                 smem_desc(v + ks * 16 * 128, S::kHalf, 1024), kIdescO, j > 0 || ks > 0);
-        mma_commit(&bars.pv_done[t]);
-      };
-      auto wait = [&](uint64_t* bar, int j) {
-        ok = ok && mbar_wait_bounded(bar, j & 1);
-        return ok;
-      };
-      auto wait_v = [&](int j) {
-        ok = ok && mbar_wait_bounded(&bars.v_full[j % kKvStages], (j / kKvStages) & 1);
-        if (ragged && j == n_tiles - 1) ok = ok && mbar_wait_bounded(&bars.v_tail, 0);
-        return ok;
-      };
-      auto wait_st = [&](uint64_t* bars_, int j) {
-        ok = ok && mbar_wait_bounded(&bars_[j % kKvStages], (j / kKvStages) & 1);
-        return ok;
-      };
-      for (int j = 0; j <= n_tiles; ++j) {
-        if (j < n_tiles) {
-          // S_0's columns: P_0 of the tile before has been used (head_dim 64: its
-          // scores have been read, which P_0 being there says)
-          if (!wait_st(bars.k_full, j)) break;
-          if (j > 0 && !wait(TM::kShared ? &bars.pv_done[0] : &bars.p_full[0], j - 1)) break;
+    // The whole warp walks the steps and waits; one lane issues.
+    constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    // fp32 accumulators; K-major A and B; N = 64 tokens, M = 128
+    constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) |
+                                 ((kStep / 8) << 17) | ((kTileRows / 16) << 24);
+    // B (V) is N-major: its rows are tokens; N = D
+    constexpr uint32_t kIdescO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) |
+                                 ((uint32_t)(D / 8) << 17) | ((kTileRows / 16) << 24);
+    constexpr uint32_t kHi = desc_hi(1024);
+    const uint32_t q_lo = desc_lo(base + S::kQ, 16), k_lo = desc_lo(base + S::kK, 16),
+                   v_lo = desc_lo(base + S::kV, S::kHalf);
+    const int t = warp - kMmaWarp;
+    const uint32_t a_lo = q_lo + t * (S::kTile >> 4), o = tmem + TM::kO + t * D;
+    // step j is half j & 1 of tile j / 2, which is in stage (j / 2) & 1
+    static_assert(kKvStages == 2, "stages by the parity of the tile");
+    if (t == 0 || two) {
+#pragma unroll 1
+      for (int j = -1; j < n_steps; ++j) {
+        const int n = j + 1, st_n = (n >> 1) & 1, st_j = (j >> 1) & 1;
+        if (n < n_steps) {  // S_t = Q_t K^T of the next step
+          if (!(n & 1)) ok = mbar_wait_clocked(&bars.k_full[st_n], (n >> 2) & 1);
+          // the buffer is free when the product with its last P is done
+          if (ok && j >= 1) ok = mbar_wait_clocked(&bars.pv_done[t], (j - 1) & 1);
+          if (!ok) break;
           fence_after();
-          scores(0, j);
-          if (!two) mma_commit(&bars.k_empty[j % kKvStages]);
-        }
-        if (two && j > 0) {
-          if (!wait(&bars.p_full[1], j - 1) || !wait_v(j - 1)) break;
-          fence_after();
-          values(1, j - 1);
-          mma_commit(&bars.v_empty[(j - 1) % kKvStages]);
-        }
-        if (j < n_tiles) {
-          if (two) {
-            if (TM::kShared && j > 0 && !wait(&bars.pv_done[1], j - 1)) break;
-            fence_after();
-            scores(1, j);
-            mma_commit(&bars.k_empty[j % kKvStages]);
+          if (elect_one()) {
+            const uint32_t d = tmem + TM::s(t, n),
+                           b_lo = k_lo + st_n * (S::kTile >> 4) + (n & 1) * (kStep * 128 >> 4);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = ((ks / 4) * S::kHalf + (ks % 4) * 32) >> 4;
+              mma_ss(d, a_lo + off, b_lo + off, kHi, kIdescS, ks > 0);
+            }
+            mma_commit(&bars.s_full[t][n & 1]);
+            if ((n & 1) || n == n_steps - 1) mma_commit(&bars.k_empty[st_n]);
           }
-          if (!wait(&bars.p_full[0], j) || !wait_v(j)) break;
+          __syncwarp();
+        }
+        if (j >= 0) {  // O_t += P_t V of this one
+          ok = mbar_wait_clocked(&bars.p_full[t][j & 1], (j >> 1) & 1);
+          if (ok && !(j & 1)) {
+            ok = mbar_wait_clocked(&bars.v_full[st_j], (j >> 2) & 1);
+            if (ok && ragged && (j >> 1) == n_tiles - 1) ok = mbar_wait_clocked(&bars.v_tail, 0);
+          }
+          if (!ok) break;
           fence_after();
-          values(0, j);
-          if (!two) mma_commit(&bars.v_empty[j % kKvStages]);
+          if (elect_one()) {
+            const uint32_t a_t = tmem + TM::s(t, j),
+                           b_lo = v_lo + st_j * (S::kTile >> 4) + (j & 1) * (kStep * 128 >> 4);
+#pragma unroll
+            for (int ks = 0; ks < kStep / 16; ++ks)
+              mma_ts(o, a_t + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO,
+                     ks > 0 ? 1u : (uint32_t)(j > 0));
+            mma_commit(&bars.pv_done[t]);
+            if ((j & 1) || j == n_steps - 1) mma_commit(&bars.v_empty[st_j]);
+            if (j == n_steps - 1) mma_commit(&bars.o_done[t]);
+          }
+          __syncwarp();
         }
       }
     }
-    __syncwarp();
   } else {
     // ---- softmax: warpgroup t, one thread to a row --------------------------------
     const int t = warp >> 2;
@@ -394,25 +413,24 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       // (a scale of 0 as one that leaves masked scores at -inf)
       const float sc = fmaxf(fabsf(a.scale_log2), 1e-30f);
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane (warp % 4) * 32
-      const uint32_t ts = tmem + lanes + TM::kS + t * kTileTokens;
-      const uint32_t tp = tmem + lanes + TM::kP + t * TM::kPStep;
       const uint32_t to = tmem + lanes + TM::kO + t * D;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n_tiles; ++j) {
-        ok = mbar_wait_bounded(&bars.s_full[t], j & 1);
+      for (int j = 0; j < n_steps; ++j) {
+        ok = mbar_wait_clocked(&bars.s_full[t][j & 1], (j >> 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
         fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(s[q], ts + q * 32);
+        const uint32_t ts = tmem + lanes + TM::s(t, j);
+        uint32_t s[2][32];
+        tmem_ld32(s[0], ts);
+        tmem_ld32(s[1], ts + 32);
         tmem_wait_ld();
+        loaded(s[0]);
+        loaded(s[1]);
+        const int tok0 = t0 + j * kStep, ring = (j >> 1) % kMaskRing;
+        if (!s_whole[ring] || tok0 + kStep > lim_min) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) loaded(s[q]);
-        const int tok0 = t0 + j * kTileTokens;
-        if (!s_whole[j % kMaskRing] || tok0 + kTileTokens > lim_min) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t mask = s_mask[j % kMaskRing][q];
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t mask = s_mask[ring][(j & 1) * 2 + q];
             const int left = lim - tok0 - q * 32;
             const uint32_t keep =
                 mask & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1);
@@ -423,23 +441,20 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < 32; i += 2)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][i]));
+          for (int q = 0; q < 4; ++q)
+            mx[q] = fmaxf(mx[q], __uint_as_float(s[q & 1][i + (q >> 1)]));
         const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc);
-        // (the products with the tile before are done: S_t was made after them, or
-        // with columns of its own P_t's barrier below has been waited for)
         const bool grow = m_new > m;
-        if (!TM::kShared && j > 0) {
-          ok = mbar_wait_bounded(&bars.pv_done[t], (j - 1) & 1);  // P_t's columns are free
-          if (!__all_sync(0xffffffffu, ok)) break;
-          fence_after();
-        }
         if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? ex2_approx(m - m_new) : 1.f;
           if (grow) m = m_new;
           l *= f;
           if (j > 0) {
+            ok = mbar_wait_clocked(&bars.pv_done[t], (j - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
@@ -455,30 +470,27 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         }
         const float off = m == -INFINITY ? 0.f : m;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t p[32];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t p[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int e = half * 64 + 2 * i;
-            const float p0 = ex2_approx(__fmaf_rn(__uint_as_float(s[e >> 5][e & 31]), sc, -off));
-            const float p1 =
-                ex2_approx(__fmaf_rn(__uint_as_float(s[e >> 5][(e & 31) + 1]), sc, -off));
-            sum[(2 * i) & 3] += p0;
-            sum[(2 * i + 1) & 3] += p1;
-            // the weights are rounded to the cache's type for the tensor cores (a
-            // relative 2^-9 in bf16, 2^-12 in fp16, each its own way); the sum is not
-            p[i] = pack2<T>(p0, p1);
-          }
-          tmem_st32(tp + half * 32, p);
+        for (int i = 0; i < 32; ++i) {
+          const int e = 2 * i;
+          const float p0 = ex2_approx(__fmaf_rn(__uint_as_float(s[e >> 5][e & 31]), sc, -off));
+          const float p1 =
+              ex2_approx(__fmaf_rn(__uint_as_float(s[e >> 5][(e & 31) + 1]), sc, -off));
+          sum[(2 * i) & 3] += p0;
+          sum[(2 * i + 1) & 3] += p1;
+          // the weights are rounded to the cache's type for the tensor cores (a
+          // relative 2^-9 in bf16, 2^-12 in fp16, each its own way); the sum is not
+          p[i] = pack2<T>(p0, p1);
         }
+        tmem_st32(ts, p);
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
         fence_before();
-        mbar_arrive(&bars.p_full[t]);
+        mbar_arrive(&bars.p_full[t][j & 1]);
       }
       // the row's part
-      if (ok) ok = mbar_wait_bounded(&bars.pv_done[t], (n_tiles - 1) & 1);
+      if (ok) ok = mbar_wait_clocked(&bars.o_done[t], 0);
       if (__all_sync(0xffffffffu, ok)) {
         fence_after();
         const int64_t at = (int64_t)split * a.B * a.hq + (int64_t)b * a.hq + head;
@@ -501,7 +513,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   if (!ok) atomicOr(a.err_word, kErrTimeout);
   fence_before();
   __syncthreads();
-  if (warp == 8)
+  if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
