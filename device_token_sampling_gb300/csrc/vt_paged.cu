@@ -21,7 +21,7 @@ struct vt_paged {
   int64_t part_rows = 0;  // rows of partial results the workspace holds
   float* d_part_o = nullptr;
   float2* d_part_ml = nullptr;
-  int32_t* d_err = nullptr;
+  int32_t* d_err = nullptr;  // the error word, then the attention's work counter
   int32_t* h_err = nullptr;
   cudaStream_t last_stream = nullptr;
   bool launched = false;
@@ -73,29 +73,35 @@ bool config_ok(const vt_paged_config& c) {
   return c.head_dim == 64 || c.head_dim == 128;
 }
 
-// How a call's work is split: so that the grid has about two rounds of the
-// CTAs the GPU holds, no split shorter than 64 (prefix) or 128 (own) tokens,
-// and the partial results fit the workspace.
+// How a call's work is split.  Units of about 256 tokens keep the warps busy to
+// the end and write 2 % of what they read as partial results; fewer where that
+// leaves warps without work, none shorter than 64 tokens.  The partial results
+// have to fit the workspace.
 void plan_attention(const vt_paged* h, int B, int prefix_len, int max_len, vt::AttnArgs& a) {
-  const int want = 4 * h->num_sms;
+  const int64_t warps = 8ll * h->num_sms;  // of unit_kernel, on the GPU at once
   const int64_t rows = (int64_t)B * a.hq;
   // more than one 16-row tile of rows behind the prefix: the tensor-memory kernel,
   // 256 rows to a CTA, one CTA to an SM (below, that kernel would pad 128-row tiles)
   a.prefix_mma = prefix_len > 0 && (int64_t)B * a.G > 16 && vt::prefix_mma_takes(a);
-  a.prefix_tiles = (int)ceil_div((int64_t)B * a.G, a.prefix_mma ? 128 : 16);
-  a.own_tiles = (int)ceil_div(a.G, 16);
+  // rows of the other units: 8, the width of their MMAs, unless more heads share a
+  // kv head or more rows the prefix
+  a.unit_rows = a.G > 8 || (prefix_len > 0 && !a.prefix_mma && (int64_t)B * a.G > 8) ? 16 : 8;
+  a.prefix_tiles = (int)ceil_div((int64_t)B * a.G, a.prefix_mma ? 128 : a.unit_rows);
+  a.own_tiles = (int)ceil_div(a.G, a.unit_rows);
   const int64_t own_len = std::max(1, max_len - (prefix_len & ~15));
-  int64_t sp = 0, so;
-  const int step = a.prefix_mma ? 128 : 64;  // tokens a split is a multiple of
-  if (a.prefix_mma)
-    // splits so that the grid is one round of CTAs
+  // splits of `len` tokens for `each` units a split
+  auto splits = [&](int64_t len, int64_t each) {
+    const int64_t fill = ceil_div(warps, each);
+    return std::clamp<int64_t>(std::max(fill, ceil_div(len, 256)), 1, ceil_div(len, 64));
+  };
+  const int step = a.prefix_mma ? 128 : 64;  // tokens a prefix split is a multiple of
+  int64_t sp = 0;
+  if (a.prefix_mma)  // so that the grid is one round of CTAs
     sp = std::clamp<int64_t>(h->num_sms / std::max<int64_t>(1, ceil_div(a.prefix_tiles, 2) * a.hkv),
                              1, std::min<int64_t>(64, ceil_div(prefix_len, step)));
   else if (prefix_len > 0)
-    sp = std::clamp<int64_t>(ceil_div(want, (int64_t)a.prefix_tiles * a.hkv), 1,
-                             std::min<int64_t>(64, ceil_div(prefix_len, 64)));
-  so = std::clamp<int64_t>(ceil_div(want, (int64_t)a.own_tiles * a.hkv * B), 1,
-                           std::min<int64_t>(32, ceil_div(own_len, 128)));
+    sp = std::min<int64_t>(64, splits(prefix_len, (int64_t)a.prefix_tiles * a.hkv));
+  int64_t so = std::min<int64_t>(64, splits(own_len, (int64_t)a.own_tiles * a.hkv * B));
   while ((sp + so) * rows > h->part_rows && (sp > 1 || so > 1)) {
     if (sp >= so) --sp;
     else --so;
@@ -132,8 +138,8 @@ int vt_paged_create(const vt_paged_config* config, vt_paged** out) {
   if (ok) {
     h->num_sms = prop.multiProcessorCount;
     ok = vt::prepare_tables() == cudaSuccess && vt::prepare_prefix_attention() == cudaSuccess &&
-         cudaMalloc(&h->d_err, sizeof(int32_t)) == cudaSuccess &&
-         cudaMemset(h->d_err, 0, sizeof(int32_t)) == cudaSuccess &&
+         cudaMalloc(&h->d_err, 2 * sizeof(int32_t)) == cudaSuccess &&
+         cudaMemset(h->d_err, 0, 2 * sizeof(int32_t)) == cudaSuccess &&
          cudaMallocHost(&h->h_err, sizeof(int32_t)) == cudaSuccess;
   }
   if (ok && config->q_heads > 0) {
@@ -300,6 +306,8 @@ int vt_paged_attention(vt_paged* h, int32_t dtype, int32_t B, const void* q, int
   a.part_ml = h->d_part_ml;
   a.out = out;
   a.lse = out_lse;
+  a.work = h->d_err + 1;
+  a.num_sms = h->num_sms;
   a.err_word = h->d_err;
   cudaStream_t st = (cudaStream_t)stream;
   VT_TRY(h, vt::launch_prefix_attention(a, dtype, c.head_dim, st));

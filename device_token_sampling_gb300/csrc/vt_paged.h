@@ -54,14 +54,17 @@ struct AttnArgs {
   float scale_log2;            // scale * log2(e)
   // the work: prefix units first, then the requests' own units
   int32_t prefix_mma;          // the prefix runs on prefix_kernel, 128 rows to a tile
-  int32_t prefix_tiles;        // row tiles (16 or 128 rows) of one kv head's B * G rows
+  int32_t unit_rows;           // rows of unit_kernel's units: 8 or 16
+  int32_t prefix_tiles;        // row tiles (unit_rows or 128 rows) of one kv head's B * G rows
   int32_t prefix_splits, prefix_chunk;  // splits of [0, prefix_len), tokens in each
-  int32_t own_tiles;           // 16-row tiles of G heads
+  int32_t own_tiles;           // unit_rows-row tiles of G heads
   int32_t own_splits, own_chunk;
   float* part_o;               // [splits][B * hq][d] fp32, not normalised
   float2* part_ml;             // [splits][B * hq] (max in log2 units, sum)
   void* out;                   // [B][hq][d]
   float* lse;                  // [B][hq] or null
+  int32_t* work;               // units taken; 0 between calls
+  int32_t num_sms;
   int32_t* err_word;
 };
 // dtype as VT_DTYPE_BF16 / VT_DTYPE_F16; head_dim 64 or 128.

@@ -18,9 +18,8 @@
 namespace vt {
 namespace {
 
-constexpr int kRows = 16;      // query rows of a unit (one mma tile)
 constexpr int kGroup = 16;     // tokens a warp takes at a time
-constexpr int kSplitWarps = 4;
+constexpr int kUnitWarps = 4;
 constexpr int kStages = 3;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
@@ -33,6 +32,18 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// 16 bytes global -> shared, zeros where !ok.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
                : "memory");
 }
 
@@ -72,280 +83,313 @@ struct Elem<__half> {
 };
 
 template <int D>
-struct SplitSmem {
+struct UnitSmem {
   static constexpr int kPitch = D + 8;                      // elements: rows 16 bytes apart in banks
   static constexpr int kTile = kGroup * kPitch;             // elements of K (or V) of a group
   static constexpr int kWarpElems = kStages * 2 * kTile;
-  static constexpr int kQElems = kRows * kPitch;
-  static constexpr size_t kBytes = 2 * ((size_t)kSplitWarps * kWarpElems + kQElems);
-  static_assert(kWarpElems * 2 >= kRows * D * 4, "a warp's stages hold its accumulators");
+  static constexpr size_t kBytes = 2 * (size_t)kUnitWarps * kWarpElems;
 };
 
-// One unit: 16 query rows of one kv head against the tokens [t0, t1) of one
-// table.  Each of the four warps takes every fourth group of 16 tokens through
-// its own ring of bulk copies, with its own running maximum and sum; the four
-// are joined at the end.
-template <typename T, int D>
-__global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(AttnArgs a) {
-  using S = SplitSmem<D>;
-  extern __shared__ __align__(128) unsigned char dyn[];
-  __shared__ uint64_t bars[kSplitWarps][kStages];
-  __shared__ float s_m[kSplitWarps][kRows], s_l[kSplitWarps][kRows];
-  __shared__ int s_lim[kRows];
-  __shared__ uint32_t s_mask[kSplitWarps][kStages];
-  T* sq = reinterpret_cast<T*>(dyn);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  T* ring = sq + S::kQElems + warp * S::kWarpElems;
-
-  // which unit
-  int u = blockIdx.x;
-  const int n_prefix_units = a.prefix_mma ? 0 : a.prefix_tiles * a.hkv * a.prefix_splits;
-  const bool prefix = u < n_prefix_units;
-  int kvh, tile, split, b0 = 0, t0, t1;
+// A unit of work: 8 or 16 query rows of one kv head against the tokens [t0, t1)
+// of one table.
+struct Unit {
+  int kvh, tile, split, b;  // b < 0: the prefix, for the rows of all requests
+  int t0, t1;
   const int32_t* table;
-  if (prefix) {
-    kvh = u % a.hkv;
-    tile = (u / a.hkv) % a.prefix_tiles;
-    split = u / (a.hkv * a.prefix_tiles);
-    table = a.prefix_blocks;
-    t0 = split * a.prefix_chunk;
-    t1 = min(t0 + a.prefix_chunk, a.prefix_len);
-  } else {
-    u -= n_prefix_units;
-    kvh = u % a.hkv;
-    tile = (u / a.hkv) % a.own_tiles;
-    b0 = (u / (a.hkv * a.own_tiles)) % a.B;
-    split = u / (a.hkv * a.own_tiles * a.B);
-    table = a.table + (int64_t)b0 * a.ld_table;
-    const int len = min(max(a.seq_lens[b0], 0), a.cols << a.shift);
-    const int base = a.prefix_len & ~(kGroup - 1);
-    // a longer request than the host reckoned with gets longer splits
-    const int even = ((len - base + a.own_splits - 1) / a.own_splits + kGroup - 1) &
-                     ~(kGroup - 1);
-    const int chunk = max(a.own_chunk, even);
-    const int64_t lo = base + (int64_t)split * chunk;
-    t0 = (int)(lo < a.prefix_len ? a.prefix_len : lo < len ? lo : len);
-    t1 = (int)(lo + chunk < len ? lo + chunk : len);
+};
+
+__device__ __forceinline__ Unit unit_of(const AttnArgs& a, int u) {
+  Unit n;
+  const int n_prefix = a.prefix_mma ? 0 : a.prefix_tiles * a.hkv * a.prefix_splits;
+  if (u < n_prefix) {
+    n.kvh = u % a.hkv;
+    n.tile = (u / a.hkv) % a.prefix_tiles;
+    n.split = u / (a.hkv * a.prefix_tiles);
+    n.b = -1;
+    n.table = a.prefix_blocks;
+    n.t0 = n.split * a.prefix_chunk;
+    n.t1 = min(n.t0 + a.prefix_chunk, a.prefix_len);
+    return n;
   }
-  const int n_rows = prefix ? a.B * a.G : a.G;
-  if (tid < kRows) {
-    const int r = tile * kRows + tid;
-    int lim = 0;
-    if (r < n_rows) lim = prefix ? min(max(a.seq_lens[r / a.G], 0), a.prefix_len) : t1;
-    s_lim[tid] = lim;
-  }
-  for (int i = tid; i < kRows * (D / 8); i += kSplitWarps * 32) {
-    const int r = tile * kRows + i / (D / 8), c = (i % (D / 8)) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < n_rows) {
-      const int b = prefix ? r / a.G : b0, g = prefix ? r % a.G : r;
-      v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + b * a.q_row +
-                                          (kvh * a.G + g) * a.q_head + c);
+  u -= n_prefix;
+  n.kvh = u % a.hkv;
+  n.tile = (u / a.hkv) % a.own_tiles;
+  n.b = (u / (a.hkv * a.own_tiles)) % a.B;
+  n.split = u / (a.hkv * a.own_tiles * a.B);
+  n.table = a.table + (int64_t)n.b * a.ld_table;
+  const int len = min(max(a.seq_lens[n.b], 0), a.cols << a.shift);
+  const int base = a.prefix_len & ~(kGroup - 1);
+  // a longer request than the host reckoned with gets longer splits
+  const int even = ((len - base + a.own_splits - 1) / a.own_splits + kGroup - 1) & ~(kGroup - 1);
+  const int chunk = max(a.own_chunk, even);
+  const int64_t lo = base + (int64_t)n.split * chunk;
+  n.t0 = (int)(lo < a.prefix_len ? a.prefix_len : lo < len ? lo : len);
+  n.t1 = (int)(lo + chunk < len ? lo + chunk : len);
+  return n;
+}
+
+// Every warp takes units off a common counter and runs them through its own ring
+// of copies, 16 tokens at a time, with its own running maxima and sums; the copies
+// of the next unit are under way while the last groups of one are worked on, so
+// that the stream of loads does not pause between units (with a CTA to a unit the
+// waits at its two ends were a third of the time).  Results do not depend on which
+// warp takes a unit.
+//
+// The products are S^T = K Q^T and O^T = V^T P^T: the 16 tokens (or dims) fill the
+// MMA's 16 rows and the query heads of a kv head only its 8 columns, NQ tiles of
+// them, where Q K^T would pad 4 or 8 heads to 16 rows.  P^T is S^T's fragment moved
+// by one transpose.  Tokens are copied 16 bytes a lane (a bulk copy a token would
+// be issued lane by lane).  What bounds it: HBM, with two groups (16 KB at head_dim
+// 128) in flight in each of 8 warps of an SM.
+template <typename T, int D, int NQ>
+__global__ void __launch_bounds__(kUnitWarps * 32) unit_kernel(AttnArgs a) {
+  using S = UnitSmem<D>;
+  constexpr int kRows = 8 * NQ;
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ int4 s_group[kUnitWarps][kStages];  // number, mask of its tokens, unit, last
+  __shared__ Unit s_unit[kUnitWarps][4];         // the units under way
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  T* ring = reinterpret_cast<T*>(dyn) + warp * S::kWarpElems;
+  const int n_units = (a.prefix_mma ? 0 : a.prefix_tiles * a.hkv * a.prefix_splits) +
+                      a.own_tiles * a.hkv * a.B * a.own_splits;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  const int64_t rows_all = (int64_t)a.B * a.hq;
+  // where row i of a unit is among the query heads of all requests, or -1
+  auto row_of = [&](const Unit& n, int i) -> int64_t {
+    const int r = n.tile * kRows + i;
+    if (n.b < 0) {
+      if (r >= a.B * a.G) return -1;
+      return (int64_t)(r / a.G) * a.hq + n.kvh * a.G + r % a.G;
     }
-    *reinterpret_cast<uint4*>(sq + (i / (D / 8)) * S::kPitch + c) = v;
-  }
-  if (lane < kStages) mbar_init(&bars[warp][lane], 1);
-  fence_mbar_init();
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncthreads();
-  int hi_lim = 0, lo_lim = 0x7fffffff;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    hi_lim = max(hi_lim, s_lim[i]);
-    if (tile * kRows + i < n_rows) lo_lim = min(lo_lim, s_lim[i]);
-  }
-  t1 = min(t1, hi_lim);
+    return r < a.G ? (int64_t)n.b * a.hq + n.kvh * a.G + r : -1;
+  };
+  auto slab_of = [&](const Unit& n) -> int64_t {
+    return (n.b < 0 ? n.split : a.prefix_splits + n.split) * rows_all;
+  };
+  auto pop = [&]() {
+    int u = 0;
+    if (lane == 0) u = atomicAdd(a.work, 1);
+    return u;  // (lane 0's)
+  };
 
-  float o[D / 8][4];
+  // ---- the side that issues copies
+  constexpr int kLanes = D / 8;              // lanes to a token
+  constexpr int kPerCopy = 32 / kLanes;      // tokens to a copy instruction
+  const int bs_mask = (1 << a.shift) - 1;
+  Unit in{};
+  int g = 0, g_end = 0, blk = -1;
+  int n_in = 0;    // units taken
+  int seq_in = 0;  // groups issued
+  int waiting = pop();
+  auto block_of = [&](int gg) {  // the block of token lane % 16 of group gg, or -1
+    const int t = gg * kGroup + (lane & 15);
+    return (gg < g_end && t >= in.t0 && t < in.t1) ? in.table[t >> a.shift] : -1;
+  };
+  auto next_unit = [&]() {
+    for (;;) {
+      const int u = __shfl_sync(0xffffffffu, waiting, 0);
+      if (u >= n_units) {
+        g = g_end = 0;
+        return;
+      }
+      waiting = pop();
+      in = unit_of(a, u);
+      if (in.b < 0) {  // no row attends past the longest
+        int lim = 0;
+        if (lane < kRows && in.tile * kRows + lane < a.B * a.G)
+          lim = max(a.seq_lens[(in.tile * kRows + lane) / a.G], 0);
+        in.t1 = min(in.t1, __reduce_max_sync(0xffffffffu, lim));
+      }
+      if (in.t0 < in.t1) break;
+      if (lane < kRows) {
+        const int64_t row = row_of(in, lane);
+        if (row >= 0) a.part_ml[slab_of(in) + row] = make_float2(-INFINITY, 0.f);
+      }
+    }
+    g = in.t0 >> 4;
+    g_end = (in.t1 + kGroup - 1) >> 4;
+    if (lane == 0) s_unit[warp][n_in & 3] = in;
+    ++n_in;
+    blk = block_of(g);
+  };
+  auto issue = [&]() {
+    if (g < g_end) {
+      const int st = seq_in % kStages;
+      const int t = g * kGroup + (lane & 15);
+      const bool fine = blk >= 0 && blk < a.num_blocks;
+      const uint32_t mask = __ballot_sync(0xffffffffu, fine) & 0xffffu;
+      if (!fine && t >= in.t0 && t < in.t1) atomicOr(a.err_word, kErrBadBlock);
+      if (lane == 0) s_group[warp][st] = make_int4(g, (int)mask, (n_in - 1) & 3, g + 1 == g_end);
+      // where this lane's token begins in the cache
+      const int64_t at = fine ? blk * a.block_stride + (t & bs_mask) * a.token_stride : 0;
+      blk = block_of(g + 1);
+      const int64_t col = in.kvh * a.head_stride + (lane % kLanes) * 8;
+      const uint32_t dst = smem_addr(ring + st * 2 * S::kTile + (lane / kLanes) * S::kPitch +
+                                     (lane % kLanes) * 8);
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  const int row0 = lane >> 2;
-  const int lim[2] = {s_lim[row0], s_lim[row0 + 8]};
+      for (int i = 0; i < kGroup / kPerCopy; ++i) {
+        const int token = i * kPerCopy + lane / kLanes;
+        const int64_t off = __shfl_sync(0xffffffffu, at, token) + col;
+        const bool ok = (mask >> token) & 1;
+        const uint32_t to = dst + i * kPerCopy * S::kPitch * (int)sizeof(T);
+        copy16(to, static_cast<const T*>(a.k) + off, ok);
+        copy16(to + S::kTile * (int)sizeof(T), static_cast<const T*>(a.v) + off, ok);
+      }
+      ++seq_in;
+      if (++g == g_end) next_unit();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  next_unit();
+#pragma unroll 1
+  for (int st = 0; st < kStages - 1; ++st) issue();
 
-  if (t0 < t1) {
-    uint32_t qf[D / 16][4];
+  // ---- the side that works on them
+  Unit n{};
+  float o[NQ][D / 16][4];
+  float m[NQ][2], l[NQ][2];
+  int lim[NQ][2], lo_lim = 0, unit = -1;
+  uint32_t qf[NQ][D / 16][2];
+#pragma unroll 1
+  for (int seq = 0; seq < seq_in; ++seq) {
+    issue();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    __syncwarp();
+    const int st = seq % kStages;
+    const int4 info = s_group[warp][st];
+    const int gg = info.x;
+    const uint32_t mask = (uint32_t)info.y;
+    if (unit != info.z) {  // the first group of a unit
+      unit = info.z;
+      n = s_unit[warp][info.z];
+      int lo = 0x7fffffff;
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t row = row_of(n, nq * 8 + (lane & 3) * 2 + h);
+          lim[nq][h] = n.t1;
+          if (n.b < 0 && row >= 0)
+            lim[nq][h] = min(max(a.seq_lens[row / a.hq], 0), a.prefix_len);
+          lo = min(lo, lim[nq][h]);
+          m[nq][h] = -INFINITY;
+          l[nq][h] = 0.f;
+        }
+        const int64_t row = row_of(n, nq * 8 + (lane >> 2)), r = max(row, (int64_t)0);
+        const T* q = static_cast<const T*>(a.q) + (r / a.hq) * a.q_row + (r % a.hq) * a.q_head +
+                     (lane & 3) * 2;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qf[nq][ks][i] =
+                row >= 0 ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + i * 8) : 0u;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[nq][i][j] = 0.f;
+      }
+      lo_lim = __reduce_min_sync(0xffffffffu, lo);
+    }
+    const T* sk = ring + st * 2 * S::kTile;
+    const T* sv = sk + S::kTile;
+    // two sums a tile: the chain of dependent MMAs is half as long
+    float s[NQ][2][4] = {};
     {
-      const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = (lane >> 4) * 8;
+      const uint32_t at = smem_addr(sk + ((lane & 7) + ((lane >> 3) & 1) * 8) * S::kPitch +
+                                    (lane >> 4) * 8);
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        ldsm_x4(qf[ks], smem_addr(sq + r * S::kPitch + ks * 16 + c));
-    }
-    const int g_first = (t0 >> 4) + warp, g_end = (t1 + kGroup - 1) >> 4;
-    const int bs_mask = (1 << a.shift) - 1;
-    const T* src = static_cast<const T*>(lane < 16 ? a.k : a.v) + kvh * a.head_stride;
-    // the block of this lane's token of group g, or -1
-    auto block_of = [&](int g) {
-      const int t = g * kGroup + (lane & 15);
-      return (g < g_end && t >= t0 && t < t1) ? table[t >> a.shift] : -1;
-    };
-    auto issue = [&](int g, int blk, int st) {
-      const int t = g * kGroup + (lane & 15);
-      const bool ok = blk >= 0 && blk < a.num_blocks;
-      const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-      if (lane == 0) {
-        s_mask[warp][st] = mask;
-        mbar_arrive_expect_tx(&bars[warp][st], __popc(mask) * 2 * D * (int)sizeof(T));
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t kf[4];
+        ldsm_x4(kf, at + ks * 32);
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+          Elem<T>::mma(s[nq][ks & 1], kf, qf[nq][ks][0], qf[nq][ks][1]);
       }
-      if (!ok && g < g_end && t >= t0 && t < t1) atomicOr(a.err_word, kErrBadBlock);
-      __syncwarp();
-      T* dst = ring + (st * 2 + (lane >> 4)) * S::kTile + (lane & 15) * S::kPitch;
-      if (ok) {
-        bulk_copy_g2s(dst, src + blk * a.block_stride + (t & bs_mask) * a.token_stride,
-                      D * (int)sizeof(T), &bars[warp][st]);
-      } else {  // zeros: a weight of 0 times whatever was there could be NaN
-#pragma unroll
-        for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
-      }
-      __syncwarp();
-    };
-    int blk = block_of(g_first);
-#pragma unroll
-    for (int st = 0; st < kStages - 1; ++st) {
-      const int g = g_first + st * kSplitWarps;
-      const int next = block_of(g + kSplitWarps);
-      if (g < g_end) issue(g, blk, st);
-      blk = next;
     }
-    int st = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int g = g_first; g < g_end; g += kSplitWarps) {
-      const int ahead = g + (kStages - 1) * kSplitWarps;
-      const int next = block_of(ahead + kSplitWarps);
-      if (ahead < g_end) issue(ahead, blk, st == 0 ? kStages - 1 : st - 1);
-      blk = next;
-      ok = mbar_wait_clocked(&bars[warp][st], phase);
-      if (!ok) break;
-      const uint32_t mask = s_mask[warp][st];
-      const T* sk = ring + st * 2 * S::kTile;
-      const T* sv = sk + S::kTile;
-      float s[2][4] = {};
-      {
-        const int r = (lane & 7) + (lane >> 4) * 8, c = ((lane >> 3) & 1) * 8;
+    uint32_t pf[NQ][2];
+    bool rescale = false;
+    float fix[NQ][2];
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t kf[4];
-          ldsm_x4(kf, smem_addr(sk + r * S::kPitch + ks * 16 + c));
-          Elem<T>::mma(s[0], qf[ks], kf[0], kf[1]);
-          Elem<T>::mma(s[1], qf[ks], kf[2], kf[3]);
+    for (int nq = 0; nq < NQ; ++nq) {
+      float z[4];  // tokens lane / 4 and 8 + lane / 4 of rows 2 (lane % 4) and the next
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = (s[nq][0][j] + s[nq][1][j]) * a.scale_log2;
+      if (mask != 0xffffu || (gg + 1) * kGroup > lo_lim) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = (lane >> 2) + (j >> 1) * 8;
+          if (!((mask >> c) & 1) || gg * kGroup + c >= lim[nq][j & 1]) z[j] = -INFINITY;
         }
       }
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[n][j] *= a.scale_log2;
-      if (mask != 0xffffu || (g + 1) * kGroup > lo_lim) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int c = n * 8 + (lane & 3) * 2 + (j & 1);
-            if (!((mask >> c) & 1) || g * kGroup + c >= lim[j >> 1]) s[n][j] = -INFINITY;
-          }
-      }
-      uint32_t pf[4];
-      float fix[2];
+      float p[4];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float mx = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[h], mx);
+        float mx = fmaxf(z[h], z[h + 2]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float mn = fmaxf(m[nq][h], mx);
         const float base = mn == -INFINITY ? 0.f : mn;
-        fix[h] = ex2_approx(m[h] - base);
-        m[h] = mn;
-        const float p0 = ex2_approx(s[0][2 * h] - base), p1 = ex2_approx(s[0][2 * h + 1] - base);
-        const float p2 = ex2_approx(s[1][2 * h] - base), p3 = ex2_approx(s[1][2 * h + 1] - base);
-        l[h] = l[h] * fix[h] + ((p0 + p1) + (p2 + p3));
-        // the weights are rounded to the cache's type for the tensor cores (a
-        // relative 2^-9 in bf16, 2^-12 in fp16, each its own way); their sum is not
-        pf[h] = Elem<T>::pack(p0, p1);
-        pf[h + 2] = Elem<T>::pack(p2, p3);
+        fix[nq][h] = ex2_approx(m[nq][h] - base);
+        rescale |= mn != m[nq][h];
+        m[nq][h] = mn;
+        p[h] = ex2_approx(z[h] - base);
+        p[h + 2] = ex2_approx(z[h + 2] - base);
+        l[nq][h] = l[nq][h] * fix[nq][h] + (p[h] + p[h + 2]);
       }
-      if (__any_sync(0xffffffffu, fix[0] != 1.f || fix[1] != 1.f)) {
+      // the weights are rounded to the cache's type for the tensor cores (a
+      // relative 2^-9 in bf16, 2^-12 in fp16, each its own way); their sum is not
+      pf[nq][0] = transpose8(Elem<T>::pack(p[0], p[1]));
+      pf[nq][1] = transpose8(Elem<T>::pack(p[2], p[3]));
+    }
+    if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= fix[0];
-          o[i][1] *= fix[0];
-          o[i][2] *= fix[1];
-          o[i][3] *= fix[1];
+      for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[nq][i][j] *= fix[nq][j & 1];
+    }
+    {
+      const uint32_t at = smem_addr(sv + ((lane & 7) + (lane >> 4) * 8) * S::kPitch +
+                                    ((lane >> 3) & 1) * 8);
+#pragma unroll
+      for (int dd = 0; dd < D / 16; ++dd) {
+        uint32_t vf[4];
+        ldsm_x4_t(vf, at + dd * 32);
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) Elem<T>::mma(o[nq][dd], vf, pf[nq][0], pf[nq][1]);
+      }
+    }
+    if (info.w) {  // the last group: the rows' parts
+      unit = -1;
+#pragma unroll
+      for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float sum = l[nq][h];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+          const int64_t row = row_of(n, nq * 8 + (lane & 3) * 2 + h);
+          if (row < 0) continue;
+          const int64_t at = slab_of(n) + row;
+          if (lane < 4) a.part_ml[at] = make_float2(m[nq][h], sum);
+          if (sum == 0.f) continue;
+          float* to = a.part_o + at * D + (lane >> 2);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            to[i * 16] = o[nq][i][h];
+            to[i * 16 + 8] = o[nq][i][h + 2];
+          }
         }
-      }
-      {
-        const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = (lane >> 4) * 8;
-#pragma unroll
-        for (int dd = 0; dd < D / 16; ++dd) {
-          uint32_t vf[4];
-          ldsm_x4_t(vf, smem_addr(sv + r * S::kPitch + dd * 16 + c));
-          Elem<T>::mma(o[2 * dd], pf, vf[0], vf[1]);
-          Elem<T>::mma(o[2 * dd + 1], pf, vf[2], vf[3]);
-        }
-      }
-      __syncwarp();
-      if (++st == kStages) {
-        st = 0;
-        phase ^= 1;
-      }
     }
-    if (!ok) {
-      // the copies in flight land before this CTA's shared memory goes to another
-      for (int i = 0; i < kStages; ++i) mbar_wait_clocked(&bars[warp][i], phase, 200000000ll);
-      atomicOr(a.err_word, kErrTimeout);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    }
+    __syncwarp();
   }
-
-  // join the four warps
-  float* so = reinterpret_cast<float*>(ring);
-  if ((lane & 3) == 0) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      s_m[warp][row0 + 8 * h] = m[h];
-      s_l[warp][row0 + 8 * h] = l[h];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<float2*>(so + (row0 + 8 * h) * D + i * 8 + (lane & 3) * 2) =
-          make_float2(o[i][2 * h], o[i][2 * h + 1]);
-  __syncthreads();
-  const int64_t rows_all = (int64_t)a.B * a.hq;
-  const int64_t slab = (prefix ? split : a.prefix_splits + split) * rows_all;
-  for (int i = tid; i < kRows * (D / 4); i += kSplitWarps * 32) {
-    const int rr = i / (D / 4), c = (i % (D / 4)) * 4;
-    const int r = tile * kRows + rr;
-    if (r >= n_rows) break;
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kSplitWarps; ++w) mm = fmaxf(mm, s_m[w][rr]);
-    const float base = mm == -INFINITY ? 0.f : mm;
-    float ll = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kSplitWarps; ++w) {
-      const float f = ex2_approx(s_m[w][rr] - base);
-      ll += s_l[w][rr] * f;
-      const float4 x = *reinterpret_cast<const float4*>(
-          reinterpret_cast<const float*>(sq + S::kQElems + w * S::kWarpElems) + rr * D + c);
-      acc.x += x.x * f;
-      acc.y += x.y * f;
-      acc.z += x.z * f;
-      acc.w += x.w * f;
-    }
-    const int b = prefix ? r / a.G : b0, g = prefix ? r % a.G : r;
-    const int64_t at = slab + (int64_t)b * a.hq + kvh * a.G + g;
-    if (c == 0) a.part_ml[at] = make_float2(mm, ll);
-    if (ll != 0.f) *reinterpret_cast<float4*>(a.part_o + at * D + c) = acc;
-  }
+  // (this grid's end then also means that of prefix_kernel, which it may overtake)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // One warp to a query head: rescale the parts to their common maximum, sum,
@@ -356,6 +400,8 @@ __global__ void __launch_bounds__(128) join_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t rows = (int64_t)a.B * a.hq;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.work = 0;  // for the next call
   if (row >= rows) return;
   const int splits = a.prefix_splits + a.own_splits;
   float mx = -INFINITY;
@@ -392,30 +438,51 @@ __global__ void __launch_bounds__(128) join_kernel(AttnArgs a) {
 
 template <typename T, int D>
 cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
-  using S = SplitSmem<D>;
+  using S = UnitSmem<D>;
   cudaError_t e;
   if (a.prefix_mma &&
       (e = launch_prefix_mma(a, std::is_same<T, __half>::value ? VT_DTYPE_F16 : VT_DTYPE_BF16, D,
                              stream)) != cudaSuccess)
     return e;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.stream = stream;
+  // beside prefix_kernel as its SMs get free; not before the work in front of that
+  cfg.numAttrs = a.prefix_mma ? 1 : 0;
   const int64_t units = (a.prefix_mma ? 0 : (int64_t)a.prefix_tiles * a.hkv * a.prefix_splits) +
                         (int64_t)a.own_tiles * a.hkv * a.B * a.own_splits;
-  split_kernel<T, D><<<(unsigned)units, kSplitWarps * 32, S::kBytes, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int64_t ctas = (units + kUnitWarps - 1) / kUnitWarps;
+  cfg.gridDim = dim3((unsigned)(ctas < 2 * a.num_sms ? ctas : 2 * a.num_sms));
+  cfg.blockDim = dim3(kUnitWarps * 32);
+  cfg.dynamicSmemBytes = S::kBytes;
+  e = a.unit_rows == 8 ? cudaLaunchKernelEx(&cfg, unit_kernel<T, D, 1>, a)
+                       : cudaLaunchKernelEx(&cfg, unit_kernel<T, D, 2>, a);
+  if (e != cudaSuccess) return e;
+  cfg.numAttrs = 1;
   const int64_t rows = (int64_t)a.B * a.hq;
-  join_kernel<T, D><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a);
 }
 
 }  // namespace
 
+template <typename T, int D>
+static cudaError_t prepare_units() {
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  const cudaError_t e = cudaFuncSetAttribute(unit_kernel<T, D, 1>, attr, UnitSmem<D>::kBytes);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(unit_kernel<T, D, 2>, attr, UnitSmem<D>::kBytes);
+}
+
 cudaError_t prepare_prefix_attention() {
   cudaError_t e;
-  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  if ((e = cudaFuncSetAttribute(split_kernel<__nv_bfloat16, 64>, attr, SplitSmem<64>::kBytes)) ||
-      (e = cudaFuncSetAttribute(split_kernel<__nv_bfloat16, 128>, attr, SplitSmem<128>::kBytes)) ||
-      (e = cudaFuncSetAttribute(split_kernel<__half, 64>, attr, SplitSmem<64>::kBytes)) ||
-      (e = cudaFuncSetAttribute(split_kernel<__half, 128>, attr, SplitSmem<128>::kBytes)))
+  if ((e = prepare_units<__nv_bfloat16, 64>()) || (e = prepare_units<__nv_bfloat16, 128>()) ||
+      (e = prepare_units<__half, 64>()) || (e = prepare_units<__half, 128>()))
     return e;
   return prepare_prefix_mma();
 }

@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const uint32_t base = (smem_addr(dyn) + 1023) & ~1023u;
   unsigned char* mem = dyn + (base - smem_addr(dyn));
 
+  asm volatile("griddepcontrol.launch_dependents;");
   int u = blockIdx.x;
   const int kvh = u % a.hkv;
   u /= a.hkv;
