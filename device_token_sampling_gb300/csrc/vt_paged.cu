@@ -74,8 +74,10 @@ bool config_ok(const vt_paged_config& c) {
 }
 
 // How a call's work is split.  Units of about 256 tokens keep the warps busy to
-// the end and write 2 % of what they read as partial results; fewer where that
-// leaves warps without work, none shorter than 64 tokens.  The partial results
+// the end and write 2 % of what they read as partial results (128 and 512 tokens
+// are 4 % slower on 256 requests of 512 tokens); shorter ones, down to 64 tokens,
+// until there are two for every warp (64 requests of 256 tokens: 25 us in units of
+// 128 tokens, 29 in units of 170).  The partial results
 // have to fit the workspace.
 void plan_attention(const vt_paged* h, int B, int prefix_len, int max_len, vt::AttnArgs& a) {
   const int64_t warps = 8ll * h->num_sms;  // of unit_kernel, on the GPU at once
@@ -91,7 +93,7 @@ void plan_attention(const vt_paged* h, int B, int prefix_len, int max_len, vt::A
   const int64_t own_len = std::max(1, max_len - (prefix_len & ~15));
   // splits of `len` tokens for `each` units a split
   auto splits = [&](int64_t len, int64_t each) {
-    const int64_t fill = ceil_div(warps, each);
+    const int64_t fill = ceil_div(2 * warps, each);
     return std::clamp<int64_t>(std::max(fill, ceil_div(len, 256)), 1, ceil_div(len, 64));
   };
   const int step = a.prefix_mma ? 128 : 64;  // tokens a prefix split is a multiple of

@@ -217,22 +217,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const int box = min(1 << a.shift, kTileTokens);  // tokens of a copy
   const bool ragged = t1 % box != 0;
 
-  // Q into swizzled shared memory, negated where the scale is negative
-  const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-  for (int i = tid; i < (two ? 2 : 1) * kTileRows * (D / 8); i += kMmaThreads) {
-    const int row = i / (D / 8), c = i % (D / 8);
-    const int r = pair * 2 * kTileRows + row;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < n_rows) {
-      const int b = r / a.G;
-      v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + b * a.q_row +
-                                          (kvh * a.G + r % a.G) * a.q_head + c * 8);
-      v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-    }
-    const int in = row % kTileRows;
-    *reinterpret_cast<uint4*>(mem + S::kQ + (row / kTileRows) * S::kTile + (c / 8) * S::kHalf +
-                              in * 128 + (((c & 7) ^ (in & 7)) << 4)) = v;
-  }
   if (tid == 0) {
     for (int i = 0; i < kKvStages; ++i) {
       mbar_init(&bars.k_full[i], 1);
@@ -257,10 +241,44 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   fence_before();
   __syncthreads();
   fence_after();
+  if (warp < kMmaWarp) {
+    // Q into swizzled shared memory, negated where the scale is negative, while the
+    // load warp begins; eight loads at once
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    constexpr int kAhead = 8, kChunks = D / 8;
+    const int all = (two ? 2 : 1) * kTileRows * kChunks;
+#pragma unroll 1
+    for (int i0 = tid; i0 < all; i0 += kMmaWarp * 32 * kAhead) {
+      uint4 v[kAhead];
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int i = i0 + q * kMmaWarp * 32, c = i % kChunks;
+        const int r = pair * 2 * kTileRows + i / kChunks;
+        v[q] = make_uint4(0, 0, 0, 0);
+        if (i < all && r < n_rows)
+          v[q] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                 (int64_t)(r / a.G) * a.q_row +
+                                                 (int64_t)(kvh * a.G + r % a.G) * a.q_head + c * 8);
+      }
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q) {
+        const int i = i0 + q * kMmaWarp * 32, c = i % kChunks, row = i / kChunks;
+        if (i >= all) break;
+        v[q].x ^= flip, v[q].y ^= flip, v[q].z ^= flip, v[q].w ^= flip;
+        const int in = row % kTileRows;
+        *reinterpret_cast<uint4*>(mem + S::kQ + (row / kTileRows) * S::kTile +
+                                  (c / 8) * S::kHalf + in * 128 + (((c & 7) ^ (in & 7)) << 4)) =
+            v[q];
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  // Q is there: all but the load warp
+  if (warp != kLoadWarp)
+    asm volatile("bar.sync 1, %0;" ::"n"(kLoadWarp * 32) : "memory");
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   bool ok = true;
 
