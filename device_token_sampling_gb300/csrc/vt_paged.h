@@ -32,8 +32,9 @@ struct TablesArgs {
   int64_t capacity;
   int32_t* status;             // [B]
   int32_t vec;                 // slots and positions 16-byte aligned
+  int32_t share;               // filled by launch_tables
 };
-cudaError_t launch_tables(const TablesArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_tables(TablesArgs a, int num_sms, cudaStream_t stream);
 
 // ---- attention behind a shared prefix (vt_prefix.cu) -------------------------
 struct AttnArgs {

@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kTabThreads = 512;
 constexpr int kTabWarps = kTabThreads / 32;
-constexpr int kTokensPerThread = 4;
+constexpr int kMaxShare = 512;  // tokens of the slot map a warp takes at a time
 constexpr int kColsPerItem = 256;
 
 struct RowNeed {
@@ -150,64 +150,67 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(TablesArgs a) {
     }
   }
 
-  // the slot map: four tokens in a row to a thread
-  const int64_t per_cta = (int64_t)kTabThreads * kTokensPerThread;
-  for (int64_t base = (int64_t)blockIdx.x * per_cta; base < a.capacity;
-       base += (int64_t)gridDim.x * per_cta) {
-    const int64_t t0 = base + (int64_t)tid * kTokensPerThread;
-    if (t0 >= a.capacity) continue;
-    int64_t slot[kTokensPerThread];
-    int32_t pos[kTokensPerThread];
+  // the slot map: a warp takes `share` tokens in a row, two neighbours a lane at a
+  // time; a lane looks its request up once and walks on from there
+  const int total = s_start[a.B];
+  for (int64_t base = ((int64_t)blockIdx.x * kTabWarps + warp) * a.share; base < a.capacity;
+       base += (int64_t)gridDim.x * kTabWarps * a.share) {
+    int r = -1, r_end = 0, off = -1, shift_pos = 0;
+    RowNeed n{};
+#pragma unroll 1
+    for (int i = 0; i < a.share; i += 64) {
+      const int64_t t0 = base + i + lane * 2;
+      if (t0 >= a.capacity) break;
+      longlong2 slot = make_longlong2(-1, -1);
+      int2 pos = make_int2(-1, -1);
 #pragma unroll
-    for (int i = 0; i < kTokensPerThread; ++i) {
-      slot[i] = -1;
-      pos[i] = -1;
-    }
-    if (t0 < s_start[a.B]) {
-      int lo = 0, hi = a.B;  // the request of t0: the last start at or below it that has tokens
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_start[mid] <= t0) lo = mid;
-        else hi = mid;
-      }
-      int r = lo;
-      RowNeed n = row_need(a, r);
-      int off = s_off[r];
-      int64_t len = a.seq_lens[r];
-#pragma unroll
-      for (int i = 0; i < kTokensPerThread; ++i) {
-        const int64_t t = t0 + i;
-        if (t < s_start[a.B]) {
-          if (t >= s_start[r + 1]) {
+      for (int e = 0; e < 2; ++e) {
+        const int64_t t64 = t0 + e;
+        if (t64 >= total) break;
+        const int t = (int)t64;
+        if (r < 0 || t >= r_end) {
+          if (r < 0) {  // the last request that starts at or before t: it holds t
+            int lo = 0, hi = a.B;
+            while (hi - lo > 1) {
+              const int mid = (lo + hi) >> 1;
+              if (s_start[mid] <= t) lo = mid;
+              else hi = mid;
+            }
+            r = lo;
+          } else {
             do ++r;
             while (t >= s_start[r + 1]);
-            n = row_need(a, r);
-            off = s_off[r];
-            len = a.seq_lens[r];
           }
-          if (off >= 0) {
-            const int p = (int)(len - n.query + (t - s_start[r]));
-            const int c = p >> a.shift;
-            const int id = c < n.held   ? a.table[(int64_t)r * a.ld + c]
-                           : c < n.have ? a.prefix[c]
-                                        : a.free_blocks[off + (c - n.have)];
-            pos[i] = p;
-            slot[i] = ((int64_t)id << a.shift) + (p & ((1 << a.shift) - 1));
-          }
+          r_end = s_start[r + 1];
+          n = row_need(a, r);
+          off = s_off[r];
+          shift_pos = (int)(a.seq_lens[r] - n.query) - s_start[r];
+        }
+        if (off < 0) continue;
+        const int p = t + shift_pos, c = p >> a.shift;
+        const int id = c < n.held   ? a.table[(int64_t)r * a.ld + c]
+                       : c < n.have ? a.prefix[c]
+                                    : a.free_blocks[off + (c - n.have)];
+        const int64_t at = ((int64_t)id << a.shift) + (p & ((1 << a.shift) - 1));
+        if (e == 0) {
+          pos.x = p;
+          slot.x = at;
+        } else {
+          pos.y = p;
+          slot.y = at;
         }
       }
-    }
-    if (a.vec && t0 + kTokensPerThread <= a.capacity) {
-      *reinterpret_cast<longlong2*>(a.slots + t0) = make_longlong2(slot[0], slot[1]);
-      *reinterpret_cast<longlong2*>(a.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
-      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kTokensPerThread; ++i)
-        if (t0 + i < a.capacity) {
-          a.slots[t0 + i] = slot[i];
-          a.positions[t0 + i] = pos[i];
+      if (a.vec && t0 + 1 < a.capacity) {
+        *reinterpret_cast<longlong2*>(a.slots + t0) = slot;
+        *reinterpret_cast<int2*>(a.positions + t0) = pos;
+      } else {
+        a.slots[t0] = slot.x;
+        a.positions[t0] = pos.x;
+        if (t0 + 1 < a.capacity) {
+          a.slots[t0 + 1] = slot.y;
+          a.positions[t0 + 1] = pos.y;
         }
+      }
     }
   }
 }
@@ -219,15 +222,19 @@ cudaError_t prepare_tables() {
                               (int)sizeof(int32_t) * (2 * VT_PAGED_MAX_BATCH + 1));
 }
 
-cudaError_t launch_tables(const TablesArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_tables(TablesArgs a, int num_sms, cudaStream_t stream) {
   const size_t smem = sizeof(int32_t) * (2 * (size_t)a.B + 1);
-  const int64_t tiles = (a.capacity + kTabThreads * kTokensPerThread - 1) /
-                        (kTabThreads * kTokensPerThread);
+  // shares so small that four CTAs an SM have one each, if the map is not longer
+  const int64_t most = 4 * num_sms;
+  const int64_t fill = (a.capacity + most * kTabWarps - 1) / (most * kTabWarps);
+  a.share = (int32_t)((fill < kMaxShare ? fill + 63 : kMaxShare) / 64 * 64);
+  if (a.share < 64) a.share = 64;
+  const int64_t tiles = (a.capacity + kTabWarps * a.share - 1) / (kTabWarps * a.share);
   const int64_t items =
       ((int64_t)a.B * ((a.cols + kColsPerItem - 1) / kColsPerItem) + 4 * kTabWarps - 1) /
       (4 * kTabWarps);
   int64_t grid = tiles > items ? tiles : items;
-  if (grid > 2 * num_sms) grid = 2 * num_sms;
+  if (grid > most) grid = most;
   if (grid < 1) grid = 1;
   tables_kernel<<<(unsigned)grid, kTabThreads, smem, stream>>>(a);
   return cudaGetLastError();
