@@ -362,11 +362,14 @@ struct Mail {
   int ok;
 };
 
-// The candidates of a row in vocabulary order, on its leader CTA.
-struct List {
-  uint32_t key[kList];  // ord_key of the tempered value
-  int idx[kList];
-};
+// A row's candidates are 64-bit entries: ord_key of the tempered value above the
+// complement of the index, so that a larger entry is earlier in the order (z
+// descending, index ascending), and a larger low half earlier in the vocabulary.
+__device__ __forceinline__ uint64_t entry_of(float z, int j) {
+  return ((uint64_t)ord_key(z) << 32) | (uint32_t)~j;
+}
+__device__ __forceinline__ float entry_z(uint64_t e) { return key_value((uint32_t)(e >> 32)); }
+__device__ __forceinline__ int entry_index(uint64_t e) { return (int)~(uint32_t)e; }
 
 struct Hist {
   uint32_t own[kBins];
@@ -389,14 +392,15 @@ struct Shared {
   uint64_t above;
   uint32_t digit_n[256];      // radix selection, 8 bits at a time
   unsigned long long digit_w[256];
+  uint64_t run[kThreadsF];  // inclusive masses of the threads' list entries
   union {
-    uint64_t run[kThreadsF];    // inclusive masses of the threads' list entries
-    uint64_t sorted[kList];     // (key, ~position in the list), descending
+    uint64_t found[kList];  // candidates, in any order
     uint16_t groups[kMaxSegs * kGroupsPerSeg / 2];  // groups to read, in order
   };
+  // (the list lies over hist.own; its buckets are in hist.sum)
   union {
     Hist hist;
-    List list;
+    uint64_t list[kList];  // candidates put in order
   };
 };
 
@@ -690,105 +694,97 @@ __device__ __noinline__ Cut radix_select(const Row<T>& row_in, Cut cut, uint64_t
 
 constexpr int kListDrop = 2;  // list masses: units of 2^(E - kElemBits + 2), 2048 below 2^62
 
-// sh.sorted[0, n), entries of (key, ~index), into the order (z descending, index
-// ascending).  Up to 512: every entry counts those ahead of it, the comparisons
-// shared out over all threads.  Beyond: a bitonic sort with four neighbouring
-// entries in each thread's registers, so that of the 66 steps over 2048 entries
-// 21 stay in a thread, 35 are shuffles and only 10 go through shared memory.
-constexpr int kSortPer = 4;
-static_assert(kSortPer * kThreadsF == kList, "a thread holds four entries of a full list");
-__device__ __noinline__ void sort_entries(int n) {
+// found[0, n) into list, by value (the order of the entries) or by index.  Up to
+// 512: every entry counts those ahead of it, the comparisons shared out over all
+// threads.  Beyond: into 4096 buckets, then each entry counts those ahead of it in
+// its bucket.  (A bitonic sort of 1400 entries took 20 000 cycles, this takes
+// 3000.)  z_least: no entry's value is below.
+template <bool BY_INDEX>
+__device__ __noinline__ void order_entries(int n, int V, float m, float z_least) {
   Shared& sh = smem();
   const int tid = threadIdx.x;
+  auto ahead_of = [](uint64_t e, uint64_t of) {
+    return BY_INDEX ? (uint32_t)e > (uint32_t)of : e > of;
+  };
   __syncthreads();
   if (n <= kThreadsF) {
     int parts = 1;  // threads that share an entry: neighbours, at most a warp
     while (parts < 32 && 2 * parts * n <= kThreadsF) parts *= 2;
     const int i = tid / parts, part = tid % parts;
-    const uint64_t mine = i < n ? sh.sorted[i] : 0ull;
+    const uint64_t mine = i < n ? sh.found[i] : 0ull;
     int ahead = 0;
     if (i < n)
-      for (int j = part; j < n; j += parts) ahead += sh.sorted[j] > mine;
+      for (int j = part; j < n; j += parts) ahead += ahead_of(sh.found[j], mine);
     for (int o = 1; o < parts; o *= 2) ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
-    __syncthreads();
-    if (i < n && part == 0) sh.sorted[ahead] = mine;
+    if (i < n && part == 0) sh.list[ahead] = mine;
     __syncthreads();
     return;
   }
-  int N = 128;
-  while (N < n) N *= 2;
-  const bool on = tid * kSortPer < N;  // whole warps
-  uint64_t v[kSortPer];
+  constexpr int kPer = kBins / kThreadsF;
+  const float per = (float)(kBins - 1) / fmaxf(m - z_least, 1e-30f);
+  int shift = 0;
+  while (((V - 1) >> shift) >= kBins) ++shift;
+  auto bucket_of = [&](uint64_t e) {
+    return BY_INDEX ? entry_index(e) >> shift
+                    : (int)fminf(fmaxf((m - entry_z(e)) * per, 0.f), (float)(kBins - 1));
+  };
+  uint32_t* bucket = sh.hist.sum;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) bucket[tid + q * kThreadsF] = 0;
   __syncthreads();
+  uint64_t e[kListPerThread];
+  int at[kListPerThread];
 #pragma unroll
-  for (int q = 0; q < kSortPer; ++q) {
-    const int i = tid * kSortPer + q;
-    v[q] = i < n ? sh.sorted[i] : 0ull;
-  }
-  for (int k = 2; k <= N; k <<= 1) {
-    int j = k >> 1;
-    if (j >= 32 * kSortPer) {
-      // through shared memory, all large steps of this merge
-      for (; j >= 32 * kSortPer; j >>= 1) {
-        __syncthreads();
-        if (on) {
-#pragma unroll
-          for (int q = 0; q < kSortPer; ++q) sh.sorted[q * kThreadsF + tid] = v[q];
-        }
-        __syncthreads();
-        if (on) {
-          const int other = tid ^ (j / kSortPer);
-          const bool lower = (tid & (j / kSortPer)) == 0;
-          const bool desc = ((tid * kSortPer) & k) == 0;
-#pragma unroll
-          for (int q = 0; q < kSortPer; ++q) {
-            const uint64_t o = sh.sorted[q * kThreadsF + other];
-            v[q] = (lower == desc) == (v[q] > o) ? v[q] : o;
-          }
-        }
-      }
-    }
-    if (on) {
-      for (; j >= kSortPer; j >>= 1) {
-        const int d = j / kSortPer;
-        const bool lower = (tid & d) == 0;
-        const bool desc = ((tid * kSortPer) & k) == 0;
-#pragma unroll
-        for (int q = 0; q < kSortPer; ++q) {
-          const uint64_t o = __shfl_xor_sync(0xffffffffu, v[q], d);
-          v[q] = (lower == desc) == (v[q] > o) ? v[q] : o;
-        }
-      }
-#pragma unroll
-      for (int jj = kSortPer / 2; jj > 0; jj >>= 1) {
-        if (jj > j) continue;
-#pragma unroll
-        for (int q = 0; q < kSortPer; ++q) {
-          if (q & jj) continue;
-          const bool desc = ((tid * kSortPer + q) & k) == 0;
-          const uint64_t x = v[q], y = v[q | jj];
-          const bool swap = desc ? x < y : x > y;
-          v[q] = swap ? y : x;
-          v[q | jj] = swap ? x : y;
-        }
-      }
-    }
+  for (int q = 0; q < kListPerThread; ++q) {
+    const int i = tid + q * kThreadsF;
+    e[q] = i < n ? sh.found[i] : 0ull;
+    at[q] = i < n ? (int)atomicAdd(&bucket[bucket_of(e[q])], 1u) : 0;
   }
   __syncthreads();
-  if (on) {
+  uint32_t c[kPer];
+  uint64_t sum = 0, all;
 #pragma unroll
-    for (int q = 0; q < kSortPer; ++q) sh.sorted[tid * kSortPer + q] = v[q];
+  for (int q = 0; q < kPer; ++q) {
+    c[q] = bucket[tid * kPer + q];
+    sum += c[q];
   }
+  uint32_t begin = (uint32_t)block_scan(sh, sum, &all);
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    bucket[tid * kPer + q] = begin;
+    begin += c[q];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kListPerThread; ++q)
+    if (tid + q * kThreadsF < n) sh.list[bucket[bucket_of(e[q])] + at[q]] = e[q];
+  __syncthreads();
+#pragma unroll 1
+  for (int q = 0; q < kListPerThread; ++q) {
+    if (tid + q * kThreadsF >= n) break;
+    const uint64_t mine = q == 0 ? e[0] : q == 1 ? e[1] : q == 2 ? e[2] : e[3];
+    const int b = bucket_of(mine), from = bucket[b], to = b + 1 < kBins ? bucket[b + 1] : n;
+    int place = from;
+    for (int i = from; i < to; ++i) place += ahead_of(sh.list[i], mine);
+    at[0] = q == 0 ? place : at[0];
+    at[1] = q == 1 ? place : at[1];
+    at[2] = q == 2 ? place : at[2];
+    at[3] = q == 3 ? place : at[3];
+  }
+  static_assert(kListPerThread == 4, "the entries of a thread above");
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kListPerThread; ++q)
+    if (tid + q * kThreadsF < n) sh.list[at[q]] = e[q];
   __syncthreads();
 }
-// The cut whose last element is entry i of the sorted list.
+// The cut whose last element is entry i of the list.
 __device__ __forceinline__ Cut sorted_cut(const Shared& sh, int i) {
-  const uint64_t e = sh.sorted[i];
-  return Cut{key_value((uint32_t)(e >> 32)), (int)~(uint32_t)e};
+  return Cut{entry_z(sh.list[i]), entry_index(sh.list[i])};
 }
-// Of the first n entries of the sorted list, those with a mass (list units) of at
-// most target before them: the cut, and their total mass in *all.  `share` >= 0:
-// the target is that part of the total instead.
+// Of the first n entries of the list, those with a mass (list units) of at most
+// target before them: the cut, and the mass of all n in *all.  `share` >= 0: the
+// target is that part of it instead.
 __device__ __forceinline__ Cut cut_by_mass(Shared& sh, const Mass& mass, int n, uint64_t target,
                                            float share, uint64_t* all) {
   const int tid = threadIdx.x;
@@ -796,7 +792,7 @@ __device__ __forceinline__ Cut cut_by_mass(Shared& sh, const Mass& mass, int n, 
 #pragma unroll
   for (int q = 0; q < kListPerThread; ++q) {
     const int i = tid * kListPerThread + q;
-    w[q] = i < n ? (mass.of(key_value((uint32_t)(sh.sorted[i] >> 32))) + 2) >> kListDrop : 0;
+    w[q] = i < n ? (mass.of(entry_z(sh.list[i])) + 2) >> kListDrop : 0;
     sum += w[q];
   }
   uint64_t a = block_scan(sh, sum, all);
@@ -809,6 +805,24 @@ __device__ __forceinline__ Cut cut_by_mass(Shared& sh, const Mass& mass, int n, 
   }
   kept = block_sum(sh, kept);
   return sorted_cut(sh, kept - 1);
+}
+
+// The lanes' marked elements (bit e of `take`: element at + e) to the CTA's found
+// entries, counted in sh.bin.  Whole warp.
+template <typename T>
+__device__ __forceinline__ void append(Shared& sh, const RowData<T>& rd, const Mass& mass, int at,
+                                       unsigned take) {
+  if (!__any_sync(0xffffffffu, take)) return;
+  const int c = __popc(take);
+  const int inc = warp_scan(c);
+  int q = 0;
+  if ((threadIdx.x & 31) == 31) q = atomicAdd(&sh.bin, inc);
+  q = __shfl_sync(0xffffffffu, q, 31) + inc - c;
+#pragma unroll 1
+  for (; take; take &= take - 1, ++q) {
+    const int j = at + __ffs(take) - 1;
+    if (q < kList) sh.found[q] = entry_of(mass.z(elem(rd.data[j])), j);
+  }
 }
 
 // The boundary of the elements kept by `cut` by linear histograms, which bracket
@@ -844,6 +858,7 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
   float top = rw.mx + 0.3f / per;
   uint64_t above = 0;  // mass (or elements) above the bracket
   int n = 0;
+  float x_lo = 0.f, x_hi = 0.f;  // of the last bracket
 #pragma unroll 1
   for (int level = 0;; ++level) {
     const Bins bins(top, per);
@@ -967,24 +982,12 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
             if (!PLAIN) in = in && cut.keeps(z, at + e);
             const bool up = x[e] >= x_up && in;
             take |= x[e] >= x_band && in && !up ? 1u << e : 0u;
-            // (a select, not a branch: the masses of a vector overlap)
+            // (a select, not a branch: the masses of a vector overlap.  Going through
+            // the lanes' marked elements alone is 9 % slower at p = 0.9.)
             if (MASS) up_w = rw.mass.add(up_w, up ? z : -INFINITY);
             else up_w += up;
           }
-          if (!__any_sync(0xffffffffu, take)) return;
-          const int c = __popc(take);
-          const int inc = warp_scan(c);
-          int q = 0;
-          if (lane == 31) q = atomicAdd(&sh.bin, inc);
-          q = __shfl_sync(0xffffffffu, q, 31) + inc - c;
-#pragma unroll 1
-          for (; take; take &= take - 1, ++q) {
-            const int e = __ffs(take) - 1;
-            if (q < kList) {
-              const float z = rw.mass.z(elem(rw.rd.data[at + e]));
-              sh.sorted[q] = ((uint64_t)ord_key(z) << 32) | (uint32_t)~(at + e);
-            }
-          }
+          append(sh, rw.rd, rw.mass, at, take);
         });
         up_w = warp_sum_u64(up_w);
       }
@@ -1009,11 +1012,13 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
     if (n <= kList) {
       if (rw.rank > 0) {  // behind the leader's own, in any order
         const int own = sh.mail.count[rw.rank];
-        uint64_t* to = rw.at(0)->sorted + base;
-        for (int i = tid; i < own; i += kThreadsF) to[i] = sh.sorted[i];
+        uint64_t* to = rw.at(0)->found + base;
+        for (int i = tid; i < own; i += kThreadsF) to[i] = sh.found[i];
       }
       rw.sync();
       if (n == 0) return false;
+      x_lo = x_band;
+      x_hi = x_up;
       break;
     }
     rw.sync();
@@ -1027,7 +1032,7 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
   if (rw.rank == 0) {
     bool ok = true;
     Cut found{0.f, kMaxIdx};
-    sort_entries(n);
+    order_entries<false>(n, rw.rd.V, rw.mass.z(fminf(x_hi, rw.mx)), rw.mass.z(x_lo));
     if (MASS) {
       // the boundary lies in the bracket: the mass above it is within the
       // target, that at its end is not
@@ -1038,8 +1043,8 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
       ok = ok && left < band;
       if (ok)
         for (int i = tid; i < n; i += kThreadsF) {
-          const int j = (int)~(uint32_t)sh.sorted[i];
-          const float z = key_value((uint32_t)(sh.sorted[i] >> 32));
+          const int j = entry_index(sh.list[i]);
+          const float z = entry_z(sh.list[i]);
           if (found.keeps(z, j))
             atomicAdd((unsigned long long*)&rw.at(j / kSeg / rw.per)->seg_w[j / kSeg],
                       (unsigned long long)rw.mass.of(z));
@@ -1280,90 +1285,52 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   // a warp takes kVecGroups groups with one 16-byte load a lane, in order
   constexpr int kLanes = kGroup / RowData<T>::N, kVecGroups = 32 / kLanes;
   const int rounds = (n_groups + kVecGroups - 1) / kVecGroups;
-  uint16_t* before = reinterpret_cast<uint16_t*>(sh.seg_w);  // candidates of each round
-  static_assert(sizeof(sh.seg_w) >= kList * sizeof(uint16_t), "a count for every round");
+  // (out of the way of the candidates, which lie over them)
+  static_assert(sizeof(sh.hist.sum) >= kList * sizeof(uint16_t), "the listed groups' room");
+  uint16_t* kept_groups = reinterpret_cast<uint16_t*>(sh.hist.sum);
+  constexpr int kAhead = 4;
+  for (int i = tid; i < n_groups; i += kThreadsF) kept_groups[i] = sh.groups[i];
+  if (tid == 0) sh.bin = 0;
+  __syncthreads();
   auto place = [&](int r) {
     const int g = r * kVecGroups + lane / kLanes;
-    return g < n_groups ? (int)sh.groups[g] * kGroup + (lane % kLanes) * RowData<T>::N : rw.rd.V;
+    return g < n_groups ? (int)kept_groups[g] * kGroup + (lane % kLanes) * RowData<T>::N
+                        : rw.rd.V;
   };
-  auto taken = [&](const uint4& v) {
-    float x[RowData<T>::N];
-    Vec<T>::unpack(v, x);
-    unsigned take = 0;
-#pragma unroll
-    for (int e = 0; e < RowData<T>::N; ++e) take |= x[e] >= x_least ? 1u << e : 0u;
-    return take;
-  };
-  constexpr int kAhead = 4;
 #pragma unroll 1
   for (int r0 = warp; r0 < rounds; r0 += kWarpsF * kAhead) {
     uint4 v[kAhead];
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) v[q] = rw.rd.raw(place(r0 + q * kWarpsF));
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      const int c = warp_sum_i(__popc(taken(v[q])));
-      if (lane == 0 && r0 + q * kWarpsF < rounds) before[r0 + q * kWarpsF] = (uint16_t)c;
-    }
-  }
-  __syncthreads();
-  uint64_t n64;
-  {
-    int c[kListPerThread];
-    uint64_t sum = 0;
-#pragma unroll
-    for (int q = 0; q < kListPerThread; ++q) {
-      const int r = tid * kListPerThread + q;
-      c[q] = r < rounds ? before[r] : 0;
-      sum += c[q];
-    }
-    uint64_t b = block_scan(sh, sum, &n64);
-    if (n64 > (uint64_t)kList) return false;
-#pragma unroll
-    for (int q = 0; q < kListPerThread; ++q) {
-      const int r = tid * kListPerThread + q;
-      if (r < rounds) before[r] = (uint16_t)b;
-      b += c[q];
-    }
-  }
-  const int n = (int)n64;
-  __syncthreads();
-  List& list = sh.list;
 #pragma unroll 1
-  for (int r0 = warp; r0 < rounds; r0 += kWarpsF * kAhead) {
-    unsigned take[kAhead];
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q) take[q] = taken(rw.rd.raw(place(r0 + q * kWarpsF)));
-#pragma unroll
     for (int q = 0; q < kAhead; ++q) {
-      const int c = __popc(take[q]);
-      const int inc = warp_scan(c);
-      if (r0 + q * kWarpsF >= rounds) break;
-      int at = before[r0 + q * kWarpsF] + inc - c;
-      const int p = place(r0 + q * kWarpsF);
-#pragma unroll 1
-      for (unsigned t = take[q]; t; t &= t - 1, ++at) {
-        const int j = p + __ffs(t) - 1;
-        list.key[at] = ord_key(rw.mass.z(elem(rw.rd.data[j])));
-        list.idx[at] = j;
-      }
+      float x[RowData<T>::N];
+      Vec<T>::unpack(v[0], x);
+      v[0] = v[1];
+      v[1] = v[2];
+      v[2] = v[3];
+      unsigned take = 0;
+#pragma unroll
+      for (int e = 0; e < RowData<T>::N; ++e) take |= x[e] >= x_least ? 1u << e : 0u;
+      append(sh, rw.rd, rw.mass, place(r0 + q * kWarpsF), take);
     }
   }
   __syncthreads();
-  for (int i = tid; i < n; i += kThreadsF)  // (over the groups' memory)
-    sh.sorted[i] = ((uint64_t)list.key[i] << 32) | (uint32_t)~list.idx[i];
-  sort_entries(n);
+  const int n = sh.bin;
+  if (n > kList) return false;
+  order_entries<false>(n, rw.rd.V, rw.m, rw.mass.z(x_least));
   int kept = 0;
-  for (int i = tid; i < n; i += kThreadsF) kept += key_value(list.key[i]) >= minp.z;
+  for (int i = tid; i < n; i += kThreadsF) kept += entry_z(sh.list[i]) >= minp.z;
   kept = min(block_sum(sh, kept), P.top_k);
   uint64_t total;
   const Cut cut = P.flags & kRowTopP ? cut_by_mass(sh, rw.mass, kept, 0, P.top_p, &total)
                                      : sorted_cut(sh, kept - 1);
+  order_entries<true>(n, rw.rd.V, 0.f, 0.f);
   // each thread holds a few neighbours of the list
   auto weight = [&](int i) -> uint64_t {
     if (i >= n) return 0;
-    const float z = key_value(list.key[i]);
-    return cut.keeps(z, list.idx[i]) ? (rw.mass.of(z) + 2) >> kListDrop : 0;
+    const float z = entry_z(sh.list[i]);
+    return cut.keeps(z, entry_index(sh.list[i])) ? (rw.mass.of(z) + 2) >> kListDrop : 0;
   };
   uint64_t mine = 0;
 #pragma unroll
@@ -1383,9 +1350,9 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
     uint64_t run = lo > 0 ? sh.run[lo - 1] : 0;
     int i = lo * kListPerThread;
     for (run += weight(i); run <= t; run += weight(i)) ++i;
-    a.out_tokens[o] = list.idx[i];
+    a.out_tokens[o] = entry_index(sh.list[i]);
     if (a.out_logprobs)
-      a.out_logprobs[o] = __fsub_rn(__fsub_rn(key_value(list.key[i]), rw.m), ln_s);
+      a.out_logprobs[o] = __fsub_rn(__fsub_rn(entry_z(sh.list[i]), rw.m), ln_s);
   }
   return true;
 }
