@@ -33,6 +33,7 @@ namespace vt {
 namespace {
 
 constexpr int kStreamThreads = 256;
+constexpr int kStreamCtas = 3;      // an SM (with four, 213 us instead of 187)
 constexpr int kThreadsF = 512;      // of finish_kernel
 constexpr int kWarpsF = kThreadsF / 32;
 constexpr int kSeg = kGivenSeg;     // elements a warp takes at a time, in vocabulary order
@@ -282,25 +283,56 @@ __device__ __forceinline__ bool sums_masses(const RowParams& P, int V) {
 }
 
 // One warp to a segment of 1024 logits, in registers (bf16: four 16-byte loads a
-// lane, fp32 eight).  What bounds it: HBM.  It keeps the loads of one segment a
-// warp in flight and needs no barrier.
+// lane, fp32 eight).  The next segment is on its way into the warp's own buffer of
+// shared memory, by one bulk copy, while this one is worked on (without that the
+// loads pause for the arithmetic: 1024 fp32 rows 210 us); segments that a bulk copy
+// cannot take (unaligned rows, a row's ragged end) are loaded directly.  What
+// bounds it: HBM.
 template <typename T>
-__global__ void __launch_bounds__(kStreamThreads, sizeof(T) == 2 ? 5 : 4)
-    stream_kernel(GivenArgs a) {
+__global__ void __launch_bounds__(kStreamThreads, kStreamCtas) stream_kernel(GivenArgs a) {
   using RD = RowData<T>;
+  extern __shared__ __align__(128) unsigned char dyn[];
   __shared__ uint2 table[kTable];
+  __shared__ uint64_t bars[kStreamThreads / 32];
   for (int i = threadIdx.x; i < kTable; i += kStreamThreads) table[i] = c_mass_table.v[i];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint4* buf = reinterpret_cast<const uint4*>(dyn) + warp * (kSeg * sizeof(T) / 16);
+  if (lane == 0) mbar_init(&bars[warp], 1);
+  fence_mbar_init();
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;");
-  const int lane = threadIdx.x & 31;
   const uint32_t items = (uint32_t)a.B * a.segs, step = gridDim.x * (kStreamThreads / 32);
-  for (uint32_t it = blockIdx.x * (kStreamThreads / 32) + (threadIdx.x >> 5); it < items;
-       it += step) {
+  // whether segment `it` comes by a bulk copy, and the copy
+  auto by_copy = [&](uint32_t it) {
+    return a.aligned && it < items && (int)(it % a.segs + 1) * kSeg <= a.V;
+  };
+  auto fetch = [&](uint32_t it) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars[warp], kSeg * sizeof(T));
+      bulk_copy_g2s(const_cast<uint4*>(buf),
+                    static_cast<const T*>(a.logits) + (it / a.segs) * a.ld +
+                        (int64_t)(it % a.segs) * kSeg,
+                    kSeg * sizeof(T), &bars[warp]);
+    }
+  };
+  uint32_t it = blockIdx.x * (kStreamThreads / 32) + warp, phase = 0;
+  if (by_copy(it)) fetch(it);
+  for (; it < items; it += step) {
     const int row = (int)(it / a.segs), seg = (int)(it % a.segs);
-    const RowData<T> rd{static_cast<const T*>(a.logits) + row * a.ld, a.V, a.aligned != 0};
     uint4 v[RD::kIters];
+    if (by_copy(it)) {
+      // (a wait that ran out leaves whatever is there; the call is reported)
+      if (!mbar_wait_clocked(&bars[warp], phase)) atomicOr(a.err_word, kErrTimeout);
+      phase ^= 1;
 #pragma unroll
-    for (int i = 0; i < RD::kIters; ++i) v[i] = rd.raw(RD::at(seg, i));
+      for (int i = 0; i < RD::kIters; ++i) v[i] = buf[i * 32 + lane];
+      __syncwarp();
+    } else {
+      const RowData<T> rd{static_cast<const T*>(a.logits) + row * a.ld, a.V, a.aligned != 0};
+#pragma unroll
+      for (int i = 0; i < RD::kIters; ++i) v[i] = rd.raw(RD::at(seg, i));
+    }
+    if (by_copy(it + step)) fetch(it + step);
     const RowParams P = a.params[row];
     float mx = -INFINITY;
     constexpr int kLanes = kGroup / RD::N;  // lanes of a group
@@ -697,10 +729,10 @@ constexpr int kListDrop = 2;  // list masses: units of 2^(E - kElemBits + 2), 20
 // found[0, n) into list, by value (the order of the entries) or by index.  Up to
 // 512: every entry counts those ahead of it, the comparisons shared out over all
 // threads.  Beyond: into 4096 buckets, then each entry counts those ahead of it in
-// its bucket.  (A bitonic sort of 1400 entries took 20 000 cycles, this takes
-// 3000.)  z_least: no entry's value is below.
+// its bucket.  (A bitonic sort of 1400 entries with few equal ones took 25 000
+// cycles, this takes 10 000.)
 template <bool BY_INDEX>
-__device__ __noinline__ void order_entries(int n, int V, float m, float z_least) {
+__device__ __noinline__ void order_entries(int n, int V) {
   Shared& sh = smem();
   const int tid = threadIdx.x;
   auto ahead_of = [](uint64_t e, uint64_t of) {
@@ -721,23 +753,48 @@ __device__ __noinline__ void order_entries(int n, int V, float m, float z_least)
     return;
   }
   constexpr int kPer = kBins / kThreadsF;
-  const float per = (float)(kBins - 1) / fmaxf(m - z_least, 1e-30f);
+  uint64_t e[kListPerThread];
+  uint64_t most = 0, least = ~0ull;
+#pragma unroll
+  for (int q = 0; q < kListPerThread; ++q) {
+    const int i = tid + q * kThreadsF;
+    e[q] = i < n ? sh.found[i] : 0ull;
+    if (i < n) {
+      most = max(most, e[q]);
+      least = min(least, e[q]);
+    }
+  }
+  float top = 0.f, per = 0.f;
+  if (!BY_INDEX) {  // the buckets span the entries' own values
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(most >> 32));
+    const uint32_t lo = __reduce_min_sync(0xffffffffu, (uint32_t)(least >> 32));
+    if ((tid & 31) == 0) {
+      sh.red_w[tid >> 5] = hi;
+      sh.red_n[tid >> 5] = lo;
+    }
+    __syncthreads();
+    uint64_t a = 0, b = ~0ull;
+    for (int i = 0; i < kWarpsF; ++i) {
+      a = max(a, sh.red_w[i]);
+      b = min(b, sh.red_n[i]);
+    }
+    top = key_value((uint32_t)a);
+    per = (float)(kBins - 1) / fmaxf(top - key_value((uint32_t)b), 1e-30f);
+  }
   int shift = 0;
   while (((V - 1) >> shift) >= kBins) ++shift;
   auto bucket_of = [&](uint64_t e) {
     return BY_INDEX ? entry_index(e) >> shift
-                    : (int)fminf(fmaxf((m - entry_z(e)) * per, 0.f), (float)(kBins - 1));
+                    : (int)fminf(fmaxf((top - entry_z(e)) * per, 0.f), (float)(kBins - 1));
   };
   uint32_t* bucket = sh.hist.sum;
 #pragma unroll
   for (int q = 0; q < kPer; ++q) bucket[tid + q * kThreadsF] = 0;
   __syncthreads();
-  uint64_t e[kListPerThread];
   int at[kListPerThread];
 #pragma unroll
   for (int q = 0; q < kListPerThread; ++q) {
     const int i = tid + q * kThreadsF;
-    e[q] = i < n ? sh.found[i] : 0ull;
     at[q] = i < n ? (int)atomicAdd(&bucket[bucket_of(e[q])], 1u) : 0;
   }
   __syncthreads();
@@ -858,7 +915,6 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
   float top = rw.mx + 0.3f / per;
   uint64_t above = 0;  // mass (or elements) above the bracket
   int n = 0;
-  float x_lo = 0.f, x_hi = 0.f;  // of the last bracket
 #pragma unroll 1
   for (int level = 0;; ++level) {
     const Bins bins(top, per);
@@ -1017,8 +1073,6 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
       }
       rw.sync();
       if (n == 0) return false;
-      x_lo = x_band;
-      x_hi = x_up;
       break;
     }
     rw.sync();
@@ -1032,7 +1086,7 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
   if (rw.rank == 0) {
     bool ok = true;
     Cut found{0.f, kMaxIdx};
-    order_entries<false>(n, rw.rd.V, rw.mass.z(fminf(x_hi, rw.mx)), rw.mass.z(x_lo));
+    order_entries<false>(n, rw.rd.V);
     if (MASS) {
       // the boundary lies in the bracket: the mass above it is within the
       // target, that at its end is not
@@ -1187,20 +1241,22 @@ __device__ int find_draw(const Row<T>& rw, const Cut& cut, uint64_t t, float* z_
   return idx;
 }
 
-// Whether the group maxima give a top-k row's candidates: at least twice top_k
-// groups, so that the elements that reach the top_k-th maximum are not many more.
-__device__ __forceinline__ bool listable(int top_k, int V) {
-  return top_k <= kListTopK && 2 * top_k <= V / kGroup;
+// Whether a filtered row is settled on the list: the whole row fits it, or the
+// group maxima give a top-k row's candidates (at least twice top_k groups, so that
+// the elements that reach the top_k-th maximum are not many more).
+__device__ __forceinline__ bool listable(const RowParams& P, bool topk, int V) {
+  if (V <= kList) return topk || (P.flags & kRowTopP);
+  return topk && P.top_k <= kListTopK && 2 * P.top_k <= V / kGroup;
 }
 
-// A listable top-k row, by one CTA: the groups that reach the top_k-th group
-// maximum hold its candidates, which go to the list; min-p, top-k and top-p are
+// A listable row, by one CTA: the groups that reach the top_k-th group maximum (a
+// row that fits: all) hold its candidates, which go to the list; min-p, top-k and top-p are
 // settled there and the draws made.  Returns false when the list does not hold
 // them.
 template <typename T>
 __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArgs& a,
-                                            const RowParams& P, const Cut minp, int row,
-                                            float ln_s) {
+                                            const RowParams& P, const Cut minp, int top_k,
+                                            int row, float ln_s) {
   Row<T> rw = row_in;  // in registers
   rw.mass.table = smem().table;
   Shared& sh = smem();
@@ -1222,36 +1278,39 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   };
   float g[kHold];
   hold(0, g);
+  const bool fits = a.V <= kList;
+  if (!fits) {
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kThreadsF] = 0;
-  if (tid == 0) sh.hi = kBins - 1;
-  __syncthreads();
+    for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kThreadsF] = 0;
+    if (tid == 0) sh.hi = kBins - 1;
+    __syncthreads();
 #pragma unroll 1
-  for (int b = 0; b < groups; b += kHold * kThreadsF) {
-    if (b > 0) hold(b, g);
+    for (int b = 0; b < groups; b += kHold * kThreadsF) {
+      if (b > 0) hold(b, g);
 #pragma unroll
-    for (int q = 0; q < kHold; ++q)
-      if (g[q] > -INFINITY) atomicAdd(&sh.hist.own[max(bin_no(bins.bin_f(g[q])), 0)], 1u);
-  }
-  __syncthreads();
-  {
-    uint32_t cn[kPer];
-    uint64_t tn = 0, unused;
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      cn[q] = sh.hist.own[tid * kPer + q];
-      tn += cn[q];
+      for (int q = 0; q < kHold; ++q)
+        if (g[q] > -INFINITY) atomicAdd(&sh.hist.own[max(bin_no(bins.bin_f(g[q])), 0)], 1u);
     }
-    uint64_t b = block_scan(sh, tn, &unused);
+    __syncthreads();
+    {
+      uint32_t cn[kPer];
+      uint64_t tn = 0, unused;
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) {
-      if (b < (uint64_t)P.top_k && b + cn[q] >= (uint64_t)P.top_k) sh.hi = tid * kPer + q;
-      b += cn[q];
+      for (int q = 0; q < kPer; ++q) {
+        cn[q] = sh.hist.own[tid * kPer + q];
+        tn += cn[q];
+      }
+      uint64_t b = block_scan(sh, tn, &unused);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        if (b < (uint64_t)top_k && b + cn[q] >= (uint64_t)top_k) sh.hi = tid * kPer + q;
+        b += cn[q];
+      }
     }
+    __syncthreads();
   }
-  __syncthreads();
   // (fewer than top_k groups with a finite element: every finite element)
-  const bool any = sh.hi == kBins - 1;
+  const bool any = fits || sh.hi == kBins - 1;
   if (warp == 0) {
     // (the far edge of that bin, a little further: a superset will do)
     const float edge =
@@ -1318,14 +1377,14 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   __syncthreads();
   const int n = sh.bin;
   if (n > kList) return false;
-  order_entries<false>(n, rw.rd.V, rw.m, rw.mass.z(x_least));
+  order_entries<false>(n, rw.rd.V);
   int kept = 0;
   for (int i = tid; i < n; i += kThreadsF) kept += entry_z(sh.list[i]) >= minp.z;
-  kept = min(block_sum(sh, kept), P.top_k);
+  kept = min(block_sum(sh, kept), top_k);
   uint64_t total;
   const Cut cut = P.flags & kRowTopP ? cut_by_mass(sh, rw.mass, kept, 0, P.top_p, &total)
                                      : sorted_cut(sh, kept - 1);
-  order_entries<true>(n, rw.rd.V, 0.f, 0.f);
+  order_entries<true>(n, rw.rd.V);
   // each thread holds a few neighbours of the list
   auto weight = [&](int i) -> uint64_t {
     if (i >= n) return 0;
@@ -1368,7 +1427,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
   const RowParams P = a.params[row];
   const bool greedy = P.flags & kRowGreedy;
   const bool topk = !greedy && P.top_k > 1 && P.top_k < a.V;
-  const bool from_list = topk && listable(P.top_k, a.V);
+  const bool from_list = !greedy && listable(P, topk, a.V);
   // rows that may read all their elements again are finished by the whole cluster
   const bool team = ctas > 1 && !greedy && !from_list &&
                     (topk || (P.flags & (kRowTopP | kRowMinP)));
@@ -1483,7 +1542,9 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
     }
     cut.z = fmaxf(cut.z, zt);
   }
-  if (from_list && draw_from_list(rw, a, P, cut, row, ln_s)) return;
+  if (from_list && (!masses || usable) &&
+      draw_from_list(rw, a, P, cut, topk ? P.top_k : a.V, row, ln_s))
+    return;
   if (topk) {
     // (an element count decides whether top-k cuts anything)
     int c = 0;
@@ -1539,12 +1600,16 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
 }
 
 template <typename T>
+constexpr size_t stream_smem() {
+  return kStreamThreads / 32 * kSeg * sizeof(T);
+}
+
+template <typename T>
 cudaError_t launch_given_typed(const GivenArgs& a, int num_sms, int ctas, cudaStream_t stream) {
   const int64_t warps = (int64_t)a.B * a.segs;
-  const int per_sm = sizeof(T) == 2 ? 5 : 4;  // as in its launch bounds
   int64_t grid = (warps + kStreamThreads / 32 - 1) / (kStreamThreads / 32);
-  if (grid > (int64_t)per_sm * num_sms) grid = (int64_t)per_sm * num_sms;
-  stream_kernel<T><<<(unsigned)grid, kStreamThreads, 0, stream>>>(a);
+  if (grid > (int64_t)kStreamCtas * num_sms) grid = (int64_t)kStreamCtas * num_sms;
+  stream_kernel<T><<<(unsigned)grid, kStreamThreads, stream_smem<T>(), stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -1568,8 +1633,11 @@ cudaError_t launch_given_typed(const GivenArgs& a, int num_sms, int ctas, cudaSt
 
 template <typename T>
 cudaError_t prepare_given_typed() {
-  const cudaError_t e = cudaFuncSetAttribute(
+  cudaError_t e = cudaFuncSetAttribute(
       finish_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(stream_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)stream_smem<T>());
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(finish_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
@@ -1585,7 +1653,12 @@ cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t strea
   int bits = 0;
   while ((1ll << bits) < a.V) ++bits;
   a.drop = max(kListDrop, bits + kElemBits - 62);
-  const int ctas = a.B <= 9 ? 16 : a.B <= 38 ? 8 : 4;
+  // CTAs that share the rows which are read again: as many as two to an SM hold for
+  // all rows, at least two (1024 fp32 rows: 491 us, with four 532; 256 bf16 rows: 127
+  // and 129), and eight segments to each (5 rows of 32003: 35 us with four or
+  // eight, 37 with sixteen; one row of 151936: 50 with eight, 46 with sixteen)
+  int ctas = 2;
+  while (ctas < kMaxCtas && 2 * ctas * a.B <= 2 * num_sms && 16 * ctas <= a.segs) ctas *= 2;
   return dtype == VT_DTYPE_F32 ? launch_given_typed<float>(a, num_sms, ctas, stream)
                                : launch_given_typed<__nv_bfloat16>(a, num_sms, ctas, stream);
 }

@@ -257,6 +257,7 @@ struct GivenArgs {
   int32_t* out_tokens;       // [B][draws]
   float* out_logprobs;       // [B][draws] or null
   int32_t* row_status;       // [B]
+  int32_t* err_word;
   // scratch, of the rows' segments: [B][segs] maxima and sums, [B][segs * 16]
   // group maxima
   float* seg_max;

@@ -1116,6 +1116,7 @@ int vt_sample_given(vt_sampler* h, const void* logits, int32_t dtype, int32_t B,
   a.out_tokens = out_tokens;
   a.out_logprobs = out_logprobs;
   a.row_status = h->d_status;
+  a.err_word = h->d_err;
   a.seg_sum = h->d_given_sum;
   a.seg_max = h->d_given_max;
   a.group_max = h->d_given_gmax;
