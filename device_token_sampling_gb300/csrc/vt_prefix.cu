@@ -466,7 +466,10 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a);
+  // (join_kernel would have set the counter back)
+  if (e != cudaSuccess) cudaMemsetAsync(a.work, 0, sizeof(int32_t), stream);
+  return e;
 }
 
 }  // namespace

@@ -588,6 +588,7 @@ cudaError_t prepare_prefix_mma() {
       (e = cudaFuncSetAttribute(prefix_kernel<__half, 64>, attr, MmaSmem<64>::kBytes)) ||
       (e = cudaFuncSetAttribute(prefix_kernel<__half, 128>, attr, MmaSmem<128>::kBytes)))
     return e;
+  encode_tiled();  // the driver's entry point, looked up once
   return cudaSuccess;
 }
 

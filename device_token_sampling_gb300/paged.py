@@ -195,9 +195,15 @@ class PagedBatch:
             raise ValueError(f"lse must be a contiguous float32 tensor [{B}, {q_heads}]")
         if made and stream is not None:
             _on_stream(stream, (out, lse))
+        # (the stride of a dimension of one element may be anything)
+        blocks = k_cache.shape[0]
+        s_block = kv[0] if blocks > 1 else block_size * kv_heads * d
+        s_token = kv[1] if block_size > 1 else kv_heads * d
+        s_head = kv[2] if kv_heads > 1 else d
         rc = self._lib.vt_paged_attention(
-            self._h, dtype, B, q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(),
-            v_cache.data_ptr(), k_cache.shape[0], kv[0], kv[1], kv[2], p_table, ld, p_seq,
+            self._h, dtype, B, q.data_ptr(), q.stride(0) if B > 1 else q_heads * d,
+            q.stride(1) if q_heads > 1 else d, k_cache.data_ptr(), v_cache.data_ptr(), blocks,
+            s_block, s_token, s_head, p_table, ld, p_seq,
             p_prefix, int(prefix_len), int(max_seq_len), d ** -0.5 if scale is None else scale,
             out.data_ptr(), lse.data_ptr(), raw_stream(stream, dev))
         if rc != VT_OK:

@@ -279,6 +279,58 @@ def test_attention_strides(layout):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,layout,bs,d,B,G,prefix", [
+    (BF, "HND", 16, 128, 40, 4, 300), (HF, "HND", 8, 64, 70, 2, 129), (BF, "NHD", 128, 64, 33, 8, 512),
+    (HF, "NHD", 256, 128, 20, 4, 700), (BF, "HND", 1024, 64, 20, 3, 1500),
+    (BF, "NHD", 4, 128, 20, 4, 77), (HF, "NHD", 32, 128, 300, 5, 2000), (BF, "NHD", 64, 128, 9, 32, 65),
+    (BF, "NHD", 16, 64, 129, 1, 4097), (HF, "HND", 64, 64, 18, 16, 64)])
+def test_attention_many_rows(dtype, layout, bs, d, B, G, prefix):
+    """More than sixteen rows behind the prefix, in both layouts, every block size's way of copying
+    a tile, one and several row tiles, splits that end inside a tile and inside a block."""
+    g = np.random.default_rng(B)
+    seq = prefix + g.integers(-prefix // 8, 80, B)
+    seq[g.integers(0, B)] = 0
+    check_attention(make_attention(B + d, seq, 2 * G, 2, d, bs, prefix, dtype, layout=layout), bs,
+                    prefix)
+
+
+@pytest.mark.gpu
+def test_attention_one_head_odd_strides():
+    """Dimensions of one element, whose strides say nothing."""
+    c = make_attention(15, [50], 1, 1, 64, 16, 0, BF)
+    one = torch.as_strided(c["q"], (1, 1, 64), (3, 5, 1))
+    k, v = (torch.as_strided(t, t.shape, (16 * 64, 64, 7, 1)) for t in (c["k"], c["v"]))
+    assert torch.equal(one, c["q"]) and torch.equal(k.nan_to_num(), c["k"].nan_to_num())
+    check_attention({**c, "q": one, "k": k, "v": v}, 16, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [3, 20])
+@pytest.mark.parametrize("scale", [2.0, -0.3, 0.0])
+def test_attention_scales(B, scale):
+    seq = [200, 150, 140] + [190 + i for i in range(B - 3)]
+    check_attention(make_attention(3, seq, 8, 2, 128, 16, 130, BF), 16, 130, scale=scale)
+
+
+@pytest.mark.gpu
+def test_attention_far_blocks():
+    """A cache past 2^31 elements: offsets of the last blocks need 64 bits."""
+    n, bs, hkv, d = 3000, 1024, 8, 128      # 3.1 G elements each
+    kc = torch.zeros((n, bs, hkv, d), dtype=BF, device="cuda")
+    vc = torch.zeros_like(kc)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(16)
+    pre = torch.tensor([2999, 2], dtype=torch.int32, device="cuda")
+    table = torch.tensor([[0, 0, 2998 - i] for i in range(20)], dtype=torch.int32, device="cuda")
+    for b in pre.tolist() + table[:, 2].tolist():
+        for c in (kc, vc):
+            c[b] = torch.randn((bs, hkv, d), generator=gen, device="cuda").to(BF)
+    q = torch.randn((20, 16, d), generator=gen, device="cuda").to(BF)
+    seq = torch.arange(20, dtype=torch.int32, device="cuda") * 40 + 2048
+    check_attention(dict(q=q, k=kc, v=vc, table=table, seq=seq, pre=pre, cols=3), bs, 2048)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("hint", [0, 1, 200, 4000])
 def test_attention_length_hint(hint):
     """The bound on the lengths shapes the launch only: a wrong one changes no result."""
