@@ -312,3 +312,32 @@ def test_refusals():
                                         None)))):
         with pytest.raises(ValueError):
             s.sample_given(*args, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,V", [(1, 151936), (3, 40000), (5, 5000), (160, 9000)])
+def test_top_p_of_half_precision_rows_with_many_equal_values(B, V):
+    """bf16 rows of few patterns under top-p: the boundary falls among equal elements, within a
+    segment and between two, on values of either sign and among the tiny ones; temperatures that
+    make patterns equal."""
+    g = torch.Generator(device="cuda").manual_seed(B + V)
+    x = torch.empty((B, V), dtype=torch.bfloat16, device="cuda")
+    for r in range(B):
+        n = torch.randint(0, 7, (V,), generator=g, device="cuda")
+        if r % 5 == 0:
+            x[r] = n.to(torch.bfloat16) - 3                     # seven values
+        elif r % 5 == 1:
+            x[r] = (n - 3).float() * 2.0 ** -14                 # all tiny
+            x[r, ::3] = 1.5
+        elif r % 5 == 2:
+            x[r] = -1.0 - (n % 2).float() / 128                 # two neighbouring patterns below 0
+        elif r % 5 == 3:
+            x[r] = torch.where(torch.arange(V, device="cuda") < 2048, 2.0, -8.0)
+        else:
+            x[r] = torch.where(n < 3, 0.5, -100.0 * n.float())  # spread over many octaves
+    u = uniforms(B, B, 5)
+    u[:, 0], u[:, 1] = 1 - 2.0 ** -24, 0.0
+    for kind in (dict(p=0.31), dict(p=0.77), dict(p=0.999), dict(p=1e-4), dict(T=0.7, p=0.6),
+                 dict(T=20.0, p=0.9), dict(T=1e30, p=0.45), dict(T=1e-3, p=0.45),
+                 dict(p=0.6, mp=0.2), dict(p=0.6, k=2000)):
+        run(x, u, [kind] * B)
