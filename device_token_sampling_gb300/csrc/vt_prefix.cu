@@ -19,7 +19,7 @@ namespace vt {
 namespace {
 
 constexpr int kGroup = 16;     // tokens a warp takes at a time
-constexpr int kUnitWarps = 4;
+constexpr int kUnitWarps = 8;  // on an SM
 constexpr int kStages = 3;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
@@ -86,8 +86,7 @@ template <int D>
 struct UnitSmem {
   static constexpr int kPitch = D + 8;                      // elements: rows 16 bytes apart in banks
   static constexpr int kTile = kGroup * kPitch;             // elements of K (or V) of a group
-  static constexpr int kWarpElems = kStages * 2 * kTile;
-  static constexpr size_t kBytes = 2 * (size_t)kUnitWarps * kWarpElems;
+  static constexpr size_t kBytes = 2 * (size_t)kStages * 2 * kTile;
 };
 
 // A unit of work: 8 or 16 query rows of one kv head against the tokens [t0, t1)
@@ -128,28 +127,34 @@ __device__ __forceinline__ Unit unit_of(const AttnArgs& a, int u) {
   return n;
 }
 
-// Every warp takes units off a common counter and runs them through its own ring
-// of copies, 16 tokens at a time, with its own running maxima and sums; the copies
-// of the next unit are under way while the last groups of one are worked on, so
-// that the stream of loads does not pause between units (with a CTA to a unit the
-// waits at its two ends were a third of the time).  Results do not depend on which
-// warp takes a unit.
+// Every warp, a CTA of its own, takes units off a common counter and runs them
+// through its ring of copies, 16 tokens at a time, with its own running maxima and
+// sums; the copies of the next unit are under way while the last groups of one are
+// worked on, so that the stream of loads does not pause between units (with a CTA
+// of four warps to a unit the waits at its two ends were a third of the time).
+// Results do not depend on which warp takes a unit.  One warp (27 KB) finds room
+// beside a CTA of prefix_kernel, which four do not: nearly half of the own tokens
+// are read while the tensor cores work on the prefix (256 requests, 16,384 shared
+// tokens and up to 1,024 of their own, head_dim 128: 169 us with CTAs of four
+// warps, 165 so; 37 requests of head_dim 64, where four have room too, 27.8 and
+// 29.8).
 //
 // The products are S^T = K Q^T and O^T = V^T P^T: the 16 tokens (or dims) fill the
 // MMA's 16 rows and the query heads of a kv head only its 8 columns, NQ tiles of
 // them, where Q K^T would pad 4 or 8 heads to 16 rows.  P^T is S^T's fragment moved
 // by one transpose.  Tokens are copied 16 bytes a lane (a bulk copy a token would
-// be issued lane by lane).  What bounds it: HBM, with two groups (16 KB at head_dim
-// 128) in flight in each of 8 warps of an SM.
+// be issued lane by lane).  What bounds it: HBM, in pieces of 256 bytes, with two
+// groups (16 KB at head_dim 128) in flight in each of 8 warps of an SM; 542 MB in
+// 106 us with the join (5.1 TB/s; 4 warps 121 us, 6 108).
 template <typename T, int D, int NQ>
-__global__ void __launch_bounds__(kUnitWarps * 32) unit_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(32) unit_kernel(AttnArgs a) {
   using S = UnitSmem<D>;
   constexpr int kRows = 8 * NQ;
   extern __shared__ __align__(128) unsigned char dyn[];
-  __shared__ int4 s_group[kUnitWarps][kStages];  // number, mask of its tokens, unit, last
-  __shared__ Unit s_unit[kUnitWarps][4];         // the units under way
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  T* ring = reinterpret_cast<T*>(dyn) + warp * S::kWarpElems;
+  __shared__ int4 s_group[kStages];  // number, mask of its tokens, unit, last
+  __shared__ Unit s_unit[4];         // the units under way
+  const int lane = threadIdx.x;
+  T* ring = reinterpret_cast<T*>(dyn);
   const int n_units = (a.prefix_mma ? 0 : a.prefix_tiles * a.hkv * a.prefix_splits) +
                       a.own_tiles * a.hkv * a.B * a.own_splits;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(kUnitWarps * 32) unit_kernel(AttnArgs a) {
     }
     g = in.t0 >> 4;
     g_end = (in.t1 + kGroup - 1) >> 4;
-    if (lane == 0) s_unit[warp][n_in & 3] = in;
+    if (lane == 0) s_unit[n_in & 3] = in;
     ++n_in;
     blk = block_of(g);
   };
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(kUnitWarps * 32) unit_kernel(AttnArgs a) {
       const bool fine = blk >= 0 && blk < a.num_blocks;
       const uint32_t mask = __ballot_sync(0xffffffffu, fine) & 0xffffu;
       if (!fine && t >= in.t0 && t < in.t1) atomicOr(a.err_word, kErrBadBlock);
-      if (lane == 0) s_group[warp][st] = make_int4(g, (int)mask, (n_in - 1) & 3, g + 1 == g_end);
+      if (lane == 0) s_group[st] = make_int4(g, (int)mask, (n_in - 1) & 3, g + 1 == g_end);
       // where this lane's token begins in the cache
       const int64_t at = fine ? blk * a.block_stride + (t & bs_mask) * a.token_stride : 0;
       blk = block_of(g + 1);
@@ -257,12 +262,12 @@ __global__ void __launch_bounds__(kUnitWarps * 32) unit_kernel(AttnArgs a) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     __syncwarp();
     const int st = seq % kStages;
-    const int4 info = s_group[warp][st];
+    const int4 info = s_group[st];
     const int gg = info.x;
     const uint32_t mask = (uint32_t)info.y;
     if (unit != info.z) {  // the first group of a unit
       unit = info.z;
-      n = s_unit[warp][info.z];
+      n = s_unit[info.z];
       int lo = 0x7fffffff;
 #pragma unroll
       for (int nq = 0; nq < NQ; ++nq) {
@@ -454,9 +459,9 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
   cfg.numAttrs = a.prefix_mma ? 1 : 0;
   const int64_t units = (a.prefix_mma ? 0 : (int64_t)a.prefix_tiles * a.hkv * a.prefix_splits) +
                         (int64_t)a.own_tiles * a.hkv * a.B * a.own_splits;
-  const int64_t ctas = (units + kUnitWarps - 1) / kUnitWarps;
-  cfg.gridDim = dim3((unsigned)(ctas < 2 * a.num_sms ? ctas : 2 * a.num_sms));
-  cfg.blockDim = dim3(kUnitWarps * 32);
+  const int64_t most = (int64_t)kUnitWarps * a.num_sms;
+  cfg.gridDim = dim3((unsigned)(units < most ? units : most));
+  cfg.blockDim = dim3(32);
   cfg.dynamicSmemBytes = S::kBytes;
   e = a.unit_rows == 8 ? cudaLaunchKernelEx(&cfg, unit_kernel<T, D, 1>, a)
                        : cudaLaunchKernelEx(&cfg, unit_kernel<T, D, 2>, a);
@@ -477,9 +482,15 @@ cudaError_t launch_typed(const AttnArgs& a, cudaStream_t stream) {
 template <typename T, int D>
 static cudaError_t prepare_units() {
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  const cudaError_t e = cudaFuncSetAttribute(unit_kernel<T, D, 1>, attr, UnitSmem<D>::kBytes);
-  return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(unit_kernel<T, D, 2>, attr, UnitSmem<D>::kBytes);
+  // (the same division of an SM's memory as prefix_kernel's, to run beside it)
+  const auto carve = cudaFuncAttributePreferredSharedMemoryCarveout;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(unit_kernel<T, D, 1>, attr, UnitSmem<D>::kBytes)) ||
+      (e = cudaFuncSetAttribute(unit_kernel<T, D, 2>, attr, UnitSmem<D>::kBytes)) ||
+      (e = cudaFuncSetAttribute(unit_kernel<T, D, 1>, carve, 100)) ||
+      (e = cudaFuncSetAttribute(unit_kernel<T, D, 2>, carve, 100)))
+    return e;
+  return cudaSuccess;
 }
 
 cudaError_t prepare_prefix_attention() {

@@ -588,6 +588,13 @@ cudaError_t prepare_prefix_mma() {
       (e = cudaFuncSetAttribute(prefix_kernel<__half, 64>, attr, MmaSmem<64>::kBytes)) ||
       (e = cudaFuncSetAttribute(prefix_kernel<__half, 128>, attr, MmaSmem<128>::kBytes)))
     return e;
+  // (all of it, so that units find room beside it)
+  const auto carve = cudaFuncAttributePreferredSharedMemoryCarveout;
+  if ((e = cudaFuncSetAttribute(prefix_kernel<__nv_bfloat16, 64>, carve, 100)) ||
+      (e = cudaFuncSetAttribute(prefix_kernel<__nv_bfloat16, 128>, carve, 100)) ||
+      (e = cudaFuncSetAttribute(prefix_kernel<__half, 64>, carve, 100)) ||
+      (e = cudaFuncSetAttribute(prefix_kernel<__half, 128>, carve, 100)))
+    return e;
   encode_tiled();  // the driver's entry point, looked up once
   return cudaSuccess;
 }
