@@ -8,10 +8,10 @@
 //
 // Tokens are whole numbers decided by comparing sums of up to 2^20 masses, so
 // masses are integers (struct Mass): their sums are exact and the same in any
-// order, and a mass is within 1.2e-9 (rms 4e-10) of exp() in relative terms.  A
-// prefix of N such errors moves a boundary by about 4e-10 / sqrt(N) of W (N the
-// distinct values among bf16 logits), which puts the chance of a draw differing
-// from the exact one below 1e-5 even for a flat row.
+// order, and a mass is within 1.0e-9 (rms 2.8e-10) of exp() in relative terms.  A
+// prefix of N such errors moves a boundary by about 2.8e-10 / sqrt(N) of W (N the
+// distinct values among bf16 logits, a hundred and more), which puts the chance of
+// a draw differing from the exact one below 1e-5 for a flat row of 151,936.
 //
 // Two launches.  stream_kernel reads the logits once: a warp takes 1024 of them
 // into registers and leaves their maximum, the maxima of their 64-element groups
@@ -20,6 +20,11 @@
 // and reads again only the segments and groups that can matter: one segment for
 // an unfiltered or greedy row's token, the groups that reach the top_k-th group
 // maximum, the whole row (from L2) only for top-p over everything.
+// What bounds them: stream_kernel HBM where few rows need sums of masses, else
+// the 24 instructions of a mass (1024 fp32 rows of 248,320, 1.02 GB: 185 us when
+// no row does, 286 us when all do); finish_kernel the chain of block-wide steps
+// of a row, and for top-p rows their two passes over the elements (256 bf16 rows
+// of 151,936: 18 us greedy, 27 unfiltered, 37 top-k 20, 143 top-p 0.9).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 

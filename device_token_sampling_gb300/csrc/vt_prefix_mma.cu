@@ -6,22 +6,25 @@
 //   - the load warp brings K and V tiles of 128 tokens by TMA, block by block of
 //     the cache, into two-stage rings of 128-byte-swizzled shared memory;
 //   - a thread per tile issues its MMAs (one for both was bound by its own
-//     instructions: 2900 cycles a step): S_t = Q_t K^T into tensor memory, O_t += P_t V
+//     instructions, 2900 cycles a step; with one each a step takes 1850): S_t = Q_t K^T into tensor memory, O_t += P_t V
 //     with P_t read from tensor memory and V as it lies (token-major);
 //   - a warpgroup per tile, one thread to a row, turns S into weights: running
 //     maximum and sum in registers, P in the cache's type over the first columns
 //     of its own S.
 // Each tile has two S buffers, so that its next scores are made while it is at its
 // exponentials: with one, scores, exponentials and product of a tile are one
-// serial chain (a 128-token step then took 5000 cycles for two tiles; 85 us for
-// 1024 rows of 8 kv heads against 16384 tokens).  A warp rescales its rows'
+// serial chain (85 us for 1024 rows of 8 kv heads against 16384 tokens, where two
+// take 71).  A warp rescales its rows'
 // accumulators only when one of their maxima has grown.  (To wait until it has
-// grown by 2^8 saves 4 us of those 85, but then the largest weight is no longer
+// grown by 2^8 saved 4 us of those 85, but then the largest weight is no longer
 // exactly 1, and the rounding of the weights to bf16 costs 1.5e-3 of the result
 // instead of 1.07e-3.)
 // What bounds it: per 64 tokens and 256 rows 1024 cycles of the special function
 // units and 1280 of the tensor cores (the scores read 48 KB of shared memory a
-// tile, at 128 bytes a cycle).
+// tile, at 128 bytes a cycle), on the chain of exponentials and products of the two
+// tiles that share an SM.  The 71 us (78 with unit_kernel reading beside it) are
+// 68.7 GFLOP at 970 TFLOP/s, half the measured bf16 rate of 1936, and 128 of the
+// 152 SMs; the others work on the requests' own tokens meanwhile.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

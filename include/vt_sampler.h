@@ -242,11 +242,14 @@ int vt_sample_ex(vt_sampler* handle, const void* logits, int32_t dtype, int32_t 
  *                  EMPTY.
  *   out_logprobs   device float[B][draws]: log-softmax of z_t over the whole row
  *                  at the token (NaN for a row without a token); may be NULL.
- * The sums that decide a token are integers of 2^-42 (V = 2^20) to 2^-45 of the
- * largest mass, each mass within 2.5e-10 of its value: a token differs from the
- * exactly computed one with a probability below 1e-4 a draw.  Same inputs give the same outputs.
+ * The sums that decide a token are integers of 2^-42 (V = 2^20) to 2^-51 (V <=
+ * 2^11) of the power of two above the largest mass, each mass within 1e-9 of its
+ * value (3e-10 rms): a token differs from the exactly computed one with a
+ * probability of the order of 1e-4 a draw at worst (a flat row of V = 2^20 in two
+ * halves of equal values), below 1e-5 at V = 151,936.  Same inputs give the same
+ * outputs.
  * Row status (vt_get_row_status) is written; seeds, counts and the debug views
- * are not touched.  One launch; enqueues only; may be captured.  Errors:
+ * are not touched.  Two launches; enqueues only; may be captured.  Errors:
  * VT_ERR_STATE (no vt_reset_params, or B larger than its rows),
  * VT_ERR_INVALID_ARG (also: a row with penalties or top-p decay),
  * VT_ERR_CAPACITY (V > max_vocab), VT_ERR_CUDA. */
