@@ -78,7 +78,8 @@ struct MassTable {
     return ((127u + 30u) << 23) + (uint32_t)((x - 1073741824.0) / 128.0 + 0.5);
   }
 };
-__constant__ MassTable c_mass_table = MassTable();
+// (not in constant memory: lanes that read other entries would take turns)
+__device__ const MassTable d_mass_table = MassTable();
 
 // x >> n, 0 from 32 on.
 __device__ __forceinline__ uint32_t shr(uint32_t x, int n) {
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) stream_kernel(Giv
   extern __shared__ __align__(128) unsigned char dyn[];
   __shared__ uint2 table[kTable];
   __shared__ uint64_t bars[kStreamThreads / 32];
-  for (int i = threadIdx.x; i < kTable; i += kStreamThreads) table[i] = c_mass_table.v[i];
+  for (int i = threadIdx.x; i < kTable; i += kStreamThreads) table[i] = d_mass_table.v[i];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint4* buf = reinterpret_cast<const uint4*>(dyn) + warp * (kSeg * sizeof(T) / 16);
   if (lane == 0) mbar_init(&bars[warp], 1);
@@ -435,7 +436,7 @@ struct Shared {
     uint16_t groups[kMaxSegs * kGroupsPerSeg / 2];  // groups to read, in order
   };
   // (the list lies over hist.own; its buckets are in hist.sum)
-  union {
+  union alignas(16) {
     Hist hist;
     uint64_t list[kList];  // candidates put in order
   };
@@ -501,6 +502,15 @@ struct Bins {
 };
 __device__ __forceinline__ int bin_no(float bin_f) {
   return __float_as_int(bin_f) - __float_as_int(kMagic);
+}
+
+// The thread's kBins / kThreadsF neighbouring bins.
+__device__ __forceinline__ void load_bins(const uint32_t* bins, uint32_t (&c)[kBins / kThreadsF]) {
+  static_assert(kBins / kThreadsF == 8, "two 16-byte loads");
+  const uint4* p = reinterpret_cast<const uint4*>(bins) + threadIdx.x * 2;
+  const uint4 a = p[0], b = p[1];
+  c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+  c[4] = b.x, c[5] = b.y, c[6] = b.z, c[7] = b.w;
 }
 
 // Block-wide exclusive sum in thread order, and the total.
@@ -805,11 +815,9 @@ __device__ __noinline__ void order_entries(int n, int V) {
   __syncthreads();
   uint32_t c[kPer];
   uint64_t sum = 0, all;
+  load_bins(bucket, c);
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    c[q] = bucket[tid * kPer + q];
-    sum += c[q];
-  }
+  for (int q = 0; q < kPer; ++q) sum += c[q];
   uint32_t begin = (uint32_t)block_scan(sh, sum, &all);
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
@@ -891,14 +899,16 @@ __device__ __forceinline__ void append(Shared& sh, const RowData<T>& rd, const M
 // it closer and closer, and a list of the elements in the bracket, once it holds
 // them.  One histogram over the row nearly always does; the masses above a
 // bracket are summed exactly before the next is made of it.
-//   MASS: elements are kept while the mass before them is <= target (row units).
+//   MASS: elements are kept while the mass before them is <= target (row units);
+//   those below z_least have too little mass for the boundary to be among them.
 //   On success the CTAs' seg_w hold the masses of the kept elements (element units).
-//   else: the first `target` of them are kept.
+//   else: the first `target` of them are kept (z_least: -inf).
 // PLAIN: `cut` has no index, so that a threshold on the logits says it all.
 // Returns false (the same in every CTA) when too many elements are equal, or, by
 // mass, when a bracket turns out not to hold the boundary.
 template <typename T, bool MASS, bool PLAIN>
-__device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint64_t target) {
+__device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint64_t target,
+                                         float z_least) {
   Row<T> rw = row_in;  // in registers
   rw.mass.table = smem().table;
   using RD = RowData<T>;
@@ -908,7 +918,8 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
   constexpr int kPer = kBins / kThreadsF;
   __syncthreads();
   if (warp == 0) {
-    const float x = least_logit(rw.mass, [&](float z) { return z >= cut.z; });
+    const float least = fmaxf(cut.z, z_least);
+    const float x = least_logit(rw.mass, [&](float z) { return z >= least; });
     if (lane == 0) sh.least[0] = x;
   }
   __syncthreads();
@@ -971,8 +982,7 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
       from = sh.hist.sum;
     }
     uint32_t cn[kPer];
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) cn[q] = from[tid * kPer + q];
+    load_bins(from, cn);
     if (MASS) {
       float cf[kPer], tf = 0.f;
 #pragma unroll
@@ -991,15 +1001,22 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
       const float want = __ull2float_rn(target - above) * 4063.f /
                          exp2f(__fmaf_rn(rw.mass.z(top) - rw.mass.c, kLog2e,
                                          (float)(kElemBits - rw.drop - rw.mass.E())));
+      int lo = kBins, hi = -1;
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
         if (cn[q] > 0) {
           // bins that end before the target are kept whole, those that begin
           // after it not at all
-          if (a + cf[q] >= want * (1.f - kSlack)) atomicMin(&sh.lo, tid * kPer + q);
-          if (a <= want * (1.f + kSlack)) atomicMax(&sh.hi, tid * kPer + q);
+          if (a + cf[q] >= want * (1.f - kSlack)) lo = min(lo, tid * kPer + q);
+          if (a <= want * (1.f + kSlack)) hi = tid * kPer + q;
         }
         a += cf[q];
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      if (lane == 0) {
+        atomicMin(&sh.lo, lo);
+        atomicMax(&sh.hi, hi);
       }
     } else {
       uint64_t tn = 0, unused;
@@ -1129,7 +1146,8 @@ __device__ __noinline__ bool band_select(const Row<T>& row_in, Cut* cut_io, uint
 // gives the masses of all prefixes exactly, without a list or a second look at a
 // bracket.  A second pass adds up the kept elements' masses by segment, from a
 // table of the slots'.  (256 rows of 151,936 with p = 0.99: 249 us by band_select,
-// 192 so; one row 71 and 54.)
+// 196 so; one row 71 and 52.)  What bounds it: the shared memory's atomics of the
+// first pass and lookups of the second, about 9 cycles a warp each.
 //   target as in band_select; *cut_io gets this CTA's own view of the cut: of the
 //   elements at the boundary, which are kept by index, its own up to idx.
 // Returns false (the same in every CTA) when the boundary is in the shared slot or
@@ -1184,55 +1202,55 @@ __device__ __noinline__ bool code_select(const Row<T>& row_in, Cut* cut_io, uint
     rw.sync();
     from = sh.hist.sum;
   }
+  // a slot's element (over the counts, once they are read) and its mass in row units
   uint32_t cn[kPer];
-  uint64_t w[kPer], sum = 0, all;  // a slot's element, and the thread's slots in row units
-  auto slot_mass = [&](int slot, uint64_t n, uint64_t each) -> uint64_t {
-    if (slot == top) return sh.digit_w[0];
-    // n * each + half a row unit, in 128 bits
-    const uint64_t lo = n * each, half = 1ull << (rw.drop - 1);
-    const uint64_t hi = __umul64hi(n, each) + (lo + half < lo);
-    return (hi << (64 - rw.drop)) | ((lo + half) >> rw.drop);
-  };
+  load_bins(from, cn);
+  static_assert(sizeof(sh.hist) >= kBins * sizeof(uint64_t), "a mass for every slot");
+  uint64_t* table = reinterpret_cast<uint64_t*>(&sh.hist);
+  __syncthreads();
+  uint64_t row_w[kPer], sum = 0, all;
 #pragma unroll
-  for (int q = 0; q < kPer; ++q) {
-    const int slot = tid * kPer + q;
-    cn[q] = from[slot];
-    w[q] = cn[q] && slot != top ? rw.mass.of(rw.mass.z(code_value(top - slot))) : 0;
-    sum += cn[q] ? slot_mass(slot, cn[q], w[q]) : 0;
+  for (int q = 0; q < kPer; q += 2) {
+    uint64_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int slot = tid * kPer + q + i;
+      w[i] = slot != top ? rw.mass.of(rw.mass.z(code_value(top - slot))) : 0;
+      // cn * w + half a row unit, in 128 bits
+      const uint64_t n = cn[q + i], lo = n * w[i], half = 1ull << (rw.drop - 1);
+      const uint64_t hi = __umul64hi(n, w[i]) + (lo + half < lo);
+      row_w[q + i] = (hi << (64 - rw.drop)) | ((lo + half) >> rw.drop);
+      if (slot == top) row_w[q + i] = sh.digit_w[0];
+      sum += row_w[q + i];
+    }
+    *reinterpret_cast<ulonglong2*>(table + tid * kPer + q) = make_ulonglong2(w[0], w[1]);
   }
   uint64_t a = block_scan(sh, sum, &all);
   int mine = -1;
-  uint64_t mine_a = 0, mine_w = 0;
+  uint64_t mine_a = 0;
   uint32_t mine_n = 0;
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
     if (cn[q] && a <= target) {
       mine = tid * kPer + q;
       mine_a = a;
-      mine_w = w[q];
       mine_n = cn[q];
     }
-    a += cn[q] ? slot_mass(tid * kPer + q, cn[q], w[q]) : 0;
+    a += row_w[q];
   }
-  if (mine >= 0) atomicMax(&sh.hi, mine);
+  const int last = __reduce_max_sync(0xffffffffu, mine);
+  if (lane == 0) atomicMax(&sh.hi, last);
   __syncthreads();
   if (mine >= 0 && mine == sh.hi) {
     sh.above = mine_a;
-    sh.red_n[0] = mine_w;
     sh.bin_n = mine_n;
   }
   __syncthreads();
   const int edge = sh.hi;
-  const uint64_t w_edge = sh.red_n[0], n_edge = sh.bin_n, left = target - sh.above;
-  if (edge < 0 || edge == top || all <= target || left >= (1ull << (62 - rw.drop)) || w_edge == 0)
-    return false;
+  if (edge < 0 || edge == top || all <= target) return false;
+  const uint64_t w_edge = table[edge], n_edge = sh.bin_n, left = target - sh.above;
+  if (left >= (1ull << (62 - rw.drop)) || w_edge == 0) return false;
   const uint64_t take = min((left << rw.drop) / w_edge + 1, n_edge);  // of the equal elements
-  // the slots' masses, over the counts (the others are done with those)
-  static_assert(sizeof(sh.hist) >= kBins * sizeof(uint64_t), "a mass for every slot");
-  uint64_t* table = reinterpret_cast<uint64_t*>(&sh.hist);
-#pragma unroll
-  for (int q = 0; q < kPer; ++q) table[tid * kPer + q] = w[q];
-  __syncthreads();
   const float x_edge = code_value(top - edge);
   int ties_all = 0;
   for (int s = rw.s0 + warp; s < rw.s1; s += kWarpsF) {
@@ -1486,11 +1504,9 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
     {
       uint32_t cn[kPer];
       uint64_t tn = 0, unused;
+      load_bins(sh.hist.own, cn);
 #pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        cn[q] = sh.hist.own[tid * kPer + q];
-        tn += cn[q];
-      }
+      for (int q = 0; q < kPer; ++q) tn += cn[q];
       uint64_t b = block_scan(sh, tn, &unused);
 #pragma unroll
       for (int q = 0; q < kPer; ++q) {
@@ -1623,7 +1639,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
   const bool team = ctas > 1 && !greedy && !from_list &&
                     (topk || (P.flags & (kRowTopP | kRowMinP)));
   if (rank > 0 && !team) return;
-  for (int i = tid; i < kTable; i += kThreadsF) sh.table[i] = c_mass_table.v[i];
+  for (int i = tid; i < kTable; i += kThreadsF) sh.table[i] = d_mass_table.v[i];
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // the row's maximum
@@ -1633,6 +1649,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
   for (int s = tid; s < a.segs; s += kThreadsF) {
     const float v = seg_max[s];
     sh.seg_max[s] = v;
+    sh.seg_w[s] = seg_sum[s];
     mx = max_nan(mx, v);
   }
 #pragma unroll
@@ -1671,7 +1688,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
       uint64_t w = 0;
       if (zm > -INFINITY) {
         const int sh_r = mass.E() - Mass(P.inv_t, zm, sh.table).E();
-        w = fabsf(zm) < kNarrow && sh_r < 64 ? seg_sum[s] >> sh_r : 0;
+        w = fabsf(zm) < kNarrow && sh_r < 64 ? sh.seg_w[s] >> sh_r : 0;
       }
       sh.seg_w[s] = w;
       all += rw.coarse(w);
@@ -1683,7 +1700,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
     for (int s = tid; s < a.segs; s += kThreadsF) {
       const float zm = mass.z(sh.seg_max[s]);
       if (zm > -INFINITY)
-        e += __uint_as_float((uint32_t)seg_sum[s]) *
+        e += __uint_as_float((uint32_t)sh.seg_w[s]) *
              ex2_approx(fmaxf(fabsf(zm), fabsf(m)) < kNarrow
                             ? lse_base(zm) - lse_base(m)
                             : __fmul_rn(__fsub_rn(zm, m), kLog2e));
@@ -1753,7 +1770,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
     rw.sync();
     int n = 0;
     for (int r = 0; r < rw.C; ++r) n += sh.mail.total[r];
-    if (n > P.top_k && !band_select<T, false, true>(rw, &cut, (uint64_t)P.top_k))
+    if (n > P.top_k && !band_select<T, false, true>(rw, &cut, (uint64_t)P.top_k, -INFINITY))
       cut = radix_select<T, false>(rw, cut, (uint64_t)P.top_k);
   }
   uint64_t before, mine, W;
@@ -1765,13 +1782,20 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
     }
     const Cut from = cut;
     const uint64_t target = part_of(all, P.top_p);
+    // V elements below this hold less than the share 1 - p (a logit's hundredth is
+    // far more than the roundings here)
+    const float z_least =
+        fabsf(m) < kUsable
+            ? m + (mass.ln_sum(all, kElemBits - a.drop, m) + logf((1.f - P.top_p) / (float)a.V)) -
+                  0.01f
+            : -INFINITY;
     bool done = false;
     if constexpr (sizeof(T) == 2) {
       if (!topk && !(P.flags & kRowMinP)) done = code_select(rw, &cut, target);
     }
     if (!done) {
-      done = from.idx == kMaxIdx ? band_select<T, true, true>(rw, &cut, target)
-                                 : band_select<T, true, false>(rw, &cut, target);
+      done = from.idx == kMaxIdx ? band_select<T, true, true>(rw, &cut, target, z_least)
+                                 : band_select<T, true, false>(rw, &cut, target, z_least);
       if (!done) {
         cut = radix_select<T, true>(rw, from, target);
         kept_mass(rw, cut);
