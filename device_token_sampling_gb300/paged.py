@@ -111,9 +111,10 @@ class PagedBatch:
         if n < 0:
             raise ValueError(f"capacity={n}")
         if out is None:
-            new = seq_lens.new_empty
-            out = (new(B), new(1), new(B + 1), torch.empty(n, dtype=_I64, device=seq_lens.device),
-                   new(n), new(B))
+            new, place = torch.empty, seq_lens.device  # (half of new_empty's time)
+            out = (new(B, dtype=_I32, device=place), new(1, dtype=_I32, device=place),
+                   new(B + 1, dtype=_I32, device=place), new(n, dtype=_I64, device=place),
+                   new(n, dtype=_I32, device=place), new(B, dtype=_I32, device=place))
             if stream is not None:
                 _on_stream(stream, out)
             po = [t.data_ptr() for t in out]
@@ -184,7 +185,7 @@ class PagedBatch:
                                  f"{prefix_len} tokens")
         made = out is None or lse is None
         if out is None:
-            out = q.new_empty((B, q_heads, d))
+            out = torch.empty((B, q_heads, d), dtype=qt, device=q.device)
         elif (out.dtype is not qt or out.get_device() != dev or not out.is_contiguous()
               or out.shape != q.shape):
             raise ValueError(f"out must be a contiguous {qt} tensor like q")

@@ -329,8 +329,9 @@ class Sampler:
             raise ValueError("uniforms must be a contiguous float32 tensor [B] or [B, draws] "
                              "beside the logits")
         if out is None:
-            lp = torch.empty_like(uniforms)
-            tok = torch.empty_like(uniforms, dtype=torch.int32)
+            place = logits.device
+            lp = torch.empty(shape, dtype=torch.float32, device=place)
+            tok = torch.empty(shape, dtype=torch.int32, device=place)
             if stream is not None:
                 tok.record_stream(stream)
                 lp.record_stream(stream)
