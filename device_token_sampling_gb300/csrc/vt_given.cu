@@ -1491,7 +1491,10 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   if (!fits) {
 #pragma unroll
     for (int q = 0; q < kPer; ++q) sh.hist.own[tid + q * kThreadsF] = 0;
-    if (tid == 0) sh.hi = kBins - 1;
+    if (tid == 0) {
+      sh.hi = kBins - 1;
+      sh.bin_n = 0xffffffffu;  // order key of the least maximum wanted
+    }
     __syncthreads();
 #pragma unroll 1
     for (int b = 0; b < groups; b += kHold * kThreadsF) {
@@ -1518,11 +1521,27 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   }
   // (fewer than top_k groups with a finite element: every finite element)
   const bool any = fits || sh.hi == kBins - 1;
+  // The threshold is the least of the group maxima down to that bin: top_k groups
+  // reach it, whatever the spacing of floats at that magnitude (an edge got by
+  // subtracting from the row's maximum rounds back onto it from 2^17 on).
+  if (!any) {
+    uint32_t least = 0xffffffffu;
+#pragma unroll 1
+    for (int b = 0; b < groups; b += kHold * kThreadsF) {
+      if (groups > kHold * kThreadsF) hold(b, g);
+#pragma unroll
+      for (int q = 0; q < kHold; ++q)
+        if (g[q] > -INFINITY && max(bin_no(bins.bin_f(g[q])), 0) <= sh.hi)
+          least = min(least, ord_key(g[q]));
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) atomicMin(&sh.bin_n, least);
+    __syncthreads();
+  }
   if (warp == 0) {
-    // (the far edge of that bin, a little further: a superset will do)
-    const float edge =
-        any ? -INFINITY : rw.mass.z(rw.mx - ((float)sh.hi + 0.51f) / kBinsPerLogit);
-    const float x = least_logit(rw.mass, [&](float z) { return z > edge; });
+    // by tempered values: equal ones are candidates too, they go by index
+    const float edge = any ? -INFINITY : rw.mass.z(key_value(sh.bin_n));
+    const float x = least_logit(rw.mass, [&](float z) { return any ? z > edge : z >= edge; });
     if (lane == 0) sh.least[0] = x;
   }
   __syncthreads();
@@ -1583,7 +1602,7 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
   }
   __syncthreads();
   const int n = sh.bin;
-  if (n > kList) return false;
+  if (n < 1 || n > kList) return false;
   order_entries<false>(n, rw.rd.V);
   int kept = 0;
   for (int i = tid; i < n; i += kThreadsF) kept += entry_z(sh.list[i]) >= minp.z;
@@ -1615,7 +1634,7 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
     }
     uint64_t run = lo > 0 ? sh.run[lo - 1] : 0;
     int i = lo * kListPerThread;
-    for (run += weight(i); run <= t; run += weight(i)) ++i;
+    for (run += weight(i); run <= t && i + 1 < n; run += weight(i)) ++i;
     a.out_tokens[o] = entry_index(sh.list[i]);
     if (a.out_logprobs)
       a.out_logprobs[o] = __fsub_rn(__fsub_rn(entry_z(sh.list[i]), rw.m), ln_s);

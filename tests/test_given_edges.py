@@ -1,0 +1,53 @@
+"""Draws from given uniform numbers where logits are large, flat or far apart, against the
+definition in 64 bits of ``test_given``."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from test_given import run, uniforms
+
+torch = pytest.importorskip("torch")
+
+F32_MIN = float(np.finfo(np.float32).min)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [5000, 40000, 151936])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_flat_rows_of_large_magnitude(dtype, V):
+    """Every logit at one value whose neighbours are further away than a histogram bin: a mask's
+    fill value, the type's lowest number.  Top-k takes the lowest indices."""
+    values = [-1e9, F32_MIN if dtype == torch.float32 else float(torch.finfo(dtype).min), 1e6,
+              -65504.0, 2.0 ** 17, 2.0 ** 17 + 1024.0, -2.0 ** 24, 3e38]
+    x = torch.empty((len(values), V), dtype=dtype, device="cuda")
+    for r, v in enumerate(values):
+        x[r] = v
+    u = uniforms(V, len(values), 4)
+    u[:, 0], u[:, 1] = 0.0, 1 - 2.0 ** -24
+    for kind in (dict(k=50), dict(k=2), dict(k=30, p=0.5), dict(k=20, mp=0.1), dict(k=1000),
+                 dict(T=0.7, k=20), dict(T=1.5, k=20)):
+        tok, _, st = run(x, u, [kind] * len(values))
+        ok = torch.from_numpy(st == 0).cuda()
+        assert bool(ok.any())
+        assert bool(((tok >= 0) & (tok < kind["k"]))[ok].all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("at", [1e6, -1e6, 2.0 ** 17, 2.0 ** 20])
+@pytest.mark.parametrize("T", [1.0, 0.7, 1.5])
+def test_neighbouring_values_of_large_magnitude(at, T):
+    """Logits a few representable steps apart far from zero: the k-th value is among them, and
+    tempering makes neighbours equal, which then go by index."""
+    V = 40000
+    step = float(np.spacing(np.float32(abs(at))))
+    j = torch.arange(V, device="cuda")
+    x = torch.empty((4, V), dtype=torch.float32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(int(abs(at)))
+    x[0] = at + step * ((j // 64) % 97)
+    x[1] = at + step * (j % 5)
+    x[2] = at + step * torch.randint(0, 2000, (V,), generator=g, device="cuda")
+    x[3] = at - step * (j // 64)
+    u = uniforms(7, 4, 6)
+    for kind in (dict(k=50), dict(k=7), dict(k=300, p=0.8), dict(k=100, mp=0.3)):
+        run(x, u, [dict(kind, T=T)] * 4)
