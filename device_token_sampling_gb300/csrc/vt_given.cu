@@ -396,6 +396,7 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) stream_kernel(Giv
 struct Mail {
   uint64_t mass[kMaxCtas], all[kMaxCtas], kept[kMaxCtas];
   int count[kMaxCtas], total[kMaxCtas], tie[kMaxCtas];
+  int last[kMaxCtas];  // last segment with a kept element, or -1
   Cut cut;  // from the leader
   int ok;
 };
@@ -1361,21 +1362,29 @@ __device__ __noinline__ void kept_mass(const Row<T>& row_in, const Cut cut) {
 }
 
 // seg_w of this CTA's segments to inclusive sums in row units; returns the team's
-// total, the mass of the CTAs before this one and this CTA's.
+// total, the mass of the CTAs before this one and this CTA's.  Mail::last gets the
+// CTAs' last segments with an element that `cut` keeps (with an index: one of the
+// elements at its value, or the end of a segment).
 template <typename T>
-__device__ uint64_t sum_segments(Row<T>& rw, uint64_t* before, uint64_t* own) {
+__device__ uint64_t sum_segments(Row<T>& rw, const Cut& cut, uint64_t* before, uint64_t* own) {
   Shared& sh = smem();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
   if (warp == 0) {
     uint64_t carry = 0;
+    int last = -1;
     for (int b = rw.s0; b < rw.s1; b += 32) {
-      const uint64_t w =
-          warp_scan(b + lane < rw.s1 ? rw.coarse(sh.seg_w[b + lane]) : (uint64_t)0) + carry;
-      if (b + lane < rw.s1) sh.seg_w[b + lane] = w;
+      const int s = b + lane;
+      const uint64_t w = warp_scan(s < rw.s1 ? rw.coarse(sh.seg_w[s]) : (uint64_t)0) + carry;
+      if (s < rw.s1) {
+        sh.seg_w[s] = w;
+        const float top = rw.seg_top(s);
+        if (top > cut.z || (top == cut.z && cut.idx >= s * kSeg)) last = s;
+      }
       carry = __shfl_sync(0xffffffffu, w, 31);
     }
     rw.send(&Mail::kept, carry);
+    rw.send(&Mail::last, __reduce_max_sync(0xffffffffu, last));
   }
   rw.sync();
   uint64_t total = 0;
@@ -1387,10 +1396,32 @@ __device__ uint64_t sum_segments(Row<T>& rw, uint64_t* before, uint64_t* own) {
   return total;
 }
 
+// The last kept element of segment s, or -1; one warp.
+template <typename T>
+__device__ int last_kept(const Row<T>& rw, const Cut& cut, int s, float* z_out) {
+  using RD = RowData<T>;
+  int idx = -1;
+#pragma unroll 1
+  for (int i = 0; i < RD::kIters; ++i) {
+    const int at = RD::at(s, i);
+    float x[RD::N];
+    rw.rd.load(at, x);
+    for (int e = 0; e < RD::N; ++e)
+      if (cut.keeps(rw.mass.z(x[e]), at + e)) idx = at + e;
+  }
+  idx = __reduce_max_sync(0xffffffffu, idx);
+  if (idx >= 0) *z_out = rw.mass.z(elem(rw.rd.data[idx]));
+  return idx;
+}
+
 // The first kept element of this CTA whose inclusive mass (from the CTA's start)
 // exceeds t (row units, below the CTA's mass); one warp.
+// streamed: the segments' masses are stream_kernel's, relative to each segment's own
+// maximum, and so are the elements' here: far below the row's maximum a segment has
+// mass where each of its elements, relative to the row's, would have none.
 template <typename T>
-__device__ int find_draw(const Row<T>& rw, const Cut& cut, uint64_t t, float* z_out) {
+__device__ int find_draw(const Row<T>& rw, const Cut& cut, uint64_t t, bool streamed,
+                         float* z_out) {
   using RD = RowData<T>;
   int lo = rw.s0, hi = rw.s1 - 1;  // the first segment whose inclusive mass exceeds t
   while (lo < hi) {
@@ -1399,7 +1430,13 @@ __device__ int find_draw(const Row<T>& rw, const Cut& cut, uint64_t t, float* z_
     else lo = mid + 1;
   }
   if (lo > rw.s0) t -= smem().seg_w[lo - 1];
-  t <<= rw.drop;  // element units
+  Mass mass = rw.mass;
+  int up = rw.drop;  // to element units
+  if (streamed) {
+    mass = Mass(rw.mass.inv_t, rw.seg_top(lo), rw.mass.table);
+    up += rw.mass.E() - mass.E();
+  }
+  t = t == 0 ? 0 : t << up;
   int idx = -1;
   float zz = 0.f;
 #pragma unroll 1
@@ -1411,7 +1448,7 @@ __device__ int find_draw(const Row<T>& rw, const Cut& cut, uint64_t t, float* z_
 #pragma unroll
     for (int e = 0; e < RD::N; ++e) {
       const float z = rw.mass.z(x[e]);
-      w[e] = cut.keeps(z, at + e) ? rw.mass.of(z) : 0;
+      w[e] = cut.keeps(z, at + e) ? mass.of(z) : 0;
       sum += w[e];
     }
     const uint64_t inc = warp_scan(sum);
@@ -1634,7 +1671,10 @@ __device__ __noinline__ bool draw_from_list(const Row<T>& row_in, const GivenArg
     }
     uint64_t run = lo > 0 ? sh.run[lo - 1] : 0;
     int i = lo * kListPerThread;
-    for (run += weight(i); run <= t && i + 1 < n; run += weight(i)) ++i;
+    if (a.uniforms[o] >= 1.f)  // the last kept one, whether it has mass or not
+      for (i = n - 1; i > 0 && !cut.keeps(entry_z(sh.list[i]), entry_index(sh.list[i]));) --i;
+    else
+      for (run += weight(i); run <= t && i + 1 < n; run += weight(i)) ++i;
     a.out_tokens[o] = entry_index(sh.list[i]);
     if (a.out_logprobs)
       a.out_logprobs[o] = __fsub_rn(__fsub_rn(entry_z(sh.list[i]), rw.m), ln_s);
@@ -1796,7 +1836,7 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
   if (P.flags & kRowTopP) {
     if (all == 0) {  // the mass of what top-p is a share of
       kept_mass(rw, cut);
-      all = sum_segments(rw, &before, &mine);
+      all = sum_segments(rw, cut, &before, &mine);
       if (masses) ln_s = mass.ln_sum(all, kElemBits - a.drop, m);
     }
     const Cut from = cut;
@@ -1820,19 +1860,30 @@ __global__ void __launch_bounds__(kThreadsF, 2) finish_kernel(GivenArgs a) {
         kept_mass(rw, cut);
       }
     }
-    W = sum_segments(rw, &before, &mine);
+    W = sum_segments(rw, cut, &before, &mine);
   } else {
     if (!usable) kept_mass(rw, cut);
-    W = sum_segments(rw, &before, &mine);
+    W = sum_segments(rw, cut, &before, &mine);
     if (masses && !usable) ln_s = mass.ln_sum(W, kElemBits - a.drop, m);
   }
 
-  // the draws: each by a warp of the CTA that holds its mass
+  // the draws: each by a warp of the CTA that holds its mass; numbers of 1 and more
+  // by the last CTA with a kept element
+  const bool streamed = usable && !(P.flags & kRowTopP);
+  bool at_end = sh.mail.last[rw.rank] >= 0;
+  for (int r = rw.rank + 1; r < rw.C; ++r) at_end = at_end && sh.mail.last[r] < 0;
   for (int d = warp; d < a.draws; d += kWarpsF) {
-    const uint64_t t = part_of(W, a.uniforms[(int64_t)row * a.draws + d]);
-    if (t < before || t - before >= mine) continue;
+    const float u = a.uniforms[(int64_t)row * a.draws + d];
     float z;
-    const int j = find_draw(rw, cut, t - before, &z);
+    int j;
+    if (u >= 1.f) {
+      if (!at_end) continue;
+      j = last_kept(rw, cut, sh.mail.last[rw.rank], &z);
+    } else {
+      const uint64_t t = part_of(W, u);
+      if (t < before || t - before >= mine) continue;
+      j = find_draw(rw, cut, t - before, streamed, &z);
+    }
     if (lane == 0) {
       out_tok[d] = j;
       if (out_lp) out_lp[d] = __fsub_rn(__fsub_rn(z, m), ln_s);

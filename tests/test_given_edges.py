@@ -51,3 +51,27 @@ def test_neighbouring_values_of_large_magnitude(at, T):
     u = uniforms(7, 4, 6)
     for kind in (dict(k=50), dict(k=7), dict(k=300, p=0.8), dict(k=100, mp=0.3)):
         run(x, u, [dict(kind, T=T)] * 4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("V", [3000, 9000, 151936])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_of_a_faint_tail(dtype, V):
+    """One logit, and all others so far below it that each has next to no mass while a stretch of
+    them has some: numbers at the ends of [0, 1) fall into such stretches.  Every draw is a
+    token."""
+    x = torch.empty((12, V), dtype=dtype, device="cuda")
+    for r, low in enumerate((-36.0, -37.0, -38.0, -40.0)):
+        for i, peak in enumerate((0, V // 2, V - 1)):
+            x[3 * r + i] = low
+            x[3 * r + i, peak] = 0.0
+    u = torch.tensor([0.0, 1 - 2.0 ** -24, 1.0, 1e-30, 0.5], device="cuda").repeat(12, 1)
+    for kind in (dict(), dict(T=0.99), dict(p=1 - 2.0 ** -24), dict(mp=1e-30), dict(k=V - 1)):
+        tok, _, st = run(x, u, [kind] * 12)
+        assert (st == 0).all()
+        assert bool(((tok >= 0) & (tok < V)).all()), kind
+    # without a filter the first logit has mass of its own: a number of 0 draws the first token
+    # wherever a stretch of the tail has any
+    tok, _, _ = run(x[:6], u[:6], [dict()] * 6)
+    if V == 9000:
+        assert bool((tok[:, 0] == 0).all())
