@@ -3,12 +3,15 @@
 // For request r with len_r tokens in blocks of 2^shift:
 //   blocks_r = ceil(len_r / 2^shift), shared_r = min(blocks_r, prefix blocks),
 //   have_r = max(held_r, shared_r), need_r = max(0, blocks_r - have_r),
-//   off_r = need_0 + ... + need_(r-1);
+//   off_r = the needs of the requests before r that got their blocks;
 //   table[r][held_r..shared_r) = prefix blocks,
 //   table[r][have_r + i] = free[cursor + off_r + i], i < need_r;
 // and the token at position p of r lives in slot table[r][p >> shift] <<
-// shift | (p mod 2^shift).  A request whose blocks do not fit the free list, or
-// whose lengths are not valid, gets none.
+// shift | (p mod 2^shift).  A request whose blocks do not fit what is left of the
+// free list, or whose lengths are not valid, gets none and uses none.  Where all fit,
+// off is one prefix sum.  Else the sum is taken again behind the first request that
+// does not fit, without those that want more than is left (what is left only
+// shrinks): once for each request that is refused because of the others in its 512.
 //
 // One launch, in which no CTA waits for another: every CTA scans all B
 // requests itself (12 bytes a request, from L2), keeps the two prefix sums in
@@ -51,9 +54,11 @@ __device__ __forceinline__ RowNeed row_need(const TablesArgs& a, int r) {
   return n;
 }
 
-// Inclusive block scan of two values; *tot_* get the totals.
-__device__ __forceinline__ void block_scan2(int64_t& x, int64_t& y, int64_t* sx, int64_t* sy) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+struct Sums {  // needed blocks, new tokens
+  int64_t x, y;
+};
+__device__ __forceinline__ void warp_scan2(int64_t& x, int64_t& y) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t px = __shfl_up_sync(0xffffffffu, x, o), py = __shfl_up_sync(0xffffffffu, y, o);
@@ -62,72 +67,94 @@ __device__ __forceinline__ void block_scan2(int64_t& x, int64_t& y, int64_t* sx,
       y += py;
     }
   }
-  if (lane == 31) {
-    sx[w] = x;
-    sy[w] = y;
+}
+// Inclusive block scan of two values; s[kTabWarps] gets the totals.  The warps'
+// sums are added up by warp 0 (by every thread for itself: 7 us more for 2048
+// requests in 608 CTAs).
+__device__ __forceinline__ void block_scan2(int64_t& x, int64_t& y, Sums* s) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  __syncthreads();
+  warp_scan2(x, y);
+  if (lane == 31) s[w + 1] = Sums{x, y};
+  __syncthreads();
+  if (w == 0) {
+    Sums v = lane > 0 && lane <= kTabWarps ? s[lane] : Sums{0, 0};
+    warp_scan2(v.x, v.y);
+    if (lane <= kTabWarps) s[lane] = v;
   }
   __syncthreads();
-  int64_t ax = 0, ay = 0;
-  for (int i = 0; i < w; ++i) {
-    ax += sx[i];
-    ay += sy[i];
-  }
-  x += ax;
-  y += ay;
+  x += s[w].x;
+  y += s[w].y;
 }
 
 __device__ __forceinline__ int clamp31(int64_t v) {
   return (int)(v > 0x7fffffffll ? 0x7fffffffll : v);
 }
 
-__global__ void __launch_bounds__(kTabThreads) tables_kernel(TablesArgs a) {
+__global__ void __launch_bounds__(kTabThreads, 4) tables_kernel(TablesArgs a) {
   extern __shared__ int32_t dyn[];
   int32_t* s_start = dyn;             // [B + 1] first token of each request
   int32_t* s_off = dyn + a.B + 1;     // [B] first free-list entry, or -1: the request got none
-  __shared__ int64_t sx[kTabWarps], sy[kTabWarps];
-  __shared__ int64_t carry[2];
-  __shared__ int s_cursor;
+  __shared__ Sums sums[kTabWarps + 1];
+  __shared__ int s_stop;
+  __shared__ int64_t s_before;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool first = blockIdx.x == 0;
   const int c_in = a.cursor[0];
   const int64_t c0 = c_in < 0 ? a.n_free : min(c_in, a.n_free);  // outside: nothing is free
-  if (tid == 0) {
-    carry[0] = carry[1] = 0;
-    s_cursor = 0;
-  }
-  __syncthreads();
+  int64_t left = a.n_free - c0;  // of the free list, behind the requests so far
+  int64_t tokens = 0;
   for (int base = 0; base < a.B; base += kTabThreads) {
     const int r = base + tid;
     RowNeed n{};
     if (r < a.B) n = row_need(a, r);
-    int64_t x = n.need, y = n.query;
-    block_scan2(x, y, sx, sy);
-    x += carry[0];
-    y += carry[1];
+    int64_t off = -1;  // first free-list entry
+    bool open = true;  // neither admitted nor refused
+    bool sum_tokens = true;
+    for (;;) {
+      const bool fits = open && n.need <= left;
+      int64_t x = fits ? n.need : 0, y = sum_tokens ? n.query : 0;
+      if (tid == 0) s_stop = kTabThreads;
+      block_scan2(x, y, sums);
+      const int64_t want = sums[kTabWarps].x;
+      if (sum_tokens && r < a.B) {
+        s_start[r + 1] = clamp31(tokens + y);
+        if (first) a.starts[r + 1] = clamp31(tokens + y);
+      }
+      tokens += sums[kTabWarps].y;
+      sum_tokens = false;
+      const int64_t at = a.n_free - left + x - n.need;
+      if (want <= left) {
+        if (fits) off = at;
+        left -= want;
+        break;
+      }
+      // the first that does not fit behind the others; those before it are settled
+      if (fits && x > left) atomicMin(&s_stop, tid);
+      __syncthreads();
+      const int stop = s_stop;
+      if (fits && tid < stop) off = at;
+      if (tid == stop) s_before = x - n.need;
+      open = open && tid > stop;
+      __syncthreads();
+      left -= s_before;
+    }
     if (r < a.B) {
-      const bool full = n.need > 0 && c0 + x > a.n_free;
+      const bool full = off < 0;
       const bool ok = !n.bad && !full;
-      s_off[r] = ok ? clamp31(c0 + x - n.need) : -1;
-      s_start[r + 1] = clamp31(y);
-      if (ok && n.need > 0) atomicMax(&s_cursor, (int)x);
+      s_off[r] = ok ? clamp31(off) : -1;
       if (first) {
         a.out_held[r] = ok ? max(n.held, n.blocks) : n.held;
-        a.starts[r + 1] = clamp31(y);
         a.status[r] = n.bad ? 2 : full ? 1 : 0;
       }
     }
-    __syncthreads();
-    if (tid == kTabThreads - 1) {
-      carry[0] = x;
-      carry[1] = y;
-    }
-    __syncthreads();
   }
   if (tid == 0) {
     s_start[0] = 0;
     if (first) {
       a.starts[0] = 0;
-      a.out_cursor[0] = s_cursor > 0 ? (int)c0 + s_cursor : c_in;
+      const int64_t end = a.n_free - left;
+      a.out_cursor[0] = end > c0 ? (int)end : c_in;
     }
   }
   __syncthreads();

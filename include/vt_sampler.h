@@ -552,7 +552,8 @@ int vt_paged_check_errors(vt_paged* handle);
  *   out_status        [B]: 0; 1 when the request's new blocks do not fit what is
  *                     left of the free list after the requests before it; 2 when
  *                     its lengths are not 0 <= query <= seq or need more than
- *                     max_blocks.  A request with status 1 or 2 gets no block, its
+ *                     max_blocks.  A request with status 1 or 2 gets no block and
+ *                     uses none (a smaller one behind it may still fit), its
  *                     table row no new entry (-1 throughout in a new table), its
  *                     tokens slot -1; with status 2 it also has no tokens.
  * A *cursor outside [0, num_free] counts as an empty free list.  One launch;
