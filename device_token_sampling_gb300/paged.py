@@ -11,8 +11,8 @@ import ctypes as C
 
 import torch
 
-from .sampler import (DTYPE_BF16, DTYPE_F16, VT_OK, P, PagedConfig, VtError, load_library,
-                      raw_stream)
+from .sampler import (DTYPE_BF16, DTYPE_F16, VT_OK, P, PagedConfig, VtError, lend, load_library,
+                      make_on, other_stream, raw_stream)
 
 # A decode step makes these calls once a layer or once a token, and at its sizes
 # the host's share is the larger one: checks read each attribute once, pointers go
@@ -29,13 +29,6 @@ def _ids(t, name, device, size=None, dtype=_I32):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor "
                          f"[{'n' if size is None else size}] on cuda:{device}, not {what}")
     return t.data_ptr()
-
-
-def _on_stream(stream, tensors):
-    """Outputs made here for another stream than the current one live until it is done."""
-    if stream is not None and stream != torch.cuda.current_stream(stream.device):
-        for t in tensors:
-            t.record_stream(stream)
 
 
 class PagedBatch:
@@ -94,7 +87,9 @@ class PagedBatch:
         ``table`` int32 [B, >= max_blocks] is written in place.  Returns ``(held, cursor,
         starts, slots, positions, status)``: int32 [B], [1] and [B + 1], int64 and int32
         [capacity] (default: ``B``, one token a request), int32 [B].  ``out`` gives those six
-        tensors; ``held`` and ``cursor`` among them must not be the inputs.  Nothing waits."""
+        tensors; ``held`` and ``cursor`` among them must not be the inputs.  Nothing waits: on a
+        ``stream`` that is not the current one the inputs have to be ready there, and the outputs
+        are."""
         dev = self.device
         B = seq_lens.shape[0] if isinstance(seq_lens, torch.Tensor) and seq_lens.dim() else 0
         p_seq = _ids(seq_lens, "seq_lens", dev, B)
@@ -110,13 +105,13 @@ class PagedBatch:
         n = B if capacity is None else int(capacity)
         if n < 0:
             raise ValueError(f"capacity={n}")
+        other = other_stream(stream)
         if out is None:
             new, place = torch.empty, seq_lens.device  # (half of new_empty's time)
-            out = (new(B, dtype=_I32, device=place), new(1, dtype=_I32, device=place),
-                   new(B + 1, dtype=_I32, device=place), new(n, dtype=_I64, device=place),
-                   new(n, dtype=_I32, device=place), new(B, dtype=_I32, device=place))
-            if stream is not None:
-                _on_stream(stream, out)
+            out = make_on(other, lambda: (
+                new(B, dtype=_I32, device=place), new(1, dtype=_I32, device=place),
+                new(B + 1, dtype=_I32, device=place), new(n, dtype=_I64, device=place),
+                new(n, dtype=_I32, device=place), new(B, dtype=_I32, device=place)))
             po = [t.data_ptr() for t in out]
         else:
             names = ("held", "cursor", "starts", "slots", "positions", "status")
@@ -129,6 +124,9 @@ class PagedBatch:
             raw_stream(stream, dev))
         if rc != VT_OK:
             self._check(rc, "vt_paged_tables")
+        if other is not None:
+            lend(other, (table, seq_lens, query_lens, free_blocks, cursor, held, prefix_blocks,
+                         *out))
         return out
 
     def _table(self, table, B, columns):
@@ -151,7 +149,8 @@ class PagedBatch:
         (of any strides that are multiples of 8 elements, the last 1; a cache stored
         [blocks, kv_heads, block_size, head_dim] goes in transposed) are bf16 or fp16.
         Returns ``(out, lse)``: q's type [B, q_heads, head_dim] and float32 [B, q_heads].
-        ``scale`` defaults to head_dim ** -0.5.  Nothing waits."""
+        ``scale`` defaults to head_dim ** -0.5.  Nothing waits: on a ``stream`` that is not the
+        current one the inputs have to be ready there, and the outputs are."""
         dev = self.device
         block_size, q_heads, kv_heads, d = self._shape
         if q_heads == 0:
@@ -183,19 +182,19 @@ class PagedBatch:
             if prefix_blocks.shape[0] * block_size < prefix_len:
                 raise ValueError(f"{prefix_blocks.shape[0]} prefix blocks do not hold "
                                  f"{prefix_len} tokens")
-        made = out is None or lse is None
+        other = other_stream(stream)
         if out is None:
-            out = torch.empty((B, q_heads, d), dtype=qt, device=q.device)
+            out, = make_on(other, lambda: (
+                torch.empty((B, q_heads, d), dtype=qt, device=q.device),))
         elif (out.dtype is not qt or out.get_device() != dev or not out.is_contiguous()
               or out.shape != q.shape):
             raise ValueError(f"out must be a contiguous {qt} tensor like q")
         if lse is None:
-            lse = torch.empty((B, q_heads), dtype=_F32, device=q.device)
+            lse, = make_on(other, lambda: (
+                torch.empty((B, q_heads), dtype=_F32, device=q.device),))
         elif (lse.dtype is not _F32 or lse.get_device() != dev or not lse.is_contiguous()
               or lse.shape != (B, q_heads)):
             raise ValueError(f"lse must be a contiguous float32 tensor [{B}, {q_heads}]")
-        if made and stream is not None:
-            _on_stream(stream, (out, lse))
         # (the stride of a dimension of one element may be anything)
         blocks = k_cache.shape[0]
         s_block = kv[0] if blocks > 1 else block_size * kv_heads * d
@@ -209,4 +208,7 @@ class PagedBatch:
             out.data_ptr(), lse.data_ptr(), raw_stream(stream, dev))
         if rc != VT_OK:
             self._check(rc, "vt_paged_attention")
+        if other is not None:
+            lend(other, (q, k_cache, v_cache, table, seq_lens,
+                         None if p_prefix is None else prefix_blocks, out, lse))
         return out, lse

@@ -144,6 +144,37 @@ def raw_stream(stream, device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def other_stream(stream):
+    """``stream`` if it is not the current stream of its device, else None."""
+    if stream is None:
+        return None
+    import torch
+    return None if stream == torch.cuda.current_stream(stream.device) else stream
+
+
+def make_on(stream, make):
+    """What ``make()`` allocates for a call on ``stream`` (None: the current stream): memory of
+    that stream's own, which no pending work of the current stream may still use.  The current
+    stream, which the caller will go on in, is recorded as a user of it."""
+    if stream is None:
+        return make()
+    import torch
+    with torch.cuda.stream(stream):
+        made = make()
+    here = torch.cuda.current_stream(stream.device)
+    for t in made:
+        t.record_stream(here)
+    return made
+
+
+def lend(stream, tensors):
+    """The tensors of a call on ``stream`` live until it is done with them, also if the caller
+    drops them at once."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 class Sampler:
     """One sampler handle (``vt_sampler_create``) on one CUDA device."""
 
@@ -306,7 +337,8 @@ class Sampler:
         """vt_sample_given: draw from given uniform numbers.  ``logits`` as in ``sample``;
         ``uniforms`` a float32 CUDA tensor [B] (one draw a row) or [B, draws].  Returns
         ``(tokens, logprobs)``, int32 and float32 in the shape of ``uniforms``.  Rows take no
-        penalties and no top-p decay.  Stream-ordered; nothing waits."""
+        penalties and no top-p decay.  Stream-ordered; nothing waits: on a ``stream`` that is
+        not the current one the inputs have to be ready there, and the outputs are."""
         import torch
         if logits.dim() != 2 or not logits.is_cuda or logits.stride(1) != 1:
             raise ValueError("logits must be a 2-D CUDA tensor with contiguous rows")
@@ -328,14 +360,12 @@ class Sampler:
                 or len(shape) not in (1, 2) or shape[0] != B or not uniforms.is_contiguous()):
             raise ValueError("uniforms must be a contiguous float32 tensor [B] or [B, draws] "
                              "beside the logits")
+        other = other_stream(stream)
         if out is None:
             place = logits.device
-            lp = torch.empty(shape, dtype=torch.float32, device=place)
-            tok = torch.empty(shape, dtype=torch.int32, device=place)
-            if stream is not None:
-                tok.record_stream(stream)
-                lp.record_stream(stream)
-            out = (tok, lp)
+            out = tok, lp = make_on(other, lambda: (
+                torch.empty(shape, dtype=torch.int32, device=place),
+                torch.empty(shape, dtype=torch.float32, device=place)))
         else:
             tok, lp = out
             for t, name, dt in ((tok, "tokens", torch.int32), (lp, "logprobs", torch.float32)):
@@ -348,6 +378,8 @@ class Sampler:
             None if lp is None else lp.data_ptr(), raw_stream(stream, self.device))
         if rc != VT_OK:
             self._check(rc, "vt_sample_given")
+        if other is not None:
+            lend(other, (logits, uniforms, tok, lp))
         return out
 
     def sample_ptr(self, logits_ptr: int, dtype: int, B: int, V: int, ld: int, num_logprobs: int,
