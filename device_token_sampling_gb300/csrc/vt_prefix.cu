@@ -397,12 +397,59 @@ __global__ void __launch_bounds__(32) unit_kernel(AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// One query head over the first `len` tokens of the prefix, token by token in fp32:
+// the way of last resort of join_kernel.  One warp; a lane has D / 32 neighbouring
+// elements.
+template <typename T, int D>
+__device__ __forceinline__ void attend_row(const AttnArgs& a, int64_t row, int len,
+                                           float (&acc)[D / 32], float* max_out, float* sum_out) {
+  constexpr int W = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t b = row / a.hq, head = row % a.hq;
+  auto load = [&](const void* from, int64_t at, float (&x)[W]) {
+    const T* p = static_cast<const T*>(from) + at + lane * W;
+#pragma unroll
+    for (int w = 0; w < W; ++w) x[w] = static_cast<float>(p[w]);
+  };
+  float q[W], m = -INFINITY, l = 0.f;
+  load(a.q, b * a.q_row + head * a.q_head, q);
+#pragma unroll
+  for (int w = 0; w < W; ++w) acc[w] = 0.f;
+#pragma unroll 1
+  for (int t = 0; t < len; ++t) {
+    const int blk = a.prefix_blocks[t >> a.shift];
+    if (blk < 0 || blk >= a.num_blocks) continue;
+    const int64_t at = blk * a.block_stride + (t & ((1 << a.shift) - 1)) * a.token_stride +
+                       head / a.G * a.head_stride;
+    float k[W], v[W], s = 0.f;
+    load(a.k, at, k);
+    load(a.v, at, v);
+#pragma unroll
+    for (int w = 0; w < W; ++w) s += q[w] * k[w];
+    const float z = warp_sum_f(s) * a.scale_log2;
+    const float mn = fmaxf(m, z), base = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2_approx(m - base), p = ex2_approx(z - base);
+    m = mn;
+    l = l * f + p;
+#pragma unroll
+    for (int w = 0; w < W; ++w) acc[w] = acc[w] * f + p * v[w];
+  }
+  *max_out = m;
+  *sum_out = l;
+}
+
 // One warp to a query head: rescale the parts to their common maximum, sum,
 // divide.  A part that holds nothing (sum 0) is not read; a NaN among the scores
 // makes its part's sum NaN and so the row NaN.  The parts' factors are made a lane
 // to a part and four parts are read at a time: one after another, the 24 parts of
 // 64 requests behind 8,192 tokens cost 2 us more (52.3 and 50.2 over all), the 24
 // of 37 requests 4 us (28.5 and 24.2).  What bounds it: those reads' latency.
+//
+// A request shorter than the prefix shares tiles of V with requests that attend to
+// more of it.  Its weights there are 0, but 0 times an infinity or a NaN is NaN; a
+// row of such a request that comes out NaN is made again from its own tokens alone.
+// (Held to the 32 registers that it takes without that, this kernel spills: 64
+// requests 47.5 us over all instead of 45.5.)
 template <typename T, int D>
 __global__ void __launch_bounds__(128) join_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 31;
@@ -453,6 +500,13 @@ __global__ void __launch_bounds__(128) join_kernel(AttnArgs a) {
     }
   }
   l = warp_sum_f(l);
+  bool nan = false;
+#pragma unroll
+  for (int w = 0; w < W; ++w) nan |= acc[w] != acc[w];
+  if (a.prefix_len > 0 && __any_sync(0xffffffffu, nan)) {
+    const int len = max(a.seq_lens[row / a.hq], 0);
+    if (len < a.prefix_len) attend_row<T, D>(a, row, len, acc, &mx, &l);
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D + lane * W);
 #pragma unroll

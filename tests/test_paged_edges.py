@@ -4,6 +4,9 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
+from pagedlib import attention_reference
+from test_paged import BF, HF, make_attention
+
 torch = pytest.importorskip("torch")
 
 
@@ -86,3 +89,41 @@ def test_free_list_shorter_than_the_requests(B, most, share, step):
         needs = np.where(g.random(B) < 0.3, needs * 5, needs // 10)
     build(needs, int(needs.sum() * share), cursor=int(g.integers(0, 9)),
           held=g.integers(0, 4, B) if step else None)
+
+
+# ---- values that are not numbers where a request does not attend ---------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("B,hq,hkv,d,bs,prefix", [(3, 4, 2, 64, 16, 96), (40, 8, 2, 128, 16, 300),
+                                                  (33, 8, 1, 64, 64, 1029), (6, 2, 2, 128, 2, 70)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_past_a_short_request_do_not_reach_it(dtype, B, hq, hkv, d, bs, prefix, bad):
+    """Requests shorter than the shared prefix beside longer ones: keys and values of the prefix
+    that only the longer ones attend to are not finite."""
+    from device_token_sampling_gb300 import PagedBatch
+    seq = np.array([prefix + 5, prefix // 2, 1, 0, prefix, prefix - 1] * 7)[:B]
+    seq[2] = min(seq[2], prefix // 3)
+    c = make_attention(B + d, seq, hq, hkv, d, bs, prefix, dtype)
+    p = PagedBatch(B, bs, c["cols"], hq, hkv, d)
+    args = (c["q"], c["k"], c["v"], c["table"], c["seq"], c["pre"], prefix)
+    clean = [t.clone() for t in p.attention(*args)]
+    pos = prefix // 2 + 1                      # past request 1, within the longest
+    where = (int(c["pre"][pos // bs]), pos % bs)
+    for cache in (c["v"], c["k"]):
+        cache[where] = bad
+        out, lse = p.attention(*args)
+        p.check_errors()
+        short = c["seq"] <= pos
+        want, wlse, b_out, b_lse = attention_reference(
+            c["q"][short], c["k"], c["v"], c["table"][short], c["seq"][short], c["pre"], prefix, bs,
+            d ** -0.5)
+        assert bool(((out[short].double() - want).abs() <= b_out).all())
+        some = wlse > -float("inf")
+        assert bool(((lse[short].double() - wlse).abs()[some] <= b_lse[some]).all())
+        assert bool((lse[short][~some] == -float("inf")).all())
+        assert bool((~out[~short].isfinite()).any(-1).all())
+    c["v"][where] = 1.0
+    c["k"][where] = 1.0
+    again, _ = p.attention(*args)
+    assert torch.equal(again[c["seq"] <= pos], clean[0][c["seq"] <= pos])
