@@ -355,7 +355,9 @@ class Sampler:
             V = cols
         elif V > cols:
             raise ValueError(f"V={V} is past the rows' {cols} columns")
-        shape, dev = uniforms.shape, logits.get_device()
+        shape, dev = uniforms.shape, self.device
+        if logits.get_device() != dev:
+            raise ValueError(f"logits on {logits.device}, the handle on cuda:{dev}")
         if (uniforms.dtype is not torch.float32 or uniforms.get_device() != dev
                 or len(shape) not in (1, 2) or shape[0] != B or not uniforms.is_contiguous()):
             raise ValueError("uniforms must be a contiguous float32 tensor [B] or [B, draws] "

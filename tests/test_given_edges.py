@@ -75,3 +75,51 @@ def test_rows_of_a_faint_tail(dtype, V):
     tok, _, _ = run(x[:6], u[:6], [dict()] * 6)
     if V == 9000:
         assert bool((tok[:, 0] == 0).all())
+
+
+class OnDevice:
+    """A tensor of another GPU, as far as its attributes go."""
+    is_cuda = True
+
+    def __init__(self, shape, index):
+        self.shape, self.index, self.dtype = shape, index, torch.float32
+        self.device = torch.device("cuda", index)
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i):
+        return self.shape[1] if i == 0 else 1
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+def test_tensors_of_another_gpu_are_refused():
+    """Their addresses mean nothing on the handle's device: nothing is called with them."""
+    from device_token_sampling_gb300 import Sampler
+    called = []
+
+    class Lib:
+        def vt_sample_given(self, *a):
+            called.append(a)
+            return 0
+
+    s = Sampler.__new__(Sampler)
+    s._lib, s._h, s.device = Lib(), None, 0
+    x, u = OnDevice((4, 100), 1), OnDevice((4, 2), 1)
+    tok, lp = OnDevice((4, 2), 1), OnDevice((4, 2), 1)
+    tok.dtype = torch.int32
+
+    class Stream:
+        cuda_stream, device = 0, torch.device("cuda", 0)
+
+    with pytest.raises(ValueError):
+        s.sample_given(x, u, out=(tok, lp), stream=Stream())
+    assert not called
