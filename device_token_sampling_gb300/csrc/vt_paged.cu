@@ -243,13 +243,13 @@ int vt_paged_tables(vt_paged* h, int32_t B, const int32_t* seq_lens, const int32
   return VT_OK;
 }
 
-int vt_paged_attention(vt_paged* h, int32_t dtype, int32_t B, const void* q, int64_t q_row,
-                       int64_t q_head, const void* k_cache, const void* v_cache,
-                       int32_t num_blocks, int64_t block_stride, int64_t token_stride,
-                       int64_t head_stride, const int32_t* table, int64_t ld_table,
-                       const int32_t* seq_lens, const int32_t* prefix_blocks, int32_t prefix_len,
-                       int32_t max_seq_len, float scale, void* out, float* out_lse,
-                       void* stream) {
+int vt_paged_attention_ex(vt_paged* h, int32_t dtype, int32_t B, const void* q, int64_t q_row,
+                          int64_t q_head, const void* k_cache, const void* v_cache,
+                          int32_t num_blocks, int64_t block_stride, int64_t token_stride,
+                          int64_t head_stride, const int32_t* table, int64_t ld_table,
+                          int32_t table_cols, const int32_t* seq_lens,
+                          const int32_t* prefix_blocks, int32_t prefix_len, int32_t max_seq_len,
+                          float scale, void* out, float* out_lse, void* stream) {
   if (!h) return VT_ERR_INVALID_ARG;
   const vt_paged_config& c = h->cfg;
   if (c.q_heads == 0)
@@ -266,9 +266,9 @@ int vt_paged_attention(vt_paged* h, int32_t dtype, int32_t B, const void* q, int
                 (long long)cap);
   if (prefix_len > 0 && !prefix_blocks)
     return fail(h, VT_ERR_INVALID_ARG, "prefix_len=%d without prefix blocks", prefix_len);
-  if (num_blocks < 1 || ld_table < 1)
-    return fail(h, VT_ERR_INVALID_ARG, "num_blocks=%d, ld_table=%lld: need at least 1", num_blocks,
-                (long long)ld_table);
+  if (num_blocks < 1 || ld_table < 1 || table_cols < 1)
+    return fail(h, VT_ERR_INVALID_ARG, "num_blocks=%d, ld_table=%lld, table_cols=%d: need at least 1",
+                num_blocks, (long long)ld_table, table_cols);
   if (max_seq_len < 0) return fail(h, VT_ERR_INVALID_ARG, "max_seq_len=%d", max_seq_len);
   if (!std::isfinite(scale)) return fail(h, VT_ERR_INVALID_ARG, "scale is not finite");
   // rows are copied 16 bytes at a time
@@ -295,7 +295,7 @@ int vt_paged_attention(vt_paged* h, int32_t dtype, int32_t B, const void* q, int
   a.seq_lens = seq_lens;
   a.prefix_blocks = prefix_blocks;
   a.prefix_len = prefix_len;
-  a.cols = (int32_t)std::min<int64_t>(c.max_blocks, ld_table);
+  a.cols = std::min(c.max_blocks, table_cols);
   a.B = B;
   a.hq = c.q_heads;
   a.hkv = c.kv_heads;
@@ -317,4 +317,17 @@ int vt_paged_attention(vt_paged* h, int32_t dtype, int32_t B, const void* q, int
   h->launched = true;
   h->err[0] = 0;
   return VT_OK;
+}
+
+int vt_paged_attention(vt_paged* h, int32_t dtype, int32_t B, const void* q, int64_t q_row,
+                       int64_t q_head, const void* k_cache, const void* v_cache,
+                       int32_t num_blocks, int64_t block_stride, int64_t token_stride,
+                       int64_t head_stride, const int32_t* table, int64_t ld_table,
+                       const int32_t* seq_lens, const int32_t* prefix_blocks, int32_t prefix_len,
+                       int32_t max_seq_len, float scale, void* out, float* out_lse,
+                       void* stream) {
+  return vt_paged_attention_ex(h, dtype, B, q, q_row, q_head, k_cache, v_cache, num_blocks,
+                               block_stride, token_stride, head_stride, table, ld_table,
+                               (int32_t)std::min<int64_t>(ld_table, 0x7fffffff), seq_lens,
+                               prefix_blocks, prefix_len, max_seq_len, scale, out, out_lse, stream);
 }

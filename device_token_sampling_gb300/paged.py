@@ -142,12 +142,13 @@ class PagedBatch:
     def attention(self, q, k_cache, v_cache, table, seq_lens, prefix_blocks=None,
                   prefix_len: int = 0, scale: float | None = None, max_seq_len: int = 0,
                   out=None, lse=None, stream=None):
-        """vt_paged_attention: one query token a request over its first ``seq_lens`` cached
+        """vt_paged_attention_ex: one query token a request over its first ``seq_lens`` cached
         tokens, the first ``prefix_len`` of which all requests share.
 
         ``q`` [B, q_heads, head_dim] and the caches [blocks, block_size, kv_heads, head_dim]
         (of any strides that are multiples of 8 elements, the last 1; a cache stored
         [blocks, kv_heads, block_size, head_dim] goes in transposed) are bf16 or fp16.
+        Requests longer than the table's columns are cut there.
         Returns ``(out, lse)``: q's type [B, q_heads, head_dim] and float32 [B, q_heads].
         ``scale`` defaults to head_dim ** -0.5.  Nothing waits: on a ``stream`` that is not the
         current one the inputs have to be ready there, and the outputs are."""
@@ -200,10 +201,10 @@ class PagedBatch:
         s_block = kv[0] if blocks > 1 else block_size * kv_heads * d
         s_token = kv[1] if block_size > 1 else kv_heads * d
         s_head = kv[2] if kv_heads > 1 else d
-        rc = self._lib.vt_paged_attention(
+        rc = self._lib.vt_paged_attention_ex(
             self._h, dtype, B, q.data_ptr(), q.stride(0) if B > 1 else q_heads * d,
             q.stride(1) if q_heads > 1 else d, k_cache.data_ptr(), v_cache.data_ptr(), blocks,
-            s_block, s_token, s_head, p_table, ld, p_seq,
+            s_block, s_token, s_head, p_table, ld, table.shape[1], p_seq,
             p_prefix, int(prefix_len), int(max_seq_len), d ** -0.5 if scale is None else scale,
             out.data_ptr(), lse.data_ptr(), raw_stream(stream, dev))
         if rc != VT_OK:

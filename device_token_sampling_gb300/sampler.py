@@ -101,6 +101,8 @@ SIGNATURES = {
                                   P, P]),
     "vt_paged_attention": (C.c_int, [P, I32, I32, P, I64, I64, P, P, I32, I64, I64, I64, P, I64,
                                      P, P, I32, I32, C.c_float, P, P, P]),
+    "vt_paged_attention_ex": (C.c_int, [P, I32, I32, P, I64, I64, P, P, I32, I64, I64, I64, P, I64,
+                                        I32, P, P, I32, I32, C.c_float, P, P, P]),
     "vt_last_error": (C.c_char_p, [P]),
     "vt_status_string": (C.c_char_p, [C.c_int]),
 }

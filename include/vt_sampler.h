@@ -579,9 +579,10 @@ int vt_paged_tables(vt_paged* handle, int32_t B, const int32_t* seq_lens,
  *                   (elements).  Query head h uses kv head h / (q_heads / kv_heads).
  *   table           [B][ld_table] block ids; columns from prefix_len / block_size on
  *                   are read.
- *   seq_lens        [B], values up to max_blocks * block_size (larger ones are cut
- *                   there).  0: out is 0 and the log-sum -inf.  A request shorter
- *                   than the prefix attends to its own length of it.
+ *   seq_lens        [B], values up to max_blocks (or ld_table, if less) * block_size;
+ *                   larger ones are cut there.  0: out is 0 and the log-sum
+ *                   -inf.  A request shorter than the prefix attends to its own
+ *                   length of it.
  *   prefix_blocks   the ids of the blocks that hold positions 0 .. prefix_len - 1.
  *   prefix_len      0 (nothing shared) .. max_blocks * block_size.
  *   max_seq_len     an upper bound of seq_lens that shapes the launch; 0: the
@@ -601,6 +602,17 @@ int vt_paged_attention(vt_paged* handle, int32_t dtype, int32_t B, const void* q
                        const int32_t* seq_lens, const int32_t* prefix_blocks, int32_t prefix_len,
                        int32_t max_seq_len, float scale, void* out, float* out_lse,
                        void* stream);
+
+/* vt_paged_attention for a table whose rows are part of wider ones: ld_table
+ * elements apart, of which the first table_cols are block ids (vt_paged_attention:
+ * all ld_table are).  Requests longer than table_cols blocks are cut there. */
+int vt_paged_attention_ex(vt_paged* handle, int32_t dtype, int32_t B, const void* q, int64_t q_row,
+                          int64_t q_head, const void* k_cache, const void* v_cache,
+                          int32_t num_blocks, int64_t block_stride, int64_t token_stride,
+                          int64_t head_stride, const int32_t* table, int64_t ld_table,
+                          int32_t table_cols, const int32_t* seq_lens,
+                          const int32_t* prefix_blocks, int32_t prefix_len, int32_t max_seq_len,
+                          float scale, void* out, float* out_lse, void* stream);
 
 /* Message for the last failing call on `handle` ("" if none); static storage
  * owned by the handle, valid until the next call on it. */

@@ -127,3 +127,25 @@ def test_values_past_a_short_request_do_not_reach_it(dtype, B, hq, hkv, d, bs, p
     c["k"][where] = 1.0
     again, _ = p.attention(*args)
     assert torch.equal(again[c["seq"] <= pos], clean[0][c["seq"] <= pos])
+
+
+# ---- a table that is part of a wider one ---------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,prefix", [(3, 0), (20, 32)])
+def test_lengths_past_a_narrowed_table_are_cut(B, prefix):
+    """A column slice of a wider table, as a contiguous table of those columns: a length past the
+    slice is cut there, whatever stands behind it."""
+    from device_token_sampling_gb300 import PagedBatch
+    c = make_attention(5, [80 + i % 3 for i in range(B)], 8, 2, 64, 16, prefix, BF)
+    narrow = c["table"][:, :4].contiguous()    # 64 tokens
+    wide = torch.zeros((B + 1, 12), dtype=torch.int32, device="cuda")
+    wide[:B, 3:7] = narrow
+    wide[:B, 7:9] = c["table"][:, 4:6].clamp(0, c["k"].shape[0] - 1)
+    # (head-room in max_blocks, so that the lengths are not cut there)
+    p = PagedBatch(B, 16, 16, 8, 2, 64)
+    rest = (c["seq"], c["pre"], prefix)
+    want, wlse = p.attention(c["q"], c["k"], c["v"], narrow, *rest)
+    got, lse = p.attention(c["q"], c["k"], c["v"], wide[:B, 3:7], *rest)
+    p.check_errors()
+    assert torch.equal(got, want) and torch.equal(lse, wlse)
