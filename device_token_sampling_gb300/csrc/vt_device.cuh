@@ -124,8 +124,9 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t phase,
 // The same where the wait is on a kernel's critical path: bounded by the SM's
 // clock (limit_cycles, about 2 s), which is read in a few cycles, and read only
 // every 64 polls.
+constexpr long long kWaitCycles = 4000000000ll;
 __device__ __forceinline__ bool mbar_wait_clocked(uint64_t* bar, uint32_t phase,
-                                                  long long limit_cycles = 4000000000ll) {
+                                                  long long limit_cycles = kWaitCycles) {
   if (mbar_try_wait(bar, phase)) return true;
   const long long t0 = clock64();
   for (uint32_t polls = 1;; ++polls) {

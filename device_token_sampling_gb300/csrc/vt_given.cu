@@ -292,8 +292,8 @@ __device__ __forceinline__ bool sums_masses(const RowParams& P, int V) {
 // lane, fp32 eight).  The next segment is on its way into the warp's own buffer of
 // shared memory, by one bulk copy, while this one is worked on (without that the
 // loads pause for the arithmetic: 1024 fp32 rows 210 us); segments that a bulk copy
-// cannot take (unaligned rows, a row's ragged end) are loaded directly.  What
-// bounds it: HBM.
+// cannot take (unaligned rows, a row's ragged end) are loaded directly, and so are
+// the rest of a warp's, once a wait for a copy has run out.  What bounds it: HBM.
 template <typename T>
 __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) stream_kernel(GivenArgs a) {
   using RD = RowData<T>;
@@ -309,8 +309,9 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) stream_kernel(Giv
   asm volatile("griddepcontrol.launch_dependents;");
   const uint32_t items = (uint32_t)a.B * a.segs, step = gridDim.x * (kStreamThreads / 32);
   // whether segment `it` comes by a bulk copy, and the copy
+  bool copies = a.aligned != 0, late = false;
   auto by_copy = [&](uint32_t it) {
-    return a.aligned && it < items && (int)(it % a.segs + 1) * kSeg <= a.V;
+    return copies && it < items && (int)(it % a.segs + 1) * kSeg <= a.V;
   };
   auto fetch = [&](uint32_t it) {
     if (lane == 0) {
@@ -326,9 +327,17 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) stream_kernel(Giv
   for (; it < items; it += step) {
     const int row = (int)(it / a.segs), seg = (int)(it % a.segs);
     uint4 v[RD::kIters];
-    if (by_copy(it)) {
-      // (a wait that ran out leaves whatever is there; the call is reported)
-      if (!mbar_wait_clocked(&bars[warp], phase)) atomicOr(a.err_word, kErrTimeout);
+    bool here = by_copy(it);
+    if (here) {
+      here = __all_sync(0xffffffffu,
+                        a.wait_cycles > 0 && mbar_wait_clocked(&bars[warp], phase, a.wait_cycles));
+      if (!here) {  // this copy is the one in flight; no other is begun
+        copies = false;
+        late = true;
+        if (lane == 0) atomicOr(a.err_word, kErrTimeout);
+      }
+    }
+    if (here) {
       phase ^= 1;
 #pragma unroll
       for (int i = 0; i < RD::kIters; ++i) v[i] = buf[i * 32 + lane];
@@ -385,6 +394,8 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) stream_kernel(Giv
       a.seg_sum[(int64_t)row * a.segs + seg] = sum;
     }
   }
+  // no copy is in flight when the CTA's memory goes to another
+  if (late) mbar_wait_clocked(&bars[warp], phase, 200000000ll);
 }
 
 // ---- finishing a row ---------------------------------------------------------

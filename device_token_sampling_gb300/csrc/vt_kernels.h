@@ -258,6 +258,7 @@ struct GivenArgs {
   float* out_logprobs;       // [B][draws] or null
   int32_t* row_status;       // [B]
   int32_t* err_word;
+  int64_t wait_cycles;       // limit of a wait for a copy; 0: it has run out
   // scratch, of the rows' segments: [B][segs] maxima and sums, [B][segs * 16]
   // group maxima
   float* seg_max;

@@ -3574,7 +3574,10 @@ __global__ void wait_probe_kernel(int32_t* err_word, unsigned long long limit_ns
   __shared__ uint64_t bar;
   mbar_init(&bar, 1);
   fence_mbar_init();
-  if (!mbar_wait_bounded(&bar, 0u, limit_ns)) atomicOr(err_word, kErrTimeout);
+  // both kinds of wait have to run out (about 2 cycles a ns)
+  const bool timed = mbar_wait_bounded(&bar, 0u, limit_ns);
+  const bool clocked = mbar_wait_clocked(&bar, 0u, 2 * (long long)limit_ns);
+  if (!timed && !clocked) atomicOr(err_word, kErrTimeout);
 }
 }  // namespace
 

@@ -55,6 +55,7 @@ struct vt_sampler {
   uint64_t* d_given_sum = nullptr;
   float* d_given_max = nullptr;
   float* d_given_gmax = nullptr;
+  int64_t given_wait = vt::kWaitCycles;  // limit of its waits
   // the side stream: rows routed straight to the selection kernel run there,
   // beside the main stream's launches (fork and join through events)
   cudaStream_t side = nullptr;
@@ -111,7 +112,9 @@ namespace {
 // Host-side fault injection for the failure-path tests, read at each call:
 //   VT_FAULT_INJECT=alloc:<n>  the n-th device allocation of vt_sampler_create
 //                              (0-based) fails as if the device were full;
-//   VT_FAULT_INJECT=upload     the parameter upload of vt_reset_params fails.
+//   VT_FAULT_INJECT=upload     the parameter upload of vt_reset_params fails;
+//   VT_FAULT_INJECT=wait       (read by vt_sampler_create) vt_sample_given takes every
+//                              wait for a copy as one that has run out.
 // Nothing on the device is made to fault.
 int fault_alloc_index() {
   const char* e = std::getenv("VT_FAULT_INJECT");
@@ -121,6 +124,10 @@ int fault_alloc_index() {
 bool fault_upload() {
   const char* e = std::getenv("VT_FAULT_INJECT");
   return e && std::strcmp(e, "upload") == 0;
+}
+bool fault_wait() {
+  const char* e = std::getenv("VT_FAULT_INJECT");
+  return e && std::strcmp(e, "wait") == 0;
 }
 
 int set_err(vt_sampler* h, int code, const char* fmt, ...) {
@@ -262,6 +269,7 @@ int vt_sampler_create(const vt_sampler_config* cfg, vt_sampler** out) {
   const size_t n = (size_t)cfg->max_logprobs;
   bool ok = true;
   const int fail_at = fault_alloc_index();
+  if (fault_wait()) h->given_wait = 0;
   int nalloc = 0;
   auto dal = [&](void** p, size_t bytes) {
     if (ok && (nalloc++ == fail_at || cudaMalloc(p, bytes) != cudaSuccess)) ok = false;
@@ -1117,6 +1125,7 @@ int vt_sample_given(vt_sampler* h, const void* logits, int32_t dtype, int32_t B,
   a.out_logprobs = out_logprobs;
   a.row_status = h->d_status;
   a.err_word = h->d_err;
+  a.wait_cycles = h->given_wait;
   a.seg_sum = h->d_given_sum;
   a.seg_max = h->d_given_max;
   a.group_max = h->d_given_gmax;

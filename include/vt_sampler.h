@@ -113,7 +113,9 @@ void vt_sampler_destroy(vt_sampler* handle);
  * successful reset).  For tests of these failure paths, the environment
  * variable VT_FAULT_INJECT=upload makes the upload fail, and
  * VT_FAULT_INJECT=alloc:<n> makes the n-th (0-based) device allocation of
- * vt_sampler_create fail; nothing on the device is made to fault. */
+ * vt_sampler_create fail; VT_FAULT_INJECT=wait, when the handle is created, makes
+ * vt_sample_given take its device waits as run out; nothing on the device is made
+ * to fault. */
 int vt_reset_params(vt_sampler* handle, int32_t B, const float* temperature,
                     const int32_t* top_k, const float* top_p, const float* min_p,
                     const float* presence, const float* frequency,
@@ -247,7 +249,8 @@ int vt_sample_ex(vt_sampler* handle, const void* logits, int32_t dtype, int32_t 
  * value (3e-10 rms): a token differs from the exactly computed one with a
  * probability of the order of 1e-4 a draw at worst (a flat row of V = 2^20 in two
  * halves of equal values), below 1e-5 at V = 151,936.  Same inputs give the same
- * outputs.
+ * outputs, also when a device wait ran out (vt_check_device_errors reports it: the
+ * logits it waited for are then loaded another way).
  * Row status (vt_get_row_status) is written; seeds, counts and the debug views
  * are not touched.  Two launches; enqueues only; may be captured.  Errors:
  * VT_ERR_STATE (no vt_reset_params, or B larger than its rows),
@@ -346,8 +349,8 @@ int vt_debug_set_phase_event(vt_sampler* handle, void* event);
 int vt_debug_last_handover(vt_sampler* handle, int32_t* rows);
 
 /* Debug: run the bounded-wait path to its end.  One thread waits on a barrier
- * that nothing completes for limit_ns (1 ns .. 1 s) of the GPU timer, as the
- * sampling kernels' bounded waits do, then records a timeout in the handle's
+ * that nothing completes for limit_ns (1 ns .. 1 s) of the GPU timer and as long
+ * again by the SM's clock, as the kernels' bounded waits do, then records a timeout in the handle's
  * error word and returns, leaving the context usable; the next
  * vt_check_device_errors returns VT_ERR_TIMEOUT.  Stream-ordered on `stream`.
  * Errors: VT_ERR_INVALID_ARG, VT_ERR_CUDA. */

@@ -5,7 +5,7 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
-from test_given import run, uniforms
+from test_given import EMPTY, ROWS, logits, run, uniforms
 
 torch = pytest.importorskip("torch")
 
@@ -123,3 +123,27 @@ def test_tensors_of_another_gpu_are_refused():
     with pytest.raises(ValueError):
         s.sample_given(x, u, out=(tok, lp), stream=Stream())
     assert not called
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_waits_that_run_out(dtype, monkeypatch):
+    """Every wait for a copy taken as run out: the call is reported and its draws are right, on
+    rows that come by copies throughout and on rows with a ragged end, several segments a warp."""
+    from device_token_sampling_gb300 import Sampler, VtError, sampler
+    for B, V in ((300, 20480), (700, 5000), (1, 4096)):
+        x, u = logits(B, B, V, dtype), uniforms(B, B, 3)
+        rows = [ROWS[i % len(ROWS)] for i in range(B)]
+        tok, lp, _ = run(x, u, rows, check=False)
+        monkeypatch.setenv("VT_FAULT_INJECT", "wait")
+        s = Sampler(max_batch=B, max_vocab=V)
+        monkeypatch.delenv("VT_FAULT_INJECT")
+        a = {n: np.array([{**EMPTY, **r}[n] for r in rows]) for n in ("T", "k", "p", "mp")}
+        s.reset_params(a["T"], a["k"], a["p"], a["mp"], np.zeros(B), np.zeros(B), np.ones(B),
+                       np.zeros(B, np.uint64))
+        got, got_lp = s.sample_given(x, u)
+        with pytest.raises(VtError) as e:
+            s.check_device_errors()
+        assert e.value.code == sampler.VT_ERR_TIMEOUT
+        s.check_device_errors()
+        assert torch.equal(got, tok) and torch.equal(got_lp, lp)
