@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <new>
 
@@ -23,6 +24,7 @@ struct vt_paged {
   float2* d_part_ml = nullptr;
   int32_t* d_err = nullptr;  // the error word, then the attention's work counter
   int32_t* h_err = nullptr;
+  int64_t wait_cycles = vt::kWaitCycles;  // limit of the attention's waits
   cudaStream_t last_stream = nullptr;
   bool launched = false;
 };
@@ -133,6 +135,9 @@ int vt_paged_create(const vt_paged_config* config, vt_paged** out) {
   if (!h) return VT_ERR_CUDA;
   h->cfg = *config;
   while ((1 << h->shift) < config->block_size) ++h->shift;
+  // (for the test of this failure path: the waits count as run out)
+  const char* fault = std::getenv("VT_FAULT_INJECT");
+  if (fault && std::strcmp(fault, "wait") == 0) h->wait_cycles = 0;
   Device guard(config->device);
   cudaDeviceProp prop;
   bool ok = guard.ok && cudaGetDeviceProperties(&prop, config->device) == cudaSuccess &&
@@ -311,6 +316,7 @@ int vt_paged_attention_ex(vt_paged* h, int32_t dtype, int32_t B, const void* q, 
   a.work = h->d_err + 1;
   a.num_sms = h->num_sms;
   a.err_word = h->d_err;
+  a.wait_cycles = h->wait_cycles;
   cudaStream_t st = (cudaStream_t)stream;
   VT_TRY(h, vt::launch_prefix_attention(a, dtype, c.head_dim, st));
   h->last_stream = st;

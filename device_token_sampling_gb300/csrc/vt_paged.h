@@ -67,6 +67,7 @@ struct AttnArgs {
   int32_t* work;               // units taken; 0 between calls
   int32_t num_sms;
   int32_t* err_word;
+  int64_t wait_cycles;         // limit of prefix_kernel's waits; 0: they have run out
 };
 // dtype as VT_DTYPE_BF16 / VT_DTYPE_F16; head_dim 64 or 128.
 cudaError_t launch_prefix_attention(const AttnArgs& a, int dtype, int head_dim,

@@ -178,12 +178,24 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return r;
 }
 
+// A wait of at most `limit` cycles; with 0 it has run out.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t phase, long long limit) {
+  return limit > 0 && mbar_wait_clocked(bar, phase, limit);
+}
+// The whole warp's: it runs out for all lanes or for none, so that they leave their
+// loops together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase, long long limit) {
+  return __all_sync(0xffffffffu, wait_for(bar, phase, limit));
+}
+constexpr long long kDrainCycles = 200000000ll;  // for what is in flight after a run-out
+
 struct Bars {
   uint64_t k_full[kKvStages], k_empty[kKvStages], v_full[kKvStages], v_empty[kKvStages];
   // of each tile, by the parity of the step where a second step may begin before
   // the first is noticed
   uint64_t s_full[2][2], p_full[2][2], pv_done[2], o_done[2];
   uint64_t v_tail;  // the last V tile's rows past the end are zeros
+  uint64_t drained[2];  // a tile's MMAs after a wait has run out
 };
 
 template <typename T, int D>
@@ -235,6 +247,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       }
       mbar_init(&bars.pv_done[t], 1);
       mbar_init(&bars.o_done[t], 1);
+      mbar_init(&bars.drained[t], 1);
     }
     fence_mbar_init();
   }
@@ -283,12 +296,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   if (warp != kLoadWarp)
     asm volatile("bar.sync 1, %0;" ::"n"(kLoadWarp * 32) : "memory");
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+  const long long limit = a.wait_cycles;
   bool ok = true;
 
   if (warp == kLoadWarp) {
     // ---- loads -----------------------------------------------------------------
     const int boxes = kTileTokens / box;
-    int issued = 0;
+    int k_issued = 0, v_issued = 0;  // tiles
     for (int j = 0; j < n_tiles; ++j) {
       const int st = j % kKvStages, tok0 = t0 + j * kTileTokens;
       const uint32_t par = ((j / kKvStages) & 1) ^ 1;
@@ -316,7 +330,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       }
       __syncwarp();
       const int in_block = tok0 & ((1 << a.shift) - 1);  // (blocks longer than a tile)
-      ok = mbar_wait_clocked(&bars.k_empty[st], par);
+      ok = warp_wait(&bars.k_empty[st], par, limit);
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&bars.k_full[st], S::kTile);
       __syncwarp();
@@ -328,7 +342,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             tma_tile(base + S::kK + st * S::kTile + h * S::kHalf + i * box * 128, &map_k,
                      &bars.k_full[st], h * 64, in_block, kvh, blk[q]);
       }
-      ok = mbar_wait_clocked(&bars.v_empty[st], par);
+      k_issued = j + 1;
+      ok = warp_wait(&bars.v_empty[st], par, limit);
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&bars.v_full[st], S::kTile);
       __syncwarp();
@@ -340,11 +355,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             tma_tile(base + S::kV + st * S::kTile + h * S::kHalf + i * box * 128, &map_v,
                      &bars.v_full[st], h * 64, in_block, kvh, blk[q]);
       }
-      issued = j + 1;
+      v_issued = j + 1;
     }
-    if (ragged && issued == n_tiles) {
+    if (ragged && v_issued == n_tiles) {
       const int j = n_tiles - 1, st = j % kKvStages;
-      ok = ok && mbar_wait_clocked(&bars.v_full[st], (j / kKvStages) & 1);
+      ok = warp_wait(&bars.v_full[st], (j / kKvStages) & 1, limit);
       const int from = t1 - t0 - j * kTileTokens, to = (from + box - 1) / box * box;
       for (int i = from * 8 + lane; i < to * 8; i += 32)
         for (int h = 0; h < D / 64; ++h)
@@ -355,10 +370,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       if (lane == 0) mbar_arrive(&bars.v_tail);
     }
     // no copy is in flight when the CTA's memory goes to another
-    for (int j = max(0, issued - kKvStages); j < issued; ++j) {
-      mbar_wait_clocked(&bars.k_full[j % kKvStages], (j / kKvStages) & 1, 200000000ll);
-      mbar_wait_clocked(&bars.v_full[j % kKvStages], (j / kKvStages) & 1, 200000000ll);
-    }
+    for (int j = max(0, k_issued - kKvStages); j < k_issued; ++j)
+      mbar_wait_clocked(&bars.k_full[j % kKvStages], (j / kKvStages) & 1, kDrainCycles);
+    for (int j = max(0, v_issued - kKvStages); j < v_issued; ++j)
+      mbar_wait_clocked(&bars.v_full[j % kKvStages], (j / kKvStages) & 1, kDrainCycles);
   } else if (warp >= kMmaWarp) {
     // ---- MMAs ------------------------------------------------------------------
     // The whole warp walks the steps and waits; one lane issues.
@@ -381,9 +396,9 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       for (int j = -1; j < n_steps; ++j) {
         const int n = j + 1, st_n = (n >> 1) & 1, st_j = (j >> 1) & 1;
         if (n < n_steps) {  // S_t = Q_t K^T of the next step
-          if (!(n & 1)) ok = mbar_wait_clocked(&bars.k_full[st_n], (n >> 2) & 1);
+          if (!(n & 1)) ok = warp_wait(&bars.k_full[st_n], (n >> 2) & 1, limit);
           // the buffer is free when the product with its last P is done
-          if (ok && j >= 1) ok = mbar_wait_clocked(&bars.pv_done[t], (j - 1) & 1);
+          if (ok && j >= 1) ok = warp_wait(&bars.pv_done[t], (j - 1) & 1, limit);
           if (!ok) break;
           fence_after();
           if (elect_one()) {
@@ -400,10 +415,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           __syncwarp();
         }
         if (j >= 0) {  // O_t += P_t V of this one
-          ok = mbar_wait_clocked(&bars.p_full[t][j & 1], (j >> 1) & 1);
+          ok = warp_wait(&bars.p_full[t][j & 1], (j >> 1) & 1, limit);
           if (ok && !(j & 1)) {
-            ok = mbar_wait_clocked(&bars.v_full[st_j], (j >> 2) & 1);
-            if (ok && ragged && (j >> 1) == n_tiles - 1) ok = mbar_wait_clocked(&bars.v_tail, 0);
+            ok = warp_wait(&bars.v_full[st_j], (j >> 2) & 1, limit);
+            if (ok && ragged && (j >> 1) == n_tiles - 1) ok = warp_wait(&bars.v_tail, 0, limit);
           }
           if (!ok) break;
           fence_after();
@@ -420,6 +435,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           }
           __syncwarp();
         }
+      }
+      if (!ok) {  // none of its MMAs is in flight when the CTA's memory goes to another
+        if (elect_one()) mma_commit(&bars.drained[t]);
+        __syncwarp();
+        mbar_wait_clocked(&bars.drained[t], 0, kDrainCycles);
       }
     }
   } else {
@@ -438,7 +458,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       const uint32_t to = tmem + lanes + TM::kO + t * D;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n_steps; ++j) {
-        ok = mbar_wait_clocked(&bars.s_full[t][j & 1], (j >> 1) & 1);
+        ok = wait_for(&bars.s_full[t][j & 1], (j >> 1) & 1, limit);
         if (!__all_sync(0xffffffffu, ok)) break;
         fence_after();
         const uint32_t ts = tmem + lanes + TM::s(t, j);
@@ -474,7 +494,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           if (grow) m = m_new;
           l *= f;
           if (j > 0) {
-            ok = mbar_wait_clocked(&bars.pv_done[t], (j - 1) & 1);
+            ok = wait_for(&bars.pv_done[t], (j - 1) & 1, limit);
             if (!__all_sync(0xffffffffu, ok)) break;
             fence_after();
 #pragma unroll 1
@@ -512,7 +532,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         mbar_arrive(&bars.p_full[t][j & 1]);
       }
       // the row's part
-      if (ok) ok = mbar_wait_clocked(&bars.o_done[t], 0);
+      if (ok) ok = wait_for(&bars.o_done[t], 0, limit);
       if (__all_sync(0xffffffffu, ok)) {
         fence_after();
         const int64_t at = (int64_t)split * a.B * a.hq + (int64_t)b * a.hq + head;

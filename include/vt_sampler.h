@@ -518,7 +518,9 @@ typedef struct vt_paged_config {
 
 /* Create a handle and allocate its workspace.  Errors: VT_ERR_INVALID_ARG (null
  * pointer, value out of range), VT_ERR_CUDA (no such device, out of memory, not
- * an sm_103 GPU). */
+ * an sm_103 GPU).  For a test of the failure path, the environment variable
+ * VT_FAULT_INJECT=wait makes the handle's attention take its device waits as run
+ * out; nothing on the device is made to fault. */
 int vt_paged_create(const vt_paged_config* config, vt_paged** out);
 
 /* Free the handle after its pending work.  NULL is ignored. */

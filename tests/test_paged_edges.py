@@ -149,3 +149,31 @@ def test_lengths_past_a_narrowed_table_are_cut(B, prefix):
     got, lse = p.attention(c["q"], c["k"], c["v"], wide[:B, 3:7], *rest)
     p.check_errors()
     assert torch.equal(got, want) and torch.equal(lse, wlse)
+
+
+# ---- waits ---------------------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_waits_that_run_out(d, monkeypatch):
+    """Every wait of the shared prefix's kernel taken as run out: the call comes back and is
+    reported, and another handle attends as before."""
+    from device_token_sampling_gb300 import PagedBatch, VtError, sampler
+    c = make_attention(17, [700 + i for i in range(40)], 8, 2, d, 16, 690, BF)
+    args = (c["q"], c["k"], c["v"], c["table"], c["seq"], c["pre"], 690)
+    with PagedBatch(40, 16, c["cols"], 8, 2, d) as p:
+        want, wlse = p.attention(*args)
+        p.check_errors()
+    monkeypatch.setenv("VT_FAULT_INJECT", "wait")
+    broken = PagedBatch(40, 16, c["cols"], 8, 2, d)
+    monkeypatch.delenv("VT_FAULT_INJECT")
+    for _ in range(2):
+        broken.attention(*args)
+        with pytest.raises(VtError) as e:
+            broken.check_errors()
+        assert e.value.code == sampler.VT_ERR_TIMEOUT
+        broken.check_errors()
+    with PagedBatch(40, 16, c["cols"], 8, 2, d) as p:
+        out, lse = p.attention(*args)
+        p.check_errors()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
