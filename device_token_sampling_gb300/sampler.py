@@ -151,7 +151,8 @@ def other_stream(stream):
     if stream is None:
         return None
     import torch
-    return None if stream == torch.cuda.current_stream(stream.device) else stream
+    here = torch._C._cuda_getCurrentRawStream(stream.device_index)
+    return None if stream.cuda_stream == here else stream
 
 
 def make_on(stream, make):
@@ -313,11 +314,12 @@ class Sampler:
         V = logits.shape[1] if V is None else V
         n = int(num_logprobs)
         dev = logits.device
+        other = other_stream(stream)
         if out is None:
-            out = (torch.empty(B, dtype=torch.int32, device=dev),
-                   torch.empty(B, dtype=torch.float32, device=dev),
-                   torch.empty((B, n), dtype=torch.int32, device=dev),
-                   torch.empty((B, n), dtype=torch.float32, device=dev))
+            out = make_on(other, lambda: (torch.empty(B, dtype=torch.int32, device=dev),
+                                          torch.empty(B, dtype=torch.float32, device=dev),
+                                          torch.empty((B, n), dtype=torch.int32, device=dev),
+                                          torch.empty((B, n), dtype=torch.float32, device=dev)))
         tok, lp, tid, tlp = out
         args = (self._h, P(logits.data_ptr()), dtype, B, V, ld, n, 1 if update_counts else 0,
                 P(tok.data_ptr()), P(lp.data_ptr()) if lp is not None else None,
@@ -325,6 +327,8 @@ class Sampler:
         if probs is None:
             rc = self._lib.vt_sample(*args, _stream_ptr(stream))
             self._check(rc, "vt_sample")
+            if other is not None:
+                lend(other, (logits, *out))
             return out
         if (probs.dim() != 2 or not probs.is_cuda or probs.dtype != torch.float32
                 or probs.shape[0] != B or probs.shape[1] < V or probs.stride(1) != 1):
@@ -332,6 +336,8 @@ class Sampler:
         rc = self._lib.vt_sample_ex(*args, P(probs.data_ptr()), probs.stride(0),
                                     _stream_ptr(stream))
         self._check(rc, "vt_sample_ex")
+        if other is not None:
+            lend(other, (logits, probs, *out))
         return out
 
     def sample_given(self, logits, uniforms, V: int | None = None, out=None, stream=None,
@@ -451,7 +457,8 @@ class Sampler:
 
     def row_status(self, B: int, stream=None):
         import torch
-        st = torch.empty(B, dtype=torch.int32, device=f"cuda:{self.device}")
+        st, = make_on(other_stream(stream), lambda: (
+            torch.empty(B, dtype=torch.int32, device=f"cuda:{self.device}"),))
         self._check(self._lib.vt_get_row_status(self._h, P(st.data_ptr()), _stream_ptr(stream)),
                     "vt_get_row_status")
         return st
@@ -459,9 +466,10 @@ class Sampler:
     def filter_boundary(self, B: int, stream=None):
         import torch
         d = f"cuda:{self.device}"
-        v = torch.empty(B, dtype=torch.float32, device=d)
-        i = torch.empty(B, dtype=torch.int32, device=d)
-        k = torch.empty(B, dtype=torch.int32, device=d)
+        v, i, k = make_on(other_stream(stream), lambda: (
+            torch.empty(B, dtype=torch.float32, device=d),
+            torch.empty(B, dtype=torch.int32, device=d),
+            torch.empty(B, dtype=torch.int32, device=d)))
         self._check(self._lib.vt_debug_filter_boundary(self._h, P(v.data_ptr()), P(i.data_ptr()),
                                                        P(k.data_ptr()), _stream_ptr(stream)),
                     "vt_debug_filter_boundary")
@@ -519,13 +527,17 @@ class Sampler:
         pb = int(self._lib.vt_shard_part_bytes(K))
         if pb < 0:
             raise ValueError(f"K={K} outside 1..256")
+        other = other_stream(stream)
         if out is None:
-            out = torch.empty((B, pb), dtype=torch.uint8, device=logits.device)
+            out, = make_on(other, lambda: (
+                torch.empty((B, pb), dtype=torch.uint8, device=logits.device),))
         elif out.dtype != torch.uint8 or tuple(out.shape) != (B, pb) or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous uint8 tensor of shape {(B, pb)}")
         rc = self._lib.vt_shard_partials(self._h, P(logits.data_ptr()), dtype, B, Vs, ld, v0, V,
                                          K, P(out.data_ptr()), _stream_ptr(stream))
         self._check(rc, "vt_shard_partials")
+        if other is not None:
+            lend(other, (logits, out))
         return out
 
     def shard_merge(self, parts, V: int, K: int, num_logprobs: int = 0, stream=None):
@@ -540,15 +552,19 @@ class Sampler:
             raise ValueError("parts do not hold records of K elements")
         n = int(num_logprobs)
         dev = parts.device
-        tok = torch.empty(B, dtype=torch.int32, device=dev)
-        lp = torch.empty(B, dtype=torch.float32, device=dev)
-        tid = torch.empty((B, n), dtype=torch.int32, device=dev)
-        tlp = torch.empty((B, n), dtype=torch.float32, device=dev)
+        other = other_stream(stream)
+        tok, lp, tid, tlp = make_on(other, lambda: (
+            torch.empty(B, dtype=torch.int32, device=dev),
+            torch.empty(B, dtype=torch.float32, device=dev),
+            torch.empty((B, n), dtype=torch.int32, device=dev),
+            torch.empty((B, n), dtype=torch.float32, device=dev)))
         rc = self._lib.vt_shard_merge(self._h, P(parts.data_ptr()), S_, B, V, K, n,
                                       P(tok.data_ptr()), P(lp.data_ptr()),
                                       P(tid.data_ptr()) if n else None,
                                       P(tlp.data_ptr()) if n else None, _stream_ptr(stream))
         self._check(rc, "vt_shard_merge")
+        if other is not None:
+            lend(other, (parts,))
         return tok, lp, tid, tlp
 
     def set_path(self, path: int):

@@ -59,7 +59,36 @@ def make_attention():
             (q, table, lens))
 
 
-@pytest.mark.parametrize("make", [make_given, make_tables, make_attention])
+def greedy(B=4096, V=4096, **kw):
+    """A sampler whose draws are the same every time, and its logits."""
+    from device_token_sampling_gb300 import Sampler
+    s = Sampler(max_batch=B, max_vocab=V, **kw)
+    one, zero = np.ones(B), np.zeros(B)
+    s.reset_params(zero, zero, one, zero, zero, zero, one, np.zeros(B, np.uint64))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    return s, torch.randn((B, V), generator=g, device="cuda")
+
+
+def make_sample():
+    s, x = greedy(max_logprobs=8)
+    return s, lambda i, stream: s.sample(i[0], num_logprobs=8, stream=stream), (x,)
+
+
+def make_partials():
+    s, x = greedy()
+    return s, lambda i, stream: (s.shard_partials(i[0], 0, 4096, 32, stream=stream),), (x,)
+
+
+def make_merge():
+    s, x = greedy(max_logprobs=8)
+    parts = s.shard_partials(x, 0, 4096, 32)[None]
+    return s, lambda i, stream: s.shard_merge(i[0], 4096, 32, 8, stream=stream), (parts,)
+
+
+CALLS = [make_given, make_tables, make_attention, make_sample, make_partials, make_merge]
+
+
+@pytest.mark.parametrize("make", CALLS)
 def test_outputs_wait_for_pending_work_on_the_current_stream(make):
     """A tensor is freed while a copy of it is still pending on the current stream; the call on
     another stream makes outputs of the same size."""
@@ -68,7 +97,7 @@ def test_outputs_wait_for_pending_work_on_the_current_stream(make):
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     torch.cuda.synchronize()
-    held = [torch.full((n // 4,), 7, dtype=torch.int32, device="cuda") for n in sizes if n >= 1 << 20]
+    held = [torch.full((n // 4,), 7, dtype=torch.int32, device="cuda") for n in sizes if n >= 1 << 16]
     assert held
     keep = busy()
     copies = [h.clone() for h in held]
@@ -80,7 +109,7 @@ def test_outputs_wait_for_pending_work_on_the_current_stream(make):
         assert bool((c == 7).all())
 
 
-@pytest.mark.parametrize("make", [make_given, make_tables, make_attention])
+@pytest.mark.parametrize("make", CALLS)
 def test_inputs_live_until_the_call_has_read_them(make):
     """Inputs that the caller drops at once, with the call still pending on its stream."""
     handle, call, inputs = make()
@@ -101,7 +130,7 @@ def test_inputs_live_until_the_call_has_read_them(make):
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("make", [make_given, make_tables, make_attention])
+@pytest.mark.parametrize("make", CALLS)
 def test_outputs_used_on_the_current_stream_live_until_it_is_done(make):
     """Outputs handed over to the current stream, read there by pending work and dropped; the
     next call on the other stream makes outputs of the same size."""
