@@ -245,8 +245,8 @@ int vt_sample_ex(vt_sampler* handle, const void* logits, int32_t dtype, int32_t 
  *   out_logprobs   device float[B][draws]: log-softmax of z_t over the whole row
  *                  at the token (NaN for a row without a token); may be NULL.
  * The sums that decide a token are integers of 2^-42 (V = 2^20) to 2^-51 (V <=
- * 2^11) of the power of two above the largest mass, each mass within 1e-9 of its
- * value (3e-10 rms): a token differs from the exactly computed one with a
+ * 2^11) of the power of two above the largest mass, each mass within 1.1e-9 of its
+ * value (3e-10 rms) before it is cut to them: a token differs from the exactly computed one with a
  * probability of the order of 1e-4 a draw at worst (a flat row of V = 2^20 in two
  * halves of equal values), below 1e-5 at V = 151,936.  Same inputs give the same
  * outputs, also when a device wait ran out (vt_check_device_errors reports it: the
