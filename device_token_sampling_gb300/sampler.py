@@ -358,6 +358,8 @@ class Sampler:
                 dtype = DTYPE_BF16
             else:
                 raise ValueError(f"unsupported logits dtype {t}")
+        elif logits.element_size() != (4 if dtype == DTYPE_F32 else 2):
+            raise ValueError(f"logits of {logits.dtype} are not of dtype {dtype}")
         B, cols = logits.shape
         if V is None:
             V = cols

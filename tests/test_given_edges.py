@@ -102,9 +102,18 @@ class OnDevice:
     def data_ptr(self):
         return 1 << 20
 
+    def element_size(self):
+        return self.dtype.itemsize
 
-def test_tensors_of_another_gpu_are_refused():
-    """Their addresses mean nothing on the handle's device: nothing is called with them."""
+
+class Stream:
+    """The default stream of device 0, as far as its attributes go."""
+    cuda_stream, device, device_index = 0, torch.device("cuda", 0), 0
+
+
+@pytest.fixture
+def recorder():
+    """A sampler on device 0 whose library only records its calls."""
     from device_token_sampling_gb300 import Sampler
     called = []
 
@@ -115,15 +124,31 @@ def test_tensors_of_another_gpu_are_refused():
 
     s = Sampler.__new__(Sampler)
     s._lib, s._h, s.device = Lib(), None, 0
+    return s, called
+
+
+def test_tensors_of_another_gpu_are_refused(recorder):
+    """Their addresses mean nothing on the handle's device: nothing is called with them."""
+    s, called = recorder
     x, u = OnDevice((4, 100), 1), OnDevice((4, 2), 1)
     tok, lp = OnDevice((4, 2), 1), OnDevice((4, 2), 1)
     tok.dtype = torch.int32
-
-    class Stream:
-        cuda_stream, device = 0, torch.device("cuda", 0)
-
     with pytest.raises(ValueError):
         s.sample_given(x, u, out=(tok, lp), stream=Stream())
+    assert not called
+
+
+@pytest.mark.parametrize("have,given", [(torch.bfloat16, 0), (torch.float32, 1), (torch.uint8, 1),
+                                        (torch.float16, 0)])
+def test_logits_of_another_size_than_the_given_dtype_are_refused(recorder, have, given):
+    """A dtype wider than the tensor's elements would read past its end."""
+    s, called = recorder
+    x, u = OnDevice((4, 100), 0), OnDevice((4, 2), 0)
+    x.dtype = have
+    tok, lp = OnDevice((4, 2), 0), OnDevice((4, 2), 0)
+    tok.dtype = torch.int32
+    with pytest.raises(ValueError):
+        s.sample_given(x, u, out=(tok, lp), stream=Stream(), dtype=given)
     assert not called
 
 
