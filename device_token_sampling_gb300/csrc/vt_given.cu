@@ -378,6 +378,8 @@ __global__ void __launch_bounds__(kStreamThreads, kStreamCtas) stream_kernel(Giv
         }
         sum = warp_sum_u64(sum);
       } else if (a.out_logprobs) {
+        // (for log-probs alone, so by the special function unit, each within 2^-22: no
+        // token depends on them)
         float s = 0.f;
         const float shift = lse_shift(zm), base = lse_base(zm);
 #pragma unroll
@@ -1961,7 +1963,9 @@ cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t strea
   // CTAs that share the rows which are read again: as many as two to an SM hold for
   // all rows, at least two (1024 fp32 rows: 491 us, with four 532; 256 bf16 rows: 127
   // and 129), and eight segments to each (5 rows of 32003: 35 us with four or
-  // eight, 37 with sixteen; one row of 151936: 50 with eight, 46 with sixteen)
+  // eight, 37 with sixteen; one row of 151936: 50 with eight, 46 with sixteen).
+  // The rule counts all rows, also those whose other CTAs leave at once (greedy,
+  // unfiltered and listed ones): batches of few team rows use few of the SMs.
   int ctas = 2;
   while (ctas < kMaxCtas && 2 * ctas * a.B <= 2 * num_sms && 16 * ctas <= a.segs) ctas *= 2;
   return dtype == VT_DTYPE_F32 ? launch_given_typed<float>(a, num_sms, ctas, stream)

@@ -441,8 +441,8 @@ __device__ __forceinline__ void attend_row(const AttnArgs& a, int64_t row, int l
 // One warp to a query head: rescale the parts to their common maximum, sum,
 // divide.  A part that holds nothing (sum 0) is not read; a NaN among the scores
 // makes its part's sum NaN and so the row NaN.  The parts' factors are made a lane
-// to a part and four parts are read at a time: one after another, the 24 parts of
-// 64 requests behind 8,192 tokens cost 2 us more (52.3 and 50.2 over all), the 24
+// to a part and four parts are read at a time: one after another, the 21 parts of
+// 64 requests behind 8,192 tokens cost 2 us more (52.3 and 50.2 over all), the 17
 // of 37 requests 4 us (28.5 and 24.2).  What bounds it: those reads' latency.
 //
 // A request shorter than the prefix shares tiles of V with requests that attend to

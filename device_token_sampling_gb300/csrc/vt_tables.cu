@@ -18,10 +18,11 @@
 // shared memory and then writes its own part of the table and of the slot map.
 // A token's block is worked out from its source (old table entry, prefix or
 // free list), never read from an entry that this launch writes.  What bounds it:
-// launch latency for a decode step's sizes (5.5 us), the 12 bytes written a token
-// for prompts (2048 requests of up to 8192 tokens, 16.7 M places in blocks of 16:
-// 47 us, 207 MB at 4.4 TB/s, a warp to a stretch of up to 512 tokens; 56 us with
-// four tokens to a thread, which finds its request for every four).
+// launch latency for a decode step's sizes (5.5 us), its instructions for prompts
+// (2048 requests of up to 8192 tokens, 16.7 M places in blocks of 16: 47 us, 207 MB
+// at 4.4 TB/s; 68 instructions to a lane's place, issued in 72 % of the cycles; a
+// warp to a stretch of up to 512 tokens; 56 us with four tokens to a thread, which
+// finds its request for every four).
 #include "vt_device.cuh"
 #include "vt_paged.h"
 #include "vt_sampler.h"
