@@ -270,4 +270,25 @@ struct GivenArgs {
 cudaError_t prepare_given();
 cudaError_t launch_given(GivenArgs a, int dtype, int num_sms, cudaStream_t stream);
 
+// ---- drafts against the target's probabilities (vt_verify.cu) -----------------
+struct VerifyArgs {
+  const void* target;        // rows of V: with starts row starts[b] + i, else row i of b
+  int64_t t_batch, t_row;
+  const int32_t* starts;     // [B + 1] or null
+  int64_t rows;              // rows there are (with starts)
+  const void* draft;         // row i of b, or null: lookups
+  int64_t d_batch, d_row;
+  const int32_t* tokens;     // [B][K]
+  const int32_t* lens;       // [B] or null: K each
+  const float* uniforms;     // [B][K + 1]
+  int32_t B, K, V;
+  int32_t vec;               // every row starts on 16 bytes
+  int32_t* out_tokens;       // [B][K + 1]
+  int32_t* out_accepted;     // [B]
+  int32_t* row_status;       // [B]
+  int32_t ctas;              // to a request; filled by launch_verify
+};
+cudaError_t prepare_verify();
+cudaError_t launch_verify(VerifyArgs a, int dtype, int num_sms, cudaStream_t stream);
+
 }  // namespace vt

@@ -23,6 +23,10 @@ struct vt_paged {
   float* d_part_o = nullptr;
   float2* d_part_ml = nullptr;
   int32_t* d_err = nullptr;  // the error word, then the attention's work counter
+  // of release and compact: a bit to a block, the used ids before each 32, two totals
+  uint32_t* d_used = nullptr;
+  int32_t* d_ranks = nullptr;
+  int32_t* d_totals = nullptr;
   int32_t* h_err = nullptr;
   int64_t wait_cycles = vt::kWaitCycles;  // limit of the attention's waits
   cudaStream_t last_stream = nullptr;
@@ -123,6 +127,9 @@ void free_paged(vt_paged* h) {
   if (h->d_part_o) cudaFree(h->d_part_o);
   if (h->d_part_ml) cudaFree(h->d_part_ml);
   if (h->d_err) cudaFree(h->d_err);
+  if (h->d_used) cudaFree(h->d_used);
+  if (h->d_ranks) cudaFree(h->d_ranks);
+  if (h->d_totals) cudaFree(h->d_totals);
   if (h->h_err) cudaFreeHost(h->h_err);
   delete h;
 }
@@ -147,7 +154,11 @@ int vt_paged_create(const vt_paged_config* config, vt_paged** out) {
     ok = vt::prepare_tables() == cudaSuccess && vt::prepare_prefix_attention() == cudaSuccess &&
          cudaMalloc(&h->d_err, 2 * sizeof(int32_t)) == cudaSuccess &&
          cudaMemset(h->d_err, 0, 2 * sizeof(int32_t)) == cudaSuccess &&
-         cudaMallocHost(&h->h_err, sizeof(int32_t)) == cudaSuccess;
+         cudaMallocHost(&h->h_err, sizeof(int32_t)) == cudaSuccess &&
+         vt::prepare_blocks() == cudaSuccess &&
+         cudaMalloc(&h->d_used, VT_PAGED_MAX_CACHE_BLOCKS / 8) == cudaSuccess &&
+         cudaMalloc(&h->d_ranks, VT_PAGED_MAX_CACHE_BLOCKS / 8) == cudaSuccess &&
+         cudaMalloc(&h->d_totals, 2 * sizeof(int32_t)) == cudaSuccess;
   }
   if (ok && config->q_heads > 0) {
     h->part_rows = 8ll * config->max_batch * config->q_heads + 32768;
@@ -183,6 +194,9 @@ int vt_paged_check_errors(vt_paged* h) {
   VT_TRY(h, cudaMemset(h->d_err, 0, sizeof(int32_t)));
   if (*h->h_err & vt::kErrTimeout)
     return fail(h, VT_ERR_TIMEOUT, "a bounded device wait ran out");
+  if (*h->h_err & vt::kErrBadRows)
+    return fail(h, VT_ERR_INVALID_ARG, "starts outside the rows of q were met; their requests "
+                                       "were left out");
   return fail(h, VT_ERR_INVALID_ARG, "a block id outside the cache was met; its tokens were "
                                      "left out");
 }
@@ -336,4 +350,263 @@ int vt_paged_attention(vt_paged* h, int32_t dtype, int32_t B, const void* q, int
                                block_stride, token_stride, head_stride, table, ld_table,
                                (int32_t)std::min<int64_t>(ld_table, 0x7fffffff), seq_lens,
                                prefix_blocks, prefix_len, max_seq_len, scale, out, out_lse, stream);
+}
+
+int vt_paged_chunk_attention(vt_paged* h, int32_t dtype, int32_t B, int32_t T, const void* q,
+                             int64_t q_row, int64_t q_head, const int32_t* starts,
+                             const void* k_cache, const void* v_cache, int32_t num_blocks,
+                             int64_t block_stride, int64_t token_stride, int64_t head_stride,
+                             const int32_t* table, int64_t ld_table, int32_t table_cols,
+                             const int32_t* seq_lens, float scale, void* out, float* out_lse,
+                             void* stream) {
+  if (!h) return VT_ERR_INVALID_ARG;
+  const vt_paged_config& c = h->cfg;
+  if (c.q_heads == 0)
+    return fail(h, VT_ERR_STATE, "the handle was created for tables alone (q_heads=0)");
+  if (dtype != VT_DTYPE_BF16 && dtype != VT_DTYPE_F16)
+    return fail(h, VT_ERR_INVALID_ARG, "dtype %d: need bf16 or fp16", dtype);
+  if (B < 1) return fail(h, VT_ERR_INVALID_ARG, "B=%d: need B >= 1", B);
+  if (B > c.max_batch) return fail(h, VT_ERR_CAPACITY, "B=%d above max_batch=%d", B, c.max_batch);
+  if (T < 0 || T > VT_PAGED_MAX_TOKENS)
+    return fail(h, VT_ERR_INVALID_ARG, "T=%d outside [0, %d]", T, VT_PAGED_MAX_TOKENS);
+  if (!starts || !k_cache || !v_cache || !table || !seq_lens || (T > 0 && (!q || !out)))
+    return fail(h, VT_ERR_INVALID_ARG, "a null array");
+  if (num_blocks < 1 || ld_table < 1 || table_cols < 1)
+    return fail(h, VT_ERR_INVALID_ARG, "num_blocks=%d, ld_table=%lld, table_cols=%d: need at least 1",
+                num_blocks, (long long)ld_table, table_cols);
+  if (!std::isfinite(scale)) return fail(h, VT_ERR_INVALID_ARG, "scale is not finite");
+  // rows are copied 16 bytes at a time
+  if ((q_row | q_head | block_stride | token_stride | head_stride) % 8 ||
+      !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
+    return fail(h, VT_ERR_INVALID_ARG,
+                "arrays must start on 16 bytes and strides be multiples of 8 elements");
+  h->err[0] = 0;
+  if (T == 0) return VT_OK;
+  Device guard(c.device);
+  if (!guard.ok) return fail(h, VT_ERR_CUDA, "cannot select device %d", c.device);
+  vt::ChunkArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.q = q;
+  a.q_row = q_row;
+  a.q_head = q_head;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.block_stride = block_stride;
+  a.token_stride = token_stride;
+  a.head_stride = head_stride;
+  a.num_blocks = num_blocks;
+  a.shift = h->shift;
+  a.table = table;
+  a.ld_table = ld_table;
+  a.cols = std::min(c.max_blocks, table_cols);
+  a.starts = starts;
+  a.seq_lens = seq_lens;
+  a.B = B;
+  a.T = T;
+  a.hq = c.q_heads;
+  a.hkv = c.kv_heads;
+  a.G = c.q_heads / c.kv_heads;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = out;
+  a.lse = out_lse;
+  a.num_sms = h->num_sms;
+  a.err_word = h->d_err;
+  a.wait_cycles = h->wait_cycles;
+  cudaStream_t st = (cudaStream_t)stream;
+  VT_TRY(h, vt::launch_chunk(a, dtype, c.head_dim, st));
+  h->last_stream = st;
+  h->launched = true;
+  return VT_OK;
+}
+
+int vt_paged_fork(vt_paged* h, int32_t R, const int32_t* parents, int32_t B, const int32_t* table,
+                  int64_t ld_table, const int32_t* held, const int32_t* seq_lens,
+                  const int32_t* free_blocks, int32_t num_free, const int32_t* cursor,
+                  int32_t* out_table, int64_t ld_out_table, int32_t* out_held,
+                  int32_t* out_seq_lens, int32_t* out_cursor, int32_t* out_src, int32_t* out_dst,
+                  int32_t* out_status, void* stream) {
+  if (!h) return VT_ERR_INVALID_ARG;
+  const vt_paged_config& c = h->cfg;
+  if (R < 1 || B < 1) return fail(h, VT_ERR_INVALID_ARG, "R=%d, B=%d: need at least 1", R, B);
+  if (R > c.max_batch || B > c.max_batch)
+    return fail(h, VT_ERR_CAPACITY, "R=%d or B=%d above max_batch=%d", R, B, c.max_batch);
+  if (!parents || !table || !held || !seq_lens || !cursor || !out_table || !out_held ||
+      !out_seq_lens || !out_cursor || !out_src || !out_dst || !out_status)
+    return fail(h, VT_ERR_INVALID_ARG, "a null array");
+  if (num_free < 0 || (num_free > 0 && !free_blocks))
+    return fail(h, VT_ERR_INVALID_ARG, "num_free=%d with %s free list", num_free,
+                free_blocks ? "its" : "no");
+  if (ld_table < c.max_blocks || ld_out_table < c.max_blocks)
+    return fail(h, VT_ERR_INVALID_ARG, "ld_table=%lld or ld_out_table=%lld below max_blocks=%d",
+                (long long)ld_table, (long long)ld_out_table, c.max_blocks);
+  if (out_table == table || out_held == held || out_seq_lens == seq_lens || out_cursor == cursor)
+    return fail(h, VT_ERR_INVALID_ARG, "table, held, seq_lens and cursor are not updated in place");
+  Device guard(c.device);
+  if (!guard.ok) return fail(h, VT_ERR_CUDA, "cannot select device %d", c.device);
+  vt::ForkArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.R = R;
+  a.B = B;
+  a.shift = h->shift;
+  a.cols = c.max_blocks;
+  a.parents = parents;
+  a.table = table;
+  a.ld = ld_table;
+  a.held = held;
+  a.seq_lens = seq_lens;
+  a.free_blocks = free_blocks;
+  a.n_free = num_free;
+  a.cursor = cursor;
+  a.out_table = out_table;
+  a.ld_out = ld_out_table;
+  a.out_held = out_held;
+  a.out_seq = out_seq_lens;
+  a.out_cursor = out_cursor;
+  a.src = out_src;
+  a.dst = out_dst;
+  a.status = out_status;
+  cudaStream_t st = (cudaStream_t)stream;
+  VT_TRY(h, vt::launch_fork(a, h->num_sms, st));
+  h->last_stream = st;
+  h->launched = true;
+  h->err[0] = 0;
+  return VT_OK;
+}
+
+namespace {
+
+// The checks and arguments that release and compact share.
+int reclaim_args(vt_paged* h, vt::ReclaimArgs& a, int32_t B, int32_t* table, int64_t ld_table,
+                 const int32_t* held, const int32_t* seq_lens, const int32_t* prefix_blocks,
+                 int32_t num_prefix_blocks, int32_t num_blocks, int32_t* out_held,
+                 int32_t* out_free_blocks, int32_t* out_cursor) {
+  const vt_paged_config& c = h->cfg;
+  if (B < 1) return fail(h, VT_ERR_INVALID_ARG, "B=%d: need B >= 1", B);
+  if (B > c.max_batch) return fail(h, VT_ERR_CAPACITY, "B=%d above max_batch=%d", B, c.max_batch);
+  if (num_blocks < 1) return fail(h, VT_ERR_INVALID_ARG, "num_blocks=%d: need at least 1", num_blocks);
+  if (num_blocks > VT_PAGED_MAX_CACHE_BLOCKS)
+    return fail(h, VT_ERR_CAPACITY, "num_blocks=%d above %d", num_blocks, VT_PAGED_MAX_CACHE_BLOCKS);
+  if (!table || !held || !seq_lens || !out_held || !out_free_blocks || !out_cursor)
+    return fail(h, VT_ERR_INVALID_ARG, "a null array");
+  if (num_prefix_blocks < 0 || (num_prefix_blocks > 0 && !prefix_blocks))
+    return fail(h, VT_ERR_INVALID_ARG, "num_prefix_blocks=%d with %s prefix blocks",
+                num_prefix_blocks, prefix_blocks ? "its" : "no");
+  if (ld_table < c.max_blocks)
+    return fail(h, VT_ERR_INVALID_ARG, "ld_table=%lld below max_blocks=%d", (long long)ld_table,
+                c.max_blocks);
+  if (out_held == held || out_held == seq_lens)
+    return fail(h, VT_ERR_INVALID_ARG, "held is not updated in place");
+  std::memset(&a, 0, sizeof a);
+  a.B = B;
+  a.shift = h->shift;
+  a.cols = c.max_blocks;
+  a.num_blocks = num_blocks;
+  a.table = table;
+  a.ld = ld_table;
+  a.held = held;
+  a.seq_lens = seq_lens;
+  a.prefix = prefix_blocks;
+  a.n_prefix = num_prefix_blocks;
+  a.out_held = out_held;
+  a.free_blocks = out_free_blocks;
+  a.out_cursor = out_cursor;
+  a.used = h->d_used;
+  a.ranks = h->d_ranks;
+  a.totals = h->d_totals;
+  a.err_word = h->d_err;
+  return VT_OK;
+}
+
+int reclaim(vt_paged* h, const vt::ReclaimArgs& a, void* stream) {
+  Device guard(h->cfg.device);
+  if (!guard.ok) return fail(h, VT_ERR_CUDA, "cannot select device %d", h->cfg.device);
+  cudaStream_t st = (cudaStream_t)stream;
+  VT_TRY(h, vt::launch_reclaim(a, h->num_sms, st));
+  h->last_stream = st;
+  h->launched = true;
+  h->err[0] = 0;
+  return VT_OK;
+}
+
+}  // namespace
+
+int vt_paged_release(vt_paged* h, int32_t B, int32_t* table, int64_t ld_table, const int32_t* held,
+                     const int32_t* seq_lens, const int32_t* prefix_blocks,
+                     int32_t num_prefix_blocks, int32_t num_blocks, int32_t* out_held,
+                     int32_t* out_free_blocks, int32_t* out_cursor, void* stream) {
+  if (!h) return VT_ERR_INVALID_ARG;
+  vt::ReclaimArgs a;
+  const int rc = reclaim_args(h, a, B, table, ld_table, held, seq_lens, prefix_blocks,
+                              num_prefix_blocks, num_blocks, out_held, out_free_blocks, out_cursor);
+  return rc != VT_OK ? rc : reclaim(h, a, stream);
+}
+
+int vt_paged_compact(vt_paged* h, int32_t B, const int32_t* table, int64_t ld_table,
+                     const int32_t* held, const int32_t* seq_lens, const int32_t* prefix_blocks,
+                     int32_t num_prefix_blocks, int32_t num_blocks, int32_t* out_table,
+                     int64_t ld_out_table, int32_t* out_held, int32_t* out_free_blocks,
+                     int32_t* out_cursor, int32_t* out_prefix_blocks, int32_t* out_src,
+                     int32_t* out_dst, int32_t* out_count, void* stream) {
+  if (!h) return VT_ERR_INVALID_ARG;
+  vt::ReclaimArgs a;
+  const int rc = reclaim_args(h, a, B, const_cast<int32_t*>(table), ld_table, held, seq_lens,
+                              prefix_blocks, num_prefix_blocks, num_blocks, out_held,
+                              out_free_blocks, out_cursor);
+  if (rc != VT_OK) return rc;
+  if (!out_table || !out_count || (num_prefix_blocks > 0 && !out_prefix_blocks) ||
+      (num_blocks > 1 && (!out_src || !out_dst)))
+    return fail(h, VT_ERR_INVALID_ARG, "a null array");
+  if (ld_out_table < h->cfg.max_blocks || (out_table == table && ld_out_table != ld_table))
+    return fail(h, VT_ERR_INVALID_ARG, "ld_out_table=%lld", (long long)ld_out_table);
+  if (num_prefix_blocks > 0 && out_prefix_blocks == prefix_blocks)
+    return fail(h, VT_ERR_INVALID_ARG, "prefix_blocks is not updated in place");
+  a.compact = 1;
+  a.out_table = out_table;
+  a.ld_out = ld_out_table;
+  a.out_prefix = out_prefix_blocks;
+  a.src = out_src;
+  a.dst = out_dst;
+  a.count = out_count;
+  return reclaim(h, a, stream);
+}
+
+int vt_paged_copy_blocks(vt_paged* h, void* const* caches, int32_t num_caches, int32_t num_blocks,
+                         int64_t block_stride, int64_t block_bytes, const int32_t* src,
+                         const int32_t* dst, int32_t n, const int32_t* count, void* stream) {
+  if (!h) return VT_ERR_INVALID_ARG;
+  if (num_caches < 0 || n < 0)
+    return fail(h, VT_ERR_INVALID_ARG, "num_caches=%d, n=%d: need at least 0", num_caches, n);
+  if (num_blocks < 1 || block_bytes < 1 || block_stride < block_bytes)
+    return fail(h, VT_ERR_INVALID_ARG, "num_blocks=%d, block_stride=%lld, block_bytes=%lld",
+                num_blocks, (long long)block_stride, (long long)block_bytes);
+  if ((num_caches > 0 && !caches) || (n > 0 && (!src || !dst)))
+    return fail(h, VT_ERR_INVALID_ARG, "a null array");
+  bool wide = (block_stride | block_bytes) % 16 == 0;
+  for (int i = 0; i < num_caches; ++i) {
+    if (!caches[i]) return fail(h, VT_ERR_INVALID_ARG, "cache %d is null", i);
+    wide = wide && aligned(caches[i], 16);
+  }
+  h->err[0] = 0;
+  if (n == 0 || num_caches == 0) return VT_OK;
+  Device guard(h->cfg.device);
+  if (!guard.ok) return fail(h, VT_ERR_CUDA, "cannot select device %d", h->cfg.device);
+  cudaStream_t st = (cudaStream_t)stream;
+  vt::CopyArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.num_blocks = num_blocks;
+  a.block_stride = block_stride;
+  a.block_bytes = block_bytes;
+  a.src = src;
+  a.dst = dst;
+  a.n = n;
+  a.count = count;
+  a.err_word = h->d_err;
+  for (int i = 0; i < num_caches; i += vt::kCopyCaches) {
+    a.n_caches = std::min(num_caches - i, vt::kCopyCaches);
+    for (int k = 0; k < a.n_caches; ++k) a.caches[k] = caches[i + k];
+    VT_TRY(h, vt::launch_copy(a, wide, h->num_sms, st));
+  }
+  h->last_stream = st;
+  h->launched = true;
+  return VT_OK;
 }

@@ -8,6 +8,7 @@
 namespace vt {
 
 constexpr int kErrBadBlock = 4;  // error word: a block id outside the cache was met
+constexpr int kErrBadRows = 8;   // a request's starts are not 0 <= first <= end <= T
 
 // ---- block tables and slot maps (vt_tables.cu) -------------------------------
 struct TablesArgs {
@@ -35,6 +36,73 @@ struct TablesArgs {
   int32_t share;               // filled by launch_tables
 };
 cudaError_t launch_tables(TablesArgs a, int num_sms, cudaStream_t stream);
+
+// ---- forks, released and compacted blocks, block copies (vt_blocks.cu) --------
+struct ForkArgs {
+  int32_t R, B;                // rows of the new and of the old table
+  int32_t shift, cols;
+  const int32_t* parents;      // [R]
+  const int32_t* table;        // [B][ld]
+  int64_t ld;
+  const int32_t* held;         // [B]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* free_blocks;  // [n_free]
+  int32_t n_free;
+  const int32_t* cursor;       // [1]
+  int32_t* out_table;          // [R][ld_out]
+  int64_t ld_out;
+  int32_t* out_held;           // [R]
+  int32_t* out_seq;            // [R]
+  int32_t* out_cursor;         // [1]
+  int32_t* src;                // [R]
+  int32_t* dst;                // [R]
+  int32_t* status;             // [R]
+};
+cudaError_t launch_fork(const ForkArgs& a, int num_sms, cudaStream_t stream);
+
+struct ReclaimArgs {
+  int32_t B, shift, cols, num_blocks;
+  int32_t compact;             // else release
+  int32_t* table;              // [B][ld]
+  int64_t ld;
+  const int32_t* held;         // [B]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* prefix;       // [n_prefix]
+  int32_t n_prefix;
+  int32_t* out_held;           // [B]
+  int32_t* free_blocks;        // [num_blocks]
+  int32_t* out_cursor;         // [1]
+  // compact alone
+  int32_t* out_table;          // [B][ld_out]; may be the table
+  int64_t ld_out;
+  int32_t* out_prefix;         // [n_prefix]
+  int32_t* src;                // [num_blocks / 2]
+  int32_t* dst;
+  int32_t* count;              // [1]
+  // scratch: a bit to a block; the used ids before each word; their number and how
+  // many of them are below it
+  uint32_t* used;
+  int32_t* ranks;
+  int32_t* totals;
+  int32_t* err_word;
+  int32_t share;               // words to a CTA; filled by launch_reclaim
+};
+cudaError_t launch_reclaim(ReclaimArgs a, int num_sms, cudaStream_t stream);
+
+constexpr int kCopyCaches = 64;  // caches of a launch
+struct CopyArgs {
+  void* caches[kCopyCaches];
+  int32_t n_caches, num_blocks;
+  int64_t block_stride, block_bytes;
+  const int32_t* src;          // [n]
+  const int32_t* dst;
+  int32_t n;
+  const int32_t* count;        // [1] or null
+  int32_t* err_word;
+};
+// wide: pointers, stride and size are multiples of 16 bytes
+cudaError_t launch_copy(const CopyArgs& a, bool wide, int num_sms, cudaStream_t stream);
+cudaError_t prepare_blocks();
 
 // ---- attention behind a shared prefix (vt_prefix.cu) -------------------------
 struct AttnArgs {
@@ -72,6 +140,30 @@ struct AttnArgs {
 // dtype as VT_DTYPE_BF16 / VT_DTYPE_F16; head_dim 64 or 128.
 cudaError_t launch_prefix_attention(const AttnArgs& a, int dtype, int head_dim,
                                     cudaStream_t stream);
+// ---- attention of chunks (vt_chunk.cu) -------------------------------------------
+struct ChunkArgs {
+  const void* q;               // [T] rows of q_row elements, heads q_head apart
+  int64_t q_row, q_head;
+  const void* k;               // cache: block, token and head strides in elements
+  const void* v;
+  int64_t block_stride, token_stride, head_stride;
+  int32_t num_blocks;
+  int32_t shift;               // log2 of the block size
+  const int32_t* table;        // [B][ld_table]
+  int64_t ld_table;
+  int32_t cols;                // table columns a row may use
+  const int32_t* starts;       // [B + 1]
+  const int32_t* seq_lens;     // [B]
+  int32_t B, T, hq, hkv, G;    // G = hq / hkv
+  float scale_log2;            // scale * log2(e)
+  void* out;                   // [T][hq][d]
+  float* lse;                  // [T][hq] or null
+  int32_t num_sms;
+  int32_t* err_word;
+  int64_t wait_cycles;         // limit of the waits; 0: they have run out
+};
+cudaError_t launch_chunk(const ChunkArgs& a, int dtype, int head_dim, cudaStream_t stream);
+
 // Kernel attributes, once for the current device.
 cudaError_t prepare_tables();
 cudaError_t prepare_prefix_attention();

@@ -261,7 +261,8 @@ int vt_sampler_create(const vt_sampler_config* cfg, vt_sampler** out) {
   // the largest row must fit the shared-memory plan (16 CTAs per row at most)
   const vt::LaunchPlan worst = vt::plan_layout(cfg->max_vocab, 4, 16, true, true);
   if (worst.smem > (size_t)prop.sharedMemPerBlockOptin) return bail(VT_ERR_CAPACITY);
-  if (vt::prepare_given() != cudaSuccess) return bail(VT_ERR_CUDA);
+  if (vt::prepare_given() != cudaSuccess || vt::prepare_verify() != cudaSuccess)
+    return bail(VT_ERR_CUDA);
   h->num_sms = prop.multiProcessorCount;
 
   const size_t B = (size_t)cfg->max_batch;
@@ -1131,6 +1132,63 @@ int vt_sample_given(vt_sampler* h, const void* logits, int32_t dtype, int32_t B,
   a.group_max = h->d_given_gmax;
   cudaStream_t st = (cudaStream_t)stream;
   VT_CK(h, vt::launch_given(a, dtype, h->num_sms, st));
+  h->last_B = B;
+  h->last_stream = st;
+  h->err.clear();
+  return VT_OK;
+}
+
+int vt_verify(vt_sampler* h, const void* target_probs, int32_t dtype, int32_t B, int32_t K,
+              int32_t V, int64_t target_batch, int64_t target_row, const int32_t* starts,
+              int64_t num_rows, const void* draft_probs, int64_t draft_batch, int64_t draft_row,
+              const int32_t* draft_tokens, const int32_t* draft_lens, const float* uniforms,
+              int32_t* out_tokens, int32_t* out_accepted, void* stream) {
+  if (!h) return VT_ERR_INVALID_ARG;
+  if (B < 1) return set_err(h, VT_ERR_INVALID_ARG, "B=%d: need B >= 1", B);
+  if (B > h->cfg.max_batch)
+    return set_err(h, VT_ERR_CAPACITY, "B=%d above max_batch=%d", B, h->cfg.max_batch);
+  if (K < 0 || K > VT_VERIFY_MAX_DRAFTS)
+    return set_err(h, VT_ERR_INVALID_ARG, "K=%d outside [0, %d]", K, VT_VERIFY_MAX_DRAFTS);
+  if (V < 1) return set_err(h, VT_ERR_INVALID_ARG, "V=%d: need V >= 1", V);
+  if (V > h->cfg.max_vocab)
+    return set_err(h, VT_ERR_CAPACITY, "V=%d above max_vocab=%d", V, h->cfg.max_vocab);
+  if (dtype != VT_DTYPE_F32 && dtype != VT_DTYPE_BF16)
+    return set_err(h, VT_ERR_INVALID_ARG, "dtype %d: need fp32 or bf16", dtype);
+  if (!target_probs || !uniforms || !out_tokens || !out_accepted || (K > 0 && !draft_tokens))
+    return set_err(h, VT_ERR_INVALID_ARG, "a null array");
+  if (target_batch < 0 || target_row < 0 || draft_batch < 0 || draft_row < 0)
+    return set_err(h, VT_ERR_INVALID_ARG, "a negative stride");
+  if (starts && num_rows < 1)
+    return set_err(h, VT_ERR_INVALID_ARG, "num_rows=%lld with starts", (long long)num_rows);
+  DeviceGuard guard(h->cfg.device);
+  if (!guard.ok) return set_err(h, VT_ERR_CUDA, "cannot select device %d", h->cfg.device);
+  vt::VerifyArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.target = target_probs;
+  a.t_batch = target_batch;
+  a.t_row = target_row;
+  a.starts = starts;
+  a.rows = num_rows;
+  a.draft = K > 0 ? draft_probs : nullptr;
+  a.d_batch = draft_batch;
+  a.d_row = draft_row;
+  a.tokens = draft_tokens;
+  a.lens = draft_lens;
+  a.uniforms = uniforms;
+  a.B = B;
+  a.K = K;
+  a.V = V;
+  const int64_t e = dtype == VT_DTYPE_F32 ? 4 : 2;
+  auto vec = [&](const void* p, int64_t batch, int64_t row) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && batch * e % 16 == 0 && row * e % 16 == 0;
+  };
+  a.vec = vec(target_probs, starts ? 0 : target_batch, target_row) &&
+          (!a.draft || vec(draft_probs, draft_batch, draft_row));
+  a.out_tokens = out_tokens;
+  a.out_accepted = out_accepted;
+  a.row_status = h->d_status;
+  cudaStream_t st = (cudaStream_t)stream;
+  VT_CK(h, vt::launch_verify(a, dtype, h->num_sms, st));
   h->last_B = B;
   h->last_stream = st;
   h->err.clear();

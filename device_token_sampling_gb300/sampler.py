@@ -17,7 +17,7 @@ from . import _build
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
-DTYPE_F16 = 2  # PagedBatch.attention only
+DTYPE_F16 = 2  # PagedBatch's attention only
 
 VT_OK = 0
 VT_ERR_INVALID_ARG = -1
@@ -73,6 +73,8 @@ SIGNATURES = {
     "vt_sample": (C.c_int, [P, P, I32, I32, I32, I64, I32, I32, P, P, P, P, P]),
     "vt_sample_ex": (C.c_int, [P, P, I32, I32, I32, I64, I32, I32, P, P, P, P, P, I64, P]),
     "vt_sample_given": (C.c_int, [P, P, I32, I32, I32, I64, P, I32, P, P, P]),
+    "vt_verify": (C.c_int, [P, P, I32, I32, I32, I32, I64, I64, P, I64, P, I64, I64, P, P, P, P, P,
+                            P]),
     "vt_sample_host": (C.c_int, [P, P, I32, I32, I32, I64, I32, I32, P, P, P, P, P]),
     "vt_check_device_errors": (C.c_int, [P]),
     "vt_get_row_status": (C.c_int, [P, P, P]),
@@ -103,6 +105,14 @@ SIGNATURES = {
                                      P, P, I32, I32, C.c_float, P, P, P]),
     "vt_paged_attention_ex": (C.c_int, [P, I32, I32, P, I64, I64, P, P, I32, I64, I64, I64, P, I64,
                                         I32, P, P, I32, I32, C.c_float, P, P, P]),
+    "vt_paged_chunk_attention": (C.c_int, [P, I32, I32, I32, P, I64, I64, P, P, P, I32, I64, I64,
+                                           I64, P, I64, I32, P, C.c_float, P, P, P]),
+    "vt_paged_fork": (C.c_int, [P, I32, P, I32, P, I64, P, P, P, I32, P, P, I64, P, P, P, P, P, P,
+                                P]),
+    "vt_paged_release": (C.c_int, [P, I32, P, I64, P, P, P, I32, I32, P, P, P, P]),
+    "vt_paged_compact": (C.c_int, [P, I32, P, I64, P, P, P, I32, I32, P, I64, P, P, P, P, P, P, P,
+                                   P]),
+    "vt_paged_copy_blocks": (C.c_int, [P, P, I32, I32, I64, I64, P, P, I32, P, P]),
     "vt_last_error": (C.c_char_p, [P]),
     "vt_status_string": (C.c_char_p, [C.c_int]),
 }
@@ -392,6 +402,82 @@ class Sampler:
             self._check(rc, "vt_sample_given")
         if other is not None:
             lend(other, (logits, uniforms, tok, lp))
+        return out
+
+    def verify(self, target_probs, draft_tokens, uniforms, draft_probs=None, draft_lens=None,
+               starts=None, out=None, stream=None):
+        """vt_verify: accept or refuse drafted tokens, and draw the token behind them.
+
+        ``target_probs`` [B, K + 1, V], or with ``starts`` (int32 [B + 1]) [rows, V], float32 or
+        bfloat16 with contiguous rows; ``draft_tokens`` int32 [B, K]; ``uniforms`` float32
+        [B, K + 1], the last column for the token behind the accepted drafts.  ``draft_probs``
+        [B, K, V] of the target's type (None: the drafts were looked up, not drawn);
+        ``draft_lens`` int32 [B] (None: K each).  Returns ``(tokens, accepted)``: int32
+        [B, K + 1] (the accepted drafts, the next token, then -1) and [B].  Stream-ordered;
+        nothing waits: on a ``stream`` that is not the current one the inputs have to be ready
+        there, and the outputs are."""
+        import torch
+        dev = self.device
+        i32 = torch.int32
+        t = target_probs.dtype
+        dtype = DTYPE_F32 if t is torch.float32 else DTYPE_BF16 if t is torch.bfloat16 else None
+        if dtype is None:
+            raise ValueError(f"unsupported target_probs dtype {t}")
+        if draft_tokens.dim() != 2:
+            raise ValueError("draft_tokens must be [B, K]")
+        B, K = draft_tokens.shape
+        V = target_probs.shape[-1]
+        if starts is None:
+            if target_probs.shape != (B, K + 1, V):
+                raise ValueError(f"target_probs must be [{B}, {K + 1}, V], "
+                                 f"not {tuple(target_probs.shape)}")
+        elif target_probs.dim() != 2:
+            raise ValueError("with starts, target_probs must be [rows, V]")
+        rows = target_probs.shape[0]
+        for x, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
+            if x is not None and (x.get_device() != dev or x.dtype is not t
+                                  or (V > 1 and x.stride(-1) != 1)):
+                raise ValueError(f"{name} must be {t} on cuda:{dev} with contiguous rows")
+        if draft_probs is not None and draft_probs.shape != (B, K, V):
+            raise ValueError(f"draft_probs must be {(B, K, V)}, not {tuple(draft_probs.shape)}")
+        checks = [(draft_tokens, "draft_tokens", i32, (B, K)),
+                  (uniforms, "uniforms", torch.float32, (B, K + 1)),
+                  (draft_lens, "draft_lens", i32, (B,)), (starts, "starts", i32, (B + 1,))]
+        other = other_stream(stream)
+        if out is None:
+            place = target_probs.device
+            out = tok, acc = make_on(other, lambda: (
+                torch.empty((B, K + 1), dtype=i32, device=place),
+                torch.empty((B,), dtype=i32, device=place)))
+        else:
+            tok, acc = out
+            checks += [(tok, "tokens", i32, (B, K + 1)), (acc, "accepted", i32, (B,))]
+        for x, name, dt, shape in checks:
+            if x is not None and (x.dtype is not dt or x.shape != shape or x.get_device() != dev
+                                  or not x.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {dt} tensor {shape} on cuda:{dev}")
+        # (the stride of a dimension of one element may be anything)
+        if starts is None:
+            t_batch = target_probs.stride(0) if B > 1 else 0
+            t_row = target_probs.stride(1) if K > 0 else 0
+        else:
+            t_batch, t_row = 0, target_probs.stride(0) if rows > 1 else 0
+        if draft_probs is None or K == 0:
+            p_draft, d_batch, d_row = None, 0, 0
+        else:
+            p_draft = draft_probs.data_ptr()
+            d_batch = draft_probs.stride(0) if B > 1 else 0
+            d_row = draft_probs.stride(1) if K > 1 else 0
+        rc = self._lib.vt_verify(
+            self._h, target_probs.data_ptr(), dtype, B, K, V, t_batch, t_row,
+            None if starts is None else starts.data_ptr(), rows, p_draft, d_batch, d_row,
+            draft_tokens.data_ptr(), None if draft_lens is None else draft_lens.data_ptr(),
+            uniforms.data_ptr(), tok.data_ptr(), acc.data_ptr(), raw_stream(stream, dev))
+        if rc != VT_OK:
+            self._check(rc, "vt_verify")
+        if other is not None:
+            lend(other, (target_probs, draft_tokens, uniforms, draft_probs, draft_lens, starts,
+                         tok, acc))
         return out
 
     def sample_ptr(self, logits_ptr: int, dtype: int, B: int, V: int, ld: int, num_logprobs: int,

@@ -65,7 +65,7 @@ extern "C" {
 /* ---- logits element types ----------------------------------------------- */
 #define VT_DTYPE_F32 0  /* IEEE binary32                                        */
 #define VT_DTYPE_BF16 1 /* bfloat16 (the top 16 bits of a binary32), widened exactly */
-#define VT_DTYPE_F16 2  /* IEEE binary16 (vt_paged_attention only)              */
+#define VT_DTYPE_F16 2  /* IEEE binary16 (attention over the paged cache only)   */
 
 /* ---- per-row status written by vt_sample (see vt_get_row_status) ------- */
 #define VT_ROW_OK 0           /* token drawn                                    */
@@ -260,6 +260,45 @@ int vt_sample_ex(vt_sampler* handle, const void* logits, int32_t dtype, int32_t 
 int vt_sample_given(vt_sampler* handle, const void* logits, int32_t dtype, int32_t B, int32_t V,
                     int64_t ld, const float* uniforms, int32_t draws, int32_t* out_tokens,
                     float* out_logprobs, void* stream);
+
+/* Verify drafted tokens against the target's probabilities with given uniform
+ * numbers (speculative sampling: the tokens have the target's distribution).
+ * Request b has n drafts x_0 .. x_{n-1}, the target's rows p_0 .. p_n (p_i: of the
+ * token in x_i's place) and the drafter's rows q_0 .. q_{n-1}.  Draft i is accepted
+ * when u_i * q_i(x_i) < p_i(x_i); the first that is not, at a, ends the drafts.  The
+ * next token is drawn from r_j = max(p_a(j) - q_a(j), 0), from p_n (a = n) when all
+ * were accepted, and from p_a as it is when r is 0 everywhere:
+ *   token = the first j with r_0 + .. + r_j > u * (r_0 + .. + r_{V-1}).
+ * Both decisions are exact on the values given (entries below 2^-31 count to 2^-54).
+ *   target_probs   device, of `dtype` (VT_DTYPE_F32 or _BF16), rows of V: row i of
+ *                  request b at b * target_batch + i * target_row; with starts at
+ *                  (starts[b] + i) * target_row.
+ *   starts         device int32[B + 1] (vt_paged_tables' out_starts for query lengths
+ *                  n + 1) or NULL; requests with fewer rows than drafts + 1 have that
+ *                  many drafts less.  num_rows: the rows there are; a request whose
+ *                  rows are not in [0, num_rows) is read no row of.
+ *   draft_probs    like target_probs, of the same dtype, row i of request b at
+ *                  b * draft_batch + i * draft_row; or NULL: drafts that were looked
+ *                  up, with q_i 1 at x_i and 0 elsewhere.
+ *   draft_tokens   device int32[B][K]; a token outside [0, V) is not accepted.
+ *   draft_lens     device int32[B], the n of each request, or NULL: K.
+ *   uniforms       device float[B][K + 1] in [0, 1): u_i for draft i, the last one for
+ *                  the next token; below 0 and NaN count as 0.
+ *   out_tokens     device int32[B][K + 1]: the accepted drafts, the next token, -1s.
+ *   out_accepted   device int32[B]: a.
+ * Probabilities are in [0, 2) (negative ones count as 0) and a row's sum below 512.
+ * Row status (vt_get_row_status): VT_ROW_NONFINITE when the row that the token is
+ * drawn from breaks that, VT_ROW_EMPTY when it is 0 everywhere or the request has no
+ * rows; then no token follows the accepted drafts (-1).  Needs no vt_reset_params;
+ * seeds, counts and the debug views are not touched.  One launch; enqueues only; may
+ * be captured.  Errors: VT_ERR_INVALID_ARG, VT_ERR_CAPACITY (B > max_batch, V >
+ * max_vocab), VT_ERR_CUDA. */
+#define VT_VERIFY_MAX_DRAFTS 4096
+int vt_verify(vt_sampler* handle, const void* target_probs, int32_t dtype, int32_t B, int32_t K,
+              int32_t V, int64_t target_batch, int64_t target_row, const int32_t* starts,
+              int64_t num_rows, const void* draft_probs, int64_t draft_batch, int64_t draft_row,
+              const int32_t* draft_tokens, const int32_t* draft_lens, const float* uniforms,
+              int32_t* out_tokens, int32_t* out_accepted, void* stream);
 
 /* vt_sample from host memory: vt_sample_host_async, then vt_sample_host_wait
  * (the outputs are in the host arrays when it returns).  Errors as vt_sample,
@@ -504,6 +543,8 @@ int vt_shard_merge(vt_sampler* handle, const void* parts, int32_t S, int32_t B, 
 typedef struct vt_paged vt_paged; /* opaque handle */
 
 #define VT_PAGED_MAX_BATCH 16384
+#define VT_PAGED_MAX_TOKENS (1 << 24)       /* query tokens of a chunk call       */
+#define VT_PAGED_MAX_CACHE_BLOCKS (1 << 24) /* blocks of a cache: release, compact */
 
 typedef struct vt_paged_config {
   int32_t max_batch;  /* largest B of any call, 1..VT_PAGED_MAX_BATCH            */
@@ -618,6 +659,108 @@ int vt_paged_attention_ex(vt_paged* handle, int32_t dtype, int32_t B, const void
                           int32_t table_cols, const int32_t* seq_lens,
                           const int32_t* prefix_blocks, int32_t prefix_len, int32_t max_seq_len,
                           float scale, void* out, float* out_lse, void* stream);
+
+/* Attention of several new query tokens a request (the chunk of a long prompt, the
+ * drafts of a verification step, or one token) over its paged cache, each up to its
+ * own position: request b's tokens are rows starts[b] .. starts[b + 1] - 1 of q, the
+ * last n_b = starts[b + 1] - starts[b] of its seq_lens[b] tokens, whose keys and values
+ * the cache already holds; row i of them attends to the positions j <= seq_lens[b] -
+ * n_b + i, none when that is negative (out 0, log-sum -inf).
+ *   T              rows of q, 0..VT_PAGED_MAX_TOKENS.
+ *   starts         device int32[B + 1], as vt_paged_tables writes it.  Rows of q behind
+ *                  starts[B] are not read and theirs of out and out_lse not written.  A
+ *                  request whose starts are decreasing or outside [0, T] is left out
+ *                  (vt_paged_check_errors reports it).
+ *   seq_lens       [B]; positions past the table's columns are not attended to.
+ *   out, out_lse   [T][q_heads][head_dim] of q's type, float [T][q_heads] (may be NULL).
+ * The other arguments, the accuracy and the treatment of bad block ids are
+ * vt_paged_attention_ex's.  Infinities and NaN at positions that a row does not attend to do not
+ * reach it.  Block sizes of 8 tokens and more run on the tensor cores; smaller ones,
+ * and caches with a stride of 0 or less, row by row.  Enqueues only; may be captured.
+ * Errors: VT_ERR_INVALID_ARG, VT_ERR_CAPACITY (B > max_batch), VT_ERR_STATE (a handle
+ * without heads), VT_ERR_CUDA. */
+int vt_paged_chunk_attention(vt_paged* handle, int32_t dtype, int32_t B, int32_t T, const void* q,
+                             int64_t q_row, int64_t q_head, const int32_t* starts,
+                             const void* k_cache, const void* v_cache, int32_t num_blocks,
+                             int64_t block_stride, int64_t token_stride, int64_t head_stride,
+                             const int32_t* table, int64_t ld_table, int32_t table_cols,
+                             const int32_t* seq_lens, float scale, void* out, float* out_lse,
+                             void* stream);
+
+/* Rows of the next step that continue rows of this one (several continuations of a
+ * request, the beams of a search).  Row r of the new table continues row p =
+ * parents[r]; -1: an empty row.  The lowest r of a parent keeps p's blocks, all
+ * held[p] of them.  Every other one shares those that seq_lens[p] tokens fill; a last
+ * one that they fill in part becomes a new block off the free list, and (out_src[r],
+ * out_dst[r]) the copy that vt_paged_copy_blocks then has to make (-1, -1: none).
+ * Blocks of rows that nobody continues are still off the free list until
+ * vt_paged_release.  All arrays are device memory.
+ *   R, parents     rows of the new table, [R].
+ *   B, table       the old one, [B][ld_table]; held, seq_lens [B].
+ *   free_blocks, num_free, cursor, out_cursor   as vt_paged_tables.
+ *   out_table      [R][ld_out_table], max_blocks columns of it written: -1 past a row's
+ *                  blocks.  Not the old table.
+ *   out_held, out_seq_lens   [R]: columns filled, and the parent's length.
+ *   out_status     [R]: 0; 1 when no block was left for its copy; 2 when parents[r] is
+ *                  outside [-1, B) or its parent's seq_lens and held are not 0 <=
+ *                  blocks <= held <= max_blocks.  A row with status 1 or 2 is empty.
+ * One launch; enqueues only; may be captured.  Errors: VT_ERR_INVALID_ARG,
+ * VT_ERR_CAPACITY (R or B > max_batch), VT_ERR_CUDA. */
+int vt_paged_fork(vt_paged* handle, int32_t R, const int32_t* parents, int32_t B,
+                  const int32_t* table, int64_t ld_table, const int32_t* held,
+                  const int32_t* seq_lens, const int32_t* free_blocks, int32_t num_free,
+                  const int32_t* cursor, int32_t* out_table, int64_t ld_out_table,
+                  int32_t* out_held, int32_t* out_seq_lens, int32_t* out_cursor, int32_t* out_src,
+                  int32_t* out_dst, int32_t* out_status, void* stream);
+
+/* Give back the blocks that no request needs: request r keeps the first
+ * min(held[r], ceil(seq_lens[r] / block_size)) of its blocks (0 for a request that
+ * ended; fewer than it held when drafts were refused).  The free list is made anew of
+ * every block in [0, num_blocks) that no request keeps and that is not one of
+ * prefix_blocks, so the table has to hold every request that lives.
+ *   table          [B][ld_table]: columns past the kept ones become -1.
+ *   out_held       [B] columns kept (not the array held).
+ *   out_free_blocks  [num_blocks]: the used ids, ascending, then the free ones,
+ *                  ascending; out_cursor [1]: where these begin.
+ * A block id outside [0, num_blocks) is left out (vt_paged_check_errors reports it).
+ * num_blocks <= VT_PAGED_MAX_CACHE_BLOCKS.  Enqueues only; may be captured.  Errors:
+ * VT_ERR_INVALID_ARG, VT_ERR_CAPACITY, VT_ERR_CUDA. */
+int vt_paged_release(vt_paged* handle, int32_t B, int32_t* table, int64_t ld_table,
+                     const int32_t* held, const int32_t* seq_lens, const int32_t* prefix_blocks,
+                     int32_t num_prefix_blocks, int32_t num_blocks, int32_t* out_held,
+                     int32_t* out_free_blocks, int32_t* out_cursor, void* stream);
+
+/* vt_paged_release, and the blocks in use renumbered to [0, n): of those that are not
+ * below n, the i-th in ascending order moves to the i-th free id below n.
+ *   out_table      [B][ld_out_table]: the rows with the new ids, -1 past the kept
+ *                  columns; may be the table.
+ *   out_free_blocks, out_cursor   0 .. num_blocks - 1, and n.
+ *   out_prefix_blocks  [num_prefix_blocks] their new ids (not the array prefix_blocks).
+ *   out_src, out_dst   [num_blocks / 2] the moves, then -1s; out_count [1] their number.
+ *                  vt_paged_copy_blocks makes them: no block is a source and a target.
+ * A block id outside [0, num_blocks) becomes -1 and is reported.  Errors as
+ * vt_paged_release. */
+int vt_paged_compact(vt_paged* handle, int32_t B, const int32_t* table, int64_t ld_table,
+                     const int32_t* held, const int32_t* seq_lens, const int32_t* prefix_blocks,
+                     int32_t num_prefix_blocks, int32_t num_blocks, int32_t* out_table,
+                     int64_t ld_out_table, int32_t* out_held, int32_t* out_free_blocks,
+                     int32_t* out_cursor, int32_t* out_prefix_blocks, int32_t* out_src,
+                     int32_t* out_dst, int32_t* out_count, void* stream);
+
+/* Copy block src[i] to block dst[i], i < n, in every one of `caches` (a host array of
+ * device pointers: the keys and values of all layers).  Block b of a cache is the
+ * block_bytes bytes from b * block_stride bytes on.
+ *   src, dst       device int32[n].  A pair with a negative id is skipped; one with an
+ *                  id of num_blocks and more too (vt_paged_check_errors reports it).
+ *                  The pairs are copied in no order: a block written by one of them must
+ *                  be in no other.
+ *   count          device int32[1]: only the first count[0] pairs; or NULL.
+ * One launch for every 64 caches; enqueues only; may be captured.  Errors:
+ * VT_ERR_INVALID_ARG, VT_ERR_CUDA. */
+int vt_paged_copy_blocks(vt_paged* handle, void* const* caches, int32_t num_caches,
+                         int32_t num_blocks, int64_t block_stride, int64_t block_bytes,
+                         const int32_t* src, const int32_t* dst, int32_t n, const int32_t* count,
+                         void* stream);
 
 /* Message for the last failing call on `handle` ("" if none); static storage
  * owned by the handle, valid until the next call on it. */

@@ -100,3 +100,20 @@ def attention_reference(q, k_cache, v_cache, table, seq, prefix_blocks, prefix_l
                                + tiny * peak[:, None] * v[:, h].abs().sum(0) + tiny)
             b_lse[b, heads] = err_s + 2.0 ** -23 * lse[b, heads].abs()
     return out, lse, b_out, b_lse
+
+
+def chunk_reference(q, starts, k_cache, v_cache, table, seq, block_size, scale):
+    """(out, lse, bound_out, bound_lse) in float64: ``attention_reference`` of each query token
+    as a request of its own that ends at its position."""
+    import torch
+    rows, lens = [], []
+    starts = [int(x) for x in starts]
+    for b in range(len(seq)):
+        n = starts[b + 1] - starts[b]
+        rows += [b] * n
+        cap = table.shape[1] * block_size
+        lens += [min(max(int(seq[b]) - n + i + 1, 0), cap) for i in range(n)]
+    T = starts[-1]
+    none = torch.zeros(0, dtype=torch.int32, device=q.device)
+    return attention_reference(q[:T], k_cache, v_cache, table[torch.tensor(rows, device=q.device)],
+                               lens, none, 0, block_size, scale)
