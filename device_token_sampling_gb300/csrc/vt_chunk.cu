@@ -137,6 +137,7 @@ cudaError_t launch_rows(const ChunkArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_chunk(const ChunkArgs& a, int dtype, int head_dim, cudaStream_t stream) {
+  if (chunk_mma_takes(a)) return launch_chunk_mma(a, dtype, head_dim, stream);
   if (dtype == VT_DTYPE_BF16)
     return head_dim == 128 ? launch_rows<__nv_bfloat16, 128>(a, stream)
                            : launch_rows<__nv_bfloat16, 64>(a, stream);

@@ -1,0 +1,999 @@
+// vt_chunk_mma.cu -- attention of chunks on the 5th-generation tensor cores.
+//
+// The n_b * G query rows (token, head) of a request and kv head are cut into units of up
+// to 256 rows, two tiles of 128; a unit attends to the tokens up to its last row's
+// position, 128 at a step.  Three launches:
+//   plan_kernel    counts the units' steps and gives every CTA its share;
+//   chunk_kernel   one CTA an SM, its pieces of units one after another;
+//   join_kernel    puts units together that more than one CTA worked on.
+#include <type_traits>
+
+#include "vt_paged.h"
+#include "vt_umma.cuh"
+
+namespace vt {
+namespace {
+
+constexpr int kUnitRows = 2 * kTileRows;
+constexpr int kChunkThreads = 512;
+constexpr int kPieces = 4;    // pieces that are known ahead
+constexpr int kMasks = 8;     // steps whose token masks are kept
+// warps: the softmax of each tile, the factors and outputs of both, then one each for
+// the tiles' MMAs, the copies of K and V, and the pieces with their rows of Q
+constexpr int kCorrWarp = 8, kMma0Warp = 12, kKvWarp = 14, kPieceWarp = 15;
+
+// ---- the units ----------------------------------------------------------------
+struct Request {
+  int s0, n;       // its rows of q
+  int64_t before;  // tokens in front of them
+  int pairs;       // units of a kv head
+};
+__device__ __forceinline__ Request request(const ChunkArgs& a, int b) {
+  Request r;
+  const int s0 = a.starts[b], s1 = a.starts[b + 1];
+  const bool fine = s0 >= 0 && s0 <= s1 && s1 <= a.T;
+  r.s0 = s0;
+  r.n = fine ? s1 - s0 : 0;
+  r.before = (int64_t)a.seq_lens[b] - r.n;
+  r.pairs = (int)(((int64_t)r.n * a.G + kUnitRows - 1) / kUnitRows);
+  return r;
+}
+// The end of the tokens that unit `pair` attends to, and its steps (one at least, so
+// that rows which attend to nothing are written).
+__device__ __forceinline__ int unit_end(const ChunkArgs& a, const Request& r, int pair) {
+  const int64_t last = min((int64_t)(pair + 1) * kUnitRows, (int64_t)r.n * a.G) - 1;
+  const int64_t end = r.before + last / a.G + 1;
+  return (int)min(max(end, (int64_t)0), (int64_t)a.cols << a.shift);
+}
+__device__ __forceinline__ int unit_steps(const ChunkArgs& a, const Request& r, int pair) {
+  return max(1, (unit_end(a, r, pair) + kTileTokens - 1) / kTileTokens);
+}
+// The order of a request's units: the longest first, its kv heads side by side.  (So
+// CTAs that run at the same time read the same keys and values from L2.)
+
+struct Sums2 {
+  int64_t x, y;
+};
+constexpr int kPlanThreads = 1024;
+
+// The last b with first[b] <= v.
+__device__ __forceinline__ int find_request(const int64_t* first, int stride, int B, int64_t v) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[(int64_t)mid * stride] <= v) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// One CTA: prefix sums of the requests' units and steps; then what each CTA of
+// chunk_kernel does.  Whole rounds of units where some request has several units a kv
+// head (which share keys and values) and there are two rounds at least; the units
+// behind the last but one whole round, or all of them, as one row of steps in equal
+// shares.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
+  __shared__ Sums2 s_warp[33];
+  __shared__ int s_several;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (tid == 0) s_several = 0;
+  int64_t units = 0, steps = 0;
+  for (int base = 0; base < a.B; base += kPlanThreads) {
+    const int b = base + tid;
+    int64_t x = 0, y = 0;
+    if (b < a.B) {
+      const Request r = request(a, b);
+      const int s0 = a.starts[b], s1 = a.starts[b + 1];
+      if (s0 < 0 || s0 > s1 || s1 > a.T) atomicOr(a.err_word, kErrBadRows);
+      x = (int64_t)r.pairs * a.hkv;
+      for (int p = 0; p < r.pairs; ++p) y += unit_steps(a, r, p);
+      y *= a.hkv;
+      if (r.pairs > 1) s_several = 1;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t px = __shfl_up_sync(0xffffffffu, x, o), py = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) {
+        x += px;
+        y += py;
+      }
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp + 1] = Sums2{x, y};
+    __syncthreads();
+    if (warp == 0) {
+      int64_t vx = s_warp[lane + 1].x, vy = s_warp[lane + 1].y;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t px = __shfl_up_sync(0xffffffffu, vx, o),
+                      py = __shfl_up_sync(0xffffffffu, vy, o);
+        if (lane >= o) {
+          vx += px;
+          vy += py;
+        }
+      }
+      s_warp[lane + 1] = Sums2{vx, vy};
+      if (lane == 0) s_warp[0] = Sums2{0, 0};
+    }
+    __syncthreads();
+    x += s_warp[warp].x;
+    y += s_warp[warp].y;
+    if (b < a.B) {
+      a.plan_first[2 * (b + 1)] = units + x;
+      a.plan_first[2 * (b + 1) + 1] = steps + y;
+    }
+    units += s_warp[32].x;
+    steps += s_warp[32].y;
+  }
+  if (tid == 0) a.plan_first[0] = a.plan_first[1] = 0;
+  __syncthreads();
+  const int64_t* first = a.plan_first;
+  const int G = a.grid;
+  const int rounds = s_several && units >= 2 * G ? (int)(units / G - 1) : 0;
+  // the steps in front of the first unit that is shared out by steps
+  int64_t skipped = 0;
+  if (rounds > 0) {
+    const int64_t u = (int64_t)rounds * G;
+    const int b = find_request(first, 2, a.B, u);
+    const Request r = request(a, b);
+    int64_t left = u - first[2 * b];
+    skipped = first[2 * b + 1];
+    for (int p = r.pairs - 1; left > 0; --p) {
+      const int64_t k = min(left, (int64_t)a.hkv);
+      skipped += k * unit_steps(a, r, p);
+      left -= k;
+    }
+  }
+  const int64_t todo = steps - skipped;
+  // (no CTA with less than kMinSteps, if that leaves some without)
+  const int64_t shares = max((int64_t)1, min((int64_t)G, todo / a.min_steps));
+  for (int c = tid; c <= G; c += kPlanThreads) {
+    const int64_t at = skipped + (c >= shares ? todo : todo * c / shares);
+    ChunkStart s{};
+    s.at = at;
+    s.b = a.B;
+    if (at < steps) {
+      const int b = find_request(first + 1, 2, a.B, at);
+      const Request r = request(a, b);
+      int64_t left = at - first[2 * b + 1];
+      int p = r.pairs - 1, n = 1;
+      for (; p > 0; --p) {
+        n = unit_steps(a, r, p);
+        if (left < (int64_t)n * a.hkv) break;
+        left -= (int64_t)n * a.hkv;
+      }
+      if (p <= 0) n = unit_steps(a, r, 0);
+      s.b = b;
+      s.pair = p;
+      s.kvh = (int)(left / n);
+      s.step = (int)(left % n);
+    }
+    s.rounds = rounds;
+    a.plan_start[c] = s;
+  }
+}
+
+// ---- what the roles of a CTA share ------------------------------------------------
+template <int D>
+struct ChunkSmem {
+  static constexpr int kHalf = kTileRows * 128;      // 128 rows of 64 elements
+  static constexpr int kTile = (D / 64) * kHalf;     // bytes of a Q, K or V tile
+  static constexpr int kRing = D == 128 ? 5 : 8;     // K and V tiles
+  static constexpr int kQ = 0;
+  static constexpr int kKv = 2 * kTile;
+  static constexpr int kRest = kKv + kRing * kTile;
+};
+
+struct Piece {
+  int b, kvh;
+  int token, g0;  // row 0 of the unit: its row of q, and its head of the G
+  int rows;       // of the unit; 0: no more pieces
+  int t0, t1;     // steps
+  int end;        // of the unit's tokens
+  int lim0;       // end of the tokens that row 0 attends to
+  int slot;       // of its partial result, or -1: the whole unit
+};
+
+template <int R>
+struct Shared {
+  uint64_t full[R], empty[R];        // of the ring
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
+  // of each tile: scores made; factors posted; weights stored and the accumulator
+  // rescaled; product done; poisoned values added; sums posted; accumulator read
+  uint64_t s_full[2], f_full[2], p_full[2], pv_done[2], fixed[2], l_full[2], o_empty[2];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t v_ok;                     // V of a step at the chunk's diagonal looked through
+  uint64_t drained[2];
+  float factor[2][kTileRows];
+  float inv[2][kTileRows];
+  Piece piece[kPieces];
+  uint32_t mask[kMasks][4];
+  int32_t whole[kMasks];
+  uint32_t poison[2][4];             // tokens of V that are not finite, by turns
+  uint32_t tmem;
+};
+
+// A place in the ring and the parity of its use.
+template <int R>
+struct RingAt {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == R) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+  __device__ __forceinline__ void skip(int n) {
+    n += st;
+    ph ^= (uint32_t)(n / R) & 1;
+    st = n % R;
+  }
+};
+
+__device__ __forceinline__ uint64_t pack_f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t addr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  return r;
+}
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// Whether one of 8 elements is an infinity or a NaN: all exponent bits set.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(const uint4& v) {
+  constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+  constexpr uint32_t kExp = kBf ? 0x7f807f80u : 0x7c007c00u, kOne = kBf ? 0x00800080u : 0x04000400u;
+  return (((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) |
+          ((v.w & kExp) + kOne)) & 0x80008000u;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    chunk_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v) {
+  using L = ChunkSmem<D>;
+  constexpr int R = L::kRing;
+  using Sh = Shared<R>;
+  extern __shared__ __align__(1024) unsigned char dyn[];
+  const uint32_t base = smem_addr(dyn);
+  Sh& sh = *reinterpret_cast<Sh*>(dyn + L::kRest);
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (base & 1023) {  // (the swizzle's atoms; no static shared memory lies in front)
+    if (tid == 0) atomicOr(a.err_word, kErrInternal);
+    return;
+  }
+  // (through a shuffle, so that the roles' control flow and addresses are known to
+  // be the same in a warp: MMA operands live in uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (tid == 0) {
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 2);  // (both tiles' MMAs)
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&sh.piece_full[i], 1);
+      mbar_init(&sh.piece_empty[i], kPieceWarp);  // (every other warp)
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.s_full[t], 1);
+      mbar_init(&sh.f_full[t], 4);
+      mbar_init(&sh.p_full[t], 8);  // (the softmax and the factors' warps)
+      mbar_init(&sh.pv_done[t], 1);
+      mbar_init(&sh.fixed[t], 4);
+      mbar_init(&sh.l_full[t], 4);
+      mbar_init(&sh.o_empty[t], 4);
+      mbar_init(&sh.q_full[t], 1);
+      mbar_init(&sh.q_empty[t], 1);
+      mbar_init(&sh.drained[t], 1);
+    }
+    mbar_init(&sh.v_ok, 4);
+    fence_mbar_init();
+  }
+  if (warp == kMma0Warp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_addr(&sh.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
+  const long long limit = a.wait_cycles;
+  bool ok = true;
+  // tensor memory columns: S of each tile (P over its first half), then O of each
+  constexpr uint32_t kO = 2 * kTileTokens;
+
+  // The next piece into `p`; false behind the last, or when the wait ran out.
+  int n_piece = 0;
+  auto next_piece = [&](Piece& p) {
+    const int at = n_piece % kPieces;
+    ok = warp_wait(&sh.piece_full[at], (n_piece / kPieces) & 1, limit);
+    if (!ok) return false;
+    p = sh.piece[at];
+    warp_arrive(&sh.piece_empty[at]);
+    ++n_piece;
+    return p.rows > 0;
+  };
+
+  if (warp < kCorrWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    // ---- softmax: a warpgroup to a tile, one thread to a row ---------------------------
+    const int t = warp >> 2, in = tid & (kTileRows - 1);
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane (warp % 4) * 32
+    const uint32_t ts = tmem + lanes + t * kTileTokens;
+    // (a scale of 0 as one that leaves masked scores at -inf)
+    const float sc = fmaxf(fabsf(a.scale_log2), 1e-30f);
+    const uint64_t sc2 = pack_f2(sc, sc);
+    uint32_t steps = 0, pieces = 0;  // of this tile
+    int n_masks = 0;
+    Piece p;
+    while (ok && next_piece(p)) {
+      const int n_steps = p.t1 - p.t0;
+      if (t * kTileRows >= p.rows) {
+        n_masks += n_steps;
+        continue;
+      }
+      const int r = t * kTileRows + in, x = p.g0 + r;
+      const bool live = r < p.rows;
+      const bool warp_live = t * kTileRows + (warp & 3) * 32 < p.rows;
+      const int lim = live ? min(max(p.lim0 + x / a.G, 0), a.cols << a.shift) : 0;
+      const int lim_min = __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff);
+      float m = -INFINITY, l = 0.f;
+      for (int j = p.t0; j < p.t1; ++j, ++steps, ++n_masks) {
+        ok = warp_wait(&sh.s_full[t], steps & 1, limit);
+        if (!ok) break;
+        fence_after();
+        if (!warp_live) {  // (the products of these rows are never read)
+          warp_arrive(&sh.f_full[t]);
+          warp_arrive(&sh.p_full[t]);
+          continue;
+        }
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s[q], ts + q * 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) loaded(s[q]);
+        const int tok0 = j * kTileTokens, ring = n_masks % kMasks;
+        if (!sh.whole[ring] || tok0 + kTileTokens > lim_min) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t mask = sh.mask[ring][q];
+            const int left = lim - tok0 - q * 32;
+            const uint32_t keep =
+                mask & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((keep >> i) & 1)) s[q][i] = 0xff800000u;
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[q][i])), __uint_as_float(s[q][i + 1]));
+        const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc);
+        const bool grow = m_new > m;
+        const float f = grow ? ex2_approx(m - m_new) : 1.f;
+        if (grow) m = m_new;
+        sh.factor[t][in] = f;
+        warp_arrive(&sh.f_full[t]);
+        const float off = m == -INFINITY ? 0.f : -m;
+        const uint64_t off2 = pack_f2(off, off);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int e = 2 * i;
+            const uint64_t z =
+                fma_f2(pack_f2(__uint_as_float(s[2 * h + (e >> 5)][e & 31]),
+                               __uint_as_float(s[2 * h + (e >> 5)][(e & 31) + 1])),
+                       sc2, off2);
+            float z0, z1;
+            unpack_f2(z, z0, z1);
+            const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
+            sum[i & 1] = add_f2(sum[i & 1], pack_f2(p0, p1));
+            // the weights are rounded to the cache's type for the tensor cores (a
+            // relative 2^-9 in bf16, 2^-12 in fp16, each its own way); the sum is not
+            w[i] = pack2<T>(p0, p1);
+          }
+          tmem_st32(ts + h * 32, w);
+        }
+        float s0, s1;
+        unpack_f2(add_f2(sum[0], sum[1]), s0, s1);
+        l = l * f + (s0 + s1);
+        tmem_wait_st();
+        fence_before();
+        warp_arrive(&sh.p_full[t]);
+      }
+      if (!ok) break;
+      // the row's sum; the last piece's has been read
+      ok = warp_wait(&sh.o_empty[t], (pieces & 1) ^ 1, limit);
+      if (!ok) break;
+      sh.inv[t][in] = l == 0.f ? 0.f : 1.f / l;
+      warp_arrive(&sh.l_full[t]);
+      ++pieces;
+      if (!live) continue;
+      if (p.slot >= 0)
+        a.part_ml[(int64_t)p.slot * kUnitRows + r] = make_float2(m, l);
+      else if (a.lse)
+        a.lse[(int64_t)(p.token + x / a.G) * a.hq + p.kvh * a.G + x % a.G] =
+            l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+    }
+  } else if (warp < kMma0Warp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // ---- the accumulators: rescaled, mended, written -------------------------------------
+    const int in = tid & (kTileRows - 1), w = warp & 3;
+    const uint32_t lanes = (uint32_t)w << 21;
+    uint32_t steps[2] = {0, 0}, pieces[2] = {0, 0}, diagonals = 0;
+    RingAt<R> ring;
+    Piece p;
+    while (ok && next_piece(p)) {
+      const int tiles = p.rows > kTileRows ? 2 : 1;
+      for (int j = p.t0; j < p.t1 && ok; ++j) {
+        const int tok0 = j * kTileTokens;
+        ring.next();  // (K)
+        // some row does not attend to the whole step: its weights there are 0, but 0
+        // times an infinity or a NaN is NaN
+        const bool diagonal = tok0 + kTileTokens > max(p.lim0, 0);
+        if (diagonal) {
+          ok = warp_wait(&sh.full[ring.st], ring.ph, limit);
+          if (!ok) break;
+          uint4* row = reinterpret_cast<uint4*>(dyn + L::kKv + ring.st * L::kTile + in * 128);
+          uint32_t bad = 0;
+          const bool behind = tok0 + in >= p.end;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              bad |= not_finite<T>(row[h * (L::kHalf / 16) + ((c + in) & 7)]);
+          if (bad) {
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              for (int c = 0; c < 8; ++c)
+                row[h * (L::kHalf / 16) + ((c + in) & 7)] = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          const uint32_t word = __ballot_sync(0xffffffffu, bad && !behind);
+          if (lane == 0) sh.poison[diagonals & 1][w] = word;
+          warp_arrive(&sh.v_ok);
+        }
+        for (int t = 0; t < tiles; ++t) {
+          ok = warp_wait(&sh.f_full[t], steps[t] & 1, limit);
+          if (!ok) break;
+          if (j > p.t0 && t * kTileRows + w * 32 < p.rows) {
+            const float f = sh.factor[t][in];
+            if (__any_sync(0xffffffffu, f != 1.f)) {
+              // (these scores were made behind the last product)
+              fence_after();
+              const uint32_t to = tmem + lanes + kO + t * D;
+              const uint64_t f2 = pack_f2(f, f);
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o, to + c);
+                tmem_wait_ld();
+                loaded(o);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float x0, x1;
+                  unpack_f2(mul_f2(pack_f2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2),
+                            x0, x1);
+                  o[i] = __float_as_uint(x0);
+                  o[i + 1] = __float_as_uint(x1);
+                }
+                tmem_st32(to + c, o);
+              }
+              tmem_wait_st();
+              fence_before();
+            }
+          }
+          warp_arrive(&sh.p_full[t]);
+        }
+        if (!ok) break;
+        if (diagonal) {
+          ok = warp_wait(&sh.v_ok, diagonals & 1, limit);
+          if (!ok) break;
+          // (written again two such steps on, behind a product that waits for this warp)
+          const uint32_t* words = sh.poison[diagonals & 1];
+          const uint32_t poison[4] = {words[0], words[1], words[2], words[3]};
+          ++diagonals;
+          const bool any = (poison[0] | poison[1] | poison[2] | poison[3]) != 0;
+          for (int t = 0; t < tiles; ++t) {
+            ok = warp_wait(&sh.pv_done[t], steps[t] & 1, limit);
+            if (!ok) break;
+            if (!any) continue;
+            // what was taken out of V, for the rows that attend to it
+            fence_after();
+            const int r = t * kTileRows + in, x = p.g0 + r;
+            const int lim = r < p.rows ? min(max(p.lim0 + x / a.G, 0), a.cols << a.shift) : 0;
+            const uint32_t ts = tmem + lanes + t * kTileTokens, to = tmem + lanes + kO + t * D;
+            for (int q = 0; q < 4; ++q)
+              for (uint32_t left = poison[q]; left; left &= left - 1) {
+                const int i = q * 32 + __ffs(left) - 1, tok = tok0 + i;
+                const uint32_t two = tmem_ld1(ts + i / 2);
+                const unsigned short bits = (unsigned short)(i & 1 ? two >> 16 : two);
+                const float weight = static_cast<float>(*reinterpret_cast<const T*>(&bits));
+                const int blk = a.table[(int64_t)p.b * a.ld_table + (tok >> a.shift)];
+                const T* v = static_cast<const T*>(a.v) + blk * a.block_stride +
+                             (tok & ((1 << a.shift) - 1)) * a.token_stride +
+                             p.kvh * a.head_stride;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(o, to + c);
+                  tmem_wait_ld();
+                  loaded(o);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (tok < lim)
+                      o[e] = __float_as_uint(__uint_as_float(o[e]) +
+                                             weight * static_cast<float>(v[c + e]));
+                  tmem_st32(to + c, o);
+                  tmem_wait_st();
+                }
+              }
+            fence_before();
+            warp_arrive(&sh.fixed[t]);
+          }
+        }
+        for (int t = 0; t < tiles; ++t) ++steps[t];
+        ring.next();  // (V)
+      }
+      if (!ok) break;
+      for (int t = 0; t < tiles; ++t) {
+        ok = warp_wait(&sh.pv_done[t], (steps[t] - 1) & 1, limit) &&
+             warp_wait(&sh.l_full[t], pieces[t] & 1, limit);
+        if (!ok) break;
+        fence_after();
+        const int r = t * kTileRows + in, x = p.g0 + r;
+        const bool live = r < p.rows;
+        if (t * kTileRows + w * 32 < p.rows) {
+          const float inv = sh.inv[t][in];
+          const uint32_t to = tmem + lanes + kO + t * D;
+          T* out = static_cast<T*>(a.out) +
+                   ((int64_t)(p.token + x / a.G) * a.hq + p.kvh * a.G + x % a.G) * D;
+          float* part = a.part_o + ((int64_t)max(p.slot, 0) * kUnitRows + r) * D;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o, to + c);
+            tmem_wait_ld();
+            loaded(o);
+            if (!live) continue;
+            if (p.slot >= 0) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<uint4*>(part + c + i) =
+                    make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            } else {
+              uint32_t y[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                y[i] = inv == 0.f ? 0u
+                                  : pack2<T>(__uint_as_float(o[2 * i]) * inv,
+                                             __uint_as_float(o[2 * i + 1]) * inv);
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint4*>(out + c + 2 * i) =
+                    make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            }
+          }
+          fence_before();
+        }
+        warp_arrive(&sh.o_empty[t]);
+        ++pieces[t];
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == kKvWarp) {
+      // ---- keys and values, tile by tile ------------------------------------------------
+      const int box = min(1 << a.shift, kTileTokens);  // tokens of a copy
+      const int boxes = kTileTokens / box;
+      int n_issued = 0, n_masks = 0;
+      RingAt<R> ring;
+      Piece p;
+      while (ok && next_piece(p)) {
+        const int32_t* table = a.table + (int64_t)p.b * a.ld_table;
+        for (int j = p.t0; j < p.t1 && ok; ++j, ++n_masks) {
+          const int tok0 = j * kTileTokens;
+          // the blocks of this tile, up to 16 of them: one a lane
+          const int tok = tok0 + lane * box;
+          const bool here = lane < boxes && tok < p.end;
+          int blk = here ? table[tok >> a.shift] : -1;
+          const bool fine = blk >= 0 && blk < a.num_blocks;
+          if (here && !fine) atomicOr(a.err_word, kErrBadBlock);
+          if (!fine) blk = a.num_blocks;  // outside: the copy fills zeros
+          const unsigned good = __ballot_sync(0xffffffffu, fine);
+          if (lane < 4) {
+            uint32_t m = 0;
+            if (box >= 32) {
+              m = (good >> (lane * 32 / box)) & 1 ? 0xffffffffu : 0u;
+            } else {
+              for (int i = 0; i < 32; i += box)
+                if ((good >> ((lane * 32 + i) / box)) & 1) m |= ((1u << box) - 1) << i;
+            }
+            const int left = p.end - tok0 - lane * 32;
+            m &= left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1;
+            sh.mask[n_masks % kMasks][lane] = m;
+            const unsigned all = __ballot_sync(0xfu, m == 0xffffffffu);
+            if (lane == 0) sh.whole[n_masks % kMasks] = all == 0xfu;
+          }
+          __syncwarp();
+          const int in_block = tok0 & ((1 << a.shift) - 1);  // (blocks longer than a tile)
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = warp_wait(&sh.empty[ring.st], ring.ph ^ 1, limit);
+            if (!ok) break;
+            uint64_t* bar = &sh.full[ring.st];
+            if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
+            __syncwarp();
+            if (lane < boxes)
+              for (int h = 0; h < D / 64; ++h)
+                tma_tile(base + L::kKv + ring.st * L::kTile + h * L::kHalf + lane * box * 128,
+                         kv ? &map_v : &map_k, bar, h * 64, in_block, p.kvh, blk);
+            ++n_issued;
+            ring.next();
+          }
+        }
+      }
+      // no copy is in flight when the CTA's memory goes to another
+      const int last = min(n_issued, R);
+      for (int i = 0; i < last; ++i) {
+        const int n = n_issued - last + i;
+        mbar_wait_clocked(&sh.full[n % R], (n / R) & 1, kDrainCycles);
+      }
+    } else if (warp == kPieceWarp) {
+      // ---- the pieces, and their rows of Q -------------------------------------------------
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      const int G = a.grid, c = blockIdx.x;
+      const ChunkStart s0 = a.plan_start[c];
+      const int64_t stop = a.plan_start[c + 1].at;
+      int64_t at = s0.at;
+      int b = s0.b, pair = s0.pair, kvh = s0.kvh, step = s0.step;
+      uint32_t uses[2] = {0, 0};
+      int round = 0;
+      const bool flip = a.scale_log2 < 0.f;
+      for (int k = 0; ok; ++k) {
+        Piece p{};
+        if (round < s0.rounds) {  // a whole unit; every other round the other way about
+          const int64_t u = (int64_t)round * G + (round & 1 ? G - 1 - c : c);
+          ++round;
+          p.b = find_request(a.plan_first, 2, a.B, u);
+          const Request r = request(a, p.b);
+          const int i = (int)(u - a.plan_first[2 * p.b]);
+          p.kvh = i % a.hkv;
+          const int pr = r.pairs - 1 - i / a.hkv;
+          p.t0 = 0;
+          p.t1 = unit_steps(a, r, pr);
+          p.slot = -1;
+          const int64_t row0 = (int64_t)pr * kUnitRows;
+          p.rows = (int)min((int64_t)kUnitRows, (int64_t)r.n * a.G - row0);
+          p.token = r.s0 + (int)(row0 / a.G);
+          p.g0 = (int)(row0 % a.G);
+          p.end = unit_end(a, r, pr);
+          p.lim0 = (int)max(min(r.before + row0 / a.G + 1, (int64_t)1 << 30), -((int64_t)1 << 30));
+        } else if (at < stop) {  // the rest of a unit, or of this CTA's steps
+          const Request r = request(a, b);
+          const int n = unit_steps(a, r, pair);
+          p.b = b;
+          p.kvh = kvh;
+          p.t0 = step;
+          p.t1 = (int)min((int64_t)n, step + (stop - at));
+          p.slot = step > 0 ? 2 * c : p.t1 < n ? 2 * c + 1 : -1;
+          const int64_t row0 = (int64_t)pair * kUnitRows;
+          p.rows = (int)min((int64_t)kUnitRows, (int64_t)r.n * a.G - row0);
+          p.token = r.s0 + (int)(row0 / a.G);
+          p.g0 = (int)(row0 % a.G);
+          p.end = unit_end(a, r, pair);
+          p.lim0 = (int)max(min(r.before + row0 / a.G + 1, (int64_t)1 << 30), -((int64_t)1 << 30));
+          at += p.t1 - p.t0;
+          step = 0;
+          if (++kvh == a.hkv) {
+            kvh = 0;
+            if (--pair < 0 && at < stop) {
+              do ++b;
+              while (b < a.B - 1 && request(a, b).pairs == 0);
+              pair = request(a, b).pairs - 1;
+            }
+          }
+        }
+        ok = warp_wait(&sh.piece_empty[k % kPieces], ((k / kPieces) & 1) ^ 1, limit);
+        if (!ok) break;
+        if (lane == 0) sh.piece[k % kPieces] = p;
+        warp_arrive(&sh.piece_full[k % kPieces]);
+        if (p.rows == 0) break;
+        for (int t = 0; t < 2 && t * kTileRows < p.rows && ok; ++t) {
+          ok = warp_wait(&sh.q_empty[t], (uses[t] & 1) ^ 1, limit);
+          if (!ok) break;
+          // 16 bytes a lane, D / 8 lanes to a row
+          constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+          const int ch = lane % kLanes;
+          const int first = lane / kLanes;
+          const int x = p.g0 + t * kTileRows + first;
+          int token = p.token + x / a.G, g = x % a.G;
+          const int n = min(kTileRows, p.rows - t * kTileRows);
+          const uint32_t to = base + L::kQ + t * L::kTile + (ch / 8) * L::kHalf;
+          for (int i = first; i < n; i += kRows) {
+            copy16_async(to + i * 128 + (((ch & 7) ^ (i & 7)) << 4),
+                         static_cast<const T*>(a.q) + (int64_t)token * a.q_row +
+                             (int64_t)(p.kvh * a.G + g) * a.q_head + ch * 8);
+            g += kRows;
+            while (g >= a.G) {
+              g -= a.G;
+              ++token;
+            }
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          if (flip)  // a negative scale: its sign on Q (each lane what it has copied)
+            for (int i = first; i < n; i += kRows) {
+              uint4* v = reinterpret_cast<uint4*>(dyn + (to - base) + i * 128 +
+                                                  (((ch & 7) ^ (i & 7)) << 4));
+              uint4 y = *v;
+              y.x ^= 0x80008000u, y.y ^= 0x80008000u, y.z ^= 0x80008000u, y.w ^= 0x80008000u;
+              *v = y;
+            }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          warp_arrive(&sh.q_full[t]);
+          ++uses[t];
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      // ---- MMAs: a warp to a tile walks the steps and waits; one lane issues ----------------
+      constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      // fp32 accumulators; K-major A and B; N = 128 tokens, M = 128
+      constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) |
+                                   ((kTileTokens / 8) << 17) | ((kTileRows / 16) << 24);
+      // B (V) is N-major: its rows are tokens; N = D
+      constexpr uint32_t kIdescO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) |
+                                   ((uint32_t)(D / 8) << 17) | ((kTileRows / 16) << 24);
+      constexpr uint32_t kHi = desc_hi(1024);
+      const int t = warp - kMma0Warp;
+      const uint32_t a_lo = desc_lo(base + L::kQ + t * L::kTile, 16),
+                     k_lo = desc_lo(base + L::kKv, 16), v_lo = desc_lo(base + L::kKv, L::kHalf);
+      const uint32_t s_at = tmem + t * kTileTokens, o_at = tmem + kO + t * D;
+      uint32_t steps = 0, pieces = 0, diagonals = 0, fixes = 0;
+      RingAt<R> ring;
+      Piece p;
+      while (ok && next_piece(p)) {
+        const bool both = p.rows > kTileRows;
+        if (t == 1 && !both) {
+          ring.skip(2 * (p.t1 - p.t0));
+          for (int j = p.t0; j < p.t1; ++j)
+            diagonals += (j + 1) * kTileTokens > max(p.lim0, 0);
+          continue;
+        }
+        ok = warp_wait(&sh.q_full[t], pieces & 1, limit);
+        for (int j = p.t0; j < p.t1 && ok; ++j) {
+          ok = warp_wait(&sh.full[ring.st], ring.ph, limit);
+          // the product with the last P, which lies over S, is done
+          if (ok && steps > 0) ok = warp_wait(&sh.pv_done[t], (steps - 1) & 1, limit);
+          if (!ok) break;
+          fence_after();
+          if (elect_one()) {
+            const uint32_t b_lo = k_lo + ring.st * (L::kTile >> 4);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = ((ks / 4) * L::kHalf + (ks % 4) * 32) >> 4;
+              mma_ss(s_at, a_lo + off, b_lo + off, kHi, kIdescS, ks > 0);
+            }
+            mma_commit(&sh.s_full[t]);
+            mma_commit(&sh.empty[ring.st]);
+            if (!both) mma_commit(&sh.empty[ring.st]);
+            if (j + 1 == p.t1) mma_commit(&sh.q_empty[t]);
+          }
+          __syncwarp();
+          ring.next();
+          ok = warp_wait(&sh.full[ring.st], ring.ph, limit);
+          const bool diagonal = (j + 1) * kTileTokens > max(p.lim0, 0);
+          bool poisoned = false;
+          if (ok && diagonal) {
+            ok = warp_wait(&sh.v_ok, diagonals & 1, limit);
+            const uint32_t* words = sh.poison[diagonals & 1];
+            poisoned = (words[0] | words[1] | words[2] | words[3]) != 0;
+            ++diagonals;
+          }
+          // the accumulator of the last piece has been read
+          if (ok && j == p.t0) ok = warp_wait(&sh.o_empty[t], (pieces & 1) ^ 1, limit);
+          if (ok) ok = warp_wait(&sh.p_full[t], steps & 1, limit);
+          if (!ok) break;
+          fence_after();
+          if (elect_one()) {
+            const uint32_t b_lo = v_lo + ring.st * (L::kTile >> 4);
+#pragma unroll
+            for (int ks = 0; ks < kTileTokens / 16; ++ks)
+              mma_ts(o_at, s_at + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO,
+                     ks > 0 ? 1u : (uint32_t)(j > p.t0));
+            mma_commit(&sh.pv_done[t]);
+            mma_commit(&sh.empty[ring.st]);
+            if (!both) mma_commit(&sh.empty[ring.st]);
+          }
+          __syncwarp();
+          ring.next();
+          ++steps;
+          if (poisoned) {
+            ok = warp_wait(&sh.fixed[t], fixes & 1, limit);
+            ++fixes;
+          }
+        }
+        ++pieces;
+      }
+      // none of its MMAs is in flight when the CTA's memory goes to another
+      if (elect_one()) mma_commit(&sh.drained[t]);
+      __syncwarp();
+      mbar_wait_clocked(&sh.drained[t], 0, kDrainCycles);
+    }
+  }
+  if (!ok) atomicOr(a.err_word, kErrTimeout);
+  fence_before();
+  __syncthreads();
+  if (warp == kMma0Warp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// A unit whose steps two or more CTAs had: CTA c began it (its second slot), the
+// following ones went on (their first slots).  A warp to a row rescales the parts to
+// their common maximum, sums and divides.  A part that holds nothing (sum 0) is not read.
+constexpr int kJoinWarps = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(ChunkArgs a) {
+  constexpr int W = D / 32;
+  const int lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.y;
+  const ChunkStart s = a.plan_start[c + 1];
+  // the unit that the end of c's share lies in, if c began it
+  if (s.step == 0 || s.b >= a.B || s.at - s.step < a.plan_start[c].at) return;
+  const Request rq = request(a, s.b);
+  const int64_t row0 = (int64_t)s.pair * kUnitRows;
+  const int rows = (int)min((int64_t)kUnitRows, (int64_t)rq.n * a.G - row0);
+  const int r = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  const int64_t end = s.at - s.step + unit_steps(a, rq, s.pair);
+  int last = c + 1;  // the CTA with the unit's last step
+  while (last + 1 < a.grid && a.plan_start[last + 1].at < end) ++last;
+  auto slot = [&](int k) { return (int64_t)(k == c ? 2 * c + 1 : 2 * k) * kUnitRows + r; };
+  float m = -INFINITY, l = 0.f, acc[W] = {};
+  for (int k0 = c; k0 <= last; k0 += 32) {
+    const int k = k0 + lane;
+    const float2 ml = k <= last && a.plan_start[k].at < a.plan_start[k + 1].at
+                          ? a.part_ml[slot(k)] : make_float2(-INFINITY, 0.f);
+    const bool some = ml.y != 0.f;
+    const float mn = fmaxf(m, warp_max(ml.x)), base = mn == -INFINITY ? 0.f : mn;
+    const float old = ex2_approx(m - base), f = some ? ex2_approx(ml.x - base) : 0.f;
+    m = mn;
+    l = l * old + warp_sum_f(some ? ml.y * f : 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) acc[w] *= old;
+    for (unsigned left = __ballot_sync(0xffffffffu, some); left; left &= left - 1) {
+      const int i = __ffs(left) - 1;
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      const float* o = a.part_o + slot(k0 + i) * D + lane * W;
+      if constexpr (W == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(o);
+        acc[0] += v.x * fi, acc[1] += v.y * fi, acc[2] += v.z * fi, acc[3] += v.w * fi;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(o);
+        acc[0] += v.x * fi, acc[1] += v.y * fi;
+      }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int x = (int)(row0 % a.G) + r;
+  const int64_t row = (rq.s0 + row0 / a.G + x / a.G) * a.hq + s.kvh * a.G + x % a.G;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D + lane * W);
+#pragma unroll
+  for (int i = 0; i < W / 2; ++i) out[i] = pack2<T>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+}
+
+template <int D>
+constexpr size_t chunk_smem() {
+  return ChunkSmem<D>::kRest + sizeof(Shared<ChunkSmem<D>::kRing>);
+}
+static_assert(chunk_smem<128>() <= 232448, "227 KB to a CTA");
+
+template <typename T, int D>
+cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
+                         cudaStream_t stream) {
+  plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3((unsigned)a.grid);
+  cfg.blockDim = dim3(kChunkThreads);
+  cfg.dynamicSmemBytes = chunk_smem<D>();
+  if ((e = cudaLaunchKernelEx(&cfg, chunk_kernel<T, D>, a, mk, mv)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(kUnitRows / kJoinWarps, (unsigned)a.grid);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T, D>, a);
+}
+
+template <typename T, int D>
+cudaError_t prepare_typed() {
+  // the roles divide up 128 registers a thread: with fewer at launch they would wait
+  // for the rest
+  cudaFuncAttributes is;
+  const cudaError_t e = cudaFuncGetAttributes(&is, chunk_kernel<T, D>);
+  if (e != cudaSuccess) return e;
+  if (is.numRegs != 128) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)chunk_smem<D>());
+}
+
+}  // namespace
+
+cudaError_t prepare_chunk() {
+  cudaError_t e;
+  if ((e = prepare_typed<__nv_bfloat16, 64>()) || (e = prepare_typed<__nv_bfloat16, 128>()) ||
+      (e = prepare_typed<__half, 64>()) || (e = prepare_typed<__half, 128>()))
+    return e;
+  encode_tiled();  // the driver's entry point, looked up once
+  return cudaSuccess;
+}
+
+int64_t chunk_part_rows(int grid) { return 2ll * grid * kUnitRows; }
+
+bool chunk_mma_takes(const ChunkArgs& a) {
+  return cache_map_takes(a.shift, a.block_stride, a.token_stride, a.head_stride);
+}
+
+cudaError_t launch_chunk_mma(const ChunkArgs& a, int dtype, int head_dim, cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  if (!cache_map(&mk, a.k, dtype, head_dim, a.shift, a.hkv, a.num_blocks, a.block_stride,
+                 a.token_stride, a.head_stride) ||
+      !cache_map(&mv, a.v, dtype, head_dim, a.shift, a.hkv, a.num_blocks, a.block_stride,
+                 a.token_stride, a.head_stride))
+    return cudaErrorInvalidValue;
+  if (dtype == VT_DTYPE_BF16)
+    return head_dim == 128 ? launch_typed<__nv_bfloat16, 128>(a, mk, mv, stream)
+                           : launch_typed<__nv_bfloat16, 64>(a, mk, mv, stream);
+  return head_dim == 128 ? launch_typed<__half, 128>(a, mk, mv, stream)
+                         : launch_typed<__half, 64>(a, mk, mv, stream);
+}
+
+}  // namespace vt

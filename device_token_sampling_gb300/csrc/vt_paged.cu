@@ -23,6 +23,8 @@ struct vt_paged {
   float* d_part_o = nullptr;
   float2* d_part_ml = nullptr;
   int32_t* d_err = nullptr;  // the error word, then the attention's work counter
+  int64_t* d_plan_first = nullptr;  // the chunks' plan
+  vt::ChunkStart* d_plan_start = nullptr;
   // of release and compact: a bit to a block, the used ids before each 32, two totals
   uint32_t* d_used = nullptr;
   int32_t* d_ranks = nullptr;
@@ -127,6 +129,8 @@ void free_paged(vt_paged* h) {
   if (h->d_part_o) cudaFree(h->d_part_o);
   if (h->d_part_ml) cudaFree(h->d_part_ml);
   if (h->d_err) cudaFree(h->d_err);
+  if (h->d_plan_first) cudaFree(h->d_plan_first);
+  if (h->d_plan_start) cudaFree(h->d_plan_start);
   if (h->d_used) cudaFree(h->d_used);
   if (h->d_ranks) cudaFree(h->d_ranks);
   if (h->d_totals) cudaFree(h->d_totals);
@@ -161,8 +165,13 @@ int vt_paged_create(const vt_paged_config* config, vt_paged** out) {
          cudaMalloc(&h->d_totals, 2 * sizeof(int32_t)) == cudaSuccess;
   }
   if (ok && config->q_heads > 0) {
-    h->part_rows = 8ll * config->max_batch * config->q_heads + 32768;
-    ok = cudaMalloc(&h->d_part_o, h->part_rows * config->head_dim * sizeof(float)) ==
+    h->part_rows = std::max(8ll * config->max_batch * config->q_heads + 32768,
+                            (long long)vt::chunk_part_rows(h->num_sms));
+    ok = vt::prepare_chunk() == cudaSuccess &&
+         cudaMalloc(&h->d_plan_first, (config->max_batch + 1) * 2 * sizeof(int64_t)) ==
+             cudaSuccess &&
+         cudaMalloc(&h->d_plan_start, (h->num_sms + 1) * sizeof(vt::ChunkStart)) == cudaSuccess &&
+         cudaMalloc(&h->d_part_o, h->part_rows * config->head_dim * sizeof(float)) ==
              cudaSuccess &&
          cudaMalloc(&h->d_part_ml, h->part_rows * sizeof(float2)) == cudaSuccess;
   }
@@ -192,6 +201,8 @@ int vt_paged_check_errors(vt_paged* h) {
   VT_TRY(h, cudaMemcpy(h->h_err, h->d_err, sizeof(int32_t), cudaMemcpyDeviceToHost));
   if (*h->h_err == 0) return VT_OK;
   VT_TRY(h, cudaMemset(h->d_err, 0, sizeof(int32_t)));
+  if (*h->h_err & vt::kErrInternal)
+    return fail(h, VT_ERR_CUDA, "a kernel found its shared memory out of place");
   if (*h->h_err & vt::kErrTimeout)
     return fail(h, VT_ERR_TIMEOUT, "a bounded device wait ran out");
   if (*h->h_err & vt::kErrBadRows)
@@ -412,6 +423,12 @@ int vt_paged_chunk_attention(vt_paged* h, int32_t dtype, int32_t B, int32_t T, c
   a.num_sms = h->num_sms;
   a.err_word = h->d_err;
   a.wait_cycles = h->wait_cycles;
+  a.grid = h->num_sms;
+  a.min_steps = 2;
+  a.plan_first = h->d_plan_first;
+  a.plan_start = h->d_plan_start;
+  a.part_o = h->d_part_o;
+  a.part_ml = h->d_part_ml;
   cudaStream_t st = (cudaStream_t)stream;
   VT_TRY(h, vt::launch_chunk(a, dtype, c.head_dim, st));
   h->last_stream = st;
