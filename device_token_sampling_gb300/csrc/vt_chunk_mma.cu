@@ -1,8 +1,10 @@
 // vt_chunk_mma.cu -- attention of chunks on the 5th-generation tensor cores.
 //
-// The n_b * G query rows (token, head) of a request and kv head are cut into units of up
-// to 256 rows, two tiles of 128; a unit attends to the tokens up to its last row's
-// position, 128 at a step.  Three launches:
+// The query rows (token, head) of a request and kv head are cut into units of up to two
+// tiles of 128 rows, whole tokens each; a unit attends to the tokens up to its last row's
+// position, 128 at a step.  A unit of two tiles takes every step with both; one that fits
+// a tile has its steps taken by the two tiles in turn, whose results are added up at the
+// end.  Three launches:
 //   plan_kernel    counts the units' steps and gives every CTA its share;
 //   chunk_kernel   one CTA an SM, its pieces of units one after another;
 //   join_kernel    puts units together that more than one CTA worked on.
@@ -23,10 +25,12 @@ constexpr int kMasks = 8;     // steps whose token masks are kept
 constexpr int kCorrWarp = 8, kMma0Warp = 12, kKvWarp = 14, kPieceWarp = 15;
 
 // ---- the units ----------------------------------------------------------------
+// Heads in one tile: a.heads of the G, a.parts times; tokens in one tile: a.tokens.  A
+// virtual head is a kv head and a part of its G.
 struct Request {
   int s0, n;       // its rows of q
   int64_t before;  // tokens in front of them
-  int pairs;       // units of a kv head
+  int units;       // of a virtual head
 };
 __device__ __forceinline__ Request request(const ChunkArgs& a, int b) {
   Request r;
@@ -35,21 +39,27 @@ __device__ __forceinline__ Request request(const ChunkArgs& a, int b) {
   r.s0 = s0;
   r.n = fine ? s1 - s0 : 0;
   r.before = (int64_t)a.seq_lens[b] - r.n;
-  r.pairs = (int)(((int64_t)r.n * a.G + kUnitRows - 1) / kUnitRows);
+  r.units = (r.n + 2 * a.tokens - 1) / (2 * a.tokens);
   return r;
 }
-// The end of the tokens that unit `pair` attends to, and its steps (one at least, so
-// that rows which attend to nothing are written).
-__device__ __forceinline__ int unit_end(const ChunkArgs& a, const Request& r, int pair) {
-  const int64_t last = min((int64_t)(pair + 1) * kUnitRows, (int64_t)r.n * a.G) - 1;
-  const int64_t end = r.before + last / a.G + 1;
+__device__ __forceinline__ int unit_tokens(const ChunkArgs& a, const Request& r, int u) {
+  return min(2 * a.tokens, r.n - u * 2 * a.tokens);
+}
+// The end of the tokens that unit u attends to, and its steps (one at least, so that
+// rows which attend to nothing are written).
+__device__ __forceinline__ int unit_end(const ChunkArgs& a, const Request& r, int u) {
+  const int64_t end = r.before + min((u + 1) * 2 * a.tokens, r.n);
   return (int)min(max(end, (int64_t)0), (int64_t)a.cols << a.shift);
 }
-__device__ __forceinline__ int unit_steps(const ChunkArgs& a, const Request& r, int pair) {
-  return max(1, (unit_end(a, r, pair) + kTileTokens - 1) / kTileTokens);
+__device__ __forceinline__ int unit_steps(const ChunkArgs& a, const Request& r, int u) {
+  return max(1, (unit_end(a, r, u) + kTileTokens - 1) / kTileTokens);
 }
-// The order of a request's units: the longest first, its kv heads side by side.  (So
-// CTAs that run at the same time read the same keys and values from L2.)
+// What a step of it costs: two tiles take turns on a unit that fits one.
+__device__ __forceinline__ int unit_weight(const ChunkArgs& a, const Request& r, int u) {
+  return unit_tokens(a, r, u) > a.tokens ? 2 : 1;
+}
+// The order of a request's units: the longest first, its heads side by side.  (So CTAs
+// that run at the same time read the same keys and values from L2.)
 
 struct Sums2 {
   int64_t x, y;
@@ -86,10 +96,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       const Request r = request(a, b);
       const int s0 = a.starts[b], s1 = a.starts[b + 1];
       if (s0 < 0 || s0 > s1 || s1 > a.T) atomicOr(a.err_word, kErrBadRows);
-      x = (int64_t)r.pairs * a.hkv;
-      for (int p = 0; p < r.pairs; ++p) y += unit_steps(a, r, p);
-      y *= a.hkv;
-      if (r.pairs > 1) s_several = 1;
+      x = (int64_t)r.units * a.heads_all;
+      for (int u = 0; u < r.units; ++u) y += unit_steps(a, r, u) * unit_weight(a, r, u);
+      y *= a.heads_all;
+      if (r.units > 1) s_several = 1;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -139,15 +149,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
     const Request r = request(a, b);
     int64_t left = u - first[2 * b];
     skipped = first[2 * b + 1];
-    for (int p = r.pairs - 1; left > 0; --p) {
-      const int64_t k = min(left, (int64_t)a.hkv);
-      skipped += k * unit_steps(a, r, p);
+    for (int v = r.units - 1; left > 0; --v) {
+      const int64_t k = min(left, (int64_t)a.heads_all);
+      skipped += k * unit_steps(a, r, v) * unit_weight(a, r, v);
       left -= k;
     }
   }
   const int64_t todo = steps - skipped;
-  // (no CTA with less than kMinSteps, if that leaves some without)
-  const int64_t shares = max((int64_t)1, min((int64_t)G, todo / a.min_steps));
+  // (shares of min_cost at least, if that leaves some without)
+  const int64_t shares = max((int64_t)1, min((int64_t)G, todo / a.min_cost));
   for (int c = tid; c <= G; c += kPlanThreads) {
     const int64_t at = skipped + (c >= shares ? todo : todo * c / shares);
     ChunkStart s{};
@@ -157,17 +167,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       const int b = find_request(first + 1, 2, a.B, at);
       const Request r = request(a, b);
       int64_t left = at - first[2 * b + 1];
-      int p = r.pairs - 1, n = 1;
-      for (; p > 0; --p) {
-        n = unit_steps(a, r, p);
-        if (left < (int64_t)n * a.hkv) break;
-        left -= (int64_t)n * a.hkv;
+      int u = r.units - 1;
+      int64_t each = 0;
+      for (;; --u) {
+        each = (int64_t)unit_steps(a, r, u) * unit_weight(a, r, u);
+        if (u == 0 || left < each * a.heads_all) break;
+        left -= each * a.heads_all;
       }
-      if (p <= 0) n = unit_steps(a, r, 0);
       s.b = b;
-      s.pair = p;
-      s.kvh = (int)(left / n);
-      s.step = (int)(left % n);
+      s.unit = u;
+      s.head = (int)(left / each);
+      const int in = (int)(left % each), w = unit_weight(a, r, u);
+      s.step = in / w;  // (a whole step)
+      s.at -= in % w;
     }
     s.rounds = rounds;
     a.plan_start[c] = s;
@@ -179,57 +191,60 @@ template <int D>
 struct ChunkSmem {
   static constexpr int kHalf = kTileRows * 128;      // 128 rows of 64 elements
   static constexpr int kTile = (D / 64) * kHalf;     // bytes of a Q, K or V tile
-  static constexpr int kRing = D == 128 ? 5 : 8;     // K and V tiles
+  static constexpr int kRing = D == 128 ? 4 : 8;     // K and V tiles
   static constexpr int kQ = 0;
   static constexpr int kKv = 2 * kTile;
   static constexpr int kRest = kKv + kRing * kTile;
 };
 
 struct Piece {
-  int b, kvh;
-  int token, g0;  // row 0 of the unit: its row of q, and its head of the G
-  int rows;       // of the unit; 0: no more pieces
-  int t0, t1;     // steps
-  int end;        // of the unit's tokens
-  int lim0;       // end of the tokens that row 0 attends to
-  int slot;       // of its partial result, or -1: the whole unit
+  int b, kvh, head;  // the first query head
+  int heads;         // of a token here
+  int token;         // the unit's first row of q
+  int tokens;        // of the unit; 0: no more pieces
+  int t0, t1;        // steps
+  int end;           // of the unit's tokens
+  int lim0;          // end of the tokens that its first row attends to
+  int slot;          // of its partial result, or -1: the whole unit
 };
 
 template <int R>
 struct Shared {
-  uint64_t full[R], empty[R];        // of the ring
+  // of the ring: what both tiles use, what one of them does (a waiter sees every use of
+  // its barriers, so that a phase's parity says which it is)
+  uint64_t full[2][R], empty[R];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
-  // of each tile: scores made; factors posted; weights stored and the accumulator
-  // rescaled; product done; poisoned values added; sums posted; accumulator read
-  uint64_t s_full[2], f_full[2], p_full[2], pv_done[2], fixed[2], l_full[2], o_empty[2];
+  // of each tile: scores made; factors posted; the first half of the weights stored and
+  // the accumulator rescaled; the second half stored; product done; V of a step at the
+  // chunk's diagonal looked through; poisoned values added; sums posted; accumulator read
+  uint64_t s_full[2], f_full[2], p_half[2], p_full[2], pv_done[2], v_ok[2], fixed[2], l_full[2],
+      o_empty[2];
+  uint64_t x_full;                   // tile 1's sums of a unit that the tiles share, for tile 0
   uint64_t q_full[2], q_empty[2];
-  uint64_t v_ok;                     // V of a step at the chunk's diagonal looked through
   uint64_t drained[2];
   float factor[2][kTileRows];
   float inv[2][kTileRows];
   Piece piece[kPieces];
   uint32_t mask[kMasks][4];
   int32_t whole[kMasks];
-  uint32_t poison[2][4];             // tokens of V that are not finite, by turns
+  uint32_t poison[4][4];             // tokens of V that are not finite, by turns
   uint32_t tmem;
 };
 
-// A place in the ring and the parity of its use.
+// A place in the ring, and the parities of the uses of its two sets of full barriers.
+// Steps go to places 0, 1; 2, 3; .. in turn, and the tiles that share a unit take even
+// and odd steps of the CTA's whole sequence: a place is always the same tile's then.
 template <int R>
 struct RingAt {
+  static_assert(R % 4 == 0, "even and odd steps have their own places");
   int st = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next() {
-    if (++st == R) {
-      st = 0;
-      ph ^= 1;
-    }
+  uint32_t ph[2] = {0, 0};
+  __device__ __forceinline__ uint32_t parity(int set) const { return (ph[set] >> st) & 1; }
+  __device__ __forceinline__ void next(int set) {
+    ph[set] ^= 1u << st;
+    st = (st + 1) % R;
   }
-  __device__ __forceinline__ void skip(int n) {
-    n += st;
-    ph ^= (uint32_t)(n / R) & 1;
-    st = n % R;
-  }
+  __device__ __forceinline__ void pass() { st = (st + 2) % R; }  // the other tile's step
 };
 
 __device__ __forceinline__ uint64_t pack_f2(float lo, float hi) {
@@ -255,14 +270,27 @@ __device__ __forceinline__ uint64_t mul_f2(uint64_t x, uint64_t y) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   return r;
 }
+// 16 columns of this thread's lane
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : VT_R8(r, 0), VT_R8(r, 8)
+      : "r"(addr));
+}
+__device__ __forceinline__ void loaded16(uint32_t (&r)[16]) {
+  asm volatile("" : VT_P8(r, 0), VT_P8(r, 8)::"memory");
+}
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t addr) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
   return r;
 }
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -280,7 +308,8 @@ __device__ __forceinline__ uint32_t not_finite(const uint4& v) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v) {
+                 const __grid_constant__ CUtensorMap map_v,
+                 const __grid_constant__ CUtensorMap map_q) {
   using L = ChunkSmem<D>;
   constexpr int R = L::kRing;
   using Sh = Shared<R>;
@@ -299,7 +328,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) {
     for (int i = 0; i < R; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[0][i], 1);
+      mbar_init(&sh.full[1][i], 1);
       mbar_init(&sh.empty[i], 2);  // (both tiles' MMAs)
     }
     for (int i = 0; i < kPieces; ++i) {
@@ -309,8 +339,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.s_full[t], 1);
       mbar_init(&sh.f_full[t], 4);
-      mbar_init(&sh.p_full[t], 8);  // (the softmax and the factors' warps)
+      mbar_init(&sh.p_half[t], 8);  // (the softmax and the factors' warps)
+      mbar_init(&sh.p_full[t], 4);
       mbar_init(&sh.pv_done[t], 1);
+      mbar_init(&sh.v_ok[t], 4);
       mbar_init(&sh.fixed[t], 4);
       mbar_init(&sh.l_full[t], 4);
       mbar_init(&sh.o_empty[t], 4);
@@ -318,7 +350,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sh.q_empty[t], 1);
       mbar_init(&sh.drained[t], 1);
     }
-    mbar_init(&sh.v_ok, 4);
+    mbar_init(&sh.x_full, 4);
     fence_mbar_init();
   }
   if (warp == kMma0Warp) {
@@ -345,39 +377,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     p = sh.piece[at];
     warp_arrive(&sh.piece_empty[at]);
     ++n_piece;
-    return p.rows > 0;
+    return p.tokens > 0;
   };
+  // row `in` of a tile
+  const int in = tid & (kTileRows - 1), in_token = in / a.heads, in_head = in % a.heads;
+  const int cap = a.cols << a.shift;
 
   if (warp < kCorrWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ---- softmax: a warpgroup to a tile, one thread to a row ---------------------------
-    const int t = warp >> 2, in = tid & (kTileRows - 1);
+    const int t = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane (warp % 4) * 32
     const uint32_t ts = tmem + lanes + t * kTileTokens;
     // (a scale of 0 as one that leaves masked scores at -inf)
     const float sc = fmaxf(fabsf(a.scale_log2), 1e-30f);
     const uint64_t sc2 = pack_f2(sc, sc);
-    uint32_t steps = 0, pieces = 0;  // of this tile
+    uint32_t steps = 0, sums = 0, shared = 0;  // of this tile
     int n_masks = 0;
     Piece p;
     while (ok && next_piece(p)) {
-      const int n_steps = p.t1 - p.t0;
-      if (t * kTileRows >= p.rows) {
-        n_masks += n_steps;
-        continue;
-      }
-      const int r = t * kTileRows + in, x = p.g0 + r;
-      const bool live = r < p.rows;
-      const bool warp_live = t * kTileRows + (warp & 3) * 32 < p.rows;
-      const int lim = live ? min(max(p.lim0 + x / a.G, 0), a.cols << a.shift) : 0;
+      const bool two = p.tokens > a.tokens;  // else the tiles share the unit
+      const int token = (two ? t * a.tokens : 0) + in_token;
+      const bool live = token < p.tokens && in_token < a.tokens && in_head < p.heads;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      const int lim = live ? min(max(p.lim0 + token, 0), cap) : 0;
       const int lim_min = __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff);
       float m = -INFINITY, l = 0.f;
-      for (int j = p.t0; j < p.t1; ++j, ++steps, ++n_masks) {
+      for (int j = two ? p.t0 : p.t0 + ((n_masks ^ t) & 1); j < p.t1; j += two ? 1 : 2, ++steps) {
         ok = warp_wait(&sh.s_full[t], steps & 1, limit);
         if (!ok) break;
         fence_after();
         if (!warp_live) {  // (the products of these rows are never read)
           warp_arrive(&sh.f_full[t]);
+          warp_arrive(&sh.p_half[t]);
           warp_arrive(&sh.p_full[t]);
           continue;
         }
@@ -387,7 +419,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int q = 0; q < 4; ++q) loaded(s[q]);
-        const int tok0 = j * kTileTokens, ring = n_masks % kMasks;
+        const int tok0 = j * kTileTokens, ring = (n_masks + j - p.t0) % kMasks;
+        if (a.scale_log2 < 0.f) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[q][i] ^= 0x80000000u;
+        }
         if (!sh.whole[ring] || tok0 + kTileTokens > lim_min) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -405,7 +443,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int i = 0; i < 32; i += 2)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[q][i])), __uint_as_float(s[q][i + 1]));
+            mx[q] = max3(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
         const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc);
         const bool grow = m_new > m;
         const float f = grow ? ex2_approx(m - m_new) : 1.f;
@@ -434,80 +472,108 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             w[i] = pack2<T>(p0, p1);
           }
           tmem_st32(ts + h * 32, w);
+          tmem_wait_st();
+          fence_before();
+          warp_arrive(h == 0 ? &sh.p_half[t] : &sh.p_full[t]);
         }
         float s0, s1;
         unpack_f2(add_f2(sum[0], sum[1]), s0, s1);
         l = l * f + (s0 + s1);
-        tmem_wait_st();
-        fence_before();
-        warp_arrive(&sh.p_full[t]);
       }
+      n_masks += p.t1 - p.t0;
       if (!ok) break;
-      // the row's sum; the last piece's has been read
-      ok = warp_wait(&sh.o_empty[t], (pieces & 1) ^ 1, limit);
+      // the rows' sums; those of the last piece have been read
+      ok = warp_wait(&sh.o_empty[t], (sums & 1) ^ 1, limit);
+      ++sums;
       if (!ok) break;
-      sh.inv[t][in] = l == 0.f ? 0.f : 1.f / l;
+      if (two) {
+        sh.inv[t][in] = l == 0.f ? 0.f : p.slot >= 0 ? 1.f : 1.f / l;
+      } else if (t == 1) {
+        sh.inv[0][in] = m;
+        sh.inv[1][in] = l;
+        warp_arrive(&sh.x_full);
+        continue;
+      } else {
+        ok = warp_wait(&sh.x_full, shared & 1, limit);
+        ++shared;
+        if (!ok) break;
+        const float m1 = sh.inv[0][in], l1 = sh.inv[1][in];
+        const float mm = fmaxf(m, m1), base = mm == -INFINITY ? 0.f : mm;
+        const float f0 = ex2_approx(m - base), f1 = ex2_approx(m1 - base);
+        l = l * f0 + l1 * f1;
+        m = mm;
+        const float inv = l == 0.f ? 0.f : p.slot >= 0 ? 1.f : 1.f / l;
+        sh.inv[0][in] = f0 * inv;
+        sh.inv[1][in] = f1 * inv;
+      }
       warp_arrive(&sh.l_full[t]);
-      ++pieces;
       if (!live) continue;
       if (p.slot >= 0)
-        a.part_ml[(int64_t)p.slot * kUnitRows + r] = make_float2(m, l);
+        a.part_ml[(int64_t)p.slot * kUnitRows + (two ? t * kTileRows : 0) + in] = make_float2(m, l);
       else if (a.lse)
-        a.lse[(int64_t)(p.token + x / a.G) * a.hq + p.kvh * a.G + x % a.G] =
+        a.lse[(int64_t)(p.token + token) * a.hq + p.head + in_head] =
             l == 0.f ? -INFINITY : m * kLn2 + logf(l);
     }
   } else if (warp < kMma0Warp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     // ---- the accumulators: rescaled, mended, written -------------------------------------
-    const int in = tid & (kTileRows - 1), w = warp & 3;
+    const int w = warp & 3;
     const uint32_t lanes = (uint32_t)w << 21;
-    uint32_t steps[2] = {0, 0}, pieces[2] = {0, 0}, diagonals = 0;
+    // bit t: the parity of tile t's steps, its sums, its steps at a diagonal
+    uint32_t step_ph = 0, sum_ph = 0, diag_ph = 0, all = 0;
     RingAt<R> ring;
     Piece p;
     while (ok && next_piece(p)) {
-      const int tiles = p.rows > kTileRows ? 2 : 1;
-      for (int j = p.t0; j < p.t1 && ok; ++j) {
+      const bool two = p.tokens > a.tokens;
+      const bool here = in_token < a.tokens && in_head < p.heads;
+      // bit t: tile t's row is one of the unit's; the warp has such rows
+      const uint32_t live = (here && in_token < p.tokens ? 1u : 0u) |
+                            (here && in_token + (two ? a.tokens : 0) < p.tokens ? 2u : 0u);
+      const uint32_t warp_live = __reduce_or_sync(0xffffffffu, live);
+      for (int j = p.t0; j < p.t1 && ok; ++j, ++all) {
         const int tok0 = j * kTileTokens;
-        ring.next();  // (K)
+        const int from = two ? 0 : all & 1, to = two ? 2 : from + 1;  // tiles
+        ring.next(!two);  // (K)
         // some row does not attend to the whole step: its weights there are 0, but 0
         // times an infinity or a NaN is NaN
         const bool diagonal = tok0 + kTileTokens > max(p.lim0, 0);
-        if (diagonal) {
-          ok = warp_wait(&sh.full[ring.st], ring.ph, limit);
+        for (int t = from; t < to; ++t) {
+          ok = warp_wait(&sh.f_full[t], (step_ph >> t) & 1, limit);
           if (!ok) break;
-          uint4* row = reinterpret_cast<uint4*>(dyn + L::kKv + ring.st * L::kTile + in * 128);
-          uint32_t bad = 0;
-          const bool behind = tok0 + in >= p.end;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              bad |= not_finite<T>(row[h * (L::kHalf / 16) + ((c + in) & 7)]);
-          if (bad) {
+          if (diagonal && t == from) {
+            // (the scores are there, so the last V of this place has been used)
+            ok = warp_wait(&sh.full[!two][ring.st], ring.parity(!two), limit);
+            if (!ok) break;
+            uint4* row = reinterpret_cast<uint4*>(dyn + L::kKv + ring.st * L::kTile + in * 128);
+            uint32_t bad = 0;
+            const bool behind = tok0 + in >= p.end;
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
+#pragma unroll
               for (int c = 0; c < 8; ++c)
-                row[h * (L::kHalf / 16) + ((c + in) & 7)] = make_uint4(0, 0, 0, 0);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bad |= not_finite<T>(row[h * (L::kHalf / 16) + ((c + in) & 7)]);
+            if (bad) {
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+                for (int c = 0; c < 8; ++c)
+                  row[h * (L::kHalf / 16) + ((c + in) & 7)] = make_uint4(0, 0, 0, 0);
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            const uint32_t word = __ballot_sync(0xffffffffu, bad && !behind);
+            if (lane == 0) sh.poison[all & 3][w] = word;
+            for (int u = from; u < to; ++u) warp_arrive(&sh.v_ok[u]);
           }
-          const uint32_t word = __ballot_sync(0xffffffffu, bad && !behind);
-          if (lane == 0) sh.poison[diagonals & 1][w] = word;
-          warp_arrive(&sh.v_ok);
-        }
-        for (int t = 0; t < tiles; ++t) {
-          ok = warp_wait(&sh.f_full[t], steps[t] & 1, limit);
-          if (!ok) break;
-          if (j > p.t0 && t * kTileRows + w * 32 < p.rows) {
+          if (j >= p.t0 + (two ? 1 : 2) && ((warp_live >> t) & 1)) {
             const float f = sh.factor[t][in];
             if (__any_sync(0xffffffffu, f != 1.f)) {
               // (these scores were made behind the last product)
               fence_after();
-              const uint32_t to = tmem + lanes + kO + t * D;
+              const uint32_t o_at = tmem + lanes + kO + t * D;
               const uint64_t f2 = pack_f2(f, f);
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
-                tmem_ld32(o, to + c);
+                tmem_ld32(o, o_at + c);
                 tmem_wait_ld();
                 loaded(o);
 #pragma unroll
@@ -518,37 +584,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                   o[i] = __float_as_uint(x0);
                   o[i + 1] = __float_as_uint(x1);
                 }
-                tmem_st32(to + c, o);
+                tmem_st32(o_at + c, o);
               }
               tmem_wait_st();
               fence_before();
             }
           }
-          warp_arrive(&sh.p_full[t]);
+          warp_arrive(&sh.p_half[t]);
         }
         if (!ok) break;
         if (diagonal) {
-          ok = warp_wait(&sh.v_ok, diagonals & 1, limit);
-          if (!ok) break;
-          // (written again two such steps on, behind a product that waits for this warp)
-          const uint32_t* words = sh.poison[diagonals & 1];
-          const uint32_t poison[4] = {words[0], words[1], words[2], words[3]};
-          ++diagonals;
-          const bool any = (poison[0] | poison[1] | poison[2] | poison[3]) != 0;
-          for (int t = 0; t < tiles; ++t) {
-            ok = warp_wait(&sh.pv_done[t], steps[t] & 1, limit);
+          for (int t = from; t < to && ok; ++t) {
+            ok = warp_wait(&sh.v_ok[t], (diag_ph >> t) & 1, limit) &&
+                 warp_wait(&sh.pv_done[t], (step_ph >> t) & 1, limit);
+            diag_ph ^= 1u << t;
             if (!ok) break;
-            if (!any) continue;
+            // (written again four steps on, which no warp reaches before all are here)
+            const uint32_t* words = sh.poison[all & 3];
+            if ((words[0] | words[1] | words[2] | words[3]) == 0) continue;
             // what was taken out of V, for the rows that attend to it
             fence_after();
-            const int r = t * kTileRows + in, x = p.g0 + r;
-            const int lim = r < p.rows ? min(max(p.lim0 + x / a.G, 0), a.cols << a.shift) : 0;
-            const uint32_t ts = tmem + lanes + t * kTileTokens, to = tmem + lanes + kO + t * D;
+            const int lim =
+                (live >> t) & 1 ? min(max(p.lim0 + (two ? t * a.tokens : 0) + in_token, 0), cap) : 0;
+            const uint32_t s_at = tmem + lanes + t * kTileTokens, o_at = tmem + lanes + kO + t * D;
             for (int q = 0; q < 4; ++q)
-              for (uint32_t left = poison[q]; left; left &= left - 1) {
+              for (uint32_t left = words[q]; left; left &= left - 1) {
                 const int i = q * 32 + __ffs(left) - 1, tok = tok0 + i;
-                const uint32_t two = tmem_ld1(ts + i / 2);
-                const unsigned short bits = (unsigned short)(i & 1 ? two >> 16 : two);
+                const uint32_t pair = tmem_ld1(s_at + i / 2);
+                const unsigned short bits = (unsigned short)(i & 1 ? pair >> 16 : pair);
                 const float weight = static_cast<float>(*reinterpret_cast<const T*>(&bits));
                 const int blk = a.table[(int64_t)p.b * a.ld_table + (tok >> a.shift)];
                 const T* v = static_cast<const T*>(a.v) + blk * a.block_stride +
@@ -557,7 +620,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                   uint32_t o[32];
-                  tmem_ld32(o, to + c);
+                  tmem_ld32(o, o_at + c);
                   tmem_wait_ld();
                   loaded(o);
 #pragma unroll
@@ -565,60 +628,79 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (tok < lim)
                       o[e] = __float_as_uint(__uint_as_float(o[e]) +
                                              weight * static_cast<float>(v[c + e]));
-                  tmem_st32(to + c, o);
+                  tmem_st32(o_at + c, o);
                   tmem_wait_st();
                 }
               }
             fence_before();
             warp_arrive(&sh.fixed[t]);
           }
+          if (!ok) break;
         }
-        for (int t = 0; t < tiles; ++t) ++steps[t];
-        ring.next();  // (V)
+        for (int t = from; t < to; ++t) step_ph ^= 1u << t;
+        ring.next(!two);  // (V)
       }
       if (!ok) break;
-      for (int t = 0; t < tiles; ++t) {
-        ok = warp_wait(&sh.pv_done[t], (steps[t] - 1) & 1, limit) &&
-             warp_wait(&sh.l_full[t], pieces[t] & 1, limit);
+      for (int t = 0; t < (two ? 2 : 1); ++t) {
+        // tiles that share the unit: both at once, if both had steps
+        ok = warp_wait(&sh.l_full[t], (sum_ph >> t) & 1, limit);
+        const bool both = !two && p.t1 - p.t0 > 1;
+        const int one = two ? t : (all - 1) & 1;  // (the last step's)
+        if (ok) ok = warp_wait(&sh.pv_done[one], ((step_ph >> one) & 1) ^ 1, limit);
+        if (ok && both)
+          ok = warp_wait(&sh.pv_done[one ^ 1], ((step_ph >> (one ^ 1)) & 1) ^ 1, limit);
         if (!ok) break;
         fence_after();
-        const int r = t * kTileRows + in, x = p.g0 + r;
-        const bool live = r < p.rows;
-        if (t * kTileRows + w * 32 < p.rows) {
-          const float inv = sh.inv[t][in];
-          const uint32_t to = tmem + lanes + kO + t * D;
-          T* out = static_cast<T*>(a.out) +
-                   ((int64_t)(p.token + x / a.G) * a.hq + p.kvh * a.G + x % a.G) * D;
-          float* part = a.part_o + ((int64_t)max(p.slot, 0) * kUnitRows + r) * D;
+        if ((warp_live >> t) & 1) {
+          const float inv = sh.inv[one][in], inv1 = sh.inv[one ^ 1][in];
+          const uint32_t o_at = tmem + lanes + kO + one * D;
+          const uint32_t o1_at = tmem + lanes + kO + (one ^ 1) * D;
+          const int token = p.token + (two ? t * a.tokens : 0) + in_token;
+          T* out = static_cast<T*>(a.out) + ((int64_t)token * a.hq + p.head + in_head) * D;
+          float* part = a.part_o + ((int64_t)max(p.slot, 0) * kUnitRows + t * kTileRows + in) * D;
+          constexpr int kCols = 16;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o, to + c);
-            tmem_wait_ld();
-            loaded(o);
-            if (!live) continue;
+          for (int c = 0; c < D; c += kCols) {
+            uint32_t o[kCols];
+            tmem_ld16(o, o_at + c);
+            if (both) {
+              uint32_t o1[kCols];
+              tmem_ld16(o1, o1_at + c);
+              tmem_wait_ld();
+              loaded16(o);
+              loaded16(o1);
+#pragma unroll
+              for (int i = 0; i < kCols; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * inv +
+                                       __uint_as_float(o1[i]) * inv1);
+            } else {
+              tmem_wait_ld();
+              loaded16(o);
+#pragma unroll
+              for (int i = 0; i < kCols; ++i)
+                o[i] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+            }
+            if (!((live >> t) & 1)) continue;
             if (p.slot >= 0) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
+              for (int i = 0; i < kCols; i += 4)
                 *reinterpret_cast<uint4*>(part + c + i) =
                     make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             } else {
-              uint32_t y[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                y[i] = inv == 0.f ? 0u
-                                  : pack2<T>(__uint_as_float(o[2 * i]) * inv,
-                                             __uint_as_float(o[2 * i + 1]) * inv);
-#pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<uint4*>(out + c + 2 * i) =
-                    make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+              for (int i = 0; i < kCols; i += 8)
+                *reinterpret_cast<uint4*>(out + c + i) = make_uint4(
+                    pack2<T>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                    pack2<T>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
+                    pack2<T>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])),
+                    pack2<T>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
             }
           }
           fence_before();
         }
+        sum_ph ^= 1u << t;
         warp_arrive(&sh.o_empty[t]);
-        ++pieces[t];
+        if (!two) warp_arrive(&sh.o_empty[1]);
       }
     }
   } else {
@@ -627,11 +709,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // ---- keys and values, tile by tile ------------------------------------------------
       const int box = min(1 << a.shift, kTileTokens);  // tokens of a copy
       const int boxes = kTileTokens / box;
-      int n_issued = 0, n_masks = 0;
+      int n_masks = 0;
+      uint32_t used = 0;   // bit of each full barrier that a copy was to complete
+      uint32_t empty = 0;  // parities of the places' uses
       RingAt<R> ring;
       Piece p;
       while (ok && next_piece(p)) {
         const int32_t* table = a.table + (int64_t)p.b * a.ld_table;
+        const int set = p.tokens <= a.tokens;  // (the tiles share the unit)
         for (int j = p.t0; j < p.t1 && ok; ++j, ++n_masks) {
           const int tok0 = j * kTileTokens;
           // the blocks of this tile, up to 16 of them: one a lane
@@ -659,26 +744,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           __syncwarp();
           const int in_block = tok0 & ((1 << a.shift) - 1);  // (blocks longer than a tile)
           for (int kv = 0; kv < 2; ++kv) {
-            ok = warp_wait(&sh.empty[ring.st], ring.ph ^ 1, limit);
+            ok = warp_wait(&sh.empty[ring.st], ((empty >> ring.st) & 1) ^ 1, limit);
             if (!ok) break;
-            uint64_t* bar = &sh.full[ring.st];
+            empty ^= 1u << ring.st;
+            used |= 1u << (set * R + ring.st);
+            uint64_t* bar = &sh.full[set][ring.st];
             if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
             __syncwarp();
             if (lane < boxes)
               for (int h = 0; h < D / 64; ++h)
                 tma_tile(base + L::kKv + ring.st * L::kTile + h * L::kHalf + lane * box * 128,
                          kv ? &map_v : &map_k, bar, h * 64, in_block, p.kvh, blk);
-            ++n_issued;
-            ring.next();
+            ring.next(set);
           }
         }
       }
       // no copy is in flight when the CTA's memory goes to another
-      const int last = min(n_issued, R);
-      for (int i = 0; i < last; ++i) {
-        const int n = n_issued - last + i;
-        mbar_wait_clocked(&sh.full[n % R], (n / R) & 1, kDrainCycles);
-      }
+      for (int i = 0; i < 2 * R; ++i)  // (the last use of each)
+        if ((used >> i) & 1)
+          mbar_wait_clocked(&sh.full[i / R][i % R], ((ring.ph[i / R] >> (i % R)) & 1) ^ 1,
+                            kDrainCycles);
     } else if (warp == kPieceWarp) {
       // ---- the pieces, and their rows of Q -------------------------------------------------
       asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -686,51 +771,52 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const ChunkStart s0 = a.plan_start[c];
       const int64_t stop = a.plan_start[c + 1].at;
       int64_t at = s0.at;
-      int b = s0.b, pair = s0.pair, kvh = s0.kvh, step = s0.step;
+      int b = s0.b, unit = s0.unit, head = s0.head, step = s0.step;
       uint32_t uses[2] = {0, 0};
       int round = 0;
-      const bool flip = a.scale_log2 < 0.f;
       for (int k = 0; ok; ++k) {
         Piece p{};
-        if (round < s0.rounds) {  // a whole unit; every other round the other way about
-          const int64_t u = (int64_t)round * G + (round & 1 ? G - 1 - c : c);
-          ++round;
-          p.b = find_request(a.plan_first, 2, a.B, u);
-          const Request r = request(a, p.b);
-          const int i = (int)(u - a.plan_first[2 * p.b]);
-          p.kvh = i % a.hkv;
-          const int pr = r.pairs - 1 - i / a.hkv;
+        const bool whole = round < s0.rounds;
+        if (whole || at < stop) {
+          int pb = b, pu = unit, ph = head;
+          if (whole) {  // every other round the other way about
+            const int64_t u = (int64_t)round * G + (round & 1 ? G - 1 - c : c);
+            ++round;
+            pb = find_request(a.plan_first, 2, a.B, u);
+            const int i = (int)(u - a.plan_first[2 * pb]);
+            ph = i % a.heads_all;
+            pu = i / a.heads_all;  // (from the last)
+          }
+          const Request r = request(a, pb);
+          if (whole) pu = r.units - 1 - pu;
+          const int n = unit_steps(a, r, pu);
+          p.b = pb;
+          p.kvh = ph / a.parts;
+          const int part = ph % a.parts * a.heads;
+          p.head = p.kvh * a.G + part;
+          p.heads = min(a.heads, a.G - part);
+          p.token = r.s0 + pu * 2 * a.tokens;
+          p.tokens = unit_tokens(a, r, pu);
+          p.end = unit_end(a, r, pu);
+          p.lim0 = (int)max(min(r.before + pu * 2 * a.tokens + 1, (int64_t)1 << 30),
+                            -((int64_t)1 << 30));
           p.t0 = 0;
-          p.t1 = unit_steps(a, r, pr);
+          p.t1 = n;
           p.slot = -1;
-          const int64_t row0 = (int64_t)pr * kUnitRows;
-          p.rows = (int)min((int64_t)kUnitRows, (int64_t)r.n * a.G - row0);
-          p.token = r.s0 + (int)(row0 / a.G);
-          p.g0 = (int)(row0 % a.G);
-          p.end = unit_end(a, r, pr);
-          p.lim0 = (int)max(min(r.before + row0 / a.G + 1, (int64_t)1 << 30), -((int64_t)1 << 30));
-        } else if (at < stop) {  // the rest of a unit, or of this CTA's steps
-          const Request r = request(a, b);
-          const int n = unit_steps(a, r, pair);
-          p.b = b;
-          p.kvh = kvh;
-          p.t0 = step;
-          p.t1 = (int)min((int64_t)n, step + (stop - at));
-          p.slot = step > 0 ? 2 * c : p.t1 < n ? 2 * c + 1 : -1;
-          const int64_t row0 = (int64_t)pair * kUnitRows;
-          p.rows = (int)min((int64_t)kUnitRows, (int64_t)r.n * a.G - row0);
-          p.token = r.s0 + (int)(row0 / a.G);
-          p.g0 = (int)(row0 % a.G);
-          p.end = unit_end(a, r, pair);
-          p.lim0 = (int)max(min(r.before + row0 / a.G + 1, (int64_t)1 << 30), -((int64_t)1 << 30));
-          at += p.t1 - p.t0;
-          step = 0;
-          if (++kvh == a.hkv) {
-            kvh = 0;
-            if (--pair < 0 && at < stop) {
-              do ++b;
-              while (b < a.B - 1 && request(a, b).pairs == 0);
-              pair = request(a, b).pairs - 1;
+          if (!whole) {  // the rest of a unit, or of this CTA's share
+            const int w = unit_weight(a, r, pu);
+            p.t0 = step;
+            p.t1 = (int)min((int64_t)n, step + (stop - at) / w);
+            p.slot = step > 0 ? 2 * c : p.t1 < n ? 2 * c + 1 : -1;
+            at += (int64_t)(p.t1 - p.t0) * w;
+            step = 0;
+            if (++head == a.heads_all) {
+              head = 0;
+              if (--unit < 0 && at < stop) {
+                do ++b;
+                while (b < a.B - 1 && request(a, b).units == 0);
+                unit = request(a, b).units - 1;
+              }
             }
           }
         }
@@ -738,43 +824,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (!ok) break;
         if (lane == 0) sh.piece[k % kPieces] = p;
         warp_arrive(&sh.piece_full[k % kPieces]);
-        if (p.rows == 0) break;
-        for (int t = 0; t < 2 && t * kTileRows < p.rows && ok; ++t) {
+        if (p.tokens == 0) break;
+        // (rows that are not this unit's are never used)
+        for (int t = 0; t < 2 && ok; ++t) {
           ok = warp_wait(&sh.q_empty[t], (uses[t] & 1) ^ 1, limit);
           if (!ok) break;
-          // 16 bytes a lane, D / 8 lanes to a row
-          constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-          const int ch = lane % kLanes;
-          const int first = lane / kLanes;
-          const int x = p.g0 + t * kTileRows + first;
-          int token = p.token + x / a.G, g = x % a.G;
-          const int n = min(kTileRows, p.rows - t * kTileRows);
-          const uint32_t to = base + L::kQ + t * L::kTile + (ch / 8) * L::kHalf;
-          for (int i = first; i < n; i += kRows) {
-            copy16_async(to + i * 128 + (((ch & 7) ^ (i & 7)) << 4),
-                         static_cast<const T*>(a.q) + (int64_t)token * a.q_row +
-                             (int64_t)(p.kvh * a.G + g) * a.q_head + ch * 8);
-            g += kRows;
-            while (g >= a.G) {
-              g -= a.G;
-              ++token;
-            }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sh.q_full[t], a.q_bytes);
+            for (int h = 0; h < D / 64; ++h)
+              tma_tile(base + L::kQ + t * L::kTile + h * L::kHalf, &map_q, &sh.q_full[t], h * 64,
+                       p.head - p.kvh * a.G, p.kvh,
+                       p.token + (p.tokens > a.tokens ? t * a.tokens : 0));
           }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          if (flip)  // a negative scale: its sign on Q (each lane what it has copied)
-            for (int i = first; i < n; i += kRows) {
-              uint4* v = reinterpret_cast<uint4*>(dyn + (to - base) + i * 128 +
-                                                  (((ch & 7) ^ (i & 7)) << 4));
-              uint4 y = *v;
-              y.x ^= 0x80008000u, y.y ^= 0x80008000u, y.z ^= 0x80008000u, y.w ^= 0x80008000u;
-              *v = y;
-            }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          warp_arrive(&sh.q_full[t]);
+          __syncwarp();
           ++uses[t];
         }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      // no copy is in flight when the CTA's memory goes to another
+      for (int t = 0; t < 2; ++t)
+        if (uses[t] > 0) mbar_wait_clocked(&sh.q_full[t], (uses[t] - 1) & 1, kDrainCycles);
     } else {
       // ---- MMAs: a warp to a tile walks the steps and waits; one lane issues ----------------
       constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
@@ -789,20 +857,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const uint32_t a_lo = desc_lo(base + L::kQ + t * L::kTile, 16),
                      k_lo = desc_lo(base + L::kKv, 16), v_lo = desc_lo(base + L::kKv, L::kHalf);
       const uint32_t s_at = tmem + t * kTileTokens, o_at = tmem + kO + t * D;
-      uint32_t steps = 0, pieces = 0, diagonals = 0, fixes = 0;
+      uint32_t steps = 0, pieces = 0, diagonals = 0, fixes = 0, all = 0;
       RingAt<R> ring;
       Piece p;
       while (ok && next_piece(p)) {
-        const bool both = p.rows > kTileRows;
-        if (t == 1 && !both) {
-          ring.skip(2 * (p.t1 - p.t0));
-          for (int j = p.t0; j < p.t1; ++j)
-            diagonals += (j + 1) * kTileTokens > max(p.lim0, 0);
-          continue;
-        }
+        const bool two = p.tokens > a.tokens;
         ok = warp_wait(&sh.q_full[t], pieces & 1, limit);
-        for (int j = p.t0; j < p.t1 && ok; ++j) {
-          ok = warp_wait(&sh.full[ring.st], ring.ph, limit);
+        const int set = !two, first = two ? p.t0 : p.t0 + ((all ^ t) & 1), by = two ? 1 : 2;
+        if (ok && first >= p.t1) {
+          if (elect_one()) mma_commit(&sh.q_empty[t]);
+          __syncwarp();
+        }
+        if (first > p.t0) ring.pass();
+        for (int j = first; j < p.t1 && ok; j += by) {
+          ok = warp_wait(&sh.full[set][ring.st], ring.parity(set), limit);
           // the product with the last P, which lies over S, is done
           if (ok && steps > 0) ok = warp_wait(&sh.pv_done[t], (steps - 1) & 1, limit);
           if (!ok) break;
@@ -816,43 +884,53 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             mma_commit(&sh.s_full[t]);
             mma_commit(&sh.empty[ring.st]);
-            if (!both) mma_commit(&sh.empty[ring.st]);
-            if (j + 1 == p.t1) mma_commit(&sh.q_empty[t]);
+            if (!two) mma_commit(&sh.empty[ring.st]);
+            if (j + by >= p.t1) mma_commit(&sh.q_empty[t]);
           }
           __syncwarp();
-          ring.next();
-          ok = warp_wait(&sh.full[ring.st], ring.ph, limit);
+          ring.next(set);
+          ok = warp_wait(&sh.full[set][ring.st], ring.parity(set), limit);
           const bool diagonal = (j + 1) * kTileTokens > max(p.lim0, 0);
           bool poisoned = false;
           if (ok && diagonal) {
-            ok = warp_wait(&sh.v_ok, diagonals & 1, limit);
-            const uint32_t* words = sh.poison[diagonals & 1];
+            ok = warp_wait(&sh.v_ok[t], diagonals & 1, limit);
+            const uint32_t* words = sh.poison[(all + (j - p.t0)) & 3];
             poisoned = (words[0] | words[1] | words[2] | words[3]) != 0;
             ++diagonals;
           }
-          // the accumulator of the last piece has been read
-          if (ok && j == p.t0) ok = warp_wait(&sh.o_empty[t], (pieces & 1) ^ 1, limit);
-          if (ok) ok = warp_wait(&sh.p_full[t], steps & 1, limit);
+          // (the factors' warps have read the last piece's accumulator by then)
+          if (ok) ok = warp_wait(&sh.p_half[t], steps & 1, limit);
+          if (!ok) break;
+          const uint32_t b_lo = v_lo + ring.st * (L::kTile >> 4);
+          fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < kTileTokens / 32; ++ks)
+              mma_ts(o_at, s_at + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO,
+                     ks > 0 ? 1u : (uint32_t)(j > first));
+          }
+          __syncwarp();
+          ok = warp_wait(&sh.p_full[t], steps & 1, limit);
           if (!ok) break;
           fence_after();
           if (elect_one()) {
-            const uint32_t b_lo = v_lo + ring.st * (L::kTile >> 4);
 #pragma unroll
-            for (int ks = 0; ks < kTileTokens / 16; ++ks)
-              mma_ts(o_at, s_at + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO,
-                     ks > 0 ? 1u : (uint32_t)(j > p.t0));
+            for (int ks = kTileTokens / 32; ks < kTileTokens / 16; ++ks)
+              mma_ts(o_at, s_at + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO, 1u);
             mma_commit(&sh.pv_done[t]);
             mma_commit(&sh.empty[ring.st]);
-            if (!both) mma_commit(&sh.empty[ring.st]);
+            if (!two) mma_commit(&sh.empty[ring.st]);
           }
           __syncwarp();
-          ring.next();
+          ring.next(set);
+          if (!two && j + 1 < p.t1) ring.pass();
           ++steps;
           if (poisoned) {
             ok = warp_wait(&sh.fixed[t], fixes & 1, limit);
             ++fixes;
           }
         }
+        all += p.t1 - p.t0;
         ++pieces;
       }
       // none of its MMAs is in flight when the CTA's memory goes to another
@@ -880,13 +958,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(ChunkArgs a
   const int c = blockIdx.y;
   const ChunkStart s = a.plan_start[c + 1];
   // the unit that the end of c's share lies in, if c began it
-  if (s.step == 0 || s.b >= a.B || s.at - s.step < a.plan_start[c].at) return;
+  if (s.step == 0 || s.b >= a.B) return;
   const Request rq = request(a, s.b);
-  const int64_t row0 = (int64_t)s.pair * kUnitRows;
-  const int rows = (int)min((int64_t)kUnitRows, (int64_t)rq.n * a.G - row0);
+  const int weight = unit_weight(a, rq, s.unit);
+  const int64_t begin = s.at - (int64_t)s.step * weight;
+  if (begin < a.plan_start[c].at) return;
   const int r = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (r >= rows) return;
-  const int64_t end = s.at - s.step + unit_steps(a, rq, s.pair);
+  const int kvh = s.head / a.parts, part = s.head % a.parts * a.heads;
+  const int tile = r / kTileRows, in = r % kTileRows;
+  const int token = tile * a.tokens + in / a.heads, head = part + in % a.heads;
+  if (in / a.heads >= a.tokens || token >= unit_tokens(a, rq, s.unit) || head >= a.G) return;
+  const int64_t end = begin + (int64_t)unit_steps(a, rq, s.unit) * weight;
   int last = c + 1;  // the CTA with the unit's last step
   while (last + 1 < a.grid && a.plan_start[last + 1].at < end) ++last;
   auto slot = [&](int k) { return (int64_t)(k == c ? 2 * c + 1 : 2 * k) * kUnitRows + r; };
@@ -916,8 +998,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(ChunkArgs a
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int x = (int)(row0 % a.G) + r;
-  const int64_t row = (rq.s0 + row0 / a.G + x / a.G) * a.hq + s.kvh * a.G + x % a.G;
+  const int64_t row =
+      (int64_t)(rq.s0 + s.unit * 2 * a.tokens + token) * a.hq + kvh * a.G + head;
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D + lane * W);
 #pragma unroll
   for (int i = 0; i < W / 2; ++i) out[i] = pack2<T>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
@@ -932,7 +1014,7 @@ static_assert(chunk_smem<128>() <= 232448, "227 KB to a CTA");
 
 template <typename T, int D>
 cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& mk, const CUtensorMap& mv,
-                         cudaStream_t stream) {
+                         const CUtensorMap& mq, cudaStream_t stream) {
   plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -946,7 +1028,7 @@ cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& mk, const CUtens
   cfg.gridDim = dim3((unsigned)a.grid);
   cfg.blockDim = dim3(kChunkThreads);
   cfg.dynamicSmemBytes = chunk_smem<D>();
-  if ((e = cudaLaunchKernelEx(&cfg, chunk_kernel<T, D>, a, mk, mv)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, chunk_kernel<T, D>, a, mk, mv, mq)) != cudaSuccess) return e;
   cfg.gridDim = dim3(kUnitRows / kJoinWarps, (unsigned)a.grid);
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
@@ -979,21 +1061,48 @@ cudaError_t prepare_chunk() {
 int64_t chunk_part_rows(int grid) { return 2ll * grid * kUnitRows; }
 
 bool chunk_mma_takes(const ChunkArgs& a) {
-  return cache_map_takes(a.shift, a.block_stride, a.token_stride, a.head_stride);
+  const int64_t most = 1ll << 38;
+  return cache_map_takes(a.shift, a.block_stride, a.token_stride, a.head_stride) && a.q_row > 0 &&
+         a.q_head > 0 && a.q_row < most && a.q_head * a.G < most;
 }
 
-cudaError_t launch_chunk_mma(const ChunkArgs& a, int dtype, int head_dim, cudaStream_t stream) {
-  CUtensorMap mk, mv;
+// q as [row][kv head][head][element], a tile of a.tokens rows and a.heads heads at a time.
+static bool q_map(CUtensorMap* map, const ChunkArgs& a, int dtype, int head_dim) {
+  const cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)a.G, (cuuint64_t)a.hkv,
+                              (cuuint64_t)a.T};
+  const cuuint64_t strides[3] = {(cuuint64_t)a.q_head * 2, (cuuint64_t)a.q_head * a.G * 2,
+                                 (cuuint64_t)a.q_row * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)a.heads, 1, (cuuint32_t)a.tokens};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return encode_tiled()(map,
+                        dtype == VT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        4, const_cast<void*>(a.q), dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_chunk_mma(ChunkArgs a, int dtype, int head_dim, cudaStream_t stream) {
+  // whole tokens of a kv head's G query heads to a tile of 128 rows (G = 7: 18 tokens, 126
+  // rows); more heads than rows in equal parts
+  a.parts = (a.G + kTileRows - 1) / kTileRows;
+  a.heads = (a.G + a.parts - 1) / a.parts;
+  a.tokens = kTileRows / a.heads;
+  a.heads_all = a.hkv * a.parts;
+  a.q_bytes = (uint32_t)(a.heads * a.tokens * head_dim * 2);
+  CUtensorMap mk, mv, mq;
   if (!cache_map(&mk, a.k, dtype, head_dim, a.shift, a.hkv, a.num_blocks, a.block_stride,
                  a.token_stride, a.head_stride) ||
       !cache_map(&mv, a.v, dtype, head_dim, a.shift, a.hkv, a.num_blocks, a.block_stride,
-                 a.token_stride, a.head_stride))
+                 a.token_stride, a.head_stride) ||
+      !q_map(&mq, a, dtype, head_dim))
     return cudaErrorInvalidValue;
   if (dtype == VT_DTYPE_BF16)
-    return head_dim == 128 ? launch_typed<__nv_bfloat16, 128>(a, mk, mv, stream)
-                           : launch_typed<__nv_bfloat16, 64>(a, mk, mv, stream);
-  return head_dim == 128 ? launch_typed<__half, 128>(a, mk, mv, stream)
-                         : launch_typed<__half, 64>(a, mk, mv, stream);
+    return head_dim == 128 ? launch_typed<__nv_bfloat16, 128>(a, mk, mv, mq, stream)
+                           : launch_typed<__nv_bfloat16, 64>(a, mk, mv, mq, stream);
+  return head_dim == 128 ? launch_typed<__half, 128>(a, mk, mv, mq, stream)
+                         : launch_typed<__half, 64>(a, mk, mv, mq, stream);
 }
 
 }  // namespace vt

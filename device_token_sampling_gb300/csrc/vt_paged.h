@@ -142,8 +142,8 @@ cudaError_t launch_prefix_attention(const AttnArgs& a, int dtype, int head_dim,
                                     cudaStream_t stream);
 // ---- attention of chunks (vt_chunk.cu) -------------------------------------------
 struct ChunkStart {  // where a CTA's share of the steps begins
-  int64_t at;                  // steps in front of it
-  int32_t b, pair, kvh, step;  // its first unit, and the step in that
+  int64_t at;                  // what the steps in front of it cost
+  int32_t b, unit, head, step; // its first unit, and the step in that
   int32_t rounds;              // whole units that the CTA has before
 };
 struct ChunkArgs {
@@ -168,17 +168,21 @@ struct ChunkArgs {
   int64_t wait_cycles;         // limit of the waits; 0: they have run out
   // the tensor cores' way
   int32_t grid;                // CTAs
-  int32_t min_steps;           // of 128 tokens to a CTA
-  int64_t* plan_first;         // [B + 1][2] units and steps in front of each request
+  int32_t min_cost;            // of a CTA's share
+  int64_t* plan_first;         // [B + 1][2] units and costs in front of each request
   ChunkStart* plan_start;      // [grid + 1]
   float* part_o;               // [grid][2][256][d] fp32, not normalised
   float2* part_ml;             // [grid][2][256] (max in log2 units, sum)
+  // filled by launch_chunk_mma: heads of a tile, parts of the G, tokens of a tile, virtual
+  // heads (hkv * parts), bytes of a tile of q
+  int32_t heads, parts, tokens, heads_all;
+  uint32_t q_bytes;
 };
 cudaError_t launch_chunk(const ChunkArgs& a, int dtype, int head_dim, cudaStream_t stream);
 // On the tensor cores (vt_chunk_mma.cu): whether the caches' layout can be taken, the
 // launch, and the rows of partial results that `grid` CTAs leave.
 bool chunk_mma_takes(const ChunkArgs& a);
-cudaError_t launch_chunk_mma(const ChunkArgs& a, int dtype, int head_dim, cudaStream_t stream);
+cudaError_t launch_chunk_mma(ChunkArgs a, int dtype, int head_dim, cudaStream_t stream);
 int64_t chunk_part_rows(int grid);
 cudaError_t prepare_chunk();
 
