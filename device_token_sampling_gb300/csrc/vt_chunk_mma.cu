@@ -20,6 +20,7 @@ constexpr int kUnitRows = 2 * kTileRows;
 constexpr int kChunkThreads = 512;
 constexpr int kPieces = 4;    // pieces that are known ahead
 constexpr int kMasks = 8;     // steps whose token masks are kept
+constexpr int kHalfStep = kTileTokens / 2;  // tokens of one product
 // warps: the softmax of each tile, the factors and outputs of both, then one each for
 // the tiles' MMAs, the copies of K and V, and the pieces with their rows of Q
 constexpr int kCorrWarp = 8, kMma0Warp = 12, kKvWarp = 14, kPieceWarp = 15;
@@ -214,15 +215,17 @@ struct Shared {
   // its barriers, so that a phase's parity says which it is)
   uint64_t full[2][R], empty[R];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
-  // of each tile: scores made; factors posted; the first half of the weights stored and
-  // the accumulator rescaled; the second half stored; product done; V of a step at the
-  // chunk's diagonal looked through; poisoned values added; sums posted; accumulator read
-  uint64_t s_full[2], f_full[2], p_half[2], p_full[2], pv_done[2], v_ok[2], fixed[2], l_full[2],
-      o_empty[2];
+  // of each tile, by halves of a step: scores made; weights stored
+  uint64_t s_full[2][2], p_full[2][2];
+  // of each tile: product of a half done; product of a unit done; sums posted; accumulator
+  // read
+  uint64_t pv_done[2], o_done[2], l_full[2], o_empty[2];
+  // of each tile, at a chunk's diagonal: V there; V looked through; weights of a half
+  // with poisoned values stored and the product before it done; those added
+  uint64_t v_there[2], v_ok[2], pv_poison[2], fixed[2];
   uint64_t x_full;                   // tile 1's sums of a unit that the tiles share, for tile 0
   uint64_t q_full[2], q_empty[2];
   uint64_t drained[2];
-  float factor[2][kTileRows];
   float inv[2][kTileRows];
   Piece piece[kPieces];
   uint32_t mask[kMasks][4];
@@ -231,21 +234,14 @@ struct Shared {
   uint32_t tmem;
 };
 
-// A place in the ring, and the parities of the uses of its two sets of full barriers.
-// Steps go to places 0, 1; 2, 3; .. in turn, and the tiles that share a unit take even
-// and odd steps of the CTA's whole sequence: a place is always the same tile's then.
+// The ring's places: K of the CTA's step g at 2 g, V behind it, modulo R.  The tiles that
+// share a unit take even and odd steps of the CTA's whole sequence, so that a place is
+// always the same tile's then.
 template <int R>
-struct RingAt {
-  static_assert(R % 4 == 0, "even and odd steps have their own places");
-  int st = 0;
-  uint32_t ph[2] = {0, 0};
-  __device__ __forceinline__ uint32_t parity(int set) const { return (ph[set] >> st) & 1; }
-  __device__ __forceinline__ void next(int set) {
-    ph[set] ^= 1u << st;
-    st = (st + 1) % R;
-  }
-  __device__ __forceinline__ void pass() { st = (st + 2) % R; }  // the other tile's step
-};
+__device__ __forceinline__ int place(uint32_t g, int v) {
+  static_assert(R == 4 || R == 8, "even and odd steps have their own places");
+  return (int)((2 * g + v) & (R - 1));
+}
 
 __device__ __forceinline__ uint64_t pack_f2(float lo, float hi) {
   uint64_t r;
@@ -337,15 +333,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sh.piece_empty[i], kPieceWarp);  // (every other warp)
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&sh.s_full[t], 1);
-      mbar_init(&sh.f_full[t], 4);
-      mbar_init(&sh.p_half[t], 8);  // (the softmax and the factors' warps)
-      mbar_init(&sh.p_full[t], 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sh.s_full[t][h], 1);
+        mbar_init(&sh.p_full[t][h], 4);
+      }
       mbar_init(&sh.pv_done[t], 1);
-      mbar_init(&sh.v_ok[t], 4);
-      mbar_init(&sh.fixed[t], 4);
+      mbar_init(&sh.o_done[t], 1);
       mbar_init(&sh.l_full[t], 4);
       mbar_init(&sh.o_empty[t], 4);
+      mbar_init(&sh.v_there[t], 1);
+      mbar_init(&sh.v_ok[t], 4);
+      mbar_init(&sh.pv_poison[t], 1);
+      mbar_init(&sh.fixed[t], 4);
       mbar_init(&sh.q_full[t], 1);
       mbar_init(&sh.q_empty[t], 1);
       mbar_init(&sh.drained[t], 1);
@@ -384,11 +383,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int cap = a.cols << a.shift;
 
   if (warp < kCorrWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
     // ---- softmax: a warpgroup to a tile, one thread to a row ---------------------------
     const int t = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane (warp % 4) * 32
-    const uint32_t ts = tmem + lanes + t * kTileTokens;
     // (a scale of 0 as one that leaves masked scores at -inf)
     const float sc = fmaxf(fabsf(a.scale_log2), 1e-30f);
     const uint64_t sc2 = pack_f2(sc, sc);
@@ -403,66 +401,97 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int lim = live ? min(max(p.lim0 + token, 0), cap) : 0;
       const int lim_min = __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff);
       float m = -INFINITY, l = 0.f;
-      for (int j = two ? p.t0 : p.t0 + ((n_masks ^ t) & 1); j < p.t1; j += two ? 1 : 2, ++steps) {
-        ok = warp_wait(&sh.s_full[t], steps & 1, limit);
-        if (!ok) break;
-        fence_after();
-        if (!warp_live) {  // (the products of these rows are never read)
-          warp_arrive(&sh.f_full[t]);
-          warp_arrive(&sh.p_half[t]);
-          warp_arrive(&sh.p_full[t]);
-          continue;
-        }
-        uint32_t s[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(s[q], ts + q * 32);
-        tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) loaded(s[q]);
-        const int tok0 = j * kTileTokens, ring = (n_masks + j - p.t0) % kMasks;
-        if (a.scale_log2 < 0.f) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[q][i] ^= 0x80000000u;
-        }
-        if (!sh.whole[ring] || tok0 + kTileTokens > lim_min) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t mask = sh.mask[ring][q];
-            const int left = lim - tok0 - q * 32;
-            const uint32_t keep =
-                mask & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((keep >> i) & 1)) s[q][i] = 0xff800000u;
-          }
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < 32; i += 2)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mx[q] = max3(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
-        const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc);
-        const bool grow = m_new > m;
-        const float f = grow ? ex2_approx(m - m_new) : 1.f;
-        if (grow) m = m_new;
-        sh.factor[t][in] = f;
-        warp_arrive(&sh.f_full[t]);
-        const float off = m == -INFINITY ? 0.f : -m;
-        const uint64_t off2 = pack_f2(off, off);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
+      bool begun = false;  // (a product has been added to the accumulator)
+      for (int j = two ? p.t0 : p.t0 + ((n_masks ^ t) & 1); j < p.t1 && ok;
+           j += two ? 1 : 2, ++steps) {
+        const int ring = (n_masks + j - p.t0) % kMasks;
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
+          ok = warp_wait(&sh.s_full[t][h], steps & 1, limit);
+          if (!ok) break;
+          fence_after();
+          if (!warp_live) {  // (the products of these rows are never read)
+            warp_arrive(&sh.p_full[t][h]);
+            continue;
+          }
+          const uint32_t ts = tmem + lanes + t * kTileTokens + h * kHalfStep;
+          uint32_t s[2][32];
+          tmem_ld32(s[0], ts);
+          tmem_ld32(s[1], ts + 32);
+          tmem_wait_ld();
+          loaded(s[0]);
+          loaded(s[1]);
+          const int tok0 = j * kTileTokens + h * kHalfStep;
+          if (a.scale_log2 < 0.f) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[q][i] ^= 0x80000000u;
+          }
+          if (!sh.whole[ring] || tok0 + kHalfStep > lim_min) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t mask = sh.mask[ring][h * 2 + q];
+              const int left = lim - tok0 - q * 32;
+              const uint32_t keep =
+                  mask & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((keep >> i) & 1)) s[q][i] = 0xff800000u;
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mx[q] = max3(mx[q], __uint_as_float(s[q & 1][i + (q & 2)]),
+                           __uint_as_float(s[q & 1][i + (q & 2) + 1]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          // The reference of the exponentials stays where it is until it is kSlack (in
+          // log2) short: weights of up to 2^kSlack are rounded like the others, each
+          // relative to itself, and a rescale of the accumulator is rare.
+          constexpr float kSlack = 8.f;
+          const bool grow = top > (m == -INFINITY ? m : m + kSlack);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? ex2_approx(m - top) : 1.f;
+            if (grow) m = top;
+            l *= f;
+            if (begun) {
+              ok = warp_wait(&sh.pv_done[t], (2 * steps + h - 1) & 1, limit);
+              if (!ok) break;
+              fence_after();
+              const uint32_t o_at = tmem + lanes + kO + t * D;
+              const uint64_t f2 = pack_f2(f, f);
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o, o_at + c);
+                tmem_wait_ld();
+                loaded(o);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float x0, x1;
+                  unpack_f2(mul_f2(pack_f2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2),
+                            x0, x1);
+                  o[i] = __float_as_uint(x0);
+                  o[i + 1] = __float_as_uint(x1);
+                }
+                tmem_st32(o_at + c, o);
+              }
+            }
+          }
+          begun = true;
+          const float off = m == -INFINITY ? 0.f : -m;
+          const uint64_t off2 = pack_f2(off, off);
+          uint64_t sum[2] = {0, 0};
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int e = 2 * i;
-            const uint64_t z =
-                fma_f2(pack_f2(__uint_as_float(s[2 * h + (e >> 5)][e & 31]),
-                               __uint_as_float(s[2 * h + (e >> 5)][(e & 31) + 1])),
-                       sc2, off2);
+            const uint64_t z = fma_f2(pack_f2(__uint_as_float(s[e >> 5][e & 31]),
+                                              __uint_as_float(s[e >> 5][(e & 31) + 1])),
+                                      sc2, off2);
             float z0, z1;
             unpack_f2(z, z0, z1);
             const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
@@ -471,14 +500,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // relative 2^-9 in bf16, 2^-12 in fp16, each its own way); the sum is not
             w[i] = pack2<T>(p0, p1);
           }
-          tmem_st32(ts + h * 32, w);
+          tmem_st32(ts, w);
+          float s0, s1;
+          unpack_f2(add_f2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
           tmem_wait_st();
           fence_before();
-          warp_arrive(h == 0 ? &sh.p_half[t] : &sh.p_full[t]);
+          warp_arrive(&sh.p_full[t][h]);
         }
-        float s0, s1;
-        unpack_f2(add_f2(sum[0], sum[1]), s0, s1);
-        l = l * f + (s0 + s1);
       }
       n_masks += p.t1 - p.t0;
       if (!ok) break;
@@ -515,13 +544,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             l == 0.f ? -INFINITY : m * kLn2 + logf(l);
     }
   } else if (warp < kMma0Warp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    // ---- the accumulators: rescaled, mended, written -------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    // ---- the accumulators: mended, written -----------------------------------------------
     const int w = warp & 3;
     const uint32_t lanes = (uint32_t)w << 21;
-    // bit t: the parity of tile t's steps, its sums, its steps at a diagonal
-    uint32_t step_ph = 0, sum_ph = 0, diag_ph = 0, all = 0;
-    RingAt<R> ring;
+    // units; bit t: the parity of tile t's sums, its steps at a diagonal, its poisoned
+    // halves; the CTA's steps; of the ring's places by set, the parity of their uses
+    uint32_t units = 0, sum_ph = 0, diag_ph = 0, poison_ph = 0, all = 0, full_ph[2] = {0, 0};
     Piece p;
     while (ok && next_piece(p)) {
       const bool two = p.tokens > a.tokens;
@@ -530,22 +559,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const uint32_t live = (here && in_token < p.tokens ? 1u : 0u) |
                             (here && in_token + (two ? a.tokens : 0) < p.tokens ? 2u : 0u);
       const uint32_t warp_live = __reduce_or_sync(0xffffffffu, live);
-      for (int j = p.t0; j < p.t1 && ok; ++j, ++all) {
+      const int n = p.t1 - p.t0;
+      // The steps that some row does not attend to the whole of: its weights there are 0,
+      // but 0 times an infinity or a NaN is NaN
+      const int diagonal = max(p.t0, max(p.lim0, 0) / kTileTokens);
+      for (int j = diagonal; j < p.t1 && ok; ++j) {
         const int tok0 = j * kTileTokens;
-        const int from = two ? 0 : all & 1, to = two ? 2 : from + 1;  // tiles
-        ring.next(!two);  // (K)
-        // some row does not attend to the whole step: its weights there are 0, but 0
-        // times an infinity or a NaN is NaN
-        const bool diagonal = tok0 + kTileTokens > max(p.lim0, 0);
+        const uint32_t g = all + (j - p.t0);
+        const int from = two ? 0 : g & 1, to = two ? 2 : from + 1;  // tiles
+        uint32_t bad = 0;
         for (int t = from; t < to; ++t) {
-          ok = warp_wait(&sh.f_full[t], (step_ph >> t) & 1, limit);
+          ok = warp_wait(&sh.v_there[t], (diag_ph >> t) & 1, limit);
           if (!ok) break;
-          if (diagonal && t == from) {
-            // (the scores are there, so the last V of this place has been used)
-            ok = warp_wait(&sh.full[!two][ring.st], ring.parity(!two), limit);
+          if (t == from) {
+            const int st = place<R>(g, 1);
+            // (uses of the place before this one in this piece)
+            const uint32_t before = (uint32_t)(j - p.t0) / (R / 2);
+            const uint32_t ph = ((!two ? full_ph[1] : full_ph[0]) >> st) + before;
+            ok = warp_wait(&sh.full[!two][st], ph & 1, limit);
             if (!ok) break;
-            uint4* row = reinterpret_cast<uint4*>(dyn + L::kKv + ring.st * L::kTile + in * 128);
-            uint32_t bad = 0;
+            uint4* row = reinterpret_cast<uint4*>(dyn + L::kKv + st * L::kTile + in * 128);
             const bool behind = tok0 + in >= p.end;
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
@@ -560,56 +593,38 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             const uint32_t word = __ballot_sync(0xffffffffu, bad && !behind);
-            if (lane == 0) sh.poison[all & 3][w] = word;
-            for (int u = from; u < to; ++u) warp_arrive(&sh.v_ok[u]);
+            if (lane == 0) sh.poison[g & 3][w] = word;
           }
-          if (j >= p.t0 + (two ? 1 : 2) && ((warp_live >> t) & 1)) {
-            const float f = sh.factor[t][in];
-            if (__any_sync(0xffffffffu, f != 1.f)) {
-              // (these scores were made behind the last product)
-              fence_after();
-              const uint32_t o_at = tmem + lanes + kO + t * D;
-              const uint64_t f2 = pack_f2(f, f);
-#pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, o_at + c);
-                tmem_wait_ld();
-                loaded(o);
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  float x0, x1;
-                  unpack_f2(mul_f2(pack_f2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2),
-                            x0, x1);
-                  o[i] = __float_as_uint(x0);
-                  o[i + 1] = __float_as_uint(x1);
-                }
-                tmem_st32(o_at + c, o);
-              }
-              tmem_wait_st();
-              fence_before();
-            }
-          }
-          warp_arrive(&sh.p_half[t]);
+          warp_arrive(&sh.v_ok[t]);
         }
         if (!ok) break;
-        if (diagonal) {
-          for (int t = from; t < to && ok; ++t) {
-            ok = warp_wait(&sh.v_ok[t], (diag_ph >> t) & 1, limit) &&
-                 warp_wait(&sh.pv_done[t], (step_ph >> t) & 1, limit);
-            diag_ph ^= 1u << t;
+        ok = warp_wait(&sh.v_ok[from], (diag_ph >> from) & 1, limit);
+        if (!ok) break;
+        for (int t = from; t < to; ++t) diag_ph ^= 1u << t;
+        // (written again four steps on, which no warp reaches before all are here)
+        const uint32_t* words = sh.poison[g & 3];
+        if ((words[0] | words[1] | words[2] | words[3]) == 0) continue;
+        // what was taken out of V, for the rows that attend to it
+        for (int h = 0; h < 2 && ok; ++h)
+          for (int t = from; t < to; ++t) {
+            ok = warp_wait(&sh.pv_poison[t], (poison_ph >> t) & 1, limit);
             if (!ok) break;
-            // (written again four steps on, which no warp reaches before all are here)
-            const uint32_t* words = sh.poison[all & 3];
-            if ((words[0] | words[1] | words[2] | words[3]) == 0) continue;
-            // what was taken out of V, for the rows that attend to it
+            poison_ph ^= 1u << t;
             fence_after();
             const int lim =
                 (live >> t) & 1 ? min(max(p.lim0 + (two ? t * a.tokens : 0) + in_token, 0), cap) : 0;
-            const uint32_t s_at = tmem + lanes + t * kTileTokens, o_at = tmem + lanes + kO + t * D;
-            for (int q = 0; q < 4; ++q)
-              for (uint32_t left = words[q]; left; left &= left - 1) {
-                const int i = q * 32 + __ffs(left) - 1, tok = tok0 + i;
+            const uint32_t s_at = tmem + lanes + t * kTileTokens + h * kHalfStep,
+                           o_at = tmem + lanes + kO + t * D;
+            if (h == 0 && j - p.t0 < (two ? 1 : 2)) {  // (the product would have begun it)
+              uint32_t o[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0;
+              for (int c = 0; c < D; c += 32) tmem_st32(o_at + c, o);
+              tmem_wait_st();
+            }
+            for (int q = 0; q < 2; ++q)
+              for (uint32_t left = words[h * 2 + q]; left; left &= left - 1) {
+                const int i = q * 32 + __ffs(left) - 1, tok = tok0 + h * kHalfStep + i;
                 const uint32_t pair = tmem_ld1(s_at + i / 2);
                 const unsigned short bits = (unsigned short)(i & 1 ? pair >> 16 : pair);
                 const float weight = static_cast<float>(*reinterpret_cast<const T*>(&bits));
@@ -635,20 +650,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             fence_before();
             warp_arrive(&sh.fixed[t]);
           }
-          if (!ok) break;
-        }
-        for (int t = from; t < to; ++t) step_ph ^= 1u << t;
-        ring.next(!two);  // (V)
       }
       if (!ok) break;
+      for (int c = 0; c < R / 2; ++c) {  // uses of V's places: every (R / 2)-th step each
+        const uint32_t uses = (uint32_t)(n + R / 2 - 1 - c) / (R / 2);
+        const uint32_t flip = (uses & 1) << place<R>(all + c, 1);
+        if (two) full_ph[0] ^= flip;
+        else full_ph[1] ^= flip;
+      }
+      all += n;
       for (int t = 0; t < (two ? 2 : 1); ++t) {
         // tiles that share the unit: both at once, if both had steps
         ok = warp_wait(&sh.l_full[t], (sum_ph >> t) & 1, limit);
-        const bool both = !two && p.t1 - p.t0 > 1;
+        const bool both = !two && n > 1;
         const int one = two ? t : (all - 1) & 1;  // (the last step's)
-        if (ok) ok = warp_wait(&sh.pv_done[one], ((step_ph >> one) & 1) ^ 1, limit);
-        if (ok && both)
-          ok = warp_wait(&sh.pv_done[one ^ 1], ((step_ph >> (one ^ 1)) & 1) ^ 1, limit);
+        for (int u = two ? t : 0; u < (two ? t + 1 : 2) && ok; ++u)
+          ok = warp_wait(&sh.o_done[u], units & 1, limit);
         if (!ok) break;
         fence_after();
         if ((warp_live >> t) & 1) {
@@ -702,22 +719,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         warp_arrive(&sh.o_empty[t]);
         if (!two) warp_arrive(&sh.o_empty[1]);
       }
+      ++units;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kKvWarp) {
       // ---- keys and values, tile by tile ------------------------------------------------
       const int box = min(1 << a.shift, kTileTokens);  // tokens of a copy
       const int boxes = kTileTokens / box;
-      int n_masks = 0;
-      uint32_t used = 0;   // bit of each full barrier that a copy was to complete
-      uint32_t empty = 0;  // parities of the places' uses
-      RingAt<R> ring;
+      uint32_t all = 0;
+      // of the full barriers: those that a copy was to complete, the parities of their
+      // uses; of the places, the parities of their uses
+      uint32_t used = 0, full_ph = 0, empty_ph = 0;
       Piece p;
       while (ok && next_piece(p)) {
         const int32_t* table = a.table + (int64_t)p.b * a.ld_table;
         const int set = p.tokens <= a.tokens;  // (the tiles share the unit)
-        for (int j = p.t0; j < p.t1 && ok; ++j, ++n_masks) {
+        for (int j = p.t0; j < p.t1 && ok; ++j, ++all) {
           const int tok0 = j * kTileTokens;
           // the blocks of this tile, up to 16 of them: one a lane
           const int tok = tok0 + lane * box;
@@ -737,33 +755,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             const int left = p.end - tok0 - lane * 32;
             m &= left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1;
-            sh.mask[n_masks % kMasks][lane] = m;
-            const unsigned all = __ballot_sync(0xfu, m == 0xffffffffu);
-            if (lane == 0) sh.whole[n_masks % kMasks] = all == 0xfu;
+            sh.mask[all % kMasks][lane] = m;
+            const unsigned every = __ballot_sync(0xfu, m == 0xffffffffu);
+            if (lane == 0) sh.whole[all % kMasks] = every == 0xfu;
           }
           __syncwarp();
           const int in_block = tok0 & ((1 << a.shift) - 1);  // (blocks longer than a tile)
           for (int kv = 0; kv < 2; ++kv) {
-            ok = warp_wait(&sh.empty[ring.st], ((empty >> ring.st) & 1) ^ 1, limit);
+            const int st = place<R>(all, kv);
+            ok = warp_wait(&sh.empty[st], ((empty_ph >> st) & 1) ^ 1, limit);
             if (!ok) break;
-            empty ^= 1u << ring.st;
-            used |= 1u << (set * R + ring.st);
-            uint64_t* bar = &sh.full[set][ring.st];
+            empty_ph ^= 1u << st;
+            const uint32_t bit = 1u << (set * R + st);
+            used |= bit;
+            full_ph ^= bit;
+            uint64_t* bar = &sh.full[set][st];
             if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
             __syncwarp();
             if (lane < boxes)
               for (int h = 0; h < D / 64; ++h)
-                tma_tile(base + L::kKv + ring.st * L::kTile + h * L::kHalf + lane * box * 128,
+                tma_tile(base + L::kKv + st * L::kTile + h * L::kHalf + lane * box * 128,
                          kv ? &map_v : &map_k, bar, h * 64, in_block, p.kvh, blk);
-            ring.next(set);
           }
         }
       }
       // no copy is in flight when the CTA's memory goes to another
       for (int i = 0; i < 2 * R; ++i)  // (the last use of each)
         if ((used >> i) & 1)
-          mbar_wait_clocked(&sh.full[i / R][i % R], ((ring.ph[i / R] >> (i % R)) & 1) ^ 1,
-                            kDrainCycles);
+          mbar_wait_clocked(&sh.full[i / R][i % R], ((full_ph >> i) & 1) ^ 1, kDrainCycles);
     } else if (warp == kPieceWarp) {
       // ---- the pieces, and their rows of Q -------------------------------------------------
       asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -846,9 +865,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     } else {
       // ---- MMAs: a warp to a tile walks the steps and waits; one lane issues ----------------
       constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-      // fp32 accumulators; K-major A and B; N = 128 tokens, M = 128
+      // fp32 accumulators; K-major A and B; N = 64 tokens, M = 128
       constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) |
-                                   ((kTileTokens / 8) << 17) | ((kTileRows / 16) << 24);
+                                   ((kHalfStep / 8) << 17) | ((kTileRows / 16) << 24);
       // B (V) is N-major: its rows are tokens; N = D
       constexpr uint32_t kIdescO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) |
                                    ((uint32_t)(D / 8) << 17) | ((kTileRows / 16) << 24);
@@ -857,80 +876,105 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const uint32_t a_lo = desc_lo(base + L::kQ + t * L::kTile, 16),
                      k_lo = desc_lo(base + L::kKv, 16), v_lo = desc_lo(base + L::kKv, L::kHalf);
       const uint32_t s_at = tmem + t * kTileTokens, o_at = tmem + kO + t * D;
-      uint32_t steps = 0, pieces = 0, diagonals = 0, fixes = 0, all = 0;
-      RingAt<R> ring;
+      // halves of a step, units, steps at a diagonal, poisoned halves, of this tile; the
+      // CTA's steps; of the ring's places by set, the parities of their uses
+      uint32_t halves = 0, pieces = 0, diagonals = 0, fixes = 0, all = 0, full_ph[2] = {0, 0};
       Piece p;
       while (ok && next_piece(p)) {
         const bool two = p.tokens > a.tokens;
+        const int set = !two, first = two ? 0 : (all ^ t) & 1, by = two ? 1 : 2;
+        const int n = p.t1 - p.t0;
+        const int n_halves = 2 * ((n - first + by - 1) / by);  // (n - first may be 0)
+        uint32_t ph = two ? full_ph[0] : full_ph[1];
         ok = warp_wait(&sh.q_full[t], pieces & 1, limit);
-        const int set = !two, first = two ? p.t0 : p.t0 + ((all ^ t) & 1), by = two ? 1 : 2;
-        if (ok && first >= p.t1) {
+        if (ok && n_halves == 0) {
           if (elect_one()) mma_commit(&sh.q_empty[t]);
           __syncwarp();
+          // (every unit's waits and arrivals, so that a parity is the last unit's)
+          ok = warp_wait(&sh.o_empty[t], (pieces & 1) ^ 1, limit);
+          if (ok) warp_arrive(&sh.o_done[t]);
         }
-        if (first > p.t0) ring.pass();
-        for (int j = first; j < p.t1 && ok; j += by) {
-          ok = warp_wait(&sh.full[set][ring.st], ring.parity(set), limit);
-          // the product with the last P, which lies over S, is done
-          if (ok && steps > 0) ok = warp_wait(&sh.pv_done[t], (steps - 1) & 1, limit);
+        bool poisoned = false;
+#pragma unroll 1
+        for (int i = -1; i < n_halves && ok; ++i) {
+          const int k = i + 1;
+          // The product with the P that lies where the next scores go is done.  (Waited for
+          // behind the last scores too: each product's phase in turn.  The next unit's
+          // first scores need no wait of their own.)
+          if (k > 0 && halves + k >= 2) ok = warp_wait(&sh.pv_done[t], (halves + k) & 1, limit);
           if (!ok) break;
-          fence_after();
-          if (elect_one()) {
-            const uint32_t b_lo = k_lo + ring.st * (L::kTile >> 4);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = ((ks / 4) * L::kHalf + (ks % 4) * 32) >> 4;
-              mma_ss(s_at, a_lo + off, b_lo + off, kHi, kIdescS, ks > 0);
+          if (k < n_halves) {  // S = Q K^T of the next half
+            const int st = place<R>(all + first + (k >> 1) * by, 0);
+            if (!(k & 1)) {
+              ok = warp_wait(&sh.full[set][st], (ph >> st) & 1, limit);
+              ph ^= 1u << st;
             }
-            mma_commit(&sh.s_full[t]);
-            mma_commit(&sh.empty[ring.st]);
-            if (!two) mma_commit(&sh.empty[ring.st]);
-            if (j + by >= p.t1) mma_commit(&sh.q_empty[t]);
-          }
-          __syncwarp();
-          ring.next(set);
-          ok = warp_wait(&sh.full[set][ring.st], ring.parity(set), limit);
-          const bool diagonal = (j + 1) * kTileTokens > max(p.lim0, 0);
-          bool poisoned = false;
-          if (ok && diagonal) {
-            ok = warp_wait(&sh.v_ok[t], diagonals & 1, limit);
-            const uint32_t* words = sh.poison[(all + (j - p.t0)) & 3];
-            poisoned = (words[0] | words[1] | words[2] | words[3]) != 0;
-            ++diagonals;
-          }
-          // (the factors' warps have read the last piece's accumulator by then)
-          if (ok) ok = warp_wait(&sh.p_half[t], steps & 1, limit);
-          if (!ok) break;
-          const uint32_t b_lo = v_lo + ring.st * (L::kTile >> 4);
-          fence_after();
-          if (elect_one()) {
+            if (!ok) break;
+            fence_after();
+            if (elect_one()) {
+              const uint32_t b_lo = k_lo + st * (L::kTile >> 4) + (k & 1) * (kHalfStep * 128 >> 4);
+              const uint32_t d = s_at + (k & 1) * kHalfStep;
 #pragma unroll
-            for (int ks = 0; ks < kTileTokens / 32; ++ks)
-              mma_ts(o_at, s_at + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO,
-                     ks > 0 ? 1u : (uint32_t)(j > first));
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = ((ks / 4) * L::kHalf + (ks % 4) * 32) >> 4;
+                mma_ss(d, a_lo + off, b_lo + off, kHi, kIdescS, ks > 0);
+              }
+              mma_commit(&sh.s_full[t][k & 1]);
+              if (k & 1) {
+                mma_commit(&sh.empty[st]);
+                if (!two) mma_commit(&sh.empty[st]);
+              }
+              if (k + 1 == n_halves) mma_commit(&sh.q_empty[t]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          ok = warp_wait(&sh.p_full[t], steps & 1, limit);
+          if (i < 0) continue;
+          const int j = first + (i >> 1) * by;  // of the piece
+          const int st = place<R>(all + j, 1);
+          if (!(i & 1)) {
+            ok = warp_wait(&sh.full[set][st], (ph >> st) & 1, limit);
+            ph ^= 1u << st;
+            poisoned = false;
+            if (ok && (p.t0 + j + 1) * kTileTokens > max(p.lim0, 0)) {
+              warp_arrive(&sh.v_there[t]);
+              ok = warp_wait(&sh.v_ok[t], diagonals & 1, limit);
+              ++diagonals;
+              const uint32_t* words = sh.poison[(all + j) & 3];
+              poisoned = (words[0] | words[1] | words[2] | words[3]) != 0;
+            }
+          }
+          // the accumulator of the last unit has been read
+          if (ok && i == 0) ok = warp_wait(&sh.o_empty[t], (pieces & 1) ^ 1, limit);
+          if (ok) ok = warp_wait(&sh.p_full[t][i & 1], ((halves + i) >> 1) & 1, limit);
           if (!ok) break;
           fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = kTileTokens / 32; ks < kTileTokens / 16; ++ks)
-              mma_ts(o_at, s_at + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO, 1u);
-            mma_commit(&sh.pv_done[t]);
-            mma_commit(&sh.empty[ring.st]);
-            if (!two) mma_commit(&sh.empty[ring.st]);
-          }
-          __syncwarp();
-          ring.next(set);
-          if (!two && j + 1 < p.t1) ring.pass();
-          ++steps;
-          if (poisoned) {
+          if (poisoned) {  // (what was taken out of V is added first, behind the last product)
+            warp_arrive(&sh.pv_poison[t]);
             ok = warp_wait(&sh.fixed[t], fixes & 1, limit);
             ++fixes;
+            if (!ok) break;
+            fence_after();
           }
+          if (elect_one()) {  // O += P V
+            const uint32_t b_lo = v_lo + st * (L::kTile >> 4) + (i & 1) * (kHalfStep * 128 >> 4);
+            const uint32_t a_t = s_at + (i & 1) * kHalfStep;
+#pragma unroll
+            for (int ks = 0; ks < kHalfStep / 16; ++ks)
+              mma_ts(o_at, a_t + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO,
+                     ks > 0 ? 1u : (uint32_t)(i > 0 || poisoned));
+            mma_commit(&sh.pv_done[t]);
+            if (i & 1) {
+              mma_commit(&sh.empty[st]);
+              if (!two) mma_commit(&sh.empty[st]);
+            }
+            if (i + 1 == n_halves) mma_commit(&sh.o_done[t]);
+          }
+          __syncwarp();
         }
-        all += p.t1 - p.t0;
+        if (two) full_ph[0] = ph;
+        else full_ph[1] = ph;
+        halves += n_halves;
+        all += n;
         ++pieces;
       }
       // none of its MMAs is in flight when the CTA's memory goes to another
