@@ -21,9 +21,9 @@ constexpr int kChunkThreads = 512;
 constexpr int kPieces = 4;    // pieces that are known ahead
 constexpr int kMasks = 8;     // steps whose token masks are kept
 constexpr int kHalfStep = kTileTokens / 2;  // tokens of one product
-// warps: the softmax of each tile, the factors and outputs of both, then one each for
-// the tiles' MMAs, the copies of K and V, and the pieces with their rows of Q
-constexpr int kCorrWarp = 8, kMma0Warp = 12, kKvWarp = 14, kPieceWarp = 15;
+// warps: the softmax of each tile; then one each for the tiles' scores, the tiles'
+// products, the copies of K and V of even and of odd steps, the pieces and their Q
+constexpr int kScoreWarp = 8, kProductWarp = 10, kKvWarp = 12, kPieceWarp = 14;
 
 // ---- the units ----------------------------------------------------------------
 // Heads in one tile: a.heads of the G, a.parts times; tokens in one tile: a.tokens.  A
@@ -215,18 +215,15 @@ struct Shared {
   // its barriers, so that a phase's parity says which it is)
   uint64_t full[2][R], empty[R];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
-  // of each tile, by halves of a step: scores made; weights stored
-  uint64_t s_full[2][2], p_full[2][2];
-  // of each tile: product of a half done; product of a unit done; sums posted; accumulator
-  // read
-  uint64_t pv_done[2], o_done[2], l_full[2], o_empty[2];
-  // of each tile, at a chunk's diagonal: V there; V looked through; weights of a half
-  // with poisoned values stored and the product before it done; those added
-  uint64_t v_there[2], v_ok[2], pv_poison[2], fixed[2];
+  // of each tile, by halves of a step: scores made; weights stored; product done
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];
+  // of each tile: products of a unit done; accumulator read
+  uint64_t o_done[2], o_empty[2];
+  uint64_t v_ok[2][4];               // of each tile, by turns: V of a step looked through
   uint64_t x_full;                   // tile 1's sums of a unit that the tiles share, for tile 0
   uint64_t q_full[2], q_empty[2];
-  uint64_t drained[2];
-  float inv[2][kTileRows];
+  uint64_t drained[4];
+  float sums[2][kTileRows];         // those: maxima, sums
   Piece piece[kPieces];
   uint32_t mask[kMasks][4];
   int32_t whole[kMasks];
@@ -266,17 +263,6 @@ __device__ __forceinline__ uint64_t mul_f2(uint64_t x, uint64_t y) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   return r;
 }
-// 16 columns of this thread's lane
-__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : VT_R8(r, 0), VT_R8(r, 8)
-      : "r"(addr));
-}
-__device__ __forceinline__ void loaded16(uint32_t (&r)[16]) {
-  asm volatile("" : VT_P8(r, 0), VT_P8(r, 8)::"memory");
-}
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t addr) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr));
@@ -299,6 +285,44 @@ __device__ __forceinline__ uint32_t not_finite(const uint4& v) {
   constexpr uint32_t kExp = kBf ? 0x7f807f80u : 0x7c007c00u, kOne = kBf ? 0x00800080u : 0x04000400u;
   return (((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) | ((v.z & kExp) + kOne) |
           ((v.w & kExp) + kOne)) & 0x80008000u;
+}
+
+// O += P V of this thread's row for the tokens of a half that V no longer holds (bits of
+// w0, w1: token tok0 + bit); O = that where it is not begun.
+template <typename T, int D>
+__device__ __noinline__ void add_poison(const ChunkArgs& a, const Piece& p, uint32_t w0,
+                                        uint32_t w1, int tok0, int lim, bool begun, uint32_t p_at,
+                                        uint32_t o_at) {
+  if (!begun) {
+    uint32_t o[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = 0;
+    for (int c = 0; c < D; c += 32) tmem_st32(o_at + c, o);
+    tmem_wait_st();
+  }
+  for (int q = 0; q < 2; ++q)
+    for (uint32_t left = q ? w1 : w0; left; left &= left - 1) {
+      const int i = q * 32 + __ffs(left) - 1, tok = tok0 + i;
+      const uint32_t pair = tmem_ld1(p_at + i / 2);
+      const unsigned short bits = (unsigned short)(i & 1 ? pair >> 16 : pair);
+      const float weight = static_cast<float>(*reinterpret_cast<const T*>(&bits));
+      const int blk = a.table[(int64_t)p.b * a.ld_table + (tok >> a.shift)];
+      const T* v = static_cast<const T*>(a.v) + blk * a.block_stride +
+                   (tok & ((1 << a.shift) - 1)) * a.token_stride + p.kvh * a.head_stride;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(o, o_at + c);
+        tmem_wait_ld();
+        loaded(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (tok < lim)
+            o[e] = __float_as_uint(__uint_as_float(o[e]) + weight * static_cast<float>(v[c + e]));
+        tmem_st32(o_at + c, o);
+        tmem_wait_st();
+      }
+    }
 }
 
 template <typename T, int D>
@@ -330,29 +354,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&sh.piece_full[i], 1);
-      mbar_init(&sh.piece_empty[i], kPieceWarp);  // (every other warp)
+      mbar_init(&sh.piece_empty[i], kPieceWarp);  // (every warp before that)
     }
     for (int t = 0; t < 2; ++t) {
       for (int h = 0; h < 2; ++h) {
         mbar_init(&sh.s_full[t][h], 1);
         mbar_init(&sh.p_full[t][h], 4);
+        mbar_init(&sh.pv_done[t][h], 1);
       }
-      mbar_init(&sh.pv_done[t], 1);
       mbar_init(&sh.o_done[t], 1);
-      mbar_init(&sh.l_full[t], 4);
       mbar_init(&sh.o_empty[t], 4);
-      mbar_init(&sh.v_there[t], 1);
-      mbar_init(&sh.v_ok[t], 4);
-      mbar_init(&sh.pv_poison[t], 1);
-      mbar_init(&sh.fixed[t], 4);
+      for (int i = 0; i < 4; ++i) mbar_init(&sh.v_ok[t][i], 4);
       mbar_init(&sh.q_full[t], 1);
       mbar_init(&sh.q_empty[t], 1);
-      mbar_init(&sh.drained[t], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.drained[i], 1);
     mbar_init(&sh.x_full, 4);
     fence_mbar_init();
   }
-  if (warp == kMma0Warp) {
+  if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_addr(&sh.tmem))
                  : "memory");
@@ -382,16 +402,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int in = tid & (kTileRows - 1), in_token = in / a.heads, in_head = in % a.heads;
   const int cap = a.cols << a.shift;
 
-  if (warp < kCorrWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    // ---- softmax: a warpgroup to a tile, one thread to a row ---------------------------
+  if (warp < kScoreWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    // ---- softmax and outputs: a warpgroup to a tile, one thread to a row -----------------
     const int t = warp >> 2;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane (warp % 4) * 32
     // (a scale of 0 as one that leaves masked scores at -inf)
     const float sc = fmaxf(fabsf(a.scale_log2), 1e-30f);
     const uint64_t sc2 = pack_f2(sc, sc);
-    uint32_t steps = 0, sums = 0, shared = 0;  // of this tile
-    int n_masks = 0;
+    // this tile's steps; units, and those that the tiles share; the CTA's steps; of the
+    // ring's places by set and of v_ok, the parities of their uses
+    uint32_t steps = 0, units = 0, shared = 0, all = 0, full_ph[2] = {0, 0}, ok_ph = 0;
     Piece p;
     while (ok && next_piece(p)) {
       const bool two = p.tokens > a.tokens;  // else the tiles share the unit
@@ -400,21 +421,60 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const bool warp_live = __any_sync(0xffffffffu, live);
       const int lim = live ? min(max(p.lim0 + token, 0), cap) : 0;
       const int lim_min = __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff);
+      const int n = p.t1 - p.t0;
       float m = -INFINITY, l = 0.f;
       bool begun = false;  // (a product has been added to the accumulator)
-      for (int j = two ? p.t0 : p.t0 + ((n_masks ^ t) & 1); j < p.t1 && ok;
+      bool poisoned = false;
+      for (int j = two ? p.t0 : p.t0 + ((all ^ t) & 1); j < p.t1 && ok;
            j += two ? 1 : 2, ++steps) {
-        const int ring = (n_masks + j - p.t0) % kMasks;
+        const uint32_t g = all + (j - p.t0);
+        const int ring = g % kMasks;
+        // Some row does not attend to the whole step: its weights there are 0, but 0
+        // times an infinity or a NaN is NaN.
+        const bool diagonal = (j + 1) * kTileTokens > max(p.lim0, 0);
+        poisoned = false;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           ok = warp_wait(&sh.s_full[t][h], steps & 1, limit);
           if (!ok) break;
           fence_after();
+          if (diagonal && h == 0 && (t == 0 || !two)) {
+            // Tokens of V that are not finite are taken out of it.  (The scores are there,
+            // so the last V of this place has been used; this piece's uses before it.)
+            const int st = place<R>(g, 1);
+            const uint32_t ph = ((two ? full_ph[0] : full_ph[1]) >> st) + (j - p.t0) / (R / 2);
+            ok = warp_wait(&sh.full[!two][st], ph & 1, limit);
+            if (!ok) break;
+            uint4* row = reinterpret_cast<uint4*>(dyn + L::kKv + st * L::kTile + in * 128);
+            uint32_t bad = 0;
+#pragma unroll
+            for (int q = 0; q < D / 64; ++q)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                bad |= not_finite<T>(row[q * (L::kHalf / 16) + ((c + in) & 7)]);
+            if (bad) {
+#pragma unroll
+              for (int q = 0; q < D / 64; ++q)
+                for (int c = 0; c < 8; ++c)
+                  row[q * (L::kHalf / 16) + ((c + in) & 7)] = make_uint4(0, 0, 0, 0);
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            const uint32_t word =
+                __ballot_sync(0xffffffffu, bad && j * kTileTokens + in < p.end);
+            if (lane == 0) sh.poison[g & 3][warp & 3] = word;
+            warp_arrive(&sh.v_ok[t][g & 3]);
+            if (two) warp_arrive(&sh.v_ok[1][g & 3]);
+          }
+          const uint32_t ts = tmem + lanes + t * kTileTokens + h * kHalfStep;
           if (!warp_live) {  // (the products of these rows are never read)
+            if (diagonal && h == 0) {
+              ok = warp_wait(&sh.v_ok[t][g & 3], (ok_ph >> (g & 3)) & 1, limit);
+              ok_ph ^= 1u << (g & 3);
+              if (!ok) break;
+            }
             warp_arrive(&sh.p_full[t][h]);
             continue;
           }
-          const uint32_t ts = tmem + lanes + t * kTileTokens + h * kHalfStep;
           uint32_t s[2][32];
           tmem_ld32(s[0], ts);
           tmem_ld32(s[1], ts + 32);
@@ -458,7 +518,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (grow) m = top;
             l *= f;
             if (begun) {
-              ok = warp_wait(&sh.pv_done[t], (2 * steps + h - 1) & 1, limit);
+              ok = warp_wait(&sh.pv_done[t][h ^ 1], (h ? steps : steps - 1) & 1, limit);
               if (!ok) break;
               fence_after();
               const uint32_t o_at = tmem + lanes + kO + t * D;
@@ -481,7 +541,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               }
             }
           }
-          begun = true;
           const float off = m == -INFINITY ? 0.f : -m;
           const uint64_t off2 = pack_f2(off, off);
           uint64_t sum[2] = {0, 0};
@@ -505,151 +564,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           unpack_f2(add_f2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
           tmem_wait_st();
+          if (diagonal) {
+            if (h == 0) {
+              ok = warp_wait(&sh.v_ok[t][g & 3], (ok_ph >> (g & 3)) & 1, limit);
+              ok_ph ^= 1u << (g & 3);
+              if (!ok) break;
+              // (written again four steps on, behind a product that waits for this warp)
+              const uint32_t* words = sh.poison[g & 3];
+              poisoned = (words[0] | words[1] | words[2] | words[3]) != 0;
+            }
+            if (poisoned) {
+              // what was taken out of V, for the rows that attend to it, added in front of
+              // the half's product
+              ok = begun ? warp_wait(&sh.pv_done[t][h ^ 1], (h ? steps : steps - 1) & 1, limit)
+                         : warp_wait(&sh.o_empty[t], (units & 1) ^ 1, limit);
+              if (!ok) break;
+              fence_after();
+              add_poison<T, D>(a, p, sh.poison[g & 3][h * 2], sh.poison[g & 3][h * 2 + 1], tok0, lim,
+                               begun, ts, tmem + lanes + kO + t * D);
+            }
+          }
+          begun = true;
           fence_before();
           warp_arrive(&sh.p_full[t][h]);
         }
-      }
-      n_masks += p.t1 - p.t0;
-      if (!ok) break;
-      // the rows' sums; those of the last piece have been read
-      ok = warp_wait(&sh.o_empty[t], (sums & 1) ^ 1, limit);
-      ++sums;
-      if (!ok) break;
-      if (two) {
-        sh.inv[t][in] = l == 0.f ? 0.f : p.slot >= 0 ? 1.f : 1.f / l;
-      } else if (t == 1) {
-        sh.inv[0][in] = m;
-        sh.inv[1][in] = l;
-        warp_arrive(&sh.x_full);
-        continue;
-      } else {
-        ok = warp_wait(&sh.x_full, shared & 1, limit);
-        ++shared;
-        if (!ok) break;
-        const float m1 = sh.inv[0][in], l1 = sh.inv[1][in];
-        const float mm = fmaxf(m, m1), base = mm == -INFINITY ? 0.f : mm;
-        const float f0 = ex2_approx(m - base), f1 = ex2_approx(m1 - base);
-        l = l * f0 + l1 * f1;
-        m = mm;
-        const float inv = l == 0.f ? 0.f : p.slot >= 0 ? 1.f : 1.f / l;
-        sh.inv[0][in] = f0 * inv;
-        sh.inv[1][in] = f1 * inv;
-      }
-      warp_arrive(&sh.l_full[t]);
-      if (!live) continue;
-      if (p.slot >= 0)
-        a.part_ml[(int64_t)p.slot * kUnitRows + (two ? t * kTileRows : 0) + in] = make_float2(m, l);
-      else if (a.lse)
-        a.lse[(int64_t)(p.token + token) * a.hq + p.head + in_head] =
-            l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-    }
-  } else if (warp < kMma0Warp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    // ---- the accumulators: mended, written -----------------------------------------------
-    const int w = warp & 3;
-    const uint32_t lanes = (uint32_t)w << 21;
-    // units; bit t: the parity of tile t's sums, its steps at a diagonal, its poisoned
-    // halves; the CTA's steps; of the ring's places by set, the parity of their uses
-    uint32_t units = 0, sum_ph = 0, diag_ph = 0, poison_ph = 0, all = 0, full_ph[2] = {0, 0};
-    Piece p;
-    while (ok && next_piece(p)) {
-      const bool two = p.tokens > a.tokens;
-      const bool here = in_token < a.tokens && in_head < p.heads;
-      // bit t: tile t's row is one of the unit's; the warp has such rows
-      const uint32_t live = (here && in_token < p.tokens ? 1u : 0u) |
-                            (here && in_token + (two ? a.tokens : 0) < p.tokens ? 2u : 0u);
-      const uint32_t warp_live = __reduce_or_sync(0xffffffffu, live);
-      const int n = p.t1 - p.t0;
-      // The steps that some row does not attend to the whole of: its weights there are 0,
-      // but 0 times an infinity or a NaN is NaN
-      const int diagonal = max(p.t0, max(p.lim0, 0) / kTileTokens);
-      for (int j = diagonal; j < p.t1 && ok; ++j) {
-        const int tok0 = j * kTileTokens;
-        const uint32_t g = all + (j - p.t0);
-        const int from = two ? 0 : g & 1, to = two ? 2 : from + 1;  // tiles
-        uint32_t bad = 0;
-        for (int t = from; t < to; ++t) {
-          ok = warp_wait(&sh.v_there[t], (diag_ph >> t) & 1, limit);
-          if (!ok) break;
-          if (t == from) {
-            const int st = place<R>(g, 1);
-            // (uses of the place before this one in this piece)
-            const uint32_t before = (uint32_t)(j - p.t0) / (R / 2);
-            const uint32_t ph = ((!two ? full_ph[1] : full_ph[0]) >> st) + before;
-            ok = warp_wait(&sh.full[!two][st], ph & 1, limit);
-            if (!ok) break;
-            uint4* row = reinterpret_cast<uint4*>(dyn + L::kKv + st * L::kTile + in * 128);
-            const bool behind = tok0 + in >= p.end;
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                bad |= not_finite<T>(row[h * (L::kHalf / 16) + ((c + in) & 7)]);
-            if (bad) {
-#pragma unroll
-              for (int h = 0; h < D / 64; ++h)
-                for (int c = 0; c < 8; ++c)
-                  row[h * (L::kHalf / 16) + ((c + in) & 7)] = make_uint4(0, 0, 0, 0);
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            }
-            const uint32_t word = __ballot_sync(0xffffffffu, bad && !behind);
-            if (lane == 0) sh.poison[g & 3][w] = word;
-          }
-          warp_arrive(&sh.v_ok[t]);
-        }
-        if (!ok) break;
-        ok = warp_wait(&sh.v_ok[from], (diag_ph >> from) & 1, limit);
-        if (!ok) break;
-        for (int t = from; t < to; ++t) diag_ph ^= 1u << t;
-        // (written again four steps on, which no warp reaches before all are here)
-        const uint32_t* words = sh.poison[g & 3];
-        if ((words[0] | words[1] | words[2] | words[3]) == 0) continue;
-        // what was taken out of V, for the rows that attend to it
-        for (int h = 0; h < 2 && ok; ++h)
-          for (int t = from; t < to; ++t) {
-            ok = warp_wait(&sh.pv_poison[t], (poison_ph >> t) & 1, limit);
-            if (!ok) break;
-            poison_ph ^= 1u << t;
-            fence_after();
-            const int lim =
-                (live >> t) & 1 ? min(max(p.lim0 + (two ? t * a.tokens : 0) + in_token, 0), cap) : 0;
-            const uint32_t s_at = tmem + lanes + t * kTileTokens + h * kHalfStep,
-                           o_at = tmem + lanes + kO + t * D;
-            if (h == 0 && j - p.t0 < (two ? 1 : 2)) {  // (the product would have begun it)
-              uint32_t o[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0;
-              for (int c = 0; c < D; c += 32) tmem_st32(o_at + c, o);
-              tmem_wait_st();
-            }
-            for (int q = 0; q < 2; ++q)
-              for (uint32_t left = words[h * 2 + q]; left; left &= left - 1) {
-                const int i = q * 32 + __ffs(left) - 1, tok = tok0 + h * kHalfStep + i;
-                const uint32_t pair = tmem_ld1(s_at + i / 2);
-                const unsigned short bits = (unsigned short)(i & 1 ? pair >> 16 : pair);
-                const float weight = static_cast<float>(*reinterpret_cast<const T*>(&bits));
-                const int blk = a.table[(int64_t)p.b * a.ld_table + (tok >> a.shift)];
-                const T* v = static_cast<const T*>(a.v) + blk * a.block_stride +
-                             (tok & ((1 << a.shift) - 1)) * a.token_stride +
-                             p.kvh * a.head_stride;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                  uint32_t o[32];
-                  tmem_ld32(o, o_at + c);
-                  tmem_wait_ld();
-                  loaded(o);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (tok < lim)
-                      o[e] = __float_as_uint(__uint_as_float(o[e]) +
-                                             weight * static_cast<float>(v[c + e]));
-                  tmem_st32(o_at + c, o);
-                  tmem_wait_st();
-                }
-              }
-            fence_before();
-            warp_arrive(&sh.fixed[t]);
-          }
       }
       if (!ok) break;
       for (int c = 0; c < R / 2; ++c) {  // uses of V's places: every (R / 2)-th step each
@@ -659,72 +597,99 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         else full_ph[1] ^= flip;
       }
       all += n;
-      for (int t = 0; t < (two ? 2 : 1); ++t) {
-        // tiles that share the unit: both at once, if both had steps
-        ok = warp_wait(&sh.l_full[t], (sum_ph >> t) & 1, limit);
-        const bool both = !two && n > 1;
-        const int one = two ? t : (all - 1) & 1;  // (the last step's)
-        for (int u = two ? t : 0; u < (two ? t + 1 : 2) && ok; ++u)
-          ok = warp_wait(&sh.o_done[u], units & 1, limit);
-        if (!ok) break;
-        fence_after();
-        if ((warp_live >> t) & 1) {
-          const float inv = sh.inv[one][in], inv1 = sh.inv[one ^ 1][in];
-          const uint32_t o_at = tmem + lanes + kO + one * D;
-          const uint32_t o1_at = tmem + lanes + kO + (one ^ 1) * D;
-          const int token = p.token + (two ? t * a.tokens : 0) + in_token;
-          T* out = static_cast<T*>(a.out) + ((int64_t)token * a.hq + p.head + in_head) * D;
-          float* part = a.part_o + ((int64_t)max(p.slot, 0) * kUnitRows + t * kTileRows + in) * D;
-          constexpr int kCols = 16;
-#pragma unroll 1
-          for (int c = 0; c < D; c += kCols) {
-            uint32_t o[kCols];
-            tmem_ld16(o, o_at + c);
-            if (both) {
-              uint32_t o1[kCols];
-              tmem_ld16(o1, o1_at + c);
-              tmem_wait_ld();
-              loaded16(o);
-              loaded16(o1);
-#pragma unroll
-              for (int i = 0; i < kCols; ++i)
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * inv +
-                                       __uint_as_float(o1[i]) * inv1);
-            } else {
-              tmem_wait_ld();
-              loaded16(o);
-#pragma unroll
-              for (int i = 0; i < kCols; ++i)
-                o[i] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-            }
-            if (!((live >> t) & 1)) continue;
-            if (p.slot >= 0) {
-#pragma unroll
-              for (int i = 0; i < kCols; i += 4)
-                *reinterpret_cast<uint4*>(part + c + i) =
-                    make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < kCols; i += 8)
-                *reinterpret_cast<uint4*>(out + c + i) = make_uint4(
-                    pack2<T>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
-                    pack2<T>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
-                    pack2<T>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])),
-                    pack2<T>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
-            }
-          }
-          fence_before();
-        }
-        sum_ph ^= 1u << t;
-        warp_arrive(&sh.o_empty[t]);
-        if (!two) warp_arrive(&sh.o_empty[1]);
+      // (every unit's, so that a parity is the last unit's)
+      ok = warp_wait(&sh.o_empty[t], (units & 1) ^ 1, limit);
+      if (!ok) break;
+      if (!two && t == 1) {
+        sh.sums[0][in] = m;
+        sh.sums[1][in] = l;
+        warp_arrive(&sh.x_full);
+        ++units;
+        continue;
       }
+      // factors of the two accumulators of a unit that the tiles share; of this tile's
+      float f0 = 1.f, f1 = 0.f;
+      const bool both = !two && n > 1;  // (both had steps)
+      int one = t;                      // the tile of the only accumulator, or the first
+      if (!two) {
+        ok = warp_wait(&sh.x_full, shared & 1, limit);
+        ++shared;
+        if (!ok) break;
+        const float m1 = sh.sums[0][in], l1 = sh.sums[1][in];
+        const float mm = fmaxf(m, m1), base = mm == -INFINITY ? 0.f : mm;
+        f0 = ex2_approx(m - base);
+        f1 = ex2_approx(m1 - base);
+        l = l * f0 + l1 * f1;
+        m = mm;
+        if (!both) {
+          one = (all - 1) & 1;
+          f0 = one ? f1 : f0;
+        }
+      }
+      // the rows: whole ones divided by their sums, parts as they are
+      const float inv = l == 0.f ? 0.f : p.slot >= 0 ? 1.f : 1.f / l;
+      f0 *= inv;
+      f1 *= inv;
+      ok = warp_wait(&sh.o_done[t], units & 1, limit);
+      if (ok && !two) ok = warp_wait(&sh.o_done[1], units & 1, limit);
+      if (!ok) break;
       ++units;
+      fence_after();
+      const int64_t row = (int64_t)(p.token + token) * a.hq + p.head + in_head;
+      const int64_t part = (int64_t)max(p.slot, 0) * kUnitRows + (two ? t * kTileRows : 0) + in;
+      if (warp_live) {
+        const uint32_t o_at = tmem + lanes + kO + one * D;
+        T* out = static_cast<T*>(a.out) + row * D;
+        float* part_o = a.part_o + part * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o, o_at + c);
+          if (both) {
+            uint32_t o1[32];
+            tmem_ld32(o1, o_at + D + c);
+            tmem_wait_ld();
+            loaded(o);
+            loaded(o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * f0 + __uint_as_float(o1[i]) * f1);
+          } else {
+            tmem_wait_ld();
+            loaded(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = f0 == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * f0);
+          }
+          if (!live) continue;
+          if (p.slot >= 0) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<uint4*>(part_o + c + i) =
+                  make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4*>(out + c + i) = make_uint4(
+                  pack2<T>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                  pack2<T>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
+                  pack2<T>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])),
+                  pack2<T>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
+          }
+        }
+        fence_before();
+      }
+      warp_arrive(&sh.o_empty[t]);
+      if (!two) warp_arrive(&sh.o_empty[1]);
+      if (!live) continue;
+      if (p.slot >= 0) a.part_ml[part] = make_float2(m, l);
+      else if (a.lse) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == kKvWarp) {
-      // ---- keys and values, tile by tile ------------------------------------------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == kKvWarp || warp == kKvWarp + 1) {
+      // ---- keys and values of even steps, of odd steps --------------------------------------
+      const int odd = warp - kKvWarp;
       const int box = min(1 << a.shift, kTileTokens);  // tokens of a copy
       const int boxes = kTileTokens / box;
       uint32_t all = 0;
@@ -735,7 +700,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       while (ok && next_piece(p)) {
         const int32_t* table = a.table + (int64_t)p.b * a.ld_table;
         const int set = p.tokens <= a.tokens;  // (the tiles share the unit)
-        for (int j = p.t0; j < p.t1 && ok; ++j, ++all) {
+        for (int j = p.t0 + ((all ^ odd) & 1); j < p.t1 && ok; j += 2) {
+          const uint32_t g = all + (j - p.t0);
           const int tok0 = j * kTileTokens;
           // the blocks of this tile, up to 16 of them: one a lane
           const int tok = tok0 + lane * box;
@@ -755,14 +721,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             const int left = p.end - tok0 - lane * 32;
             m &= left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1;
-            sh.mask[all % kMasks][lane] = m;
+            sh.mask[g % kMasks][lane] = m;
             const unsigned every = __ballot_sync(0xfu, m == 0xffffffffu);
-            if (lane == 0) sh.whole[all % kMasks] = every == 0xfu;
+            if (lane == 0) sh.whole[g % kMasks] = every == 0xfu;
           }
           __syncwarp();
           const int in_block = tok0 & ((1 << a.shift) - 1);  // (blocks longer than a tile)
           for (int kv = 0; kv < 2; ++kv) {
-            const int st = place<R>(all, kv);
+            const int st = place<R>(g, kv);
             ok = warp_wait(&sh.empty[st], ((empty_ph >> st) & 1) ^ 1, limit);
             if (!ok) break;
             empty_ph ^= 1u << st;
@@ -778,6 +744,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                          kv ? &map_v : &map_k, bar, h * 64, in_block, p.kvh, blk);
           }
         }
+        all += p.t1 - p.t0;
       }
       // no copy is in flight when the CTA's memory goes to another
       for (int i = 0; i < 2 * R; ++i)  // (the last use of each)
@@ -862,8 +829,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // no copy is in flight when the CTA's memory goes to another
       for (int t = 0; t < 2; ++t)
         if (uses[t] > 0) mbar_wait_clocked(&sh.q_full[t], (uses[t] - 1) & 1, kDrainCycles);
-    } else {
-      // ---- MMAs: a warp to a tile walks the steps and waits; one lane issues ----------------
+    } else if (warp < kKvWarp) {
+      // ---- MMAs: a warp to a tile's scores, another to its products, walk the halves of its
+      // steps and wait; one lane issues
       constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
       // fp32 accumulators; K-major A and B; N = 64 tokens, M = 128
       constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) |
@@ -872,121 +840,105 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       constexpr uint32_t kIdescO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) |
                                    ((uint32_t)(D / 8) << 17) | ((kTileRows / 16) << 24);
       constexpr uint32_t kHi = desc_hi(1024);
-      const int t = warp - kMma0Warp;
-      const uint32_t a_lo = desc_lo(base + L::kQ + t * L::kTile, 16),
+      const int t = warp & 1;
+      const bool product = warp >= kProductWarp;
+      const uint32_t q_lo = desc_lo(base + L::kQ + t * L::kTile, 16),
                      k_lo = desc_lo(base + L::kKv, 16), v_lo = desc_lo(base + L::kKv, L::kHalf);
       const uint32_t s_at = tmem + t * kTileTokens, o_at = tmem + kO + t * D;
-      // halves of a step, units, steps at a diagonal, poisoned halves, of this tile; the
-      // CTA's steps; of the ring's places by set, the parities of their uses
-      uint32_t halves = 0, pieces = 0, diagonals = 0, fixes = 0, all = 0, full_ph[2] = {0, 0};
+      // steps and units of this tile; the CTA's steps; of the ring's places by set, the
+      // parities of their uses
+      uint32_t steps = 0, units = 0, all = 0, full_ph[2] = {0, 0};
       Piece p;
       while (ok && next_piece(p)) {
         const bool two = p.tokens > a.tokens;
-        const int set = !two, first = two ? 0 : (all ^ t) & 1, by = two ? 1 : 2;
-        const int n = p.t1 - p.t0;
-        const int n_halves = 2 * ((n - first + by - 1) / by);  // (n - first may be 0)
+        const int first = two ? 0 : (all ^ t) & 1, by = two ? 1 : 2, n = p.t1 - p.t0;
         uint32_t ph = two ? full_ph[0] : full_ph[1];
-        ok = warp_wait(&sh.q_full[t], pieces & 1, limit);
-        if (ok && n_halves == 0) {
-          if (elect_one()) mma_commit(&sh.q_empty[t]);
-          __syncwarp();
-          // (every unit's waits and arrivals, so that a parity is the last unit's)
-          ok = warp_wait(&sh.o_empty[t], (pieces & 1) ^ 1, limit);
-          if (ok) warp_arrive(&sh.o_done[t]);
+        // (every unit's waits and arrivals, so that a parity is the last unit's)
+        if (product) ok = warp_wait(&sh.o_empty[t], (units & 1) ^ 1, limit);
+        else ok = warp_wait(&sh.q_full[t], units & 1, limit);
+        if (ok && first >= n) {
+          if (product) {
+            warp_arrive(&sh.o_done[t]);
+          } else {
+            warp_arrive(&sh.q_empty[t]);
+          }
         }
-        bool poisoned = false;
 #pragma unroll 1
-        for (int i = -1; i < n_halves && ok; ++i) {
-          const int k = i + 1;
-          // The product with the P that lies where the next scores go is done.  (Waited for
-          // behind the last scores too: each product's phase in turn.  The next unit's
-          // first scores need no wait of their own.)
-          if (k > 0 && halves + k >= 2) ok = warp_wait(&sh.pv_done[t], (halves + k) & 1, limit);
+        for (int j = first; j < n && ok; j += by, ++steps) {
+          const int st = place<R>(all + j, product);
+          ok = warp_wait(&sh.full[!two][st], (ph >> st) & 1, limit);
+          ph ^= 1u << st;
           if (!ok) break;
-          if (k < n_halves) {  // S = Q K^T of the next half
-            const int st = place<R>(all + first + (k >> 1) * by, 0);
-            if (!(k & 1)) {
-              ok = warp_wait(&sh.full[set][st], (ph >> st) & 1, limit);
-              ph ^= 1u << st;
-            }
-            if (!ok) break;
-            fence_after();
-            if (elect_one()) {
-              const uint32_t b_lo = k_lo + st * (L::kTile >> 4) + (k & 1) * (kHalfStep * 128 >> 4);
-              const uint32_t d = s_at + (k & 1) * kHalfStep;
+          const uint32_t tile = st * (L::kTile >> 4);
+          if (!product) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {  // S = Q K^T
+              // the product with the P that lies there is done
+              if (steps > 0) ok = warp_wait(&sh.pv_done[t][h], (steps - 1) & 1, limit);
+              if (!ok) break;
+              fence_after();
+              if (elect_one()) {
+                const uint32_t b_lo = k_lo + tile + h * (kHalfStep * 128 >> 4);
+                const uint32_t d = s_at + h * kHalfStep;
 #pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = ((ks / 4) * L::kHalf + (ks % 4) * 32) >> 4;
-                mma_ss(d, a_lo + off, b_lo + off, kHi, kIdescS, ks > 0);
+                for (int ks = 0; ks < D / 16; ++ks) {
+                  const uint32_t off = ((ks / 4) * L::kHalf + (ks % 4) * 32) >> 4;
+                  mma_ss(d, q_lo + off, b_lo + off, kHi, kIdescS, ks > 0);
+                }
+                mma_commit(&sh.s_full[t][h]);
+                if (h) {
+                  mma_commit(&sh.empty[st]);
+                  if (!two) mma_commit(&sh.empty[st]);
+                  if (j + by >= n) mma_commit(&sh.q_empty[t]);
+                }
               }
-              mma_commit(&sh.s_full[t][k & 1]);
-              if (k & 1) {
-                mma_commit(&sh.empty[st]);
-                if (!two) mma_commit(&sh.empty[st]);
+              __syncwarp();
+            }
+          } else {
+            bool poisoned = false;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {  // O += P V
+              ok = warp_wait(&sh.p_full[t][h], steps & 1, limit);
+              if (!ok) break;
+              if (j == first && (p.t0 + j + 1) * kTileTokens > max(p.lim0, 0)) {
+                const uint32_t* words = sh.poison[(all + j) & 3];
+                poisoned = (words[0] | words[1] | words[2] | words[3]) != 0;
               }
-              if (k + 1 == n_halves) mma_commit(&sh.q_empty[t]);
-            }
-            __syncwarp();
-          }
-          if (i < 0) continue;
-          const int j = first + (i >> 1) * by;  // of the piece
-          const int st = place<R>(all + j, 1);
-          if (!(i & 1)) {
-            ok = warp_wait(&sh.full[set][st], (ph >> st) & 1, limit);
-            ph ^= 1u << st;
-            poisoned = false;
-            if (ok && (p.t0 + j + 1) * kTileTokens > max(p.lim0, 0)) {
-              warp_arrive(&sh.v_there[t]);
-              ok = warp_wait(&sh.v_ok[t], diagonals & 1, limit);
-              ++diagonals;
-              const uint32_t* words = sh.poison[(all + j) & 3];
-              poisoned = (words[0] | words[1] | words[2] | words[3]) != 0;
-            }
-          }
-          // the accumulator of the last unit has been read
-          if (ok && i == 0) ok = warp_wait(&sh.o_empty[t], (pieces & 1) ^ 1, limit);
-          if (ok) ok = warp_wait(&sh.p_full[t][i & 1], ((halves + i) >> 1) & 1, limit);
-          if (!ok) break;
-          fence_after();
-          if (poisoned) {  // (what was taken out of V is added first, behind the last product)
-            warp_arrive(&sh.pv_poison[t]);
-            ok = warp_wait(&sh.fixed[t], fixes & 1, limit);
-            ++fixes;
-            if (!ok) break;
-            fence_after();
-          }
-          if (elect_one()) {  // O += P V
-            const uint32_t b_lo = v_lo + st * (L::kTile >> 4) + (i & 1) * (kHalfStep * 128 >> 4);
-            const uint32_t a_t = s_at + (i & 1) * kHalfStep;
+              fence_after();
+              if (elect_one()) {
+                const uint32_t b_lo = v_lo + tile + h * (kHalfStep * 128 >> 4);
+                const uint32_t a_t = s_at + h * kHalfStep;
 #pragma unroll
-            for (int ks = 0; ks < kHalfStep / 16; ++ks)
-              mma_ts(o_at, a_t + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO,
-                     ks > 0 ? 1u : (uint32_t)(i > 0 || poisoned));
-            mma_commit(&sh.pv_done[t]);
-            if (i & 1) {
-              mma_commit(&sh.empty[st]);
-              if (!two) mma_commit(&sh.empty[st]);
+                for (int ks = 0; ks < kHalfStep / 16; ++ks)
+                  mma_ts(o_at, a_t + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO,
+                         ks > 0 ? 1u : (uint32_t)(j > first || h > 0 || poisoned));
+                mma_commit(&sh.pv_done[t][h]);
+                if (h) {
+                  mma_commit(&sh.empty[st]);
+                  if (!two) mma_commit(&sh.empty[st]);
+                  if (j + by >= n) mma_commit(&sh.o_done[t]);
+                }
+              }
+              __syncwarp();
             }
-            if (i + 1 == n_halves) mma_commit(&sh.o_done[t]);
           }
-          __syncwarp();
         }
         if (two) full_ph[0] = ph;
         else full_ph[1] = ph;
-        halves += n_halves;
         all += n;
-        ++pieces;
+        ++units;
       }
       // none of its MMAs is in flight when the CTA's memory goes to another
-      if (elect_one()) mma_commit(&sh.drained[t]);
+      uint64_t* drained = &sh.drained[warp - kScoreWarp];
+      if (elect_one()) mma_commit(drained);
       __syncwarp();
-      mbar_wait_clocked(&sh.drained[t], 0, kDrainCycles);
+      mbar_wait_clocked(drained, 0, kDrainCycles);
     }
   }
   if (!ok) atomicOr(a.err_word, kErrTimeout);
   fence_before();
   __syncthreads();
-  if (warp == kMma0Warp)
+  if (warp == kScoreWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
