@@ -263,6 +263,15 @@ __device__ __forceinline__ uint64_t mul_f2(uint64_t x, uint64_t y) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   return r;
 }
+// 32 columns of this thread's lane and their maximum, NaN left out
+__device__ __forceinline__ void tmem_ld32_max(uint32_t (&r)[32], uint32_t& top, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,"
+      "%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
+      : VT_R8(r, 0), VT_R8(r, 8), VT_R8(r, 16), VT_R8(r, 24), "=r"(top)
+      : "r"(addr));
+}
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t addr) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr));
@@ -476,19 +485,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             continue;
           }
           uint32_t s[2][32];
-          tmem_ld32(s[0], ts);
-          tmem_ld32(s[1], ts + 32);
+          uint32_t top0, top1;
+          tmem_ld32_max(s[0], top0, ts);
+          tmem_ld32_max(s[1], top1, ts + 32);
           tmem_wait_ld();
           loaded(s[0]);
           loaded(s[1]);
+          asm volatile("" : "+r"(top0), "+r"(top1)::"memory");
+          float top = fmaxf(__uint_as_float(top0), __uint_as_float(top1));
           const int tok0 = j * kTileTokens + h * kHalfStep;
-          if (a.scale_log2 < 0.f) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) s[q][i] ^= 0x80000000u;
-          }
-          if (!sh.whole[ring] || tok0 + kHalfStep > lim_min) {
+          const bool flip = a.scale_log2 < 0.f;
+          if (flip || !sh.whole[ring] || tok0 + kHalfStep > lim_min) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               const uint32_t mask = sh.mask[ring][h * 2 + q];
@@ -496,18 +503,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               const uint32_t keep =
                   mask & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
+              for (int i = 0; i < 32; ++i) {
+                if (flip) s[q][i] ^= 0x80000000u;
                 if (!((keep >> i) & 1)) s[q][i] = 0xff800000u;
+              }
             }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mx[q] = max3(mx[q], __uint_as_float(s[q & 1][i + (q & 2)]),
+                             __uint_as_float(s[q & 1][i + (q & 2) + 1]));
+            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              mx[q] = max3(mx[q], __uint_as_float(s[q & 1][i + (q & 2)]),
-                           __uint_as_float(s[q & 1][i + (q & 2) + 1]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+          top *= sc;
           // The reference of the exponentials stays where it is until it is kSlack (in
           // log2) short: weights of up to 2^kSlack are rounded like the others, each
           // relative to itself, and a rescale of the accumulator is rare.
