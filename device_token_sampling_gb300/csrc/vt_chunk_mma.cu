@@ -21,9 +21,10 @@ constexpr int kChunkThreads = 512;
 constexpr int kPieces = 4;    // pieces that are known ahead
 constexpr int kMasks = 8;     // steps whose token masks are kept
 constexpr int kHalfStep = kTileTokens / 2;  // tokens of one product
-// warps: the softmax of each tile; then one each for the tiles' scores, the tiles'
-// products, the copies of K and V of even and of odd steps, the pieces and their Q
-constexpr int kScoreWarp = 8, kProductWarp = 10, kKvWarp = 12, kPieceWarp = 14;
+constexpr int kWeights = kTileTokens;       // tensor memory: S, then each tile's P, then O
+// warps: the softmax of each tile; then one each for the scores, the products of each
+// tile, the copies of K and V of even and of odd steps, the pieces and their Q
+constexpr int kScoreWarp = 8, kProductWarp = 9, kKvWarp = 11, kPieceWarp = 13;
 
 // ---- the units ----------------------------------------------------------------
 // Heads in one tile: a.heads of the G, a.parts times; tokens in one tile: a.tokens.  A
@@ -215,8 +216,9 @@ struct Shared {
   // its barriers, so that a phase's parity says which it is)
   uint64_t full[2][R], empty[R];
   uint64_t piece_full[kPieces], piece_empty[kPieces];
-  // of each tile, by halves of a step: scores made; weights stored; product done
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];
+  uint64_t s_full[2], s_free;        // scores made, of each tile; read
+  // of each tile, by halves of a step: weights stored; product done
+  uint64_t p_full[2][2], pv_done[2][2];
   // of each tile: products of a unit done; accumulator read
   uint64_t o_done[2], o_empty[2];
   uint64_t v_ok[2][4];               // of each tile, by turns: V of a step looked through
@@ -271,6 +273,24 @@ __device__ __forceinline__ void tmem_ld32_max(uint32_t (&r)[32], uint32_t& top, 
       "%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"
       : VT_R8(r, 0), VT_R8(r, 8), VT_R8(r, 16), VT_R8(r, 24), "=r"(top)
       : "r"(addr));
+}
+// 16 columns of this thread's lane
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : VT_R8(r, 0), VT_R8(r, 8)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      VT_I8(r, 0), VT_I8(r, 8)
+      : "memory");
+}
+__device__ __forceinline__ void loaded16(uint32_t (&r)[16]) {
+  asm volatile("" : VT_P8(r, 0), VT_P8(r, 8)::"memory");
 }
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t addr) {
   uint32_t r;
@@ -367,10 +387,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       for (int h = 0; h < 2; ++h) {
-        mbar_init(&sh.s_full[t][h], 1);
         mbar_init(&sh.p_full[t][h], 4);
         mbar_init(&sh.pv_done[t][h], 1);
       }
+      mbar_init(&sh.s_full[t], 1);
       mbar_init(&sh.o_done[t], 1);
       mbar_init(&sh.o_empty[t], 4);
       for (int i = 0; i < 4; ++i) mbar_init(&sh.v_ok[t][i], 4);
@@ -378,6 +398,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sh.q_empty[t], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&sh.drained[i], 1);
+    mbar_init(&sh.s_free, 4);
     mbar_init(&sh.x_full, 4);
     fence_mbar_init();
   }
@@ -393,7 +414,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const long long limit = a.wait_cycles;
   bool ok = true;
-  // tensor memory columns: S of each tile (P over its first half), then O of each
   constexpr uint32_t kO = 2 * kTileTokens;
 
   // The next piece into `p`; false behind the last, or when the wait ran out.
@@ -442,125 +462,127 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // times an infinity or a NaN is NaN.
         const bool diagonal = (j + 1) * kTileTokens > max(p.lim0, 0);
         poisoned = false;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          ok = warp_wait(&sh.s_full[t][h], steps & 1, limit);
+        ok = warp_wait(&sh.s_full[t], steps & 1, limit);
+        if (!ok) break;
+        fence_after();
+        if (diagonal && (t == 0 || !two)) {
+          // Tokens of V that are not finite are taken out of it.  (The scores are there, and
+          // the last product but one, so the last V of this place has been used.)
+          const int st = place<R>(g, 1);
+          const uint32_t ph = ((two ? full_ph[0] : full_ph[1]) >> st) + (j - p.t0) / (R / 2);
+          if (steps > 0) ok = warp_wait(&sh.pv_done[t][0], (steps - 1) & 1, limit);
+          if (ok) ok = warp_wait(&sh.full[!two][st], ph & 1, limit);
           if (!ok) break;
-          fence_after();
-          if (diagonal && h == 0 && (t == 0 || !two)) {
-            // Tokens of V that are not finite are taken out of it.  (The scores are there,
-            // so the last V of this place has been used; this piece's uses before it.)
-            const int st = place<R>(g, 1);
-            const uint32_t ph = ((two ? full_ph[0] : full_ph[1]) >> st) + (j - p.t0) / (R / 2);
-            ok = warp_wait(&sh.full[!two][st], ph & 1, limit);
-            if (!ok) break;
-            uint4* row = reinterpret_cast<uint4*>(dyn + L::kKv + st * L::kTile + in * 128);
-            uint32_t bad = 0;
+          uint4* row = reinterpret_cast<uint4*>(dyn + L::kKv + st * L::kTile + in * 128);
+          uint32_t bad = 0;
+#pragma unroll
+          for (int q = 0; q < D / 64; ++q)
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              bad |= not_finite<T>(row[q * (L::kHalf / 16) + ((c + in) & 7)]);
+          if (bad) {
 #pragma unroll
             for (int q = 0; q < D / 64; ++q)
-#pragma unroll
               for (int c = 0; c < 8; ++c)
-                bad |= not_finite<T>(row[q * (L::kHalf / 16) + ((c + in) & 7)]);
-            if (bad) {
-#pragma unroll
-              for (int q = 0; q < D / 64; ++q)
-                for (int c = 0; c < 8; ++c)
-                  row[q * (L::kHalf / 16) + ((c + in) & 7)] = make_uint4(0, 0, 0, 0);
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            }
-            const uint32_t word =
-                __ballot_sync(0xffffffffu, bad && j * kTileTokens + in < p.end);
-            if (lane == 0) sh.poison[g & 3][warp & 3] = word;
-            warp_arrive(&sh.v_ok[t][g & 3]);
-            if (two) warp_arrive(&sh.v_ok[1][g & 3]);
+                row[q * (L::kHalf / 16) + ((c + in) & 7)] = make_uint4(0, 0, 0, 0);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
-          const uint32_t ts = tmem + lanes + t * kTileTokens + h * kHalfStep;
-          if (!warp_live) {  // (the products of these rows are never read)
-            if (diagonal && h == 0) {
-              ok = warp_wait(&sh.v_ok[t][g & 3], (ok_ph >> (g & 3)) & 1, limit);
-              ok_ph ^= 1u << (g & 3);
-              if (!ok) break;
-            }
-            warp_arrive(&sh.p_full[t][h]);
-            continue;
+          const uint32_t word = __ballot_sync(0xffffffffu, bad && j * kTileTokens + in < p.end);
+          if (lane == 0) sh.poison[g & 3][warp & 3] = word;
+          warp_arrive(&sh.v_ok[t][g & 3]);
+          if (two) warp_arrive(&sh.v_ok[1][g & 3]);
+        }
+        if (!warp_live) {  // (the products of these rows are never read)
+          warp_arrive(&sh.s_free);
+          if (diagonal) {
+            ok = warp_wait(&sh.v_ok[t][g & 3], (ok_ph >> (g & 3)) & 1, limit);
+            ok_ph ^= 1u << (g & 3);
           }
-          uint32_t s[2][32];
-          uint32_t top0, top1;
-          tmem_ld32_max(s[0], top0, ts);
-          tmem_ld32_max(s[1], top1, ts + 32);
-          tmem_wait_ld();
-          loaded(s[0]);
-          loaded(s[1]);
-          asm volatile("" : "+r"(top0), "+r"(top1)::"memory");
-          float top = fmaxf(__uint_as_float(top0), __uint_as_float(top1));
-          const int tok0 = j * kTileTokens + h * kHalfStep;
-          const bool flip = a.scale_log2 < 0.f;
-          if (flip || !sh.whole[ring] || tok0 + kHalfStep > lim_min) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const uint32_t mask = sh.mask[ring][h * 2 + q];
-              const int left = lim - tok0 - q * 32;
-              const uint32_t keep =
-                  mask & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                if (flip) s[q][i] ^= 0x80000000u;
-                if (!((keep >> i) & 1)) s[q][i] = 0xff800000u;
-              }
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                mx[q] = max3(mx[q], __uint_as_float(s[q & 1][i + (q & 2)]),
-                             __uint_as_float(s[q & 1][i + (q & 2) + 1]));
-            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          for (int h = 0; h < 2 && ok; ++h) {
+            if (steps > 0) ok = warp_wait(&sh.pv_done[t][h], (steps - 1) & 1, limit);
+            if (ok) warp_arrive(&sh.p_full[t][h]);
           }
-          top *= sc;
-          // The reference of the exponentials stays where it is until it is kSlack (in
-          // log2) short: weights of up to 2^kSlack are rounded like the others, each
-          // relative to itself, and a rescale of the accumulator is rare.
-          constexpr float kSlack = 8.f;
-          const bool grow = top > (m == -INFINITY ? m : m + kSlack);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? ex2_approx(m - top) : 1.f;
-            if (grow) m = top;
-            l *= f;
-            if (begun) {
-              ok = warp_wait(&sh.pv_done[t][h ^ 1], (h ? steps : steps - 1) & 1, limit);
-              if (!ok) break;
-              fence_after();
-              const uint32_t o_at = tmem + lanes + kO + t * D;
-              const uint64_t f2 = pack_f2(f, f);
+          continue;
+        }
+        uint32_t s[4][32], tops[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32_max(s[q], tops[q], tmem + lanes + q * 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          loaded(s[q]);
+          asm volatile("" : "+r"(tops[q])::"memory");
+        }
+        fence_before();
+        warp_arrive(&sh.s_free);
+        float top = max3(fmaxf(__uint_as_float(tops[0]), __uint_as_float(tops[1])),
+                         __uint_as_float(tops[2]), __uint_as_float(tops[3]));
+        const int tok0 = j * kTileTokens;
+        const bool flip = a.scale_log2 < 0.f;
+        if (flip || !sh.whole[ring] || tok0 + kTileTokens > lim_min) {
+          top = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t mask = sh.mask[ring][q];
+            const int left = lim - tok0 - q * 32;
+            const uint32_t keep =
+                mask & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (flip) s[q][i] ^= 0x80000000u;
+              if (!((keep >> i) & 1)) s[q][i] = 0xff800000u;
+              top = fmaxf(top, __uint_as_float(s[q][i]));
+            }
+          }
+        }
+        top *= sc;
+        // The reference of the exponentials stays where it is until it is kSlack (in log2)
+        // short: weights of up to 2^kSlack are rounded like the others, each relative to
+        // itself, and a rescale of the accumulator is rare.
+        constexpr float kSlack = 8.f;
+        const bool grow = top > (m == -INFINITY ? m : m + kSlack);
+        const uint32_t o_at = tmem + lanes + kO + t * D;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2_approx(m - top) : 1.f;
+          if (grow) m = top;
+          l *= f;
+          if (begun) {
+            ok = warp_wait(&sh.pv_done[t][1], (steps - 1) & 1, limit);
+            if (!ok) break;
+            fence_after();
+            const uint64_t f2 = pack_f2(f, f);
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, o_at + c);
-                tmem_wait_ld();
-                loaded(o);
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(o, o_at + c);
+              tmem_wait_ld();
+              loaded16(o);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  float x0, x1;
-                  unpack_f2(mul_f2(pack_f2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2),
-                            x0, x1);
-                  o[i] = __float_as_uint(x0);
-                  o[i + 1] = __float_as_uint(x1);
-                }
-                tmem_st32(o_at + c, o);
+              for (int i = 0; i < 16; i += 2) {
+                float x0, x1;
+                unpack_f2(mul_f2(pack_f2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2),
+                          x0, x1);
+                o[i] = __float_as_uint(x0);
+                o[i + 1] = __float_as_uint(x1);
               }
+              tmem_st16(o_at + c, o);
             }
           }
-          const float off = m == -INFINITY ? 0.f : -m;
-          const uint64_t off2 = pack_f2(off, off);
-          uint64_t sum[2] = {0, 0};
+        }
+        const float off = m == -INFINITY ? 0.f : -m;
+        const uint64_t off2 = pack_f2(off, off);
+        uint64_t sum[2] = {0, 0};
+        const uint32_t p_at = tmem + lanes + kWeights + t * kHalfStep;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           uint32_t w[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const int e = 2 * i;
-            const uint64_t z = fma_f2(pack_f2(__uint_as_float(s[e >> 5][e & 31]),
-                                              __uint_as_float(s[e >> 5][(e & 31) + 1])),
-                                      sc2, off2);
+            const uint64_t z =
+                fma_f2(pack_f2(__uint_as_float(s[2 * h + (e >> 5)][e & 31]),
+                               __uint_as_float(s[2 * h + (e >> 5)][(e & 31) + 1])),
+                       sc2, off2);
             float z0, z1;
             unpack_f2(z, z0, z1);
             const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
@@ -569,10 +591,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // relative 2^-9 in bf16, 2^-12 in fp16, each its own way); the sum is not
             w[i] = pack2<T>(p0, p1);
           }
-          tmem_st32(ts, w);
-          float s0, s1;
-          unpack_f2(add_f2(sum[0], sum[1]), s0, s1);
-          l += s0 + s1;
+          // (the product with the last ones is done)
+          if (steps > 0) ok = warp_wait(&sh.pv_done[t][h], (steps - 1) & 1, limit);
+          if (!ok) break;
+          fence_after();
+          tmem_st32(p_at + h * 32, w);
           tmem_wait_st();
           if (diagonal) {
             if (h == 0) {
@@ -586,18 +609,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (poisoned) {
               // what was taken out of V, for the rows that attend to it, added in front of
               // the half's product
-              ok = begun ? warp_wait(&sh.pv_done[t][h ^ 1], (h ? steps : steps - 1) & 1, limit)
+              const bool added = begun || h > 0;
+              ok = added ? warp_wait(&sh.pv_done[t][h ^ 1], (h ? steps : steps - 1) & 1, limit)
                          : warp_wait(&sh.o_empty[t], (units & 1) ^ 1, limit);
               if (!ok) break;
               fence_after();
-              add_poison<T, D>(a, p, sh.poison[g & 3][h * 2], sh.poison[g & 3][h * 2 + 1], tok0, lim,
-                               begun, ts, tmem + lanes + kO + t * D);
+              add_poison<T, D>(a, p, sh.poison[g & 3][h * 2], sh.poison[g & 3][h * 2 + 1],
+                               tok0 + h * kHalfStep, lim, added, p_at + h * 32, o_at);
             }
           }
-          begun = true;
           fence_before();
           warp_arrive(&sh.p_full[t][h]);
         }
+        begun = true;
+        float s0, s1;
+        unpack_f2(add_f2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
       }
       if (!ok) break;
       for (int c = 0; c < R / 2; ++c) {  // uses of V's places: every (R / 2)-th step each
@@ -840,71 +867,78 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int t = 0; t < 2; ++t)
         if (uses[t] > 0) mbar_wait_clocked(&sh.q_full[t], (uses[t] - 1) & 1, kDrainCycles);
     } else if (warp < kKvWarp) {
-      // ---- MMAs: a warp to a tile's scores, another to its products, walk the halves of its
-      // steps and wait; one lane issues
+      // ---- MMAs: a warp to the scores of both tiles by turns, one to each tile's products,
+      // walk the steps and wait; one lane issues
       constexpr uint32_t kType = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-      // fp32 accumulators; K-major A and B; N = 64 tokens, M = 128
+      // fp32 accumulators; K-major A and B; N = 128 tokens, M = 128
       constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) |
-                                   ((kHalfStep / 8) << 17) | ((kTileRows / 16) << 24);
+                                   ((kTileTokens / 8) << 17) | ((kTileRows / 16) << 24);
       // B (V) is N-major: its rows are tokens; N = D
       constexpr uint32_t kIdescO = (1u << 4) | (kType << 7) | (kType << 10) | (1u << 16) |
                                    ((uint32_t)(D / 8) << 17) | ((kTileRows / 16) << 24);
       constexpr uint32_t kHi = desc_hi(1024);
-      const int t = warp & 1;
-      const bool product = warp >= kProductWarp;
-      const uint32_t q_lo = desc_lo(base + L::kQ + t * L::kTile, 16),
-                     k_lo = desc_lo(base + L::kKv, 16), v_lo = desc_lo(base + L::kKv, L::kHalf);
-      const uint32_t s_at = tmem + t * kTileTokens, o_at = tmem + kO + t * D;
-      // steps and units of this tile; the CTA's steps; of the ring's places by set, the
-      // parities of their uses
-      uint32_t steps = 0, units = 0, all = 0, full_ph[2] = {0, 0};
+      // units; the CTA's steps; of the ring's places by set, the parities of their uses
+      uint32_t units = 0, all = 0, full_ph[2] = {0, 0};
       Piece p;
-      while (ok && next_piece(p)) {
-        const bool two = p.tokens > a.tokens;
-        const int first = two ? 0 : (all ^ t) & 1, by = two ? 1 : 2, n = p.t1 - p.t0;
-        uint32_t ph = two ? full_ph[0] : full_ph[1];
-        // (every unit's waits and arrivals, so that a parity is the last unit's)
-        if (product) ok = warp_wait(&sh.o_empty[t], (units & 1) ^ 1, limit);
-        else ok = warp_wait(&sh.q_full[t], units & 1, limit);
-        if (ok && first >= n) {
-          if (product) {
-            warp_arrive(&sh.o_done[t]);
-          } else {
-            warp_arrive(&sh.q_empty[t]);
-          }
-        }
+      if (warp == kScoreWarp) {
+        const uint32_t q_lo = desc_lo(base + L::kQ, 16), k_lo = desc_lo(base + L::kKv, 16);
+        uint32_t scores = 0;  // of both tiles
+        while (ok && next_piece(p)) {
+          const bool two = p.tokens > a.tokens;
+          const int n = p.t1 - p.t0;
+          uint32_t ph = two ? full_ph[0] : full_ph[1];
+          for (int t = 0; t < 2 && ok; ++t) ok = warp_wait(&sh.q_full[t], units & 1, limit);
+          if (ok && !two && n == 1) warp_arrive(&sh.q_empty[(all & 1) ^ 1]);
 #pragma unroll 1
-        for (int j = first; j < n && ok; j += by, ++steps) {
-          const int st = place<R>(all + j, product);
-          ok = warp_wait(&sh.full[!two][st], (ph >> st) & 1, limit);
-          ph ^= 1u << st;
-          if (!ok) break;
-          const uint32_t tile = st * (L::kTile >> 4);
-          if (!product) {
+          for (int j = 0; j < n && ok; ++j) {
+            const int st = place<R>(all + j, 0);
+            ok = warp_wait(&sh.full[!two][st], (ph >> st) & 1, limit);
+            ph ^= 1u << st;
+            const int from = two ? 0 : (all + j) & 1, to = two ? 2 : from + 1;
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {  // S = Q K^T
-              // the product with the P that lies there is done
-              if (steps > 0) ok = warp_wait(&sh.pv_done[t][h], (steps - 1) & 1, limit);
+            for (int t = from; t < to; ++t, ++scores) {  // S = Q K^T
+              // the last scores have been read
+              if (ok && scores > 0) ok = warp_wait(&sh.s_free, (scores - 1) & 1, limit);
               if (!ok) break;
               fence_after();
               if (elect_one()) {
-                const uint32_t b_lo = k_lo + tile + h * (kHalfStep * 128 >> 4);
-                const uint32_t d = s_at + h * kHalfStep;
+                const uint32_t a_lo = q_lo + t * (L::kTile >> 4), b_lo = k_lo + st * (L::kTile >> 4);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                   const uint32_t off = ((ks / 4) * L::kHalf + (ks % 4) * 32) >> 4;
-                  mma_ss(d, q_lo + off, b_lo + off, kHi, kIdescS, ks > 0);
+                  mma_ss(tmem, a_lo + off, b_lo + off, kHi, kIdescS, ks > 0);
                 }
-                mma_commit(&sh.s_full[t][h]);
-                if (h) {
-                  mma_commit(&sh.empty[st]);
-                  if (!two) mma_commit(&sh.empty[st]);
-                  if (j + by >= n) mma_commit(&sh.q_empty[t]);
-                }
+                mma_commit(&sh.s_full[t]);
+                mma_commit(&sh.empty[st]);
+                if (!two) mma_commit(&sh.empty[st]);
+                if (j + (two ? 1 : 2) >= n) mma_commit(&sh.q_empty[t]);
               }
               __syncwarp();
             }
-          } else {
+          }
+          if (two) full_ph[0] = ph;
+          else full_ph[1] = ph;
+          all += n;
+          ++units;
+        }
+      } else {
+        const int t = warp - kProductWarp;
+        const uint32_t v_lo = desc_lo(base + L::kKv, L::kHalf);
+        const uint32_t p_at = tmem + kWeights + t * kHalfStep, o_at = tmem + kO + t * D;
+        uint32_t steps = 0;  // of this tile
+        while (ok && next_piece(p)) {
+          const bool two = p.tokens > a.tokens;
+          const int first = two ? 0 : (all ^ t) & 1, by = two ? 1 : 2, n = p.t1 - p.t0;
+          uint32_t ph = two ? full_ph[0] : full_ph[1];
+          // (every unit's waits and arrivals, so that a parity is the last unit's)
+          ok = warp_wait(&sh.o_empty[t], (units & 1) ^ 1, limit);
+          if (ok && first >= n) warp_arrive(&sh.o_done[t]);
+#pragma unroll 1
+          for (int j = first; j < n && ok; j += by, ++steps) {
+            const int st = place<R>(all + j, 1);
+            ok = warp_wait(&sh.full[!two][st], (ph >> st) & 1, limit);
+            ph ^= 1u << st;
+            if (!ok) break;
             bool poisoned = false;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {  // O += P V
@@ -916,11 +950,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               }
               fence_after();
               if (elect_one()) {
-                const uint32_t b_lo = v_lo + tile + h * (kHalfStep * 128 >> 4);
-                const uint32_t a_t = s_at + h * kHalfStep;
+                const uint32_t b_lo = v_lo + st * (L::kTile >> 4) + h * (kHalfStep * 128 >> 4);
 #pragma unroll
                 for (int ks = 0; ks < kHalfStep / 16; ++ks)
-                  mma_ts(o_at, a_t + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO,
+                  mma_ts(o_at, p_at + h * 32 + ks * 8, b_lo + (ks * 16 * 128 >> 4), kHi, kIdescO,
                          ks > 0 ? 1u : (uint32_t)(j > first || h > 0 || poisoned));
                 mma_commit(&sh.pv_done[t][h]);
                 if (h) {
@@ -932,11 +965,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               __syncwarp();
             }
           }
+          if (two) full_ph[0] = ph;
+          else full_ph[1] = ph;
+          all += n;
+          ++units;
         }
-        if (two) full_ph[0] = ph;
-        else full_ph[1] = ph;
-        all += n;
-        ++units;
       }
       // none of its MMAs is in flight when the CTA's memory goes to another
       uint64_t* drained = &sh.drained[warp - kScoreWarp];
