@@ -4,10 +4,10 @@
 // tiles of 128 rows, whole tokens each; a unit attends to the tokens up to its last row's
 // position, 128 at a step.  A unit of two tiles takes every step with both; one that fits
 // a tile has its steps taken by the two tiles in turn, whose results are added up at the
-// end.  Three launches:
+// end.  Two launches:
 //   plan_kernel    counts the units' steps and gives every CTA its share;
-//   chunk_kernel   one CTA an SM, its pieces of units one after another;
-//   join_kernel    puts units together that more than one CTA worked on.
+//   chunk_kernel   one CTA an SM, its pieces of units one after another; units that more
+//                  than one CTA worked on are put together by the last to come.
 #include <type_traits>
 
 #include "vt_paged.h"
@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) s_several = 0;
+  for (int i = tid; i < 8 * a.grid; i += kPlanThreads) a.plan_count[i] = 0;
   int64_t units = 0, steps = 0;
   for (int base = 0; base < a.B; base += kPlanThreads) {
     const int b = base + tid;
@@ -208,6 +209,8 @@ struct Piece {
   int end;           // of the unit's tokens
   int lim0;          // end of the tokens that its first row attends to
   int slot;          // of its partial result, or -1: the whole unit
+  int job, last;     // a part: the CTAs that began and end the unit
+  int parts;         // how many parts it has
 };
 
 template <int R>
@@ -292,6 +295,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
 __device__ __forceinline__ void loaded16(uint32_t (&r)[16]) {
   asm volatile("" : VT_P8(r, 0), VT_P8(r, 8)::"memory");
 }
+// 32 bytes, a whole sector, at once
+__device__ __forceinline__ void store32(void* to, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t addr) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr));
@@ -354,6 +363,70 @@ __device__ __noinline__ void add_poison(const ChunkArgs& a, const Piece& p, uint
     }
 }
 
+// The 32 rows of a warp (row r0 of a unit on; this lane's goes to `row` of the output, -1:
+// none) from the parts that CTAs job .. last left: their first slots but for job's second.
+// Each row is rescaled to its parts' common maximum, summed and divided; the order is the
+// CTAs'.  A part that holds nothing (sum 0) is not read.
+template <typename T, int D>
+__device__ __noinline__ void join_rows(const ChunkArgs& a, int job, int last, int r0, int64_t row) {
+  constexpr int W = D / 32, kRows = 8;
+  const int lane = threadIdx.x & 31;
+  auto slot = [&](int k) { return (int64_t)(k == job ? 2 * job + 1 : 2 * k) * kUnitRows + r0; };
+  auto there = [&](int k) { return a.plan_start[k].at < a.plan_start[k + 1].at; };
+  float m = -INFINITY, l = 0.f;
+  for (int k = job; k <= last; ++k) {
+    if (!there(k)) continue;
+    const float2 ml = row >= 0 ? __ldcg(a.part_ml + slot(k) + lane) : make_float2(-INFINITY, 0.f);
+    const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+    l = l * ex2_approx(m - base) + (ml.y == 0.f ? 0.f : ml.y * ex2_approx(ml.x - base));
+    m = mn;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+  for (int q = 0; q < 32; q += kRows) {
+    if (!__any_sync(0xffffffffu, row >= 0 && lane >= q && lane < q + kRows)) continue;
+    float acc[kRows][W] = {};
+#pragma unroll 1
+    for (int k = job; k <= last; ++k) {
+      if (!there(k)) continue;
+      float f = 0.f;  // this lane's row's
+      if (row >= 0) {
+        const float2 ml = __ldcg(a.part_ml + slot(k) + lane);
+        f = ml.y == 0.f ? 0.f : ex2_approx(ml.x - (m == -INFINITY ? 0.f : m)) * inv;
+      }
+      float x[kRows][W];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const float* o = a.part_o + (slot(k) + q + i) * D + lane * W;
+        if constexpr (W == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(o));
+          x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
+          x[i][0] = v.x, x[i][1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, q + i);
+        if (fi != 0.f) {  // (a NaN too)
+#pragma unroll
+          for (int w = 0; w < W; ++w) acc[i][w] += x[i][w] * fi;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t to = __shfl_sync(0xffffffffu, row, q + i);
+      if (to < 0) continue;
+      uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + to * D + lane * W);
+#pragma unroll
+      for (int w = 0; w < W / 2; ++w) out[w] = pack2<T>(acc[i][2 * w], acc[i][2 * w + 1]);
+    }
+  }
+  if (a.lse && row >= 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap map_k,
@@ -374,7 +447,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // be the same in a warp: MMA operands live in uniform registers)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
-  asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) {
     for (int i = 0; i < R; ++i) {
       mbar_init(&sh.full[0][i], 1);
@@ -520,20 +592,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int tok0 = j * kTileTokens;
         const bool flip = a.scale_log2 < 0.f;
         if (flip || !sh.whole[ring] || tok0 + kTileTokens > lim_min) {
-          top = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 4; ++q) {  // (32 tokens that every row sees stay as they are)
             const uint32_t mask = sh.mask[ring][q];
             const int left = lim - tok0 - q * 32;
             const uint32_t keep =
                 mask & (left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1);
+            if (__any_sync(0xffffffffu, flip || keep != 0xffffffffu)) {
+              float most = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (flip) s[q][i] ^= 0x80000000u;
-              if (!((keep >> i) & 1)) s[q][i] = 0xff800000u;
-              top = fmaxf(top, __uint_as_float(s[q][i]));
+              for (int i = 0; i < 32; ++i) {
+                if (flip) s[q][i] ^= 0x80000000u;
+                if (!((keep >> i) & 1)) s[q][i] = 0xff800000u;
+                most = fmaxf(most, __uint_as_float(s[q][i]));
+              }
+              tops[q] = __float_as_uint(most);
             }
           }
+          top = fmaxf(fmaxf(__uint_as_float(tops[0]), __uint_as_float(tops[1])),
+                      fmaxf(__uint_as_float(tops[2]), __uint_as_float(tops[3])));
         }
         top *= sc;
         // The reference of the exponentials stays where it is until it is kSlack (in log2)
@@ -701,26 +778,41 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (!live) continue;
           if (p.slot >= 0) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(part_o + c + i) =
-                  make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < 32; i += 8) store32(part_o + c + i, &o[i]);
           } else {
+            uint32_t y[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4*>(out + c + i) = make_uint4(
-                  pack2<T>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
-                  pack2<T>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
-                  pack2<T>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])),
-                  pack2<T>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
+            for (int i = 0; i < 16; ++i)
+              y[i] = pack2<T>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+            if (a.out_wide) {
+              store32(out + c, &y[0]);
+              store32(out + c + 16, &y[8]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<uint4*>(out + c + 2 * i) =
+                    make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            }
           }
         }
         fence_before();
       }
       warp_arrive(&sh.o_empty[t]);
       if (!two) warp_arrive(&sh.o_empty[1]);
-      if (!live) continue;
-      if (p.slot >= 0) a.part_ml[part] = make_float2(m, l);
-      else if (a.lse) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+      if (p.slot < 0) {
+        if (live && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+      } else if (warp_live) {
+        // the last warp to leave its part of these rows puts them together
+        if (live) a.part_ml[part] = make_float2(m, l);
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(a.plan_count + p.job * 8 + (two ? t : 0) * 4 + (warp & 3), 1);
+        if (__shfl_sync(0xffffffffu, before, 0) == p.parts - 1) {
+          __threadfence();
+          join_rows<T, D>(a, p.job, p.last, (two ? t * kTileRows : 0) + (in & ~31), live ? row : -1);
+        }
+      }
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -831,6 +923,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             p.t0 = step;
             p.t1 = (int)min((int64_t)n, step + (stop - at) / w);
             p.slot = step > 0 ? 2 * c : p.t1 < n ? 2 * c + 1 : -1;
+            if (p.slot >= 0) {  // who else has some of the unit
+              const int64_t begin = at - (int64_t)p.t0 * w, end = begin + (int64_t)n * w;
+              p.job = c;
+              while (p.job > 0 && a.plan_start[p.job].at > begin) --p.job;
+              p.last = c;
+              while (p.last + 1 < G && a.plan_start[p.last + 1].at < end) ++p.last;
+              for (int q = p.job; q <= p.last; ++q)
+                p.parts += a.plan_start[q].at < a.plan_start[q + 1].at;
+            }
             at += (int64_t)(p.t1 - p.t0) * w;
             step = 0;
             if (++head == a.heads_all) {
@@ -985,66 +1086,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// A unit whose steps two or more CTAs had: CTA c began it (its second slot), the
-// following ones went on (their first slots).  A warp to a row rescales the parts to
-// their common maximum, sums and divides.  A part that holds nothing (sum 0) is not read.
-constexpr int kJoinWarps = 8;
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(ChunkArgs a) {
-  constexpr int W = D / 32;
-  const int lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.y;
-  const ChunkStart s = a.plan_start[c + 1];
-  // the unit that the end of c's share lies in, if c began it
-  if (s.step == 0 || s.b >= a.B) return;
-  const Request rq = request(a, s.b);
-  const int weight = unit_weight(a, rq, s.unit);
-  const int64_t begin = s.at - (int64_t)s.step * weight;
-  if (begin < a.plan_start[c].at) return;
-  const int r = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  const int kvh = s.head / a.parts, part = s.head % a.parts * a.heads;
-  const int tile = r / kTileRows, in = r % kTileRows;
-  const int token = tile * a.tokens + in / a.heads, head = part + in % a.heads;
-  if (in / a.heads >= a.tokens || token >= unit_tokens(a, rq, s.unit) || head >= a.G) return;
-  const int64_t end = begin + (int64_t)unit_steps(a, rq, s.unit) * weight;
-  int last = c + 1;  // the CTA with the unit's last step
-  while (last + 1 < a.grid && a.plan_start[last + 1].at < end) ++last;
-  auto slot = [&](int k) { return (int64_t)(k == c ? 2 * c + 1 : 2 * k) * kUnitRows + r; };
-  float m = -INFINITY, l = 0.f, acc[W] = {};
-  for (int k0 = c; k0 <= last; k0 += 32) {
-    const int k = k0 + lane;
-    const float2 ml = k <= last && a.plan_start[k].at < a.plan_start[k + 1].at
-                          ? a.part_ml[slot(k)] : make_float2(-INFINITY, 0.f);
-    const bool some = ml.y != 0.f;
-    const float mn = fmaxf(m, warp_max(ml.x)), base = mn == -INFINITY ? 0.f : mn;
-    const float old = ex2_approx(m - base), f = some ? ex2_approx(ml.x - base) : 0.f;
-    m = mn;
-    l = l * old + warp_sum_f(some ? ml.y * f : 0.f);
-#pragma unroll
-    for (int w = 0; w < W; ++w) acc[w] *= old;
-    for (unsigned left = __ballot_sync(0xffffffffu, some); left; left &= left - 1) {
-      const int i = __ffs(left) - 1;
-      const float fi = __shfl_sync(0xffffffffu, f, i);
-      const float* o = a.part_o + slot(k0 + i) * D + lane * W;
-      if constexpr (W == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(o);
-        acc[0] += v.x * fi, acc[1] += v.y * fi, acc[2] += v.z * fi, acc[3] += v.w * fi;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(o);
-        acc[0] += v.x * fi, acc[1] += v.y * fi;
-      }
-    }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t row =
-      (int64_t)(rq.s0 + s.unit * 2 * a.tokens + token) * a.hq + kvh * a.G + head;
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D + lane * W);
-#pragma unroll
-  for (int i = 0; i < W / 2; ++i) out[i] = pack2<T>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-}
-
 template <int D>
 constexpr size_t chunk_smem() {
   return ChunkSmem<D>::kRest + sizeof(Shared<ChunkSmem<D>::kRing>);
@@ -1067,11 +1108,7 @@ cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& mk, const CUtens
   cfg.gridDim = dim3((unsigned)a.grid);
   cfg.blockDim = dim3(kChunkThreads);
   cfg.dynamicSmemBytes = chunk_smem<D>();
-  if ((e = cudaLaunchKernelEx(&cfg, chunk_kernel<T, D>, a, mk, mv, mq)) != cudaSuccess) return e;
-  cfg.gridDim = dim3(kUnitRows / kJoinWarps, (unsigned)a.grid);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T, D>, a);
+  return cudaLaunchKernelEx(&cfg, chunk_kernel<T, D>, a, mk, mv, mq);
 }
 
 template <typename T, int D>
@@ -1130,6 +1167,7 @@ cudaError_t launch_chunk_mma(ChunkArgs a, int dtype, int head_dim, cudaStream_t 
   a.tokens = kTileRows / a.heads;
   a.heads_all = a.hkv * a.parts;
   a.q_bytes = (uint32_t)(a.heads * a.tokens * head_dim * 2);
+  a.out_wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   CUtensorMap mk, mv, mq;
   if (!cache_map(&mk, a.k, dtype, head_dim, a.shift, a.hkv, a.num_blocks, a.block_stride,
                  a.token_stride, a.head_stride) ||

@@ -25,6 +25,7 @@ struct vt_paged {
   int32_t* d_err = nullptr;  // the error word, then the attention's work counter
   int64_t* d_plan_first = nullptr;  // the chunks' plan
   vt::ChunkStart* d_plan_start = nullptr;
+  int32_t* d_plan_count = nullptr;
   // of release and compact: a bit to a block, the used ids before each 32, two totals
   uint32_t* d_used = nullptr;
   int32_t* d_ranks = nullptr;
@@ -131,6 +132,7 @@ void free_paged(vt_paged* h) {
   if (h->d_err) cudaFree(h->d_err);
   if (h->d_plan_first) cudaFree(h->d_plan_first);
   if (h->d_plan_start) cudaFree(h->d_plan_start);
+  if (h->d_plan_count) cudaFree(h->d_plan_count);
   if (h->d_used) cudaFree(h->d_used);
   if (h->d_ranks) cudaFree(h->d_ranks);
   if (h->d_totals) cudaFree(h->d_totals);
@@ -171,6 +173,7 @@ int vt_paged_create(const vt_paged_config* config, vt_paged** out) {
          cudaMalloc(&h->d_plan_first, (config->max_batch + 1) * 2 * sizeof(int64_t)) ==
              cudaSuccess &&
          cudaMalloc(&h->d_plan_start, (h->num_sms + 1) * sizeof(vt::ChunkStart)) == cudaSuccess &&
+         cudaMalloc(&h->d_plan_count, h->num_sms * 8 * sizeof(int32_t)) == cudaSuccess &&
          cudaMalloc(&h->d_part_o, h->part_rows * config->head_dim * sizeof(float)) ==
              cudaSuccess &&
          cudaMalloc(&h->d_part_ml, h->part_rows * sizeof(float2)) == cudaSuccess;
@@ -427,6 +430,7 @@ int vt_paged_chunk_attention(vt_paged* h, int32_t dtype, int32_t B, int32_t T, c
   a.min_cost = 2;
   a.plan_first = h->d_plan_first;
   a.plan_start = h->d_plan_start;
+  a.plan_count = h->d_plan_count;
   a.part_o = h->d_part_o;
   a.part_ml = h->d_part_ml;
   cudaStream_t st = (cudaStream_t)stream;

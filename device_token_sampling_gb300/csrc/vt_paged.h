@@ -171,12 +171,14 @@ struct ChunkArgs {
   int32_t min_cost;            // of a CTA's share
   int64_t* plan_first;         // [B + 1][2] units and costs in front of each request
   ChunkStart* plan_start;      // [grid + 1]
+  int32_t* plan_count;         // [grid][2][4] parts of a unit's rows that are there
   float* part_o;               // [grid][2][256][d] fp32, not normalised
   float2* part_ml;             // [grid][2][256] (max in log2 units, sum)
   // filled by launch_chunk_mma: heads of a tile, parts of the G, tokens of a tile, virtual
   // heads (hkv * parts), bytes of a tile of q
   int32_t heads, parts, tokens, heads_all;
   uint32_t q_bytes;
+  int32_t out_wide;            // out starts on 32 bytes
 };
 cudaError_t launch_chunk(const ChunkArgs& a, int dtype, int head_dim, cudaStream_t stream);
 // On the tensor cores (vt_chunk_mma.cu): whether the caches' layout can be taken, the
