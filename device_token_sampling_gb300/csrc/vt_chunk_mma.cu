@@ -86,11 +86,13 @@ __device__ __forceinline__ int find_request(const int64_t* first, int stride, in
 // shares.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
   __shared__ Sums2 s_warp[33];
-  __shared__ int s_several;
+  __shared__ int64_t s_first[2 * (kPlanThreads + 1)];  // plan_first, where it fits
+  __shared__ int s_several, s_longest;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
-  if (tid == 0) s_several = 0;
+  if (tid == 0) s_several = s_longest = 0;
   for (int i = tid; i < 8 * a.grid; i += kPlanThreads) a.plan_count[i] = 0;
+  __syncthreads();
   int64_t units = 0, steps = 0;
   for (int base = 0; base < a.B; base += kPlanThreads) {
     const int b = base + tid;
@@ -101,6 +103,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       if (s0 < 0 || s0 > s1 || s1 > a.T) atomicOr(a.err_word, kErrBadRows);
       x = (int64_t)r.units * a.heads_all;
       for (int u = 0; u < r.units; ++u) y += unit_steps(a, r, u) * unit_weight(a, r, u);
+      if (r.units > 0) {
+        const int u = r.units - 1;
+        atomicMax(&s_longest, unit_steps(a, r, u) * (u > 0 ? 2 : unit_weight(a, r, u)));
+      }
       y *= a.heads_all;
       if (r.units > 1) s_several = 1;
     }
@@ -135,13 +141,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
     if (b < a.B) {
       a.plan_first[2 * (b + 1)] = units + x;
       a.plan_first[2 * (b + 1) + 1] = steps + y;
+      if (a.B <= kPlanThreads) {
+        s_first[2 * (b + 1)] = units + x;
+        s_first[2 * (b + 1) + 1] = steps + y;
+      }
     }
     units += s_warp[32].x;
     steps += s_warp[32].y;
   }
-  if (tid == 0) a.plan_first[0] = a.plan_first[1] = 0;
+  if (tid == 0) a.plan_first[0] = a.plan_first[1] = s_first[0] = s_first[1] = 0;
   __syncthreads();
-  const int64_t* first = a.plan_first;
+  const int64_t* first = a.B <= kPlanThreads ? s_first : a.plan_first;
   const int G = a.grid;
   const int rounds = s_several && units >= 2 * G ? (int)(units / G - 1) : 0;
   // the steps in front of the first unit that is shared out by steps
@@ -159,10 +169,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
     }
   }
   const int64_t todo = steps - skipped;
-  // (shares of min_cost at least, if that leaves some without)
-  const int64_t shares = max((int64_t)1, min((int64_t)G, todo / a.min_cost));
+  // Short units are not taken apart: a unit to a CTA, where there are enough CTAs.
+  // (Four requests of 5 new tokens behind up to 600 in 32 units of up to 5 steps: WHOLE.)
+  const bool whole = units <= G && s_longest <= a.whole_cost;
   for (int c = tid; c <= G; c += kPlanThreads) {
-    const int64_t at = skipped + (c >= shares ? todo : todo * c / shares);
+    int64_t at = whole ? steps : skipped + todo * c / G;
+    if (whole && c < units) {
+      const int b = find_request(first, 2, a.B, c);
+      const Request r = request(a, b);
+      int left = (int)(c - first[2 * b]);
+      at = first[2 * b + 1];
+      for (int u = r.units - 1; left > 0; --u) {
+        const int k = min(left, a.heads_all);
+        at += (int64_t)k * unit_steps(a, r, u) * unit_weight(a, r, u);
+        left -= k;
+      }
+    }
     ChunkStart s{};
     s.at = at;
     s.b = a.B;
@@ -369,52 +391,60 @@ __device__ __noinline__ void add_poison(const ChunkArgs& a, const Piece& p, uint
 // CTAs'.  A part that holds nothing (sum 0) is not read.
 template <typename T, int D>
 __device__ __noinline__ void join_rows(const ChunkArgs& a, int job, int last, int r0, int64_t row) {
-  constexpr int W = D / 32, kRows = 8;
+  constexpr int W = D / 32, kRows = 16;
   const int lane = threadIdx.x & 31;
   auto slot = [&](int k) { return (int64_t)(k == job ? 2 * job + 1 : 2 * k) * kUnitRows + r0; };
-  auto there = [&](int k) { return a.plan_start[k].at < a.plan_start[k + 1].at; };
+  // the CTAs from k0 on, 32 at most, that have a part: a bit each
+  auto parts = [&](int k0) {
+    const int k = k0 + lane;
+    return __ballot_sync(0xffffffffu, k <= last && a.plan_start[k].at < a.plan_start[k + 1].at);
+  };
   float m = -INFINITY, l = 0.f;
-  for (int k = job; k <= last; ++k) {
-    if (!there(k)) continue;
-    const float2 ml = row >= 0 ? __ldcg(a.part_ml + slot(k) + lane) : make_float2(-INFINITY, 0.f);
-    const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
-    l = l * ex2_approx(m - base) + (ml.y == 0.f ? 0.f : ml.y * ex2_approx(ml.x - base));
-    m = mn;
-  }
+  for (int k0 = job; k0 <= last; k0 += 32)
+#pragma unroll 4
+    for (uint32_t left = parts(k0); left; left &= left - 1) {
+      const float2 ml = row >= 0 ? __ldcg(a.part_ml + slot(k0 + __ffs(left) - 1) + lane)
+                                 : make_float2(-INFINITY, 0.f);
+      const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+      l = l * ex2_approx(m - base) + (ml.y == 0.f ? 0.f : ml.y * ex2_approx(ml.x - base));
+      m = mn;
+    }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
   for (int q = 0; q < 32; q += kRows) {
     if (!__any_sync(0xffffffffu, row >= 0 && lane >= q && lane < q + kRows)) continue;
     float acc[kRows][W] = {};
 #pragma unroll 1
-    for (int k = job; k <= last; ++k) {
-      if (!there(k)) continue;
-      float f = 0.f;  // this lane's row's
-      if (row >= 0) {
-        const float2 ml = __ldcg(a.part_ml + slot(k) + lane);
-        f = ml.y == 0.f ? 0.f : ex2_approx(ml.x - (m == -INFINITY ? 0.f : m)) * inv;
-      }
-      float x[kRows][W];
+    for (int k0 = job; k0 <= last; k0 += 32)
+#pragma unroll 1
+      for (uint32_t left = parts(k0); left; left &= left - 1) {
+        const int64_t at = slot(k0 + __ffs(left) - 1);
+        float x[kRows][W];
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const float* o = a.part_o + (slot(k) + q + i) * D + lane * W;
-        if constexpr (W == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(o));
-          x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
-          x[i][0] = v.x, x[i][1] = v.y;
+        for (int i = 0; i < kRows; ++i) {
+          const float* o = a.part_o + (at + q + i) * D + lane * W;
+          if constexpr (W == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(o));
+            x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
+            x[i][0] = v.x, x[i][1] = v.y;
+          }
+        }
+        float f = 0.f;  // this lane's row's
+        if (row >= 0) {
+          const float2 ml = __ldcg(a.part_ml + at + lane);
+          f = ml.y == 0.f ? 0.f : ex2_approx(ml.x - (m == -INFINITY ? 0.f : m)) * inv;
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const float fi = __shfl_sync(0xffffffffu, f, q + i);
+          if (fi != 0.f) {  // (a NaN too)
+#pragma unroll
+            for (int w = 0; w < W; ++w) acc[i][w] += x[i][w] * fi;
+          }
         }
       }
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, q + i);
-        if (fi != 0.f) {  // (a NaN too)
-#pragma unroll
-          for (int w = 0; w < W; ++w) acc[i][w] += x[i][w] * fi;
-        }
-      }
-    }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int64_t to = __shfl_sync(0xffffffffu, row, q + i);
