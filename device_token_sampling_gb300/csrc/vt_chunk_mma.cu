@@ -23,8 +23,9 @@ constexpr int kMasks = 8;     // steps whose token masks are kept
 constexpr int kHalfStep = kTileTokens / 2;  // tokens of one product
 constexpr int kWeights = kTileTokens;       // tensor memory: S, then each tile's P, then O
 // warps: the softmax of each tile; then one each for the scores, the products of each
-// tile, the copies of K and V of even and of odd steps, the pieces and their Q
-constexpr int kScoreWarp = 8, kProductWarp = 9, kKvWarp = 11, kPieceWarp = 13;
+// tile, the copies of K and V of even and of odd steps, the pieces and their Q; two that
+// look through V
+constexpr int kScoreWarp = 8, kProductWarp = 9, kKvWarp = 11, kPieceWarp = 13, kLookWarp = 14;
 
 // ---- the units ----------------------------------------------------------------
 // Heads in one tile: a.heads of the G, a.parts times; tokens in one tile: a.tokens.  A
@@ -56,9 +57,14 @@ __device__ __forceinline__ int unit_end(const ChunkArgs& a, const Request& r, in
 __device__ __forceinline__ int unit_steps(const ChunkArgs& a, const Request& r, int u) {
   return max(1, (unit_end(a, r, u) + kTileTokens - 1) / kTileTokens);
 }
-// What a step of it costs: two tiles take turns on a unit that fits one.
+// What a step of it costs (two tiles take turns on a unit that fits one),
 __device__ __forceinline__ int unit_weight(const ChunkArgs& a, const Request& r, int u) {
   return unit_tokens(a, r, u) > a.tokens ? 2 : 1;
+}
+// and what beginning and ending it costs besides.
+constexpr int kUnitCost = 6;
+__device__ __forceinline__ int64_t unit_cost(const ChunkArgs& a, const Request& r, int u) {
+  return kUnitCost + (int64_t)unit_steps(a, r, u) * unit_weight(a, r, u);
 }
 // The order of a request's units: the longest first, its heads side by side.  (So CTAs
 // that run at the same time read the same keys and values from L2.)
@@ -102,7 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       const int s0 = a.starts[b], s1 = a.starts[b + 1];
       if (s0 < 0 || s0 > s1 || s1 > a.T) atomicOr(a.err_word, kErrBadRows);
       x = (int64_t)r.units * a.heads_all;
-      for (int u = 0; u < r.units; ++u) y += unit_steps(a, r, u) * unit_weight(a, r, u);
+      for (int u = 0; u < r.units; ++u) y += unit_cost(a, r, u);
       if (r.units > 0) {
         const int u = r.units - 1;
         atomicMax(&s_longest, unit_steps(a, r, u) * (u > 0 ? 2 : unit_weight(a, r, u)));
@@ -154,8 +160,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
   const int64_t* first = a.B <= kPlanThreads ? s_first : a.plan_first;
   const int G = a.grid;
   const int rounds = s_several && units >= 2 * G ? (int)(units / G - 1) : 0;
-  // the steps in front of the first unit that is shared out by steps
-  int64_t skipped = 0;
+  // what the units cost that whole rounds take, and each CTA's of them
+  int64_t skipped = 0, want = 0;
   if (rounds > 0) {
     const int64_t u = (int64_t)rounds * G;
     const int b = find_request(first, 2, a.B, u);
@@ -164,16 +170,44 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
     skipped = first[2 * b + 1];
     for (int v = r.units - 1; left > 0; --v) {
       const int64_t k = min(left, (int64_t)a.heads_all);
-      skipped += k * unit_steps(a, r, v) * unit_weight(a, r, v);
+      skipped += k * unit_cost(a, r, v);
       left -= k;
     }
   }
   const int64_t todo = steps - skipped;
+  // The rest goes in shares that make up for it: up to the mean of all.  (Equal shares
+  // left the CTAs' sums 9 % apart on 4 prompts of up to 4096 tokens.)
+  if (tid < G) {
+    want = steps / G + 1;
+    for (int i = 0; i < rounds; ++i) {
+      const int64_t u = (int64_t)i * G + (i & 1 ? G - 1 - tid : tid);
+      const int b = find_request(first, 2, a.B, u);
+      const Request r = request(a, b);
+      want -= unit_cost(a, r, r.units - 1 - (int)(u - first[2 * b]) / a.heads_all);
+    }
+    want = max(want, (int64_t)0);
+  }
+  int64_t upto = want;  // of the CTAs up to this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += up;
+  }
+  if (lane == 31) s_warp[warp + 1].x = upto;
+  __syncthreads();
+  int64_t all = 0, before = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w < warp) before += s_warp[w + 1].x;
+    all += s_warp[w + 1].x;
+  }
+  before += upto - want;
   // Short units are not taken apart: a unit to a CTA, where there are enough CTAs.
-  // (Four requests of 5 new tokens behind up to 600 in 32 units of up to 5 steps: WHOLE.)
+  // (Four requests of 5 new tokens behind up to 600, 32 units of up to 5 steps: 21.6 us,
+  // in shares of 2 steps 33.)
   const bool whole = units <= G && s_longest <= a.whole_cost;
-  for (int c = tid; c <= G; c += kPlanThreads) {
-    int64_t at = whole ? steps : skipped + todo * c / G;
+  const int c = tid;
+  if (c <= G) {
+    int64_t at = whole ? steps : c == G ? steps : skipped + todo * before / max(all, (int64_t)1);
     if (whole && c < units) {
       const int b = find_request(first, 2, a.B, c);
       const Request r = request(a, b);
@@ -181,7 +215,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       at = first[2 * b + 1];
       for (int u = r.units - 1; left > 0; --u) {
         const int k = min(left, a.heads_all);
-        at += (int64_t)k * unit_steps(a, r, u) * unit_weight(a, r, u);
+        at += k * unit_cost(a, r, u);
         left -= k;
       }
     }
@@ -195,7 +229,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       int u = r.units - 1;
       int64_t each = 0;
       for (;; --u) {
-        each = (int64_t)unit_steps(a, r, u) * unit_weight(a, r, u);
+        each = unit_cost(a, r, u);
         if (u == 0 || left < each * a.heads_all) break;
         left -= each * a.heads_all;
       }
@@ -203,8 +237,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       s.unit = u;
       s.head = (int)(left / each);
       const int in = (int)(left % each), w = unit_weight(a, r, u);
-      s.step = in / w;  // (a whole step)
-      s.at -= in % w;
+      s.step = max(in - kUnitCost, 0) / w;  // (a whole step)
+      s.at += (s.step > 0 ? kUnitCost + s.step * w : 0) - in;
     }
     s.rounds = rounds;
     a.plan_start[c] = s;
@@ -481,11 +515,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (int i = 0; i < R; ++i) {
       mbar_init(&sh.full[0][i], 1);
       mbar_init(&sh.full[1][i], 1);
-      mbar_init(&sh.empty[i], 2);  // (both tiles' MMAs)
+      mbar_init(&sh.empty[i], i & 1 ? 4 : 2);  // (both tiles' MMAs; V: who looks through it)
     }
     for (int i = 0; i < kPieces; ++i) {
       mbar_init(&sh.piece_full[i], 1);
-      mbar_init(&sh.piece_empty[i], kPieceWarp);  // (every warp before that)
+      mbar_init(&sh.piece_empty[i], 15);  // (every other warp)
     }
     for (int t = 0; t < 2; ++t) {
       for (int h = 0; h < 2; ++h) {
@@ -495,7 +529,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_init(&sh.s_full[t], 1);
       mbar_init(&sh.o_done[t], 1);
       mbar_init(&sh.o_empty[t], 4);
-      for (int i = 0; i < 4; ++i) mbar_init(&sh.v_ok[t][i], 4);
+      for (int i = 0; i < 4; ++i) mbar_init(&sh.v_ok[t][i], 2);
       mbar_init(&sh.q_full[t], 1);
       mbar_init(&sh.q_empty[t], 1);
     }
@@ -541,9 +575,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // (a scale of 0 as one that leaves masked scores at -inf)
     const float sc = fmaxf(fabsf(a.scale_log2), 1e-30f);
     const uint64_t sc2 = pack_f2(sc, sc);
-    // this tile's steps; units, and those that the tiles share; the CTA's steps; of the
-    // ring's places by set and of v_ok, the parities of their uses
-    uint32_t steps = 0, units = 0, shared = 0, all = 0, full_ph[2] = {0, 0}, ok_ph = 0;
+    // this tile's steps; units, and those that the tiles share; the CTA's steps; the
+    // parities of v_ok's uses
+    uint32_t steps = 0, units = 0, shared = 0, all = 0, ok_ph = 0;
     Piece p;
     while (ok && next_piece(p)) {
       const bool two = p.tokens > a.tokens;  // else the tiles share the unit
@@ -567,33 +601,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         ok = warp_wait(&sh.s_full[t], steps & 1, limit);
         if (!ok) break;
         fence_after();
-        if (diagonal && (t == 0 || !two)) {
-          // Tokens of V that are not finite are taken out of it.  (The scores are there, and
-          // the last product but one, so the last V of this place has been used.)
-          const int st = place<R>(g, 1);
-          const uint32_t ph = ((two ? full_ph[0] : full_ph[1]) >> st) + (j - p.t0) / (R / 2);
-          if (steps > 0) ok = warp_wait(&sh.pv_done[t][0], (steps - 1) & 1, limit);
-          if (ok) ok = warp_wait(&sh.full[!two][st], ph & 1, limit);
-          if (!ok) break;
-          uint4* row = reinterpret_cast<uint4*>(dyn + L::kKv + st * L::kTile + in * 128);
-          uint32_t bad = 0;
-#pragma unroll
-          for (int q = 0; q < D / 64; ++q)
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              bad |= not_finite<T>(row[q * (L::kHalf / 16) + ((c + in) & 7)]);
-          if (bad) {
-#pragma unroll
-            for (int q = 0; q < D / 64; ++q)
-              for (int c = 0; c < 8; ++c)
-                row[q * (L::kHalf / 16) + ((c + in) & 7)] = make_uint4(0, 0, 0, 0);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          }
-          const uint32_t word = __ballot_sync(0xffffffffu, bad && j * kTileTokens + in < p.end);
-          if (lane == 0) sh.poison[g & 3][warp & 3] = word;
-          warp_arrive(&sh.v_ok[t][g & 3]);
-          if (two) warp_arrive(&sh.v_ok[1][g & 3]);
-        }
         if (!warp_live) {  // (the products of these rows are never read)
           warp_arrive(&sh.s_free);
           if (diagonal) {
@@ -734,12 +741,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         l += s0 + s1;
       }
       if (!ok) break;
-      for (int c = 0; c < R / 2; ++c) {  // uses of V's places: every (R / 2)-th step each
-        const uint32_t uses = (uint32_t)(n + R / 2 - 1 - c) / (R / 2);
-        const uint32_t flip = (uses & 1) << place<R>(all + c, 1);
-        if (two) full_ph[0] ^= flip;
-        else full_ph[1] ^= flip;
-      }
       all += n;
       // (every unit's, so that a parity is the last unit's)
       ok = warp_wait(&sh.o_empty[t], (units & 1) ^ 1, limit);
@@ -950,11 +951,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           p.slot = -1;
           if (!whole) {  // the rest of a unit, or of this CTA's share
             const int w = unit_weight(a, r, pu);
+            const int64_t begin = at - (step > 0 ? kUnitCost + (int64_t)step * w : 0);
+            const int64_t end = begin + kUnitCost + (int64_t)n * w;
             p.t0 = step;
-            p.t1 = (int)min((int64_t)n, step + (stop - at) / w);
+            p.t1 = stop >= end ? n : (int)((stop - begin - kUnitCost) / w);
             p.slot = step > 0 ? 2 * c : p.t1 < n ? 2 * c + 1 : -1;
             if (p.slot >= 0) {  // who else has some of the unit
-              const int64_t begin = at - (int64_t)p.t0 * w, end = begin + (int64_t)n * w;
               p.job = c;
               while (p.job > 0 && a.plan_start[p.job].at > begin) --p.job;
               p.last = c;
@@ -962,7 +964,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               for (int q = p.job; q <= p.last; ++q)
                 p.parts += a.plan_start[q].at < a.plan_start[q + 1].at;
             }
-            at += (int64_t)(p.t1 - p.t0) * w;
+            at = min(end, stop);
             step = 0;
             if (++head == a.heads_all) {
               head = 0;
@@ -997,6 +999,51 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // no copy is in flight when the CTA's memory goes to another
       for (int t = 0; t < 2; ++t)
         if (uses[t] > 0) mbar_wait_clocked(&sh.q_full[t], (uses[t] - 1) & 1, kDrainCycles);
+    } else if (warp >= kLookWarp) {
+      // ---- V of the steps that some row does not attend to the whole of -----------------------
+      // Its weights there are 0, but 0 times an infinity or a NaN is NaN: tokens that are
+      // not finite are taken out.  64 tokens to a warp, two to a lane.
+      const int mine = warp - kLookWarp;
+      uint32_t all = 0, full_ph[2] = {0, 0};
+      Piece p;
+      while (ok && next_piece(p)) {
+        const bool two = p.tokens > a.tokens;
+        uint32_t ph = two ? full_ph[0] : full_ph[1];
+        for (int j = p.t0; j < p.t1 && ok; ++j, ++all) {
+          const int st = place<R>(all, 1);
+          ok = warp_wait(&sh.full[!two][st], (ph >> st) & 1, limit);
+          ph ^= 1u << st;
+          if (!ok) break;
+          if ((j + 1) * kTileTokens > max(p.lim0, 0)) {
+            bool found = false;
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              const int token = (mine * 2 + q) * 32 + lane;
+              uint4* row = reinterpret_cast<uint4*>(dyn + L::kKv + st * L::kTile + token * 128);
+              uint32_t bad = 0;
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  bad |= not_finite<T>(row[h * (L::kHalf / 16) + ((i + lane) & 7)]);
+              if (bad) {
+                found = true;
+#pragma unroll 1
+                for (int h = 0; h < D / 64; ++h)
+                  for (int i = 0; i < 8; ++i) row[h * (L::kHalf / 16) + i] = make_uint4(0, 0, 0, 0);
+              }
+              const uint32_t word = __ballot_sync(0xffffffffu, bad && j * kTileTokens + token < p.end);
+              if (lane == 0) sh.poison[all & 3][mine * 2 + q] = word;
+            }
+            if (found) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            const int from = two ? 0 : all & 1, to = two ? 2 : from + 1;
+            for (int t = from; t < to; ++t) warp_arrive(&sh.v_ok[t][all & 3]);
+          }
+          warp_arrive(&sh.empty[st]);
+        }
+        if (two) full_ph[0] = ph;
+        else full_ph[1] = ph;
+      }
     } else if (warp < kKvWarp) {
       // ---- MMAs: a warp to the scores of both tiles by turns, one to each tile's products,
       // walk the steps and wait; one lane issues
