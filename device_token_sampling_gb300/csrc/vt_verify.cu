@@ -9,7 +9,7 @@
 //   token = the first j with r_0 + .. + r_j > u * (r_0 + .. + r_{V-1}).
 // The tokens then have the target's distribution.  Both decisions are exact: the
 // product of two 24-bit mantissas fits 64 bits, and the sums are integers of 2^-54,
-// p and q converted on their own (values below 2^-31 are cut to 2^-54).  So no order
+// p and q converted on their own (to the nearest; exact from 2^-31 on).  So no order
 // of summing and no number of CTAs changes a token.
 //
 // One launch.  A cluster of CTAs shares a request: each finds `a` itself (2 K values),
@@ -24,7 +24,7 @@
 namespace vt {
 namespace {
 
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 256;
 constexpr int kVerWarps = kVerThreads / 32;
 constexpr int kVerMaxCtas = 16;
 
@@ -53,29 +53,58 @@ struct Wide<__nv_bfloat16> {
   static __device__ __forceinline__ float one(__nv_bfloat16 v) { return __bfloat162float(v); }
 };
 
-// (these shifts give 0 for amounts of 32 and more)
-__device__ __forceinline__ uint32_t shl_clamped(uint32_t x, uint32_t n) {
-  uint32_t r;
-  asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(n));
+// A value v in [0, 2) as a whole number of 2^-54, by three additions whose roundings
+// leave multiples of 2^-21, 2^-44 and 2^-54 (of v, of what is left, of what is left of
+// that); the rests are exact.  The wholes are the differences of the sums' bits to those
+// of the constants, so that sums of wholes are sums of bits.
+constexpr float kC1 = 6.f, kC2 = 6.f / (1 << 23), kC3 = 1.5f / (1u << 31);
+constexpr uint32_t kB1 = 0x40c00000u, kB2 = 0x35400000u, kB3 = 0x30400000u;  // their bits
+__device__ __forceinline__ uint64_t whole(uint32_t s1, uint32_t s2, uint32_t s3) {
+  return ((uint64_t)s1 << 33) + (uint64_t)((int64_t)(int32_t)s2 << 10) +
+         (uint64_t)(int64_t)(int32_t)s3;
+}
+__device__ __forceinline__ uint64_t fixed(float v) {
+  const float a = __fadd_rn(v, kC1), r = __fsub_rn(v, __fsub_rn(a, kC1));
+  const float b = __fadd_rn(r, kC2), q = __fsub_rn(r, __fsub_rn(b, kC2));
+  const float c = __fadd_rn(q, kC3);
+  return whole(__float_as_uint(a) - kB1, __float_as_uint(b) - kB2, __float_as_uint(c) - kB3);
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
   return r;
 }
-__device__ __forceinline__ uint32_t shr_clamped(uint32_t x, uint32_t n) {
-  uint32_t r;
-  asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(n));
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   return r;
 }
-// v in units of 2^-54, 0 <= v < 2: mantissa * 2^(exponent - 96), of which one of the
-// two terms is 0.
-__device__ __forceinline__ void add_fixed(float v, uint64_t& sum, uint32_t& small) {
-  const uint32_t b = __float_as_uint(v), e = b >> 23, m = (b & 0x7fffffu) | 0x800000u;
-  sum += (uint64_t)m * shl_clamped(1u, e - 96u);
-  small += shr_clamped(m >> 1, 95u - e);
+__device__ __forceinline__ uint64_t sub2(uint64_t x, uint64_t y) {  // x - y
+  uint64_t r;
+  const uint64_t minus = 0xbf800000bf800000ull;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(y), "l"(minus), "l"(x));
+  return r;
+}
+// Two values at once into the three sums of bits (out of them for kSign -1).
+template <int kSign>
+__device__ __forceinline__ void add_bits(uint64_t v, uint32_t (&s)[3]) {
+  const uint64_t c1 = 0x40c0000040c00000ull, c2 = 0x3540000035400000ull,
+                 c3 = 0x3040000030400000ull;
+  const uint64_t a = add2(v, c1), r = sub2(v, sub2(a, c1));
+  const uint64_t b = add2(r, c2), q = sub2(r, sub2(b, c2));
+  const uint64_t c = add2(q, c3);
+  const uint64_t w[3] = {a, b, c};
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (kSign > 0) s[i] += (uint32_t)w[i] + (uint32_t)(w[i] >> 32);
+    else s[i] -= (uint32_t)w[i] + (uint32_t)(w[i] >> 32);
+  }
 }
 
 struct Sum {
   uint64_t mass = 0;
-  uint32_t top = 0;   // the largest magnitude's bits
-  float rough = 0.f;  // tells a sum that would not fit
+  uint32_t bits = 0;  // of all values, together
+  uint32_t over = 0;  // of the masses' upper halves on the way, together
 };
 
 // The row that the token is drawn from: p, less q where there is one, without `skip`.
@@ -84,36 +113,12 @@ struct Row {
   const T* p;
   const T* q;
   int skip;
-  bool vec;  // 16-byte loads
+  bool vec;    // 16-byte loads
+  bool clamp;  // values below 0 are met: they count as 0
 };
 
-// Adds the elements of a lane's E of a block of 32 E (from element j, below `end`).
-template <typename T, bool Q>
-__device__ __forceinline__ void add_block(const float (&p)[Wide<T>::E], const float (&q)[Wide<T>::E],
-                                          int j, int skip, Sum& s) {
-  constexpr int E = Wide<T>::E;
-  uint64_t less = 0;
-  uint32_t small = 0, small_less = 0;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    s.top = max(s.top, __float_as_uint(p[i]) & 0x7fffffffu);
-    if constexpr (Q) {
-      s.top = max(s.top, __float_as_uint(q[i]) & 0x7fffffffu);
-      const float b = fmaxf(q[i], 0.f);
-      const bool more = p[i] > b;
-      const float v = more ? p[i] : 0.f;
-      add_fixed(v, s.mass, small);
-      add_fixed(more ? b : 0.f, less, small_less);
-      s.rough += v;
-    } else {
-      const float v = j + i == skip ? 0.f : fmaxf(p[i], 0.f);
-      add_fixed(v, s.mass, small);
-      s.rough += v;
-    }
-  }
-  s.mass += small;
-  if constexpr (Q) s.mass -= less + small_less;
-}
+// (a NaN stays one)
+__device__ __forceinline__ float at_least_0(float v) { return v <= 0.f ? 0.f : v; }
 
 // A lane's E elements from j on, zeros past `end`.
 template <typename T>
@@ -128,24 +133,60 @@ __device__ __forceinline__ void load_part(const T* row, int j, int end, bool vec
   }
 }
 
-// Elements [lo, hi) of the row over the lanes of a warp; lo a multiple of 32 E.
+// Adds N elements, max(p - q, 0) of each: p less the smaller of p and q.  Values below 0
+// and of 2 and more show in `bits` (bits 31 and 30), and the sum is not used then.
+template <bool Q, int N>
+__device__ __forceinline__ void add_values(const float (&p)[N], const float (&q)[N], Sum& s) {
+  uint32_t t[3] = {};
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    s.bits |= __float_as_uint(p[i]) | __float_as_uint(p[i + 1]);
+    add_bits<1>(pair(p[i], p[i + 1]), t);
+    if constexpr (Q) {
+      s.bits |= __float_as_uint(q[i]) | __float_as_uint(q[i + 1]);
+      add_bits<-1>(pair(fminf(p[i], q[i]), fminf(p[i + 1], q[i + 1])), t);
+    }
+  }
+  constexpr uint32_t n = Q ? 0 : N;
+  s.mass += whole(t[0] - n * kB1, t[1] - n * kB2, t[2] - n * kB3);
+  s.over |= (uint32_t)(s.mass >> 32);
+}
+
+// Elements [lo, hi) of the row over the lanes of a warp, the next loads under way while
+// some are added; lo a multiple of 32 E.
 template <typename T, bool Q>
 __device__ __forceinline__ void add_range(const Row<T>& r, int lo, int hi, Sum& s) {
-  constexpr int E = Wide<T>::E, kStep = 32 * E, kAhead = Q ? 2 : 4;
+  constexpr int E = Wide<T>::E, kStep = 32 * E, kAhead = 8 / E;
   const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int j0 = lo; j0 < hi; j0 += kAhead * kStep) {
-    float p[kAhead][E], q[kAhead][E];
+  float p[kAhead][E], q[kAhead][E];
+  auto load = [&](int j0) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       const int j = j0 + a * kStep + lane * E;
       load_part(r.p, j, hi, r.vec, p[a]);
       if constexpr (Q) load_part(r.q, j, hi, r.vec, q[a]);
     }
+    if (r.clamp)
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a)
-      add_block<T, Q>(p[a], q[a], j0 + a * kStep + lane * E, r.skip, s);
+      for (int i = 0; i < kAhead * E; ++i) {
+        p[i / E][i % E] = at_least_0(p[i / E][i % E]);
+        if constexpr (Q) q[i / E][i % E] = at_least_0(q[i / E][i % E]);
+      }
+  };
+  if (lo < hi) load(lo);
+#pragma unroll 1
+  for (int j0 = lo; j0 < hi; j0 += kAhead * kStep) {
+    float x[kAhead * E], y[kAhead * E];
+#pragma unroll
+    for (int i = 0; i < kAhead * E; ++i) {
+      x[i] = p[i / E][i % E];
+      y[i] = Q ? q[i / E][i % E] : 0.f;
+    }
+    if (j0 + kAhead * kStep < hi) load(j0 + kAhead * kStep);
+    add_values<Q, kAhead * E>(x, y, s);
   }
+  if (!Q && r.skip >= lo && r.skip < hi && lane == (r.skip - lo) / E % 32)
+    s.mass -= fixed(r.clamp ? at_least_0(Wide<T>::one(r.p[r.skip])) : Wide<T>::one(r.p[r.skip]));
 }
 template <typename T>
 __device__ __forceinline__ void add_range(const Row<T>& r, int lo, int hi, Sum& s) {
@@ -193,14 +234,13 @@ __device__ __forceinline__ void store_remote(uint64_t* at, uint32_t rank, uint64
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyArgs a) {
+__global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(VerifyArgs a) {
   constexpr int E = Wide<T>::E, kStep = 32 * E;
   __shared__ int s_accepted;
   __shared__ uint64_t s_warp[kVerWarps];
-  // of each CTA of the cluster: its sum, and 1 where a value is not a probability; two
-  // rounds, the second where the difference has no mass
+  // of each CTA of the cluster: its sum, and what was met; by turns
   __shared__ uint64_t s_mass[2][kVerMaxCtas], s_bad[2][kVerMaxCtas];
-  __shared__ uint32_t s_wrong[kVerWarps];
+  __shared__ uint32_t s_bits[kVerWarps];
   __shared__ float s_rough[kVerWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = a.ctas, rank = (int)cluster_ctarank();
@@ -209,6 +249,15 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyArgs a) {
   cluster_arrive();  // (the others' shared memory may be written behind the wait)
 
   // ---- how many drafts are accepted
+  // (what does not depend on anything is asked for at once)
+  const int32_t* tokens = a.tokens + (int64_t)b * K;
+  const float* uniforms = a.uniforms + (int64_t)b * (K + 1);
+  int x = -1;
+  float u = 0.f;
+  if (warp == 0 && lane < K) {
+    x = tokens[lane];
+    u = uniforms[lane];
+  }
   int n = a.lens ? min(max(a.lens[b], 0), K) : K;
   const T* target;
   bool rows = true;
@@ -221,21 +270,21 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyArgs a) {
     target = static_cast<const T*>(a.target) + b * a.t_batch;
   }
   const T* draft = static_cast<const T*>(a.draft);
-  const int32_t* tokens = a.tokens + (int64_t)b * K;
-  const float* uniforms = a.uniforms + (int64_t)b * (K + 1);
   if (draft) draft += b * a.d_batch;
   if (warp == 0) {
     int first = rows ? n : 0;
     for (int i0 = 0; i0 < first; i0 += 32) {
       const int i = i0 + lane;
       bool no = false;
+      if (i0 > 0 && i < n) {
+        x = tokens[i];
+        u = uniforms[i];
+      }
       if (i < n) {
-        const int x = tokens[i];
         no = true;
         if (x >= 0 && x < a.V) {
           const double p = Wide<T>::one(target[i * a.t_row + x]);
           const double q = draft ? Wide<T>::one(draft[i * a.d_row + x]) : 1.f;
-          const float u = uniforms[i];
           no = !((u > 0.f ? (double)u : 0.) * q < p);
         }
       }
@@ -254,6 +303,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyArgs a) {
   row.q = refused && draft ? draft + acc * a.d_row : nullptr;
   row.skip = refused && !draft ? tokens[acc] : -1;
   row.vec = a.vec;
+  row.clamp = false;
   // whole blocks to a warp
   const int chunk = ((a.V + ctas * kVerWarps - 1) / (ctas * kVerWarps) + kStep - 1) / kStep * kStep;
   const int64_t from = (int64_t)rank * kVerWarps * chunk;
@@ -264,31 +314,34 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyArgs a) {
   uint64_t total = 0, before = 0, mine = 0;
   bool bad = false;
   cluster_wait();
-  for (int round = 0; round < 2; ++round) {
+  for (int round = 0;; ++round) {  // (four at most)
     Sum s;
     int lo, hi;
     warp_range(warp, lo, hi);
     if (rows) add_range(row, lo, hi, s);
+    // the sum, roughly, where a lane's may not have fit: large
+    const float rough =
+        warp_sum_f(s.over & 0xc0000000u ? 1e9f : (float)(uint32_t)(s.mass >> 44) * (1.f / 1024.f));
     const uint64_t mass = warp_sum_u64(s.mass);
-    const float rough = warp_sum_f(s.rough);
-    const uint32_t top = __reduce_max_sync(0xffffffffu, s.top);
+    const uint32_t bits = __reduce_or_sync(0xffffffffu, s.bits);
     __syncthreads();
     if (lane == 0) {
       s_warp[warp] = mass;
-      // 2 and more, infinities and NaN; or a sum that may not fit
-      s_wrong[warp] = top >= 0x40000000u || !(rough < 512.f);
+      s_bits[warp] = bits;
       s_rough[warp] = rough;
     }
     __syncthreads();
+    const int turn = round & 1;
     if (warp == 0) {
       const uint64_t m = warp_sum_u64(lane < kVerWarps ? s_warp[lane] : 0);
-      const uint32_t wrong = __any_sync(0xffffffffu, lane < kVerWarps && s_wrong[lane]);
+      const uint32_t any = __reduce_or_sync(0xffffffffu, lane < kVerWarps ? s_bits[lane] : 0u);
       const float r = warp_sum_f(lane < kVerWarps ? s_rough[lane] : 0.f);
-      // (the rough sum travels beside the flag, in whole units)
-      const uint64_t flag = wrong || !(r < 512.f) ? 1u << 20 : (uint32_t)r;
+      // the sum in whole units (bits 0..19), values below 0 (20..), no probabilities (32..)
+      const uint64_t flag = (uint64_t)fminf(r, 1024.f) + ((uint64_t)(any >> 31) << 20) +
+                            ((uint64_t)((any >> 30) & 1) << 32);
       if (lane < ctas) {
-        store_remote(&s_mass[round][rank], lane, m);
-        store_remote(&s_bad[round][rank], lane, flag);
+        store_remote(&s_mass[turn][rank], lane, m);
+        store_remote(&s_bad[turn][rank], lane, flag);
       }
     }
     cluster_arrive();
@@ -296,18 +349,23 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyArgs a) {
     total = before = 0;
     uint64_t flags = 0;
     for (int c = 0; c < ctas; ++c) {
-      const uint64_t m = s_mass[round][c];
+      const uint64_t m = s_mass[turn][c];
       if (c < rank) before += m;
       if (c == rank) mine = m;
       total += m;
-      flags += s_bad[round][c];
+      flags += s_bad[turn][c];
     }
-    bad = flags >= 512;
+    if (((flags >> 20) & 0xfff) != 0 && !row.clamp) {
+      row.clamp = true;
+      continue;
+    }
+    bad = (flags >> 32) != 0 || (flags & 0xfffff) >= 512;
     // nothing left of the target's row (a drafter above it everywhere): drawn from it
     // as it is
-    if (bad || total != 0 || !refused) break;
+    if (bad || total != 0 || !(row.q || row.skip >= 0)) break;
     row.q = nullptr;
     row.skip = -1;
+    row.clamp = false;
   }
 
   // ---- the outputs
@@ -325,7 +383,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyArgs a) {
   const uint64_t t = target_of(uniforms[K], total);
   if (t < before || t - before >= mine) return;
 
-  // ---- the token: the warp's chunk, a sixteenth of it, the block, the lane, the element
+  // ---- the token: the warp's chunk, a part of it, the block, the lane, the element
   uint64_t left = t - before;
   int w = 0;
   while (w + 1 < kVerWarps && left >= s_warp[w]) left -= s_warp[w++];
@@ -350,31 +408,29 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(VerifyArgs a) {
     float p[E], q[E];
     load_part(row.p, j, p_hi, row.vec, p);
     if (row.q) load_part(row.q, j, p_hi, row.vec, q);
-    Sum own;
-    if (row.q) add_block<T, true>(p, q, j, row.skip, own);
-    else add_block<T, false>(p, q, j, row.skip, own);
-    const uint64_t upto = warp_scan_u64(own.mass);
+    uint64_t each[E], own = 0;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      if (row.clamp) p[i] = at_least_0(p[i]);
+      each[i] = j + i == row.skip ? 0 : fixed(p[i]);
+      if (row.q) each[i] -= fixed(fminf(p[i], row.clamp ? at_least_0(q[i]) : q[i]));
+      own += each[i];
+    }
+    const uint64_t upto = warp_scan_u64(own);
     const uint64_t block = __shfl_sync(0xffffffffu, upto, 31);
     if (left >= block) {
       left -= block;
       continue;
     }
-    if (left < upto && left >= upto - own.mass) {
-      uint64_t rest = left - (upto - own.mass);
+    if (left < upto && left >= upto - own) {
+      uint64_t rest = left - (upto - own);
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        // the element alone, by the same arithmetic
-        float pe[E] = {}, qe[E] = {};
-        pe[0] = p[i];
-        if (row.q) qe[0] = q[i];
-        Sum e;
-        if (row.q) add_block<T, true>(pe, qe, j + i, row.skip, e);
-        else add_block<T, false>(pe, qe, j + i, row.skip, e);
-        if (rest < e.mass) {
+        if (rest < each[i]) {
           out[acc] = j + i;
           break;
         }
-        rest -= e.mass;
+        rest -= each[i];
       }
     }
     break;
@@ -405,9 +461,9 @@ cudaError_t prepare_verify() {
 }
 
 cudaError_t launch_verify(VerifyArgs a, int dtype, int num_sms, cudaStream_t stream) {
-  // CTAs to a request until there are two for every SM, 4096 elements to each at least
+  // CTAs to a request until there are four for every SM, 4096 elements to each at least
   a.ctas = 1;
-  while (a.ctas < kVerMaxCtas && (int64_t)a.ctas * a.B < 2 * num_sms && a.V / a.ctas >= 8192)
+  while (a.ctas < kVerMaxCtas && (int64_t)a.ctas * a.B < 4 * num_sms && a.V / a.ctas >= 8192)
     a.ctas *= 2;
   return dtype == VT_DTYPE_F32 ? launch_typed<float>(a, stream)
                                : launch_typed<__nv_bfloat16>(a, stream);
