@@ -32,6 +32,16 @@ def _ids(t, name, device, size=None, dtype=_I32):
     return t.data_ptr()
 
 
+def _outputs(out, names, sizes, place, device, other):
+    """int32 outputs of ``sizes`` elements, new ones where ``out`` is None, and their addresses."""
+    if out is None:
+        empty = torch.empty
+        out = make_on(other, lambda: tuple([empty(n, dtype=_I32, device=place) for n in sizes]))
+        return out, [t.data_ptr() for t in out]
+    return out, [_ids(t, "out " + nm, device, n)
+                 for t, nm, n in zip(out, names, sizes, strict=True)]
+
+
 class PagedBatch:
     """One ``vt_paged`` handle: a batch of requests over a paged cache."""
 
@@ -294,13 +304,8 @@ class PagedBatch:
         p_table, ld = self._table(table, B, self.cfg.max_blocks)
         p_out, ld_out = self._table(out_table, R, self.cfg.max_blocks, "out_table")
         other = other_stream(stream)
-        sizes = (R, R, 1, R, R, R)
-        if out is None:
-            place = seq_lens.device
-            out = make_on(other, lambda: tuple(
-                torch.empty(n, dtype=_I32, device=place) for n in sizes))
-        names = ("held", "seq_lens", "cursor", "src", "dst", "status")
-        po = [_ids(t, "out " + nm, dev, n) for t, nm, n in zip(out, names, sizes, strict=True)]
+        out, po = _outputs(out, ("held", "seq_lens", "cursor", "src", "dst", "status"),
+                           (R, R, 1, R, R, R), seq_lens.device, dev, other)
         rc = self._lib.vt_paged_fork(
             self._h, R, p_parents, B, p_table, ld, p_held, p_seq, p_free, free_blocks.shape[0],
             p_cursor, p_out, ld_out, *po, raw_stream(stream, dev))
@@ -320,12 +325,8 @@ class PagedBatch:
         a ``stream`` that is not the current one the inputs have to be ready there, and the
         outputs are."""
         args, other, ins = self._reclaim(table, held, seq_lens, num_blocks, prefix_blocks, stream)
-        sizes = (seq_lens.shape[0], num_blocks, 1)
-        if out is None:
-            out = make_on(other, lambda: tuple(
-                torch.empty(n, dtype=_I32, device=seq_lens.device) for n in sizes))
-        po = [_ids(t, "out " + nm, self.device, n)
-              for t, nm, n in zip(out, ("held", "free_blocks", "cursor"), sizes, strict=True)]
+        out, po = _outputs(out, ("held", "free_blocks", "cursor"), (args[0], num_blocks, 1),
+                           seq_lens.device, self.device, other)
         rc = self._lib.vt_paged_release(self._h, *args, *po, raw_stream(stream, self.device))
         if rc != VT_OK:
             self._check(rc, "vt_paged_release")
@@ -348,13 +349,9 @@ class PagedBatch:
             out_table = table
         p_table, ld_out = self._table(out_table, B, self.cfg.max_blocks, "out_table")
         n_prefix, most = args[6], num_blocks // 2
-        sizes = (B, num_blocks, 1, most, most, 1, n_prefix)
-        if out is None:
-            out = make_on(other, lambda: tuple(
-                torch.empty(n, dtype=_I32, device=seq_lens.device) for n in sizes))
-        names = ("held", "free_blocks", "cursor", "src", "dst", "count", "prefix_blocks")
-        po = [_ids(t, "out " + nm, self.device, n)
-              for t, nm, n in zip(out, names, sizes, strict=True)]
+        out, po = _outputs(
+            out, ("held", "free_blocks", "cursor", "src", "dst", "count", "prefix_blocks"),
+            (B, num_blocks, 1, most, most, 1, n_prefix), seq_lens.device, self.device, other)
         rc = self._lib.vt_paged_compact(
             self._h, *args, p_table, ld_out, po[0], po[1], po[2], po[6], po[3], po[4], po[5],
             raw_stream(stream, self.device))
@@ -401,8 +398,7 @@ class PagedBatch:
             if t.get_device() != dev:
                 raise ValueError(f"a cache is on {t.device}, the handle on cuda:{dev}")
         each = 1
-        for size, stride in sorted(((s, st) for s, st in zip(shape[1:], strides[1:]) if s != 1),
-                                   key=lambda x: x[1]):
+        for stride, size in sorted([(st, s) for s, st in zip(shape[1:], strides[1:]) if s != 1]):
             if stride != each:
                 raise ValueError(f"the elements of a block have gaps: strides {tuple(strides)}")
             each *= size
