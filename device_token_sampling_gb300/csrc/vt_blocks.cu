@@ -155,6 +155,7 @@ __device__ __forceinline__ void mark(const ReclaimArgs& a, int id) {
 // A warp to 256 columns of a row.
 __global__ void __launch_bounds__(kBlkThreads) mark_kernel(ReclaimArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");
   const int per_row = (a.cols + kBlkCols - 1) / kBlkCols;
   const int64_t items = (int64_t)a.B * per_row;
   if (blockIdx.x == 0)
@@ -181,18 +182,26 @@ __global__ void __launch_bounds__(kBlkThreads) mark_kernel(ReclaimArgs a) {
   }
 }
 
-// Sums over the block of the set bits of words [0, n) that are below bit `end`.
-__device__ int64_t count_bits(const uint32_t* used, int64_t n, int* s) {
-  int sum = 0;
+// The set bits of words [0, n), and those of words [0, w0), w0 a multiple of 4; of all
+// threads together.
+__device__ __forceinline__ void count_bits(const uint32_t* used, int64_t n, int64_t w0, int* s,
+                                           int* total, int* before) {
+  int sum = 0, low = 0;
   const int64_t quads = n / 4;
+#pragma unroll 4
   for (int64_t i = threadIdx.x; i < quads; i += kBlkThreads) {
     const uint4 v = __ldcg(reinterpret_cast<const uint4*>(used) + i);
-    sum += __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+    const int bits = __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+    sum += bits;
+    low += i * 4 < w0 ? bits : 0;
   }
-  for (int64_t i = quads * 4 + threadIdx.x; i < n; i += kBlkThreads) sum += __popc(__ldcg(used + i));
-  int total;
-  block_scan_i(sum, s, &total);
-  return total;
+  for (int64_t i = quads * 4 + threadIdx.x; i < n; i += kBlkThreads) {
+    const int bits = __popc(__ldcg(used + i));
+    sum += bits;
+    low += i < w0 ? bits : 0;
+  }
+  block_scan_i(sum, s, total);
+  block_scan_i(low, s, before);
 }
 
 // A CTA to a stretch of words; it counts the words before it, and all of them, itself.
@@ -204,11 +213,14 @@ __global__ void __launch_bounds__(kBlkThreads) sweep_kernel(ReclaimArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t words = ((int64_t)a.num_blocks + 31) >> 5;
   const int64_t w0 = (int64_t)blockIdx.x * a.share, w1 = min(w0 + a.share, words);
-  const int n_used = (int)count_bits(a.used, words, s_scan);
-  int before = (int)count_bits(a.used, w0, s_scan);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  int n_used, before;
+  count_bits(a.used, words, w0, s_scan, &n_used, &before);
   int low = 0;  // used ids below n_used
   if (a.compact) {
-    low = (int)count_bits(a.used, n_used >> 5, s_scan);
+    int none;
+    count_bits(a.used, n_used >> 5, 0, s_scan, &low, &none);
     if (n_used & 31) low += __popc(__ldcg(a.used + (n_used >> 5)) & ((1u << (n_used & 31)) - 1));
   }
   if (blockIdx.x == 0 && tid == 0) {
@@ -256,6 +268,7 @@ __device__ __forceinline__ int new_id(const ReclaimArgs& a, int id, int n_used, 
 }
 __global__ void __launch_bounds__(kBlkThreads) renumber_kernel(ReclaimArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int per_row = (a.cols + kBlkCols - 1) / kBlkCols;
   const int64_t items = (int64_t)a.B * per_row;
   const int n_used = a.totals[0], low = a.totals[1];
@@ -276,11 +289,15 @@ __global__ void __launch_bounds__(kBlkThreads) renumber_kernel(ReclaimArgs a) {
 }
 
 // ---- block copies ----------------------------------------------------------------
-// Pair i: block src[i] to dst[i] in every cache.  A CTA takes pieces of kPiece units of
-// W bytes, the pieces of a block next to each other.
+// Pair i: block src[i] to dst[i] in every cache.  A CTA takes pieces of kPiece units, the
+// pieces of a block next to each other.  Bound by the memory: 717 MB read and as many
+// written in 213 us (2 layers' K and V; 6.7 TB/s, 0.99 of a plain copy's rate).  What gives
+// that is loads under way: 16 of 16 bytes a thread and 32 CTAs an SM, handed out as others
+// end, where 8 of each took 224 us.  More CTAs gain nothing and cost those calls whose
+// count, known on the device only, is small.
+constexpr int kCopyThreads = 256, kAhead = 16, kPiece = kCopyThreads * kAhead;
 template <typename U>
-__global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ CopyArgs a) {
-  constexpr int kAhead = 8, kPiece = 256 * kAhead;
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyArgs a) {
   int n = a.n;
   if (a.count) n = min(n, max(a.count[0], 0));
   const int64_t units = a.block_bytes / (int64_t)sizeof(U);
@@ -303,10 +320,10 @@ __global__ void __launch_bounds__(256) copy_kernel(const __grid_constant__ CopyA
     U v[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (u0 + k * 256 < units) v[k] = from[u0 + k * 256];
+      if (u0 + k * kCopyThreads < units) v[k] = from[u0 + k * kCopyThreads];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (u0 + k * 256 < units) to[u0 + k * 256] = v[k];
+      if (u0 + k * kCopyThreads < units) to[u0 + k * kCopyThreads] = v[k];
   }
 }
 
@@ -339,19 +356,28 @@ cudaError_t launch_reclaim(ReclaimArgs a, int num_sms, cudaStream_t stream) {
   // one round of 512 words to a CTA, more where that would be over two CTAs an SM
   int64_t share = (words + 2 * num_sms - 1) / (2 * num_sms);
   a.share = (int32_t)((share + kBlkThreads - 1) / kBlkThreads * kBlkThreads);
-  sweep_kernel<<<(unsigned)((words + a.share - 1) / a.share), kBlkThreads, 0, stream>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || !a.compact) return e;
-  renumber_kernel<<<(unsigned)grid, kBlkThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  // (each begins while the one before it ends, and waits for it)
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = stream;
+  cfg.gridDim = dim3((unsigned)((words + a.share - 1) / a.share));
+  cfg.blockDim = dim3(kBlkThreads);
+  if ((e = cudaLaunchKernelEx(&cfg, sweep_kernel, a)) != cudaSuccess || !a.compact) return e;
+  cfg.gridDim = dim3((unsigned)grid);
+  return cudaLaunchKernelEx(&cfg, renumber_kernel, a);
 }
 
 cudaError_t launch_copy(const CopyArgs& a, bool wide, int num_sms, cudaStream_t stream) {
   const int64_t unit = wide ? 16 : 1;
-  const int64_t pieces = (a.block_bytes / unit + 2047) / 2048 * a.n_caches * a.n;
-  const int64_t most = 8ll * num_sms;
+  const int64_t pieces = (a.block_bytes / unit + kPiece - 1) / kPiece * a.n_caches * a.n;
+  const int64_t most = 32ll * num_sms;
   const unsigned grid = (unsigned)(pieces < most ? pieces : most);
-  if (wide) copy_kernel<uint4><<<grid, 256, 0, stream>>>(a);
-  else copy_kernel<unsigned char><<<grid, 256, 0, stream>>>(a);
+  if (wide) copy_kernel<uint4><<<grid, kCopyThreads, 0, stream>>>(a);
+  else copy_kernel<unsigned char><<<grid, kCopyThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
