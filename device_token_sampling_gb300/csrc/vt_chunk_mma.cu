@@ -32,8 +32,9 @@ constexpr int kScoreWarp = 8, kProductWarp = 9, kKvWarp = 11, kPieceWarp = 13, k
 // virtual head is a kv head and a part of its G.
 struct Request {
   int s0, n;       // its rows of q
-  int64_t before;  // tokens in front of them
-  int units;       // of a virtual head
+  int before;  // tokens in front of them, none past the table's columns; below 0: the first
+               // rows have no position
+  int units;   // of a virtual head
 };
 __device__ __forceinline__ Request request(const ChunkArgs& a, int b) {
   Request r;
@@ -41,33 +42,84 @@ __device__ __forceinline__ Request request(const ChunkArgs& a, int b) {
   const bool fine = s0 >= 0 && s0 <= s1 && s1 <= a.T;
   r.s0 = s0;
   r.n = fine ? s1 - s0 : 0;
-  r.before = (int64_t)a.seq_lens[b] - r.n;
+  r.before = min(max(a.seq_lens[b], -1) - r.n, a.cols << a.shift);
   r.units = (r.n + 2 * a.tokens - 1) / (2 * a.tokens);
   return r;
 }
-__device__ __forceinline__ int unit_tokens(const ChunkArgs& a, const Request& r, int u) {
-  return min(2 * a.tokens, r.n - u * 2 * a.tokens);
+__device__ __forceinline__ int unit_tokens(int tokens, const Request& r, int u) {
+  return min(2 * tokens, r.n - u * 2 * tokens);
 }
-// The end of the tokens that unit u attends to, and its steps (one at least, so that
-// rows which attend to nothing are written).
-__device__ __forceinline__ int unit_end(const ChunkArgs& a, const Request& r, int u) {
-  const int64_t end = r.before + min((u + 1) * 2 * a.tokens, r.n);
-  return (int)min(max(end, (int64_t)0), (int64_t)a.cols << a.shift);
+// The end of the tokens that unit u attends to, of cap at most, and its steps (one at least,
+// so that rows which attend to nothing are written).
+__device__ __forceinline__ int unit_end(int tokens, int cap, const Request& r, int u) {
+  return min(max(r.before + min((u + 1) * 2 * tokens, r.n), 0), cap);
 }
-__device__ __forceinline__ int unit_steps(const ChunkArgs& a, const Request& r, int u) {
-  return max(1, (unit_end(a, r, u) + kTileTokens - 1) / kTileTokens);
+__device__ __forceinline__ int unit_steps(int tokens, int cap, const Request& r, int u) {
+  return max(1, (unit_end(tokens, cap, r, u) + kTileTokens - 1) / kTileTokens);
 }
 // What a step of it costs (two tiles take turns on a unit that fits one),
-__device__ __forceinline__ int unit_weight(const ChunkArgs& a, const Request& r, int u) {
-  return unit_tokens(a, r, u) > a.tokens ? 2 : 1;
+__device__ __forceinline__ int unit_weight(int tokens, const Request& r, int u) {
+  return unit_tokens(tokens, r, u) > tokens ? 2 : 1;
 }
 // and what beginning and ending it costs besides.
 constexpr int kUnitCost = 6;
-__device__ __forceinline__ int64_t unit_cost(const ChunkArgs& a, const Request& r, int u) {
-  return kUnitCost + (int64_t)unit_steps(a, r, u) * unit_weight(a, r, u);
+__device__ __forceinline__ int unit_cost(int tokens, int cap, const Request& r, int u) {
+  return kUnitCost + unit_steps(tokens, cap, r, u) * unit_weight(tokens, r, u);
 }
-// The order of a request's units: the longest first, its heads side by side.  (So CTAs
-// that run at the same time read the same keys and values from L2.)
+__device__ __forceinline__ int unit_cost(const ChunkArgs& a, const Request& r, int u) {
+  return unit_cost(a.tokens, a.cols << a.shift, r, u);
+}
+// floor(b / m) + floor((k + b) / m) + .. of n terms; b below 2^31, the rest below 2^24.  By
+// Euclid's steps on k and m: what lies under the line, then what lies beside it.
+__device__ __forceinline__ int64_t sum_of_floors(uint32_t n, uint32_t m, uint32_t k, uint32_t b) {
+  int64_t sum = 0;
+  while (n > 0) {
+    sum += (int64_t)(k / m) * ((int64_t)n * (n - 1) / 2) + (int64_t)n * (b / m);
+    k %= m;
+    b %= m;
+    const uint32_t top = k * n + b;  // (k < m <= 128 from here on)
+    if (top < m) break;
+    n = top / m;
+    b = top % m;
+    const uint32_t was = m;
+    m = k;
+    k = was;
+  }
+  return sum;
+}
+// The cost of units u0 .. u1 - 1: a walk through a few; of more in closed form, so that a
+// prompt of 10^5 tokens costs the one CTA no more than one of 1000.  (Not in line: from a
+// cold cache its code's copies would cost an ordinary plan 6 us.)
+constexpr int kWalk = 16;
+__device__ __noinline__ int64_t many_units_cost(Request r, int tokens, int cap, int u0, int u1) {
+  int64_t cost = 0;
+  if (u1 == r.units) cost = unit_cost(tokens, cap, r, --u1);
+  // the others have two tiles and end at before + (u + 1) k: some at nothing, some at the
+  // table's end
+  const int k = 2 * tokens;
+  const int none = r.before < 0 ? -r.before / k : 0;
+  const int some = cap < r.before ? 0 : (cap - r.before) / k;
+  const int lo = min(max(none, u0), u1), hi = min(max(some, lo), u1);
+  const int64_t steps =
+      lo - u0 + (int64_t)(u1 - hi) * ((cap + kTileTokens - 1) / kTileTokens) +
+      (hi > lo ? sum_of_floors(hi - lo, kTileTokens, k, r.before + (lo + 1) * k + kTileTokens - 1)
+               : 0);
+  return cost + (int64_t)kUnitCost * (u1 - u0) + 2 * steps;
+}
+__device__ __forceinline__ int64_t units_cost(const ChunkArgs& a, const Request& r, int u0, int u1) {
+  if (u1 - u0 > kWalk) return many_units_cost(r, a.tokens, a.cols << a.shift, u0, u1);
+  int64_t cost = 0;
+#pragma unroll 1
+  for (int u = u0; u < u1; ++u) cost += unit_cost(a, r, u);
+  return cost;
+}
+// That of the first `count` units and heads.  The order of a request's units: the longest
+// first, its heads side by side.  (So CTAs that run at the same time read the same keys and
+// values from L2.)
+__device__ __forceinline__ int64_t first_cost(const ChunkArgs& a, const Request& r, int64_t count) {
+  const int u = r.units - (int)(count / a.heads_all), rest = (int)(count % a.heads_all);
+  return a.heads_all * units_cost(a, r, u, r.units) + (rest ? (int64_t)rest * unit_cost(a, r, u - 1) : 0);
+}
 
 struct Sums2 {
   int64_t x, y;
@@ -108,10 +160,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       const int s0 = a.starts[b], s1 = a.starts[b + 1];
       if (s0 < 0 || s0 > s1 || s1 > a.T) atomicOr(a.err_word, kErrBadRows);
       x = (int64_t)r.units * a.heads_all;
-      for (int u = 0; u < r.units; ++u) y += unit_cost(a, r, u);
+      y = units_cost(a, r, 0, r.units);
       if (r.units > 0) {
         const int u = r.units - 1;
-        atomicMax(&s_longest, unit_steps(a, r, u) * (u > 0 ? 2 : unit_weight(a, r, u)));
+        atomicMax(&s_longest, unit_steps(a.tokens, a.cols << a.shift, r, u) *
+                                    (u > 0 ? 2 : unit_weight(a.tokens, r, u)));
       }
       y *= a.heads_all;
       if (r.units > 1) s_several = 1;
@@ -166,13 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
     const int64_t u = (int64_t)rounds * G;
     const int b = find_request(first, 2, a.B, u);
     const Request r = request(a, b);
-    int64_t left = u - first[2 * b];
-    skipped = first[2 * b + 1];
-    for (int v = r.units - 1; left > 0; --v) {
-      const int64_t k = min(left, (int64_t)a.heads_all);
-      skipped += k * unit_cost(a, r, v);
-      left -= k;
-    }
+    skipped = first[2 * b + 1] + first_cost(a, r, u - first[2 * b]);
   }
   const int64_t todo = steps - skipped;
   // The rest goes in shares that make up for it: up to the mean of all.  (Equal shares
@@ -211,13 +258,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
     if (whole && c < units) {
       const int b = find_request(first, 2, a.B, c);
       const Request r = request(a, b);
-      int left = (int)(c - first[2 * b]);
-      at = first[2 * b + 1];
-      for (int u = r.units - 1; left > 0; --u) {
-        const int k = min(left, a.heads_all);
-        at += k * unit_cost(a, r, u);
-        left -= k;
-      }
+      at = first[2 * b + 1] + first_cost(a, r, c - first[2 * b]);
     }
     ChunkStart s{};
     s.at = at;
@@ -226,17 +267,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       const int b = find_request(first + 1, 2, a.B, at);
       const Request r = request(a, b);
       int64_t left = at - first[2 * b + 1];
-      int u = r.units - 1;
-      int64_t each = 0;
-      for (;; --u) {
-        each = unit_cost(a, r, u);
-        if (u == 0 || left < each * a.heads_all) break;
+      int u0 = 0, u = r.units;  // the unit that it is in: from u0 on, below u
+      while (u - u0 > kWalk) {
+        const int mid = (u0 + u) >> 1;
+        if (units_cost(a, r, mid, r.units) * a.heads_all > left) u0 = mid;
+        else u = mid;
+      }
+      left -= units_cost(a, r, u, r.units) * a.heads_all;
+      int64_t each;
+      for (;;) {
+        each = unit_cost(a, r, --u);
+        if (u == u0 || left < each * a.heads_all) break;
         left -= each * a.heads_all;
       }
       s.b = b;
       s.unit = u;
       s.head = (int)(left / each);
-      const int in = (int)(left % each), w = unit_weight(a, r, u);
+      const int in = (int)(left % each), w = unit_weight(a.tokens, r, u);
       s.step = max(in - kUnitCost, 0) / w;  // (a whole step)
       s.at += (s.step > 0 ? kUnitCost + s.step * w : 0) - in;
     }
@@ -845,6 +892,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
     }
+    tmem_wait_st();  // (where a wait ran out)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kKvWarp || warp == kKvWarp + 1) {
@@ -935,22 +983,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           const Request r = request(a, pb);
           if (whole) pu = r.units - 1 - pu;
-          const int n = unit_steps(a, r, pu);
+          const int n = unit_steps(a.tokens, cap, r, pu);
           p.b = pb;
           p.kvh = ph / a.parts;
           const int part = ph % a.parts * a.heads;
           p.head = p.kvh * a.G + part;
           p.heads = min(a.heads, a.G - part);
           p.token = r.s0 + pu * 2 * a.tokens;
-          p.tokens = unit_tokens(a, r, pu);
-          p.end = unit_end(a, r, pu);
-          p.lim0 = (int)max(min(r.before + pu * 2 * a.tokens + 1, (int64_t)1 << 30),
-                            -((int64_t)1 << 30));
+          p.tokens = unit_tokens(a.tokens, r, pu);
+          p.end = unit_end(a.tokens, cap, r, pu);
+          p.lim0 = r.before + pu * 2 * a.tokens + 1;
           p.t0 = 0;
           p.t1 = n;
           p.slot = -1;
           if (!whole) {  // the rest of a unit, or of this CTA's share
-            const int w = unit_weight(a, r, pu);
+            const int w = unit_weight(a.tokens, r, pu);
             const int64_t begin = at - (step > 0 ? kUnitCost + (int64_t)step * w : 0);
             const int64_t end = begin + kUnitCost + (int64_t)n * w;
             p.t0 = step;

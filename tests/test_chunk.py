@@ -366,6 +366,97 @@ def test_two_handles_at_once():
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_one_query_over_all_ctas(dtype):
+    """One request of few rows and a long context: split over every CTA, joined from 64 parts."""
+    for n, total in ((1, 70000), (5, 40001), (40, 33000)):
+        run(batch([n], [total], 4, 1, 128, 64, dtype, seed=n), 64)
+
+
+@gpu
+def test_far_rows():
+    """Query rows and results past 2^31 elements, starts that do not begin at 0."""
+    bs, hq, T = 16, 32, 700_000
+    x = batch([3, 200], [90, 333], hq, 8, 128, bs, torch.bfloat16)
+    with handle(x, bs) as p:
+        want, wlse = p.chunk_attention(**x)
+        q = torch.empty((T, hq, 128), dtype=torch.bfloat16, device="cuda")
+        q[-203:] = x["q"]
+        y = dict(x, q=q, starts=dev([T - 203, T - 200, T]))
+        out, lse = torch.full_like(q, 7.0), torch.full((T, hq), 9.0, device="cuda")
+        p.chunk_attention(**y, out=out, lse=lse)
+        p.check_errors()
+    assert torch.equal(out[-203:], want) and torch.equal(lse[-203:], wlse)
+    assert (out[:T - 203] == 7).all() and (lse[:T - 203] == 9).all()
+
+
+@gpu
+@pytest.mark.parametrize("bs", [4, 16])
+def test_one_query_for_all_heads_and_rows(bs):
+    """q of stride 0."""
+    x = batch([3, 140], [80, 333], 8, 2, 64, bs, torch.bfloat16)
+    x["q"] = x["q"][:1, :1].expand(143, 8, 64)
+    run(x, bs)
+
+
+@gpu
+@pytest.mark.parametrize("bs", [4, 16])
+def test_outputs_at_odd_addresses(bs):
+    """out and lse on 16 and 4 bytes only."""
+    x = batch([3, 140], [80, 333], 8, 2, 64, bs, torch.bfloat16)
+    want = run(x, bs)
+    out = torch.zeros(143 * 8 * 64 + 8, dtype=torch.bfloat16, device="cuda")[8:].view(143, 8, 64)
+    lse = torch.zeros(143 * 8 + 1, device="cuda")[1:].view(143, 8)
+    with handle(x, bs) as p:
+        p.chunk_attention(**x, out=out, lse=lse)
+        p.check_errors()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@gpu
+def test_two_graphs_of_one_handle():
+    """Two captured calls share the handle's workspaces: replayed one after another."""
+    xs = [batch([3, 4, 250], [40, 700, 300], 8, 2, 64, 16, torch.bfloat16, seed=1),
+          batch([1, 400, 2], [3000, 700, 90], 8, 2, 64, 16, torch.bfloat16, seed=2)]
+    cols = max(x["table"].shape[1] for x in xs)
+    from device_token_sampling_gb300 import PagedBatch
+    with PagedBatch(3, 16, cols, 8, 2, 64) as p:
+        graphs, got = [], []
+        for x in xs:
+            p.chunk_attention(**x)
+            torch.cuda.synchronize()
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                got.append(p.chunk_attention(**x))
+        for i in (0, 1, 1, 0, 1):
+            got[i][0].zero_()
+            graphs[i].replay()
+            compare(got[i], xs[i], 16, 64 ** -0.5)
+        p.check_errors()
+
+
+@gpu
+def test_waits_that_run_out(monkeypatch):
+    """Every wait taken as run out: the call comes back and is reported, and another handle
+    attends as before."""
+    from device_token_sampling_gb300 import VtError, sampler
+    x = batch([3, 4, 250, 1], [4000, 700, 300, 900], 8, 2, 128, 16, torch.bfloat16)
+    want, wlse = run(x, 16)
+    monkeypatch.setenv("VT_FAULT_INJECT", "wait")
+    broken = handle(x, 16)
+    monkeypatch.delenv("VT_FAULT_INJECT")
+    for _ in range(2):
+        broken.chunk_attention(**x)
+        with pytest.raises(VtError) as e:
+            broken.check_errors()
+        assert e.value.code == sampler.VT_ERR_TIMEOUT
+        broken.check_errors()
+    broken.close()
+    out, lse = run(x, 16)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@gpu
 def test_refusals():
     from device_token_sampling_gb300 import PagedBatch, VtError
     x = batch([3, 2], [30, 50], 4, 2, 64, 16, torch.bfloat16)
