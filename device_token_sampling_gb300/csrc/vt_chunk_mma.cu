@@ -125,6 +125,7 @@ struct Sums2 {
   int64_t x, y;
 };
 constexpr int kPlanThreads = 1024;
+constexpr int kMostRounds = 16;  // of units that are looked at one by one
 
 // The last b with first[b] <= v.
 __device__ __forceinline__ int find_request(const int64_t* first, int stride, int B, int64_t v) {
@@ -137,18 +138,27 @@ __device__ __forceinline__ int find_request(const int64_t* first, int stride, in
   return lo;
 }
 
-// One CTA: prefix sums of the requests' units and steps; then what each CTA of
-// chunk_kernel does.  Whole rounds of units where some request has several units a kv
-// head (which share keys and values) and there are two rounds at least; the units
-// behind the last but one whole round, or all of them, as one row of steps in equal
-// shares.
+// One CTA: prefix sums of the requests' units and what they cost; then what each CTA of
+// chunk_kernel does.  Units go whole, in rounds, every other round the other way about
+// (a request's come longest first), or as one row of steps cut into shares:
+//   - all whole, where that leaves no CTA with much more than the mean: 16 and a 16th.
+//     A unit that is cut is written out in parts and put together, which costs about as
+//     much as 16 steps of one tile.  us whole and cut, 32/8 heads of 128: one prompt of 1024
+//     tokens 29 and 48, of 4096 107 and 129, of 8192 337 and 363; 256 requests of up to 4
+//     new tokens behind up to 2000 215 and 249.  A limit of 12 left 8 prompts of 512 (54
+//     and 68) cut, of 24 made 20 requests of 5 tokens behind 2000 whole (59 and 53); an 8th
+//     made 4 prompts of up to 4096 whole, 9 % apart (1004 and 975).
+//   - else, where some request has several units a kv head (which share keys and values)
+//     and there are two rounds at least, all but the last whole round and what is behind
+//     it, which goes in shares that make up for the CTAs' differences;
+//   - else all in shares.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
   __shared__ Sums2 s_warp[33];
   __shared__ int64_t s_first[2 * (kPlanThreads + 1)];  // plan_first, where it fits
-  __shared__ int s_several, s_longest;
+  __shared__ int s_several, s_most;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
-  if (tid == 0) s_several = s_longest = 0;
+  if (tid == 0) s_several = s_most = 0;
   for (int i = tid; i < 8 * a.grid; i += kPlanThreads) a.plan_count[i] = 0;
   __syncthreads();
   int64_t units = 0, steps = 0;
@@ -161,11 +171,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       if (s0 < 0 || s0 > s1 || s1 > a.T) atomicOr(a.err_word, kErrBadRows);
       x = (int64_t)r.units * a.heads_all;
       y = units_cost(a, r, 0, r.units);
-      if (r.units > 0) {
-        const int u = r.units - 1;
-        atomicMax(&s_longest, unit_steps(a.tokens, a.cols << a.shift, r, u) *
-                                    (u > 0 ? 2 : unit_weight(a.tokens, r, u)));
-      }
       y *= a.heads_all;
       if (r.units > 1) s_several = 1;
     }
@@ -213,9 +218,28 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
   const int64_t* first = a.B <= kPlanThreads ? s_first : a.plan_first;
   const int G = a.grid;
   const int rounds = s_several && units >= 2 * G ? (int)(units / G - 1) : 0;
-  // what the units cost that whole rounds take, and each CTA's of them
-  int64_t skipped = 0, want = 0;
-  if (rounds > 0) {
+  const int64_t rounds_all = (units + G - 1) / G;
+  const bool maybe = rounds_all <= kMostRounds;
+  // what the units of rounds cost, each CTA's: of all, of `rounds`
+  int mine = 0;
+  int64_t most = 0, want = 0;
+  if (tid < G) {
+    for (int64_t i = 0; i < (maybe ? rounds_all : rounds); ++i) {
+      const int64_t u = i * G + (i & 1 ? G - 1 - tid : tid);
+      if (u >= units) break;
+      const int b = find_request(first, 2, a.B, u);
+      const Request r = request(a, b);
+      const int cost = unit_cost(a, r, r.units - 1 - (int)(u - first[2 * b]) / a.heads_all);
+      most += cost;
+      if (i < rounds) want += cost;
+      ++mine;
+    }
+    if (maybe) atomicMax(&s_most, (int)min(most, (int64_t)0x7fffffff));
+  }
+  __syncthreads();
+  const bool whole = maybe && s_most <= steps / G + steps / G / 16 + 16;
+  int64_t skipped = 0;
+  if (rounds > 0 && !whole) {
     const int64_t u = (int64_t)rounds * G;
     const int b = find_request(first, 2, a.B, u);
     const Request r = request(a, b);
@@ -224,16 +248,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
   const int64_t todo = steps - skipped;
   // The rest goes in shares that make up for it: up to the mean of all.  (Equal shares
   // left the CTAs' sums 9 % apart on 4 prompts of up to 4096 tokens.)
-  if (tid < G) {
-    want = steps / G + 1;
-    for (int i = 0; i < rounds; ++i) {
-      const int64_t u = (int64_t)i * G + (i & 1 ? G - 1 - tid : tid);
-      const int b = find_request(first, 2, a.B, u);
-      const Request r = request(a, b);
-      want -= unit_cost(a, r, r.units - 1 - (int)(u - first[2 * b]) / a.heads_all);
-    }
-    want = max(want, (int64_t)0);
-  }
+  want = tid < G ? max(steps / G + 1 - want, (int64_t)0) : 0;
   int64_t upto = want;  // of the CTAs up to this one
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -248,18 +263,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
     all += s_warp[w + 1].x;
   }
   before += upto - want;
-  // Short units are not taken apart: a unit to a CTA, where there are enough CTAs.
-  // (Four requests of 5 new tokens behind up to 600, 32 units of up to 5 steps: 21.6 us,
-  // in shares of 2 steps 33.)
-  const bool whole = units <= G && s_longest <= a.whole_cost;
   const int c = tid;
   if (c <= G) {
     int64_t at = whole ? steps : c == G ? steps : skipped + todo * before / max(all, (int64_t)1);
-    if (whole && c < units) {
-      const int b = find_request(first, 2, a.B, c);
-      const Request r = request(a, b);
-      at = first[2 * b + 1] + first_cost(a, r, c - first[2 * b]);
-    }
     ChunkStart s{};
     s.at = at;
     s.b = a.B;
@@ -287,7 +293,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       s.step = max(in - kUnitCost, 0) / w;  // (a whole step)
       s.at += (s.step > 0 ? kUnitCost + s.step * w : 0) - in;
     }
-    s.rounds = rounds;
+    s.rounds = whole ? mine : rounds;
     a.plan_start[c] = s;
   }
 }

@@ -427,7 +427,6 @@ int vt_paged_chunk_attention(vt_paged* h, int32_t dtype, int32_t B, int32_t T, c
   a.err_word = h->d_err;
   a.wait_cycles = h->wait_cycles;
   a.grid = h->num_sms;
-  a.whole_cost = 8;
   a.plan_first = h->d_plan_first;
   a.plan_start = h->d_plan_start;
   a.plan_count = h->d_plan_count;

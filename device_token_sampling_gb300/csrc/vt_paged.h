@@ -168,7 +168,6 @@ struct ChunkArgs {
   int64_t wait_cycles;         // limit of the waits; 0: they have run out
   // the tensor cores' way
   int32_t grid;                // CTAs
-  int32_t whole_cost;          // of a unit that is not taken apart, if the CTAs suffice
   int64_t* plan_first;         // [B + 1][2] units and costs in front of each request
   ChunkStart* plan_start;      // [grid + 1]
   int32_t* plan_count;         // [grid][2][4] parts of a unit's rows that are there

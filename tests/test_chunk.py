@@ -103,6 +103,15 @@ def test_one_long_request_among_short_ones():
 
 
 @gpu
+@pytest.mark.parametrize("n,ctx,hq,hkv", [
+    ([2048], [0], 16, 8), ([500, 700, 3], [0, 40, 900], 32, 8),       # whole units, several rounds
+    ([5] * 20, [2000] * 20, 32, 8), ([1, 2, 3], [7000, 9000, 1], 16, 4),  # units cut into shares
+    ([1500, 2900, 40], [900, 0, 4000], 16, 4)])                       # whole rounds and shares
+def test_units_whole_and_cut(n, ctx, hq, hkv):
+    run(batch(n, np.add(n, ctx), hq, hkv, 64, 64, torch.bfloat16, seed=hq), 64)
+
+
+@gpu
 def test_many_requests():
     g = np.random.default_rng(3)
     n = g.integers(0, 6, 1500)
