@@ -15,6 +15,12 @@
 // One launch.  A cluster of CTAs shares a request: each finds `a` itself (2 K values),
 // sums its part of row a, and gives its sum to the others' shared memory; the part that
 // holds the token is read once more, from L2.
+//
+// Bound by the reads of the two rows: 256 requests of 151936 fp32 entries, 220 MB, in 52 us
+// (4.2 TB/s; 32 us at the rate of a plain copy).  A CTA's beginning (starts, drafts and
+// their entries, one after another) and end (the cluster's sums, the part read again) read
+// little; four CTAs an SM fill some of that.  One request takes 13 us, all of it such
+// latency and the launch.
 #include <cuda_bf16.h>
 
 #include "vt_device.cuh"
@@ -101,6 +107,31 @@ __device__ __forceinline__ void add_bits(uint64_t v, uint32_t (&s)[3]) {
   }
 }
 
+// Values below 2^-8 need two of them: multiples of 2^-31, and the same of 2^-54.  (Nearly
+// all entries of a large vocabulary are.  256 requests of 151936 entries: 55 to 52 us.)
+constexpr float kLow = 1.f / 256;
+template <int kSign>
+__device__ __forceinline__ void add_low_bits(uint64_t v, uint32_t (&s)[3]) {
+  const uint64_t c1 = 0x3b8000003b800000ull, c3 = 0x3040000030400000ull;  // kLow, kC3
+  const uint64_t a = add2(v, c1), r = sub2(v, sub2(a, c1)), c = add2(r, c3);
+  if (kSign > 0) {
+    s[0] += (uint32_t)a + (uint32_t)(a >> 32);
+    s[2] += (uint32_t)c + (uint32_t)(c >> 32);
+  } else {
+    s[0] -= (uint32_t)a + (uint32_t)(a >> 32);
+    s[2] -= (uint32_t)c + (uint32_t)(c >> 32);
+  }
+}
+constexpr uint32_t kBLow = 0x3b800000u;
+__device__ __forceinline__ uint64_t whole_low(uint32_t s1, uint32_t s3) {
+  return ((uint64_t)s1 << 23) + (uint64_t)(int64_t)(int32_t)s3;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 struct Sum {
   uint64_t mass = 0;
   uint32_t bits = 0;  // of all values, together
@@ -138,60 +169,114 @@ __device__ __forceinline__ void load_part(const T* row, int j, int end, bool vec
 template <bool Q, int N>
 __device__ __forceinline__ void add_values(const float (&p)[N], const float (&q)[N], Sum& s) {
   uint32_t t[3] = {};
+  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     s.bits |= __float_as_uint(p[i]) | __float_as_uint(p[i + 1]);
-    add_bits<1>(pair(p[i], p[i + 1]), t);
-    if constexpr (Q) {
-      s.bits |= __float_as_uint(q[i]) | __float_as_uint(q[i + 1]);
-      add_bits<-1>(pair(fminf(p[i], q[i]), fminf(p[i + 1], q[i + 1])), t);
-    }
+    if constexpr (Q) s.bits |= __float_as_uint(q[i]) | __float_as_uint(q[i + 1]);
+    top = max3(top, p[i], p[i + 1]);
   }
   constexpr uint32_t n = Q ? 0 : N;
-  s.mass += whole(t[0] - n * kB1, t[1] - n * kB2, t[2] - n * kB3);
+  if (top < kLow) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      add_low_bits<1>(pair(p[i], p[i + 1]), t);
+      if constexpr (Q) add_low_bits<-1>(pair(fminf(p[i], q[i]), fminf(p[i + 1], q[i + 1])), t);
+    }
+    s.mass += whole_low(t[0] - n * kBLow, t[2] - n * kB3);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      add_bits<1>(pair(p[i], p[i + 1]), t);
+      if constexpr (Q) add_bits<-1>(pair(fminf(p[i], q[i]), fminf(p[i + 1], q[i + 1])), t);
+    }
+    s.mass += whole(t[0] - n * kB1, t[1] - n * kB2, t[2] - n * kB3);
+  }
   s.over |= (uint32_t)(s.mass >> 32);
 }
 
-// Elements [lo, hi) of the row over the lanes of a warp, the next loads under way while
-// some are added; lo a multiple of 32 E.
+__device__ __forceinline__ uint4 load_shared(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// Elements [lo, hi) of the row over the lanes of a warp, lo a multiple of 32 E.  A lane
+// takes 8 at a time; kStages - 1 of its next loads are under way into 16-byte places of
+// its own in shared memory (`ring`: the first, kVerThreads * 16 bytes apart), so that
+// nobody waits for another.  (One load ahead in registers, which is what four CTAs an SM
+// leave room for: 256 requests of 151936 bf16 entries in 85 us, with the ring 57.)
+constexpr int kEach = 8, kStages = 3;  // elements; loads under way and the one in use
+template <typename T>
+constexpr int ring_bytes() {
+  return kStages * 2 * kEach * (int)sizeof(T) * kVerThreads;
+}
 template <typename T, bool Q>
-__device__ __forceinline__ void add_range(const Row<T>& r, int lo, int hi, Sum& s) {
-  constexpr int E = Wide<T>::E, kStep = 32 * E, kAhead = 8 / E;
+__device__ __forceinline__ void add_range(const Row<T>& r, int lo, int hi, uint32_t ring, Sum& s) {
+  constexpr int E = Wide<T>::E, kStep = 32 * E, kAhead = kEach / E, kNext = kAhead * kStep;
   const int lane = threadIdx.x & 31;
-  float p[kAhead][E], q[kAhead][E];
-  auto load = [&](int j0) {
+  auto at = [&](int stage, int a, int q) {
+    return ring + (uint32_t)((stage * kAhead + a) * 2 + q) * (kVerThreads * 16);
+  };
+  auto load = [&](int stage, int j0) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       const int j = j0 + a * kStep + lane * E;
-      load_part(r.p, j, hi, r.vec, p[a]);
-      if constexpr (Q) load_part(r.q, j, hi, r.vec, q[a]);
+      if (r.vec && j + E <= hi) {
+        copy16(at(stage, a, 0), r.p + j);
+        if constexpr (Q) copy16(at(stage, a, 1), r.q + j);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) load(i, lo + i * kNext);
+  int stage = 0;
+#pragma unroll 1
+  for (int j0 = lo; j0 < hi; j0 += kNext) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    float x[kEach], y[kEach];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int j = j0 + a * kStep + lane * E;
+      float p[E], q[E];
+      if (r.vec && j + E <= hi) {
+        Wide<T>::split(load_shared(at(stage, a, 0)), p);
+        if constexpr (Q) Wide<T>::split(load_shared(at(stage, a, 1)), q);
+      } else {
+        load_part(r.p, j, hi, false, p);
+        if constexpr (Q) load_part(r.q, j, hi, false, q);
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        x[a * E + i] = p[i];
+        y[a * E + i] = Q ? q[i] : 0.f;
+      }
     }
     if (r.clamp)
 #pragma unroll
-      for (int i = 0; i < kAhead * E; ++i) {
-        p[i / E][i % E] = at_least_0(p[i / E][i % E]);
-        if constexpr (Q) q[i / E][i % E] = at_least_0(q[i / E][i % E]);
+      for (int i = 0; i < kEach; ++i) {
+        x[i] = at_least_0(x[i]);
+        if constexpr (Q) y[i] = at_least_0(y[i]);
       }
-  };
-  if (lo < hi) load(lo);
-#pragma unroll 1
-  for (int j0 = lo; j0 < hi; j0 += kAhead * kStep) {
-    float x[kAhead * E], y[kAhead * E];
-#pragma unroll
-    for (int i = 0; i < kAhead * E; ++i) {
-      x[i] = p[i / E][i % E];
-      y[i] = Q ? q[i / E][i % E] : 0.f;
-    }
-    if (j0 + kAhead * kStep < hi) load(j0 + kAhead * kStep);
-    add_values<Q, kAhead * E>(x, y, s);
+    load(stage == 0 ? kStages - 1 : stage - 1, j0 + (kStages - 1) * kNext);
+    stage = stage == kStages - 1 ? 0 : stage + 1;
+    add_values<Q, kEach>(x, y, s);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!Q && r.skip >= lo && r.skip < hi && lane == (r.skip - lo) / E % 32)
     s.mass -= fixed(r.clamp ? at_least_0(Wide<T>::one(r.p[r.skip])) : Wide<T>::one(r.p[r.skip]));
 }
 template <typename T>
-__device__ __forceinline__ void add_range(const Row<T>& r, int lo, int hi, Sum& s) {
-  if (r.q) add_range<T, true>(r, lo, hi, s);
-  else add_range<T, false>(r, lo, hi, s);
+__device__ __forceinline__ void add_range(const Row<T>& r, int lo, int hi, uint32_t ring, Sum& s) {
+  if (r.q) add_range<T, true>(r, lo, hi, ring, s);
+  else add_range<T, false>(r, lo, hi, ring, s);
 }
 
 __device__ __forceinline__ uint64_t warp_scan_u64(uint64_t v) {
@@ -242,7 +327,9 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(VerifyArgs a) {
   __shared__ uint64_t s_mass[2][kVerMaxCtas], s_bad[2][kVerMaxCtas];
   __shared__ uint32_t s_bits[kVerWarps];
   __shared__ float s_rough[kVerWarps];
+  extern __shared__ __align__(16) unsigned char s_ring[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t ring = smem_addr(s_ring) + tid * 16;
   const int ctas = a.ctas, rank = (int)cluster_ctarank();
   const int b = blockIdx.x / ctas;
   const int K = a.K;
@@ -318,7 +405,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(VerifyArgs a) {
     Sum s;
     int lo, hi;
     warp_range(warp, lo, hi);
-    if (rows) add_range(row, lo, hi, s);
+    if (rows) add_range(row, lo, hi, ring, s);
     // the sum, roughly, where a lane's may not have fit: large
     const float rough =
         warp_sum_f(s.over & 0xc0000000u ? 1e9f : (float)(uint32_t)(s.mass >> 44) * (1.f / 1024.f));
@@ -393,7 +480,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(VerifyArgs a) {
   __syncthreads();  // (s_warp is written again)
   const int p_lo = min(lo + warp * part, hi), p_hi = min(p_lo + part, hi);
   Sum s;
-  add_range(row, p_lo, p_hi, s);
+  add_range(row, p_lo, p_hi, ring, s);
   const uint64_t mass = warp_sum_u64(s.mass);
   if (lane == 0) s_warp[warp] = mass;
   __syncthreads();
@@ -449,21 +536,35 @@ cudaError_t launch_typed(const VerifyArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.gridDim = dim3((unsigned)(a.B * a.ctas));
   cfg.blockDim = dim3(kVerThreads);
+  cfg.dynamicSmemBytes = ring_bytes<T>();
   return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a);
+}
+
+template <typename T>
+cudaError_t prepare_typed() {
+  const cudaError_t e = cudaFuncSetAttribute(
+      verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(verify_kernel<T>,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     ring_bytes<T>());
 }
 
 }  // namespace
 
 cudaError_t prepare_verify() {
-  const auto attr = cudaFuncAttributeNonPortableClusterSizeAllowed;
-  const cudaError_t e = cudaFuncSetAttribute(verify_kernel<float>, attr, 1);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(verify_kernel<__nv_bfloat16>, attr, 1);
+  const cudaError_t e = prepare_typed<float>();
+  return e != cudaSuccess ? e : prepare_typed<__nv_bfloat16>();
 }
 
 cudaError_t launch_verify(VerifyArgs a, int dtype, int num_sms, cudaStream_t stream) {
-  // CTAs to a request until there are four for every SM, 4096 elements to each at least
+  // CTAs to a request until there are four for every SM, 4096 elements to each at least;
+  // more than that, so that some begin when others end, only where each still has 128 KB
+  // of a row: 64 requests of 151936 bf16 entries take 24 us with 8 CTAs each and 32 with
+  // 16 (19 KB), 512 fp32 ones 134 us with 2 (300 KB) and 157 with 1.
   a.ctas = 1;
-  while (a.ctas < kVerMaxCtas && (int64_t)a.ctas * a.B < 4 * num_sms && a.V / a.ctas >= 8192)
+  const int64_t row = (int64_t)a.V * (dtype == VT_DTYPE_F32 ? 4 : 2), room = 4ll * num_sms;
+  while (a.ctas < kVerMaxCtas && a.ctas * (int64_t)a.B < room && a.V / a.ctas >= 8192 &&
+         (2ll * a.ctas * a.B <= room || row / (2 * a.ctas) >= 128 << 10))
     a.ctas *= 2;
   return dtype == VT_DTYPE_F32 ? launch_typed<float>(a, stream)
                                : launch_typed<__nv_bfloat16>(a, stream);
