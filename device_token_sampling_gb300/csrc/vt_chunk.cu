@@ -4,7 +4,8 @@
 // head h, is out = sum_j p_j v_j / sum_j p_j over the positions j <= len_b - n_b + i, with
 // p_j = exp(scale q . k_j - max).
 //
-// This file: rows one at a time, in fp32, for caches whose layout no tensor map holds.
+// This file: rows one at a time, in fp32, for layouts that no tensor map holds: q or
+// caches with a stride of 0 (broadcast heads, say) or less.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -544,7 +544,9 @@ __device__ __noinline__ void join_rows(const ChunkArgs& a, int job, int last, in
   if (a.lse && row >= 0) a.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
-template <typename T, int D>
+// kSmall: blocks of 1 or 2 tokens, more than 32 to a step.  (In one kernel with the others
+// these lost up to 9 %.)
+template <typename T, int D, bool kSmall>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v,
@@ -917,7 +919,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int j = p.t0 + ((all ^ odd) & 1); j < p.t1 && ok; j += 2) {
           const uint32_t g = all + (j - p.t0);
           const int tok0 = j * kTileTokens;
-          // the blocks of this tile, up to 16 of them: one a lane
+          // the blocks of this tile, up to 32 of them: one a lane
           const int tok = tok0 + lane * box;
           const bool here = lane < boxes && tok < p.end;
           int blk = here ? table[tok >> a.shift] : -1;
@@ -925,9 +927,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (here && !fine) atomicOr(a.err_word, kErrBadBlock);
           if (!fine) blk = a.num_blocks;  // outside: the copy fills zeros
           const unsigned good = __ballot_sync(0xffffffffu, fine);
+          // (the rest of them, where a block has 1 or 2 tokens)
+          int more[3];
+          unsigned good_more[3] = {0, 0, 0};
+          if constexpr (kSmall)
+            for (int i = 0; i < 3; ++i) {
+              const int at = lane + 32 * (i + 1), tok = tok0 + at * box;
+              const bool here = at < boxes && tok < p.end;
+              more[i] = here ? table[tok >> a.shift] : -1;
+              const bool fine = more[i] >= 0 && more[i] < a.num_blocks;
+              if (here && !fine) atomicOr(a.err_word, kErrBadBlock);
+              if (!fine) more[i] = a.num_blocks;
+              good_more[i] = __ballot_sync(0xffffffffu, fine);
+            }
           if (lane < 4) {
             uint32_t m = 0;
-            if (box >= 32) {
+            if constexpr (kSmall) {
+              if (box == 1) {
+                m = lane == 0 ? good : lane == 1 ? good_more[0] : lane == 2 ? good_more[1] : good_more[2];
+              } else {
+                const uint32_t bits = (lane < 2 ? good : good_more[0]) >> (lane & 1) * 16;
+                for (int i = 0; i < 16; ++i) m |= ((bits >> i) & 1) * 3u << 2 * i;
+              }
+            } else if (box >= 32) {
               m = (good >> (lane * 32 / box)) & 1 ? 0xffffffffu : 0u;
             } else {
               for (int i = 0; i < 32; i += box)
@@ -952,10 +974,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             uint64_t* bar = &sh.full[set][st];
             if (lane == 0) mbar_arrive_expect_tx(bar, L::kTile);
             __syncwarp();
+            // (the swizzle goes by the address, so that parts of its atoms of 8 tokens may come
+            // from copies of their own)
             if (lane < boxes)
               for (int h = 0; h < D / 64; ++h)
                 tma_tile(base + L::kKv + st * L::kTile + h * L::kHalf + lane * box * 128,
                          kv ? &map_v : &map_k, bar, h * 64, in_block, p.kvh, blk);
+            if constexpr (kSmall)
+              for (int i = 0; i < 3; ++i)
+                if (lane + 32 * (i + 1) < boxes)
+                  for (int h = 0; h < D / 64; ++h)
+                    tma_tile(base + L::kKv + st * L::kTile + h * L::kHalf +
+                                 (lane + 32 * (i + 1)) * box * 128,
+                             kv ? &map_v : &map_k, bar, h * 64, in_block, p.kvh, more[i]);
           }
         }
         all += p.t1 - p.t0;
@@ -1238,19 +1269,25 @@ cudaError_t launch_typed(const ChunkArgs& a, const CUtensorMap& mk, const CUtens
   cfg.gridDim = dim3((unsigned)a.grid);
   cfg.blockDim = dim3(kChunkThreads);
   cfg.dynamicSmemBytes = chunk_smem<D>();
-  return cudaLaunchKernelEx(&cfg, chunk_kernel<T, D>, a, mk, mv, mq);
+  return a.shift < 2 ? cudaLaunchKernelEx(&cfg, chunk_kernel<T, D, true>, a, mk, mv, mq)
+                     : cudaLaunchKernelEx(&cfg, chunk_kernel<T, D, false>, a, mk, mv, mq);
 }
 
-template <typename T, int D>
-cudaError_t prepare_typed() {
+template <typename T, int D, bool kSmall>
+cudaError_t prepare_kernel() {
   // the roles divide up 128 registers a thread: with fewer at launch they would wait
   // for the rest
   cudaFuncAttributes is;
-  const cudaError_t e = cudaFuncGetAttributes(&is, chunk_kernel<T, D>);
+  const cudaError_t e = cudaFuncGetAttributes(&is, chunk_kernel<T, D, kSmall>);
   if (e != cudaSuccess) return e;
   if (is.numRegs != 128) return cudaErrorInvalidConfiguration;
-  return cudaFuncSetAttribute(chunk_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)chunk_smem<D>());
+  return cudaFuncSetAttribute(chunk_kernel<T, D, kSmall>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)chunk_smem<D>());
+}
+template <typename T, int D>
+cudaError_t prepare_typed() {
+  const cudaError_t e = prepare_kernel<T, D, false>();
+  return e != cudaSuccess ? e : prepare_kernel<T, D, true>();
 }
 
 }  // namespace
@@ -1268,7 +1305,7 @@ int64_t chunk_part_rows(int grid) { return 2ll * grid * kUnitRows; }
 
 bool chunk_mma_takes(const ChunkArgs& a) {
   const int64_t most = 1ll << 38;
-  return cache_map_takes(a.shift, a.block_stride, a.token_stride, a.head_stride) && a.q_row > 0 &&
+  return cache_map_takes(a.block_stride, a.token_stride, a.head_stride) && a.q_row > 0 &&
          a.q_head > 0 && a.q_row < most && a.q_head * a.G < most;
 }
 

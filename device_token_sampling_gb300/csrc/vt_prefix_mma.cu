@@ -464,7 +464,8 @@ cudaError_t prepare_prefix_mma() {
 }
 
 bool prefix_mma_takes(const AttnArgs& a) {
-  return cache_map_takes(a.shift, a.block_stride, a.token_stride, a.head_stride);
+  // (whole swizzle atoms, 8 tokens, to a copy)
+  return a.shift >= 3 && cache_map_takes(a.block_stride, a.token_stride, a.head_stride);
 }
 
 cudaError_t launch_prefix_mma(const AttnArgs& a, int dtype, int head_dim, cudaStream_t stream) {

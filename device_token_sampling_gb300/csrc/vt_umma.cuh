@@ -175,12 +175,11 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// Whether a tensor map can hold the cache: whole swizzle atoms to a copy, strides in
-// range.
-[[maybe_unused]] bool cache_map_takes(int shift, int64_t block_stride, int64_t token_stride,
+// Whether a tensor map can hold the cache: strides in range.
+[[maybe_unused]] bool cache_map_takes(int64_t block_stride, int64_t token_stride,
                                       int64_t head_stride) {
   const int64_t most = 1ll << 38;
-  return shift >= 3 && block_stride > 0 && token_stride > 0 && head_stride > 0 &&
+  return block_stride > 0 && token_stride > 0 && head_stride > 0 &&
          block_stride < most && token_stride < most && head_stride < most &&
          encode_tiled() != nullptr;
 }

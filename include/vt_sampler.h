@@ -675,8 +675,9 @@ int vt_paged_attention_ex(vt_paged* handle, int32_t dtype, int32_t B, const void
  *   out, out_lse   [T][q_heads][head_dim] of q's type, float [T][q_heads] (may be NULL).
  * The other arguments, the accuracy and the treatment of bad block ids are
  * vt_paged_attention_ex's.  Infinities and NaN at positions that a row does not attend to do not
- * reach it.  Block sizes of 8 tokens and more run on the tensor cores; smaller ones,
- * and caches with a stride of 0 or less, row by row.  Enqueues only; may be captured.
+ * reach it.  q and caches with a stride of 0 or less are taken row by row, everything
+ * else on the tensor cores; a block of 1, 2 or 4 tokens is a copy of its own there, which
+ * takes longer than the same tokens in larger ones.  Enqueues only; may be captured.
  * Errors: VT_ERR_INVALID_ARG, VT_ERR_CAPACITY (B > max_batch), VT_ERR_STATE (a handle
  * without heads), VT_ERR_CUDA. */
 int vt_paged_chunk_attention(vt_paged* handle, int32_t dtype, int32_t B, int32_t T, const void* q,

@@ -303,6 +303,75 @@ def test_equal_to_single_tokens():
 
 
 @gpu
+@pytest.mark.parametrize("bs", [1, 2, 4])
+@pytest.mark.parametrize("d", [64, 128])
+def test_small_blocks(bs, d):
+    """Several copies a lane fetch a tile; blocks outside the cache inside it."""
+    from device_token_sampling_gb300 import VtError
+    x = batch([3, 150, 1], [700, 1000, 129], 8, 2, d, bs, torch.bfloat16, seed=bs)
+    run(x, bs)
+    bad = [5, 64 // bs, 700 // bs - 1]
+    x["table"][0, bad] = torch.tensor([-1, 1 << 20, -5], dtype=torch.int32, device="cuda")
+    with handle(x, bs) as p:
+        out, lse = p.chunk_attention(**x)
+        with pytest.raises(VtError, match="block"):
+            p.check_errors()
+    # the same without those tokens
+    y = dict(x)
+    keep = [j for j in range(700) if j // bs not in bad]
+    rows = x["table"][0, torch.tensor(keep, device="cuda") // bs].long()
+    at = torch.tensor(keep, device="cuda") % bs
+    n = len(keep)
+    one = dict(q=x["q"][2:3], starts=dev([0, 1]), k_cache=x["k_cache"][rows, at][:, None],
+               v_cache=x["v_cache"][rows, at][:, None], table=dev(np.arange(n)[None]),
+               seq_lens=dev([n]))
+    compare((out[2:3], lse[2:3]), one, 1, d ** -0.5)
+
+
+def spread(x):
+    """One kv head for all, a stride of 0: what no tensor map holds."""
+    x.update({k: x[k][:, :, :1].expand_as(x[k]) for k in ("k_cache", "v_cache")})
+    return x
+
+
+@gpu
+@pytest.mark.parametrize("bs", [1, 16, 64])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_row_by_row(bs, d, dtype):
+    run(spread(batch([1, 3, 40, 0, 5], [130, 700, 40, 9, 2], 8, 2, d, bs, dtype, seed=bs)), bs)
+    run(spread(batch([20], [333], 28, 4, d, bs, dtype)), bs, scale=-0.2)
+
+
+@gpu
+def test_row_by_row_of_bad_blocks_and_values():
+    """Blocks outside the cache are left out and reported; values that are not finite reach the
+    rows that see them only; rows behind the last request stay."""
+    from device_token_sampling_gb300 import VtError
+    bs = 16
+    x = batch([40, 3], [100, 131], 4, 2, 64, bs, torch.bfloat16)
+    v = x["v_cache"].clone()
+    v[int(x["table"][0, 5]), 10] = float("nan")          # token 90 of the first
+    v[int(x["table"][1, 8]), 3:] = float("inf")          # behind the second's end
+    y = spread(dict(x, v_cache=v))
+    want, _ = run(spread(x), bs)
+    y["q"] = torch.cat([x["q"], torch.full_like(x["q"], float("nan"))])
+    out = torch.full_like(y["q"], 7.0)
+    with handle(x, bs) as p:
+        p.chunk_attention(**y, out=out)
+        p.check_errors()
+        assert torch.equal(out[:30], want[:30]) and torch.equal(out[40:43], want[40:])
+        assert torch.isnan(out[30:40].float()).all() and (out[43:] == 7).all()
+        y = dict(x, table=x["table"].clone())
+        y["table"][1, 2] = 1 << 20
+        out, _ = p.chunk_attention(**y)
+        with pytest.raises(VtError, match="block"):
+            p.check_errors()
+    assert torch.equal(out[:40], want[:40]) and torch.isfinite(out.float()).all()
+    assert not torch.equal(out[40:], want[40:])
+
+
+@gpu
 def test_far_blocks():
     """A cache past 2^31 elements."""
     bs, hkv, d = 64, 8, 128
