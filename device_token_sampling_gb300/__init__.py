@@ -2,7 +2,9 @@
 
 The compute path is a C-ABI shared library of hand-written sm_103a CUDA
 kernels (``csrc/``, declared in ``include/vt_sampler.h``); ``sampler`` is a thin
-ctypes binding over it, and ``paged`` the same for the batch's cache.  ``workloads`` makes seeded synthetic inputs.
+ctypes binding over it (sampling, draws from given numbers, verification of drafts), and
+``paged`` the same for the batch's cache (block tables, attention, branching, blocks given
+back).  ``workloads`` makes seeded synthetic inputs.
 
 The binding is imported lazily, so that ``workloads`` can be used without the
 built library; touching ``Sampler`` (or anything from ``sampler``) loads the
