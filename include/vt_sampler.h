@@ -695,7 +695,9 @@ int vt_paged_chunk_attention(vt_paged* handle, int32_t dtype, int32_t B, int32_t
  * one that they fill in part becomes a new block off the free list, and (out_src[r],
  * out_dst[r]) the copy that vt_paged_copy_blocks then has to make (-1, -1: none).
  * Blocks of rows that nobody continues are still off the free list until
- * vt_paged_release.  All arrays are device memory.
+ * vt_paged_release.  A row writes its new tokens into blocks of its own as long as it
+ * only grows: one that is to be cut back into what it shares is forked at the shorter
+ * length instead.  All arrays are device memory.
  *   R, parents     rows of the new table, [R].
  *   B, table       the old one, [B][ld_table]; held, seq_lens [B].
  *   free_blocks, num_free, cursor, out_cursor   as vt_paged_tables.
