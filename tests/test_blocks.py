@@ -167,6 +167,65 @@ def test_release_and_compact(B, bs, cols, n_blocks, n_prefix, compact):
 
 
 @gpu
+def test_largest_batch():
+    """As many rows as a handle takes, all of one parent, then of as many."""
+    B, bs, cols = 16384, 16, 3
+    g = np.random.default_rng(0)
+    seq = g.integers(0, cols * bs + 1, B)
+    held = -(-seq // bs)
+    table = g.integers(0, 50000, (B, cols))
+    free = np.arange(50000, 50000 + B)
+    with paged(B, bs, cols) as p:
+        for parents in (np.full(B, 16383), g.integers(0, B, B), np.full(B, -1)):
+            want = fork_reference(table, held, seq, parents, free, 0, bs, cols)
+            out = torch.empty((B, cols), dtype=torch.int32, device="cuda")
+            got = p.fork(dev(table), dev(held), dev(seq), dev(parents), dev(free), dev([0]), out)
+            p.check_errors()
+            np.testing.assert_array_equal(out.cpu(), want[0])
+            for x, w in zip(got, want[1:]):
+                np.testing.assert_array_equal(x.cpu().numpy(), np.atleast_1d(w))
+
+
+@gpu
+@pytest.mark.parametrize("compact", [False, True])
+def test_largest_cache(compact):
+    """As many blocks as a cache may have, few of them in use, at both ends."""
+    n, bs, cols = 1 << 24, 1, 5
+    table = np.array([[n - 1, 0, n // 2, 7, 9], [3, n - 2, n - 1, 5, 5]])
+    held, seq = np.array([3, 5]), np.array([4, 3])
+    want = reclaim_reference(table, held, seq, 64, [], bs, cols)[1]
+    used = sorted({n - 1, 0, n // 2, 3, n - 2})
+    with paged(2, bs, cols) as p:
+        t = dev(table)
+        if not compact:
+            h, free, cursor = p.release(t, dev(held), dev(seq), n)
+            p.check_errors()
+            assert h.tolist() == want and cursor.item() == 5 and free[:5].tolist() == used
+            rest = torch.arange(n, device="cuda")
+            rest = rest[~torch.isin(rest, torch.tensor(used, device="cuda"))]
+            assert torch.equal(free[5:].long(), rest)
+        else:
+            h, free, cursor, src, dst, count, _ = p.compact(t, dev(held), dev(seq), n)
+            p.check_errors()
+            assert cursor.item() == 5 and count.item() == 3
+            assert src[:4].tolist() == [n // 2, n - 2, n - 1, -1] and dst[:3].tolist() == [1, 2, 4]
+            assert t.tolist() == [[4, 0, 1, -1, -1], [3, 2, 4, -1, -1]]
+            assert torch.equal(free, torch.arange(n, device="cuda").int())
+
+
+@gpu
+@pytest.mark.parametrize("count,copied", [(-3, 0), (0, 0), (1, 1), (2, 2), (99, 2)])
+def test_copies_counted_on_the_device(count, copied):
+    cache = torch.arange(6 * 8, device="cuda").view(6, 8).float()
+    want = cache.clone()
+    want[torch.tensor([4, 5][:copied], dtype=torch.long)] = cache[:copied]
+    with paged(1, 16, 1) as p:
+        p.copy_blocks([cache], dev([0, 1]), dev([4, 5]), count=dev([count]))
+        p.check_errors()
+    assert torch.equal(cache, want)
+
+
+@gpu
 def test_ids_outside_the_cache_are_reported():
     from device_token_sampling_gb300 import VtError
     table = np.array([[0, -1, 99], [5, 2 ** 30, 3]])

@@ -492,6 +492,27 @@ def test_outputs_at_odd_addresses(bs):
 
 
 @gpu
+@pytest.mark.parametrize("bs", [2, 16])
+def test_without_log_sums(bs):
+    """out_lse NULL at the C entry; whole units and parts."""
+    from device_token_sampling_gb300.sampler import DTYPE_BF16
+    x = batch([3, 140], [6000, 333], 8, 2, 64, bs, torch.bfloat16)
+    want = run(x, bs)
+    out = torch.empty_like(x["q"])
+    with handle(x, bs) as p:
+        kv = x["k_cache"].stride()
+        rc = p._lib.vt_paged_chunk_attention(
+            p._h, DTYPE_BF16, 2, 143, x["q"].data_ptr(), 512, 64, x["starts"].data_ptr(),
+            x["k_cache"].data_ptr(), x["v_cache"].data_ptr(), x["k_cache"].shape[0], kv[0], kv[1],
+            kv[2], x["table"].data_ptr(), x["table"].shape[1], x["table"].shape[1],
+            x["seq_lens"].data_ptr(), 0.125, out.data_ptr(), None,
+            torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        p.check_errors()
+    assert torch.equal(out, want[0])
+
+
+@gpu
 def test_two_graphs_of_one_handle():
     """Two captured calls share the handle's workspaces: replayed one after another."""
     xs = [batch([3, 4, 250], [40, 700, 300], 8, 2, 64, 16, torch.bfloat16, seed=1),
