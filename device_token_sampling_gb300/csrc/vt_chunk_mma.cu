@@ -252,8 +252,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
   }
   __syncthreads();
   const bool whole = maybe && s_most <= steps / G + steps / G / 16 + 16;
+  if (whole) {
+    if (tid <= G) {
+      ChunkStart s{};
+      s.at = steps;  // (no share)
+      s.b = a.B;
+      s.rounds = mine;
+      a.plan_start[tid] = s;
+    }
+    return;
+  }
   int64_t skipped = 0;
-  if (rounds > 0 && !whole) {
+  if (rounds > 0) {
     const int64_t u = (int64_t)rounds * G;
     const int b = find_request(first, 2, a.B, u);
     const Request r = request(a, b);
@@ -279,7 +289,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
   before += upto - want;
   const int c = tid;
   if (c <= G) {
-    int64_t at = whole ? steps : c == G ? steps : skipped + todo * before / max(all, (int64_t)1);
+    const int64_t at = c == G ? steps : skipped + todo * before / max(all, (int64_t)1);
     ChunkStart s{};
     s.at = at;
     s.b = a.B;
@@ -307,7 +317,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
       s.step = max(in - kUnitCost, 0) / w;  // (a whole step)
       s.at += (s.step > 0 ? kUnitCost + s.step * w : 0) - in;
     }
-    s.rounds = whole ? mine : rounds;
+    s.rounds = rounds;
     a.plan_start[c] = s;
   }
 }
