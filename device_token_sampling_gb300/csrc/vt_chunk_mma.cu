@@ -173,7 +173,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) s_several = s_most = 0;
-  for (int i = tid; i < 8 * a.grid; i += kPlanThreads) a.plan_count[i] = 0;
   __syncthreads();
   int64_t units = 0, steps = 0;
   for (int base = 0; base < a.B; base += kPlanThreads) {
@@ -231,15 +230,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
   __syncthreads();
   const int64_t* first = a.B <= kPlanThreads ? s_first : a.plan_first;
   const int G = a.grid;
-  const int rounds = s_several && units >= 2 * G ? (int)(units / G - 1) : 0;
-  const int64_t rounds_all = (units + G - 1) / G;
-  const bool maybe = rounds_all <= kMostRounds;
+  const int rounds = s_several && units >= 2 * G ? (int)units / G - 1 : 0;
+  const bool maybe = units <= kMostRounds * G;
   // what the units of rounds cost, each CTA's: of all, of `rounds`
   int mine = 0;
   int64_t most = 0, want = 0;
   if (tid < G) {
-    for (int64_t i = 0; i < (maybe ? rounds_all : rounds); ++i) {
-      const int64_t u = i * G + (i & 1 ? G - 1 - tid : tid);
+    for (int i = 0; i < (maybe ? kMostRounds : rounds); ++i) {
+      const int64_t u = (int64_t)i * G + (i & 1 ? G - 1 - tid : tid);
       if (u >= units) break;
       const int b = find_request(first, 2, a.B, u);
       const Request r = request(a, b);
@@ -251,7 +249,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
     if (maybe) atomicMax(&s_most, (int)min(most, (int64_t)0x7fffffff));
   }
   __syncthreads();
-  const bool whole = maybe && s_most <= steps / G + steps / G / 16 + 16;
+  const bool whole = maybe && (int64_t)s_most * G <= steps + steps / 16 + 16 * G;
   if (whole) {
     if (tid <= G) {
       ChunkStart s{};
@@ -262,6 +260,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
     }
     return;
   }
+  for (int i = tid; i < 8 * G; i += kPlanThreads) a.plan_count[i] = 0;
   int64_t skipped = 0;
   if (rounds > 0) {
     const int64_t u = (int64_t)rounds * G;
