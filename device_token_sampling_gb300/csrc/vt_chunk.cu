@@ -6,7 +6,7 @@
 //
 // This file: rows one at a time, in fp32, for layouts that no tensor map holds: q or
 // caches with a stride of 0 (broadcast heads, say) or less.  A warp a row reads all of its
-// keys and values itself: 1024 tokens of 32 heads take 1.8 ms, on the tensor cores 29 us.
+// keys and values itself: 1024 tokens of 32 heads take 1.8 ms, on the tensor cores 25 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -17,11 +17,11 @@
 // Measured with 32/8 heads of 128 in bf16:
 //   long chunks are bound by the tensor cores and the power cap: 4 of 2048 to 4096 tokens
 //   behind up to 16384, 2.03 TFLOP in 1.2 ms, 1.68 PFLOP/s, pipe active in 80 % of the
-//   cycles; one of 16384 tokens 1.73 PFLOP/s;
+//   cycles; one of 16384 tokens 1.76 PFLOP/s;
 //   few rows over long contexts by the memory: 64 requests of 1 to 8 behind 4096 to 8192,
 //   1.64 GB in 261 us, 6.3 TB/s (0.94 of a plain copy's rate);
-//   small batches by latency: 4 requests of 5 tokens behind up to 600 21 us, of which the
-//   plan is 5.
+//   small batches by latency: 4 requests of 5 tokens behind up to 600 17 us, of which the
+//   plan is 3.5.
 #include <type_traits>
 
 #include "vt_paged.h"
@@ -569,7 +569,7 @@ __device__ __noinline__ void join_rows(const ChunkArgs& a, int job, int last, in
 
 // kSmall: blocks of 1 or 2 tokens, more than 32 to a step.  (In one kernel with the others
 // these lost up to 9 %.)  The copies of such blocks bound it: a prompt of 1024 tokens takes
-// 82, 56, 41, 33 and 29 us in blocks of 1, 2, 4, 8 and 64.
+// 80, 51, 35, 29 and 25 us in blocks of 1, 2, 4, 8 and 64.
 //
 // Roles of a CTA's 16 warps, each with barriers of its own towards the others: 0-3 and 4-7
 // the softmax and the outputs of a tile (a row a thread, 200 registers), 8 the scores of both
