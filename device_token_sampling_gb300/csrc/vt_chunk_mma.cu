@@ -139,6 +139,10 @@ struct Sums2 {
   int64_t x, y;
 };
 constexpr int kPlanThreads = 1024;
+// What a share is worth at least: a CTA more is a part more to be put together, about 1 us
+// each.  5 tokens behind 12000 of one request of 20/4 heads: 44 us, shares of 1 step (all
+// CTAs) 62, of 24 43; 4 requests of 5 behind 2000 32, 31 and 39.
+constexpr int kLeast = 8;
 constexpr int kMostRounds = 16;  // of units that are looked at one by one
 
 // The last b with first[b] <= v.
@@ -271,7 +275,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ChunkArgs a) {
   const int64_t todo = steps - skipped;
   // The rest goes in shares that make up for it: up to the mean of all.  (Equal shares
   // left the CTAs' sums 9 % apart on 4 prompts of up to 4096 tokens.)
-  want = tid < G ? max(steps / G + 1 - want, (int64_t)0) : 0;
+  // CTAs that get some
+  const int some = rounds > 0 ? G : (int)min((int64_t)G, steps / kLeast + 1);
+  want = tid < some ? max(steps / some + 1 - want, (int64_t)0) : 0;
   int64_t upto = want;  // of the CTAs up to this one
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
